@@ -31,6 +31,11 @@ SGEMM_ERR_CAPTURE = -11
 SGEMM_OP_N = 0
 SGEMM_OP_T = 1
 
+SGEMM_TYPE_F32 = 0
+SGEMM_TYPE_BF16 = 1
+SGEMM_TYPE_F16 = 2
+SGEMM_I8_MAX_K = 131071
+
 PARAM_NAMES = ("BM", "BN", "BK", "WM", "WN", "WNITER", "TM", "TN", "NT", "STAGES", "MINB", "KU", "ORDER")
 
 
@@ -90,6 +95,11 @@ def lib() -> ctypes.CDLL:
                 "sgemm_config_layouts": (I, [I]),
                 "sgemm_diag_tf32_mma_rate": (I, [I, ctypes.POINTER(ctypes.c_double)]),
                 "sgemm_diag_tf32_pair_mma_rate": (I, [I, ctypes.POINTER(ctypes.c_double)]),
+                "sgemm_grouped": (I, [I, I, I, I, I, I, I, F, P, I, P, I, LL, P, F, P, I, P]),
+                "sgemm_grouped_wgrad": (I, [I, I, I, I, I, I, F, P, I, P, I, P, F, P, I, LL, P]),
+                "sgemm_i8_quantize": (I, [I, I, I, P, I, P, I, P, P]),
+                "sgemm_i8": (I, [I, I, I, P, I, P, P, I, P, I, P, I, P]),
+                "sgemm_grad_clip": (I, [I, P, P, P, P, F, P, P]),
                 "sgemm_strided_batched": (I, [I, I, I, I, I, F, P, I, LL, P, I, LL, F, P, I, LL,
                                               I, P]),
             }
@@ -341,6 +351,46 @@ def sgemm_3xtf32_set_kernel_form(form: int) -> int:
     return lib().sgemm_3xtf32_set_kernel_form(form)
 
 
+# ---- products grouped by expert, 8-bit products, gradient clipping -------------------
+def sgemm_grouped(op, type, out_type, E, T, N, K, alpha, X, ldx, W, ldw, strideW, offsets, beta, Y,
+                  ldy, stream=None) -> int:
+    """Y[r] = alpha*X[r]*op(W_e) + beta*Y[r] for the rows r of group e, whose
+    bounds are E + 1 ints on the device. Returns the status code."""
+    return lib().sgemm_grouped(op, type, out_type, E, T, N, K, alpha, X, ldx, W, ldw, strideW,
+                               offsets, beta, Y, ldy, stream)
+
+
+def sgemm_grouped_wgrad(type, out_type, E, T, M, N, alpha, A, lda, B, ldb, offsets, beta, C, ldc,
+                        strideC, stream=None) -> int:
+    """C_e = alpha*A_e^T*B_e + beta*C_e over the rows of each group. Returns the
+    status code."""
+    return lib().sgemm_grouped_wgrad(type, out_type, E, T, M, N, alpha, A, lda, B, ldb, offsets,
+                                     beta, C, ldc, strideC, stream)
+
+
+def sgemm_i8_quantize(M, K, type, X, ldx, Q, ldq, scale, stream=None) -> int:
+    """Rows of X to 8-bit integers Q with one FP32 scale a row. Returns the
+    status code."""
+    return lib().sgemm_i8_quantize(M, K, type, X, ldx, Q, ldq, scale, stream)
+
+
+def sgemm_i8(M, N, K, A, lda, scaleA, B, ldb, scaleB, out_type, C, ldc, stream=None) -> int:
+    """C = (A B^T) * scaleA[:, None] * scaleB on 8-bit integers (B is N x K).
+    Returns the status code."""
+    return lib().sgemm_i8(M, N, K, A, lda, scaleA, B, ldb, scaleB, out_type, C, ldc, stream)
+
+
+def sgemm_grad_clip(grads, out, sizes, types, max_norm, norm, stream=None) -> int:
+    """The 2-norm of tensors taken together, and out_i = grads_i * min(1,
+    max_norm / (norm + 1e-6)): sequences of device addresses, element counts
+    and SGEMM_TYPE_* codes. out None: the norm only. Returns the status code."""
+    n = len(grads)
+    vp = (ctypes.c_void_p * n)(*grads)
+    vo = None if out is None else (ctypes.c_void_p * n)(*out)
+    return lib().sgemm_grad_clip(n, vp, vo, (ctypes.c_longlong * n)(*sizes),
+                                 (ctypes.c_int * n)(*types), max_norm, norm, stream)
+
+
 # ---- torch conveniences (marshalling only) ------------------------------------------
 def _stream_handle(stream):
     import torch
@@ -371,3 +421,171 @@ def gemm(A, B, C, alpha=1.0, beta=0.0, stream=None):
     if st != SGEMM_OK:
         raise SgemmError(st, "sgemm")
     return C
+
+
+def _type(t, name):
+    import torch
+    codes = {torch.float32: SGEMM_TYPE_F32, torch.bfloat16: SGEMM_TYPE_BF16,
+             torch.float16: SGEMM_TYPE_F16}
+    if t.dtype not in codes:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16")
+    return codes[t.dtype]
+
+
+def _pitch(t, name):
+    """Row pitch of a row-major matrix (or of the matrices of a 3-D tensor)."""
+    if t.size(-1) > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be row-major (unit stride along rows)")
+    cols = max(t.size(-1), 1)
+    return max(t.stride(-2), cols) if t.size(-2) > 1 else cols
+
+
+def _check(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _same_device(ref, **tensors):
+    _check(ref.is_cuda, "tensors must be on a CUDA device")
+    for name, t in tensors.items():
+        _check(t.device == ref.device, f"{name} is on another device")
+
+
+def _launch_stream(ref, stream):
+    import torch
+    s = stream if stream is not None else torch.cuda.current_stream(ref.device)
+    return s.cuda_stream
+
+
+def _offsets(offsets, groups):
+    import torch
+    _check(offsets.dtype == torch.int32 and offsets.dim() == 1 and offsets.is_contiguous(),
+           "offsets must be a contiguous 1-D int32 tensor")
+    _check(offsets.numel() == groups + 1, "offsets must hold one bound more than there are groups")
+
+
+def grouped_gemm(X, W, offsets, Y=None, op="T", alpha=1.0, beta=0.0, out_dtype=None, stream=None):
+    """Y[r] = alpha * X[r] @ op(W[e]) + beta * Y[r] for the rows r of group e,
+    offsets[e] <= r < offsets[e + 1] (int32, on the device). W is (E, N, K) with
+    op "T" and (E, K, N) with op "N"; the gradient of X is grouped_gemm(dY, W,
+    offsets, op=the other). Without Y a new tensor of out_dtype (default: X's)
+    is returned, in which rows outside every group are not set."""
+    import torch
+    _check(op in ("N", "T"), 'op must be "N" or "T"')
+    _check(X.dim() == 2 and W.dim() == 3, "X must be 2-D and W 3-D")
+    E, T, K = W.size(0), X.size(0), X.size(1)
+    N = W.size(1) if op == "T" else W.size(2)
+    _check(W.size(2 if op == "T" else 1) == K, "shape mismatch")
+    _check(W.dtype == X.dtype, "X and W must have one type")
+    _offsets(offsets, E)
+    if Y is None:
+        _check(beta == 0.0, "beta needs Y")
+        Y = torch.empty((T, N), dtype=out_dtype or X.dtype, device=X.device)
+    _check(tuple(Y.shape) == (T, N), "shape mismatch")
+    _same_device(X, W=W, offsets=offsets, Y=Y)
+    with torch.cuda.device(X.device):
+        st = sgemm_grouped(SGEMM_OP_T if op == "T" else SGEMM_OP_N, _type(X, "X"), _type(Y, "Y"), E,
+                           T, N, K, float(alpha), X.data_ptr(), _pitch(X, "X"), W.data_ptr(),
+                           _pitch(W, "W"), W.stride(0) if E > 1 else 0, offsets.data_ptr(),
+                           float(beta), Y.data_ptr(), _pitch(Y, "Y"), _launch_stream(X, stream))
+    if st != SGEMM_OK:
+        raise SgemmError(st, "sgemm_grouped")
+    return Y
+
+
+def grouped_wgrad(A, B, offsets, C=None, alpha=1.0, beta=0.0, out_dtype=None, stream=None):
+    """C[e] = alpha * A_e.T @ B_e + beta * C[e] over the rows of each group: the
+    gradient of W (E, N, K) with A = dY, B = X, of W (E, K, N) with A = X, B = dY.
+    Without C a new (E, M, N) tensor of out_dtype (default: A's) is returned."""
+    import torch
+    _check(A.dim() == 2 and B.dim() == 2 and A.size(0) == B.size(0), "shape mismatch")
+    _check(A.dtype == B.dtype, "A and B must have one type")
+    E = offsets.numel() - 1
+    _check(E >= 0, "offsets must hold one bound more than there are groups")
+    _offsets(offsets, E)
+    T, M, N = A.size(0), A.size(1), B.size(1)
+    if C is None:
+        _check(beta == 0.0, "beta needs C")
+        C = torch.empty((E, M, N), dtype=out_dtype or A.dtype, device=A.device)
+    _check(tuple(C.shape) == (E, M, N), "shape mismatch")
+    _same_device(A, B=B, offsets=offsets, C=C)
+    with torch.cuda.device(A.device):
+        st = sgemm_grouped_wgrad(_type(A, "A"), _type(C, "C"), E, T, M, N, float(alpha),
+                                 A.data_ptr(), _pitch(A, "A"), B.data_ptr(), _pitch(B, "B"),
+                                 offsets.data_ptr(), float(beta), C.data_ptr(), _pitch(C, "C"),
+                                 C.stride(0) if E > 1 else 0, _launch_stream(A, stream))
+    if st != SGEMM_OK:
+        raise SgemmError(st, "sgemm_grouped_wgrad")
+    return C
+
+
+def i8_quantize(X, Q=None, scale=None, stream=None):
+    """(Q, scale): the rows of X as 8-bit integers with one FP32 scale a row,
+    scale = max|X[m]| / 127."""
+    import torch
+    _check(X.dim() == 2, "X must be 2-D")
+    M, K = X.shape
+    if Q is None:
+        # rows padded to 16 bytes, so that sgemm_i8 reads them in place
+        Q = torch.empty((M, (K + 15) // 16 * 16), dtype=torch.int8, device=X.device)[:, :K]
+    if scale is None:
+        scale = torch.empty((M,), dtype=torch.float32, device=X.device)
+    _check(Q.dtype == torch.int8 and tuple(Q.shape) == (M, K), "Q must be int8 of X's shape")
+    _check(scale.dtype == torch.float32 and tuple(scale.shape) == (M,) and scale.is_contiguous(),
+           "scale must be a contiguous float32 vector with one value a row")
+    _same_device(X, Q=Q, scale=scale)
+    with torch.cuda.device(X.device):
+        st = sgemm_i8_quantize(M, K, _type(X, "X"), X.data_ptr(), _pitch(X, "X"), Q.data_ptr(),
+                               _pitch(Q, "Q"), scale.data_ptr(), _launch_stream(X, stream))
+    if st != SGEMM_OK:
+        raise SgemmError(st, "sgemm_i8_quantize")
+    return Q, scale
+
+
+def i8_gemm(A, scaleA, B, scaleB, C=None, out_dtype=None, stream=None):
+    """C = (A @ B.T) * scaleA[:, None] * scaleB on int8 A (M, K) and B (N, K), the
+    sum an exact integer. Without C a new tensor of out_dtype (default bfloat16)
+    is returned."""
+    import torch
+    _check(A.dim() == 2 and B.dim() == 2 and A.size(1) == B.size(1), "shape mismatch")
+    _check(A.dtype == torch.int8 and B.dtype == torch.int8, "A and B must be int8")
+    M, K = A.shape
+    N = B.size(0)
+    for s, n, name in ((scaleA, M, "scaleA"), (scaleB, N, "scaleB")):
+        _check(s.dtype == torch.float32 and tuple(s.shape) == (n,) and s.is_contiguous(),
+               f"{name} must be a contiguous float32 vector of {n}")
+    if C is None:
+        C = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=A.device)
+    _check(tuple(C.shape) == (M, N), "shape mismatch")
+    _same_device(A, scaleA=scaleA, B=B, scaleB=scaleB, C=C)
+    with torch.cuda.device(A.device):
+        st = sgemm_i8(M, N, K, A.data_ptr(), _pitch(A, "A"), scaleA.data_ptr(), B.data_ptr(),
+                      _pitch(B, "B"), scaleB.data_ptr(), _type(C, "C"), C.data_ptr(),
+                      _pitch(C, "C"), _launch_stream(A, stream))
+    if st != SGEMM_OK:
+        raise SgemmError(st, "sgemm_i8")
+    return C
+
+
+def clip_grad_norm(grads, max_norm, out=None, stream=None):
+    """The 2-norm (a float32 scalar tensor) of contiguous CUDA tensors taken
+    together, before clipping; out[i] = grads[i] * min(1, max_norm / (norm +
+    1e-6)), in place without `out`."""
+    import torch
+    grads = list(grads)
+    _check(len(grads) > 0, "no gradients")
+    out = grads if out is None else list(out)
+    _check(len(out) == len(grads), "out must hold a tensor for every gradient")
+    for g, o in zip(grads, out):
+        _check(g.is_cuda and g.device == grads[0].device and o.device == g.device,
+               "gradients must be on one CUDA device")
+        _check(g.is_contiguous() and o.is_contiguous(), "gradients must be contiguous")
+        _check(o.dtype == g.dtype and o.shape == g.shape, "out must have the gradients' types and shapes")
+    norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
+    with torch.cuda.device(grads[0].device):
+        st = sgemm_grad_clip([g.data_ptr() for g in grads], [o.data_ptr() for o in out],
+                             [g.numel() for g in grads], [_type(g, "gradients") for g in grads],
+                             float(max_norm), norm.data_ptr(), _launch_stream(norm, stream))
+    if st != SGEMM_OK:
+        raise SgemmError(st, "sgemm_grad_clip")
+    return norm

@@ -1,0 +1,378 @@
+// grad_clip.cu -- sgemm_grad_clip: the 2-norm of many tensors taken together,
+// and every tensor scaled so that the norm stays below a bound.
+//
+//   norm = sqrt(sum over all tensors of g^2)
+//   coef = min(1, max_norm / (norm + 1e-6)),  out = g * coef
+//
+// Two launches a list of up to kTable tensors: the squares, then the scaling.
+// The tensors are cut into 16 KB pieces that start on 16-byte addresses
+// (the elements before a tensor's first such address form its first, shorter
+// vector), dealt to the CTAs in turn. Squares are summed in FP32 over one
+// thread's share of a piece (16 or 32 values) and in FP64 beyond; every CTA of
+// the second launch adds the first one's per-CTA sums in the same order, so
+// the result does not depend on timing.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <cstring>
+
+#include "../../include/sgemm_gb300.h"
+#include "ptx.cuh"
+
+#define SGEMM_API extern "C" __attribute__((visibility("default")))
+
+namespace sgemm_gb300 {
+
+int library_workspace(int dev, cudaStream_t stream, size_t floats, size_t nflags, float** scratch,
+                      int** status, uint32_t** flags, uint32_t* epoch);
+int library_device_sms(int dev, int* sms);
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPiece = 16384;           // bytes of a piece
+constexpr int kVecs = kPiece / 16 / kThreads;  // 16-byte vectors per thread and piece
+constexpr int kTable = 1000;            // tensors per launch (they are kernel parameters)
+constexpr int kCtasPerSm = 8;
+
+struct Entry {
+  const void* in;
+  void* out;
+  long long n;     // elements
+};
+template <int CAP>
+struct Table {
+  int count;
+  unsigned pieces;
+  Entry e[CAP];
+  unsigned first[CAP];        // number of the tensor's first piece
+  unsigned char type[CAP];
+};
+static_assert(sizeof(Table<kTable>) + 64 <= 32764, "kernel parameters");
+
+__device__ __forceinline__ float elem_f32(const void* p, long long i, int type) {
+  if (type == SGEMM_TYPE_F32) return static_cast<const float*>(p)[i];
+  if (type == SGEMM_TYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  return __half2float(static_cast<const __half*>(p)[i]);
+}
+__device__ __forceinline__ void put_elem(void* p, long long i, int type, float v) {
+  if (type == SGEMM_TYPE_F32)
+    static_cast<float*>(p)[i] = v;
+  else if (type == SGEMM_TYPE_BF16)
+    static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+  else
+    static_cast<__half*>(p)[i] = __float2half_rn(v);
+}
+
+// The values of a 16-byte vector (4 FP32, or 8 of 16 bits) as FP32.
+__device__ __forceinline__ void unpack(const uint4& v, int type, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if (type == SGEMM_TYPE_F32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = __uint_as_float(w[i]);
+      x[i + 4] = 0.f;
+    }
+  } else if (type == SGEMM_TYPE_BF16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    }
+  }
+}
+__device__ __forceinline__ uint4 pack(const float (&x)[8], int type) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (type == SGEMM_TYPE_F32) {
+      w[i] = __float_as_uint(x[i]);
+    } else if (type == SGEMM_TYPE_BF16) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    } else {
+      const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The tensor of piece `at` and the piece's place in it, in vectors counted
+// from the 16-byte address at or below the tensor's start.
+template <int CAP>
+__device__ __forceinline__ int find(const Table<CAP>& t, unsigned at) {
+  int lo = 0, hi = t.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.first[mid] <= at) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+__device__ __forceinline__ int elem_size(int type) { return type == SGEMM_TYPE_F32 ? 4 : 2; }
+
+// Sum of a block's values in FP64 (the same order every time), in thread 0.
+__device__ __forceinline__ double block_sum(double v, double* buf) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_down_sync(0xffffffffu, v, d);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double s = 0.0;
+  if (threadIdx.x == 0)
+    for (int w = 0; w < kThreads / 32; ++w) s += buf[w];
+  return s;
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads)
+    squares_kernel(const __grid_constant__ Table<CAP> t, double* sums) {
+  __shared__ double buf[kThreads / 32];
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  double total = 0.0;
+  for (unsigned at = blockIdx.x; at < t.pieces; at += gridDim.x) {
+    const int i = find(t, at);
+    const int type = t.type[i], es = elem_size(type), per = 16 / es;
+    const char* in = static_cast<const char*>(t.e[i].in);
+    const int head = (int)(reinterpret_cast<uintptr_t>(in) & 15u) / es;
+    const long long n = t.e[i].n;
+    const long long v0 = (long long)(at - t.first[i]) * (kPiece / 16) + threadIdx.x;
+    uint4 raw[kVecs];
+    bool whole[kVecs];
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      const long long lo = (v0 + j * kThreads) * per - head;   // first element of the vector
+      whole[j] = lo >= 0 && lo + per <= n;
+      if (whole[j]) raw[j] = __ldg(reinterpret_cast<const uint4*>(in + lo * es));
+    }
+    float s = 0.f;
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      if (whole[j]) {
+        unpack(raw[j], type, x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s = fmaf(x[k], x[k], s);
+      } else {
+        const long long lo = (v0 + j * kThreads) * per - head;
+        for (int k = 0; k < per; ++k)
+          if (lo + k >= 0 && lo + k < n) {
+            const float e = elem_f32(in, lo + k, type);
+            s = fmaf(e, e, s);
+          }
+      }
+    }
+    if (s > 1e-30f && s < 1e37f) {
+      total += (double)s;
+    } else if (s != 0.f) {
+      // squares near the ends of FP32's range (or no numbers): in FP64
+      for (int j = 0; j < kVecs; ++j) {
+        const long long lo = (v0 + j * kThreads) * per - head;
+        for (int k = 0; k < per; ++k)
+          if (lo + k >= 0 && lo + k < n) {
+            const double e = (double)elem_f32(in, lo + k, type);
+            total += e * e;
+          }
+      }
+    }
+  }
+  const double s = block_sum(total, buf);
+  if (threadIdx.x == 0) sums[blockIdx.x] = s;
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads)
+    scale_kernel(const __grid_constant__ Table<CAP> t, const double* sums, int nsums,
+                 float max_norm, float* norm) {
+  __shared__ double buf[kThreads / 32];
+  __shared__ float coef_s;
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  double v = 0.0;
+  for (int i = threadIdx.x; i < nsums; i += kThreads) v += __ldcg(sums + i);
+  v = block_sum(v, buf);
+  if (threadIdx.x == 0) {
+    const float nrm = (float)sqrt(v);
+    float c = max_norm / (nrm + 1e-6f);
+    if (c > 1.f) c = 1.f;      // (a NaN stays)
+    coef_s = c;
+    if (blockIdx.x == 0 && norm != nullptr) *norm = nrm;
+  }
+  __syncthreads();
+  const float coef = coef_s;
+  for (unsigned at = blockIdx.x; at < t.pieces; at += gridDim.x) {
+    const int i = find(t, at);
+    const int type = t.type[i], es = elem_size(type), per = 16 / es;
+    const char* in = static_cast<const char*>(t.e[i].in);
+    char* out = static_cast<char*>(t.e[i].out);
+    if (out == nullptr || (coef == 1.f && out == in)) continue;
+    const int head = (int)(reinterpret_cast<uintptr_t>(in) & 15u) / es;
+    const bool same = ((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
+    const long long n = t.e[i].n;
+    const long long v0 = (long long)(at - t.first[i]) * (kPiece / 16) + threadIdx.x;
+    uint4 raw[kVecs];
+    bool whole[kVecs];
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      const long long lo = (v0 + j * kThreads) * per - head;
+      whole[j] = lo >= 0 && lo + per <= n;
+      if (whole[j]) raw[j] = *reinterpret_cast<const uint4*>(in + lo * es);
+    }
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      const long long lo = (v0 + j * kThreads) * per - head;
+      if (whole[j]) {
+        float x[8];
+        unpack(raw[j], type, x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] *= coef;
+        if (same) {
+          *reinterpret_cast<uint4*>(out + lo * es) = pack(x, type);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k < per) put_elem(out, lo + k, type, x[k]);
+        }
+      } else {
+        for (int k = 0; k < per; ++k)
+          if (lo + k >= 0 && lo + k < n)
+            put_elem(out, lo + k, type, elem_f32(in, lo + k, type) * coef);
+      }
+    }
+  }
+}
+
+template <int CAP>
+Table<CAP> fill(int from, int to, const void* const* in, void* const* out, const long long* sizes,
+                const int* types) {
+  Table<CAP> t;
+  t.count = 0;
+  unsigned pieces = 0;
+  for (int i = from; i < to; ++i) {
+    if (sizes[i] == 0) continue;
+    const int es = types[i] == SGEMM_TYPE_F32 ? 4 : 2;
+    const long long bytes = sizes[i] * es + (long long)(reinterpret_cast<uintptr_t>(in[i]) & 15u);
+    t.e[t.count] = Entry{in[i], out == nullptr ? nullptr : out[i], sizes[i]};
+    t.first[t.count] = pieces;
+    t.type[t.count] = (unsigned char)types[i];
+    pieces += (unsigned)((bytes + kPiece - 1) / kPiece);
+    ++t.count;
+  }
+  t.pieces = pieces;
+  return t;
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch(void (*kernel)(KArgs...), int grid, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t lc = {};
+  cudaLaunchAttribute la[1];
+  la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  la[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.gridDim = dim3((unsigned)grid);
+  lc.blockDim = dim3(kThreads);
+  lc.stream = stream;
+  lc.attrs = la;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, kernel, static_cast<KArgs>(args)...);
+}
+
+}  // namespace
+}  // namespace sgemm_gb300
+
+using namespace sgemm_gb300;
+
+SGEMM_API int sgemm_grad_clip(int n, const void* const* grads, void* const* out,
+                              const long long* sizes, const int* types, float max_norm, float* norm,
+                              void* stream_) {
+  if (n < 0) return SGEMM_ERR_INVALID_DIM;
+  if (!(max_norm >= 0.f)) return SGEMM_ERR_INVALID_VALUE;
+  if (n > 0 && (grads == nullptr || sizes == nullptr || types == nullptr))
+    return SGEMM_ERR_NULL_PTR;
+  if (norm == nullptr && out == nullptr) return SGEMM_ERR_NULL_PTR;
+  long long bytes = 0;
+  for (int i = 0; i < n; ++i) {
+    if (types[i] != SGEMM_TYPE_F32 && types[i] != SGEMM_TYPE_BF16 && types[i] != SGEMM_TYPE_F16)
+      return SGEMM_ERR_INVALID_VALUE;
+    if (sizes[i] < 0 || sizes[i] > (1LL << 40)) return SGEMM_ERR_INVALID_DIM;
+    if (sizes[i] == 0) continue;
+    if (grads[i] == nullptr || (out != nullptr && out[i] == nullptr)) return SGEMM_ERR_NULL_PTR;
+    const uintptr_t mask = types[i] == SGEMM_TYPE_F32 ? 3u : 1u;
+    if ((reinterpret_cast<uintptr_t>(grads[i]) & mask) ||
+        (out != nullptr && (reinterpret_cast<uintptr_t>(out[i]) & mask)))
+      return SGEMM_ERR_MISALIGNED;
+    bytes += sizes[i] * (types[i] == SGEMM_TYPE_F32 ? 4 : 2) + kPiece;
+    if (bytes > (1LL << 44)) return SGEMM_ERR_INVALID_DIM;   // the piece numbers are 32 bits
+  }
+  if (reinterpret_cast<uintptr_t>(norm) & 3u) return SGEMM_ERR_MISALIGNED;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return SGEMM_ERR_LAUNCH;
+  }
+  int st = library_device_sms(dev, &sms);
+  if (st != SGEMM_OK) return st;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+
+  const int lists = n > 0 ? (n + kTable - 1) / kTable : 1;
+  const int per_list = sms * kCtasPerSm;
+  float* ws = nullptr;
+  int* status = nullptr;
+  st = library_workspace(dev, stream, (size_t)lists * per_list * 2, 0, &ws, &status, nullptr,
+                         nullptr);
+  if (st != SGEMM_OK) return st;
+  double* sums = reinterpret_cast<double*>(ws);
+  // the first launches write their sums one list after another
+  int nsums = 0;
+  auto each = [&](auto&& fn) -> cudaError_t {
+    for (int l = 0; l < lists; ++l) {
+      const int from = l * kTable, to = from + kTable < n ? from + kTable : n;
+      const cudaError_t e = fn(from, to);
+      if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+  };
+  auto grid_of = [&](unsigned pieces) {
+    return pieces < 1 ? 1 : (pieces < (unsigned)per_list ? (int)pieces : per_list);
+  };
+  cudaError_t e = each([&](int from, int to) {
+    cudaError_t r;
+    if (to - from <= 64) {
+      const auto t = fill<64>(from, to, grads, out, sizes, types);
+      const int grid = grid_of(t.pieces);
+      r = launch(squares_kernel<64>, grid, stream, t, sums + nsums);
+      nsums += grid;
+    } else {
+      const auto t = fill<kTable>(from, to, grads, out, sizes, types);
+      const int grid = grid_of(t.pieces);
+      r = launch(squares_kernel<kTable>, grid, stream, t, sums + nsums);
+      nsums += grid;
+    }
+    return r;
+  });
+  if (e == cudaSuccess)
+    e = each([&](int from, int to) {
+      if (to - from <= 64) {
+        const auto t = fill<64>(from, to, grads, out, sizes, types);
+        return launch(scale_kernel<64>, out == nullptr ? 1 : grid_of(t.pieces), stream, t,
+                      (const double*)sums, nsums, max_norm, norm);
+      }
+      const auto t = fill<kTable>(from, to, grads, out, sizes, types);
+      return launch(scale_kernel<kTable>, out == nullptr ? 1 : grid_of(t.pieces), stream, t,
+                    (const double*)sums, nsums, max_norm, norm);
+    });
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return SGEMM_ERR_LAUNCH;
+  }
+  return SGEMM_OK;
+}

@@ -185,5 +185,41 @@ __host__ __device__ constexpr uint32_t idesc_tf32(int M, int N) {
          ((uint32_t)(M >> 4) << 24);
 }
 
+// ---- kind::f16: F16 or BF16 operands (both of one type), FP32 accumulate ----
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor of kind::f16 with FP32 accumulation: D format F32
+// (bits 4-5 = 1), A and B format (bits 7-9 and 10-12: 0 = F16, 1 = BF16), an
+// operand that is MN-major in shared memory has its transpose bit set (15: A,
+// 16: B), N >> 3 (bits 17-22), M >> 4 (bits 24-28).
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool bf16, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) |
+         ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
+}
+
+// Descriptor of an operand tile with its layout fields given: leading byte
+// offset (between 64-element chunks of an MN-major tile; unused K-major),
+// stride byte offset (between 8-row groups), swizzle of 128 or 64 bytes. Only
+// the start address differs between the k-steps of one tile.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t smem_addr, uint32_t lead_bytes,
+                                              uint32_t stride_bytes, bool swizzle128) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lead_bytes >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)((stride_bytes >> 4) & 0x3FFFu) << 32;
+  d |= (uint64_t)1u << 46;                    // descriptor version
+  d |= (swizzle128 ? (uint64_t)2u : (uint64_t)4u) << 61;
+  return d;
+}
+
 }  // namespace tc
 }  // namespace sgemm_gb300

@@ -487,6 +487,109 @@ int sgemm_noalloc_poll_status(void* stream, int* detail);
 int sgemm_ladder(int kernel, int M, int N, int K, float alpha, const float* A, int lda,
                  const float* B, int ldb, float beta, float* C, int ldc, void* stream);
 
+/*
+ * The linear layers of a language model's experts: products grouped by expert
+ * with ragged row counts, their weight gradients, the 8-bit integer product
+ * that serves such a layer, and the clipping of many gradients. The pages
+ * have none of these.
+ */
+
+/* Element types of the calls below. */
+typedef enum {
+  SGEMM_TYPE_F32 = 0,  /* IEEE single precision */
+  SGEMM_TYPE_BF16 = 1, /* bfloat16              */
+  SGEMM_TYPE_F16 = 2   /* IEEE half precision   */
+} sgemm_type;
+
+/*
+ * Y[r, :] = alpha * X[r, :] * op(W_e) + beta * Y[r, :] for every row r of group
+ * e, e = 0 .. E - 1. X is T x K and Y is T x N, row-major; group e is the rows
+ * [offsets[e], offsets[e + 1]), offsets being E + 1 ints on the DEVICE (they
+ * may come from a kernel queued before; the host never reads them). op(W_e) is
+ * K x N: W_e = W + e * strideW (in elements) as stored K x N (SGEMM_OP_N, ldw >=
+ * max(1, N)) or the transpose of a W_e stored N x K (SGEMM_OP_T, ldw >= max(1,
+ * K)). The gradient of X is the same call on dY with the other op.
+ *
+ * type is that of X and W, out_type that of Y: FP32 operands give FP32; BF16
+ * and F16 operands give any type. Products are accumulated in FP32 and rounded
+ * once; FP32 operands are cut into three BF16 parts each (an error below
+ * 2^-23 of |x||w| per product). An FP32 operand that is infinite or NaN makes
+ * every output it takes part in NaN; BF16 and F16 follow IEEE arithmetic.
+ * beta == 0 never reads Y; alpha == 0 or K == 0 never reads X or W.
+ *
+ * Rows outside every group are not touched. Groups may be empty. Offsets are
+ * clamped to 0 .. T, and a group whose end lies before its start is empty;
+ * groups must not overlap. E <= 1024. Any element-aligned pointers and leading
+ * dimensions work; operands whose rows (or strideW) are not multiples of 16
+ * bytes are first copied into the per-stream workspace. Y must not overlap X or
+ * W. Workspace, capture and device status as for sgemm().
+ * Returns SGEMM_ERR_INVALID_VALUE for another op or type, E > 1024, strideW <
+ * 0 or 16-bit results of FP32 operands; SGEMM_ERR_INVALID_DIM, _INVALID_LD,
+ * _NULL_PTR and _MISALIGNED as sgemm().
+ */
+int sgemm_grouped(int op, int type, int out_type, int E, int T, int N, int K, float alpha,
+                  const void* X, int ldx, const void* W, int ldw, long long strideW,
+                  const int* offsets, float beta, void* Y, int ldy, void* stream);
+
+/*
+ * C_e = alpha * A_e^T * B_e + beta * C_e, e = 0 .. E - 1: A is T x M, B is T x
+ * N, row-major, A_e and B_e their rows [offsets[e], offsets[e + 1]), and C_e =
+ * C + e * strideC (in elements) is M x N. With A = dY and B = X it is the
+ * gradient of weights stored N x K (op T above), with A = X and B = dY of
+ * weights stored K x N. An empty group gives beta * C_e (zeros for beta == 0,
+ * without reading C). Types, offsets, accuracy and errors as sgemm_grouped();
+ * FP32 results of 16-bit operands leave the tensor cores every 256 rows and
+ * are added in FP32 with rounding to nearest. The C_e must not overlap.
+ */
+int sgemm_grouped_wgrad(int type, int out_type, int E, int T, int M, int N, float alpha,
+                        const void* A, int lda, const void* B, int ldb, const int* offsets,
+                        float beta, void* C, int ldc, long long strideC, void* stream);
+
+/*
+ * Rows of X (M x K, of `type`) to 8-bit integers with one scale a row:
+ * scale[m] = max_k |X[m, k]| / 127, Q[m, k] = X[m, k] / scale[m] rounded to the
+ * nearest integer (ties to even) within +-127; both quotients are rounded to
+ * FP32. A row of zeros has scale 0 and zeros. A row with an infinity or a NaN
+ * gets it as its scale (NaN where both occur), and its products are NaN.
+ */
+int sgemm_i8_quantize(int M, int K, int type, const void* X, int ldx, signed char* Q, int ldq,
+                      float* scale, void* stream);
+
+/*
+ * C[m, n] = (sum_k A[m, k] * B[n, k]) * scaleA[m] * scaleB[n]: A is M x K and B
+ * N x K (a channel per row), 8-bit integers; scaleA has M, scaleB N FP32
+ * values. The sum is an exact 32-bit integer for every input; its product with
+ * the scales is formed in FP32 and rounded once to out_type. K <=
+ * SGEMM_I8_MAX_K (SGEMM_ERR_INVALID_DIM beyond). K == 0 gives zeros times the
+ * scales. Any leading dimensions (>= max(1, K), ldc >= max(1, N)) and byte
+ * alignment; rows of A or B that are not multiples of 16 bytes are first copied
+ * into the workspace. Errors, workspace and capture as sgemm().
+ */
+#define SGEMM_I8_MAX_K 131071
+int sgemm_i8(int M, int N, int K, const signed char* A, int lda, const float* scaleA,
+             const signed char* B, int ldb, const float* scaleB, int out_type, void* C, int ldc,
+             void* stream);
+
+/*
+ * The 2-norm of n tensors taken together, and their clipping:
+ *   norm = sqrt(sum of all g^2), coef = min(1, max_norm / (norm + 1e-6)),
+ *   out_i = grads_i * coef.
+ * grads, out, sizes and types are HOST arrays of n: device pointers, element
+ * counts and element types (out_i has the type of grads_i, and is grads_i or
+ * does not overlap any grads_j). *norm (device memory; may be NULL) receives
+ * the norm before clipping. out == NULL computes the norm only. Tensors that
+ * are their own out are not written when coef is 1. Squares are summed in FP32
+ * over at most 32 values and in FP64 beyond, in an order that does not depend
+ * on timing. A NaN among the gradients makes the norm and every output NaN; an
+ * infinity makes the norm infinite and coef 0, as the formula says. The host
+ * arrays are read before the call returns (a captured graph keeps them).
+ * Returns SGEMM_ERR_INVALID_DIM for n < 0 or a size < 0 or above 2^40,
+ * SGEMM_ERR_INVALID_VALUE for max_norm < 0 or NaN or an unknown type,
+ * SGEMM_ERR_NULL_PTR, SGEMM_ERR_MISALIGNED (pointers need element alignment).
+ */
+int sgemm_grad_clip(int n, const void* const* grads, void* const* out, const long long* sizes,
+                    const int* types, float max_norm, float* norm, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
