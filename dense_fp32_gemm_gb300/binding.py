@@ -6,7 +6,9 @@ There is no fallback: if the CUDA library is not built, every call raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import functools
 import os
 import threading
 
@@ -54,6 +56,8 @@ def library_path() -> str:
 def lib() -> ctypes.CDLL:
     """The loaded CUDA library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = library_path()
@@ -99,6 +103,7 @@ def lib() -> ctypes.CDLL:
                 "sgemm_grouped_wgrad": (I, [I, I, I, I, I, I, F, P, I, P, I, P, F, P, I, LL, P]),
                 "sgemm_i8_quantize": (I, [I, I, I, P, I, P, I, P, P]),
                 "sgemm_i8": (I, [I, I, I, P, I, P, P, I, P, I, P, I, P]),
+                "sgemm_grouped_set_tile": (I, [I, I]),
                 "sgemm_grad_clip": (I, [I, P, P, P, P, F, P, P]),
                 "sgemm_strided_batched": (I, [I, I, I, I, I, F, P, I, LL, P, I, LL, F, P, I, LL,
                                               I, P]),
@@ -380,6 +385,12 @@ def sgemm_i8(M, N, K, A, lda, scaleA, B, ldb, scaleB, out_type, C, ldc, stream=N
     return lib().sgemm_i8(M, N, K, A, lda, scaleA, B, ldb, scaleB, out_type, C, ldc, stream)
 
 
+def sgemm_grouped_set_tile(width: int, ctas: int = 1) -> int:
+    """Tile width and CTAs per tile of later grouped and 8-bit products; 0
+    restores the choice by size. Returns the status code."""
+    return lib().sgemm_grouped_set_tile(width, ctas)
+
+
 def sgemm_grad_clip(grads, out, sizes, types, max_norm, norm, stream=None) -> int:
     """The 2-norm of tensors taken together, and out_i = grads_i * min(1,
     max_norm / (norm + 1e-6)): sequences of device addresses, element counts
@@ -423,21 +434,27 @@ def gemm(A, B, C, alpha=1.0, beta=0.0, stream=None):
     return C
 
 
-def _type(t, name):
+@functools.cache
+def _type_codes():
     import torch
-    codes = {torch.float32: SGEMM_TYPE_F32, torch.bfloat16: SGEMM_TYPE_BF16,
-             torch.float16: SGEMM_TYPE_F16}
-    if t.dtype not in codes:
+    return {torch.float32: SGEMM_TYPE_F32, torch.bfloat16: SGEMM_TYPE_BF16,
+            torch.float16: SGEMM_TYPE_F16}
+
+
+def _type(t, name):
+    code = _type_codes().get(t.dtype)
+    if code is None:
         raise ValueError(f"{name} must be float32, bfloat16 or float16")
-    return codes[t.dtype]
+    return code
 
 
 def _pitch(t, name):
     """Row pitch of a row-major matrix (or of the matrices of a 3-D tensor)."""
-    if t.size(-1) > 1 and t.stride(-1) != 1:
+    shape, stride = t.shape, t.stride()
+    cols = shape[-1]
+    if cols > 1 and stride[-1] != 1:
         raise ValueError(f"{name} must be row-major (unit stride along rows)")
-    cols = max(t.size(-1), 1)
-    return max(t.stride(-2), cols) if t.size(-2) > 1 else cols
+    return max(stride[-2], cols, 1) if shape[-2] > 1 else max(cols, 1)
 
 
 def _check(ok, what):
@@ -445,21 +462,33 @@ def _check(ok, what):
         raise ValueError(what)
 
 
-def _same_device(ref, **tensors):
-    _check(ref.is_cuda, "tensors must be on a CUDA device")
-    for name, t in tensors.items():
-        _check(t.device == ref.device, f"{name} is on another device")
-
-
-def _launch_stream(ref, stream):
+def _run(fn, name, device, stream, *args):
+    """One C call on `device` and `stream` (default: its current one)."""
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream(ref.device)
-    return s.cuda_stream
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device)
+    else:
+        handle = stream.cuda_stream
+    if torch.cuda.current_device() == device:
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, handle)
+    if st != SGEMM_OK:
+        raise SgemmError(st, name)
+
+
+def _device(first, *others):
+    """The device index that all tensors share."""
+    device = first.get_device()
+    _check(device >= 0 and all(t.get_device() == device for t in others),
+           "tensors must be on one CUDA device")
+    return device
 
 
 def _offsets(offsets, groups):
     import torch
-    _check(offsets.dtype == torch.int32 and offsets.dim() == 1 and offsets.is_contiguous(),
+    _check(offsets.dtype is torch.int32 and offsets.dim() == 1 and offsets.is_contiguous(),
            "offsets must be a contiguous 1-D int32 tensor")
     _check(offsets.numel() == groups + 1, "offsets must hold one bound more than there are groups")
 
@@ -470,26 +499,26 @@ def grouped_gemm(X, W, offsets, Y=None, op="T", alpha=1.0, beta=0.0, out_dtype=N
     op "T" and (E, K, N) with op "N"; the gradient of X is grouped_gemm(dY, W,
     offsets, op=the other). Without Y a new tensor of out_dtype (default: X's)
     is returned, in which rows outside every group are not set."""
-    import torch
-    _check(op in ("N", "T"), 'op must be "N" or "T"')
+    _check(op == "N" or op == "T", 'op must be "N" or "T"')
     _check(X.dim() == 2 and W.dim() == 3, "X must be 2-D and W 3-D")
-    E, T, K = W.size(0), X.size(0), X.size(1)
-    N = W.size(1) if op == "T" else W.size(2)
-    _check(W.size(2 if op == "T" else 1) == K, "shape mismatch")
-    _check(W.dtype == X.dtype, "X and W must have one type")
+    T, K = X.shape
+    E, N, WK = W.shape
+    if op == "N":
+        N, WK = WK, N
+    _check(WK == K, "shape mismatch")
+    _check(W.dtype is X.dtype, "X and W must have one type")
     _offsets(offsets, E)
+    code = _type(X, "X")
     if Y is None:
         _check(beta == 0.0, "beta needs Y")
-        Y = torch.empty((T, N), dtype=out_dtype or X.dtype, device=X.device)
-    _check(tuple(Y.shape) == (T, N), "shape mismatch")
-    _same_device(X, W=W, offsets=offsets, Y=Y)
-    with torch.cuda.device(X.device):
-        st = sgemm_grouped(SGEMM_OP_T if op == "T" else SGEMM_OP_N, _type(X, "X"), _type(Y, "Y"), E,
-                           T, N, K, float(alpha), X.data_ptr(), _pitch(X, "X"), W.data_ptr(),
-                           _pitch(W, "W"), W.stride(0) if E > 1 else 0, offsets.data_ptr(),
-                           float(beta), Y.data_ptr(), _pitch(Y, "Y"), _launch_stream(X, stream))
-    if st != SGEMM_OK:
-        raise SgemmError(st, "sgemm_grouped")
+        _check(X.is_cuda, "tensors must be on one CUDA device")
+        Y = X.new_empty((T, N), dtype=out_dtype)
+    else:
+        _check(Y.dim() == 2 and Y.shape[0] == T and Y.shape[1] == N, "shape mismatch")
+    _run(lib().sgemm_grouped, "sgemm_grouped", _device(X, W, offsets, Y), stream,
+         SGEMM_OP_T if op == "T" else SGEMM_OP_N, code, _type(Y, "Y"), E, T, N, K, alpha,
+         X.data_ptr(), _pitch(X, "X"), W.data_ptr(), _pitch(W, "W"), W.stride(0) if E > 1 else 0,
+         offsets.data_ptr(), beta, Y.data_ptr(), _pitch(Y, "Y"))
     return Y
 
 
@@ -497,25 +526,23 @@ def grouped_wgrad(A, B, offsets, C=None, alpha=1.0, beta=0.0, out_dtype=None, st
     """C[e] = alpha * A_e.T @ B_e + beta * C[e] over the rows of each group: the
     gradient of W (E, N, K) with A = dY, B = X, of W (E, K, N) with A = X, B = dY.
     Without C a new (E, M, N) tensor of out_dtype (default: A's) is returned."""
-    import torch
-    _check(A.dim() == 2 and B.dim() == 2 and A.size(0) == B.size(0), "shape mismatch")
-    _check(A.dtype == B.dtype, "A and B must have one type")
+    _check(A.dim() == 2 and B.dim() == 2 and A.shape[0] == B.shape[0], "shape mismatch")
+    _check(A.dtype is B.dtype, "A and B must have one type")
     E = offsets.numel() - 1
     _check(E >= 0, "offsets must hold one bound more than there are groups")
     _offsets(offsets, E)
-    T, M, N = A.size(0), A.size(1), B.size(1)
+    (T, M), N = A.shape, B.shape[1]
+    code = _type(A, "A")
     if C is None:
         _check(beta == 0.0, "beta needs C")
-        C = torch.empty((E, M, N), dtype=out_dtype or A.dtype, device=A.device)
-    _check(tuple(C.shape) == (E, M, N), "shape mismatch")
-    _same_device(A, B=B, offsets=offsets, C=C)
-    with torch.cuda.device(A.device):
-        st = sgemm_grouped_wgrad(_type(A, "A"), _type(C, "C"), E, T, M, N, float(alpha),
-                                 A.data_ptr(), _pitch(A, "A"), B.data_ptr(), _pitch(B, "B"),
-                                 offsets.data_ptr(), float(beta), C.data_ptr(), _pitch(C, "C"),
-                                 C.stride(0) if E > 1 else 0, _launch_stream(A, stream))
-    if st != SGEMM_OK:
-        raise SgemmError(st, "sgemm_grouped_wgrad")
+        _check(A.is_cuda, "tensors must be on one CUDA device")
+        C = A.new_empty((E, M, N), dtype=out_dtype)
+    else:
+        _check(tuple(C.shape) == (E, M, N), "shape mismatch")
+    _run(lib().sgemm_grouped_wgrad, "sgemm_grouped_wgrad", _device(A, B, offsets, C), stream, code,
+         _type(C, "C"), E, T, M, N, alpha, A.data_ptr(), _pitch(A, "A"), B.data_ptr(),
+         _pitch(B, "B"), offsets.data_ptr(), beta, C.data_ptr(), _pitch(C, "C"),
+         C.stride(0) if E > 1 else 0)
     return C
 
 
@@ -525,21 +552,26 @@ def i8_quantize(X, Q=None, scale=None, stream=None):
     import torch
     _check(X.dim() == 2, "X must be 2-D")
     M, K = X.shape
+    code = _type(X, "X")
+    _check(X.is_cuda, "tensors must be on one CUDA device")
     if Q is None:
         # rows padded to 16 bytes, so that sgemm_i8 reads them in place
-        Q = torch.empty((M, (K + 15) // 16 * 16), dtype=torch.int8, device=X.device)[:, :K]
+        Q = X.new_empty((M, (K + 15) // 16 * 16), dtype=torch.int8)
+        if K & 15:
+            Q = Q[:, :K]
     if scale is None:
-        scale = torch.empty((M,), dtype=torch.float32, device=X.device)
-    _check(Q.dtype == torch.int8 and tuple(Q.shape) == (M, K), "Q must be int8 of X's shape")
-    _check(scale.dtype == torch.float32 and tuple(scale.shape) == (M,) and scale.is_contiguous(),
-           "scale must be a contiguous float32 vector with one value a row")
-    _same_device(X, Q=Q, scale=scale)
-    with torch.cuda.device(X.device):
-        st = sgemm_i8_quantize(M, K, _type(X, "X"), X.data_ptr(), _pitch(X, "X"), Q.data_ptr(),
-                               _pitch(Q, "Q"), scale.data_ptr(), _launch_stream(X, stream))
-    if st != SGEMM_OK:
-        raise SgemmError(st, "sgemm_i8_quantize")
+        scale = X.new_empty((M,), dtype=torch.float32)
+    _check(Q.dtype is torch.int8 and Q.shape == X.shape, "Q must be int8 of X's shape")
+    _vector(scale, M, "scale")
+    _run(lib().sgemm_i8_quantize, "sgemm_i8_quantize", _device(X, Q, scale), stream, M, K, code,
+         X.data_ptr(), _pitch(X, "X"), Q.data_ptr(), _pitch(Q, "Q"), scale.data_ptr())
     return Q, scale
+
+
+def _vector(s, n, name):
+    import torch
+    _check(s.dtype is torch.float32 and s.dim() == 1 and s.shape[0] == n and s.is_contiguous(),
+           f"{name} must be a contiguous float32 vector of {n}")
 
 
 def i8_gemm(A, scaleA, B, scaleB, C=None, out_dtype=None, stream=None):
@@ -547,24 +579,37 @@ def i8_gemm(A, scaleA, B, scaleB, C=None, out_dtype=None, stream=None):
     sum an exact integer. Without C a new tensor of out_dtype (default bfloat16)
     is returned."""
     import torch
-    _check(A.dim() == 2 and B.dim() == 2 and A.size(1) == B.size(1), "shape mismatch")
-    _check(A.dtype == torch.int8 and B.dtype == torch.int8, "A and B must be int8")
+    _check(A.dim() == 2 and B.dim() == 2 and A.shape[1] == B.shape[1], "shape mismatch")
+    _check(A.dtype is torch.int8 and B.dtype is torch.int8, "A and B must be int8")
     M, K = A.shape
-    N = B.size(0)
-    for s, n, name in ((scaleA, M, "scaleA"), (scaleB, N, "scaleB")):
-        _check(s.dtype == torch.float32 and tuple(s.shape) == (n,) and s.is_contiguous(),
-               f"{name} must be a contiguous float32 vector of {n}")
+    N = B.shape[0]
+    _vector(scaleA, M, "scaleA")
+    _vector(scaleB, N, "scaleB")
     if C is None:
-        C = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=A.device)
-    _check(tuple(C.shape) == (M, N), "shape mismatch")
-    _same_device(A, scaleA=scaleA, B=B, scaleB=scaleB, C=C)
-    with torch.cuda.device(A.device):
-        st = sgemm_i8(M, N, K, A.data_ptr(), _pitch(A, "A"), scaleA.data_ptr(), B.data_ptr(),
-                      _pitch(B, "B"), scaleB.data_ptr(), _type(C, "C"), C.data_ptr(),
-                      _pitch(C, "C"), _launch_stream(A, stream))
-    if st != SGEMM_OK:
-        raise SgemmError(st, "sgemm_i8")
+        _check(A.is_cuda, "tensors must be on one CUDA device")
+        C = A.new_empty((M, N), dtype=out_dtype or torch.bfloat16)
+    else:
+        _check(C.dim() == 2 and C.shape[0] == M and C.shape[1] == N, "shape mismatch")
+    _run(lib().sgemm_i8, "sgemm_i8", _device(A, scaleA, B, scaleB, C), stream, M, N, K,
+         A.data_ptr(), _pitch(A, "A"), scaleA.data_ptr(), B.data_ptr(), _pitch(B, "B"),
+         scaleB.data_ptr(), _type(C, "C"), C.data_ptr(), _pitch(C, "C"))
     return C
+
+
+def _tensor_list(tensors, device):
+    """(addresses, element counts, type codes) of contiguous tensors as arrays
+    that the C call reads. (One pass per property: with hundreds of tensors the
+    calls per tensor are what this costs.)"""
+    import torch
+    T = torch.Tensor
+    _check(set(map(T.get_device, tensors)) == {device}, "gradients must be on one CUDA device")
+    _check(all(map(T.is_contiguous, tensors)), "gradients must be contiguous")
+    codes = _type_codes()
+    try:
+        types = array.array("i", [codes[t.dtype] for t in tensors])
+    except KeyError:
+        raise ValueError("gradients must be float32, bfloat16 or float16") from None
+    return array.array("Q", map(T.data_ptr, tensors)), array.array("q", map(T.numel, tensors)), types
 
 
 def clip_grad_norm(grads, max_norm, out=None, stream=None):
@@ -574,18 +619,17 @@ def clip_grad_norm(grads, max_norm, out=None, stream=None):
     import torch
     grads = list(grads)
     _check(len(grads) > 0, "no gradients")
-    out = grads if out is None else list(out)
-    _check(len(out) == len(grads), "out must hold a tensor for every gradient")
-    for g, o in zip(grads, out):
-        _check(g.is_cuda and g.device == grads[0].device and o.device == g.device,
-               "gradients must be on one CUDA device")
-        _check(g.is_contiguous() and o.is_contiguous(), "gradients must be contiguous")
-        _check(o.dtype == g.dtype and o.shape == g.shape, "out must have the gradients' types and shapes")
-    norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
-    with torch.cuda.device(grads[0].device):
-        st = sgemm_grad_clip([g.data_ptr() for g in grads], [o.data_ptr() for o in out],
-                             [g.numel() for g in grads], [_type(g, "gradients") for g in grads],
-                             float(max_norm), norm.data_ptr(), _launch_stream(norm, stream))
-    if st != SGEMM_OK:
-        raise SgemmError(st, "sgemm_grad_clip")
+    device = grads[0].get_device()
+    _check(device >= 0, "gradients must be on one CUDA device")
+    src, sizes, types = _tensor_list(grads, device)
+    dst = src
+    if out is not None:
+        out = list(out)
+        _check(len(out) == len(grads), "out must hold a tensor for every gradient")
+        dst, osizes, otypes = _tensor_list(out, device)
+        _check(osizes == sizes and otypes == types, "out must have the gradients' types and sizes")
+    norm = grads[0].new_empty((), dtype=torch.float32)
+    _run(lib().sgemm_grad_clip, "sgemm_grad_clip", device, stream, len(grads),
+         src.buffer_info()[0], dst.buffer_info()[0], sizes.buffer_info()[0], types.buffer_info()[0],
+         max_norm, norm.data_ptr())
     return norm

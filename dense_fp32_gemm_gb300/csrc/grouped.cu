@@ -2,7 +2,9 @@
 // expert with ragged row counts) and sgemm_i8 (8-bit integer product with
 // token and channel scales): argument checks, tile width, operand maps and
 // the launch of ragged_kernel.
+#include <atomic>
 #include <cstdio>
+#include <mutex>
 
 #include "ragged_launch.cuh"
 
@@ -27,46 +29,100 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encode() {
 
 namespace {
 
-// Rows of `cols` elements from pitch ld (and matrix pitch stride) to one
-// after another at pitch ldo.
-template <typename E>
-__global__ void pack_kernel(const E* __restrict__ src, long long ld, long long stride, int rows,
-                            int cols, int batch, E* __restrict__ dst, long long ldo) {
-  // may start before the kernel ahead on the stream has finished
-  ptx::griddep_wait();
-  const long long total = (long long)rows * batch;
-  for (long long r = blockIdx.x; r < total; r += gridDim.x) {
-    const E* s = src + (r / rows) * stride + (r % rows) * ld;
-    E* d = dst + r * ldo;
-    for (int c = threadIdx.x; c < cols; c += blockDim.x) d[c] = s[c];
+// 16 bytes from any address, by the widest loads that its alignment allows.
+__device__ __forceinline__ uint4 load16(const unsigned char* s) {
+  union {
+    uint4 v;
+    uint64_t d[2];
+    uint32_t w[4];
+    uint16_t h[8];
+    unsigned char b[16];
+  } u;
+  const unsigned a = (unsigned)reinterpret_cast<uintptr_t>(s);
+  if ((a & 15u) == 0) {
+    u.v = __ldg(reinterpret_cast<const uint4*>(s));
+  } else if ((a & 7u) == 0) {
+    u.d[0] = __ldg(reinterpret_cast<const unsigned long long*>(s));
+    u.d[1] = __ldg(reinterpret_cast<const unsigned long long*>(s) + 1);
+  } else if ((a & 3u) == 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u.w[i] = __ldg(reinterpret_cast<const uint32_t*>(s) + i);
+  } else if ((a & 1u) == 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u.h[i] = __ldg(reinterpret_cast<const uint16_t*>(s) + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) u.b[i] = __ldg(s + i);
   }
+  return u.v;
 }
 
-template <typename E>
-cudaError_t pack(const Operand& op, void* dst, int sms, cudaStream_t stream) {
-  cudaLaunchConfig_t lc = {};
-  cudaLaunchAttribute la[1];
-  la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  la[0].val.programmaticStreamSerializationAllowed = 1;
-  const long long rows = op.rows * op.batch;
-  lc.gridDim = dim3((unsigned)(rows < sms * 8 ? rows : sms * 8));
-  lc.blockDim = dim3(256);
-  lc.stream = stream;
-  lc.attrs = la;
-  lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, pack_kernel<E>, static_cast<const E*>(op.ptr), op.ld, op.stride,
-                            (int)op.rows, (int)op.cols, op.batch, static_cast<E*>(dst),
-                            op.packed_ld());
+// Rows of `bytes` bytes from pitch ld (and matrix pitch stride), any alignment,
+// to one after another at pitch ldo, a multiple of 16 bytes: a copy, or (WIDEN)
+// 8-bit integers as F16. A thread moves 16 bytes of the source at a time;
+// what lies between a row's end and its pitch is not set beyond its last 16
+// bytes, which are filled with zeros.
+template <bool WIDEN>
+__global__ void __launch_bounds__(256)
+    pack_kernel(const unsigned char* __restrict__ src, long long ld, long long stride, int rows,
+                int bytes, long long total, unsigned char* __restrict__ dst, long long ldo) {
+  // may start before the kernel ahead on the stream has finished
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const int chunks = (bytes + 15) / 16;   // per row
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+    const long long r = i / chunks;
+    const int c = (int)(i - r * chunks) * 16;
+    const unsigned char* s = src + (r / rows) * stride + (r % rows) * ld + c;
+    uint4 v;
+    if (c + 16 <= bytes) {
+      v = load16(s);
+    } else {
+      union {
+        uint4 v;
+        unsigned char b[16];
+      } u;
+      u.v = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        if (c + k < bytes) u.b[k] = s[k];
+      v = u.v;
+    }
+    if (WIDEN) {
+      const uint2 a = i8_to_f16(v.x), b = i8_to_f16(v.y), d = i8_to_f16(v.z), e = i8_to_f16(v.w);
+      uint4* o = reinterpret_cast<uint4*>(dst + r * ldo + 2 * c);
+      o[0] = make_uint4(a.x, a.y, b.x, b.y);
+      // (a row's pitch is a multiple of 8 F16 values, not always of 16)
+      if (2 * c + 16 < ldo) o[1] = make_uint4(d.x, d.y, e.x, e.y);
+    } else {
+      *reinterpret_cast<uint4*>(dst + r * ldo + c) = v;
+    }
+  }
 }
 
 }  // namespace
 
-cudaError_t pack_operand(Operand* op, void* dst, int sms, cudaStream_t stream) {
-  const cudaError_t e = op->elem == 1   ? pack<uint8_t>(*op, dst, sms, stream)
-                        : op->elem == 2 ? pack<uint16_t>(*op, dst, sms, stream)
-                                        : pack<uint32_t>(*op, dst, sms, stream);
+cudaError_t pack_operand(Operand* op, bool widen, void* dst, int sms, cudaStream_t stream) {
+  const long long bytes = op->cols * op->elem, total = op->rows * op->batch * ((bytes + 15) / 16);
+  const long long ldo = op->packed_pitch(widen);
+  cudaLaunchConfig_t lc = {};
+  cudaLaunchAttribute la[1];
+  la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  la[0].val.programmaticStreamSerializationAllowed = 1;
+  const long long blocks = (total + 255) / 256;
+  lc.gridDim = dim3((unsigned)(blocks < sms * 32ll ? blocks : sms * 32ll));
+  lc.blockDim = dim3(256);
+  lc.stream = stream;
+  lc.attrs = la;
+  lc.numAttrs = 1;
+  const unsigned char* src = static_cast<const unsigned char*>(op->ptr);
+  const cudaError_t e =
+      cudaLaunchKernelEx(&lc, widen ? pack_kernel<true> : pack_kernel<false>, src,
+                         op->ld * op->elem, op->stride * op->elem, (int)op->rows, (int)bytes, total,
+                         static_cast<unsigned char*>(dst), ldo);
+  if (widen) op->elem = 2;
   op->ptr = dst;
-  op->ld = op->packed_ld();
+  op->ld = ldo / op->elem;
   op->stride = op->rows * op->ld;
   return e;
 }
@@ -97,17 +153,69 @@ bool misaligned(const void* p, int bytes) {
   return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) != 0;
 }
 
-// Tile width in q. rows: wide enough that a typical group's rows fit one
-// tile, at most 256 (128 for converted operands).
-int rows_width(long long rows_per_group, int widest) {
-  int bq = 32;
-  while (bq < widest && bq < rows_per_group) bq *= 2;
-  return bq;
+// The built kernels, and per device what prepare() said of each.
+constexpr int kMaxDevices = 64, kMaxForms = 24;
+struct Built {
+  bool ready;
+  int workers;
+};
+std::mutex g_mutex;
+Built g_built[kMaxDevices][kMaxForms];
+// Tile width and CTAs per worker for later calls (tests, measurements); 0: by rule.
+std::atomic<int> g_width{0}, g_ctas{0};
+
+const FormEntry* form_entry(int i) {
+  if (i < kNumForms16) return &kForms16[i];
+  i -= kNumForms16;
+  if (i < kNumFormsF32) return &kFormsF32[i];
+  i -= kNumFormsF32;
+  return i < kNumFormsI8 ? &kFormsI8[i] : nullptr;
 }
 
-// src: a Src; the operands as stored. Fills the maps (packing what TMA cannot
-// read), the workspace fields of `p`, and launches.
-int run(int src, int type, Params p, Operand op_p, Operand op_q, int bq, cudaStream_t stream,
+// The entry of a form and its resident workers on `dev` (null: not built or,
+// for pairs, not runnable).
+const FormEntry* find_form(int dev, int sms, int src, int bq, int cl, int* workers) {
+  if (dev < 0 || dev >= kMaxDevices) return nullptr;
+  for (int i = 0; const FormEntry* f = form_entry(i); ++i) {
+    if (f->form.src != src || f->form.bq != bq || f->form.cl != cl) continue;
+    std::lock_guard<std::mutex> lock(g_mutex);
+    Built& b = g_built[dev][i];
+    if (!b.ready) {
+      if (f->prepare(sms, &b.workers) != cudaSuccess) {
+        cudaGetLastError();
+        return nullptr;
+      }
+      b.ready = true;
+    }
+    *workers = b.workers;
+    return b.workers > 0 ? f : nullptr;
+  }
+  return nullptr;
+}
+
+// The tile of a call. rows: `per` is the mean number of rows of a group, wgrad:
+// the rows of its output (Q).
+struct Tile {
+  int src, bq, cl;
+};
+Tile choose_tile(int src, const Params& p, long long per, int sms) {
+  const int least = p.wgrad ? 64 : 16;
+  const int widest = src == k16 || src == kI8Wide ? 256 : 128;
+  int bq = least;
+  while (bq < widest && bq < per) bq *= 2;
+  Tile t{src, bq, 1};
+  if (src == kI8Wide) return Tile{src, 256, 2};
+  // pairs: the widest tiles, at least one for every pair of SMs
+  if (bq == widest) {
+    const long long q = p.wgrad ? (long long)p.E * cdiv(p.Q, bq) : (long long)p.T / bq;
+    if (cdiv(p.P, 2 * BP) * q >= sms / 2) t.cl = 2;
+  }
+  return t;
+}
+
+// The operands as stored. Fills the maps (copying what TMA cannot read), the
+// workspace fields of `p`, and launches.
+int run(int src, int type, Params p, Operand op_p, Operand op_q, long long per, cudaStream_t stream,
         const char* what) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -118,33 +226,43 @@ int run(int src, int type, Params p, Operand op_p, Operand op_q, int bq, cudaStr
   if (st != SGEMM_OK) return st;
   if (tensor_map_encode() == nullptr) return SGEMM_ERR_LAUNCH;
 
-  // the most tiles the offsets can give
-  const long long ptiles = cdiv(p.P, BP);
-  const long long qtiles = p.wgrad ? (long long)p.E * cdiv(p.Q, bq)
-                                   : (long long)p.T / bq + (p.T < p.E ? p.T : p.E);
-  if (ptiles * qtiles > 0x7fffffffLL) return SGEMM_ERR_INVALID_DIM;
-  const bool reads = p.K > 0;
+  Tile t = choose_tile(src, p, per, sms);
+  int workers = 0;
+  const FormEntry* form = nullptr;
+  const int width = g_width.load(), ctas = g_ctas.load();
+  if (width > 0 && (!p.wgrad || width >= 64)) form = find_form(dev, sms, src, width, ctas, &workers);
+  if (form == nullptr) form = find_form(dev, sms, t.src, t.bq, t.cl, &workers);
+  if (form == nullptr && t.cl == 2) form = find_form(dev, sms, t.src, t.bq, 1, &workers);
+  if (form == nullptr) return SGEMM_ERR_LAUNCH;
+  const int bq = form->form.bq, cl = form->form.cl;
+
+  // tiles and k-slices are numbered with 32-bit integers
   const int slice = src == kF32 ? 32 : 64;
-  // tiles are cut along k only when there may be fewer of them than CTAs
-  const long long least = p.wgrad ? ptiles * qtiles : ptiles * (p.T / bq > 0 ? p.T / bq : 1);
-  const bool may_split = reads && 2 * least <= sms;
-  const size_t pack_p = reads ? op_p.packed_bytes() : 0, pack_q = reads ? op_q.packed_bytes() : 0;
-  const size_t partial = may_split ? (size_t)sms * BP * bq * 4 : 0;
+  const long long tiles = (long long)cdiv(p.P, BP * cl) *
+                          (p.wgrad ? (long long)p.E * cdiv(p.Q, bq)
+                                   : (long long)p.T / bq + (p.T < p.E ? p.T : p.E));
+  const long long slices =
+      p.wgrad ? (long long)cdiv(p.P, BP * cl) * cdiv(p.Q, bq) * ((long long)p.T / slice + 2 * p.E)
+              : tiles * (cdiv(p.K, slice) + 1);
+  if (tiles > 0x7fffffffLL || slices > 0x7fffffffLL) return SGEMM_ERR_INVALID_DIM;
+
+  const bool reads = p.K > 0;
+  const bool widen = src == kI8Wide;
+  const size_t pack_p = reads ? op_p.packed_bytes(widen) : 0;
+  const size_t pack_q = reads ? op_q.packed_bytes(widen) : 0;
+  const size_t partial = (size_t)workers * cl * 2 * BP * bq * 4;
   float* ws = nullptr;
   uint32_t epoch = 0;
-  st = library_workspace(dev, stream, (pack_p + pack_q + partial) / 4, (size_t)sms, &ws, &p.status,
-                         &p.counters, &epoch);
+  st = library_workspace(dev, stream, (pack_p + pack_q + partial) / 4, (size_t)workers * cl, &ws,
+                         &p.status, &p.counters, &epoch);
   if (st != SGEMM_OK) return st;
   char* at = reinterpret_cast<char*>(ws);
-  if (pack_p && pack_operand(&op_p, at, sms, stream) != cudaSuccess) {
+  if ((pack_p && pack_operand(&op_p, widen, at, sms, stream) != cudaSuccess) ||
+      (pack_q && pack_operand(&op_q, widen, at + pack_p, sms, stream) != cudaSuccess)) {
     cudaGetLastError();
     return SGEMM_ERR_LAUNCH;
   }
-  if (pack_q && pack_operand(&op_q, at + pack_p, sms, stream) != cudaSuccess) {
-    cudaGetLastError();
-    return SGEMM_ERR_LAUNCH;
-  }
-  p.partials = may_split ? reinterpret_cast<float*>(at + pack_p + pack_q) : nullptr;
+  p.partials = reinterpret_cast<float*>(at + pack_p + pack_q);
   p.timeout_ns = library_wait_timeout_ns();
 
   CUtensorMap mp = {}, mq = {};
@@ -157,20 +275,17 @@ int run(int src, int type, Params p, Operand op_p, Operand op_q, int bq, cudaStr
                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16));
     const int row_bytes = src == kI8 ? 64 : 128;
     if (!encode_operand(&mp, op_p, dt, row_bytes, p.p_mn ? slice : BP) ||
-        !encode_operand(&mq, op_q, dt, row_bytes, p.q_mn ? slice : bq))
+        !encode_operand(&mq, op_q, dt, row_bytes, p.q_mn ? slice : bq / cl))
       return SGEMM_ERR_LAUNCH;
   }
-  const cudaError_t e = src == k16    ? launch_k16(dev, bq, sms, p, mp, mq, stream)
-                        : src == kF32 ? launch_f32(dev, bq, sms, p, mp, mq, stream)
-                                      : launch_i8(dev, bq, sms, p, mp, mq, stream);
-  if (e != cudaSuccess) {
+  if (form->launch(workers, p, mp, mq, stream) != cudaSuccess) {
     cudaGetLastError();
     return SGEMM_ERR_LAUNCH;
   }
   char text[160];
-  snprintf(text, sizeof(text), "%s_%s_128x%dx%d grid=%d chunk=%d%s%s", what,
+  snprintf(text, sizeof(text), "%s_%s_%dx%dx%d cluster=%d grid=%d%s%s", what,
            src == k16 ? (type == SGEMM_TYPE_BF16 ? "bf16" : "f16") : (src == kF32 ? "f32" : "i8"),
-           bq, slice, sms, p.chunk, pack_p ? " p=copied" : "", pack_q ? " q=copied" : "");
+           BP * cl, bq, slice, cl, workers * cl, pack_p ? " p=copied" : "", pack_q ? " q=copied" : "");
   note_last_config(text);
   return SGEMM_OK;
 }
@@ -180,7 +295,7 @@ int run(int src, int type, Params p, Operand op_p, Operand op_q, int bq, cudaStr
 // a truncating sum of 4096 values is far below their rounding.
 int accumulation_chunk(int src, int out_type) {
   if (src == kF32) return 2;
-  if (src == kI8) return Geo<kI8, 32>::kExactChunk;
+  if (src == kI8 || src == kI8Wide) return kExactChunk;
   return out_type == kOutF32 ? 4 : 0x40000000;
 }
 
@@ -229,8 +344,8 @@ SGEMM_API int sgemm_grouped(int op, int type, int out_type, int E, int T, int N,
   p.chunk = ragged::accumulation_chunk(src, out_type);
   const Operand w{W, eb, op == SGEMM_OP_N ? K : N, op == SGEMM_OP_N ? N : K, ldw, strideW, E};
   const Operand x{X, eb, T, K, ldx, 0, 1};
-  const int bq = ragged::rows_width(((long long)T + E - 1) / E, src == ragged::k16 ? 256 : 128);
-  return ragged::run(src, type, p, w, x, bq, static_cast<cudaStream_t>(stream), "grouped");
+  return ragged::run(src, type, p, w, x, ((long long)T + E - 1) / E,
+                     static_cast<cudaStream_t>(stream), "grouped");
 }
 
 SGEMM_API int sgemm_grouped_wgrad(int type, int out_type, int E, int T, int M, int N, float alpha,
@@ -271,9 +386,7 @@ SGEMM_API int sgemm_grouped_wgrad(int type, int out_type, int E, int T, int M, i
   p.beta = beta;
   p.chunk = ragged::accumulation_chunk(src, out_type);
   const Operand pb{B, eb, T, N, ldb, 0, 1}, qa{A, eb, T, M, lda, 0, 1};
-  int bq = src == ragged::k16 ? 256 : 128;
-  while (bq > 64 && bq / 2 >= M) bq /= 2;
-  return ragged::run(src, type, p, pb, qa, bq, static_cast<cudaStream_t>(stream), "wgrad");
+  return ragged::run(src, type, p, pb, qa, M, static_cast<cudaStream_t>(stream), "wgrad");
 }
 
 SGEMM_API int sgemm_i8(int M, int N, int K, const signed char* A, int lda, const float* scaleA,
@@ -305,6 +418,21 @@ SGEMM_API int sgemm_i8(int M, int N, int K, const signed char* A, int lda, const
   p.scale_q = scaleA;
   p.chunk = ragged::accumulation_chunk(ragged::kI8, out_type);
   const Operand w{B, 1, N, K, ldb, 0, 1}, x{A, 1, M, K, lda, 0, 1};
-  return ragged::run(ragged::kI8, 0, p, w, x, ragged::rows_width(M, 128),
-                     static_cast<cudaStream_t>(stream), "i8");
+  // Many rows: both operands are widened to F16 first and the widest tiles run
+  // (4 bytes written and read per weight, against converting a weight tile
+  // once for every 128 rows).
+  const int src = M >= 512 ? ragged::kI8Wide : ragged::kI8;
+  return ragged::run(src, SGEMM_TYPE_F16, p, w, x, M, static_cast<cudaStream_t>(stream), "i8");
+}
+
+SGEMM_API int sgemm_grouped_set_tile(int width, int ctas) {
+  if (width != 0) {
+    bool built = false;
+    for (int i = 0; const ragged::FormEntry* f = ragged::form_entry(i); ++i)
+      built = built || (f->form.bq == width && f->form.cl == ctas);
+    if (!built) return SGEMM_ERR_INVALID_VALUE;
+  }
+  ragged::g_width.store(width);
+  ragged::g_ctas.store(ctas);
+  return SGEMM_OK;
 }

@@ -4,15 +4,14 @@
 namespace sgemm_gb300 {
 namespace ragged {
 
-cudaError_t launch_f32(int dev, int bq, int grid, const Params& p, const CUtensorMap& mp,
-                       const CUtensorMap& mq, cudaStream_t stream) {
-  switch (bq) {
-    case 32: return launch_one<kF32, 32>(dev, grid, p, mp, mq, stream);
-    case 64: return launch_one<kF32, 64>(dev, grid, p, mp, mq, stream);
-    case 128: return launch_one<kF32, 128>(dev, grid, p, mp, mq, stream);
-    default: return cudaErrorInvalidValue;
-  }
-}
+extern const FormEntry kFormsF32[] = {
+    SGEMM_GB300_FORM(kF32, 16, 1),
+    SGEMM_GB300_FORM(kF32, 32, 1),
+    SGEMM_GB300_FORM(kF32, 64, 1),
+    SGEMM_GB300_FORM(kF32, 128, 1),
+    SGEMM_GB300_FORM(kF32, 128, 2),
+};
+extern const int kNumFormsF32 = sizeof(kFormsF32) / sizeof(kFormsF32[0]);
 
 }  // namespace ragged
 }  // namespace sgemm_gb300

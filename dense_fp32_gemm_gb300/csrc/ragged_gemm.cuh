@@ -21,7 +21,8 @@
 //   kI8   8-bit integers, turned by converter warps into F16 (exact), since
 //         sm_103a has no integer tensor instruction of this generation. A
 //         product is at most 2^14, so the FP32 sums of 1024 products are
-//         exact integers.
+//         exact integers;
+//   kI8Wide  the same integers, already as F16 in the workspace.
 //
 // Accumulation. The tensor core adds into FP32 with truncation, an error that
 // grows with the number of instructions. For 32-bit results a tile's sum is
@@ -29,14 +30,30 @@
 // tensor-memory accumulators and is added in registers (round to nearest; for
 // kI8 as 32-bit integers) while the other is filled.
 //
-// Roles: warp 0 issues the TMA loads, warp 1 the MMAs, warps 2-9 read the
+// Kernel forms (CL): single CTAs, or clusters of two on vertically adjacent
+// tiles whose even CTA issues M = 256 MMAs over both (cta_group::2): each CTA
+// holds its 128 rows of P and half of the Q tile in shared memory and its 128
+// lanes of the accumulator in tensor memory, so a slice moves two thirds of
+// the bytes per multiply-add of a single 128 x 256 tile. Each CTA loads only
+// its own tiles.
+//
+// Schedule. The work list is computed on the device from the offsets: every
+// CTA scans them. Whole tiles are dealt out in waves of one per worker (a CTA
+// or a pair) while at least two waves are left; the k-slices of the tiles that
+// remain are dealt out evenly, each worker a contiguous range, so that it ends
+// with (or, with few tiles, is) part of a tile. The worker that arrives last
+// at a cut tile adds the partial tiles in the order of k, so results do not
+// depend on the order of arrival -- no CTA waits for another. (Dealing out all
+// tiles by slices would balance sums of different lengths exactly, but
+// spreads the workers over all groups at once: the weight gradient of 8 groups
+// of 1024 x (4096 + 1024) took ten times as long, its tiles no longer shared
+// in L2.)
+//
+// Roles: warp 0 issues the TMA loads (both CTAs of a pair signal the even
+// one's barriers), warp 1 the MMAs (in the odd CTA it reports the stages that
+// threads write there: conversions, cleared rows), warps 4-11 read the
 // accumulators (two warps per lane quarter, each half of the columns) and
-// write the output, warps 10-17 (kF32, kI8) convert. The work list is
-// computed on the device from the offsets: every CTA scans them, then takes
-// the units blockIdx.x, + gridDim.x, ... With fewer tiles than CTAs each
-// tile's sum is cut into ranges along k; the CTA that arrives last adds the
-// partial tiles in a fixed order (so results do not depend on the order of
-// arrival) -- no CTA waits for another.
+// write the output, warps 12-19 (kF32, kI8) convert.
 //
 // Every wait is bounded; a CTA that gives up drains its copies and MMAs,
 // frees its tensor memory and returns. Offsets are clamped to the row count,
@@ -55,12 +72,12 @@
 namespace sgemm_gb300 {
 namespace ragged {
 
-enum Src : int { k16 = 0, kF32 = 1, kI8 = 2 };
+enum Src : int { k16 = 0, kF32 = 1, kI8 = 2, kI8Wide = 3 };
 enum OutType : int { kOutF32 = 0, kOutBf16 = 1, kOutF16 = 2 };
 
 constexpr int BP = 128;            // tile height in p (MMA M)
 constexpr int kMaxGroups = 1024;   // the scanned offsets live in shared memory
-constexpr int kEpiWarp0 = 2, kEpiWarps = 8, kEpiThreads = kEpiWarps * 32;
+constexpr int kEpiWarp0 = 4, kEpiWarps = 8, kEpiThreads = kEpiWarps * 32;
 constexpr int kConvWarp0 = kEpiWarp0 + kEpiWarps, kConvWarps = 8;
 
 struct Params {
@@ -69,7 +86,7 @@ struct Params {
   int P, Q;               // output columns; output rows per group (wgrad)
   int K;                  // contraction length (rows); 0 skips the products
   int p_mn, q_mn;         // operand stored with k as its slow dimension
-  int bf16;               // k16: operand type (else F16)
+  int bf16;               // k16: operand type (else F16; kI8Wide is F16)
   const int* offsets;     // E + 1 row bounds on the device; null: one group of T rows
   void* out;
   long long ldo, stride_o;  // row pitch; pitch between the groups' outputs (wgrad)
@@ -78,25 +95,27 @@ struct Params {
   const float* scale_p;   // kI8: scales of p and q
   const float* scale_q;
   int chunk;              // k-slices per tensor-memory accumulation
-  float* partials;        // gridDim.x tiles of BQ x 128 floats (when tiles are cut along k)
-  uint32_t* counters;     // arrivals per cut tile, zero between launches
+  float* partials;        // two tiles of BQ x 128 floats per CTA
+  uint32_t* counters;     // arrivals at a cut tile, one per CTA, zero between launches
   int* status;
   long long timeout_ns;
 };
 
 // Stage geometry. Raw tiles as TMA writes them (kSlice elements of k), and
 // the converted operand tiles (kF32, kI8).
-template <int SRC, int BQ>
+template <int SRC, int BQ, int CL>
 struct Geo {
+  static constexpr bool kConv = SRC == kF32 || SRC == kI8;
+  static constexpr bool kInt = SRC == kI8 || SRC == kI8Wide;
   static constexpr int kSlice = SRC == kF32 ? 32 : 64;
-  static constexpr int kElem = SRC == k16 ? 2 : (SRC == kF32 ? 4 : 1);
-  static constexpr int kRawRow = kSlice * kElem;               // 128, 128, 64 bytes
-  static constexpr int kRawP = BP * kRawRow, kRawQ = BQ * kRawRow;
+  static constexpr int kElem = SRC == kF32 ? 4 : (SRC == kI8 ? 1 : 2);
+  static constexpr int kRows = BQ / CL;                         // rows of Q in one CTA
+  static constexpr int kRawRow = kSlice * kElem;                // 128, 128, 64 bytes
+  static constexpr int kRawP = BP * kRawRow, kRawQ = kRows * kRawRow;
   static constexpr int kRaw = kRawP + kRawQ;
   static constexpr int kParts = SRC == kF32 ? 3 : 1;
-  static constexpr int kOpP = BP * kSlice * 2, kOpQ = BQ * kSlice * 2;  // one part
-  static constexpr int kOp = SRC == k16 ? 0 : kParts * (kOpP + kOpQ);
-  static constexpr bool kConv = SRC != k16;
+  static constexpr int kOpP = BP * kSlice * 2, kOpQ = kRows * kSlice * 2;  // one part
+  static constexpr int kOp = kConv ? kParts * (kOpP + kOpQ) : 0;
   static constexpr int kRegion = 192 * 1024;
   // operand stages first (at most 4), then as many raw stages as fit
   static constexpr int kOpFit = kConv ? (kRegion - 2 * kRaw) / kOp : 0;
@@ -106,23 +125,42 @@ struct Geo {
   static_assert(!kConv || kOpStages >= 2, "operand stages");
   static_assert(kRawStages >= 2, "raw stages");
   static constexpr int kThreads = (kConv ? kConvWarp0 + kConvWarps : kConvWarp0) * 32;
+  // A thread of the epilogue holds BQ / 2 sums. For the widest tiles of a kind
+  // they need more registers than the launch gives every thread, so the other
+  // warpgroups give some up (what is raised is what is lowered).
+  static constexpr bool kMoveRegs = BQ == (kConv ? 128 : 256);
+  static constexpr int kRegs = kConv ? 96 : 168;      // at launch: 640 or 384 threads
+  static constexpr int kRegsFew = kConv ? 48 : 72, kRegsMany = kConv ? 144 : 216;
+  static constexpr int kRegsConv = 72;
+  static_assert((kThreads == 640 || !kConv) && (kThreads == 384 || kConv) &&
+                    128 * kRegsFew + 256 * kRegsMany + (kConv ? 256 * kRegsConv : 0) <=
+                        kThreads * kRegs &&
+                    kThreads * kRegs <= 65536,
+                "register shares");
   static constexpr int kTmemCols = 2 * BQ;
   static_assert(kTmemCols >= 32 && kTmemCols <= 512, "tensor memory");
-  // FP32 sums leave tensor memory at the latest after this many slices when
-  // they have to be exact integers (kI8: 1024 products of at most 2^14)
-  static constexpr int kExactChunk = 1024 / kSlice;
+  // (a K-major tile of 8-row groups, an MN-major one of 64-wide chunks)
+  static_assert(kRows % 8 == 0 && BQ % 16 == 0 && BQ <= 256, "tile width");
 };
+// FP32 sums of integers leave tensor memory at the latest after this many
+// 64-wide slices (1024 products of at most 2^14).
+constexpr int kExactChunk = 1024 / 64;
+// Fewest k-slices a worker gets when the tiles of a small problem are cut.
+constexpr int kMinSlices = 4;
 
 struct Shared {
   uint64_t raw_full[12], raw_empty[12];
   uint64_t op_full[4], op_empty[4];
+  uint64_t peer_full[12];       // even CTA of a pair: the odd CTA's stage has landed
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain, epi_sync;
   uint32_t tmem;
   int abort;
-  int last;                     // this CTA's unit is the last of its tile
-  int tiles, splits;
-  int row0[kMaxGroups], rows[kMaxGroups], first[kMaxGroups + 1];  // the scanned groups
+  int last;                     // this CTA arrived last at its cut tile
+  int tiles, dp;                // tiles; how many of them are dealt out whole
+  int base, len, cutters;       // slices dealt out: first position, number, workers
+  // the scanned groups: first row, rows, number and slice position of the first tile
+  int row0[kMaxGroups], rows[kMaxGroups], first[kMaxGroups], pos[kMaxGroups];
 };
 constexpr int kSharedBytes = ((int)sizeof(Shared) + 15) / 16 * 16;
 constexpr int kSmemBytes = 1024 + 192 * 1024 + kSharedBytes;
@@ -130,41 +168,117 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 
 __host__ __device__ constexpr int cdiv(int a, int b) { return a / b + (a % b != 0); }
 
+// Slices that a tile of a group counts for (one without a sum counts one, so
+// that it has a place in the list).
+template <int SLICE>
+__device__ __forceinline__ int tile_slices(const Params& p, int rows) {
+  return max(1, cdiv(p.K == 0 ? 0 : (p.wgrad ? rows : p.K), SLICE));
+}
+
+// Part of a worker's list: tile (p0, q0) of group e, its k-slices kb .. ke.
 struct Unit {
   int e, p0, q0;       // group, first p, first q within the group
   int row0, nq;        // first token row of the group; valid q in the tile
   int kb, ke, klen;    // slices of this unit, contraction length
-  int tile, part;      // tile number, which k-range
+  int c0, parts;       // workers c0 .. c0 + parts - 1 share the tile
 };
 
-// Unit u of the work list (see Shared::first): tiles of a group are
-// consecutive, q fastest, so that CTAs running together share weight tiles.
-template <int SLICE, int BQ>
-__device__ __forceinline__ Unit get_unit(const Params& p, const Shared* sh, int u) {
-  Unit w;
-  const int S = sh->splits;
-  w.tile = u / S;
-  w.part = u - w.tile * S;
-  int lo = 0, hi = p.E - 1;     // last group with first <= tile
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (sh->first[mid] <= w.tile) lo = mid; else hi = mid - 1;
+// Walks the list of worker w of `workers`; every role walks its own copy.
+template <int SLICE, int BQ, int CL>
+struct Walk {
+  const Params& p;
+  const Shared* sh;
+  int w, workers, t, at, end;
+  __device__ __forceinline__ Walk(const Params& p_, const Shared* sh_, int w_, int workers_)
+      : p(p_), sh(sh_), w(w_), workers(workers_), t(w_), at(0), end(0) {
+    if (w < sh->cutters) {
+      at = sh->base + (int)((long long)sh->len * w / sh->cutters);
+      end = sh->base + (int)((long long)sh->len * (w + 1) / sh->cutters);
+    }
   }
-  w.e = lo;
-  const int j = w.tile - sh->first[lo];
-  w.row0 = sh->row0[lo];
-  const int n = sh->rows[lo];
-  const int qdim = p.wgrad ? p.Q : n;
-  const int qt = cdiv(qdim, BQ);
-  const int tp = j / qt, tq = j - tp * qt;
-  w.p0 = tp * BP;
-  w.q0 = tq * BQ;
-  w.nq = min(BQ, qdim - w.q0);
-  w.klen = p.K == 0 ? 0 : (p.wgrad ? n : p.K);
-  const int ks = cdiv(w.klen, SLICE);
-  w.kb = (int)((long long)ks * w.part / S);
-  w.ke = (int)((long long)ks * (w.part + 1) / S);
-  return w;
+  // last group whose entry is at most v (of equal entries the last, which has
+  // the tiles)
+  __device__ __forceinline__ int find(const int* a, int v) const {
+    int lo = 0, hi = p.E - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (a[mid] <= v) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+  }
+  // the worker that has the slice at position v
+  __device__ __forceinline__ int owner(int v) const {
+    return (int)((((long long)(v - sh->base) + 1) * sh->cutters - 1) / sh->len);
+  }
+  __device__ __forceinline__ bool next(Unit& u) {
+    int j, slices;
+    u.parts = 1;
+    if (t < sh->dp) {
+      u.e = find(sh->first, t);
+      j = t - sh->first[u.e];
+      slices = tile_slices<SLICE>(p, sh->rows[u.e]);
+      u.kb = 0;
+      u.ke = slices;
+      t += workers;
+    } else if (at < end) {
+      u.e = find(sh->pos, at);
+      slices = tile_slices<SLICE>(p, sh->rows[u.e]);
+      const int off = at - sh->pos[u.e];
+      j = off / slices;
+      u.kb = off - j * slices;
+      u.ke = min(slices, u.kb + end - at);
+      if (u.ke - u.kb < slices) {
+        u.c0 = owner(at - u.kb);
+        u.parts = owner(at - u.kb + slices - 1) - u.c0 + 1;
+      }
+      at += u.ke - u.kb;
+    } else {
+      return false;
+    }
+    u.row0 = sh->row0[u.e];
+    const int n = sh->rows[u.e];
+    const int qdim = p.wgrad ? p.Q : n;
+    const int qt = cdiv(qdim, BQ);
+    const int tp = j / qt;     // q fastest: workers running together share weight tiles
+    u.p0 = tp * (BP * CL);
+    u.q0 = (j - tp * qt) * BQ;
+    u.nq = min(BQ, qdim - u.q0);
+    u.klen = p.K == 0 ? 0 : (p.wgrad ? n : p.K);
+    if (u.klen == 0) u.ke = u.kb;   // nothing to add
+    return true;
+  }
+};
+
+// Waits for a barrier's phase, at most timeout_ns: then the abort word is set,
+// the code recorded, and false returned. The clock is read only after some
+// dozens of polls: a read takes longer than a k-slice.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_w,
+                                         int* status, int code, long long timeout_ns) {
+  uint64_t t0 = 0;
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (ptx::mbar_try_wait(bar, parity)) return true;
+    if (*abort_w) return false;
+    const uint64_t t = ptx::global_ns();
+    if (t0 == 0) {
+      t0 = t;
+    } else if ((long long)(t - t0) > timeout_ns) {
+      *abort_w = 1;
+      atomicCAS(status, 0, code);
+      return false;
+    }
+  }
+}
+
+// The same for a barrier that threads of the peer CTA arrive on: once the phase
+// is complete, one more test of it acquires at cluster scope (the phase cannot
+// move on in between, its next completion needs work this thread has not
+// issued yet).
+__device__ __forceinline__ bool wait_for_pair(uint32_t bar, uint32_t parity, volatile int* abort_w,
+                                              int* status, int code, long long timeout_ns) {
+  if (!wait_for(bar, parity, abort_w, status, code, timeout_ns)) return false;
+  return ptx::mbar_try_wait_cluster(bar, parity);
 }
 
 // ---- conversions --------------------------------------------------------------
@@ -252,37 +366,50 @@ __device__ __forceinline__ void store_out(void* base, long long at, int type, fl
     static_cast<__half*>(base)[at] = __float2half_rn(v);
 }
 
-template <int SRC, int BQ>
-__global__ void __launch_bounds__(Geo<SRC, BQ>::kThreads, 1)
+template <int SRC, int BQ, int CL>
+__global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     ragged_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap mapP,
                   const __grid_constant__ CUtensorMap mapQ) {
-  using G = Geo<SRC, BQ>;
+  using G = Geo<SRC, BQ, CL>;
+  using List = Walk<G::kSlice, BQ, CL>;
   constexpr int SL = G::kSlice;
-  constexpr int RS = G::kRawStages, OS = G::kOpStages;
+  constexpr int RS = G::kRawStages, OS = G::kConv ? G::kOpStages : RS;
+  constexpr bool kPair = CL == 2;
+  constexpr uint16_t kBoth = 0x3;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw_addr = ptx::smem_addr(smem_raw);
   unsigned char* base = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   const uint32_t base_addr = ptx::smem_addr(base);
   // operand stages (kConv) start on 1024-byte boundaries, then the raw ones
-  unsigned char* raw_base = base + OS * G::kOp;
-  const uint32_t raw_base_addr = base_addr + OS * G::kOp;
+  constexpr int kRawAt = G::kConv ? G::kOpStages * G::kOp : 0;
+  unsigned char* raw_base = base + kRawAt;
+  const uint32_t raw_base_addr = base_addr + kRawAt;
   Shared* sh = reinterpret_cast<Shared*>(base + G::kRegion);
   volatile int* abort_w = &sh->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = kPair ? (int)ptx::cluster_ctarank() : 0;
+  const int worker = (int)blockIdx.x / CL, workers = (int)gridDim.x / CL;
   constexpr uint32_t kAll = 0xffffffffu;
 
   if (tid == 0) {
+    // pair form: the even CTA's MMA warp waits on the stages of both CTAs
+    // (converted ones: its own, and one relayed arrival for the odd CTA's),
+    // and on the epilogue warps of both; its commits arrive in both CTAs
     for (int s = 0; s < RS; ++s) {
-      ptx::mbar_init(ptx::smem_addr(&sh->raw_full[s]), 1);
+      // (even CTA of a pair: the producers of both)
+      ptx::mbar_init(ptx::smem_addr(&sh->raw_full[s]), kPair && !G::kConv && rank == 0 ? 2 : 1);
       ptx::mbar_init(ptx::smem_addr(&sh->raw_empty[s]), G::kConv ? kConvWarps : 1);
     }
     for (int s = 0; s < OS; ++s) {
-      ptx::mbar_init(ptx::smem_addr(&sh->op_full[s]), kConvWarps);
-      ptx::mbar_init(ptx::smem_addr(&sh->op_empty[s]), 1);
+      if (G::kConv) {
+        ptx::mbar_init(ptx::smem_addr(&sh->op_full[s]), kConvWarps);
+        ptx::mbar_init(ptx::smem_addr(&sh->op_empty[s]), 1);
+      }
+      ptx::mbar_init(ptx::smem_addr(&sh->peer_full[s]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(ptx::smem_addr(&sh->acc_full[i]), 1);
-      ptx::mbar_init(ptx::smem_addr(&sh->acc_empty[i]), kEpiWarps);
+      ptx::mbar_init(ptx::smem_addr(&sh->acc_empty[i]), CL * kEpiWarps);
     }
     ptx::mbar_init(ptx::smem_addr(&sh->drain), 1);
     ptx::mbar_init(ptx::smem_addr(&sh->epi_sync), kEpiThreads);
@@ -292,8 +419,8 @@ __global__ void __launch_bounds__(Geo<SRC, BQ>::kThreads, 1)
     ptx::tma_prefetch_desc(&mapQ);
   }
   if (warp == 1) {
-    tc::tmem_alloc(ptx::smem_addr(&sh->tmem), G::kTmemCols);
-    tc::tmem_relinquish();
+    tc::tmem_alloc<CL>(ptx::smem_addr(&sh->tmem), G::kTmemCols);
+    tc::tmem_relinquish<CL>();
   }
   // launched with programmatic stream serialization: the set-up above overlaps
   // the end of the kernel ahead; nothing below touches global memory before it
@@ -301,9 +428,9 @@ __global__ void __launch_bounds__(Geo<SRC, BQ>::kThreads, 1)
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   if (warp == 0) {
-    // scan of the groups: rows, and the number of the first tile of each
-    const int ptiles = cdiv(p.P, BP);
-    int carry = 0;
+    // scan of the groups: rows, number and slice position of each one's first tile
+    const int ptiles = cdiv(p.P, BP * CL);
+    int tiles_before = 0, pos_before = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
       int lo = 0, n = 0, tiles = 0;
@@ -313,136 +440,245 @@ __global__ void __launch_bounds__(Geo<SRC, BQ>::kThreads, 1)
         n = max(hi - lo, 0);
         tiles = ptiles * cdiv(p.wgrad ? p.Q : n, BQ);
       }
-      int incl = tiles;
+      int incl = tiles, incl_pos = tiles * tile_slices<SL>(p, n);
+      const int own_pos = incl_pos;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(kAll, incl, d);
-        if (lane >= d) incl += o;
+        const int o = __shfl_up_sync(kAll, incl, d), q = __shfl_up_sync(kAll, incl_pos, d);
+        if (lane >= d) {
+          incl += o;
+          incl_pos += q;
+        }
       }
       if (e < p.E) {
         sh->row0[e] = lo;
         sh->rows[e] = n;
-        sh->first[e] = carry + incl - tiles;
+        sh->first[e] = tiles_before + incl - tiles;
+        sh->pos[e] = pos_before + incl_pos - own_pos;
       }
-      carry += __shfl_sync(kAll, incl, 31);
+      tiles_before += __shfl_sync(kAll, incl, 31);
+      pos_before += __shfl_sync(kAll, incl_pos, 31);
     }
+    __syncwarp();
     if (lane == 0) {
-      sh->first[p.E] = carry;
-      sh->tiles = carry;
-      // fewer tiles than CTAs: cut each along k, at least four slices a range
-      const int mean = p.wgrad ? p.T / p.E : p.K;
-      const int most = cdiv(mean, SL) / 4;
-      int S = carry > 0 ? (int)gridDim.x / carry : 1;
-      S = min(S, most);
-      sh->splits = S > 1 && p.partials != nullptr ? S : 1;
+      const int tiles = tiles_before, total = pos_before;
+      sh->tiles = tiles;
+      // whole waves first; what is left, one to two waves, by slices
+      int dp = 0;
+      dp = tiles % workers == 0 ? tiles : max(0, tiles / workers - 1) * workers;
+      sh->dp = dp;
+      int base_pos = total;
+      if (dp < tiles) {
+        List l(p, sh, 0, 0);
+        const int e = l.find(sh->first, dp);
+        base_pos = sh->pos[e] + (dp - sh->first[e]) * tile_slices<SL>(p, sh->rows[e]);
+      }
+      sh->base = base_pos;
+      sh->len = total - base_pos;
+      sh->cutters = dp < tiles ? min(workers, max(tiles - dp, sh->len / kMinSlices)) : 0;
     }
   }
   tc::fence_before_sync();
   __syncthreads();
+  // the peer's barriers must be initialised before the pair's first remote
+  // arrival or commit reaches them
+  if (kPair) ptx::cluster_sync();
   tc::fence_after_sync();
   const uint32_t tmem = sh->tmem;
-  const int units = sh->tiles * sh->splits;
+  if (kPair) {
+    if (tid == 0) {
+      // the MMAs of the pair write the same tensor-memory address in both CTAs
+      const uint32_t peer = ptx::ld_shared_cluster(
+          ptx::mapa(ptx::smem_addr(&sh->tmem), (uint32_t)(rank ^ 1)));
+      if (peer != tmem) {
+        *abort_w = 1;
+        atomicCAS(p.status, 0, (int)kDevTmemMismatch);
+      }
+    }
+    __syncthreads();  // every role sees the abort word
+  }
 
-  if (warp == 0) {
-    // ---- TMA producer ---------------------------------------------------------
-    if (lane == 0) {
+  // a stage whose rows of k end inside a 16-row step (wgrad): the rows behind
+  // them belong to the next group and are cleared by warp 1
+  auto clears = [&](const Unit& u, int ks) {
+    const int rem = u.klen - ks * SL;
+    return !G::kConv && p.wgrad && (rem & 15) != 0 && rem < SL;
+  };
+
+  if (warp < kEpiWarp0) {
+    if (G::kMoveRegs) ptx::regs_lower<G::kRegsFew>();
+    // ---- warp 0: TMA producer ---------------------------------------------------
+    if (warp == 0) {
       int it = 0;
-      for (int u = blockIdx.x; u < units && !*abort_w; u += gridDim.x) {
-        const Unit w = get_unit<SL, BQ>(p, sh, u);
-        const int qrow = p.wgrad ? 0 : w.row0;
-        bool ok = true;
+      uint32_t own_phase = 0;   // odd CTA: phases of its own raw_full barriers (a bit each)
+      bool ok = true;
+      Unit w;
+      for (List list(p, sh, worker, workers); ok && list.next(w);) {
+        const int p0 = w.p0 + rank * BP, q0 = w.q0 + rank * G::kRows;
         for (int ks = w.kb; ks < w.ke; ++ks, ++it) {
           const int s = it % RS;
-          if (!bounded_wait(ptx::smem_addr(&sh->raw_empty[s]), (uint32_t)((it / RS) & 1) ^ 1u,
-                            abort_w, p.status, kDevTimeoutEmpty, p.timeout_ns)) {
-            ok = false;
-            break;
+          ok = wait_for(ptx::smem_addr(&sh->raw_empty[s]), (uint32_t)((it / RS) & 1) ^ 1u, abort_w,
+                        p.status, kDevTimeoutEmpty, p.timeout_ns);
+          ok = __all_sync(kAll, ok);
+          if (!ok) break;
+          // pair: the even CTA's MMA warp waits for the loads of both, but for
+          // a stage that the odd CTA has to clear
+          const bool remote = kPair && !G::kConv && rank != 0 && !clears(w, ks);
+          if (rank != 0 && !remote) own_phase ^= 1u << s;
+          if (ptx::elect_one()) {
+            uint32_t fb = ptx::smem_addr(&sh->raw_full[s]);
+            const uint32_t st = raw_base_addr + (uint32_t)(s * G::kRaw);
+            if (remote) {
+              fb = ptx::mapa(fb, 0u);
+              ptx::mbar_arrive_expect_tx_remote(fb, (uint32_t)G::kRaw);
+            } else {
+              ptx::mbar_arrive_expect_tx(fb, (uint32_t)G::kRaw);
+            }
+            auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, int z) {
+              if (kPair && !G::kConv)
+                ptx::tma_load_3d_pair(dst, map, x, y, z, fb);
+              else
+                ptx::tma_load_3d(dst, map, x, y, z, fb);
+            };
+            const int k = ks * SL + (p.wgrad ? w.row0 : 0);
+            constexpr int BOX = G::kRawRow / G::kElem;  // elements along the fast dimension of a box
+            if (p.p_mn) {
+#pragma unroll
+              for (int i = 0; i < BP / BOX; ++i)
+                load(st + (uint32_t)(i * SL * G::kRawRow), &mapP, p0 + i * BOX, k,
+                     p.wgrad ? 0 : w.e);
+            } else {
+              load(st, &mapP, k, p0, w.e);
+            }
+            if (p.q_mn) {
+#pragma unroll
+              for (int i = 0; i < G::kRows / BOX; ++i)
+                load(st + (uint32_t)(G::kRawP + i * SL * G::kRawRow), &mapQ, q0 + i * BOX, k, 0);
+            } else {
+              load(st + G::kRawP, &mapQ, k, w.row0 + q0, 0);
+            }
           }
-          const uint32_t fb = ptx::smem_addr(&sh->raw_full[s]);
-          const uint32_t st = raw_base_addr + (uint32_t)(s * G::kRaw);
-          ptx::mbar_arrive_expect_tx(fb, (uint32_t)G::kRaw);
-          const int k = ks * SL + (p.wgrad ? w.row0 : 0);
-          const int pe = p.wgrad ? 0 : w.e;
-          constexpr int BOX = G::kRawRow / G::kElem;  // elements along the fast dimension of a box
-          if (p.p_mn) {
-            for (int i = 0; i < BP / BOX; ++i)
-              ptx::tma_load_3d(st + (uint32_t)(i * SL * G::kRawRow), &mapP, w.p0 + i * BOX, k, pe, fb);
-          } else {
-            ptx::tma_load_3d(st, &mapP, k, w.p0, pe, fb);
-          }
-          if (p.q_mn) {
-            for (int i = 0; i < BQ / BOX; ++i)
-              ptx::tma_load_3d(st + (uint32_t)(G::kRawP + i * SL * G::kRawRow), &mapQ,
-                               w.q0 + i * BOX, k, 0, fb);
-          } else {
-            ptx::tma_load_3d(st + G::kRawP, &mapQ, k, qrow + w.q0, 0, fb);
-          }
+          __syncwarp();
         }
-        if (!ok) break;
       }
       // nothing may land after the CTA is gone: wait (bounded) for the last
       // stages issued
       const uint64_t t0 = ptx::global_ns();
       for (int j = it - 1; j >= 0 && j >= it - RS; --j) {
+        // (odd CTA: its own barriers only carry the stages that are cleared;
+        // the others have landed once the even CTA's MMAs have read them)
         const uint32_t fb = ptx::smem_addr(&sh->raw_full[j % RS]);
-        while (!ptx::mbar_try_wait(fb, (uint32_t)((j / RS) & 1)))
+        const uint32_t par = kPair && !G::kConv && rank != 0 ? (own_phase >> (j % RS) & 1u) ^ 1u
+                                                             : (uint32_t)((j / RS) & 1);
+        while (!ptx::mbar_try_wait(fb, par))
           if ((long long)(ptx::global_ns() - t0) > cleanup_bound_ns(p.timeout_ns)) break;
       }
+      if (kPair && !G::kConv) {
+        // the even CTA's commits arrive on this CTA's raw_empty barriers: wait
+        // (bounded) for its arrivals on the last use of every stage
+        for (int j = it; j < it + RS; ++j) {
+          const uint32_t eb = ptx::smem_addr(&sh->raw_empty[j % RS]);
+          while (!ptx::mbar_try_wait(eb, (uint32_t)((j / RS) & 1) ^ 1u))
+            if ((long long)(ptx::global_ns() - t0) > cleanup_bound_ns(p.timeout_ns)) break;
+        }
+      }
+      __syncwarp();
     }
-  } else if (warp == 1) {
-    // ---- MMA issuer -------------------------------------------------------------
+    // ---- warp 1: MMA issuer (even CTA of a pair), or relay (odd CTA) --------------
+    if (warp == 1) {
     // operand tiles: K-major rows of 128 bytes (64 for kF32) in 8-row groups;
     // MN-major chunks of 64 elements x SL rows of k, 128 bytes a row
     constexpr bool kNarrow = SRC == kF32;
     const bool a_mn = p.p_mn, b_mn = p.q_mn;
-    const uint32_t idesc = tc::idesc_f16(BP, BQ, SRC == kF32 || (SRC == k16 && p.bf16), a_mn, b_mn);
+    const uint32_t idesc =
+        tc::idesc_f16(BP * CL, BQ, SRC == kF32 || (SRC == k16 && p.bf16), a_mn, b_mn);
     auto desc = [](uint32_t addr, bool mn) {
       return mn ? tc::smem_desc(addr, SL * 128, 1024, true)
                 : tc::smem_desc(addr, 16, kNarrow ? 512 : 1024, !kNarrow);
     };
+    auto mma = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t add) {
+      if (kPair)
+        tc::mma_f16_pair(d, a, b, idesc, add);
+      else
+        tc::mma_f16(d, a, b, idesc, add);
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (kPair)
+        tc::commit_pair_multicast(ptx::smem_addr(bar), kBoth);
+      else
+        tc::commit(ptx::smem_addr(bar));
+    };
     const uint32_t a_step = a_mn ? 2048u : 32u, b_step = b_mn ? 2048u : 32u;
     int it = 0, acc = 0;
+    uint32_t own_phase = 0;   // odd CTA: next phases of its own raw_full barriers
     bool issued_any = false, ok = true;
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-      const Unit w = get_unit<SL, BQ>(p, sh, u);
+    Unit w;
+    for (List list(p, sh, worker, workers); ok && list.next(w);) {
       for (int k0 = w.kb; k0 < w.ke && ok; k0 += p.chunk, ++acc) {
         const int buf = acc & 1;
         const uint32_t d = tmem + (uint32_t)(buf * BQ);
-        ok = bounded_wait(ptx::smem_addr(&sh->acc_empty[buf]), (uint32_t)((acc >> 1) & 1) ^ 1u,
-                          abort_w, p.status, kDevTimeoutSync, p.timeout_ns);
-        ok = __all_sync(kAll, ok);
-        if (!ok) break;
-        tc::fence_after_sync();
-        const int k1 = min(w.ke, k0 + p.chunk);
-        for (int ks = k0; ks < k1; ++ks, ++it) {
-          const int s = G::kConv ? it % (OS > 0 ? OS : 1) : it % RS;
-          const uint32_t par = (uint32_t)((G::kConv ? it / (OS > 0 ? OS : 1) : it / RS) & 1);
-          ok = bounded_wait(ptx::smem_addr(G::kConv ? &sh->op_full[s] : &sh->raw_full[s]), par,
-                            abort_w, p.status, kDevTimeoutFull, p.timeout_ns);
+        if (rank == 0) {
+          const uint32_t eb = ptx::smem_addr(&sh->acc_empty[buf]);
+          const uint32_t par = (uint32_t)((acc >> 1) & 1) ^ 1u;
+          ok = kPair ? wait_for_pair(eb, par, abort_w, p.status, kDevTimeoutSync, p.timeout_ns)
+                     : wait_for(eb, par, abort_w, p.status, kDevTimeoutSync, p.timeout_ns);
           ok = __all_sync(kAll, ok);
           if (!ok) break;
-          const uint32_t st = base_addr + (uint32_t)(s * (G::kConv ? G::kOp : G::kRaw));
+          tc::fence_after_sync();
+        }
+        const int k1 = min(w.ke, k0 + p.chunk);
+        for (int ks = k0; ks < k1; ++ks, ++it) {
+          const int s = it % OS;
+          const uint32_t par = (uint32_t)((it / OS) & 1);
+          const bool clear = clears(w, ks);
           const int rem = w.klen - ks * SL;   // > 0
           const int steps = min(SL / 16, cdiv(rem, 16));
-          if (SRC == k16 && p.wgrad && (rem & 15) && rem < SL) {
-            // rows of k past the group's end belong to the next group: clear
-            // them in both operands up to the end of their 16-row step (the
-            // steps beyond are not issued)
+          const uint32_t st = base_addr + (uint32_t)(s * (G::kConv ? G::kOp : G::kRaw));
+          if (kPair && !G::kConv && rank != 0 && !clear) continue;
+          if (G::kConv || !kPair) {
+            ok = wait_for(ptx::smem_addr(G::kConv ? &sh->op_full[s] : &sh->raw_full[s]), par,
+                              abort_w, p.status, kDevTimeoutFull, p.timeout_ns);
+          } else if (rank == 0) {
+            // the loads of both CTAs (and what the odd one has cleared)
+            ok = wait_for_pair(ptx::smem_addr(&sh->raw_full[s]), par, abort_w, p.status,
+                                   kDevTimeoutFull, p.timeout_ns);
+          } else {
+            ok = wait_for(ptx::smem_addr(&sh->raw_full[s]), own_phase >> s & 1u, abort_w,
+                              p.status, kDevTimeoutFull, p.timeout_ns);
+            own_phase ^= 1u << s;
+          }
+          ok = __all_sync(kAll, ok);
+          if (!ok) break;
+          if (clear) {
+            // clear the rows of k past the group's end in both operands up to
+            // the end of their 16-row step (the steps beyond are not issued)
             unsigned char* stp = base + s * G::kRaw;
-            const int z0 = rem, nz = steps * 16 - rem;
-            constexpr int kBoxes = (BP + BQ) / 64;
+            const int nz = steps * 16 - rem;
+            constexpr int kBoxes = (BP + G::kRows) / 64;
             for (int i = lane; i < kBoxes * nz * 8; i += 32) {
               const int box = i / (nz * 8), r = i - box * nz * 8;
-              *reinterpret_cast<uint4*>(stp + box * (SL * 128) + z0 * 128 + r * 16) =
+              *reinterpret_cast<uint4*>(stp + box * (SL * 128) + rem * 128 + r * 16) =
                   make_uint4(0u, 0u, 0u, 0u);
             }
             ptx::fence_proxy_async_shared();
             __syncwarp();
           }
+          if (rank != 0) {
+            if (lane == 0)
+              ptx::mbar_arrive_remote(
+                  ptx::mapa(ptx::smem_addr(G::kConv ? &sh->peer_full[s] : &sh->raw_full[s]), 0u));
+            continue;
+          }
+          if (kPair && G::kConv) {
+            ok = wait_for_pair(ptx::smem_addr(&sh->peer_full[s]), par, abort_w, p.status,
+                                   kDevTimeoutFull, p.timeout_ns);
+            ok = __all_sync(kAll, ok);
+            if (!ok) break;
+          }
           tc::fence_after_sync();
-          if (lane == 0) {
-            constexpr int OP_P = SRC == k16 ? G::kRawP : G::kOpP;   // one part
-            constexpr int OP_Q = SRC == k16 ? G::kRawQ : G::kOpQ;
+          if (ptx::elect_one()) {
+            constexpr int OP_P = G::kConv ? G::kOpP : G::kRawP;   // one part
+            constexpr int OP_Q = G::kConv ? G::kOpQ : G::kRawQ;
             const uint32_t pa = st, qa = st + (uint32_t)(G::kParts * OP_P);
             for (int kk = 0; kk < steps; ++kk) {
               const uint32_t first = (ks == k0 && kk == 0) ? 0u : 1u;
@@ -452,47 +688,57 @@ __global__ void __launch_bounds__(Geo<SRC, BQ>::kThreads, 1)
                 const uint64_t a2 = desc(pa + 2 * OP_P + kk * a_step, a_mn);
                 const uint64_t b1 = desc(qa + OP_Q + kk * b_step, b_mn);
                 const uint64_t b2 = desc(qa + 2 * OP_Q + kk * b_step, b_mn);
-                tc::mma_f16(d, a2, b0, idesc, first);
-                tc::mma_f16(d, a0, b2, idesc, 1u);
-                tc::mma_f16(d, a1, b1, idesc, 1u);
-                tc::mma_f16(d, a1, b0, idesc, 1u);
-                tc::mma_f16(d, a0, b1, idesc, 1u);
-                tc::mma_f16(d, a0, b0, idesc, 1u);
+                mma(d, a2, b0, first);
+                mma(d, a0, b2, 1u);
+                mma(d, a1, b1, 1u);
+                mma(d, a1, b0, 1u);
+                mma(d, a0, b1, 1u);
+                mma(d, a0, b0, 1u);
               } else {
-                tc::mma_f16(d, a0, b0, idesc, first);
+                mma(d, a0, b0, first);
               }
             }
-            tc::commit(ptx::smem_addr(G::kConv ? &sh->op_empty[s] : &sh->raw_empty[s]));
+            commit(G::kConv ? &sh->op_empty[s] : &sh->raw_empty[s]);
           }
+          __syncwarp();
           issued_any = true;
         }
         if (!ok) break;
-        if (lane == 0) tc::commit(ptx::smem_addr(&sh->acc_full[buf]));
+        if (rank == 0 && ptx::elect_one()) commit(&sh->acc_full[buf]);
+        __syncwarp();
       }
     }
-    if (*abort_w && issued_any && lane == 0) {
+    const bool aborted = __any_sync(kAll, *abort_w != 0);
+    if (aborted && issued_any) {
       // wait (bounded) until every MMA issued has completed
-      tc::commit(ptx::smem_addr(&sh->drain));
+      if (ptx::elect_one()) {
+        if (kPair)
+          tc::commit_pair(ptx::smem_addr(&sh->drain));
+        else
+          tc::commit(ptx::smem_addr(&sh->drain));
+      }
+      __syncwarp();
       const uint64_t t0 = ptx::global_ns();
       while (!ptx::mbar_try_wait(ptx::smem_addr(&sh->drain), 0u))
         if ((long long)(ptx::global_ns() - t0) > cleanup_bound_ns(p.timeout_ns)) break;
     }
     __syncwarp();
+    }
   } else if (G::kConv && warp >= kConvWarp0) {
     // ---- converters: raw tiles -> operand tiles ----------------------------------
+    if (G::kMoveRegs) ptx::regs_lower<G::kRegsConv>();
     const int t = tid - kConvWarp0 * 32;
     constexpr int NT = kConvWarps * 32;
     int it = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-      const Unit w = get_unit<SL, BQ>(p, sh, u);
+    Unit w;
+    for (List list(p, sh, worker, workers); ok && list.next(w);) {
       for (int ks = w.kb; ks < w.ke; ++ks, ++it) {
-        const int rs = it % RS, os = it % (OS > 0 ? OS : 1);
-        ok = bounded_wait(ptx::smem_addr(&sh->raw_full[rs]), (uint32_t)((it / RS) & 1), abort_w,
+        const int rs = it % RS, os = it % OS;
+        ok = wait_for(ptx::smem_addr(&sh->raw_full[rs]), (uint32_t)((it / RS) & 1), abort_w,
                           p.status, kDevTimeoutFull, p.timeout_ns) &&
-             bounded_wait(ptx::smem_addr(&sh->op_empty[os]),
-                          (uint32_t)((it / (OS > 0 ? OS : 1)) & 1) ^ 1u, abort_w, p.status,
-                          kDevTimeoutEmpty, p.timeout_ns);
+             wait_for(ptx::smem_addr(&sh->op_empty[os]), (uint32_t)((it / OS) & 1) ^ 1u,
+                          abort_w, p.status, kDevTimeoutEmpty, p.timeout_ns);
         ok = __all_sync(kAll, ok);
         if (!ok) break;
         const unsigned char* raw = raw_base + rs * G::kRaw;
@@ -500,10 +746,10 @@ __global__ void __launch_bounds__(Geo<SRC, BQ>::kThreads, 1)
         if (SRC == kF32) {
           const int klim = p.wgrad ? w.klen - ks * SL : SL;
           convert_f32<BP>(raw, op, p.p_mn, klim, t, NT);
-          convert_f32<BQ>(raw + G::kRawP, op + G::kParts * G::kOpP, p.q_mn, klim, t, NT);
+          convert_f32<G::kRows>(raw + G::kRawP, op + G::kParts * G::kOpP, p.q_mn, klim, t, NT);
         } else {
           convert_i8<BP>(raw, op, t, NT);
-          convert_i8<BQ>(raw + G::kRawP, op + G::kOpP, t, NT);
+          convert_i8<G::kRows>(raw + G::kRawP, op + G::kOpP, t, NT);
         }
         // the MMAs read the operand tiles, and TMA refills the raw ones,
         // through the async proxy
@@ -515,8 +761,19 @@ __global__ void __launch_bounds__(Geo<SRC, BQ>::kThreads, 1)
         }
       }
     }
-  } else if (warp >= kEpiWarp0 && warp < kConvWarp0) {
+    if (kPair && t == 0) {
+      // the even CTA's commits arrive on this CTA's op_empty barriers: wait
+      // (bounded) for its arrivals on the last use of every stage
+      const uint64_t t0 = ptx::global_ns();
+      for (int j = it; j < it + OS; ++j) {
+        const uint32_t eb = ptx::smem_addr(&sh->op_empty[j % OS]);
+        while (!ptx::mbar_try_wait(eb, (uint32_t)((j / OS) & 1) ^ 1u))
+          if ((long long)(ptx::global_ns() - t0) > cleanup_bound_ns(p.timeout_ns)) break;
+      }
+    }
+  } else {
     // ---- epilogue: accumulators -> registers -> output or partial tile -------------
+    if (G::kMoveRegs) ptx::regs_raise<G::kRegsMany>();
     constexpr int HC = BQ / 2;                         // columns of this warp
     constexpr int CH = HC < 32 ? HC : 32;              // columns per tensor-memory read
     const int quarter = warp & 3;                      // TMEM lanes 32*quarter ..
@@ -526,22 +783,23 @@ __global__ void __launch_bounds__(Geo<SRC, BQ>::kThreads, 1)
     uint32_t sync_phase = 0;
     auto epi_sync = [&]() -> bool {                    // bounded rendezvous of the epilogue
       ptx::mbar_arrive(ptx::smem_addr(&sh->epi_sync));
-      const bool ok = bounded_wait(ptx::smem_addr(&sh->epi_sync), sync_phase, abort_w, p.status,
+      const bool ok = wait_for(ptx::smem_addr(&sh->epi_sync), sync_phase, abort_w, p.status,
                                    kDevTimeoutSync, p.timeout_ns);
       sync_phase ^= 1u;
       return __all_sync(kAll, ok);
     };
     int acc = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-      const Unit w = get_unit<SL, BQ>(p, sh, u);
-      // kI8: the sums as 32-bit integers, kept in the same registers
+    Unit w;
+    for (List list(p, sh, worker, workers); ok && list.next(w);) {
+      const int nq = w.nq - half * HC;                 // valid columns of this warp (may be <= 0)
+      // integer sums are kept in the same registers
       float sum[HC];
 #pragma unroll
       for (int c = 0; c < HC; ++c) sum[c] = 0.f;
       for (int k0 = w.kb; k0 < w.ke; k0 += p.chunk, ++acc) {
         const int buf = acc & 1;
-        ok = bounded_wait(ptx::smem_addr(&sh->acc_full[buf]), (uint32_t)((acc >> 1) & 1), abort_w,
+        ok = wait_for(ptx::smem_addr(&sh->acc_full[buf]), (uint32_t)((acc >> 1) & 1), abort_w,
                           p.status, kDevTimeoutFull, p.timeout_ns);
         ok = __all_sync(kAll, ok);
         if (!ok) break;
@@ -549,14 +807,19 @@ __global__ void __launch_bounds__(Geo<SRC, BQ>::kThreads, 1)
         const uint32_t src = tmem + lane_base + (uint32_t)(buf * BQ + half * HC);
 #pragma unroll
         for (int c0 = 0; c0 < HC; c0 += CH) {
+          if (c0 >= nq) continue;                      // (the whole warp)
           uint32_t v[CH];
+          if constexpr (CH == 8) {
+            tc::tmem_ld8(src, v);
+          } else {
 #pragma unroll
-          for (int i = 0; i < CH; i += 16)
-            tc::tmem_ld16(src + (uint32_t)(c0 + i), *reinterpret_cast<uint32_t(*)[16]>(&v[i]));
+            for (int i = 0; i < CH; i += 16)
+              tc::tmem_ld16(src + (uint32_t)(c0 + i), *reinterpret_cast<uint32_t(*)[16]>(&v[i]));
+          }
           tc::tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < CH; ++i) {
-            if (SRC == kI8)
+            if (G::kInt)
               sum[c0 + i] = __int_as_float(__float_as_int(sum[c0 + i]) +
                                            __float2int_rn(__uint_as_float(v[i])));
             else
@@ -565,15 +828,23 @@ __global__ void __launch_bounds__(Geo<SRC, BQ>::kThreads, 1)
         }
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&sh->acc_empty[buf]));
+        if (lane == 0) {
+          // the even CTA's MMA warp waits for the epilogues of both
+          if (kPair && rank != 0)
+            ptx::mbar_arrive_remote(ptx::mapa(ptx::smem_addr(&sh->acc_empty[buf]), 0u));
+          else
+            ptx::mbar_arrive(ptx::smem_addr(&sh->acc_empty[buf]));
+        }
       }
       if (!ok) break;
-      const int nq = w.nq - half * HC;                 // valid columns of this warp (may be <= 0)
-      if (sh->splits > 1) {
-        // publish this range's partial tile; the last CTA to arrive adds all
-        // of them in order
-        const int S = sh->splits;
-        float* part = p.partials + (long long)u * (BP * BQ) + half * HC * BP + pr;
+      if (w.parts > 1) {
+        // publish this range's partial tile (slot 1 of this CTA for the range
+        // that starts the tile, else slot 0); the last to arrive adds them all
+        const long long kTile = BP * BQ;
+        auto slot = [&](int c, int which) -> float* {
+          return p.partials + (((long long)c * 2 + which) * CL + rank) * kTile + half * HC * BP + pr;
+        };
+        float* part = slot(worker, w.kb == 0 ? 1 : 0);
 #pragma unroll
         for (int c = 0; c < HC; ++c)
           if (c < nq) __stcg(part + c * BP, sum[c]);
@@ -581,9 +852,9 @@ __global__ void __launch_bounds__(Geo<SRC, BQ>::kThreads, 1)
         ok = epi_sync();
         if (!ok) break;
         if (warp == kEpiWarp0 && lane == 0) {
-          const uint32_t before = atomicAdd(p.counters + w.tile, 1u);
-          const int last = before == (uint32_t)(S - 1);
-          if (last) p.counters[w.tile] = 0u;           // ready for the next launch
+          uint32_t* counter = p.counters + w.c0 * CL + rank;
+          const int last = atomicAdd(counter, 1u) == (uint32_t)(w.parts - 1);
+          if (last) *counter = 0u;                     // ready for the next launch
           __threadfence();
           sh->last = last;
         }
@@ -591,24 +862,36 @@ __global__ void __launch_bounds__(Geo<SRC, BQ>::kThreads, 1)
         if (!ok) break;
         if (!*reinterpret_cast<volatile int*>(&sh->last)) continue;
         __threadfence();
-        const float* all = p.partials + (long long)w.tile * S * (BP * BQ) + half * HC * BP + pr;
+        // (of two, the own one is still in registers: a sum of two terms does
+        // not depend on their order)
+        const int own = w.parts == 2 ? worker - w.c0 : -1;
+        for (int i = 0; i < w.parts; ++i) {
+          if (i == own) continue;
+          const float* src = slot(w.c0 + i, i == 0 ? 1 : 0);
+          // a batch of independent loads at a time (one after another, each
+          // column would cost the latency of L2)
+          constexpr int LB = HC < 32 ? HC : 32;
 #pragma unroll
-        for (int c = 0; c < HC; ++c) {
-          if (c >= nq) continue;
-          float v = 0.f;
-          for (int s = 0; s < S; ++s) {
-            const float x = __ldcg(all + (long long)s * (BP * BQ) + c * BP);
-            if (SRC == kI8)
-              v = __int_as_float(__float_as_int(v) + __float_as_int(x));
-            else
-              v += x;
+          for (int c0 = 0; c0 < HC; c0 += LB) {
+            if (c0 >= nq) continue;
+            float x[LB];
+#pragma unroll
+            for (int c = 0; c < LB; ++c) x[c] = c0 + c < nq ? __ldcg(src + (c0 + c) * BP) : 0.f;
+#pragma unroll
+            for (int c = 0; c < LB; ++c) {
+              if (i == 0 && own < 0)
+                sum[c0 + c] = x[c];
+              else if (G::kInt)
+                sum[c0 + c] = __int_as_float(__float_as_int(sum[c0 + c]) + __float_as_int(x[c]));
+              else
+                sum[c0 + c] += x[c];
+            }
           }
-          sum[c] = v;
         }
       }
-      const int pp = w.p0 + pr;
+      const int pp = w.p0 + rank * BP + pr;
       if (pp < p.P && nq > 0) {
-        const float sp = SRC == kI8 ? p.scale_p[pp] : 1.f;
+        const float sp = G::kInt ? p.scale_p[pp] : 1.f;
         const long long row = (long long)(p.wgrad ? 0 : w.row0) + w.q0 + half * HC;
         const long long at0 = (p.wgrad ? (long long)w.e * p.stride_o : 0ll) + row * p.ldo + pp;
 #pragma unroll
@@ -616,7 +899,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ>::kThreads, 1)
           if (c >= nq) continue;
           const long long at = at0 + c * p.ldo;
           float v;
-          if (SRC == kI8)
+          if (G::kInt)
             v = (float)__float_as_int(sum[c]) * p.scale_q[row + c] * sp;
           else
             v = p.alpha * sum[c];
@@ -629,9 +912,12 @@ __global__ void __launch_bounds__(Geo<SRC, BQ>::kThreads, 1)
 
   tc::fence_before_sync();
   __syncthreads();
+  // the even CTA's MMAs write the odd CTA's tensor memory and read its shared
+  // memory: the pair frees its tensor memory together, once both are done
+  if (kPair) ptx::cluster_sync();
   if (warp == 1) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, G::kTmemCols);
+    tc::tmem_dealloc<CL>(tmem, G::kTmemCols);
   }
 }
 

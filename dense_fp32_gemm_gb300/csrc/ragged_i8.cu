@@ -4,15 +4,15 @@
 namespace sgemm_gb300 {
 namespace ragged {
 
-cudaError_t launch_i8(int dev, int bq, int grid, const Params& p, const CUtensorMap& mp,
-                      const CUtensorMap& mq, cudaStream_t stream) {
-  switch (bq) {
-    case 32: return launch_one<kI8, 32>(dev, grid, p, mp, mq, stream);
-    case 64: return launch_one<kI8, 64>(dev, grid, p, mp, mq, stream);
-    case 128: return launch_one<kI8, 128>(dev, grid, p, mp, mq, stream);
-    default: return cudaErrorInvalidValue;
-  }
-}
+extern const FormEntry kFormsI8[] = {
+    SGEMM_GB300_FORM(kI8, 16, 1),
+    SGEMM_GB300_FORM(kI8, 32, 1),
+    SGEMM_GB300_FORM(kI8, 64, 1),
+    SGEMM_GB300_FORM(kI8, 128, 1),
+    SGEMM_GB300_FORM(kI8Wide, 256, 1),
+    SGEMM_GB300_FORM(kI8Wide, 256, 2),
+};
+extern const int kNumFormsI8 = sizeof(kFormsI8) / sizeof(kFormsI8[0]);
 
 }  // namespace ragged
 }  // namespace sgemm_gb300

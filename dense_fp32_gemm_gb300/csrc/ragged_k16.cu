@@ -4,16 +4,15 @@
 namespace sgemm_gb300 {
 namespace ragged {
 
-cudaError_t launch_k16(int dev, int bq, int grid, const Params& p, const CUtensorMap& mp,
-                       const CUtensorMap& mq, cudaStream_t stream) {
-  switch (bq) {
-    case 32: return launch_one<k16, 32>(dev, grid, p, mp, mq, stream);
-    case 64: return launch_one<k16, 64>(dev, grid, p, mp, mq, stream);
-    case 128: return launch_one<k16, 128>(dev, grid, p, mp, mq, stream);
-    case 256: return launch_one<k16, 256>(dev, grid, p, mp, mq, stream);
-    default: return cudaErrorInvalidValue;
-  }
-}
+extern const FormEntry kForms16[] = {
+    SGEMM_GB300_FORM(k16, 16, 1),
+    SGEMM_GB300_FORM(k16, 32, 1),
+    SGEMM_GB300_FORM(k16, 64, 1),
+    SGEMM_GB300_FORM(k16, 128, 1),
+    SGEMM_GB300_FORM(k16, 256, 1),
+    SGEMM_GB300_FORM(k16, 256, 2),
+};
+extern const int kNumForms16 = sizeof(kForms16) / sizeof(kForms16[0]);
 
 }  // namespace ragged
 }  // namespace sgemm_gb300

@@ -7,8 +7,6 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
-#include <mutex>
-
 #include "../../include/sgemm_gb300.h"
 #include "ragged_gemm.cuh"
 
@@ -35,56 +33,90 @@ struct Operand {
     return ((reinterpret_cast<uintptr_t>(ptr) & 15u) == 0) && (ld * elem) % 16 == 0 &&
            (batch <= 1 || (stride * elem) % 16 == 0);
   }
-  long long packed_ld() const { return (cols * elem + 15) / 16 * 16 / elem; }
-  size_t packed_bytes() const {
-    return direct() ? 0 : ((size_t)batch * rows * packed_ld() * elem + 255) / 256 * 256;
+  // The copy's row pitch and size in bytes; `widen`: 8-bit integers as F16
+  // (always copied).
+  long long packed_pitch(bool widen) const { return (cols * (widen ? 2 : elem) + 15) / 16 * 16; }
+  size_t packed_bytes(bool widen) const {
+    if (direct() && !widen) return 0;
+    return ((size_t)batch * rows * packed_pitch(widen) + 255) / 256 * 256;
   }
 };
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encode();
-// Copies `op` to `dst` with 16-byte aligned rows and describes the copy.
-cudaError_t pack_operand(Operand* op, void* dst, int sms, cudaStream_t stream);
+// Copies `op` to `dst` with 16-byte aligned rows (widen: as F16) and describes
+// the copy.
+cudaError_t pack_operand(Operand* op, bool widen, void* dst, int sms, cudaStream_t stream);
 // The 3-D map of an operand with boxes of box_rows rows of row_bytes bytes.
 bool encode_operand(CUtensorMap* map, const Operand& op, CUtensorMapDataType type, int row_bytes,
                     int box_rows);
 
-// One launch of ragged_kernel<SRC, BQ>; bq must be one of the built widths.
-cudaError_t launch_k16(int dev, int bq, int grid, const Params& p, const CUtensorMap& mp,
-                       const CUtensorMap& mq, cudaStream_t stream);
-cudaError_t launch_f32(int dev, int bq, int grid, const Params& p, const CUtensorMap& mp,
-                       const CUtensorMap& mq, cudaStream_t stream);
-cudaError_t launch_i8(int dev, int bq, int grid, const Params& p, const CUtensorMap& mp,
-                      const CUtensorMap& mq, cudaStream_t stream);
+// A built kernel: source, tile width, CTAs per worker (1, or 2: pairs).
+struct Form {
+  int src, bq, cl;
+};
+// Makes the kernel of a form ready on a device and gives the workers that are
+// resident at once (0: the form is not built, or pairs cannot run); launches it.
+cudaError_t form_workers(int dev, int sms, const Form& f, int* workers);
+cudaError_t form_launch(const Form& f, int workers, const Params& p, const CUtensorMap& mp,
+                        const CUtensorMap& mq, cudaStream_t stream);
 
-constexpr int kMaxDevices = 64;
+// One entry of the table of built kernels (a translation unit per source).
+struct FormEntry {
+  Form form;
+  cudaError_t (*prepare)(int sms, int* workers);
+  cudaError_t (*launch)(int workers, const Params& p, const CUtensorMap& mp, const CUtensorMap& mq,
+                        cudaStream_t stream);
+};
+extern const FormEntry kForms16[], kFormsF32[], kFormsI8[];
+extern const int kNumForms16, kNumFormsF32, kNumFormsI8;
 
-template <int SRC, int BQ>
-cudaError_t launch_one(int dev, int grid, const Params& p, const CUtensorMap& mp,
-                       const CUtensorMap& mq, cudaStream_t stream) {
-  static std::mutex mutex;
-  static bool ready[kMaxDevices];
-  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  {
-    std::lock_guard<std::mutex> lock(mutex);
-    if (!ready[dev]) {
-      const cudaError_t e = cudaFuncSetAttribute(
-          ragged_kernel<SRC, BQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-      if (e != cudaSuccess) return e;
-      ready[dev] = true;
-    }
+template <int SRC, int BQ, int CL>
+struct FormOf {
+  using G = Geo<SRC, BQ, CL>;
+  static cudaLaunchConfig_t config(int workers, cudaLaunchAttribute (&la)[2], cudaStream_t stream) {
+    la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    la[0].val.programmaticStreamSerializationAllowed = 1;
+    la[1].id = cudaLaunchAttributeClusterDimension;
+    la[1].val.clusterDim.x = CL;
+    la[1].val.clusterDim.y = 1;
+    la[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)(workers * CL));
+    lc.blockDim = dim3(G::kThreads);
+    lc.dynamicSmemBytes = kSmemBytes;
+    lc.stream = stream;
+    lc.attrs = la;
+    lc.numAttrs = CL == 2 ? 2 : 1;
+    return lc;
   }
-  cudaLaunchConfig_t lc = {};
-  cudaLaunchAttribute la[1];
-  la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  la[0].val.programmaticStreamSerializationAllowed = 1;
-  lc.gridDim = dim3((unsigned)grid);
-  lc.blockDim = dim3(Geo<SRC, BQ>::kThreads);
-  lc.dynamicSmemBytes = kSmemBytes;
-  lc.stream = stream;
-  lc.attrs = la;
-  lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, ragged_kernel<SRC, BQ>, p, mp, mq);
-}
+  static cudaError_t prepare(int sms, int* workers) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        ragged_kernel<SRC, BQ, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    *workers = sms;
+    if (e != cudaSuccess || CL == 1) return e;
+    // pairs that fit at once (SMs pair up within a GPC, so it can be below sms / 2)
+    cudaLaunchAttribute la[2];
+    cudaLaunchConfig_t lc = config(sms / 2 > 0 ? sms / 2 : 1, la, nullptr);
+    lc.attrs = la + 1;
+    lc.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, ragged_kernel<SRC, BQ, CL>, &lc) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    *workers = n;
+    return cudaSuccess;
+  }
+  static cudaError_t launch(int workers, const Params& p, const CUtensorMap& mp,
+                            const CUtensorMap& mq, cudaStream_t stream) {
+    cudaLaunchAttribute la[2];
+    const cudaLaunchConfig_t lc = config(workers, la, stream);
+    return cudaLaunchKernelEx(&lc, ragged_kernel<SRC, BQ, CL>, p, mp, mq);
+  }
+};
+
+#define SGEMM_GB300_FORM(SRC, BQ, CL) \
+  { {SRC, BQ, CL}, &FormOf<SRC, BQ, CL>::prepare, &FormOf<SRC, BQ, CL>::launch }
 
 }  // namespace ragged
 }  // namespace sgemm_gb300

@@ -571,6 +571,17 @@ int sgemm_i8(int M, int N, int K, const signed char* A, int lda, const float* sc
              void* stream);
 
 /*
+ * Tile of later sgemm_grouped, sgemm_grouped_wgrad and sgemm_i8 calls
+ * (process-wide; for measurements and tests): `width` token rows (wgrad: rows
+ * of C) by 128 output columns on one CTA (ctas = 1), or by 256 on a pair of CTAs
+ * that share their MMAs (ctas = 2). width 0 restores the choice by size. A call
+ * whose types have no kernel of that tile keeps its own choice. Results differ
+ * only in the order of sums. Returns SGEMM_ERR_INVALID_VALUE (nothing changed)
+ * for a tile that no kernel is built for.
+ */
+int sgemm_grouped_set_tile(int width, int ctas);
+
+/*
  * The 2-norm of n tensors taken together, and their clipping:
  *   norm = sqrt(sum of all g^2), coef = min(1, max_norm / (norm + 1e-6)),
  *   out_i = grads_i * coef.

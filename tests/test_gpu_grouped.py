@@ -273,3 +273,30 @@ def test_other_stream_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, want)
+
+
+FORMS = [(16, 1), (32, 1), (64, 1), (128, 1), (256, 1), (128, 2), (256, 2)]
+
+
+@pytest.fixture
+def tile(request):
+    assert B.sgemm_grouped_set_tile(*request.param) == 0
+    yield request.param
+    assert B.sgemm_grouped_set_tile(0) == 0
+
+
+@pytest.mark.parametrize("tile", FORMS, indirect=True, ids=str)
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+def test_every_tile(tile, t):
+    """Every built tile, on ragged groups of a few and of many tiles (whole
+    tiles, and tiles cut along k), with odd edges."""
+    for counts, n, k in [([3, 0, 300, 17], 264, 200), ([40], 130, 4100), ([900, 0, 1, 1500, 31], 1500, 136)]:
+        for op in ("T", "N"):
+            run_rows(op, TYPES[t], torch.float32, counts, n, k, ints=True, lead=1, tail=2, seed=k)
+    for counts, m, n in [([3, 0, 300, 17], 264, 200), ([5000, 31], 130, 140), ([900, 0, 1, 1500, 31], 700, 1000)]:
+        run_wgrad(TYPES[t], torch.float32, counts, m, n, ints=True, lead=1, tail=2, seed=m)
+
+
+def test_set_tile_refuses():
+    for width, ctas in [(8, 1), (16, 2), (512, 1), (-1, 1), (64, 3)]:
+        assert B.sgemm_grouped_set_tile(width, ctas) == B.SGEMM_ERR_INVALID_VALUE

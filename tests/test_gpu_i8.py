@@ -148,3 +148,29 @@ def test_quantised_linear_layer():
     want_q, want_s = reference_quantize(x.cpu().float())
     ref = exact_sum(torch.from_numpy(want_q), w) * torch.from_numpy(want_s).cuda().double()[:, None] * sw.double()
     assert bool(((y.double() - ref).abs() <= (2.0 ** -8 + 2.0 ** -22) * ref.abs()).all())
+
+
+@pytest.mark.parametrize("m,n,k", [(512, 130, 1000), (513, 264, 65), (1500, 777, 2049), (700, 1030, 16)])
+@pytest.mark.parametrize("pads", [0, 3])
+def test_many_rows(m, n, k, pads):
+    """The widened path: whole and cut tiles, odd edges, unaligned rows."""
+    a, da = ints((m, k), m, k + pads, pads)
+    b, db = ints((n, k), n + k, k + pads, 2 * pads)
+    sa, sb = torch.full((m,), 0.25, device="cuda"), torch.full((n,), 2.0, device="cuda")
+    got = B.i8_gemm(da, sa, db, sb, out_dtype=torch.float32)
+    assert B.sgemm_poll_device_status(torch.cuda.current_stream().cuda_stream)[0] == 0
+    assert torch.equal(got, (exact_sum(a, b) * 0.5).float())
+
+
+@pytest.mark.parametrize("form", [(16, 1), (32, 1), (64, 1), (128, 1), (256, 1), (256, 2)], ids=str)
+@pytest.mark.parametrize("m", [70, 600])
+def test_every_tile(form, m):
+    a, da = ints((m, 2100), 1)
+    b, db = ints((300, 2100), 2)
+    one_m, one_n = torch.ones(m, device="cuda"), torch.ones(300, device="cuda")
+    assert B.sgemm_grouped_set_tile(*form) == 0
+    try:
+        got = B.i8_gemm(da, one_m, db, one_n, out_dtype=torch.float32)
+    finally:
+        assert B.sgemm_grouped_set_tile(0) == 0
+    assert torch.equal(got, exact_sum(a, b).float())
