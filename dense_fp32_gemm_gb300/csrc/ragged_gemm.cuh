@@ -352,18 +352,41 @@ __device__ __forceinline__ void convert_i8(const unsigned char* raw, unsigned ch
   }
 }
 
-__device__ __forceinline__ float load_out(const void* base, long long at, int type) {
-  if (type == kOutF32) return static_cast<const float*>(base)[at];
-  if (type == kOutBf16) return __bfloat162float(static_cast<const __nv_bfloat16*>(base)[at]);
-  return __half2float(static_cast<const __half*>(base)[at]);
-}
-__device__ __forceinline__ void store_out(void* base, long long at, int type, float v) {
-  if (type == kOutF32)
-    static_cast<float*>(base)[at] = v;
-  else if (type == kOutBf16)
-    static_cast<__nv_bfloat16*>(base)[at] = __float2bfloat16_rn(v);
-  else
-    static_cast<__half*>(base)[at] = __float2half_rn(v);
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ void from_f32(float* d, float v) { *d = v; }
+__device__ __forceinline__ void from_f32(__nv_bfloat16* d, float v) { *d = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void from_f32(__half* d, float v) { *d = __float2half_rn(v); }
+
+// A thread's column of the tile: `n` valid values (of HC) at pitch ld. A warp
+// writes 32 neighbours at a time. The element type, the full column and beta
+// are decided once: the loops are unrolled over the registers, and a branch per
+// value made them outgrow the instruction cache (20 to 60 thousand cycles a
+// tile, against one thousand).
+template <bool INT, int HC, typename T>
+__device__ __forceinline__ void write_column(T* out, long long ld, const float (&sum)[HC],
+                                             float scale, const float* scale_q, float beta, int n) {
+  auto value = [&](int c) {
+    return INT ? (float)__float_as_int(sum[c]) * __ldg(scale_q + c) * scale : scale * sum[c];
+  };
+  if (beta == 0.f && n >= HC) {
+#pragma unroll
+    for (int c = 0; c < HC; ++c) {
+      from_f32(out, value(c));
+      out += ld;
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < HC; ++c) {
+      if (c < n) {
+        float v = value(c);
+        if (beta != 0.f) v = fmaf(beta, to_f32(*out), v);
+        from_f32(out, v);
+      }
+      out += ld;
+    }
+  }
 }
 
 template <int SRC, int BQ, int CL>
@@ -509,22 +532,26 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     if (G::kMoveRegs) ptx::regs_lower<G::kRegsFew>();
     // ---- warp 0: TMA producer ---------------------------------------------------
     if (warp == 0) {
-      int it = 0;
+      int it = 0, s = 0;
+      uint32_t phase = 1;       // parity of raw_empty to wait for
       uint32_t own_phase = 0;   // odd CTA: phases of its own raw_full barriers (a bit each)
       bool ok = true;
+      constexpr int BOX = G::kRawRow / G::kElem;  // elements along the fast dimension of a box
+      const bool p_mn = p.p_mn, q_mn = p.q_mn, wgrad = p.wgrad;
       Unit w;
       for (List list(p, sh, worker, workers); ok && list.next(w);) {
         const int p0 = w.p0 + rank * BP, q0 = w.q0 + rank * G::kRows;
-        for (int ks = w.kb; ks < w.ke; ++ks, ++it) {
-          const int s = it % RS;
-          ok = wait_for(ptx::smem_addr(&sh->raw_empty[s]), (uint32_t)((it / RS) & 1) ^ 1u, abort_w,
-                        p.status, kDevTimeoutEmpty, p.timeout_ns);
+        const int pe = wgrad ? 0 : w.e, qrow = wgrad ? 0 : w.row0 + q0;
+        int k = w.kb * SL + (wgrad ? w.row0 : 0);
+        for (int ks = w.kb; ks < w.ke; ++ks, ++it, k += SL) {
+          ok = wait_for(ptx::smem_addr(&sh->raw_empty[s]), phase, abort_w, p.status,
+                        kDevTimeoutEmpty, p.timeout_ns);
           ok = __all_sync(kAll, ok);
           if (!ok) break;
           // pair: the even CTA's MMA warp waits for the loads of both, but for
           // a stage that the odd CTA has to clear
           const bool remote = kPair && !G::kConv && rank != 0 && !clears(w, ks);
-          if (rank != 0 && !remote) own_phase ^= 1u << s;
+          if (kPair && !G::kConv && rank != 0 && !remote) own_phase ^= 1u << s;
           if (ptx::elect_one()) {
             uint32_t fb = ptx::smem_addr(&sh->raw_full[s]);
             const uint32_t st = raw_base_addr + (uint32_t)(s * G::kRaw);
@@ -540,25 +567,26 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
               else
                 ptx::tma_load_3d(dst, map, x, y, z, fb);
             };
-            const int k = ks * SL + (p.wgrad ? w.row0 : 0);
-            constexpr int BOX = G::kRawRow / G::kElem;  // elements along the fast dimension of a box
-            if (p.p_mn) {
+            if (p_mn) {
 #pragma unroll
               for (int i = 0; i < BP / BOX; ++i)
-                load(st + (uint32_t)(i * SL * G::kRawRow), &mapP, p0 + i * BOX, k,
-                     p.wgrad ? 0 : w.e);
+                load(st + (uint32_t)(i * SL * G::kRawRow), &mapP, p0 + i * BOX, k, pe);
             } else {
-              load(st, &mapP, k, p0, w.e);
+              load(st, &mapP, k, p0, pe);
             }
-            if (p.q_mn) {
+            if (q_mn) {
 #pragma unroll
               for (int i = 0; i < G::kRows / BOX; ++i)
                 load(st + (uint32_t)(G::kRawP + i * SL * G::kRawRow), &mapQ, q0 + i * BOX, k, 0);
             } else {
-              load(st + G::kRawP, &mapQ, k, w.row0 + q0, 0);
+              load(st + G::kRawP, &mapQ, k, qrow, 0);
             }
           }
           __syncwarp();
+          if (++s == RS) {
+            s = 0;
+            phase ^= 1u;
+          }
         }
       }
       // nothing may land after the CTA is gone: wait (bounded) for the last
@@ -587,8 +615,14 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     // ---- warp 1: MMA issuer (even CTA of a pair), or relay (odd CTA) --------------
     if (warp == 1) {
     // operand tiles: K-major rows of 128 bytes (64 for kF32) in 8-row groups;
-    // MN-major chunks of 64 elements x SL rows of k, 128 bytes a row
+    // MN-major chunks of 64 elements x SL rows of k, 128 bytes a row. The
+    // descriptors of stage 0 are made once; a stage, a part or a k-step moves
+    // their address field. (Made anew for every MMA they cost more than a
+    // slice's MMAs: the loop below took 540 cycles for a slice of any size.)
     constexpr bool kNarrow = SRC == kF32;
+    constexpr int OP_P = G::kConv ? G::kOpP : G::kRawP;   // one part
+    constexpr int OP_Q = G::kConv ? G::kOpQ : G::kRawQ;
+    constexpr uint32_t kStage16 = (G::kConv ? G::kOp : G::kRaw) >> 4;
     const bool a_mn = p.p_mn, b_mn = p.q_mn;
     const uint32_t idesc =
         tc::idesc_f16(BP * CL, BQ, SRC == kF32 || (SRC == k16 && p.bf16), a_mn, b_mn);
@@ -596,11 +630,28 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
       return mn ? tc::smem_desc(addr, SL * 128, 1024, true)
                 : tc::smem_desc(addr, 16, kNarrow ? 512 : 1024, !kNarrow);
     };
+    const uint64_t a_desc = desc(base_addr, a_mn);
+    const uint64_t b_desc = desc(base_addr + (uint32_t)(G::kParts * OP_P), b_mn);
+    const uint32_t a_step = a_mn ? 2048u >> 4 : 32u >> 4, b_step = b_mn ? 2048u >> 4 : 32u >> 4;
     auto mma = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t add) {
       if (kPair)
         tc::mma_f16_pair(d, a, b, idesc, add);
       else
         tc::mma_f16(d, a, b, idesc, add);
+    };
+    // the MMAs of one 16-wide k-step
+    auto step = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t add) {
+      if (SRC == kF32) {
+        constexpr uint64_t P1 = OP_P >> 4, Q1 = OP_Q >> 4;
+        mma(d, a + 2 * P1, b, add);
+        mma(d, a, b + 2 * Q1, 1u);
+        mma(d, a + P1, b + Q1, 1u);
+        mma(d, a + P1, b, 1u);
+        mma(d, a, b + Q1, 1u);
+        mma(d, a, b, 1u);
+      } else {
+        mma(d, a, b, add);
+      }
     };
     auto commit = [&](uint64_t* bar) {
       if (kPair)
@@ -608,13 +659,14 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
       else
         tc::commit(ptx::smem_addr(bar));
     };
-    const uint32_t a_step = a_mn ? 2048u : 32u, b_step = b_mn ? 2048u : 32u;
-    int it = 0, acc = 0;
+    int acc = 0, s = 0;
+    uint32_t phase = 0;       // parity of the full barriers to wait for
     uint32_t own_phase = 0;   // odd CTA: next phases of its own raw_full barriers
     bool issued_any = false, ok = true;
+    const int chunk = p.chunk;
     Unit w;
     for (List list(p, sh, worker, workers); ok && list.next(w);) {
-      for (int k0 = w.kb; k0 < w.ke && ok; k0 += p.chunk, ++acc) {
+      for (int k0 = w.kb; k0 < w.ke && ok; k0 += chunk, ++acc) {
         const int buf = acc & 1;
         const uint32_t d = tmem + (uint32_t)(buf * BQ);
         if (rank == 0) {
@@ -626,34 +678,33 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
           if (!ok) break;
           tc::fence_after_sync();
         }
-        const int k1 = min(w.ke, k0 + p.chunk);
-        for (int ks = k0; ks < k1; ++ks, ++it) {
-          const int s = it % OS;
-          const uint32_t par = (uint32_t)((it / OS) & 1);
+        const int k1 = min(w.ke, k0 + chunk);
+        for (int ks = k0; ks < k1; ++ks) {
           const bool clear = clears(w, ks);
           const int rem = w.klen - ks * SL;   // > 0
-          const int steps = min(SL / 16, cdiv(rem, 16));
-          const uint32_t st = base_addr + (uint32_t)(s * (G::kConv ? G::kOp : G::kRaw));
-          if (kPair && !G::kConv && rank != 0 && !clear) continue;
-          if (G::kConv || !kPair) {
-            ok = wait_for(ptx::smem_addr(G::kConv ? &sh->op_full[s] : &sh->raw_full[s]), par,
-                              abort_w, p.status, kDevTimeoutFull, p.timeout_ns);
-          } else if (rank == 0) {
-            // the loads of both CTAs (and what the odd one has cleared)
-            ok = wait_for_pair(ptx::smem_addr(&sh->raw_full[s]), par, abort_w, p.status,
-                                   kDevTimeoutFull, p.timeout_ns);
-          } else {
-            ok = wait_for(ptx::smem_addr(&sh->raw_full[s]), own_phase >> s & 1u, abort_w,
-                              p.status, kDevTimeoutFull, p.timeout_ns);
-            own_phase ^= 1u << s;
+          if (!kPair || G::kConv || rank == 0 || clear) {
+            if (G::kConv || !kPair) {
+              ok = wait_for(ptx::smem_addr(G::kConv ? &sh->op_full[s] : &sh->raw_full[s]), phase,
+                            abort_w, p.status, kDevTimeoutFull, p.timeout_ns);
+            } else if (rank == 0) {
+              // the loads of both CTAs (and what the odd one has cleared)
+              ok = clear ? wait_for_pair(ptx::smem_addr(&sh->raw_full[s]), phase, abort_w, p.status,
+                                         kDevTimeoutFull, p.timeout_ns)
+                         : wait_for(ptx::smem_addr(&sh->raw_full[s]), phase, abort_w, p.status,
+                                    kDevTimeoutFull, p.timeout_ns);
+            } else {
+              ok = wait_for(ptx::smem_addr(&sh->raw_full[s]), own_phase >> s & 1u, abort_w,
+                            p.status, kDevTimeoutFull, p.timeout_ns);
+              own_phase ^= 1u << s;
+            }
+            ok = __all_sync(kAll, ok);
+            if (!ok) break;
           }
-          ok = __all_sync(kAll, ok);
-          if (!ok) break;
           if (clear) {
             // clear the rows of k past the group's end in both operands up to
             // the end of their 16-row step (the steps beyond are not issued)
             unsigned char* stp = base + s * G::kRaw;
-            const int nz = steps * 16 - rem;
+            const int nz = cdiv(rem, 16) * 16 - rem;
             constexpr int kBoxes = (BP + G::kRows) / 64;
             for (int i = lane; i < kBoxes * nz * 8; i += 32) {
               const int box = i / (nz * 8), r = i - box * nz * 8;
@@ -664,44 +715,39 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
             __syncwarp();
           }
           if (rank != 0) {
-            if (lane == 0)
+            if ((G::kConv || clear) && lane == 0)
               ptx::mbar_arrive_remote(
                   ptx::mapa(ptx::smem_addr(G::kConv ? &sh->peer_full[s] : &sh->raw_full[s]), 0u));
-            continue;
-          }
-          if (kPair && G::kConv) {
-            ok = wait_for_pair(ptx::smem_addr(&sh->peer_full[s]), par, abort_w, p.status,
-                                   kDevTimeoutFull, p.timeout_ns);
-            ok = __all_sync(kAll, ok);
-            if (!ok) break;
-          }
-          tc::fence_after_sync();
-          if (ptx::elect_one()) {
-            constexpr int OP_P = G::kConv ? G::kOpP : G::kRawP;   // one part
-            constexpr int OP_Q = G::kConv ? G::kOpQ : G::kRawQ;
-            const uint32_t pa = st, qa = st + (uint32_t)(G::kParts * OP_P);
-            for (int kk = 0; kk < steps; ++kk) {
-              const uint32_t first = (ks == k0 && kk == 0) ? 0u : 1u;
-              const uint64_t a0 = desc(pa + kk * a_step, a_mn), b0 = desc(qa + kk * b_step, b_mn);
-              if (SRC == kF32) {
-                const uint64_t a1 = desc(pa + OP_P + kk * a_step, a_mn);
-                const uint64_t a2 = desc(pa + 2 * OP_P + kk * a_step, a_mn);
-                const uint64_t b1 = desc(qa + OP_Q + kk * b_step, b_mn);
-                const uint64_t b2 = desc(qa + 2 * OP_Q + kk * b_step, b_mn);
-                mma(d, a2, b0, first);
-                mma(d, a0, b2, 1u);
-                mma(d, a1, b1, 1u);
-                mma(d, a1, b0, 1u);
-                mma(d, a0, b1, 1u);
-                mma(d, a0, b0, 1u);
-              } else {
-                mma(d, a0, b0, first);
-              }
+          } else {
+            if (kPair && G::kConv) {
+              ok = wait_for_pair(ptx::smem_addr(&sh->peer_full[s]), phase, abort_w, p.status,
+                                 kDevTimeoutFull, p.timeout_ns);
+              ok = __all_sync(kAll, ok);
+              if (!ok) break;
             }
-            commit(G::kConv ? &sh->op_empty[s] : &sh->raw_empty[s]);
+            tc::fence_after_sync();
+            if (ptx::elect_one()) {
+              const uint64_t a = a_desc + (uint64_t)(s * kStage16);
+              const uint64_t b = b_desc + (uint64_t)(s * kStage16);
+              const uint32_t add = ks == k0 ? 0u : 1u;
+              if (rem >= SL) {
+#pragma unroll
+                for (int kk = 0; kk < SL / 16; ++kk)
+                  step(d, a + kk * a_step, b + kk * b_step, kk == 0 ? add : 1u);
+              } else {
+#pragma unroll 1
+                for (int kk = 0; kk * 16 < rem; ++kk)
+                  step(d, a + kk * a_step, b + kk * b_step, kk == 0 ? add : 1u);
+              }
+              commit(G::kConv ? &sh->op_empty[s] : &sh->raw_empty[s]);
+            }
+            __syncwarp();
+            issued_any = true;
           }
-          __syncwarp();
-          issued_any = true;
+          if (++s == OS) {
+            s = 0;
+            phase ^= 1u;
+          }
         }
         if (!ok) break;
         if (rank == 0 && ptx::elect_one()) commit(&sh->acc_full[buf]);
@@ -891,21 +937,18 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
       }
       const int pp = w.p0 + rank * BP + pr;
       if (pp < p.P && nq > 0) {
-        const float sp = G::kInt ? p.scale_p[pp] : 1.f;
+        const float sp = G::kInt ? p.scale_p[pp] : p.alpha;
         const long long row = (long long)(p.wgrad ? 0 : w.row0) + w.q0 + half * HC;
-        const long long at0 = (p.wgrad ? (long long)w.e * p.stride_o : 0ll) + row * p.ldo + pp;
-#pragma unroll
-        for (int c = 0; c < HC; ++c) {
-          if (c >= nq) continue;
-          const long long at = at0 + c * p.ldo;
-          float v;
-          if (G::kInt)
-            v = (float)__float_as_int(sum[c]) * p.scale_q[row + c] * sp;
-          else
-            v = p.alpha * sum[c];
-          if (p.beta != 0.f) v = fmaf(p.beta, load_out(p.out, at, p.out_type), v);
-          store_out(p.out, at, p.out_type, v);
-        }
+        const long long at = (p.wgrad ? (long long)w.e * p.stride_o : 0ll) + row * p.ldo + pp;
+        const float* sq = G::kInt ? p.scale_q + row : nullptr;
+        if (p.out_type == kOutF32)
+          write_column<G::kInt, HC>(static_cast<float*>(p.out) + at, p.ldo, sum, sp, sq, p.beta, nq);
+        else if (p.out_type == kOutBf16)
+          write_column<G::kInt, HC>(static_cast<__nv_bfloat16*>(p.out) + at, p.ldo, sum, sp, sq,
+                                    p.beta, nq);
+        else
+          write_column<G::kInt, HC>(static_cast<__half*>(p.out) + at, p.ldo, sum, sp, sq, p.beta,
+                                    nq);
       }
     }
   }
