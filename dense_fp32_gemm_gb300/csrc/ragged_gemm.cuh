@@ -180,6 +180,7 @@ struct Unit {
   int e, p0, q0;       // group, first p, first q within the group
   int row0, nq;        // first token row of the group; valid q in the tile
   int kb, ke, klen;    // slices of this unit, contraction length
+  int clear;           // wgrad: the slice whose last rows belong to the next group, or -1
   int c0, parts;       // workers c0 .. c0 + parts - 1 share the tile
 };
 
@@ -245,6 +246,8 @@ struct Walk {
     u.nq = min(BQ, qdim - u.q0);
     u.klen = p.K == 0 ? 0 : (p.wgrad ? n : p.K);
     if (u.klen == 0) u.ke = u.kb;   // nothing to add
+    // a sum that ends inside a 16-row step of its last slice
+    u.clear = p.wgrad && (u.klen & 15) ? u.klen / SLICE : -1;
     return true;
   }
 };
@@ -416,11 +419,10 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
 
   if (tid == 0) {
     // pair form: the even CTA's MMA warp waits on the stages of both CTAs
-    // (converted ones: its own, and one relayed arrival for the odd CTA's),
-    // and on the epilogue warps of both; its commits arrive in both CTAs
+    // (converted or cleared ones: its own, and one relayed arrival for the odd
+    // CTA's), and on the epilogue warps of both; its commits arrive in both
     for (int s = 0; s < RS; ++s) {
-      // (even CTA of a pair: the producers of both)
-      ptx::mbar_init(ptx::smem_addr(&sh->raw_full[s]), kPair && !G::kConv && rank == 0 ? 2 : 1);
+      ptx::mbar_init(ptx::smem_addr(&sh->raw_full[s]), 1);
       ptx::mbar_init(ptx::smem_addr(&sh->raw_empty[s]), G::kConv ? kConvWarps : 1);
     }
     for (int s = 0; s < OS; ++s) {
@@ -521,13 +523,6 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     __syncthreads();  // every role sees the abort word
   }
 
-  // a stage whose rows of k end inside a 16-row step (wgrad): the rows behind
-  // them belong to the next group and are cleared by warp 1
-  auto clears = [&](const Unit& u, int ks) {
-    const int rem = u.klen - ks * SL;
-    return !G::kConv && p.wgrad && (rem & 15) != 0 && rem < SL;
-  };
-
   if (warp < kEpiWarp0) {
     if (G::kMoveRegs) ptx::regs_lower<G::kRegsFew>();
     // ---- warp 0: TMA producer ---------------------------------------------------
@@ -548,19 +543,21 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
                         kDevTimeoutEmpty, p.timeout_ns);
           ok = __all_sync(kAll, ok);
           if (!ok) break;
-          // pair: the even CTA's MMA warp waits for the loads of both, but for
-          // a stage that the odd CTA has to clear
-          const bool remote = kPair && !G::kConv && rank != 0 && !clears(w, ks);
-          if (kPair && !G::kConv && rank != 0 && !remote) own_phase ^= 1u << s;
+          // pair: the even CTA's barrier counts the bytes of both (the odd
+          // CTA's loads may complete before it expects them), but for a stage
+          // that the odd CTA has to clear. (A remote arrival for each of the
+          // odd CTA's stages took its producer 1300 cycles.)
+          const bool clear = !G::kConv && ks == w.clear;
+          const bool remote = kPair && !G::kConv && rank != 0 && !clear;
+          if (kPair && !G::kConv && rank != 0 && clear) own_phase ^= 1u << s;
           if (ptx::elect_one()) {
             uint32_t fb = ptx::smem_addr(&sh->raw_full[s]);
             const uint32_t st = raw_base_addr + (uint32_t)(s * G::kRaw);
-            if (remote) {
+            if (remote)
               fb = ptx::mapa(fb, 0u);
-              ptx::mbar_arrive_expect_tx_remote(fb, (uint32_t)G::kRaw);
-            } else {
-              ptx::mbar_arrive_expect_tx(fb, (uint32_t)G::kRaw);
-            }
+            else
+              ptx::mbar_arrive_expect_tx(
+                  fb, (uint32_t)(kPair && !G::kConv && !clear ? 2 * G::kRaw : G::kRaw));
             auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, int z) {
               if (kPair && !G::kConv)
                 ptx::tma_load_3d_pair(dst, map, x, y, z, fb);
@@ -661,7 +658,9 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     };
     int acc = 0, s = 0;
     uint32_t phase = 0;       // parity of the full barriers to wait for
-    uint32_t own_phase = 0;   // odd CTA: next phases of its own raw_full barriers
+    // phases (a bit per stage) of the barriers that only cleared stages use:
+    // the odd CTA's raw_full, the even one's peer_full
+    uint32_t own_phase = 0;
     bool issued_any = false, ok = true;
     const int chunk = p.chunk;
     Unit w;
@@ -680,23 +679,13 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
         }
         const int k1 = min(w.ke, k0 + chunk);
         for (int ks = k0; ks < k1; ++ks) {
-          const bool clear = clears(w, ks);
+          const bool clear = !G::kConv && ks == w.clear;
           const int rem = w.klen - ks * SL;   // > 0
+          const uint32_t bit = 1u << s;
           if (!kPair || G::kConv || rank == 0 || clear) {
-            if (G::kConv || !kPair) {
-              ok = wait_for(ptx::smem_addr(G::kConv ? &sh->op_full[s] : &sh->raw_full[s]), phase,
-                            abort_w, p.status, kDevTimeoutFull, p.timeout_ns);
-            } else if (rank == 0) {
-              // the loads of both CTAs (and what the odd one has cleared)
-              ok = clear ? wait_for_pair(ptx::smem_addr(&sh->raw_full[s]), phase, abort_w, p.status,
-                                         kDevTimeoutFull, p.timeout_ns)
-                         : wait_for(ptx::smem_addr(&sh->raw_full[s]), phase, abort_w, p.status,
-                                    kDevTimeoutFull, p.timeout_ns);
-            } else {
-              ok = wait_for(ptx::smem_addr(&sh->raw_full[s]), own_phase >> s & 1u, abort_w,
-                            p.status, kDevTimeoutFull, p.timeout_ns);
-              own_phase ^= 1u << s;
-            }
+            const uint32_t par = kPair && rank != 0 && !G::kConv ? (own_phase & bit) != 0 : phase;
+            ok = wait_for(ptx::smem_addr(G::kConv ? &sh->op_full[s] : &sh->raw_full[s]), par,
+                          abort_w, p.status, kDevTimeoutFull, p.timeout_ns);
             ok = __all_sync(kAll, ok);
             if (!ok) break;
           }
@@ -716,11 +705,12 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
           }
           if (rank != 0) {
             if ((G::kConv || clear) && lane == 0)
-              ptx::mbar_arrive_remote(
-                  ptx::mapa(ptx::smem_addr(G::kConv ? &sh->peer_full[s] : &sh->raw_full[s]), 0u));
+              ptx::mbar_arrive_remote(ptx::mapa(ptx::smem_addr(&sh->peer_full[s]), 0u));
           } else {
-            if (kPair && G::kConv) {
-              ok = wait_for_pair(ptx::smem_addr(&sh->peer_full[s]), phase, abort_w, p.status,
+            if (kPair && (G::kConv || clear)) {
+              // what threads of the odd CTA have written
+              const uint32_t par = G::kConv ? phase : (own_phase & bit) != 0;
+              ok = wait_for_pair(ptx::smem_addr(&sh->peer_full[s]), par, abort_w, p.status,
                                  kDevTimeoutFull, p.timeout_ns);
               ok = __all_sync(kAll, ok);
               if (!ok) break;
@@ -744,6 +734,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
             __syncwarp();
             issued_any = true;
           }
+          if (kPair && clear) own_phase ^= bit;
           if (++s == OS) {
             s = 0;
             phase ^= 1u;
