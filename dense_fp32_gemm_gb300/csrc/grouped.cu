@@ -263,6 +263,7 @@ int run(int src, int type, Params p, Operand op_p, Operand op_q, long long per, 
     return SGEMM_ERR_LAUNCH;
   }
   p.partials = reinterpret_cast<float*>(at + pack_p + pack_q);
+  p.cut_slices = 4 + bq / 16;
   p.timeout_ns = library_wait_timeout_ns();
 
   CUtensorMap mp = {}, mq = {};

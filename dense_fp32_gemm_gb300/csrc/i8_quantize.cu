@@ -28,32 +28,105 @@ __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 
 constexpr int kThreads = 256;
 
-template <typename E>
+// 16 values of a row at a time: from any address (V: 16-byte aligned), and as 8-bit
+// integers to any address.
+template <typename E, bool V>
+__device__ __forceinline__ void load_16(const E* x, int n, float (&v)[16]) {
+  if (V && n >= 16) {
+    constexpr int W = sizeof(E);      // 16-byte vectors of the 16 values
+    uint4 raw[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) raw[i] = __ldg(reinterpret_cast<const uint4*>(x) + i);
+    const E* e = reinterpret_cast<const E*>(raw);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = to_f32(e[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = i < n ? to_f32(x[i]) : 0.f;
+  }
+}
+
+// rint(x / s), the quotient rounded to FP32 first. x * (1 / s) is within 2^-22
+// of it (relative), so the two round to the same integer unless the product
+// lies that near to the middle of two integers; only then the division runs.
+__device__ __forceinline__ int quotient(float x, float s, float inv) {
+  float v = x * inv;
+  const float r = rintf(v);
+  if (!(fabsf(fabsf(v - r) - 0.5f) >= 1e-4f) || !(inv < 1e37f)) {   // (or no number)
+    v = __fdiv_rn(x, s);
+    if (!(v == v)) return 0;
+    return __float2int_rn(fminf(fmaxf(v, -127.f), 127.f));
+  }
+  return __float2int_rn(fminf(fmaxf(r, -127.f), 127.f));
+}
+
+template <typename E, bool V>
+__device__ __forceinline__ uint32_t magnitude(const float (&v)[16], uint32_t most) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) most = max(most, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  return most;
+}
+
+// One row per block of `threads` = blockDim.x. Up to 16 * kHeld values a thread
+// stay in registers between the two passes (the maximum, the quotients); of a
+// longer row the rest is read again. One read of X and one write of Q are all
+// that a call has to move: at 4096 x 4096 bf16 it is bound by them.
+template <typename E, bool V>
 __global__ void __launch_bounds__(kThreads)
     quantize_kernel(int M, int K, const E* __restrict__ X, long long ldx,
                     signed char* __restrict__ Q, long long ldq, float* __restrict__ scale) {
   __shared__ uint32_t warp_max[kThreads / 32];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
+  const int step = 16 * blockDim.x, k0 = 16 * threadIdx.x;
+  constexpr int kHeld = 2;
   for (int m = blockIdx.x; m < M; m += gridDim.x) {
     const E* x = X + m * ldx;
     // magnitudes compared as bit patterns: a NaN is above infinity, so either
     // survives the maximum
     uint32_t most = 0;
-    for (int k = threadIdx.x; k < K; k += kThreads)
-      most = max(most, __float_as_uint(to_f32(x[k])) & 0x7FFFFFFFu);
+    float held[kHeld][16];
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) load_16<E, V>(x + k0 + h * step, K - k0 - h * step, held[h]);
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) most = magnitude<E, V>(held[h], most);
+    for (int k = k0 + kHeld * step; k < K; k += step) {
+      float v[16];
+      load_16<E, V>(x + k, K - k, v);
+      most = magnitude<E, V>(v, most);
+    }
     most = __reduce_max_sync(0xffffffffu, most);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = most;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) most = max(most, warp_max[w]);
+    for (int w = 0; w < (int)blockDim.x / 32; ++w) most = max(most, warp_max[w]);
     const float s = __fdiv_rn(__uint_as_float(most), 127.f);
     if (threadIdx.x == 0) scale[m] = s;
-    for (int k = threadIdx.x; k < K; k += kThreads) {
-      const float v = s > 0.f ? __fdiv_rn(to_f32(x[k]), s) : 0.f;   // (NaN scale: 0)
-      const int q = __float2int_rn(fminf(fmaxf(v, -127.f), 127.f));
-      Q[m * ldq + k] = (signed char)(v == v ? q : 0);
+    const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
+    auto put = [&](const float (&v)[16], int k) {
+      const int n = K - k;
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+      if (s > 0.f) {     // (a NaN scale: zeros)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          w[i >> 2] |= (uint32_t)(quotient(v[i], s, inv) & 255) << (8 * (i & 3));
+      }
+      signed char* q = Q + m * ldq + k;
+      if (n >= 16 && (reinterpret_cast<uintptr_t>(q) & 15u) == 0) {
+        *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (i < n) q[i] = (signed char)(w[i >> 2] >> (8 * (i & 3)));
+      }
+    };
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h)
+      if (k0 + h * step < K) put(held[h], k0 + h * step);
+    for (int k = k0 + kHeld * step; k < K; k += step) {
+      float v[16];
+      load_16<E, V>(x + k, K - k, v);
+      put(v, k);
     }
   }
 }
@@ -65,13 +138,20 @@ cudaError_t quantize(int M, int K, const void* X, int ldx, signed char* Q, int l
   cudaLaunchAttribute la[1];
   la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   la[0].val.programmaticStreamSerializationAllowed = 1;
-  lc.gridDim = dim3((unsigned)(M < sms * 8 ? M : sms * 8));
-  lc.blockDim = dim3(kThreads);
+  // as many threads as the row has 16-value pieces: short rows take few
+  int threads = (K + 15) / 16;
+  threads = threads < 32 ? 32 : (threads + 31) / 32 * 32;
+  if (threads > kThreads) threads = kThreads;
+  const int fit = sms * (2048 / kThreads) * (kThreads / threads);
+  lc.gridDim = dim3((unsigned)(M < fit ? M : fit));
+  lc.blockDim = dim3((unsigned)threads);
   lc.stream = stream;
   lc.attrs = la;
   lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, quantize_kernel<E>, M, K, static_cast<const E*>(X),
-                            (long long)ldx, Q, (long long)ldq, scale);
+  const bool aligned = (reinterpret_cast<uintptr_t>(X) & 15u) == 0 &&
+                       ((long long)ldx * (int)sizeof(E)) % 16 == 0;
+  return cudaLaunchKernelEx(&lc, aligned ? quantize_kernel<E, true> : quantize_kernel<E, false>, M,
+                            K, static_cast<const E*>(X), (long long)ldx, Q, (long long)ldq, scale);
 }
 
 }  // namespace

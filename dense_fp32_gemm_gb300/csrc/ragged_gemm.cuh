@@ -15,9 +15,9 @@
 // Sources (SRC) and how they become MMA operands:
 //   k16   BF16 or F16 tiles, read by the MMAs as TMA wrote them;
 //   kF32  FP32 tiles, cut by converter warps into three BF16 parts
-//         x = h + m + l (8 significant bits each, rounded to nearest, so 24 in
-//         all); per k-step the six products hh, hm, mh, mm, hl, lh are
-//         accumulated, what is dropped is below 2^-24 |a b|;
+//         x = h + m + l (8 significant bits each, 24 in all); per k-step the
+//         six products hh, hm, mh, mm, hl, lh are accumulated, what is dropped
+//         is below 2^-23 |a b|;
 //   kI8   8-bit integers, turned by converter warps into F16 (exact), since
 //         sm_103a has no integer tensor instruction of this generation. A
 //         product is at most 2^14, so the FP32 sums of 1024 products are
@@ -95,6 +95,7 @@ struct Params {
   const float* scale_p;   // kI8: scales of p and q
   const float* scale_q;
   int chunk;              // k-slices per tensor-memory accumulation
+  int cut_slices;         // tiles are cut along k only to save at least so many k-slices
   float* partials;        // two tiles of BQ x 128 floats per CTA
   uint32_t* counters;     // arrivals at a cut tile, one per CTA, zero between launches
   int* status;
@@ -117,12 +118,18 @@ struct Geo {
   static constexpr int kOpP = BP * kSlice * 2, kOpQ = kRows * kSlice * 2;  // one part
   static constexpr int kOp = kConv ? kParts * (kOpP + kOpQ) : 0;
   static constexpr int kRegion = 192 * 1024;
-  // operand stages first (at most 4), then as many raw stages as fit
-  static constexpr int kOpFit = kConv ? (kRegion - 2 * kRaw) / kOp : 0;
-  static constexpr int kOpStages = kConv ? (kOpFit < 4 ? kOpFit : 4) : 0;
+  // Converter warps work in groups that take the slices in turn: a slice's
+  // conversion is a chain of latencies (wait, load, store, proxy fence), and
+  // the chains of several slices overlap. Four groups where four stages of
+  // each kind fit, else two. A raw stage always belongs to one group (their
+  // number is a multiple of the groups): a group that waited for a stage in
+  // which another group's slice has not landed yet would take the phase before
+  // that one for its own.
+  static constexpr int kConvGroups = !kConv ? 1 : (4 * (kOp + kRaw) <= kRegion ? 4 : 2);
+  static constexpr int kGroupWarps = kConvWarps / kConvGroups;
+  static constexpr int kOpStages = kConv ? kConvGroups : 0;
   static constexpr int kRawFit = (kRegion - kOpStages * kOp) / kRaw;
-  static constexpr int kRawStages = kRawFit < 12 ? kRawFit : 12;
-  static_assert(!kConv || kOpStages >= 2, "operand stages");
+  static constexpr int kRawStages = (kRawFit < 12 ? kRawFit : 12) / kConvGroups * kConvGroups;
   static_assert(kRawStages >= 2, "raw stages");
   static constexpr int kThreads = (kConv ? kConvWarp0 + kConvWarps : kConvWarp0) * 32;
   // A thread of the epilogue holds BQ / 2 sums. For the widest tiles of a kind
@@ -285,16 +292,18 @@ __device__ __forceinline__ bool wait_for_pair(uint32_t bar, uint32_t parity, vol
 }
 
 // ---- conversions --------------------------------------------------------------
-// Two FP32 values into packed BF16 parts h, m, l (x = h + m + l up to 2^-24 |x|).
+// Two FP32 values into packed BF16 parts with x = h + m + l exactly (but for
+// underflow): h is x rounded to nearest, so at most 16 significant bits are
+// left, of which m takes the first 8 and l the rest (both by truncation: two
+// byte permutes instead of two conversions).
 __device__ __forceinline__ void split2(float x, float y, uint32_t& h, uint32_t& m, uint32_t& l) {
-  auto pack = [](float a, float b) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  };
-  h = pack(x, y);
+  const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+  h = *reinterpret_cast<const uint32_t*>(&v);
   const float rx = x - __uint_as_float(h << 16), ry = y - __uint_as_float(h & 0xFFFF0000u);
-  m = pack(rx, ry);
-  l = pack(rx - __uint_as_float(m << 16), ry - __uint_as_float(m & 0xFFFF0000u));
+  m = __byte_perm(__float_as_uint(rx), __float_as_uint(ry), 0x7632);
+  const float sx = rx - __uint_as_float(__float_as_uint(rx) & 0xFFFF0000u);
+  const float sy = ry - __uint_as_float(__float_as_uint(ry) & 0xFFFF0000u);
+  l = __byte_perm(__float_as_uint(sx), __float_as_uint(sy), 0x7632);
 }
 
 // Four 8-bit integers into four F16 values: with the sign bit flipped a byte
@@ -423,11 +432,11 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     // CTA's), and on the epilogue warps of both; its commits arrive in both
     for (int s = 0; s < RS; ++s) {
       ptx::mbar_init(ptx::smem_addr(&sh->raw_full[s]), 1);
-      ptx::mbar_init(ptx::smem_addr(&sh->raw_empty[s]), G::kConv ? kConvWarps : 1);
+      ptx::mbar_init(ptx::smem_addr(&sh->raw_empty[s]), G::kConv ? G::kGroupWarps : 1);
     }
     for (int s = 0; s < OS; ++s) {
       if (G::kConv) {
-        ptx::mbar_init(ptx::smem_addr(&sh->op_full[s]), kConvWarps);
+        ptx::mbar_init(ptx::smem_addr(&sh->op_full[s]), G::kGroupWarps);
         ptx::mbar_init(ptx::smem_addr(&sh->op_empty[s]), 1);
       }
       ptx::mbar_init(ptx::smem_addr(&sh->peer_full[s]), 1);
@@ -488,12 +497,17 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     if (lane == 0) {
       const int tiles = tiles_before, total = pos_before;
       sh->tiles = tiles;
-      // whole waves first; what is left, one to two waves, by slices
-      int dp = 0;
-      dp = tiles % workers == 0 ? tiles : max(0, tiles / workers - 1) * workers;
+      // whole waves first; what is left, one to two waves, by slices, unless
+      // that saves less time than publishing and adding the parts takes
+      const int over = tiles % workers;
+      const int saved = over == 0 ? 0 : (int)((long long)total / tiles * (workers - over) / workers);
+      int dp = tiles;
+      if (over != 0 && saved >= p.cut_slices) dp = max(0, tiles / workers - 1) * workers;
       sh->dp = dp;
       int base_pos = total;
-      if (dp < tiles) {
+      if (dp == 0) {
+        base_pos = 0;
+      } else if (dp < tiles) {
         List l(p, sh, 0, 0);
         const int e = l.find(sh->first, dp);
         base_pos = sh->pos[e] + (dp - sh->first[e]) * tile_slices<SL>(p, sh->rows[e]);
@@ -764,18 +778,20 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
   } else if (G::kConv && warp >= kConvWarp0) {
     // ---- converters: raw tiles -> operand tiles ----------------------------------
     if (G::kMoveRegs) ptx::regs_lower<G::kRegsConv>();
-    const int t = tid - kConvWarp0 * 32;
-    constexpr int NT = kConvWarps * 32;
+    const int group = (warp - kConvWarp0) / G::kGroupWarps;
+    const int t = tid - (kConvWarp0 + group * G::kGroupWarps) * 32;
+    constexpr int NT = G::kGroupWarps * 32;
     int it = 0;
     bool ok = true;
     Unit w;
     for (List list(p, sh, worker, workers); ok && list.next(w);) {
       for (int ks = w.kb; ks < w.ke; ++ks, ++it) {
+        if (it % G::kConvGroups != group) continue;
         const int rs = it % RS, os = it % OS;
         ok = wait_for(ptx::smem_addr(&sh->raw_full[rs]), (uint32_t)((it / RS) & 1), abort_w,
-                          p.status, kDevTimeoutFull, p.timeout_ns) &&
-             wait_for(ptx::smem_addr(&sh->op_empty[os]), (uint32_t)((it / OS) & 1) ^ 1u,
-                          abort_w, p.status, kDevTimeoutEmpty, p.timeout_ns);
+                      p.status, kDevTimeoutFull, p.timeout_ns) &&
+             wait_for(ptx::smem_addr(&sh->op_empty[os]), (uint32_t)((it / OS) & 1) ^ 1u, abort_w,
+                      p.status, kDevTimeoutEmpty, p.timeout_ns);
         ok = __all_sync(kAll, ok);
         if (!ok) break;
         const unsigned char* raw = raw_base + rs * G::kRaw;
@@ -798,7 +814,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
         }
       }
     }
-    if (kPair && t == 0) {
+    if (kPair && t == 0 && group == 0) {
       // the even CTA's commits arrive on this CTA's op_empty barriers: wait
       // (bounded) for its arrivals on the last use of every stage
       const uint64_t t0 = ptx::global_ns();
@@ -900,28 +916,34 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
         if (!*reinterpret_cast<volatile int*>(&sh->last)) continue;
         __threadfence();
         // (of two, the own one is still in registers: a sum of two terms does
-        // not depend on their order)
+        // not depend on their order). LP partials by LB columns are loaded at a
+        // time: one after another, each would cost the latency of L2.
+        constexpr int LB = HC < 32 ? HC : 32, LP = 32 / LB;
         const int own = w.parts == 2 ? worker - w.c0 : -1;
-        for (int i = 0; i < w.parts; ++i) {
-          if (i == own) continue;
-          const float* src = slot(w.c0 + i, i == 0 ? 1 : 0);
-          // a batch of independent loads at a time (one after another, each
-          // column would cost the latency of L2)
-          constexpr int LB = HC < 32 ? HC : 32;
+        for (int i0 = 0; i0 < w.parts; i0 += LP) {
 #pragma unroll
           for (int c0 = 0; c0 < HC; c0 += LB) {
             if (c0 >= nq) continue;
-            float x[LB];
+            float x[LP][LB];
 #pragma unroll
-            for (int c = 0; c < LB; ++c) x[c] = c0 + c < nq ? __ldcg(src + (c0 + c) * BP) : 0.f;
+            for (int i = 0; i < LP; ++i) {
+              const float* src = slot(w.c0 + i0 + i, i0 + i == 0 ? 1 : 0);
+              const bool take = i0 + i < w.parts && i0 + i != own;
 #pragma unroll
-            for (int c = 0; c < LB; ++c) {
-              if (i == 0 && own < 0)
-                sum[c0 + c] = x[c];
-              else if (G::kInt)
-                sum[c0 + c] = __int_as_float(__float_as_int(sum[c0 + c]) + __float_as_int(x[c]));
-              else
-                sum[c0 + c] += x[c];
+              for (int c = 0; c < LB; ++c)
+                x[i][c] = take && c0 + c < nq ? __ldcg(src + (c0 + c) * BP) : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < LP; ++i) {
+#pragma unroll
+              for (int c = 0; c < LB; ++c) {
+                if (i0 + i == 0 && own < 0)
+                  sum[c0 + c] = x[i][c];
+                else if (G::kInt)
+                  sum[c0 + c] = __int_as_float(__float_as_int(sum[c0 + c]) + __float_as_int(x[i][c]));
+                else
+                  sum[c0 + c] += x[i][c];
+              }
             }
           }
         }
