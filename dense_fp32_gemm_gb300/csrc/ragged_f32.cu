@@ -9,7 +9,6 @@ extern const FormEntry kFormsF32[] = {
     SGEMM_GB300_FORM(kF32, 32, 1),
     SGEMM_GB300_FORM(kF32, 64, 1),
     SGEMM_GB300_FORM(kF32, 128, 1),
-    SGEMM_GB300_FORM(kF32, 128, 2),
 };
 extern const int kNumFormsF32 = sizeof(kFormsF32) / sizeof(kFormsF32[0]);
 

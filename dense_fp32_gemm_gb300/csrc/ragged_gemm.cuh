@@ -158,7 +158,7 @@ constexpr int kMinSlices = 4;
 struct Shared {
   uint64_t raw_full[12], raw_empty[12];
   uint64_t op_full[4], op_empty[4];
-  uint64_t peer_full[12];       // even CTA of a pair: the odd CTA's stage has landed
+  uint64_t peer_full[12];       // even CTA of a pair: the odd CTA's stage has been cleared
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain, epi_sync;
   uint32_t tmem;
@@ -259,6 +259,14 @@ struct Walk {
   }
 };
 
+// The same value in every lane, told to the compiler (the reduction's result is
+// a uniform register): what the issue loops add up stays in the uniform
+// registers that the copy and tensor instructions read, instead of being moved
+// there for each of them (70 cycles an MMA).
+__device__ __forceinline__ int uniform(int v) {
+  return (int)__reduce_or_sync(0xffffffffu, (unsigned)v);
+}
+
 // Waits for a barrier's phase, at most timeout_ns: then the abort word is set,
 // the code recorded, and false returned. The clock is read only after some
 // dozens of polls: a read takes longer than a k-slice.
@@ -321,46 +329,70 @@ __device__ __forceinline__ uint2 i8_to_f16(uint32_t v) {
 // K-major: row r = element r of the side, its 32 values of k -> parts with
 // rows of 64 bytes (64-byte swizzle). MN-major: boxes of 32 elements x 32 rows
 // of k -> chunks of 64 elements x 32 rows (128-byte swizzle). Rows of k at or
-// past `klim` are written as zeros.
-template <int ROWS>
+// past `klim` are written as zeros. NT threads, each 8 values at a time; U such
+// pieces are loaded before the first is converted.
+template <int ROWS, int NT, int U>
 __device__ __forceinline__ void convert_f32(const unsigned char* raw, unsigned char* op, bool mn,
-                                            int klim, int t, int nt) {
-  constexpr int PART = ROWS * 64;
-  for (int i = t; i < ROWS * 4; i += nt) {
-    const int r = i >> 2, c = i & 3;   // MN-major: r = box * 32 + k
-    float4 a = *reinterpret_cast<const float4*>(raw + r * 128 + (((2 * c) ^ (r & 7)) << 4));
-    float4 b = *reinterpret_cast<const float4*>(raw + r * 128 + (((2 * c + 1) ^ (r & 7)) << 4));
-    int at;
-    if (mn) {
-      const int k = r & 31, box = r >> 5;
-      if (k >= klim) a = b = make_float4(0.f, 0.f, 0.f, 0.f);
-      at = (box >> 1) * 4096 + k * 128 + ((((box & 1) * 4 + c) ^ (k & 7)) << 4);
-    } else {
-      at = r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+                                            int klim, int t) {
+  constexpr int PART = ROWS * 64, N = ROWS * 4;
+#pragma unroll 1
+  for (int i0 = t; i0 < N; i0 += NT * U) {
+    float4 a[U], b[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int i = i0 + j * NT, r = i >> 2, c = i & 3;   // MN-major: r = box * 32 + k
+      if (N % (NT * U) && i >= N) continue;
+      a[j] = *reinterpret_cast<const float4*>(raw + r * 128 + (((2 * c) ^ (r & 7)) << 4));
+      b[j] = *reinterpret_cast<const float4*>(raw + r * 128 + (((2 * c + 1) ^ (r & 7)) << 4));
     }
-    uint4 h, m, l;
-    split2(a.x, a.y, h.x, m.x, l.x);
-    split2(a.z, a.w, h.y, m.y, l.y);
-    split2(b.x, b.y, h.z, m.z, l.z);
-    split2(b.z, b.w, h.w, m.w, l.w);
-    *reinterpret_cast<uint4*>(op + at) = h;
-    *reinterpret_cast<uint4*>(op + PART + at) = m;
-    *reinterpret_cast<uint4*>(op + 2 * PART + at) = l;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int i = i0 + j * NT, r = i >> 2, c = i & 3;
+      if (N % (NT * U) && i >= N) continue;
+      int at;
+      if (mn) {
+        const int k = r & 31, box = r >> 5;
+        if (k >= klim) a[j] = b[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        at = (box >> 1) * 4096 + k * 128 + ((((box & 1) * 4 + c) ^ (k & 7)) << 4);
+      } else {
+        at = r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+      }
+      uint4 h, m, l;
+      split2(a[j].x, a[j].y, h.x, m.x, l.x);
+      split2(a[j].z, a[j].w, h.y, m.y, l.y);
+      split2(b[j].x, b[j].y, h.z, m.z, l.z);
+      split2(b[j].z, b[j].w, h.w, m.w, l.w);
+      *reinterpret_cast<uint4*>(op + at) = h;
+      *reinterpret_cast<uint4*>(op + PART + at) = m;
+      *reinterpret_cast<uint4*>(op + 2 * PART + at) = l;
+    }
   }
 }
 
 // kI8: raw rows of 64 bytes (64-byte swizzle) -> rows of 64 F16 values
 // (128-byte swizzle).
-template <int ROWS>
-__device__ __forceinline__ void convert_i8(const unsigned char* raw, unsigned char* op, int t,
-                                           int nt) {
-  for (int i = t; i < ROWS * 4; i += nt) {
-    const int r = i >> 2, c = i & 3;
-    const uint4 v = *reinterpret_cast<const uint4*>(raw + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
-    const uint2 a = i8_to_f16(v.x), b = i8_to_f16(v.y), d = i8_to_f16(v.z), e = i8_to_f16(v.w);
-    unsigned char* row = op + r * 128;
-    *reinterpret_cast<uint4*>(row + (((2 * c) ^ (r & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
-    *reinterpret_cast<uint4*>(row + (((2 * c + 1) ^ (r & 7)) << 4)) = make_uint4(d.x, d.y, e.x, e.y);
+template <int ROWS, int NT, int U>
+__device__ __forceinline__ void convert_i8(const unsigned char* raw, unsigned char* op, int t) {
+  constexpr int N = ROWS * 4;
+#pragma unroll 1
+  for (int i0 = t; i0 < N; i0 += NT * U) {
+    uint4 v[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int i = i0 + j * NT, r = i >> 2, c = i & 3;
+      if (N % (NT * U) && i >= N) continue;
+      v[j] = *reinterpret_cast<const uint4*>(raw + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int i = i0 + j * NT, r = i >> 2, c = i & 3;
+      if (N % (NT * U) && i >= N) continue;
+      const uint2 a = i8_to_f16(v[j].x), b = i8_to_f16(v[j].y), d = i8_to_f16(v[j].z),
+                  e = i8_to_f16(v[j].w);
+      unsigned char* row = op + r * 128;
+      *reinterpret_cast<uint4*>(row + (((2 * c) ^ (r & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
+      *reinterpret_cast<uint4*>(row + (((2 * c + 1) ^ (r & 7)) << 4)) = make_uint4(d.x, d.y, e.x, e.y);
+    }
   }
 }
 
@@ -410,6 +442,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
   constexpr int SL = G::kSlice;
   constexpr int RS = G::kRawStages, OS = G::kConv ? G::kOpStages : RS;
   constexpr bool kPair = CL == 2;
+  static_assert(!kPair || !G::kConv, "pairs read their tiles as TMA wrote them");
   constexpr uint16_t kBoth = 0x3;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw_addr = ptx::smem_addr(smem_raw);
@@ -428,8 +461,8 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
 
   if (tid == 0) {
     // pair form: the even CTA's MMA warp waits on the stages of both CTAs
-    // (converted or cleared ones: its own, and one relayed arrival for the odd
-    // CTA's), and on the epilogue warps of both; its commits arrive in both
+    // (cleared ones: its own, and one relayed arrival for the odd CTA's), and
+    // on the epilogue warps of both; its commits arrive in both
     for (int s = 0; s < RS; ++s) {
       ptx::mbar_init(ptx::smem_addr(&sh->raw_full[s]), 1);
       ptx::mbar_init(ptx::smem_addr(&sh->raw_empty[s]), G::kConv ? G::kGroupWarps : 1);
@@ -439,7 +472,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
         ptx::mbar_init(ptx::smem_addr(&sh->op_full[s]), G::kGroupWarps);
         ptx::mbar_init(ptx::smem_addr(&sh->op_empty[s]), 1);
       }
-      ptx::mbar_init(ptx::smem_addr(&sh->peer_full[s]), 1);
+      if (kPair) ptx::mbar_init(ptx::smem_addr(&sh->peer_full[s]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(ptx::smem_addr(&sh->acc_full[i]), 1);
@@ -523,7 +556,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
   // arrival or commit reaches them
   if (kPair) ptx::cluster_sync();
   tc::fence_after_sync();
-  const uint32_t tmem = sh->tmem;
+  const uint32_t tmem = (uint32_t)uniform((int)sh->tmem);
   if (kPair) {
     if (tid == 0) {
       // the MMAs of the pair write the same tensor-memory address in both CTAs
@@ -549,10 +582,11 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
       const bool p_mn = p.p_mn, q_mn = p.q_mn, wgrad = p.wgrad;
       Unit w;
       for (List list(p, sh, worker, workers); ok && list.next(w);) {
-        const int p0 = w.p0 + rank * BP, q0 = w.q0 + rank * G::kRows;
-        const int pe = wgrad ? 0 : w.e, qrow = wgrad ? 0 : w.row0 + q0;
-        int k = w.kb * SL + (wgrad ? w.row0 : 0);
-        for (int ks = w.kb; ks < w.ke; ++ks, ++it, k += SL) {
+        const int p0 = uniform(w.p0 + rank * BP), q0 = uniform(w.q0 + rank * G::kRows);
+        const int pe = uniform(wgrad ? 0 : w.e), qrow = uniform(wgrad ? 0 : w.row0 + q0);
+        const int kb = uniform(w.kb), ke = uniform(w.ke), clear_at = uniform(w.clear);
+        int k = uniform(w.kb * SL + (wgrad ? w.row0 : 0));
+        for (int ks = kb; ks < ke; ++ks, ++it, k += SL) {
           ok = wait_for(ptx::smem_addr(&sh->raw_empty[s]), phase, abort_w, p.status,
                         kDevTimeoutEmpty, p.timeout_ns);
           ok = __all_sync(kAll, ok);
@@ -561,9 +595,9 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
           // CTA's loads may complete before it expects them), but for a stage
           // that the odd CTA has to clear. (A remote arrival for each of the
           // odd CTA's stages took its producer 1300 cycles.)
-          const bool clear = !G::kConv && ks == w.clear;
-          const bool remote = kPair && !G::kConv && rank != 0 && !clear;
-          if (kPair && !G::kConv && rank != 0 && clear) own_phase ^= 1u << s;
+          const bool clear = !G::kConv && ks == clear_at;
+          const bool remote = kPair && rank != 0 && !clear;
+          if (kPair && rank != 0 && clear) own_phase ^= 1u << s;
           if (ptx::elect_one()) {
             uint32_t fb = ptx::smem_addr(&sh->raw_full[s]);
             const uint32_t st = raw_base_addr + (uint32_t)(s * G::kRaw);
@@ -571,9 +605,9 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
               fb = ptx::mapa(fb, 0u);
             else
               ptx::mbar_arrive_expect_tx(
-                  fb, (uint32_t)(kPair && !G::kConv && !clear ? 2 * G::kRaw : G::kRaw));
+                  fb, (uint32_t)(kPair && !clear ? 2 * G::kRaw : G::kRaw));
             auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, int z) {
-              if (kPair && !G::kConv)
+              if (kPair)
                 ptx::tma_load_3d_pair(dst, map, x, y, z, fb);
               else
                 ptx::tma_load_3d(dst, map, x, y, z, fb);
@@ -607,12 +641,12 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
         // (odd CTA: its own barriers only carry the stages that are cleared;
         // the others have landed once the even CTA's MMAs have read them)
         const uint32_t fb = ptx::smem_addr(&sh->raw_full[j % RS]);
-        const uint32_t par = kPair && !G::kConv && rank != 0 ? (own_phase >> (j % RS) & 1u) ^ 1u
+        const uint32_t par = kPair && rank != 0 ? (own_phase >> (j % RS) & 1u) ^ 1u
                                                              : (uint32_t)((j / RS) & 1);
         while (!ptx::mbar_try_wait(fb, par))
           if ((long long)(ptx::global_ns() - t0) > cleanup_bound_ns(p.timeout_ns)) break;
       }
-      if (kPair && !G::kConv) {
+      if (kPair) {
         // the even CTA's commits arrive on this CTA's raw_empty barriers: wait
         // (bounded) for its arrivals on the last use of every stage
         for (int j = it; j < it + RS; ++j) {
@@ -679,7 +713,9 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     const int chunk = p.chunk;
     Unit w;
     for (List list(p, sh, worker, workers); ok && list.next(w);) {
-      for (int k0 = w.kb; k0 < w.ke && ok; k0 += chunk, ++acc) {
+      const int kb = uniform(w.kb), ke = uniform(w.ke), clear_at = uniform(w.clear);
+      const int klen = uniform(w.klen);
+      for (int k0 = kb; k0 < ke && ok; k0 += chunk, ++acc) {
         const int buf = acc & 1;
         const uint32_t d = tmem + (uint32_t)(buf * BQ);
         if (rank == 0) {
@@ -691,13 +727,13 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
           if (!ok) break;
           tc::fence_after_sync();
         }
-        const int k1 = min(w.ke, k0 + chunk);
+        const int k1 = min(ke, k0 + chunk);
         for (int ks = k0; ks < k1; ++ks) {
-          const bool clear = !G::kConv && ks == w.clear;
-          const int rem = w.klen - ks * SL;   // > 0
+          const bool clear = !G::kConv && ks == clear_at;
+          const int rem = klen - ks * SL;   // > 0
           const uint32_t bit = 1u << s;
-          if (!kPair || G::kConv || rank == 0 || clear) {
-            const uint32_t par = kPair && rank != 0 && !G::kConv ? (own_phase & bit) != 0 : phase;
+          if (!kPair || rank == 0 || clear) {
+            const uint32_t par = kPair && rank != 0 ? (own_phase & bit) != 0 : phase;
             ok = wait_for(ptx::smem_addr(G::kConv ? &sh->op_full[s] : &sh->raw_full[s]), par,
                           abort_w, p.status, kDevTimeoutFull, p.timeout_ns);
             ok = __all_sync(kAll, ok);
@@ -718,14 +754,13 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
             __syncwarp();
           }
           if (rank != 0) {
-            if ((G::kConv || clear) && lane == 0)
+            if (clear && lane == 0)
               ptx::mbar_arrive_remote(ptx::mapa(ptx::smem_addr(&sh->peer_full[s]), 0u));
           } else {
-            if (kPair && (G::kConv || clear)) {
-              // what threads of the odd CTA have written
-              const uint32_t par = G::kConv ? phase : (own_phase & bit) != 0;
-              ok = wait_for_pair(ptx::smem_addr(&sh->peer_full[s]), par, abort_w, p.status,
-                                 kDevTimeoutFull, p.timeout_ns);
+            if (kPair && clear) {
+              // the odd CTA has cleared its rows
+              ok = wait_for_pair(ptx::smem_addr(&sh->peer_full[s]), (own_phase & bit) != 0, abort_w,
+                                 p.status, kDevTimeoutFull, p.timeout_ns);
               ok = __all_sync(kAll, ok);
               if (!ok) break;
             }
@@ -798,11 +833,11 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
         unsigned char* op = base + os * G::kOp;
         if (SRC == kF32) {
           const int klim = p.wgrad ? w.klen - ks * SL : SL;
-          convert_f32<BP>(raw, op, p.p_mn, klim, t, NT);
-          convert_f32<G::kRows>(raw + G::kRawP, op + G::kParts * G::kOpP, p.q_mn, klim, t, NT);
+          convert_f32<BP, NT, 2>(raw, op, p.p_mn, klim, t);
+          convert_f32<BQ, NT, 2>(raw + G::kRawP, op + G::kParts * G::kOpP, p.q_mn, klim, t);
         } else {
-          convert_i8<BP>(raw, op, t, NT);
-          convert_i8<G::kRows>(raw + G::kRawP, op + G::kOpP, t, NT);
+          convert_i8<BP, NT, 4>(raw, op, t);
+          convert_i8<BQ, NT, BQ >= 64 ? 4 : 1>(raw + G::kRawP, op + G::kOpP, t);
         }
         // the MMAs read the operand tiles, and TMA refills the raw ones,
         // through the async proxy
@@ -812,16 +847,6 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
           ptx::mbar_arrive(ptx::smem_addr(&sh->op_full[os]));
           ptx::mbar_arrive(ptx::smem_addr(&sh->raw_empty[rs]));
         }
-      }
-    }
-    if (kPair && t == 0 && group == 0) {
-      // the even CTA's commits arrive on this CTA's op_empty barriers: wait
-      // (bounded) for its arrivals on the last use of every stage
-      const uint64_t t0 = ptx::global_ns();
-      for (int j = it; j < it + OS; ++j) {
-        const uint32_t eb = ptx::smem_addr(&sh->op_empty[j % OS]);
-        while (!ptx::mbar_try_wait(eb, (uint32_t)((j / OS) & 1) ^ 1u))
-          if ((long long)(ptx::global_ns() - t0) > cleanup_bound_ns(p.timeout_ns)) break;
       }
     }
   } else {

@@ -275,7 +275,7 @@ def test_other_stream_and_graph():
     assert torch.equal(y, want)
 
 
-FORMS = [(16, 1), (32, 1), (64, 1), (128, 1), (256, 1), (128, 2), (256, 2)]
+FORMS = [(16, 1), (32, 1), (64, 1), (128, 1), (256, 1), (256, 2)]
 
 
 @pytest.fixture
@@ -298,5 +298,5 @@ def test_every_tile(tile, t):
 
 
 def test_set_tile_refuses():
-    for width, ctas in [(8, 1), (16, 2), (512, 1), (-1, 1), (64, 3)]:
+    for width, ctas in [(8, 1), (16, 2), (128, 2), (512, 1), (-1, 1), (64, 3)]:
         assert B.sgemm_grouped_set_tile(width, ctas) == B.SGEMM_ERR_INVALID_VALUE
