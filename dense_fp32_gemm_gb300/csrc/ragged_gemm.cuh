@@ -115,22 +115,30 @@ struct Geo {
   static constexpr int kRawP = BP * kRawRow, kRawQ = kRows * kRawRow;
   static constexpr int kRaw = kRawP + kRawQ;
   static constexpr int kParts = SRC == kF32 ? 3 : 1;
-  static constexpr int kOpP = BP * kSlice * 2, kOpQ = kRows * kSlice * 2;  // one part
-  static constexpr int kOp = kConv ? kParts * (kOpP + kOpQ) : 0;
+  static constexpr int kOpQ = kRows * kSlice * 2;               // one converted part of Q
+  static constexpr int kOp = kConv ? kParts * kOpQ : 0;
   static constexpr int kRegion = 192 * 1024;
-  // Converter warps work in groups that take the slices in turn: a slice's
-  // conversion is a chain of latencies (wait, load, store, proxy fence), and
-  // the chains of several slices overlap. Four groups where four stages of
-  // each kind fit, else two. A raw stage always belongs to one group (their
-  // number is a multiple of the groups): a group that waited for a stage in
-  // which another group's slice has not landed yet would take the phase before
-  // that one for its own.
-  static constexpr int kConvGroups = !kConv ? 1 : (4 * (kOp + kRaw) <= kRegion ? 4 : 2);
-  static constexpr int kGroupWarps = kConvWarps / kConvGroups;
-  static constexpr int kOpStages = kConv ? kConvGroups : 0;
+  // Converted stages: Q's parts in shared memory, P's in tensor memory behind
+  // the two accumulators (a part is kSlice / 2 columns). The MMAs then read
+  // only Q from shared memory: with both operands there, the six products of a
+  // 128 x 128 FP32 tile moved 208 KB of it per slice, 1660 cycles against 770
+  // of the MMAs. Up to 8 stages, as long as three raw ones fit beside them.
+  static constexpr int kSlotCols = kParts * kSlice / 2;
+  static constexpr int kSlotFit = (512 - 2 * BQ) / kSlotCols;
+  static constexpr int kOpFit = kConv ? (kRegion - 3 * kRaw) / (kOp > 0 ? kOp : 1) : 0;
+  static constexpr int kOpMin = kSlotFit < kOpFit ? kSlotFit : kOpFit;
+  static constexpr int kOpStages = kConv ? (kOpMin < 8 ? kOpMin : 8) : 0;
   static constexpr int kRawFit = (kRegion - kOpStages * kOp) / kRaw;
-  static constexpr int kRawStages = (kRawFit < 12 ? kRawFit : 12) / kConvGroups * kConvGroups;
-  static_assert(kRawStages >= 2, "raw stages");
+  static constexpr int kRawStages = kRawFit < 12 ? kRawFit : 12;
+  static_assert(kRawStages >= 2 && (!kConv || kOpStages >= 2), "stages");
+  // Converter warps work in two groups (of four: each covers the 128 lanes of
+  // tensor memory) that take the slices in turn, so that their chains of
+  // latencies (wait, load, store, fence) overlap. Every raw barrier belongs to
+  // one group: one that waited on a barrier whose phase before is another
+  // group's, not yet complete, would take the phase before that for its own. So
+  // the barriers form a ring of an even number, whatever the stages do.
+  static constexpr int kConvGroups = 2, kGroupWarps = 4;
+  static constexpr int kRawBars = kConv && kRawStages % 2 ? 2 * kRawStages : kRawStages;
   static constexpr int kThreads = (kConv ? kConvWarp0 + kConvWarps : kConvWarp0) * 32;
   // A thread of the epilogue holds BQ / 2 sums. For the widest tiles of a kind
   // they need more registers than the launch gives every thread, so the other
@@ -144,8 +152,10 @@ struct Geo {
                         kThreads * kRegs &&
                     kThreads * kRegs <= 65536,
                 "register shares");
-  static constexpr int kTmemCols = 2 * BQ;
-  static_assert(kTmemCols >= 32 && kTmemCols <= 512, "tensor memory");
+  static constexpr int kTmemCols = kConv ? 512 : 2 * BQ;
+  static_assert(kTmemCols >= 32 && kTmemCols <= 512 &&
+                    (!kConv || 2 * BQ + kOpStages * kSlotCols <= 512),
+                "tensor memory");
   // (a K-major tile of 8-row groups, an MN-major one of 64-wide chunks)
   static_assert(kRows % 8 == 0 && BQ % 16 == 0 && BQ <= 256, "tile width");
 };
@@ -156,8 +166,8 @@ constexpr int kExactChunk = 1024 / 64;
 constexpr int kMinSlices = 4;
 
 struct Shared {
-  uint64_t raw_full[12], raw_empty[12];
-  uint64_t op_full[4], op_empty[4];
+  uint64_t raw_full[24], raw_empty[24];
+  uint64_t op_full[8], op_empty[8];
   uint64_t peer_full[12];       // even CTA of a pair: the odd CTA's stage has been cleared
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain, epi_sync;
@@ -325,7 +335,7 @@ __device__ __forceinline__ uint2 i8_to_f16(uint32_t v) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
 
-// One operand side of a stage, kF32: raw rows of 128 bytes (128-byte swizzle).
+// The Q side of a stage, kF32: raw rows of 128 bytes (128-byte swizzle).
 // K-major: row r = element r of the side, its 32 values of k -> parts with
 // rows of 64 bytes (64-byte swizzle). MN-major: boxes of 32 elements x 32 rows
 // of k -> chunks of 64 elements x 32 rows (128-byte swizzle). Rows of k at or
@@ -369,8 +379,59 @@ __device__ __forceinline__ void convert_f32(const unsigned char* raw, unsigned c
   }
 }
 
-// kI8: raw rows of 64 bytes (64-byte swizzle) -> rows of 64 F16 values
-// (128-byte swizzle).
+// The P side of a stage into tensor memory, a thread per element of the side
+// (lane `r` of the tile, `taddr` its warp's lanes at the slot): 16 values of k
+// at a time, part j at columns 16 * j .. (8 columns per 16 values).
+__device__ __forceinline__ void convert_p_f32(const unsigned char* raw, uint32_t taddr, bool mn,
+                                              int klim, int r) {
+#pragma unroll
+  for (int hk = 0; hk < 2; ++hk) {
+    float v[16];
+    if (mn) {
+      // boxes of 32 elements x 32 rows of k: a warp reads 128 bytes a row
+      const unsigned char* box = raw + (r >> 5) * 4096 + (r & 3) * 4;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int k = hk * 16 + j;
+        const float x =
+            *reinterpret_cast<const float*>(box + k * 128 + ((((r & 31) >> 2) ^ (k & 7)) << 4));
+        v[j] = k < klim ? x : 0.f;
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<float4*>(&v[4 * c]) =
+            *reinterpret_cast<const float4*>(raw + r * 128 + (((hk * 4 + c) ^ (r & 7)) << 4));
+    }
+    uint32_t h[8], m[8], l[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) split2(v[2 * j], v[2 * j + 1], h[j], m[j], l[j]);
+    tc::tmem_st8(taddr + hk * 8, h);
+    tc::tmem_st8(taddr + 16 + hk * 8, m);
+    tc::tmem_st8(taddr + 32 + hk * 8, l);
+  }
+}
+// kI8: 64 values, 32 columns.
+__device__ __forceinline__ void convert_p_i8(const unsigned char* raw, uint32_t taddr, int r) {
+  uint32_t o[32];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint4 v = *reinterpret_cast<const uint4*>(raw + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+    const uint2 a = i8_to_f16(v.x), b = i8_to_f16(v.y), d = i8_to_f16(v.z), e = i8_to_f16(v.w);
+    o[8 * c] = a.x;
+    o[8 * c + 1] = a.y;
+    o[8 * c + 2] = b.x;
+    o[8 * c + 3] = b.y;
+    o[8 * c + 4] = d.x;
+    o[8 * c + 5] = d.y;
+    o[8 * c + 6] = e.x;
+    o[8 * c + 7] = e.y;
+  }
+  tc::tmem_st32(taddr, o);
+}
+
+// The Q side, kI8: raw rows of 64 bytes (64-byte swizzle) -> rows of 64 F16
+// values (128-byte swizzle).
 template <int ROWS, int NT, int U>
 __device__ __forceinline__ void convert_i8(const unsigned char* raw, unsigned char* op, int t) {
   constexpr int N = ROWS * 4;
@@ -440,7 +501,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
   using G = Geo<SRC, BQ, CL>;
   using List = Walk<G::kSlice, BQ, CL>;
   constexpr int SL = G::kSlice;
-  constexpr int RS = G::kRawStages, OS = G::kConv ? G::kOpStages : RS;
+  constexpr int RS = G::kRawStages, RB = G::kRawBars, OS = G::kConv ? G::kOpStages : RS;
   constexpr bool kPair = CL == 2;
   static_assert(!kPair || !G::kConv, "pairs read their tiles as TMA wrote them");
   constexpr uint16_t kBoth = 0x3;
@@ -463,7 +524,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     // pair form: the even CTA's MMA warp waits on the stages of both CTAs
     // (cleared ones: its own, and one relayed arrival for the odd CTA's), and
     // on the epilogue warps of both; its commits arrive in both
-    for (int s = 0; s < RS; ++s) {
+    for (int s = 0; s < RB; ++s) {
       ptx::mbar_init(ptx::smem_addr(&sh->raw_full[s]), 1);
       ptx::mbar_init(ptx::smem_addr(&sh->raw_empty[s]), G::kConv ? G::kGroupWarps : 1);
     }
@@ -574,8 +635,11 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     if (G::kMoveRegs) ptx::regs_lower<G::kRegsFew>();
     // ---- warp 0: TMA producer ---------------------------------------------------
     if (warp == 0) {
-      int it = 0, s = 0;
-      uint32_t phase = 1;       // parity of raw_empty to wait for
+      int it = 0, s = 0, bf = 0;            // stage and barrier to fill
+      // the stage's last use: its barrier, and the parity to wait for (first
+      // uses of a stage pass at once, on barriers that nothing has used)
+      int be = RB == RS ? 0 : RS;
+      uint32_t phase = 1;
       uint32_t own_phase = 0;   // odd CTA: phases of its own raw_full barriers (a bit each)
       bool ok = true;
       constexpr int BOX = G::kRawRow / G::kElem;  // elements along the fast dimension of a box
@@ -587,7 +651,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
         const int kb = uniform(w.kb), ke = uniform(w.ke), clear_at = uniform(w.clear);
         int k = uniform(w.kb * SL + (wgrad ? w.row0 : 0));
         for (int ks = kb; ks < ke; ++ks, ++it, k += SL) {
-          ok = wait_for(ptx::smem_addr(&sh->raw_empty[s]), phase, abort_w, p.status,
+          ok = wait_for(ptx::smem_addr(&sh->raw_empty[be]), phase, abort_w, p.status,
                         kDevTimeoutEmpty, p.timeout_ns);
           ok = __all_sync(kAll, ok);
           if (!ok) break;
@@ -599,7 +663,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
           const bool remote = kPair && rank != 0 && !clear;
           if (kPair && rank != 0 && clear) own_phase ^= 1u << s;
           if (ptx::elect_one()) {
-            uint32_t fb = ptx::smem_addr(&sh->raw_full[s]);
+            uint32_t fb = ptx::smem_addr(&sh->raw_full[bf]);
             const uint32_t st = raw_base_addr + (uint32_t)(s * G::kRaw);
             if (remote)
               fb = ptx::mapa(fb, 0u);
@@ -628,8 +692,10 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
             }
           }
           __syncwarp();
-          if (++s == RS) {
-            s = 0;
+          if (++s == RS) s = 0;
+          if (++bf == RB) bf = 0;
+          if (++be == RB) {
+            be = 0;
             phase ^= 1u;
           }
         }
@@ -640,9 +706,9 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
       for (int j = it - 1; j >= 0 && j >= it - RS; --j) {
         // (odd CTA: its own barriers only carry the stages that are cleared;
         // the others have landed once the even CTA's MMAs have read them)
-        const uint32_t fb = ptx::smem_addr(&sh->raw_full[j % RS]);
+        const uint32_t fb = ptx::smem_addr(&sh->raw_full[j % RB]);
         const uint32_t par = kPair && rank != 0 ? (own_phase >> (j % RS) & 1u) ^ 1u
-                                                             : (uint32_t)((j / RS) & 1);
+                                                : (uint32_t)((j / RB) & 1);
         while (!ptx::mbar_try_wait(fb, par))
           if ((long long)(ptx::global_ns() - t0) > cleanup_bound_ns(p.timeout_ns)) break;
       }
@@ -665,10 +731,9 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     // their address field. (Made anew for every MMA they cost more than a
     // slice's MMAs: the loop below took 540 cycles for a slice of any size.)
     constexpr bool kNarrow = SRC == kF32;
-    constexpr int OP_P = G::kConv ? G::kOpP : G::kRawP;   // one part
-    constexpr int OP_Q = G::kConv ? G::kOpQ : G::kRawQ;
+    constexpr int OP_Q = G::kConv ? G::kOpQ : G::kRawQ;   // one part
     constexpr uint32_t kStage16 = (G::kConv ? G::kOp : G::kRaw) >> 4;
-    const bool a_mn = p.p_mn, b_mn = p.q_mn;
+    const bool a_mn = !G::kConv && p.p_mn, b_mn = p.q_mn;   // (tensor memory: K-major)
     const uint32_t idesc =
         tc::idesc_f16(BP * CL, BQ, SRC == kF32 || (SRC == k16 && p.bf16), a_mn, b_mn);
     auto desc = [](uint32_t addr, bool mn) {
@@ -676,26 +741,32 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
                 : tc::smem_desc(addr, 16, kNarrow ? 512 : 1024, !kNarrow);
     };
     const uint64_t a_desc = desc(base_addr, a_mn);
-    const uint64_t b_desc = desc(base_addr + (uint32_t)(G::kParts * OP_P), b_mn);
+    const uint64_t b_desc = desc(base_addr + (uint32_t)(G::kConv ? 0 : G::kRawP), b_mn);
     const uint32_t a_step = a_mn ? 2048u >> 4 : 32u >> 4, b_step = b_mn ? 2048u >> 4 : 32u >> 4;
-    auto mma = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t add) {
-      if (kPair)
-        tc::mma_f16_pair(d, a, b, idesc, add);
-      else
-        tc::mma_f16(d, a, b, idesc, add);
-    };
-    // the MMAs of one 16-wide k-step
-    auto step = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t add) {
-      if (SRC == kF32) {
-        constexpr uint64_t P1 = OP_P >> 4, Q1 = OP_Q >> 4;
-        mma(d, a + 2 * P1, b, add);
-        mma(d, a, b + 2 * Q1, 1u);
-        mma(d, a + P1, b + Q1, 1u);
-        mma(d, a + P1, b, 1u);
-        mma(d, a, b + Q1, 1u);
-        mma(d, a, b, 1u);
+    const uint32_t a_slots = tmem + 2 * BQ;      // P's converted parts
+    // the MMAs of k-step kk of stage s
+    auto step = [&](uint32_t d, int s, int kk, uint32_t add) {
+      const uint64_t b = b_desc + (uint64_t)(s * kStage16) + kk * b_step;
+      if (G::kConv) {
+        const uint32_t a = a_slots + (uint32_t)(s * G::kSlotCols + kk * 8);
+        if (SRC == kF32) {
+          constexpr uint32_t P1 = SL / 2;
+          constexpr uint64_t Q1 = OP_Q >> 4;
+          tc::mma_f16_ts(d, a + 2 * P1, b, idesc, add);
+          tc::mma_f16_ts(d, a, b + 2 * Q1, idesc, 1u);
+          tc::mma_f16_ts(d, a + P1, b + Q1, idesc, 1u);
+          tc::mma_f16_ts(d, a + P1, b, idesc, 1u);
+          tc::mma_f16_ts(d, a, b + Q1, idesc, 1u);
+          tc::mma_f16_ts(d, a, b, idesc, 1u);
+        } else {
+          tc::mma_f16_ts(d, a, b, idesc, add);
+        }
       } else {
-        mma(d, a, b, add);
+        const uint64_t a = a_desc + (uint64_t)(s * kStage16) + kk * a_step;
+        if (kPair)
+          tc::mma_f16_pair(d, a, b, idesc, add);
+        else
+          tc::mma_f16(d, a, b, idesc, add);
       }
     };
     auto commit = [&](uint64_t* bar) {
@@ -766,17 +837,13 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
             }
             tc::fence_after_sync();
             if (ptx::elect_one()) {
-              const uint64_t a = a_desc + (uint64_t)(s * kStage16);
-              const uint64_t b = b_desc + (uint64_t)(s * kStage16);
               const uint32_t add = ks == k0 ? 0u : 1u;
               if (rem >= SL) {
 #pragma unroll
-                for (int kk = 0; kk < SL / 16; ++kk)
-                  step(d, a + kk * a_step, b + kk * b_step, kk == 0 ? add : 1u);
+                for (int kk = 0; kk < SL / 16; ++kk) step(d, s, kk, kk == 0 ? add : 1u);
               } else {
 #pragma unroll 1
-                for (int kk = 0; kk * 16 < rem; ++kk)
-                  step(d, a + kk * a_step, b + kk * b_step, kk == 0 ? add : 1u);
+                for (int kk = 0; kk * 16 < rem; ++kk) step(d, s, kk, kk == 0 ? add : 1u);
               }
               commit(G::kConv ? &sh->op_empty[s] : &sh->raw_empty[s]);
             }
@@ -814,6 +881,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     // ---- converters: raw tiles -> operand tiles ----------------------------------
     if (G::kMoveRegs) ptx::regs_lower<G::kRegsConv>();
     const int group = (warp - kConvWarp0) / G::kGroupWarps;
+    const int pr = (warp & 3) * 32 + lane;             // this thread's lane of the tile
     const int t = tid - (kConvWarp0 + group * G::kGroupWarps) * 32;
     constexpr int NT = G::kGroupWarps * 32;
     int it = 0;
@@ -822,8 +890,8 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     for (List list(p, sh, worker, workers); ok && list.next(w);) {
       for (int ks = w.kb; ks < w.ke; ++ks, ++it) {
         if (it % G::kConvGroups != group) continue;
-        const int rs = it % RS, os = it % OS;
-        ok = wait_for(ptx::smem_addr(&sh->raw_full[rs]), (uint32_t)((it / RS) & 1), abort_w,
+        const int rs = it % RS, rb = it % RB, os = it % OS;
+        ok = wait_for(ptx::smem_addr(&sh->raw_full[rb]), (uint32_t)((it / RB) & 1), abort_w,
                       p.status, kDevTimeoutFull, p.timeout_ns) &&
              wait_for(ptx::smem_addr(&sh->op_empty[os]), (uint32_t)((it / OS) & 1) ^ 1u, abort_w,
                       p.status, kDevTimeoutEmpty, p.timeout_ns);
@@ -831,21 +899,27 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
         if (!ok) break;
         const unsigned char* raw = raw_base + rs * G::kRaw;
         unsigned char* op = base + os * G::kOp;
+        // the MMAs that read this slot last have completed (they freed it)
+        tc::fence_after_sync();
+        const uint32_t slot = tmem + ((uint32_t)((warp & 3) * 32) << 16) +
+                              (uint32_t)(2 * BQ + os * G::kSlotCols);
         if (SRC == kF32) {
           const int klim = p.wgrad ? w.klen - ks * SL : SL;
-          convert_f32<BP, NT, 2>(raw, op, p.p_mn, klim, t);
-          convert_f32<BQ, NT, 2>(raw + G::kRawP, op + G::kParts * G::kOpP, p.q_mn, klim, t);
+          convert_p_f32(raw, slot, p.p_mn, klim, pr);
+          convert_f32<BQ, NT, 2>(raw + G::kRawP, op, p.q_mn, klim, t);
         } else {
-          convert_i8<BP, NT, 4>(raw, op, t);
-          convert_i8<BQ, NT, BQ >= 64 ? 4 : 1>(raw + G::kRawP, op + G::kOpP, t);
+          convert_p_i8(raw, slot, pr);
+          convert_i8<BQ, NT, BQ >= 64 ? 4 : 1>(raw + G::kRawP, op, t);
         }
         // the MMAs read the operand tiles, and TMA refills the raw ones,
         // through the async proxy
         ptx::fence_proxy_async_shared();
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) {
           ptx::mbar_arrive(ptx::smem_addr(&sh->op_full[os]));
-          ptx::mbar_arrive(ptx::smem_addr(&sh->raw_empty[rs]));
+          ptx::mbar_arrive(ptx::smem_addr(&sh->raw_empty[rb]));
         }
       }
     }
