@@ -193,29 +193,57 @@ const FormEntry* find_form(int dev, int sms, int src, int bq, int cl, int* worke
   return nullptr;
 }
 
-// The tile of a call. rows: `per` is the mean number of rows of a group, wgrad:
-// the rows of its output (Q).
-struct Tile {
-  int src, bq, cl;
+// What a tile of each width costs on a worker, in ns: a slice of 64 values of k
+// (measured on GB300, 8192 x 4096 x 4096 over 8 groups for 16-bit operands, one
+// wave of tiles for the others) and its epilogue.
+struct TileCost {
+  int src, bq, cl, slice, epilogue;
 };
-Tile choose_tile(int src, const Params& p, long long per, int sms) {
-  const int least = p.wgrad ? 64 : 16;
-  const int widest = src == k16 || src == kI8Wide ? 256 : 128;
-  int bq = least;
-  while (bq < widest && bq < per) bq *= 2;
-  Tile t{src, bq, 1};
-  if (src == kI8Wide) return Tile{src, 256, 2};
-  // pairs: the widest tiles, at least one for every pair of SMs
-  if (bq == widest) {
-    const long long q = p.wgrad ? (long long)p.E * cdiv(p.Q, bq) : (long long)p.T / bq;
-    if (cdiv(p.P, 2 * BP) * q >= sms / 2) t.cl = 2;
+constexpr TileCost kTileCosts[] = {
+    {k16, 16, 1, 200, 600},    {k16, 32, 1, 205, 700},   {k16, 64, 1, 335, 1100},
+    {k16, 128, 1, 342, 1300},  {k16, 256, 1, 415, 2000}, {k16, 256, 2, 390, 2500},
+    {kF32, 16, 1, 490, 600},   {kF32, 32, 1, 500, 700},  {kF32, 64, 1, 1200, 1100},
+    {kF32, 128, 1, 1500, 1300},
+    {kI8, 16, 1, 270, 600},    {kI8, 32, 1, 275, 700},   {kI8, 64, 1, 425, 1100},
+    {kI8, 128, 1, 460, 1300},
+    {kI8Wide, 256, 2, 390, 2500},
+};
+// Time of publishing and adding the parts of a tile that is cut along k, ns.
+int cut_cost(int bq) { return 1600 + 25 * bq; }
+
+// The tile of a call: the one whose list takes least time on the workers it
+// has, by the costs above. The host does not know the groups' sizes: they are
+// taken to be equal but for half a tile of raggedness each.
+Form choose_tile(int src, const Params& p, int sms) {
+  Form best{src, 0, 1};
+  double least = 0;
+  for (const TileCost& c : kTileCosts) {
+    if (c.src != src || (p.wgrad && c.bq < 64)) continue;
+    const int workers = sms / c.cl;
+    const double groups = p.E < p.T ? p.E : (p.T > 0 ? p.T : 1);
+    const double q = p.wgrad ? (double)p.E * cdiv(p.Q, c.bq)
+                             : (p.E == 1 ? (double)cdiv(p.T, c.bq)
+                                         : (double)p.T / c.bq + groups / 2 > groups
+                                               ? (double)p.T / c.bq + groups / 2
+                                               : groups);
+    const double tiles = q * cdiv(p.P, BP * c.cl);
+    const double k = p.wgrad ? (double)p.T / p.E : p.K;
+    const double sum = (k / 64 < 1 ? 1 : k / 64) * c.slice;
+    const double tile = sum > c.epilogue ? sum : c.epilogue;
+    const double whole = (double)(long long)((tiles + workers - 1) / workers) * tile;
+    const double cut = tiles / workers * tile + cut_cost(c.bq);
+    const double time = (cut < whole ? cut : whole) + c.epilogue;
+    if (best.bq == 0 || time < least) {
+      least = time;
+      best = Form{src, c.bq, c.cl};
+    }
   }
-  return t;
+  return best;
 }
 
 // The operands as stored. Fills the maps (copying what TMA cannot read), the
 // workspace fields of `p`, and launches.
-int run(int src, int type, Params p, Operand op_p, Operand op_q, long long per, cudaStream_t stream,
+int run(int src, int type, Params p, Operand op_p, Operand op_q, cudaStream_t stream,
         const char* what) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -226,7 +254,7 @@ int run(int src, int type, Params p, Operand op_p, Operand op_q, long long per, 
   if (st != SGEMM_OK) return st;
   if (tensor_map_encode() == nullptr) return SGEMM_ERR_LAUNCH;
 
-  Tile t = choose_tile(src, p, per, sms);
+  const Form t = choose_tile(src, p, sms);
   int workers = 0;
   const FormEntry* form = nullptr;
   const int width = g_width.load(), ctas = g_ctas.load();
@@ -237,7 +265,7 @@ int run(int src, int type, Params p, Operand op_p, Operand op_q, long long per, 
   const int bq = form->form.bq, cl = form->form.cl;
 
   // tiles and k-slices are numbered with 32-bit integers
-  const int slice = src == kF32 ? 32 : 64;
+  const int sub_k = src == kF32 ? 32 : 64, slice = bq <= 32 ? 2 * sub_k : sub_k;
   const long long tiles = (long long)cdiv(p.P, BP * cl) *
                           (p.wgrad ? (long long)p.E * cdiv(p.Q, bq)
                                    : (long long)p.T / bq + (p.T < p.E ? p.T : p.E));
@@ -263,7 +291,9 @@ int run(int src, int type, Params p, Operand op_p, Operand op_q, long long per, 
     return SGEMM_ERR_LAUNCH;
   }
   p.partials = reinterpret_cast<float*>(at + pack_p + pack_q);
-  p.cut_slices = 4 + bq / 16;
+  for (const TileCost& c : kTileCosts)
+    if (c.src == src && c.bq == bq && c.cl == cl)
+      p.cut_slices = cut_cost(bq) * 64 / (c.slice * slice) + 1;
   p.timeout_ns = library_wait_timeout_ns();
 
   CUtensorMap mp = {}, mq = {};
@@ -275,8 +305,8 @@ int run(int src, int type, Params p, Operand op_p, Operand op_q, long long per, 
                           : (type == SGEMM_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16));
     const int row_bytes = src == kI8 ? 64 : 128;
-    if (!encode_operand(&mp, op_p, dt, row_bytes, p.p_mn ? slice : BP) ||
-        !encode_operand(&mq, op_q, dt, row_bytes, p.q_mn ? slice : bq / cl))
+    if (!encode_operand(&mp, op_p, dt, row_bytes, p.p_mn ? sub_k : BP) ||
+        !encode_operand(&mq, op_q, dt, row_bytes, p.q_mn ? sub_k : bq / cl))
       return SGEMM_ERR_LAUNCH;
   }
   if (form->launch(workers, p, mp, mq, stream) != cudaSuccess) {
@@ -291,13 +321,13 @@ int run(int src, int type, Params p, Operand op_p, Operand op_q, long long per, 
   return SGEMM_OK;
 }
 
-// k-slices per tensor-memory accumulation. 32-bit results leave it every 256
-// values of k (64 for kF32: 24 instructions), 16-bit results once: the error of
-// a truncating sum of 4096 values is far below their rounding.
+// Values of k per tensor-memory accumulation. 32-bit results leave it every 256
+// values (64 for kF32: 24 instructions), 16-bit results once: the error of a
+// truncating sum of 4096 values is far below their rounding.
 int accumulation_chunk(int src, int out_type) {
-  if (src == kF32) return 2;
-  if (src == kI8 || src == kI8Wide) return kExactChunk;
-  return out_type == kOutF32 ? 4 : 0x40000000;
+  if (src == kF32) return 64;
+  if (src == kI8 || src == kI8Wide) return kExactK;
+  return out_type == kOutF32 ? 256 : 0x40000000;
 }
 
 }  // namespace
@@ -345,8 +375,7 @@ SGEMM_API int sgemm_grouped(int op, int type, int out_type, int E, int T, int N,
   p.chunk = ragged::accumulation_chunk(src, out_type);
   const Operand w{W, eb, op == SGEMM_OP_N ? K : N, op == SGEMM_OP_N ? N : K, ldw, strideW, E};
   const Operand x{X, eb, T, K, ldx, 0, 1};
-  return ragged::run(src, type, p, w, x, ((long long)T + E - 1) / E,
-                     static_cast<cudaStream_t>(stream), "grouped");
+  return ragged::run(src, type, p, w, x, static_cast<cudaStream_t>(stream), "grouped");
 }
 
 SGEMM_API int sgemm_grouped_wgrad(int type, int out_type, int E, int T, int M, int N, float alpha,
@@ -387,7 +416,7 @@ SGEMM_API int sgemm_grouped_wgrad(int type, int out_type, int E, int T, int M, i
   p.beta = beta;
   p.chunk = ragged::accumulation_chunk(src, out_type);
   const Operand pb{B, eb, T, N, ldb, 0, 1}, qa{A, eb, T, M, lda, 0, 1};
-  return ragged::run(src, type, p, pb, qa, M, static_cast<cudaStream_t>(stream), "wgrad");
+  return ragged::run(src, type, p, pb, qa, static_cast<cudaStream_t>(stream), "wgrad");
 }
 
 SGEMM_API int sgemm_i8(int M, int N, int K, const signed char* A, int lda, const float* scaleA,
@@ -423,7 +452,7 @@ SGEMM_API int sgemm_i8(int M, int N, int K, const signed char* A, int lda, const
   // (4 bytes written and read per weight, against converting a weight tile
   // once for every 128 rows).
   const int src = M >= 512 ? ragged::kI8Wide : ragged::kI8;
-  return ragged::run(src, SGEMM_TYPE_F16, p, w, x, M, static_cast<cudaStream_t>(stream), "i8");
+  return ragged::run(src, SGEMM_TYPE_F16, p, w, x, static_cast<cudaStream_t>(stream), "i8");
 }
 
 SGEMM_API int sgemm_grouped_set_tile(int width, int ctas) {

@@ -94,7 +94,7 @@ struct Params {
   float alpha, beta;
   const float* scale_p;   // kI8: scales of p and q
   const float* scale_q;
-  int chunk;              // k-slices per tensor-memory accumulation
+  int chunk;              // values of k per tensor-memory accumulation (a multiple of the slice)
   int cut_slices;         // tiles are cut along k only to save at least so many k-slices
   float* partials;        // two tiles of BQ x 128 floats per CTA
   uint32_t* counters;     // arrivals at a cut tile, one per CTA, zero between launches
@@ -108,22 +108,28 @@ template <int SRC, int BQ, int CL>
 struct Geo {
   static constexpr bool kConv = SRC == kF32 || SRC == kI8;
   static constexpr bool kInt = SRC == kI8 || SRC == kI8Wide;
-  static constexpr int kSlice = SRC == kF32 ? 32 : 64;
+  // A slice is kSub tiles of kSubK values of k, each [P | Q] in rows of kRawRow
+  // bytes. Narrow tiles take two: their MMAs are short, and the hand-offs of a
+  // stage (some 700 cycles of waits and issue in the producer and in the MMA
+  // warp) would bound the bytes they stream.
+  static constexpr int kSubK = SRC == kF32 ? 32 : 64;
+  static constexpr int kSub = BQ <= 32 ? 2 : 1;
+  static constexpr int kSlice = kSub * kSubK;
   static constexpr int kElem = SRC == kF32 ? 4 : (SRC == kI8 ? 1 : 2);
   static constexpr int kRows = BQ / CL;                         // rows of Q in one CTA
-  static constexpr int kRawRow = kSlice * kElem;                // 128, 128, 64 bytes
+  static constexpr int kRawRow = kSubK * kElem;                 // 128, 128, 64 bytes
   static constexpr int kRawP = BP * kRawRow, kRawQ = kRows * kRawRow;
-  static constexpr int kRaw = kRawP + kRawQ;
+  static constexpr int kRawSub = kRawP + kRawQ, kRaw = kSub * kRawSub;
   static constexpr int kParts = SRC == kF32 ? 3 : 1;
-  static constexpr int kOpQ = kRows * kSlice * 2;               // one converted part of Q
-  static constexpr int kOp = kConv ? kParts * kOpQ : 0;
+  static constexpr int kOpQ = kRows * kSubK * 2;                // one converted part of Q's tile
+  static constexpr int kOpSub = kParts * kOpQ, kOp = kConv ? kSub * kOpSub : 0;
   static constexpr int kRegion = 192 * 1024;
   // Converted stages: Q's parts in shared memory, P's in tensor memory behind
-  // the two accumulators (a part is kSlice / 2 columns). The MMAs then read
+  // the two accumulators (a part is kSubK / 2 columns). The MMAs then read
   // only Q from shared memory: with both operands there, the six products of a
   // 128 x 128 FP32 tile moved 208 KB of it per slice, 1660 cycles against 770
   // of the MMAs. Up to 8 stages, as long as three raw ones fit beside them.
-  static constexpr int kSlotCols = kParts * kSlice / 2;
+  static constexpr int kSubCols = kParts * kSubK / 2, kSlotCols = kSub * kSubCols;
   static constexpr int kSlotFit = (512 - 2 * BQ) / kSlotCols;
   static constexpr int kOpFit = kConv ? (kRegion - 3 * kRaw) / (kOp > 0 ? kOp : 1) : 0;
   static constexpr int kOpMin = kSlotFit < kOpFit ? kSlotFit : kOpFit;
@@ -160,10 +166,10 @@ struct Geo {
   static_assert(kRows % 8 == 0 && BQ % 16 == 0 && BQ <= 256, "tile width");
 };
 // FP32 sums of integers leave tensor memory at the latest after this many
-// 64-wide slices (1024 products of at most 2^14).
-constexpr int kExactChunk = 1024 / 64;
+// values of k (products of at most 2^14 each).
+constexpr int kExactK = 1024;
 // Fewest k-slices a worker gets when the tiles of a small problem are cut.
-constexpr int kMinSlices = 4;
+constexpr int kMinSlices = 3;
 
 struct Shared {
   uint64_t raw_full[24], raw_empty[24];
@@ -503,6 +509,9 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
   constexpr int SL = G::kSlice;
   constexpr int RS = G::kRawStages, RB = G::kRawBars, OS = G::kConv ? G::kOpStages : RS;
   constexpr bool kPair = CL == 2;
+  // weight gradients (Q stored with k as its slow dimension) take tiles of 64
+  // and wider
+  constexpr bool kQmn = BQ >= 64;
   static_assert(!kPair || !G::kConv, "pairs read their tiles as TMA wrote them");
   constexpr uint16_t kBoth = 0x3;
   extern __shared__ unsigned char smem_raw[];
@@ -659,7 +668,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
           // CTA's loads may complete before it expects them), but for a stage
           // that the odd CTA has to clear. (A remote arrival for each of the
           // odd CTA's stages took its producer 1300 cycles.)
-          const bool clear = !G::kConv && ks == clear_at;
+          const bool clear = kQmn && !G::kConv && ks == clear_at;
           const bool remote = kPair && rank != 0 && !clear;
           if (kPair && rank != 0 && clear) own_phase ^= 1u << s;
           if (ptx::elect_one()) {
@@ -676,19 +685,25 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
               else
                 ptx::tma_load_3d(dst, map, x, y, z, fb);
             };
-            if (p_mn) {
 #pragma unroll
-              for (int i = 0; i < BP / BOX; ++i)
-                load(st + (uint32_t)(i * SL * G::kRawRow), &mapP, p0 + i * BOX, k, pe);
-            } else {
-              load(st, &mapP, k, p0, pe);
-            }
-            if (q_mn) {
+            for (int sub = 0; sub < G::kSub; ++sub) {
+              const int ksub = k + sub * G::kSubK;
+              const uint32_t at = st + (uint32_t)(sub * G::kRawSub);
+              if (p_mn) {
 #pragma unroll
-              for (int i = 0; i < G::kRows / BOX; ++i)
-                load(st + (uint32_t)(G::kRawP + i * SL * G::kRawRow), &mapQ, q0 + i * BOX, k, 0);
-            } else {
-              load(st + G::kRawP, &mapQ, k, qrow, 0);
+                for (int i = 0; i < BP / BOX; ++i)
+                  load(at + (uint32_t)(i * G::kSubK * G::kRawRow), &mapP, p0 + i * BOX, ksub, pe);
+              } else {
+                load(at, &mapP, ksub, p0, pe);
+              }
+              if (kQmn && q_mn) {
+#pragma unroll
+                for (int i = 0; i < G::kRows / BOX; ++i)
+                  load(at + (uint32_t)(G::kRawP + i * G::kSubK * G::kRawRow), &mapQ, q0 + i * BOX,
+                       ksub, 0);
+              } else {
+                load(at + G::kRawP, &mapQ, ksub, qrow, 0);
+              }
             }
           }
           __syncwarp();
@@ -733,11 +748,11 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     constexpr bool kNarrow = SRC == kF32;
     constexpr int OP_Q = G::kConv ? G::kOpQ : G::kRawQ;   // one part
     constexpr uint32_t kStage16 = (G::kConv ? G::kOp : G::kRaw) >> 4;
-    const bool a_mn = !G::kConv && p.p_mn, b_mn = p.q_mn;   // (tensor memory: K-major)
+    const bool a_mn = !G::kConv && p.p_mn, b_mn = kQmn && p.q_mn;   // (tensor memory: K-major)
     const uint32_t idesc =
         tc::idesc_f16(BP * CL, BQ, SRC == kF32 || (SRC == k16 && p.bf16), a_mn, b_mn);
     auto desc = [](uint32_t addr, bool mn) {
-      return mn ? tc::smem_desc(addr, SL * 128, 1024, true)
+      return mn ? tc::smem_desc(addr, G::kSubK * 128, 1024, true)
                 : tc::smem_desc(addr, 16, kNarrow ? 512 : 1024, !kNarrow);
     };
     const uint64_t a_desc = desc(base_addr, a_mn);
@@ -746,11 +761,15 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     const uint32_t a_slots = tmem + 2 * BQ;      // P's converted parts
     // the MMAs of k-step kk of stage s
     auto step = [&](uint32_t d, int s, int kk, uint32_t add) {
-      const uint64_t b = b_desc + (uint64_t)(s * kStage16) + kk * b_step;
+      constexpr int kSteps = G::kSubK / 16;
+      const int sub = kk / kSteps;
+      kk -= sub * kSteps;
+      const uint64_t b = b_desc + kk * b_step +
+                         (uint64_t)(s * kStage16 + sub * ((G::kConv ? G::kOpSub : G::kRawSub) >> 4));
       if (G::kConv) {
-        const uint32_t a = a_slots + (uint32_t)(s * G::kSlotCols + kk * 8);
+        const uint32_t a = a_slots + (uint32_t)(s * G::kSlotCols + sub * G::kSubCols + kk * 8);
         if (SRC == kF32) {
-          constexpr uint32_t P1 = SL / 2;
+          constexpr uint32_t P1 = G::kSubK / 2;
           constexpr uint64_t Q1 = OP_Q >> 4;
           tc::mma_f16_ts(d, a + 2 * P1, b, idesc, add);
           tc::mma_f16_ts(d, a, b + 2 * Q1, idesc, 1u);
@@ -762,7 +781,8 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
           tc::mma_f16_ts(d, a, b, idesc, add);
         }
       } else {
-        const uint64_t a = a_desc + (uint64_t)(s * kStage16) + kk * a_step;
+        const uint64_t a =
+            a_desc + kk * a_step + (uint64_t)(s * kStage16 + sub * (G::kRawSub >> 4));
         if (kPair)
           tc::mma_f16_pair(d, a, b, idesc, add);
         else
@@ -781,7 +801,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     // the odd CTA's raw_full, the even one's peer_full
     uint32_t own_phase = 0;
     bool issued_any = false, ok = true;
-    const int chunk = p.chunk;
+    const int chunk = p.chunk / SL;
     Unit w;
     for (List list(p, sh, worker, workers); ok && list.next(w);) {
       const int kb = uniform(w.kb), ke = uniform(w.ke), clear_at = uniform(w.clear);
@@ -800,7 +820,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
         }
         const int k1 = min(ke, k0 + chunk);
         for (int ks = k0; ks < k1; ++ks) {
-          const bool clear = !G::kConv && ks == clear_at;
+          const bool clear = kQmn && !G::kConv && ks == clear_at;
           const int rem = klen - ks * SL;   // > 0
           const uint32_t bit = 1u << s;
           if (!kPair || rank == 0 || clear) {
@@ -903,13 +923,18 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
         tc::fence_after_sync();
         const uint32_t slot = tmem + ((uint32_t)((warp & 3) * 32) << 16) +
                               (uint32_t)(2 * BQ + os * G::kSlotCols);
-        if (SRC == kF32) {
-          const int klim = p.wgrad ? w.klen - ks * SL : SL;
-          convert_p_f32(raw, slot, p.p_mn, klim, pr);
-          convert_f32<BQ, NT, 2>(raw + G::kRawP, op, p.q_mn, klim, t);
-        } else {
-          convert_p_i8(raw, slot, pr);
-          convert_i8<BQ, NT, BQ >= 64 ? 4 : 1>(raw + G::kRawP, op, t);
+#pragma unroll 1
+        for (int sub = 0; sub < G::kSub; ++sub) {
+          const unsigned char* rw = raw + sub * G::kRawSub;
+          const uint32_t cols = slot + (uint32_t)(sub * G::kSubCols);
+          if (SRC == kF32) {
+            const int klim = p.wgrad ? w.klen - ks * SL : SL;
+            convert_p_f32(rw, cols, p.p_mn, klim, pr);
+            convert_f32<BQ, NT, 2>(rw + G::kRawP, op + sub * G::kOpSub, kQmn && p.q_mn, klim, t);
+          } else {
+            convert_p_i8(rw, cols, pr);
+            convert_i8<BQ, NT, BQ >= 64 ? 4 : 1>(rw + G::kRawP, op + sub * G::kOpSub, t);
+          }
         }
         // the MMAs read the operand tiles, and TMA refills the raw ones,
         // through the async proxy
@@ -940,6 +965,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
       sync_phase ^= 1u;
       return __all_sync(kAll, ok);
     };
+    const int chunk = p.chunk / SL;
     int acc = 0;
     bool ok = true;
     Unit w;
@@ -949,7 +975,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
       float sum[HC];
 #pragma unroll
       for (int c = 0; c < HC; ++c) sum[c] = 0.f;
-      for (int k0 = w.kb; k0 < w.ke; k0 += p.chunk, ++acc) {
+      for (int k0 = w.kb; k0 < w.ke; k0 += chunk, ++acc) {
         const int buf = acc & 1;
         ok = wait_for(ptx::smem_addr(&sh->acc_full[buf]), (uint32_t)((acc >> 1) & 1), abort_w,
                           p.status, kDevTimeoutFull, p.timeout_ns);
