@@ -321,13 +321,17 @@ int run(int src, int type, Params p, Operand op_p, Operand op_q, cudaStream_t st
   return SGEMM_OK;
 }
 
-// Values of k per tensor-memory accumulation. 32-bit results leave it every 256
-// values (64 for kF32: 24 instructions), 16-bit results once: the error of a
-// truncating sum of 4096 values is far below their rounding.
+// Values of k per tensor-memory accumulation. Each instruction truncates its
+// sum: with n of them in one accumulation a 32-bit result is off by 1.4e-8 n
+// (2-norm, relative). Measured: 32 (512 values) 4.5e-7 for 16-bit operands, the
+// gradient of 8 groups of 1024 x (4096 + 1024) in 71 us (16: 2.3e-7 and 82 us,
+// all: 1.7e-6 and 68 us); for kF32, six a step, 36 (96 values) 6e-7 (a sum in
+// FP32 of 2048 products: 8e-7). 16-bit results leave it once: that error is
+// far below their rounding.
 int accumulation_chunk(int src, int out_type) {
-  if (src == kF32) return 64;
+  if (src == kF32) return 96;
   if (src == kI8 || src == kI8Wide) return kExactK;
-  return out_type == kOutF32 ? 256 : 0x40000000;
+  return out_type == kOutF32 ? 512 : 0x40000000;
 }
 
 }  // namespace
