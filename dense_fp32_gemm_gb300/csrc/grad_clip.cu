@@ -35,7 +35,7 @@ constexpr int kThreads = 256;
 constexpr int kPiece = 16384;           // bytes of a piece
 constexpr int kVecs = kPiece / 16 / kThreads;  // 16-byte vectors per thread and piece
 constexpr int kTable = 1000;            // tensors per launch (they are kernel parameters)
-constexpr int kCtasPerSm = 8;
+constexpr int kCtasPerSm = 5;             // resident (48 registers)
 
 struct Entry {
   const void* in;
@@ -46,6 +46,7 @@ template <int CAP>
 struct Table {
   int count;
   unsigned pieces;
+  bool in_place;              // every tensor is its own output
   Entry e[CAP];
   unsigned first[CAP];        // number of the tensor's first piece
   unsigned char type[CAP];
@@ -110,7 +111,10 @@ __device__ __forceinline__ uint4 pack(const float (&x)[8], int type) {
 // The tensor of piece `at` and the piece's place in it, in vectors counted
 // from the 16-byte address at or below the tensor's start.
 template <int CAP>
-__device__ __forceinline__ int find(const Table<CAP>& t, unsigned at) {
+__device__ __forceinline__ int find(const Table<CAP>& t, unsigned at, int last) {
+  // (most often that of the piece before)
+  if (last >= 0 && t.first[last] <= at && (last + 1 == t.count || at < t.first[last + 1]))
+    return last;
   int lo = 0, hi = t.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -134,14 +138,15 @@ __device__ __forceinline__ double block_sum(double v, double* buf) {
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     squares_kernel(const __grid_constant__ Table<CAP> t, double* sums) {
   __shared__ double buf[kThreads / 32];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   double total = 0.0;
+  int i = -1;
   for (unsigned at = blockIdx.x; at < t.pieces; at += gridDim.x) {
-    const int i = find(t, at);
+    i = find(t, at, i);
     const int type = t.type[i], es = elem_size(type), per = 16 / es;
     const char* in = static_cast<const char*>(t.e[i].in);
     const int head = (int)(reinterpret_cast<uintptr_t>(in) & 15u) / es;
@@ -191,7 +196,7 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     scale_kernel(const __grid_constant__ Table<CAP> t, const double* sums, int nsums,
                  float max_norm, float* norm) {
   __shared__ double buf[kThreads / 32];
@@ -210,8 +215,13 @@ __global__ void __launch_bounds__(kThreads)
   }
   __syncthreads();
   const float coef = coef_s;
-  for (unsigned at = blockIdx.x; at < t.pieces; at += gridDim.x) {
-    const int i = find(t, at);
+  if (coef == 1.f && t.in_place) return;
+  // from the end: what the first pass read last is still in L2 (400 M bf16
+  // values: 420 against 424 us)
+  int i = -1;
+  for (unsigned left = blockIdx.x; left < t.pieces; left += gridDim.x) {
+    const unsigned at = t.pieces - 1 - left;
+    i = find(t, at, i);
     const int type = t.type[i], es = elem_size(type), per = 16 / es;
     const char* in = static_cast<const char*>(t.e[i].in);
     char* out = static_cast<char*>(t.e[i].out);
@@ -257,12 +267,14 @@ Table<CAP> fill(int from, int to, const void* const* in, void* const* out, const
                 const int* types) {
   Table<CAP> t;
   t.count = 0;
+  t.in_place = true;
   unsigned pieces = 0;
   for (int i = from; i < to; ++i) {
     if (sizes[i] == 0) continue;
     const int es = types[i] == SGEMM_TYPE_F32 ? 4 : 2;
     const long long bytes = sizes[i] * es + (long long)(reinterpret_cast<uintptr_t>(in[i]) & 15u);
     t.e[t.count] = Entry{in[i], out == nullptr ? nullptr : out[i], sizes[i]};
+    t.in_place = t.in_place && out != nullptr && out[i] == in[i];
     t.first[t.count] = pieces;
     t.type[t.count] = (unsigned char)types[i];
     pieces += (unsigned)((bytes + kPiece - 1) / kPiece);

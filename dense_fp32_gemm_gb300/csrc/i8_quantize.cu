@@ -28,49 +28,90 @@ __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 
 constexpr int kThreads = 256;
 
-// 16 values of a row at a time: from any address (V: 16-byte aligned), and as 8-bit
-// integers to any address.
+// 16 values of a row as they are stored: from a 16-byte aligned address (V) or
+// any; what lies past the row's end reads as zeros.
+template <typename E>
+struct Raw {
+  uint4 v[sizeof(E)];
+};
 template <typename E, bool V>
-__device__ __forceinline__ void load_16(const E* x, int n, float (&v)[16]) {
+__device__ __forceinline__ Raw<E> load_16(const E* x, int n) {
+  Raw<E> r;
   if (V && n >= 16) {
-    constexpr int W = sizeof(E);      // 16-byte vectors of the 16 values
-    uint4 raw[W];
 #pragma unroll
-    for (int i = 0; i < W; ++i) raw[i] = __ldg(reinterpret_cast<const uint4*>(x) + i);
-    const E* e = reinterpret_cast<const E*>(raw);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = to_f32(e[i]);
+    for (int i = 0; i < (int)sizeof(E); ++i) r.v[i] = __ldg(reinterpret_cast<const uint4*>(x) + i);
   } else {
+    E* e = reinterpret_cast<E*>(r.v);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = i < n ? to_f32(x[i]) : 0.f;
+    for (int i = 0; i < 16; ++i) e[i] = i < n ? x[i] : (E)0.f;
   }
+  return r;
+}
+template <typename E>
+__device__ __forceinline__ float value(const Raw<E>& r, int i) {
+  return to_f32(reinterpret_cast<const E*>(r.v)[i]);
 }
 
-// rint(x / s), the quotient rounded to FP32 first. x * (1 / s) is within 2^-22
-// of it (relative), so the two round to the same integer unless the product
-// lies that near to the middle of two integers; only then the division runs.
-__device__ __forceinline__ int quotient(float x, float s, float inv) {
-  float v = x * inv;
-  const float r = rintf(v);
-  if (!(fabsf(fabsf(v - r) - 0.5f) >= 1e-4f) || !(inv < 1e37f)) {   // (or no number)
-    v = __fdiv_rn(x, s);
-    if (!(v == v)) return 0;
-    return __float2int_rn(fminf(fmaxf(v, -127.f), 127.f));
-  }
-  return __float2int_rn(fminf(fmaxf(r, -127.f), 127.f));
-}
-
-template <typename E, bool V>
-__device__ __forceinline__ uint32_t magnitude(const float (&v)[16], uint32_t most) {
+// The largest magnitude, as bits: a NaN is above infinity, so either survives.
+template <typename E>
+__device__ __forceinline__ uint32_t magnitude(const Raw<E>& r, uint32_t most) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) most = max(most, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  for (int i = 0; i < 16; ++i) most = max(most, __float_as_uint(value(r, i)) & 0x7FFFFFFFu);
   return most;
 }
 
-// One row per block of `threads` = blockDim.x. Up to 16 * kHeld values a thread
-// stay in registers between the two passes (the maximum, the quotients); of a
-// longer row the rest is read again. One read of X and one write of Q are all
-// that a call has to move: at 4096 x 4096 bf16 it is bound by them.
+// rint(x / s), the quotient rounded to FP32 first, in [-127, 127]; 0 for a NaN.
+__device__ __forceinline__ uint32_t quotient(float x, float s) {
+  const float d = __fdiv_rn(x, s);
+  return d == d ? (uint32_t)__float2int_rn(fminf(fmaxf(d, -127.f), 127.f)) : 0u;
+}
+
+// The quotients of 16 values (r, also at x in memory), written to q (n of them).
+// x * inv, inv = 1 / s, is within 2^-22 of the quotient (relative; |x / s| <=
+// 127), so the two round to the same integer unless the product lies that near
+// to the middle of two. Adding 1.5 * 2^23 rounds to the nearest integer, ties
+// to even, and leaves it in the sum's low byte. Where one of the 16 lies near a
+// middle (or 1 / s is no number to multiply by), all are divided.
+template <typename E>
+__device__ __forceinline__ void put_16(const Raw<E>& r, const E* x, float s, float inv,
+                                       signed char* q, int n) {
+  constexpr float kMagic = 12582912.f;
+  if (!(s > 0.f)) {     // a row of zeros, or a NaN scale
+    for (int i = 0; i < min(n, 16); ++i) q[i] = 0;
+    return;
+  }
+  uint32_t w[4];
+  bool near = !(inv < 1e37f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t b[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float v = value(r, 4 * i + j) * inv, t = v + kMagic;
+      // (also for no number)
+      near = near || !(fabsf(v - (t - kMagic)) <= 0.5f - 1e-4f);
+      b[j] = __float_as_uint(t);
+    }
+    w[i] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+  }
+  if (near) {
+#pragma unroll 1
+    for (int i = 0; i < min(n, 16); ++i) q[i] = (signed char)quotient(to_f32(x[i]), s);
+    return;
+  }
+  if (n >= 16 && (reinterpret_cast<uintptr_t>(q) & 15u) == 0) {
+    *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < n) q[i] = (signed char)(w[i >> 2] >> (8 * (i & 3)));
+  }
+}
+
+// A row per block. Of a row up to kHeld groups of 16 values a thread stay in
+// registers between the two passes (the maximum, the quotients); the rest of a
+// longer row is read again. A call has to read X and write Q once.
+constexpr int kHeld = 2;
 template <typename E, bool V>
 __global__ void __launch_bounds__(kThreads)
     quantize_kernel(int M, int K, const E* __restrict__ X, long long ldx,
@@ -79,22 +120,16 @@ __global__ void __launch_bounds__(kThreads)
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const int step = 16 * blockDim.x, k0 = 16 * threadIdx.x;
-  constexpr int kHeld = 2;
   for (int m = blockIdx.x; m < M; m += gridDim.x) {
     const E* x = X + m * ldx;
-    // magnitudes compared as bit patterns: a NaN is above infinity, so either
-    // survives the maximum
     uint32_t most = 0;
-    float held[kHeld][16];
+    Raw<E> h[kHeld];
 #pragma unroll
-    for (int h = 0; h < kHeld; ++h) load_16<E, V>(x + k0 + h * step, K - k0 - h * step, held[h]);
+    for (int i = 0; i < kHeld; ++i) h[i] = load_16<E, V>(x + k0 + i * step, K - k0 - i * step);
 #pragma unroll
-    for (int h = 0; h < kHeld; ++h) most = magnitude<E, V>(held[h], most);
-    for (int k = k0 + kHeld * step; k < K; k += step) {
-      float v[16];
-      load_16<E, V>(x + k, K - k, v);
-      most = magnitude<E, V>(v, most);
-    }
+    for (int i = 0; i < kHeld; ++i) most = magnitude(h[i], most);
+    for (int k = k0 + kHeld * step; k < K; k += step)
+      most = magnitude(load_16<E, V>(x + k, K - k), most);
     most = __reduce_max_sync(0xffffffffu, most);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = most;
@@ -103,31 +138,13 @@ __global__ void __launch_bounds__(kThreads)
     const float s = __fdiv_rn(__uint_as_float(most), 127.f);
     if (threadIdx.x == 0) scale[m] = s;
     const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
-    auto put = [&](const float (&v)[16], int k) {
-      const int n = K - k;
-      uint32_t w[4] = {0u, 0u, 0u, 0u};
-      if (s > 0.f) {     // (a NaN scale: zeros)
+    signed char* q = Q + m * ldq;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          w[i >> 2] |= (uint32_t)(quotient(v[i], s, inv) & 255) << (8 * (i & 3));
-      }
-      signed char* q = Q + m * ldq + k;
-      if (n >= 16 && (reinterpret_cast<uintptr_t>(q) & 15u) == 0) {
-        *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (i < n) q[i] = (signed char)(w[i >> 2] >> (8 * (i & 3)));
-      }
-    };
-#pragma unroll
-    for (int h = 0; h < kHeld; ++h)
-      if (k0 + h * step < K) put(held[h], k0 + h * step);
-    for (int k = k0 + kHeld * step; k < K; k += step) {
-      float v[16];
-      load_16<E, V>(x + k, K - k, v);
-      put(v, k);
-    }
+    for (int i = 0; i < kHeld; ++i)
+      if (k0 + i * step < K)
+        put_16(h[i], x + k0 + i * step, s, inv, q + k0 + i * step, K - k0 - i * step);
+    for (int k = k0 + kHeld * step; k < K; k += step)
+      put_16(load_16<E, V>(x + k, K - k), x + k, s, inv, q + k, K - k);
   }
 }
 
@@ -138,11 +155,13 @@ cudaError_t quantize(int M, int K, const void* X, int ldx, signed char* Q, int l
   cudaLaunchAttribute la[1];
   la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   la[0].val.programmaticStreamSerializationAllowed = 1;
-  // as many threads as the row has 16-value pieces: short rows take few
-  int threads = (K + 15) / 16;
-  threads = threads < 32 ? 32 : (threads + 31) / 32 * 32;
+  // Few rows: as many threads as the row has groups, for its latency. Rows that
+  // fill the SMs: half as many, so that twice the rows are in flight (a row is
+  // a chain of a load, a block-wide maximum and a store).
+  const int groups = (K + 15) / 16, want = M < 4 * sms ? groups : (groups + 1) / 2;
+  int threads = want < 32 ? 32 : (want + 31) / 32 * 32;
   if (threads > kThreads) threads = kThreads;
-  const int fit = sms * (2048 / kThreads) * (kThreads / threads);
+  const int fit = sms * (2048 / threads < 32 ? 2048 / threads : 32);
   lc.gridDim = dim3((unsigned)(M < fit ? M : fit));
   lc.blockDim = dim3((unsigned)threads);
   lc.stream = stream;

@@ -86,6 +86,7 @@ struct Params {
   int P, Q;               // output columns; output rows per group (wgrad)
   int K;                  // contraction length (rows); 0 skips the products
   int p_mn, q_mn;         // operand stored with k as its slow dimension
+  int p_shared;           // rows: one P matrix for all groups
   int bf16;               // k16: operand type (else F16; kI8Wide is F16)
   const int* offsets;     // E + 1 row bounds on the device; null: one group of T rows
   void* out;
@@ -656,7 +657,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
       Unit w;
       for (List list(p, sh, worker, workers); ok && list.next(w);) {
         const int p0 = uniform(w.p0 + rank * BP), q0 = uniform(w.q0 + rank * G::kRows);
-        const int pe = uniform(wgrad ? 0 : w.e), qrow = uniform(wgrad ? 0 : w.row0 + q0);
+        const int pe = uniform(wgrad || p.p_shared ? 0 : w.e), qrow = uniform(wgrad ? 0 : w.row0 + q0);
         const int kb = uniform(w.kb), ke = uniform(w.ke), clear_at = uniform(w.clear);
         int k = uniform(w.kb * SL + (wgrad ? w.row0 : 0));
         for (int ks = kb; ks < ke; ++ks, ++it, k += SL) {

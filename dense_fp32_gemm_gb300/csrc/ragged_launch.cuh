@@ -43,9 +43,10 @@ struct Operand {
 };
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encode();
-// Copies `op` to `dst` with 16-byte aligned rows (widen: as F16) and describes
-// the copy.
-cudaError_t pack_operand(Operand* op, bool widen, void* dst, int sms, cudaStream_t stream);
+// Copies the operands that have a destination there, with 16-byte aligned rows
+// (widen: as F16), in one launch, and describes the copies.
+cudaError_t pack_operands(Operand* a, void* dst_a, Operand* b, void* dst_b, bool widen, int sms,
+                          cudaStream_t stream);
 // The 3-D map of an operand with boxes of box_rows rows of row_bytes bytes.
 bool encode_operand(CUtensorMap* map, const Operand& op, CUtensorMapDataType type, int row_bytes,
                     int box_rows);

@@ -519,6 +519,7 @@ typedef enum {
  *
  * Rows outside every group are not touched. Groups may be empty. Offsets are
  * clamped to 0 .. T, and a group whose end lies before its start is empty;
+ * strideW == 0 reads one matrix for every group;
  * groups must not overlap. E <= 1024. Any element-aligned pointers and leading
  * dimensions work; operands whose rows (or strideW) are not multiples of 16
  * bytes are first copied into the per-stream workspace. Y must not overlap X or

@@ -300,3 +300,13 @@ def test_every_tile(tile, t):
 def test_set_tile_refuses():
     for width, ctas in [(8, 1), (16, 2), (128, 2), (512, 1), (-1, 1), (64, 3)]:
         assert B.sgemm_grouped_set_tile(width, ctas) == B.SGEMM_ERR_INVALID_VALUE
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("op", ["T", "N"])
+@pytest.mark.parametrize("k", [96, 91])
+def test_one_matrix_for_every_group(t, op, k):
+    x, w = values((50, k), TYPES[t], 1, True).cuda(), values((40, k) if op == "T" else (k, 40), TYPES[t], 2, True).cuda()
+    off = torch.tensor([0, 20, 20, 50], dtype=torch.int32, device="cuda")
+    y = B.grouped_gemm(x, w.expand(3, *w.shape), off, op=op)
+    assert torch.equal(y.float(), x.float() @ (w.float().mT if op == "T" else w.float()))

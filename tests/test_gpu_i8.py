@@ -81,7 +81,8 @@ def reference_quantize(x):
 
 
 @pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
-@pytest.mark.parametrize("m,k", [(1, 1), (3, 7), (17, 255), (40, 4096), (500, 1000), (2, 70001)])
+@pytest.mark.parametrize("m,k", [(1, 1), (3, 7), (17, 255), (40, 4096), (500, 1000), (2, 70001), (700, 1000), (900, 4096),
+                                 (650, 4100), (1300, 33)])
 def test_quantize(t, m, k):
     g = torch.Generator().manual_seed(m + k)
     x = torch.randn((m, k), generator=g)
