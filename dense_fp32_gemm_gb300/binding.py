@@ -6,9 +6,10 @@ There is no fallback: if the CUDA library is not built, every call raises.
 """
 from __future__ import annotations
 
-import array
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -434,63 +435,22 @@ def gemm(A, B, C, alpha=1.0, beta=0.0, stream=None):
     return C
 
 
+# (csrc_torch/marshal.cpp: checks, allocation and the C call in native code)
 @functools.cache
-def _type_codes():
-    import torch
-    return {torch.float32: SGEMM_TYPE_F32, torch.bfloat16: SGEMM_TYPE_BF16,
-            torch.float16: SGEMM_TYPE_F16}
-
-
-def _type(t, name):
-    code = _type_codes().get(t.dtype)
-    if code is None:
-        raise ValueError(f"{name} must be float32, bfloat16 or float16")
-    return code
-
-
-def _pitch(t, name):
-    """Row pitch of a row-major matrix (or of the matrices of a 3-D tensor)."""
-    shape, stride = t.shape, t.stride()
-    cols = shape[-1]
-    if cols > 1 and stride[-1] != 1:
-        raise ValueError(f"{name} must be row-major (unit stride along rows)")
-    return max(stride[-2], cols, 1) if shape[-2] > 1 else max(cols, 1)
-
-
-def _check(ok, what):
-    if not ok:
-        raise ValueError(what)
-
-
-def _run(fn, name, device, stream, *args):
-    """One C call on `device` and `stream` (default: its current one)."""
-    import torch
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(device)
-    else:
-        handle = stream.cuda_stream
-    if torch.cuda.current_device() == device:
-        st = fn(*args, handle)
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, handle)
-    if st != SGEMM_OK:
-        raise SgemmError(st, name)
-
-
-def _device(first, *others):
-    """The device index that all tensors share."""
-    device = first.get_device()
-    _check(device >= 0 and all(t.get_device() == device for t in others),
-           "tensors must be on one CUDA device")
-    return device
-
-
-def _offsets(offsets, groups):
-    import torch
-    _check(offsets.dtype is torch.int32 and offsets.dim() == 1 and offsets.is_contiguous(),
-           "offsets must be a contiguous 1-D int32 tensor")
-    _check(offsets.numel() == groups + 1, "offsets must hold one bound more than there are groups")
+def _native():
+    """The marshalling module, bound to the loaded library."""
+    import torch  # noqa: F401  (its libraries come first)
+    path = _build.marshal_path()
+    if not os.path.exists(path):
+        raise RuntimeError(
+            f"{path} is missing: build the CUDA library first "
+            "(python -c 'import __graft_entry__ as g; g.build()')")
+    loader = importlib.machinery.ExtensionFileLoader("_marshal", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
+    loader.exec_module(module)
+    names = ("sgemm_grouped", "sgemm_grouped_wgrad", "sgemm_i8_quantize", "sgemm_i8", "sgemm_grad_clip")
+    module.bind(*(ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in names), SgemmError)
+    return module
 
 
 def grouped_gemm(X, W, offsets, Y=None, op="T", alpha=1.0, beta=0.0, out_dtype=None, stream=None):
@@ -499,137 +459,33 @@ def grouped_gemm(X, W, offsets, Y=None, op="T", alpha=1.0, beta=0.0, out_dtype=N
     op "T" and (E, K, N) with op "N"; the gradient of X is grouped_gemm(dY, W,
     offsets, op=the other). Without Y a new tensor of out_dtype (default: X's)
     is returned, in which rows outside every group are not set."""
-    _check(op == "N" or op == "T", 'op must be "N" or "T"')
-    _check(X.dim() == 2 and W.dim() == 3, "X must be 2-D and W 3-D")
-    T, K = X.shape
-    E, N, WK = W.shape
-    if op == "N":
-        N, WK = WK, N
-    _check(WK == K, "shape mismatch")
-    _check(W.dtype is X.dtype, "X and W must have one type")
-    _offsets(offsets, E)
-    code = _type(X, "X")
-    if Y is None:
-        _check(beta == 0.0, "beta needs Y")
-        _check(X.is_cuda, "tensors must be on one CUDA device")
-        Y = X.new_empty((T, N), dtype=out_dtype)
-    else:
-        _check(Y.dim() == 2 and Y.shape[0] == T and Y.shape[1] == N, "shape mismatch")
-    _run(lib().sgemm_grouped, "sgemm_grouped", _device(X, W, offsets, Y), stream,
-         SGEMM_OP_T if op == "T" else SGEMM_OP_N, code, _type(Y, "Y"), E, T, N, K, alpha,
-         X.data_ptr(), _pitch(X, "X"), W.data_ptr(), _pitch(W, "W"), W.stride(0) if E > 1 else 0,
-         offsets.data_ptr(), beta, Y.data_ptr(), _pitch(Y, "Y"))
-    return Y
+    if op != "N" and op != "T":
+        raise ValueError('op must be "N" or "T"')
+    return _native().grouped_gemm(X, W, offsets, Y, op == "T", alpha, beta, out_dtype, stream)
 
 
 def grouped_wgrad(A, B, offsets, C=None, alpha=1.0, beta=0.0, out_dtype=None, stream=None):
     """C[e] = alpha * A_e.T @ B_e + beta * C[e] over the rows of each group: the
     gradient of W (E, N, K) with A = dY, B = X, of W (E, K, N) with A = X, B = dY.
     Without C a new (E, M, N) tensor of out_dtype (default: A's) is returned."""
-    _check(A.dim() == 2 and B.dim() == 2 and A.shape[0] == B.shape[0], "shape mismatch")
-    _check(A.dtype is B.dtype, "A and B must have one type")
-    E = offsets.numel() - 1
-    _check(E >= 0, "offsets must hold one bound more than there are groups")
-    _offsets(offsets, E)
-    (T, M), N = A.shape, B.shape[1]
-    code = _type(A, "A")
-    if C is None:
-        _check(beta == 0.0, "beta needs C")
-        _check(A.is_cuda, "tensors must be on one CUDA device")
-        C = A.new_empty((E, M, N), dtype=out_dtype)
-    else:
-        _check(tuple(C.shape) == (E, M, N), "shape mismatch")
-    _run(lib().sgemm_grouped_wgrad, "sgemm_grouped_wgrad", _device(A, B, offsets, C), stream, code,
-         _type(C, "C"), E, T, M, N, alpha, A.data_ptr(), _pitch(A, "A"), B.data_ptr(),
-         _pitch(B, "B"), offsets.data_ptr(), beta, C.data_ptr(), _pitch(C, "C"),
-         C.stride(0) if E > 1 else 0)
-    return C
+    return _native().grouped_wgrad(A, B, offsets, C, alpha, beta, out_dtype, stream)
 
 
 def i8_quantize(X, Q=None, scale=None, stream=None):
     """(Q, scale): the rows of X as 8-bit integers with one FP32 scale a row,
-    scale = max|X[m]| / 127."""
-    import torch
-    _check(X.dim() == 2, "X must be 2-D")
-    M, K = X.shape
-    code = _type(X, "X")
-    _check(X.is_cuda, "tensors must be on one CUDA device")
-    if Q is None:
-        # rows padded to 16 bytes, so that sgemm_i8 reads them in place
-        Q = X.new_empty((M, (K + 15) // 16 * 16), dtype=torch.int8)
-        if K & 15:
-            Q = Q[:, :K]
-    if scale is None:
-        scale = X.new_empty((M,), dtype=torch.float32)
-    _check(Q.dtype is torch.int8 and Q.shape == X.shape, "Q must be int8 of X's shape")
-    _vector(scale, M, "scale")
-    _run(lib().sgemm_i8_quantize, "sgemm_i8_quantize", _device(X, Q, scale), stream, M, K, code,
-         X.data_ptr(), _pitch(X, "X"), Q.data_ptr(), _pitch(Q, "Q"), scale.data_ptr())
-    return Q, scale
-
-
-def _vector(s, n, name):
-    import torch
-    _check(s.dtype is torch.float32 and s.dim() == 1 and s.shape[0] == n and s.is_contiguous(),
-           f"{name} must be a contiguous float32 vector of {n}")
+    scale = max|X[m]| / 127. A new Q has rows padded to 16 bytes."""
+    return _native().i8_quantize(X, Q, scale, stream)
 
 
 def i8_gemm(A, scaleA, B, scaleB, C=None, out_dtype=None, stream=None):
     """C = (A @ B.T) * scaleA[:, None] * scaleB on int8 A (M, K) and B (N, K), the
     sum an exact integer. Without C a new tensor of out_dtype (default bfloat16)
     is returned."""
-    import torch
-    _check(A.dim() == 2 and B.dim() == 2 and A.shape[1] == B.shape[1], "shape mismatch")
-    _check(A.dtype is torch.int8 and B.dtype is torch.int8, "A and B must be int8")
-    M, K = A.shape
-    N = B.shape[0]
-    _vector(scaleA, M, "scaleA")
-    _vector(scaleB, N, "scaleB")
-    if C is None:
-        _check(A.is_cuda, "tensors must be on one CUDA device")
-        C = A.new_empty((M, N), dtype=out_dtype or torch.bfloat16)
-    else:
-        _check(C.dim() == 2 and C.shape[0] == M and C.shape[1] == N, "shape mismatch")
-    _run(lib().sgemm_i8, "sgemm_i8", _device(A, scaleA, B, scaleB, C), stream, M, N, K,
-         A.data_ptr(), _pitch(A, "A"), scaleA.data_ptr(), B.data_ptr(), _pitch(B, "B"),
-         scaleB.data_ptr(), _type(C, "C"), C.data_ptr(), _pitch(C, "C"))
-    return C
-
-
-def _tensor_list(tensors, device):
-    """(addresses, element counts, type codes) of contiguous tensors as arrays
-    that the C call reads. (One pass per property: with hundreds of tensors the
-    calls per tensor are what this costs.)"""
-    import torch
-    T = torch.Tensor
-    _check(set(map(T.get_device, tensors)) == {device}, "gradients must be on one CUDA device")
-    _check(all(map(T.is_contiguous, tensors)), "gradients must be contiguous")
-    codes = _type_codes()
-    try:
-        types = array.array("i", [codes[t.dtype] for t in tensors])
-    except KeyError:
-        raise ValueError("gradients must be float32, bfloat16 or float16") from None
-    return array.array("Q", map(T.data_ptr, tensors)), array.array("q", map(T.numel, tensors)), types
+    return _native().i8_gemm(A, scaleA, B, scaleB, C, out_dtype, stream)
 
 
 def clip_grad_norm(grads, max_norm, out=None, stream=None):
     """The 2-norm (a float32 scalar tensor) of contiguous CUDA tensors taken
     together, before clipping; out[i] = grads[i] * min(1, max_norm / (norm +
     1e-6)), in place without `out`."""
-    import torch
-    grads = list(grads)
-    _check(len(grads) > 0, "no gradients")
-    device = grads[0].get_device()
-    _check(device >= 0, "gradients must be on one CUDA device")
-    src, sizes, types = _tensor_list(grads, device)
-    dst = src
-    if out is not None:
-        out = list(out)
-        _check(len(out) == len(grads), "out must hold a tensor for every gradient")
-        dst, osizes, otypes = _tensor_list(out, device)
-        _check(osizes == sizes and otypes == types, "out must have the gradients' types and sizes")
-    norm = grads[0].new_empty((), dtype=torch.float32)
-    _run(lib().sgemm_grad_clip, "sgemm_grad_clip", device, stream, len(grads),
-         src.buffer_info()[0], dst.buffer_info()[0], sizes.buffer_info()[0], types.buffer_info()[0],
-         max_norm, norm.data_ptr())
-    return norm
+    return _native().clip_grad_norm(grads, max_norm, out, stream)

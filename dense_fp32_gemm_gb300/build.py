@@ -11,14 +11,20 @@ declared in include/sgemm_gb300.h are exported.
 ``build(config_list=..., tuned_table=..., out_dir=...)`` builds a separate
 library from another configuration list (the tuner's candidate set) without
 touching the product library.
+
+Beside it, csrc_torch/marshal.cpp (the torch conveniences of binding.py) is
+compiled with the host compiler against the installed torch.
 """
 from __future__ import annotations
 
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -41,6 +47,38 @@ _CFG_TU = """// Generated by dense_fp32_gemm_gb300/build.py from the configurati
 
 SGEMM_GB300_DEFINE_CONFIG({name})
 """
+
+
+MARSHAL_SOURCE = os.path.join(HERE, "csrc_torch", "marshal.cpp")
+
+
+def marshal_path() -> str:
+    """The torch marshalling module built for the installed torch (another
+    version needs another build)."""
+    version = importlib.metadata.version("torch").replace("+", "_")
+    return os.path.join(OUT_DIR, f"_marshal_{version}.so")
+
+
+def build_marshal() -> str:
+    """Compile csrc_torch/marshal.cpp against the installed torch, if it or the
+    torch version changed."""
+    path = marshal_path()
+    if not _stale(path, [MARSHAL_SOURCE]):
+        return path
+    os.makedirs(OUT_DIR, exist_ok=True)
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    includes = [sysconfig.get_paths()["include"], os.path.join(torch_dir, "include"),
+                os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), cuda]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden"]
+    cmd += [f"-I{d}" for d in includes]
+    cmd += [MARSHAL_SOURCE, "-o", path + ".tmp", "-L" + os.path.join(torch_dir, "lib"),
+            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on marshal.cpp:\n{r.stderr[-4000:]}")
+    os.replace(path + ".tmp", path)
+    return path
 
 
 def nvcc() -> str:
@@ -128,8 +166,12 @@ def build(verbose: bool = False, jobs: int | None = None, config_list: str | Non
         if o not in keep:
             os.remove(o)
     n = jobs or min(len(srcs), os.cpu_count() or 1)
-    with ThreadPoolExecutor(max(1, n)) as ex:
+    with ThreadPoolExecutor(max(1, n + 1)) as ex:
+        # (a candidate build of the tuner takes the product's marshalling module)
+        marshal = ex.submit(build_marshal) if out_dir == OUT_DIR else None
         list(ex.map(compile_one, zip(srcs, objs)))
+        if marshal is not None:
+            marshal.result()
     if verbose:
         for src, log in sorted(logs.items()):
             print(f"== {os.path.basename(src)}\n{log}", file=sys.stderr)

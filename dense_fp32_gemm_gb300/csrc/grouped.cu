@@ -164,12 +164,19 @@ bool encode_operand(CUtensorMap* map, const Operand& op, CUtensorMapDataType typ
   cuuint64_t strides[2] = {(cuuint64_t)pitch, (cuuint64_t)mat};
   cuuint32_t box[3] = {(cuuint32_t)(row_bytes / op.elem), (cuuint32_t)box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  return tensor_map_encode()(map, type, 3, const_cast<void*>(op.ptr), dims, strides, box, estr,
-                             CU_TENSOR_MAP_INTERLEAVE_NONE,
-                             row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
-                                              : CU_TENSOR_MAP_SWIZZLE_64B,
-                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  auto encode = [&] {
+    return tensor_map_encode()(map, type, 3, const_cast<void*>(op.ptr), dims, strides, box, estr,
+                               CU_TENSOR_MAP_INTERLEAVE_NONE,
+                               row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                                : CU_TENSOR_MAP_SWIZZLE_64B,
+                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (encode()) return true;
+  // a host thread whose first CUDA work this is (autograd's, for one) has no
+  // context yet, which the encoder needs: selecting the device gives it one
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode();
 }
 
 namespace {

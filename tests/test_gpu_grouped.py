@@ -310,3 +310,22 @@ def test_one_matrix_for_every_group(t, op, k):
     off = torch.tensor([0, 20, 20, 50], dtype=torch.int32, device="cuda")
     y = B.grouped_gemm(x, w.expand(3, *w.shape), off, op=op)
     assert torch.equal(y.float(), x.float() @ (w.float().mT if op == "T" else w.float()))
+
+
+def test_from_a_new_host_thread():
+    """A thread whose first CUDA work is the call (as autograd's is)."""
+    import threading
+    x, w = values((40, 64), torch.bfloat16, 1).cuda(), values((2, 32, 64), torch.bfloat16, 2).cuda()
+    off = torch.tensor([0, 7, 40], dtype=torch.int32, device="cuda")
+    want = B.grouped_gemm(x, w, off)
+    torch.cuda.synchronize()
+    y = torch.zeros_like(want)
+    s = torch.cuda.current_stream().cuda_stream
+    args = (B.SGEMM_OP_T, B.SGEMM_TYPE_BF16, B.SGEMM_TYPE_BF16, 2, 40, 32, 64, 1.0, x.data_ptr(), 64, w.data_ptr(),
+            64, 32 * 64, off.data_ptr(), 0.0, y.data_ptr(), 32, s)
+    got = []
+    t = threading.Thread(target=lambda: got.append(B.sgemm_grouped(*args)))
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert got == [0] and torch.equal(y, want)
