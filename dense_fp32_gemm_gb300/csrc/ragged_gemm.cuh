@@ -471,28 +471,32 @@ __device__ __forceinline__ void from_f32(float* d, float v) { *d = v; }
 __device__ __forceinline__ void from_f32(__nv_bfloat16* d, float v) { *d = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void from_f32(__half* d, float v) { *d = __float2half_rn(v); }
 
-// A thread's column of the tile: `n` valid values (of HC) at pitch ld. A warp
-// writes 32 neighbours at a time. The element type, the full column and beta
-// are decided once: the loops are unrolled over the registers, and a branch per
-// value made them outgrow the instruction cache (20 to 60 thousand cycles a
-// tile, against one thousand).
+// Part of a thread's column of the tile: `n` valid values (of HC) at pitch ld,
+// `live` when its p is inside the output. A warp writes 32 neighbours at a
+// time. The element type, the full column and beta are decided once for all
+// values: a branch per value made the unrolled loops outgrow the instruction
+// cache (20 to 60 thousand cycles a tile, against one thousand). INT: scale_q
+// holds the columns' scales.
 template <bool INT, int HC, typename T>
 __device__ __forceinline__ void write_column(T* out, long long ld, const float (&sum)[HC],
-                                             float scale, const float* scale_q, float beta, int n) {
+                                             float scale, const float* scale_q, float beta, int n,
+                                             bool live) {
   auto value = [&](int c) {
-    return INT ? (float)__float_as_int(sum[c]) * __ldg(scale_q + c) * scale : scale * sum[c];
+    return INT ? (float)__float_as_int(sum[c]) * (c < n ? __ldg(scale_q + c) : 0.f) * scale
+               : scale * sum[c];
   };
   if (beta == 0.f && n >= HC) {
 #pragma unroll
     for (int c = 0; c < HC; ++c) {
-      from_f32(out, value(c));
+      const float v = value(c);
+      if (live) from_f32(out, v);
       out += ld;
     }
   } else {
 #pragma unroll
     for (int c = 0; c < HC; ++c) {
-      if (c < n) {
-        float v = value(c);
+      float v = value(c);
+      if (live && c < n) {
         if (beta != 0.f) v = fmaf(beta, to_f32(*out), v);
         from_f32(out, v);
       }
@@ -972,61 +976,126 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     Unit w;
     for (List list(p, sh, worker, workers); ok && list.next(w);) {
       const int nq = w.nq - half * HC;                 // valid columns of this warp (may be <= 0)
-      // integer sums are kept in the same registers
-      float sum[HC];
+      const int pp = w.p0 + rank * BP + pr;
+      const bool live = pp < p.P;
+      const float sp = !G::kInt ? p.alpha : (live ? p.scale_p[pp] : 0.f);
+      const long long row = (long long)(p.wgrad ? 0 : w.row0) + w.q0 + half * HC;
+      const long long at = (p.wgrad ? (long long)w.e * p.stride_o : 0ll) + row * p.ldo + pp;
+      // writes the sums of N columns from column c0 on
+      auto write = [&](const auto& sums, int c0) {
+        constexpr int N = sizeof(sums) / sizeof(float);
+        const float* sq = G::kInt ? p.scale_q + row + c0 : nullptr;
+        const long long a = at + c0 * p.ldo;
+        if (p.out_type == kOutF32)
+          write_column<G::kInt, N>(static_cast<float*>(p.out) + a, p.ldo, sums, sp, sq, p.beta,
+                                   nq - c0, live);
+        else if (p.out_type == kOutBf16)
+          write_column<G::kInt, N>(static_cast<__nv_bfloat16*>(p.out) + a, p.ldo, sums, sp, sq,
+                                   p.beta, nq - c0, live);
+        else
+          write_column<G::kInt, N>(static_cast<__half*>(p.out) + a, p.ldo, sums, sp, sq, p.beta,
+                                   nq - c0, live);
+      };
+      // CH columns of the accumulator in use; integers as such, in the same registers
+      auto load = [&](int c0, float (&v)[CH]) {
+        uint32_t* r = reinterpret_cast<uint32_t*>(v);
+        const uint32_t src = tmem + lane_base + (uint32_t)((acc & 1) * BQ + half * HC + c0);
+        if constexpr (CH == 8) {
+          tc::tmem_ld8(src, *reinterpret_cast<uint32_t(*)[8]>(r));
+        } else {
 #pragma unroll
-      for (int c = 0; c < HC; ++c) sum[c] = 0.f;
-      for (int k0 = w.kb; k0 < w.ke; k0 += chunk, ++acc) {
-        const int buf = acc & 1;
-        ok = wait_for(ptx::smem_addr(&sh->acc_full[buf]), (uint32_t)((acc >> 1) & 1), abort_w,
-                          p.status, kDevTimeoutFull, p.timeout_ns);
-        ok = __all_sync(kAll, ok);
-        if (!ok) break;
-        tc::fence_after_sync();
-        const uint32_t src = tmem + lane_base + (uint32_t)(buf * BQ + half * HC);
-#pragma unroll
-        for (int c0 = 0; c0 < HC; c0 += CH) {
-          if (c0 >= nq) continue;                      // (the whole warp)
-          uint32_t v[CH];
-          if constexpr (CH == 8) {
-            tc::tmem_ld8(src, v);
-          } else {
-#pragma unroll
-            for (int i = 0; i < CH; i += 16)
-              tc::tmem_ld16(src + (uint32_t)(c0 + i), *reinterpret_cast<uint32_t(*)[16]>(&v[i]));
-          }
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < CH; ++i) {
-            if (G::kInt)
-              sum[c0 + i] = __int_as_float(__float_as_int(sum[c0 + i]) +
-                                           __float2int_rn(__uint_as_float(v[i])));
-            else
-              sum[c0 + i] += __uint_as_float(v[i]);
-          }
+          for (int i = 0; i < CH; i += 16)
+            tc::tmem_ld16(src + (uint32_t)i, *reinterpret_cast<uint32_t(*)[16]>(r + i));
         }
+        tc::tmem_wait_ld();
+        if (G::kInt) {
+#pragma unroll
+          for (int i = 0; i < CH; ++i) v[i] = __int_as_float(__float2int_rn(v[i]));
+        }
+      };
+      auto acquire = [&]() -> bool {                   // waits for the next accumulator
+        const bool full =
+            wait_for(ptx::smem_addr(&sh->acc_full[acc & 1]), (uint32_t)((acc >> 1) & 1), abort_w,
+                     p.status, kDevTimeoutFull, p.timeout_ns);
+        const bool all = __all_sync(kAll, full);
+        tc::fence_after_sync();
+        return all;
+      };
+      auto release = [&] {                             // all of its columns have been read
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) {
           // the even CTA's MMA warp waits for the epilogues of both
+          uint64_t* bar = &sh->acc_empty[acc & 1];
           if (kPair && rank != 0)
-            ptx::mbar_arrive_remote(ptx::mapa(ptx::smem_addr(&sh->acc_empty[buf]), 0u));
+            ptx::mbar_arrive_remote(ptx::mapa(ptx::smem_addr(bar), 0u));
           else
-            ptx::mbar_arrive(ptx::smem_addr(&sh->acc_empty[buf]));
+            ptx::mbar_arrive(ptx::smem_addr(bar));
+        }
+        ++acc;
+      };
+      // this range's partial tile: slot 1 of this CTA for the range that starts
+      // the tile, else slot 0
+      auto slot = [&](int c, int which) -> float* {
+        return p.partials + (((long long)c * 2 + which) * CL + rank) * (BP * BQ) + half * HC * BP + pr;
+      };
+      float* part = slot(worker, w.kb == 0 ? 1 : 0);
+
+      // Sums that are all in one accumulation go straight from tensor memory to
+      // their place, CH columns at a time in a rolled loop: a tile's first
+      // pass through unrolled code waits for the instructions (3 us for 128
+      // columns), which is most of a small call's epilogue. Others are added up
+      // in registers, which only unrolled code can index.
+      if (w.ke > w.kb && w.ke - w.kb <= chunk) {
+        ok = acquire();
+        if (!ok) break;
+#pragma unroll 1
+        for (int c0 = 0; c0 < HC && c0 < nq; c0 += CH) {
+          float v[CH];
+          load(c0, v);
+          if (w.parts > 1) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+              if (c0 + c < nq) __stcg(part + (c0 + c) * BP, v[c]);
+          } else {
+            write(v, c0);
+          }
+        }
+        release();
+      } else {
+        float sum[HC];
+#pragma unroll
+        for (int c = 0; c < HC; ++c) sum[c] = 0.f;
+        for (int k0 = w.kb; k0 < w.ke; k0 += chunk) {
+          ok = acquire();
+          if (!ok) break;
+#pragma unroll
+          for (int c0 = 0; c0 < HC; c0 += CH) {
+            if (c0 >= nq) continue;                    // (the whole warp)
+            float v[CH];
+            load(c0, v);
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+              if (G::kInt)
+                sum[c0 + i] = __int_as_float(__float_as_int(sum[c0 + i]) + __float_as_int(v[i]));
+              else
+                sum[c0 + i] += v[i];
+            }
+          }
+          release();
+        }
+        if (!ok) break;
+        if (w.parts > 1) {
+#pragma unroll
+          for (int c = 0; c < HC; ++c)
+            if (c < nq) __stcg(part + c * BP, sum[c]);
+        } else if (nq > 0) {
+          write(sum, 0);
         }
       }
-      if (!ok) break;
       if (w.parts > 1) {
-        // publish this range's partial tile (slot 1 of this CTA for the range
-        // that starts the tile, else slot 0); the last to arrive adds them all
-        const long long kTile = BP * BQ;
-        auto slot = [&](int c, int which) -> float* {
-          return p.partials + (((long long)c * 2 + which) * CL + rank) * kTile + half * HC * BP + pr;
-        };
-        float* part = slot(worker, w.kb == 0 ? 1 : 0);
-#pragma unroll
-        for (int c = 0; c < HC; ++c)
-          if (c < nq) __stcg(part + c * BP, sum[c]);
+        // all of the partial tile is written; the last worker to arrive adds
+        // the parts in the order of k
         __threadfence();
         ok = epi_sync();
         if (!ok) break;
@@ -1041,53 +1110,37 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
         if (!ok) break;
         if (!*reinterpret_cast<volatile int*>(&sh->last)) continue;
         __threadfence();
-        // (of two, the own one is still in registers: a sum of two terms does
-        // not depend on their order). LP partials by LB columns are loaded at a
-        // time: one after another, each would cost the latency of L2.
-        constexpr int LB = HC < 32 ? HC : 32, LP = 32 / LB;
-        const int own = w.parts == 2 ? worker - w.c0 : -1;
-        for (int i0 = 0; i0 < w.parts; i0 += LP) {
+        // LP partials by CH columns are loaded at a time: one after another,
+        // each would cost the latency of L2
+        constexpr int LP = 32 / CH;
+#pragma unroll 1
+        for (int c0 = 0; c0 < HC && c0 < nq; c0 += CH) {
+          float sum[CH];
 #pragma unroll
-          for (int c0 = 0; c0 < HC; c0 += LB) {
-            if (c0 >= nq) continue;
-            float x[LP][LB];
+          for (int c = 0; c < CH; ++c) sum[c] = 0.f;
+#pragma unroll 1
+          for (int i0 = 0; i0 < w.parts; i0 += LP) {
+            float x[LP][CH];
 #pragma unroll
             for (int i = 0; i < LP; ++i) {
-              const float* src = slot(w.c0 + i0 + i, i0 + i == 0 ? 1 : 0);
-              const bool take = i0 + i < w.parts && i0 + i != own;
+              const float* src = slot(w.c0 + i0 + i, i0 + i == 0 ? 1 : 0) + c0 * BP;
 #pragma unroll
-              for (int c = 0; c < LB; ++c)
-                x[i][c] = take && c0 + c < nq ? __ldcg(src + (c0 + c) * BP) : 0.f;
+              for (int c = 0; c < CH; ++c)
+                x[i][c] = i0 + i < w.parts && c0 + c < nq ? __ldcg(src + c * BP) : 0.f;
             }
 #pragma unroll
             for (int i = 0; i < LP; ++i) {
 #pragma unroll
-              for (int c = 0; c < LB; ++c) {
-                if (i0 + i == 0 && own < 0)
-                  sum[c0 + c] = x[i][c];
-                else if (G::kInt)
-                  sum[c0 + c] = __int_as_float(__float_as_int(sum[c0 + c]) + __float_as_int(x[i][c]));
+              for (int c = 0; c < CH; ++c) {
+                if (G::kInt)
+                  sum[c] = __int_as_float(__float_as_int(sum[c]) + __float_as_int(x[i][c]));
                 else
-                  sum[c0 + c] += x[i][c];
+                  sum[c] += x[i][c];
               }
             }
           }
+          write(sum, c0);
         }
-      }
-      const int pp = w.p0 + rank * BP + pr;
-      if (pp < p.P && nq > 0) {
-        const float sp = G::kInt ? p.scale_p[pp] : p.alpha;
-        const long long row = (long long)(p.wgrad ? 0 : w.row0) + w.q0 + half * HC;
-        const long long at = (p.wgrad ? (long long)w.e * p.stride_o : 0ll) + row * p.ldo + pp;
-        const float* sq = G::kInt ? p.scale_q + row : nullptr;
-        if (p.out_type == kOutF32)
-          write_column<G::kInt, HC>(static_cast<float*>(p.out) + at, p.ldo, sum, sp, sq, p.beta, nq);
-        else if (p.out_type == kOutBf16)
-          write_column<G::kInt, HC>(static_cast<__nv_bfloat16*>(p.out) + at, p.ldo, sum, sp, sq,
-                                    p.beta, nq);
-        else
-          write_column<G::kInt, HC>(static_cast<__half*>(p.out) + at, p.ldo, sum, sp, sq, p.beta,
-                                    nq);
       }
     }
   }
