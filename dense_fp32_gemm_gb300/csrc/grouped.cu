@@ -3,6 +3,7 @@
 // token and channel scales): argument checks, tile width, operand maps and
 // the launch of ragged_kernel.
 #include <atomic>
+#include <cmath>
 #include <cstdio>
 #include <mutex>
 
@@ -259,8 +260,18 @@ constexpr TileCost kTileCosts[] = {
     {kI8, 128, 1, 460, 1300},
     {kI8Wide, 256, 2, 390, 2500},
 };
-// Time of publishing and adding the parts of a tile that is cut along k, ns.
-int cut_cost(int bq) { return 1600 + 25 * bq; }
+// What cutting a tile along k costs, ns: publishing a part and the rendezvous,
+// and reading one part back (a load of L2 for every 32 columns of a warp; four
+// narrow parts go in one).
+int cut_once(int bq) { return 1500 + 6 * bq; }
+int cut_part(int bq) { return bq <= 32 ? 12 * bq : 100 + 12 * bq; }
+// Slices (of `slice` ns) that a part of a tile of `sum` slices has at least: with
+// p parts the sum takes sum / p slices and adding them p * cut_part, least at
+// parts of this length.
+int cut_least(double sum, int slice, int bq) {
+  const int n = (int)std::sqrt(sum * cut_part(bq) / slice);
+  return n < 3 ? 3 : n;
+}
 
 // The tile of a call: the one whose list takes least time on the workers it
 // has, by the costs above. The host does not know the groups' sizes: they are
@@ -278,11 +289,16 @@ Form choose_tile(int src, const Params& p, int sms) {
                                                ? (double)p.T / c.bq + groups / 2
                                                : groups);
     const double tiles = q * cdiv(p.P, BP * c.cl);
-    const double k = p.wgrad ? (double)p.T / p.E : p.K;
-    const double sum = (k / 64 < 1 ? 1 : k / 64) * c.slice;
-    const double tile = sum > c.epilogue ? sum : c.epilogue;
+    const double k = p.wgrad ? (double)p.T / p.E : p.K, slices = k / 64 < 1 ? 1 : k / 64;
+    const double sum = slices * c.slice, tile = sum > c.epilogue ? sum : c.epilogue;
     const double whole = (double)(long long)((tiles + workers - 1) / workers) * tile;
-    const double cut = tiles / workers * tile + cut_cost(c.bq);
+    double parts = 2, cutters = workers;
+    if (tiles < workers) {
+      const double most = tiles * slices / cut_least(slices, c.slice, c.bq);
+      cutters = most < tiles ? tiles : (most < workers ? most : workers);
+      parts = cutters / tiles + 1;
+    }
+    const double cut = tiles / cutters * tile + cut_once(c.bq) + parts * cut_part(c.bq);
     const double time = (cut < whole ? cut : whole) + c.epilogue;
     if (best.bq == 0 || time < least) {
       least = time;
@@ -343,9 +359,14 @@ int run(int src, int type, Params p, Operand op_p, Operand op_q, cudaStream_t st
     return SGEMM_ERR_LAUNCH;
   }
   p.partials = reinterpret_cast<float*>(at + pack_p + pack_q);
-  for (const TileCost& c : kTileCosts)
-    if (c.src == src && c.bq == bq && c.cl == cl)
-      p.cut_slices = cut_cost(bq) * 64 / (c.slice * slice) + 1;
+  for (const TileCost& c : kTileCosts) {
+    if (c.src != src || c.bq != bq) continue;
+    const double ns = (double)c.slice * slice / 64;
+    const double sum = (double)(p.wgrad ? p.T / p.E : p.K) / slice;
+    p.cut_least = cut_least(sum < 1 ? 1 : sum, (int)ns, bq);
+    p.cut_once = (int)(16 * cut_once(bq) / ns) + 1;
+    p.cut_part = (int)(16 * cut_part(bq) / ns) + 1;
+  }
   p.timeout_ns = library_wait_timeout_ns();
 
   CUtensorMap mp = {}, mq = {};

@@ -96,7 +96,9 @@ struct Params {
   const float* scale_p;   // kI8: scales of p and q
   const float* scale_q;
   int chunk;              // values of k per tensor-memory accumulation (a multiple of the slice)
-  int cut_slices;         // tiles are cut along k only to save at least so many k-slices
+  // when tiles are cut along k: the slices a part has at least, and what a cut
+  // costs, in 1/16 slices: once, and for each part of the tile
+  int cut_least, cut_once, cut_part;
   float* partials;        // two tiles of BQ x 128 floats per CTA
   uint32_t* counters;     // arrivals at a cut tile, one per CTA, zero between launches
   int* status;
@@ -169,8 +171,6 @@ struct Geo {
 // FP32 sums of integers leave tensor memory at the latest after this many
 // values of k (products of at most 2^14 each).
 constexpr int kExactK = 1024;
-// Fewest k-slices a worker gets when the tiles of a small problem are cut.
-constexpr int kMinSlices = 3;
 
 struct Shared {
   uint64_t raw_full[24], raw_empty[24];
@@ -605,12 +605,21 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     if (lane == 0) {
       const int tiles = tiles_before, total = pos_before;
       sh->tiles = tiles;
-      // whole waves first; what is left, one to two waves, by slices, unless
-      // that saves less time than publishing and adding the parts takes
+      // whole waves first; what is left, one to two waves (or, with fewer tiles
+      // than workers, all of them), by slices, unless that saves less time than
+      // publishing and adding the parts takes
       const int over = tiles % workers;
-      const int saved = over == 0 ? 0 : (int)((long long)total / tiles * (workers - over) / workers);
-      int dp = tiles;
-      if (over != 0 && saved >= p.cut_slices) dp = max(0, tiles / workers - 1) * workers;
+      int dp = tiles, cutters = workers;
+      if (over != 0) {
+        const int mean = total / tiles;
+        int saved = mean * 16 / workers * (workers - over), parts = 2;
+        if (tiles < workers) {
+          cutters = min(workers, max(tiles, total / p.cut_least));
+          parts = cutters / tiles + 1;
+          saved = 16 * (mean - total / cutters);
+        }
+        if (saved >= p.cut_once + parts * p.cut_part) dp = max(0, tiles / workers - 1) * workers;
+      }
       sh->dp = dp;
       int base_pos = total;
       if (dp == 0) {
@@ -622,7 +631,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
       }
       sh->base = base_pos;
       sh->len = total - base_pos;
-      sh->cutters = dp < tiles ? min(workers, max(tiles - dp, sh->len / kMinSlices)) : 0;
+      sh->cutters = dp < tiles ? cutters : 0;
     }
   }
   tc::fence_before_sync();
