@@ -318,12 +318,12 @@ __device__ __forceinline__ bool wait_for_pair(uint32_t bar, uint32_t parity, vol
 
 // ---- conversions --------------------------------------------------------------
 // Two FP32 values into packed BF16 parts with x = h + m + l exactly (but for
-// underflow): h is x rounded to nearest, so at most 16 significant bits are
+// underflow): h is x rounded to nearest (and to BF16's largest value, not to
+// infinity, where FP32 reaches beyond it), so at most 16 significant bits are
 // left, of which m takes the first 8 and l the rest (both by truncation: two
 // byte permutes instead of two conversions).
 __device__ __forceinline__ void split2(float x, float y, uint32_t& h, uint32_t& m, uint32_t& l) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
-  h = *reinterpret_cast<const uint32_t*>(&v);
+  asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(y), "f"(x));
   const float rx = x - __uint_as_float(h << 16), ry = y - __uint_as_float(h & 0xFFFF0000u);
   m = __byte_perm(__float_as_uint(rx), __float_as_uint(ry), 0x7632);
   const float sx = rx - __uint_as_float(__float_as_uint(rx) & 0xFFFF0000u);
@@ -570,15 +570,28 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   if (warp == 0) {
-    // scan of the groups: rows, number and slice position of each one's first tile
+    // scan of the groups: rows, number and slice position of each one's first
+    // tile. A group starts at the end of those before it at the earliest, so the
+    // groups together have at most T rows whatever the offsets hold.
     const int ptiles = cdiv(p.P, BP * CL);
-    int tiles_before = 0, pos_before = 0;
+    int tiles_before = 0, pos_before = 0, end_before = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
-      int lo = 0, n = 0, tiles = 0;
+      int lo = 0, hi = 0, n = 0, tiles = 0;
       if (e < p.E) {
         lo = p.offsets == nullptr ? 0 : min(max(p.offsets[e], 0), p.T);
-        const int hi = p.offsets == nullptr ? p.T : min(max(p.offsets[e + 1], 0), p.T);
+        hi = p.offsets == nullptr ? p.T : min(max(p.offsets[e + 1], 0), p.T);
+      }
+      int ends = hi;                    // largest end up to this group
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(kAll, ends, d);
+        if (lane >= d) ends = max(ends, o);
+      }
+      const int before = __shfl_up_sync(kAll, ends, 1);
+      lo = max(lo, max(end_before, lane > 0 ? before : 0));
+      end_before = max(end_before, __shfl_sync(kAll, ends, 31));
+      if (e < p.E) {
         n = max(hi - lo, 0);
         tiles = ptiles * cdiv(p.wgrad ? p.Q : n, BQ);
       }

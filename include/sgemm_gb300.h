@@ -518,9 +518,9 @@ typedef enum {
  * beta == 0 never reads Y; alpha == 0 or K == 0 never reads X or W.
  *
  * Rows outside every group are not touched. Groups may be empty. Offsets are
- * clamped to 0 .. T, and a group whose end lies before its start is empty;
- * strideW == 0 reads one matrix for every group;
- * groups must not overlap. E <= 1024. Any element-aligned pointers and leading
+ * clamped to 0 .. T; a group whose end lies before its start is empty, and rows
+ * that an earlier group has are left out of a later one. strideW == 0 reads one
+ * matrix for every group. E <= 1024. Any element-aligned pointers and leading
  * dimensions work; operands whose rows (or strideW) are not multiples of 16
  * bytes are first copied into the per-stream workspace. Y must not overlap X or
  * W. Workspace, capture and device status as for sgemm().

@@ -329,3 +329,59 @@ def test_from_a_new_host_thread():
     t.join()
     torch.cuda.synchronize()
     assert got == [0] and torch.equal(y, want)
+
+
+def test_overlapping_groups_take_each_row_once():
+    """Bounds that no caller means: every row belongs to the first group that
+    has it, however many claim it."""
+    e, t = 1024, 500
+    x, w = values((t, 32), torch.bfloat16, 1, True).cuda(), values((e, 24, 32), torch.bfloat16, 2, True).cuda()
+    off = torch.tensor([0, t] * (e // 2) + [0], dtype=torch.int32, device="cuda")
+    y = B.grouped_gemm(x, w, off)
+    assert torch.equal(y.float(), x.float() @ w[0].float().mT)
+    dw = B.grouped_wgrad(y, x, off, out_dtype=torch.float32)
+    assert torch.equal(dw[0], y.float().mT @ x.float()) and not bool(dw[1:].any())
+
+
+def test_fp32_operands_up_to_the_largest():
+    """Values beyond BF16's largest, and the smallest normal ones, keep their bits."""
+    most = torch.finfo(torch.float32).max
+    x = torch.tensor([[most, -most, 3.39e38, 1.2e-38]], device="cuda")
+    w = torch.eye(4, device="cuda") * 0.5
+    y = B.grouped_gemm(x, w[None].contiguous(), torch.tensor([0, 1], dtype=torch.int32, device="cuda"))
+    assert torch.equal(y[0, :3], x[0, :3] * 0.5)
+    assert abs(float(y[0, 3]) - 0.6e-38) < 1e-40
+
+
+def test_shares_the_workspace_with_the_other_products():
+    """Split-K flags, partial tiles and counters of one stream, call after call."""
+    a, b = values((256, 8192), torch.float32, 1, True).cuda(), values((8192, 256), torch.float32, 2, True).cuda()
+    want = (a.double() @ b.double()).float()
+    xb, off = a.bfloat16(), torch.tensor([0, 100, 256], dtype=torch.int32, device="cuda")
+    wb = b.mT.contiguous().bfloat16()[None].expand(2, 256, 8192)
+    s = torch.cuda.current_stream().cuda_stream
+    for _ in range(3):
+        for call in (B.sgemm, B.sgemm_3xtf32):
+            c = torch.empty(256, 256, device="cuda")
+            assert call(256, 256, 8192, 1.0, a.data_ptr(), 8192, b.data_ptr(), 256, 0.0, c.data_ptr(), 256, s) == 0
+            y = B.grouped_gemm(xb, wb, off, out_dtype=torch.float32)
+            assert torch.equal(c, want) and torch.equal(y, want)
+    assert B.sgemm_poll_device_status(s)[0] == 0
+
+
+def test_capture_needs_the_workspace():
+    x, w = values((40, 64), torch.bfloat16, 1).cuda(), values((2, 32, 64), torch.bfloat16, 2).cuda()
+    off = torch.tensor([0, 7, 40], dtype=torch.int32, device="cuda")
+    y = torch.zeros(40, 32, dtype=torch.bfloat16, device="cuda")
+    want = B.grouped_gemm(x, w, off)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            with pytest.raises(B.SgemmError) as e:
+                B.grouped_gemm(x, w, off, Y=y)
+    assert e.value.status == B.SGEMM_ERR_CAPTURE
+    B.grouped_gemm(x, w, off, Y=y, stream=s)
+    s.synchronize()
+    assert torch.equal(y, want)
