@@ -5,7 +5,7 @@
 //   coef = min(1, max_norm / (norm + 1e-6)),  out = g * coef
 //
 // Two launches a list of up to kTable tensors: the squares, then the scaling.
-// The tensors are cut into 16 KB pieces that start on 16-byte addresses
+// The tensors are cut into pieces of 16 or 32 KB that start on 16-byte addresses
 // (the elements before a tensor's first such address form its first, shorter
 // vector), dealt to the CTAs in turn. Squares are summed in FP32 over one
 // thread's share of a piece (16 or 32 values) and in FP64 beyond; every CTA of
@@ -32,10 +32,15 @@ int library_device_sms(int dev, int* sms);
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPiece = 16384;           // bytes of a piece
-constexpr int kVecs = kPiece / 16 / kThreads;  // 16-byte vectors per thread and piece
+// A piece is `vecs` 16-byte vectors a thread: 4 (16 KB), or, in the first pass
+// over at least kLarge bytes, 8: twice the bytes in flight (60 M FP32 values 44
+// against 50 us). In the second pass 8 need more registers than its CTAs have
+// (150 M values 312 against 306 us).
+constexpr long long kLarge = 64 << 20;
+constexpr int piece_bytes(int vecs) { return vecs * 16 * kThreads; }
+// CTAs resident per SM (64 and 51 registers a thread)
+constexpr int ctas_per_sm(int vecs) { return vecs == 8 ? 4 : 5; }
 constexpr int kTable = 1000;            // tensors per launch (they are kernel parameters)
-constexpr int kCtasPerSm = 5;             // resident (48 registers)
 
 struct Entry {
   const void* in;
@@ -137,8 +142,8 @@ __device__ __forceinline__ double block_sum(double v, double* buf) {
   return s;
 }
 
-template <int CAP>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+template <int CAP, int VECS>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(VECS))
     squares_kernel(const __grid_constant__ Table<CAP> t, double* sums) {
   __shared__ double buf[kThreads / 32];
   ptx::griddep_wait();
@@ -151,11 +156,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     const char* in = static_cast<const char*>(t.e[i].in);
     const int head = (int)(reinterpret_cast<uintptr_t>(in) & 15u) / es;
     const long long n = t.e[i].n;
-    const long long v0 = (long long)(at - t.first[i]) * (kPiece / 16) + threadIdx.x;
-    uint4 raw[kVecs];
-    bool whole[kVecs];
+    const long long v0 = (long long)(at - t.first[i]) * (VECS * kThreads) + threadIdx.x;
+    uint4 raw[VECS];
+    bool whole[VECS];
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
+    for (int j = 0; j < VECS; ++j) {
       const long long lo = (v0 + j * kThreads) * per - head;   // first element of the vector
       whole[j] = lo >= 0 && lo + per <= n;
       if (whole[j]) raw[j] = __ldg(reinterpret_cast<const uint4*>(in + lo * es));
@@ -163,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     float s = 0.f;
     float x[8];
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
+    for (int j = 0; j < VECS; ++j) {
       if (whole[j]) {
         unpack(raw[j], type, x);
 #pragma unroll
@@ -181,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       total += (double)s;
     } else if (s != 0.f) {
       // squares near the ends of FP32's range (or no numbers): in FP64
-      for (int j = 0; j < kVecs; ++j) {
+      for (int j = 0; j < VECS; ++j) {
         const long long lo = (v0 + j * kThreads) * per - head;
         for (int k = 0; k < per; ++k)
           if (lo + k >= 0 && lo + k < n) {
@@ -195,16 +200,39 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   if (threadIdx.x == 0) sums[blockIdx.x] = s;
 }
 
-template <int CAP>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+template <int CAP, int VECS>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(VECS))
     scale_kernel(const __grid_constant__ Table<CAP> t, const double* sums, int nsums,
                  float max_norm, float* norm) {
   __shared__ double buf[kThreads / 32];
   __shared__ float coef_s;
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
+  // from the end: what the first pass read last is still in L2 (400 M bf16
+  // values: 420 against 424 us)
+  int i = -1;
+  uint4 raw[VECS];
+  bool whole[VECS];
+  // loads the whole vectors of the piece that is `left` from the end
+  auto load = [&](unsigned left) {
+    const unsigned at = t.pieces - 1 - left;
+    i = find(t, at, i);
+    const int es = elem_size(t.type[i]), per = 16 / es;
+    const char* in = static_cast<const char*>(t.e[i].in);
+    const int head = (int)(reinterpret_cast<uintptr_t>(in) & 15u) / es;
+    const long long v0 = (long long)(at - t.first[i]) * (VECS * kThreads) + threadIdx.x;
+#pragma unroll
+    for (int j = 0; j < VECS; ++j) {
+      const long long lo = (v0 + j * kThreads) * per - head;
+      whole[j] = lo >= 0 && lo + per <= t.e[i].n;
+      if (whole[j]) raw[j] = *reinterpret_cast<const uint4*>(in + lo * es);
+    }
+  };
+  // the first piece is on its way while the norm is formed
+  const bool writes = t.count > 0 && t.e[0].out != nullptr;
+  if (writes && blockIdx.x < t.pieces) load(blockIdx.x);
   double v = 0.0;
-  for (int i = threadIdx.x; i < nsums; i += kThreads) v += __ldcg(sums + i);
+  for (int k = threadIdx.x; k < nsums; k += kThreads) v += __ldcg(sums + k);
   v = block_sum(v, buf);
   if (threadIdx.x == 0) {
     const float nrm = (float)sqrt(v);
@@ -215,31 +243,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   }
   __syncthreads();
   const float coef = coef_s;
-  if (coef == 1.f && t.in_place) return;
-  // from the end: what the first pass read last is still in L2 (400 M bf16
-  // values: 420 against 424 us)
-  int i = -1;
+  if (!writes || (coef == 1.f && t.in_place)) return;
   for (unsigned left = blockIdx.x; left < t.pieces; left += gridDim.x) {
+    if (left != blockIdx.x) load(left);
     const unsigned at = t.pieces - 1 - left;
-    i = find(t, at, i);
     const int type = t.type[i], es = elem_size(type), per = 16 / es;
     const char* in = static_cast<const char*>(t.e[i].in);
     char* out = static_cast<char*>(t.e[i].out);
-    if (out == nullptr || (coef == 1.f && out == in)) continue;
+    if (coef == 1.f && out == in) continue;
     const int head = (int)(reinterpret_cast<uintptr_t>(in) & 15u) / es;
     const bool same = ((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
     const long long n = t.e[i].n;
-    const long long v0 = (long long)(at - t.first[i]) * (kPiece / 16) + threadIdx.x;
-    uint4 raw[kVecs];
-    bool whole[kVecs];
+    const long long v0 = (long long)(at - t.first[i]) * (VECS * kThreads) + threadIdx.x;
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-      const long long lo = (v0 + j * kThreads) * per - head;
-      whole[j] = lo >= 0 && lo + per <= n;
-      if (whole[j]) raw[j] = *reinterpret_cast<const uint4*>(in + lo * es);
-    }
-#pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
+    for (int j = 0; j < VECS; ++j) {
       const long long lo = (v0 + j * kThreads) * per - head;
       if (whole[j]) {
         float x[8];
@@ -263,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 }
 
 template <int CAP>
-Table<CAP> fill(int from, int to, const void* const* in, void* const* out, const long long* sizes,
+Table<CAP> fill(int vecs, int from, int to, const void* const* in, void* const* out, const long long* sizes,
                 const int* types) {
   Table<CAP> t;
   t.count = 0;
@@ -277,7 +294,7 @@ Table<CAP> fill(int from, int to, const void* const* in, void* const* out, const
     t.in_place = t.in_place && out != nullptr && out[i] == in[i];
     t.first[t.count] = pieces;
     t.type[t.count] = (unsigned char)types[i];
-    pieces += (unsigned)((bytes + kPiece - 1) / kPiece);
+    pieces += (unsigned)((bytes + piece_bytes(vecs) - 1) / piece_bytes(vecs));
     ++t.count;
   }
   t.pieces = pieces;
@@ -322,7 +339,7 @@ SGEMM_API int sgemm_grad_clip(int n, const void* const* grads, void* const* out,
     if ((reinterpret_cast<uintptr_t>(grads[i]) & mask) ||
         (out != nullptr && (reinterpret_cast<uintptr_t>(out[i]) & mask)))
       return SGEMM_ERR_MISALIGNED;
-    bytes += sizes[i] * (types[i] == SGEMM_TYPE_F32 ? 4 : 2) + kPiece;
+    bytes += sizes[i] * (types[i] == SGEMM_TYPE_F32 ? 4 : 2) + piece_bytes(4);
     if (bytes > (1LL << 44)) return SGEMM_ERR_INVALID_DIM;   // the piece numbers are 32 bits
   }
   if (reinterpret_cast<uintptr_t>(norm) & 3u) return SGEMM_ERR_MISALIGNED;
@@ -336,52 +353,45 @@ SGEMM_API int sgemm_grad_clip(int n, const void* const* grads, void* const* out,
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
 
   const int lists = n > 0 ? (n + kTable - 1) / kTable : 1;
-  const int per_list = sms * kCtasPerSm;
+  const int wide = bytes >= kLarge ? 8 : 4;   // vectors a piece of the first pass
+  const size_t most = (size_t)lists * sms * ctas_per_sm(4);
   float* ws = nullptr;
   int* status = nullptr;
-  st = library_workspace(dev, stream, (size_t)lists * per_list * 2, 0, &ws, &status, nullptr,
-                         nullptr);
+  st = library_workspace(dev, stream, most * 2, 0, &ws, &status, nullptr, nullptr);
   if (st != SGEMM_OK) return st;
   double* sums = reinterpret_cast<double*>(ws);
   // the first launches write their sums one list after another
   int nsums = 0;
-  auto each = [&](auto&& fn) -> cudaError_t {
-    for (int l = 0; l < lists; ++l) {
-      const int from = l * kTable, to = from + kTable < n ? from + kTable : n;
-      const cudaError_t e = fn(from, to);
-      if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+  auto grid_of = [&](unsigned pieces, int vecs) {
+    const unsigned fit = (unsigned)(sms * ctas_per_sm(vecs));
+    return pieces < 1 ? 1 : (int)(pieces < fit ? pieces : fit);
   };
-  auto grid_of = [&](unsigned pieces) {
-    return pieces < 1 ? 1 : (pieces < (unsigned)per_list ? (int)pieces : per_list);
-  };
-  cudaError_t e = each([&](int from, int to) {
-    cudaError_t r;
-    if (to - from <= 64) {
-      const auto t = fill<64>(from, to, grads, out, sizes, types);
-      const int grid = grid_of(t.pieces);
-      r = launch(squares_kernel<64>, grid, stream, t, sums + nsums);
-      nsums += grid;
-    } else {
-      const auto t = fill<kTable>(from, to, grads, out, sizes, types);
-      const int grid = grid_of(t.pieces);
-      r = launch(squares_kernel<kTable>, grid, stream, t, sums + nsums);
-      nsums += grid;
-    }
+  auto squares = [&](const auto& t, auto* kernel) {
+    const int grid = grid_of(t.pieces, wide);
+    const cudaError_t r = launch(kernel, grid, stream, t, sums + nsums);
+    nsums += grid;
     return r;
-  });
-  if (e == cudaSuccess)
-    e = each([&](int from, int to) {
+  };
+  auto scale = [&](const auto& t, auto* kernel) {
+    return launch(kernel, out == nullptr ? 1 : grid_of(t.pieces, 4), stream, t,
+                  (const double*)sums, nsums, max_norm, norm);
+  };
+  cudaError_t e = cudaSuccess;
+  for (int pass = 0; pass < 2; ++pass)
+    for (int l = 0; l < lists && e == cudaSuccess; ++l) {
+      const int from = l * kTable, to = from + kTable < n ? from + kTable : n;
+      const int vecs = pass == 0 ? wide : 4;
       if (to - from <= 64) {
-        const auto t = fill<64>(from, to, grads, out, sizes, types);
-        return launch(scale_kernel<64>, out == nullptr ? 1 : grid_of(t.pieces), stream, t,
-                      (const double*)sums, nsums, max_norm, norm);
+        const auto t = fill<64>(vecs, from, to, grads, out, sizes, types);
+        e = pass == 0 ? squares(t, wide == 8 ? squares_kernel<64, 8> : squares_kernel<64, 4>)
+                      : scale(t, scale_kernel<64, 4>);
+      } else {
+        const auto t = fill<kTable>(vecs, from, to, grads, out, sizes, types);
+        e = pass == 0
+                ? squares(t, wide == 8 ? squares_kernel<kTable, 8> : squares_kernel<kTable, 4>)
+                : scale(t, scale_kernel<kTable, 4>);
       }
-      const auto t = fill<kTable>(from, to, grads, out, sizes, types);
-      return launch(scale_kernel<kTable>, out == nullptr ? 1 : grid_of(t.pieces), stream, t,
-                    (const double*)sums, nsums, max_norm, norm);
-    });
+    }
   if (e != cudaSuccess) {
     cudaGetLastError();
     return SGEMM_ERR_LAUNCH;
