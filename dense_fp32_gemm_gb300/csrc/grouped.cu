@@ -32,102 +32,120 @@ namespace {
 
 // One operand to copy: rows of `bytes` bytes at pitch ld (matrices at `stride`)
 // from any address, to rows one after another at pitch ldo, a multiple of 16
-// bytes.
+// bytes. `lanes` threads copy a segment of a row at a time, each some 16-byte
+// pieces of it.
 struct Pack {
   const unsigned char* src;
   unsigned char* dst;
-  long long ld, stride, ldo, total;   // total: 16-byte pieces of all rows
+  long long ld, stride, ldo, total;   // total: segments of all rows
   const unsigned char* end;           // of the last row
-  int rows, bytes;
+  int rows, bytes, segments;          // segments: of a row
+  int lanes;                          // 4 .. 32: as many as a short row needs
 };
+constexpr int kPackThreads = 256;
+// Pieces of a thread, all loaded before the first is stored. Copies: 4 (25 MB in
+// rows of 1554 bytes with their product 23.6 us, 24.6 with 2; the copy is some
+// 9 us of it, 5.6 TB/s read and written). Widened ones write twice what they read
+// and are best at 1 (2000 and 4096 rows of 1001 bytes with their product 35.3 us;
+// 2: 36.0, 4: 37.6).
+__host__ __device__ constexpr int pack_pieces(bool widen) { return widen ? 1 : 4; }
 
-// 16 bytes from any address of the operand: by the widest loads that its
-// alignment allows, or, at odd addresses, from the two aligned 16-byte words
-// they lie in (where both are inside the operand). At even addresses the two
-// words and the shift took longer: 13.0 against 11.9 us for 16000 rows of 1554
-// bytes.
-__device__ __forceinline__ uint4 load16(const unsigned char* s, const Pack& p) {
-  union {
-    uint4 v;
-    unsigned long long d[2];
-    uint32_t w[4];
-    uint16_t h[8];
-    unsigned char b[16];
-  } u;
-  const unsigned a = (unsigned)reinterpret_cast<uintptr_t>(s);
-  if ((a & 15u) == 0) {
-    u.v = __ldg(reinterpret_cast<const uint4*>(s));
-  } else if ((a & 7u) == 0) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) u.d[i] = __ldg(reinterpret_cast<const unsigned long long*>(s) + i);
-  } else if ((a & 3u) == 0) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) u.w[i] = __ldg(reinterpret_cast<const uint32_t*>(s) + i);
-  } else if ((a & 1u) == 0) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) u.h[i] = __ldg(reinterpret_cast<const uint16_t*>(s) + i);
-  } else if (s - (a & 15u) >= p.src && s - (a & 15u) + 32 <= p.end) {
-    const uint4* w = reinterpret_cast<const uint4*>(s - (a & 15u));
-    const uint4 x = __ldg(w), y = __ldg(w + 1);
-    const uint32_t in[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-    uint32_t f[6], g[5];
-#pragma unroll
-    for (int i = 0; i < 6; ++i) f[i] = a & 8u ? in[i + 2] : in[i];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) g[i] = a & 4u ? f[i + 1] : f[i];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) u.w[i] = __funnelshift_r(g[i], g[i + 1], (a & 3u) * 8u);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) u.b[i] = __ldg(s + i);
-  }
-  return u.v;
+// Bytes a .. a + 15 of the 32 bytes x, y (W = a / 4).
+template <int W>
+__device__ __forceinline__ uint4 window(const uint4& x, const uint4& y, unsigned a) {
+  const uint32_t in[9] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, 0u};
+  const unsigned sh = (a & 3u) * 8u;
+  return make_uint4(
+      __funnelshift_r(in[W], in[W + 1], sh), __funnelshift_r(in[W + 1], in[W + 2], sh),
+      __funnelshift_r(in[W + 2], in[W + 3], sh), __funnelshift_r(in[W + 3], in[W + 4], sh));
 }
 
-// Copies a and then b (either may have no pieces), WIDEN: 8-bit integers as F16
-// (two 16-byte words a piece). What lies between a row's end and the end of its
-// last piece is set to zero, the rest of its pitch is not set.
+// Copies a and then b (either may have no segments), WIDEN: 8-bit integers as
+// F16 (two 16-byte words a piece). What lies between a row's end and the end of
+// its last piece is set to zero, the rest of its pitch is not set. A piece at
+// an odd address comes from the two aligned words it lies in, one shift for all
+// of a segment.
 template <bool WIDEN>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kPackThreads)
     pack_kernel(const __grid_constant__ Pack a, const __grid_constant__ Pack b) {
   // may start before the kernel ahead on the stream has finished
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < a.total + b.total;
-       i += gridDim.x * 256ll) {
-    const bool first = i < a.total;
+  constexpr int kPieces = pack_pieces(WIDEN);
+  // the threads of a first, then those of b
+  const long long threads = gridDim.x * (long long)kPackThreads;
+  const long long of_a = a.total * a.lanes, all = of_a + b.total * b.lanes;
+  for (long long i = blockIdx.x * (long long)kPackThreads + threadIdx.x; i < all; i += threads) {
+    const bool first = i < of_a;
     const Pack& p = first ? a : b;
-    const long long piece = first ? i : i - a.total;
-    const int chunks = (p.bytes + 15) / 16;   // per row
-    long long r;
-    int c;
-    if (piece < 0x7fffffff) {                 // (a 64-bit division takes far longer)
-      r = (int)piece / chunks;
-      c = ((int)piece - (int)r * chunks) * 16;
+    const int shift = __ffs(p.lanes) - 1;
+    const long long unit = (first ? i : i - of_a) >> shift;
+    const int lane = (int)(first ? i : i - of_a) & (p.lanes - 1);
+    const int step = 16 * p.lanes;             // bytes between a thread's pieces
+    long long r, mat;
+    int seg;
+    if (unit < 0x7fffffff) {                  // (a 64-bit division takes far longer)
+      r = (int)unit / p.segments;
+      seg = (int)unit - (int)r * p.segments;
+      mat = p.stride == 0 ? 0 : (int)r / p.rows;
     } else {
-      r = piece / chunks;
-      c = (int)(piece - r * chunks) * 16;
+      r = unit / p.segments;
+      seg = (int)(unit - r * p.segments);
+      mat = p.stride == 0 ? 0 : r / p.rows;
     }
-    const long long mat = p.stride == 0 ? 0 : (r < 0x7fffffff ? (int)r / p.rows : r / p.rows);
-    const unsigned char* s = p.src + mat * p.stride + (r - mat * p.rows) * p.ld + c;
-    uint4 v;
-    if (c + 16 <= p.bytes) {
-      v = load16(s, p);
-    } else {
-      uint32_t w[4] = {0u, 0u, 0u, 0u};
+    const int c0 = seg * kPieces * step + lane * 16;   // the thread's first piece: byte of the row
+    const unsigned char* s = p.src + mat * p.stride + (r - mat * p.rows) * p.ld + c0;
+    const unsigned at = (unsigned)reinterpret_cast<uintptr_t>(s) & 15u;   // (a segment's lanes agree)
+    const unsigned char* base = s - at;
+    uint4 x[kPieces], y[kPieces];
+    bool inside[kPieces];                     // both words lie in the operand
 #pragma unroll
-      for (int k = 0; k < 16; ++k)
-        if (c + k < p.bytes) w[k >> 2] |= (uint32_t)s[k] << (8 * (k & 3));
-      v = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int j = 0; j < kPieces; ++j) {
+      const unsigned char* w = base + step * j;
+      inside[j] = c0 + step * j < p.bytes && w >= p.src && w + (at ? 32 : 16) <= p.end;
+      if (inside[j]) {
+        x[j] = __ldg(reinterpret_cast<const uint4*>(w));
+        if (at) y[j] = __ldg(reinterpret_cast<const uint4*>(w) + 1);
+      }
     }
-    if (WIDEN) {
-      const uint2 e = i8_to_f16(v.x), f = i8_to_f16(v.y), g = i8_to_f16(v.z), h = i8_to_f16(v.w);
-      uint4* o = reinterpret_cast<uint4*>(p.dst + r * p.ldo + 2 * c);
-      o[0] = make_uint4(e.x, e.y, f.x, f.y);
-      // (a row's pitch is a multiple of 8 F16 values, not always of 16)
-      if (2 * c + 16 < p.ldo) o[1] = make_uint4(g.x, g.y, h.x, h.y);
-    } else {
-      *reinterpret_cast<uint4*>(p.dst + r * p.ldo + c) = v;
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const int c = c0 + step * j;
+      if (c >= p.bytes) break;
+      uint32_t w[4];
+      if (inside[j]) {
+        uint4 v = x[j];
+        switch (at >> 2) {
+          case 0: if (at) v = window<0>(x[j], y[j], at); break;
+          case 1: v = window<1>(x[j], y[j], at); break;
+          case 2: v = window<2>(x[j], y[j], at); break;
+          default: v = window<3>(x[j], y[j], at); break;
+        }
+        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+        if (c + 16 > p.bytes) {               // the row's end
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int n = p.bytes - c - 4 * k;   // valid bytes from this word on
+            w[k] &= n >= 4 ? 0xffffffffu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u);
+          }
+        }
+      } else {                                // at the operand's ends: byte by byte
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = 0u;
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (c + k < p.bytes) w[k >> 2] |= (uint32_t)s[step * j + k] << (8 * (k & 3));
+      }
+      if (WIDEN) {
+        const uint2 e = i8_to_f16(w[0]), f = i8_to_f16(w[1]), g = i8_to_f16(w[2]),
+                    h = i8_to_f16(w[3]);
+        uint4* o = reinterpret_cast<uint4*>(p.dst + r * p.ldo + 2 * c);
+        o[0] = make_uint4(e.x, e.y, f.x, f.y);
+        // (a row's pitch is a multiple of 8 F16 values, not always of 16)
+        if (2 * c + 16 < p.ldo) o[1] = make_uint4(g.x, g.y, h.x, h.y);
+      } else {
+        *reinterpret_cast<uint4*>(p.dst + r * p.ldo + c) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
   }
 }
@@ -149,11 +167,16 @@ cudaError_t pack_operands(Operand* a, void* dst_a, Operand* b, void* dst_b, bool
     p[i].ld = op.ld * op.elem;
     p[i].stride = op.batch > 1 ? op.stride * op.elem : 0;
     p[i].ldo = op.packed_pitch(widen);
-    p[i].total = op.rows * op.batch * ((bytes + 15) / 16);
+    p[i].lanes = 4;
+    const int per_lane = 16 * pack_pieces(widen);
+    while (p[i].lanes < 32 && p[i].lanes * per_lane < bytes) p[i].lanes *= 2;
+    const int segment = p[i].lanes * per_lane;
+    p[i].segments = (int)((bytes + segment - 1) / segment);
+    p[i].total = op.rows * op.batch * p[i].segments;
     p[i].end = p[i].src + (op.batch - 1) * p[i].stride + (op.rows - 1) * p[i].ld + bytes;
     p[i].rows = (int)op.rows;
     p[i].bytes = (int)bytes;
-    total += p[i].total;
+    total += p[i].total * p[i].lanes;
     if (widen) op.elem = 2;
     op.ptr = dsts[i];
     op.ld = p[i].ldo / op.elem;
@@ -163,9 +186,9 @@ cudaError_t pack_operands(Operand* a, void* dst_a, Operand* b, void* dst_b, bool
   cudaLaunchAttribute la[1];
   la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   la[0].val.programmaticStreamSerializationAllowed = 1;
-  const long long blocks = (total + 255) / 256;
+  const long long blocks = (total + kPackThreads - 1) / kPackThreads;
   lc.gridDim = dim3((unsigned)(blocks < sms * 32ll ? blocks : sms * 32ll));
-  lc.blockDim = dim3(256);
+  lc.blockDim = dim3(kPackThreads);
   lc.stream = stream;
   lc.attrs = la;
   lc.numAttrs = 1;

@@ -385,3 +385,12 @@ def test_capture_needs_the_workspace():
     B.grouped_gemm(x, w, off, Y=y, stream=s)
     s.synchronize()
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("op", ["T", "N"])
+def test_copied_rows_from_every_address(t, op):
+    """Operands at every element offset and pitch within 16 bytes, rows that end inside a copied piece."""
+    for r in range(8):
+        run_rows(op, TYPES[t], TYPES[t], [20, 0, 45], 61 + r, 500 + 3 * r, ints=True,
+                 pads=(r, (3 * r) % 8, r % 3), offs=(r, 7 - r, 0))

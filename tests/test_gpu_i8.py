@@ -175,3 +175,14 @@ def test_every_tile(form, m):
     finally:
         assert B.sgemm_grouped_set_tile(0) == 0
     assert torch.equal(got, exact_sum(a, b).float())
+
+
+@pytest.mark.parametrize("m", [40, 600])
+@pytest.mark.parametrize("k", [37, 1100])
+def test_every_byte_alignment(m, k):
+    """Start addresses and pitches of every remainder by 16, one row a piece longer than the last."""
+    sa, sb = torch.ones(m, device="cuda"), torch.ones(130, device="cuda")
+    for r in range(16):
+        a, da = ints((m, k), r, k + r, 16 - r)
+        b, db = ints((130, k), 100 + r, k + (5 * r) % 16, r)
+        assert torch.equal(B.i8_gemm(da, sa, db, sb, out_dtype=torch.float32), exact_sum(a, b).float())
