@@ -11,6 +11,12 @@
 // thread's share of a piece (16 or 32 values) and in FP64 beyond; every CTA of
 // the second launch adds the first one's per-CTA sums in the same order, so
 // the result does not depend on timing.
+//
+// Bound by HBM: the gradients are read twice (the norm is not known before all of
+// them have been) and written once, or read once where nothing is clipped.
+// 400 M BF16 values: 392 us, 6.1 TB/s of 2.4 GB (measured copy: 6.78 TB/s);
+// 60 M FP32 values below the bound: 45 us, 5.3 TB/s; 48 tensors of 1 M FP32
+// values in all: 10.7 us a call, the two launches.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -208,8 +214,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(VECS))
   __shared__ float coef_s;
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  // from the end: what the first pass read last is still in L2 (400 M bf16
-  // values: 420 against 424 us)
+  // from the end: what the first pass read last is still in L2 (1 % of the call
+  // at 400 M bf16 values)
   int i = -1;
   uint4 raw[VECS];
   bool whole[VECS];

@@ -110,7 +110,11 @@ __device__ __forceinline__ void put_16(const Raw<E>& r, const E* x, float s, flo
 
 // A row per block. Of a row up to kHeld groups of 16 values a thread stay in
 // registers between the two passes (the maximum, the quotients); the rest of a
-// longer row is read again. A call has to read X and write Q once.
+// longer row is read again. A call has to read X and write Q once: 50 MB for
+// 4096 x 4096 BF16 values, 18 us under the profiler (14 instructions a value, a
+// third of the issue slots; the row's chain of load, maximum and store is the
+// rest). Fewer registers a thread for more rows in flight spill: 22.2 against
+// 23.8 us for 133 x 1000 with its product. A row per warp took 37 us.
 constexpr int kHeld = 2;
 template <typename E, bool V>
 __global__ void __launch_bounds__(kThreads)

@@ -46,14 +46,28 @@
 // depend on the order of arrival -- no CTA waits for another. (Dealing out all
 // tiles by slices would balance sums of different lengths exactly, but
 // spreads the workers over all groups at once: the weight gradient of 8 groups
-// of 1024 x (4096 + 1024) took ten times as long, its tiles no longer shared
-// in L2.)
+// of 1024 x (4096 + 1024) took 996 us that way against 141 in waves, at the
+// same step of the work, its tiles no longer shared in L2.)
 //
 // Roles: warp 0 issues the TMA loads (both CTAs of a pair signal the even
 // one's barriers), warp 1 the MMAs (in the odd CTA it reports the stages that
 // threads write there: conversions, cleared rows), warps 4-11 read the
 // accumulators (two warps per lane quarter, each half of the columns) and
 // write the output, warps 12-19 (kF32, kI8) convert.
+//
+// Measured on GB300 (graphs of calls, operands larger than L2 but where noted;
+// peaks: copy 6.78 TB/s, library BF16 product 1945 TFLOP/s):
+//   256 x 2, BF16, 8192 rows in 8 groups, 4096 x 4096: 190 us, 1450 TFLOP/s; with
+//     K = 16384 the rate is 1680. Between them: the first wave's fill, the
+//     epilogues that nothing overlaps, the parts of the last tiles.
+//   16 x 1, BF16: weights of 320 MB stream at 6.2 TB/s. The weights that 16 rows
+//     choose of 32 of 1024 x 2048 (38 MB) take 13.7 us, DRAM's share 5.6: launch,
+//     scan and first loads are some 3 us, the exchange of the parts of cut
+//     tiles 2.5 us.
+//   kF32 128: a slice of 32 in 713 ns, 41 % of the tensor pipe: bound by the
+//     hand-offs between converters, tensor memory and MMAs, not by DRAM.
+//   kI8 16: a slice of 64 in 270 ns, bound by the converters' chain; kI8Wide: as
+//     k16, plus 19 us to widen 2 x 4096 x 4096.
 //
 // Every wait is bounded; a CTA that gives up drains its copies and MMAs,
 // frees its tensor memory and returns. Offsets are clamped to the row count,
@@ -112,9 +126,9 @@ struct Geo {
   static constexpr bool kConv = SRC == kF32 || SRC == kI8;
   static constexpr bool kInt = SRC == kI8 || SRC == kI8Wide;
   // A slice is kSub tiles of kSubK values of k, each [P | Q] in rows of kRawRow
-  // bytes. Narrow tiles take two: their MMAs are short, and the hand-offs of a
-  // stage (some 700 cycles of waits and issue in the producer and in the MMA
-  // warp) would bound the bytes they stream.
+  // bytes. Narrow tiles take two: four MMAs of 16 columns last 160 cycles, the
+  // waits and hand-offs of a stage some 270 more, which would bound the bytes
+  // they stream.
   static constexpr int kSubK = SRC == kF32 ? 32 : 64;
   static constexpr int kSub = BQ <= 32 ? 2 : 1;
   static constexpr int kSlice = kSub * kSubK;
@@ -275,14 +289,6 @@ struct Walk {
     return true;
   }
 };
-
-// The same value in every lane, told to the compiler (the reduction's result is
-// a uniform register): what the issue loops add up stays in the uniform
-// registers that the copy and tensor instructions read, instead of being moved
-// there for each of them (70 cycles an MMA).
-__device__ __forceinline__ int uniform(int v) {
-  return (int)__reduce_or_sync(0xffffffffu, (unsigned)v);
-}
 
 // Waits for a barrier's phase, at most timeout_ns: then the abort word is set,
 // the code recorded, and false returned. The clock is read only after some
@@ -653,7 +659,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
   // arrival or commit reaches them
   if (kPair) ptx::cluster_sync();
   tc::fence_after_sync();
-  const uint32_t tmem = (uint32_t)uniform((int)sh->tmem);
+  const uint32_t tmem = sh->tmem;
   if (kPair) {
     if (tid == 0) {
       // the MMAs of the pair write the same tensor-memory address in both CTAs
@@ -682,10 +688,10 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
       const bool p_mn = p.p_mn, q_mn = p.q_mn, wgrad = p.wgrad;
       Unit w;
       for (List list(p, sh, worker, workers); ok && list.next(w);) {
-        const int p0 = uniform(w.p0 + rank * BP), q0 = uniform(w.q0 + rank * G::kRows);
-        const int pe = uniform(wgrad || p.p_shared ? 0 : w.e), qrow = uniform(wgrad ? 0 : w.row0 + q0);
-        const int kb = uniform(w.kb), ke = uniform(w.ke), clear_at = uniform(w.clear);
-        int k = uniform(w.kb * SL + (wgrad ? w.row0 : 0));
+        const int p0 = w.p0 + rank * BP, q0 = w.q0 + rank * G::kRows;
+        const int pe = wgrad || p.p_shared ? 0 : w.e, qrow = wgrad ? 0 : w.row0 + q0;
+        const int kb = w.kb, ke = w.ke, clear_at = w.clear;
+        int k = w.kb * SL + (wgrad ? w.row0 : 0);
         for (int ks = kb; ks < ke; ++ks, ++it, k += SL) {
           ok = wait_for(ptx::smem_addr(&sh->raw_empty[be]), phase, abort_w, p.status,
                         kDevTimeoutEmpty, p.timeout_ns);
@@ -831,8 +837,8 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     const int chunk = p.chunk / SL;
     Unit w;
     for (List list(p, sh, worker, workers); ok && list.next(w);) {
-      const int kb = uniform(w.kb), ke = uniform(w.ke), clear_at = uniform(w.clear);
-      const int klen = uniform(w.klen);
+      const int kb = w.kb, ke = w.ke, clear_at = w.clear;
+      const int klen = w.klen;
       for (int k0 = kb; k0 < ke && ok; k0 += chunk, ++acc) {
         const int buf = acc & 1;
         const uint32_t d = tmem + (uint32_t)(buf * BQ);
