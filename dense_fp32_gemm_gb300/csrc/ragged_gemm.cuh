@@ -50,8 +50,8 @@
 // same step of the work, its tiles no longer shared in L2.)
 //
 // Roles: warp 0 issues the TMA loads (both CTAs of a pair signal the even
-// one's barriers), warp 1 the MMAs (in the odd CTA it reports the stages that
-// threads write there: conversions, cleared rows), warps 4-11 read the
+// one's barriers), warp 1 the MMAs (in a pair only the even CTA's), warp 2 clears
+// rows that belong to the next group (weight gradients), warps 4-11 read the
 // accumulators (two warps per lane quarter, each half of the columns) and
 // write the output, warps 12-19 (kF32, kI8) convert.
 //
@@ -189,6 +189,7 @@ constexpr int kExactK = 1024;
 struct Shared {
   uint64_t raw_full[24], raw_empty[24];
   uint64_t op_full[8], op_empty[8];
+  uint64_t tail_full[12];       // stages that end past their group: loaded, not yet cleared
   uint64_t peer_full[12];       // even CTA of a pair: the odd CTA's stage has been cleared
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain, epi_sync;
@@ -541,8 +542,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
   constexpr uint32_t kAll = 0xffffffffu;
 
   if (tid == 0) {
-    // pair form: the even CTA's MMA warp waits on the stages of both CTAs
-    // (cleared ones: its own, and one relayed arrival for the odd CTA's), and
+    // pair form: the even CTA's MMA warp waits on the stages of both CTAs, and
     // on the epilogue warps of both; its commits arrive in both
     for (int s = 0; s < RB; ++s) {
       ptx::mbar_init(ptx::smem_addr(&sh->raw_full[s]), 1);
@@ -553,7 +553,10 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
         ptx::mbar_init(ptx::smem_addr(&sh->op_full[s]), G::kGroupWarps);
         ptx::mbar_init(ptx::smem_addr(&sh->op_empty[s]), 1);
       }
-      if (kPair) ptx::mbar_init(ptx::smem_addr(&sh->peer_full[s]), 1);
+      if (!G::kConv) {
+        ptx::mbar_init(ptx::smem_addr(&sh->tail_full[s]), 1);
+        ptx::mbar_init(ptx::smem_addr(&sh->peer_full[s]), 1);
+      }
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(ptx::smem_addr(&sh->acc_full[i]), 1);
@@ -682,7 +685,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
       // uses of a stage pass at once, on barriers that nothing has used)
       int be = RB == RS ? 0 : RS;
       uint32_t phase = 1;
-      uint32_t own_phase = 0;   // odd CTA: phases of its own raw_full barriers (a bit each)
+      uint32_t tail_phase = 0;  // phases of the tail_full barriers (a bit each)
       bool ok = true;
       constexpr int BOX = G::kRawRow / G::kElem;  // elements along the fast dimension of a box
       const bool p_mn = p.p_mn, q_mn = p.q_mn, wgrad = p.wgrad;
@@ -699,13 +702,13 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
           if (!ok) break;
           // pair: the even CTA's barrier counts the bytes of both (the odd
           // CTA's loads may complete before it expects them), but for a stage
-          // that the odd CTA has to clear. (A remote arrival for each of the
-          // odd CTA's stages took its producer 1300 cycles.)
+          // that is to be cleared. (A remote arrival for each of the odd CTA's
+          // stages took its producer 1300 cycles.)
           const bool clear = kQmn && !G::kConv && ks == clear_at;
           const bool remote = kPair && rank != 0 && !clear;
-          if (kPair && rank != 0 && clear) own_phase ^= 1u << s;
+          if (clear) tail_phase ^= 1u << s;
           if (ptx::elect_one()) {
-            uint32_t fb = ptx::smem_addr(&sh->raw_full[bf]);
+            uint32_t fb = ptx::smem_addr(clear ? &sh->tail_full[s] : &sh->raw_full[bf]);
             const uint32_t st = raw_base_addr + (uint32_t)(s * G::kRaw);
             if (remote)
               fb = ptx::mapa(fb, 0u);
@@ -752,10 +755,11 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
       // stages issued
       const uint64_t t0 = ptx::global_ns();
       for (int j = it - 1; j >= 0 && j >= it - RS; --j) {
-        // (odd CTA: its own barriers only carry the stages that are cleared;
-        // the others have landed once the even CTA's MMAs have read them)
-        const uint32_t fb = ptx::smem_addr(&sh->raw_full[j % RB]);
-        const uint32_t par = kPair && rank != 0 ? (own_phase >> (j % RS) & 1u) ^ 1u
+        // (odd CTA: only stages that are cleared have a barrier here; the others
+        // have landed once the even CTA's MMAs have read them)
+        const uint32_t fb = ptx::smem_addr(kPair && rank != 0 ? &sh->tail_full[j % RS]
+                                                              : &sh->raw_full[j % RB]);
+        const uint32_t par = kPair && rank != 0 ? (tail_phase >> (j % RS) & 1u) ^ 1u
                                                 : (uint32_t)((j / RB) & 1);
         while (!ptx::mbar_try_wait(fb, par))
           if ((long long)(ptx::global_ns() - t0) > cleanup_bound_ns(p.timeout_ns)) break;
@@ -771,8 +775,52 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
       }
       __syncwarp();
     }
-    // ---- warp 1: MMA issuer (even CTA of a pair), or relay (odd CTA) --------------
-    if (warp == 1) {
+    // ---- warp 2: clears the rows past a group's end (weight gradients) -------------
+    // A slice that ends inside a 16-row step has rows of the next group in it, up
+    // to that step's end (the steps beyond are not issued). They are set to zero
+    // in both operands (what they hold may be no number) here, ahead of the MMAs:
+    // in the MMA warp a tile's last slice cost it 0.7 to 1.1 us (8 groups of 1009
+    // x (4096 + 1024): 64.1 us, of 1008: 56.9).
+    if (!G::kConv && kQmn && warp == 2 && p.wgrad) {
+      int it = 0;
+      uint32_t tail_phase = 0;
+      bool ok = true;
+      Unit w;
+      for (List list(p, sh, worker, workers); ok && list.next(w);) {
+        it += w.ke - w.kb;
+        if (w.ke == w.kb || w.ke - 1 != w.clear) continue;
+        const int s = (it - 1) % RS, rem = w.klen - w.clear * SL;
+        const uint32_t par = tail_phase >> s & 1u;
+        tail_phase ^= 1u << s;
+        ok = wait_for(ptx::smem_addr(&sh->tail_full[s]), par, abort_w, p.status, kDevTimeoutFull,
+                      p.timeout_ns);
+        ok = __all_sync(kAll, ok);
+        if (!ok) break;
+        unsigned char* rows = base + s * G::kRaw + rem * 128;
+        const int n = (cdiv(rem, 16) * 16 - rem) * 8;
+        for (int i = lane; i < n; i += 32) {
+#pragma unroll
+          for (int box = 0; box < (BP + G::kRows) / 64; ++box)
+            *reinterpret_cast<uint4*>(rows + box * (SL * 128) + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        ptx::fence_proxy_async_shared();
+        __syncwarp();
+        if (rank != 0) {
+          if (lane == 0)
+            ptx::mbar_arrive_remote(ptx::mapa(ptx::smem_addr(&sh->peer_full[s]), 0u));
+        } else {
+          if (kPair) {
+            ok = wait_for_pair(ptx::smem_addr(&sh->peer_full[s]), par, abort_w, p.status,
+                               kDevTimeoutFull, p.timeout_ns);
+            ok = __all_sync(kAll, ok);
+            if (!ok) break;
+          }
+          if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&sh->raw_full[s]));
+        }
+      }
+    }
+    // ---- warp 1: MMA issuer (even CTA of a pair) -----------------------------------
+    if (warp == 1 && rank == 0) {
     // operand tiles: K-major rows of 128 bytes (64 for kF32) in 8-row groups;
     // MN-major chunks of 64 elements x SL rows of k, 128 bytes a row. The
     // descriptors of stage 0 are made once; a stage, a part or a k-step moves
@@ -830,87 +878,49 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     };
     int acc = 0, s = 0;
     uint32_t phase = 0;       // parity of the full barriers to wait for
-    // phases (a bit per stage) of the barriers that only cleared stages use:
-    // the odd CTA's raw_full, the even one's peer_full
-    uint32_t own_phase = 0;
     bool issued_any = false, ok = true;
     const int chunk = p.chunk / SL;
     Unit w;
     for (List list(p, sh, worker, workers); ok && list.next(w);) {
-      const int kb = w.kb, ke = w.ke, clear_at = w.clear;
-      const int klen = w.klen;
+      const int kb = w.kb, ke = w.ke, klen = w.klen;
       for (int k0 = kb; k0 < ke && ok; k0 += chunk, ++acc) {
         const int buf = acc & 1;
         const uint32_t d = tmem + (uint32_t)(buf * BQ);
-        if (rank == 0) {
-          const uint32_t eb = ptx::smem_addr(&sh->acc_empty[buf]);
-          const uint32_t par = (uint32_t)((acc >> 1) & 1) ^ 1u;
-          ok = kPair ? wait_for_pair(eb, par, abort_w, p.status, kDevTimeoutSync, p.timeout_ns)
-                     : wait_for(eb, par, abort_w, p.status, kDevTimeoutSync, p.timeout_ns);
+        const uint32_t eb = ptx::smem_addr(&sh->acc_empty[buf]);
+        const uint32_t par = (uint32_t)((acc >> 1) & 1) ^ 1u;
+        ok = kPair ? wait_for_pair(eb, par, abort_w, p.status, kDevTimeoutSync, p.timeout_ns)
+                   : wait_for(eb, par, abort_w, p.status, kDevTimeoutSync, p.timeout_ns);
+        ok = __all_sync(kAll, ok);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const int k1 = min(ke, k0 + chunk);
+        for (int ks = k0; ks < k1; ++ks) {
+          const int rem = klen - ks * SL;   // > 0
+          ok = wait_for(ptx::smem_addr(G::kConv ? &sh->op_full[s] : &sh->raw_full[s]), phase,
+                        abort_w, p.status, kDevTimeoutFull, p.timeout_ns);
           ok = __all_sync(kAll, ok);
           if (!ok) break;
           tc::fence_after_sync();
-        }
-        const int k1 = min(ke, k0 + chunk);
-        for (int ks = k0; ks < k1; ++ks) {
-          const bool clear = kQmn && !G::kConv && ks == clear_at;
-          const int rem = klen - ks * SL;   // > 0
-          const uint32_t bit = 1u << s;
-          if (!kPair || rank == 0 || clear) {
-            const uint32_t par = kPair && rank != 0 ? (own_phase & bit) != 0 : phase;
-            ok = wait_for(ptx::smem_addr(G::kConv ? &sh->op_full[s] : &sh->raw_full[s]), par,
-                          abort_w, p.status, kDevTimeoutFull, p.timeout_ns);
-            ok = __all_sync(kAll, ok);
-            if (!ok) break;
-          }
-          if (clear) {
-            // clear the rows of k past the group's end in both operands up to
-            // the end of their 16-row step (the steps beyond are not issued)
-            unsigned char* stp = base + s * G::kRaw;
-            const int nz = cdiv(rem, 16) * 16 - rem;
-            constexpr int kBoxes = (BP + G::kRows) / 64;
-            for (int i = lane; i < kBoxes * nz * 8; i += 32) {
-              const int box = i / (nz * 8), r = i - box * nz * 8;
-              *reinterpret_cast<uint4*>(stp + box * (SL * 128) + rem * 128 + r * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
-            }
-            ptx::fence_proxy_async_shared();
-            __syncwarp();
-          }
-          if (rank != 0) {
-            if (clear && lane == 0)
-              ptx::mbar_arrive_remote(ptx::mapa(ptx::smem_addr(&sh->peer_full[s]), 0u));
-          } else {
-            if (kPair && clear) {
-              // the odd CTA has cleared its rows
-              ok = wait_for_pair(ptx::smem_addr(&sh->peer_full[s]), (own_phase & bit) != 0, abort_w,
-                                 p.status, kDevTimeoutFull, p.timeout_ns);
-              ok = __all_sync(kAll, ok);
-              if (!ok) break;
-            }
-            tc::fence_after_sync();
-            if (ptx::elect_one()) {
-              const uint32_t add = ks == k0 ? 0u : 1u;
-              if (rem >= SL) {
+          if (ptx::elect_one()) {
+            const uint32_t add = ks == k0 ? 0u : 1u;
+            if (rem >= SL) {
 #pragma unroll
-                for (int kk = 0; kk < SL / 16; ++kk) step(d, s, kk, kk == 0 ? add : 1u);
-              } else {
+              for (int kk = 0; kk < SL / 16; ++kk) step(d, s, kk, kk == 0 ? add : 1u);
+            } else {
 #pragma unroll 1
-                for (int kk = 0; kk * 16 < rem; ++kk) step(d, s, kk, kk == 0 ? add : 1u);
-              }
-              commit(G::kConv ? &sh->op_empty[s] : &sh->raw_empty[s]);
+              for (int kk = 0; kk * 16 < rem; ++kk) step(d, s, kk, kk == 0 ? add : 1u);
             }
-            __syncwarp();
-            issued_any = true;
+            commit(G::kConv ? &sh->op_empty[s] : &sh->raw_empty[s]);
           }
-          if (kPair && clear) own_phase ^= bit;
+          __syncwarp();
+          issued_any = true;
           if (++s == OS) {
             s = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        if (rank == 0 && ptx::elect_one()) commit(&sh->acc_full[buf]);
+        if (ptx::elect_one()) commit(&sh->acc_full[buf]);
         __syncwarp();
       }
     }

@@ -394,3 +394,13 @@ def test_copied_rows_from_every_address(t, op):
     for r in range(8):
         run_rows(op, TYPES[t], TYPES[t], [20, 0, 45], 61 + r, 500 + 3 * r, ints=True,
                  pads=(r, (3 * r) % 8, r % 3), offs=(r, 7 - r, 0))
+
+
+@pytest.mark.parametrize("tile", FORMS, indirect=True, ids=str)
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("counts", [[300, 20, 0, 700, 65, 128, 1, 300], [3000, 1, 1, 1, 64, 2, 2], [5, 900, 901, 3],
+                                    list(range(0, 130, 2)) + [1000] + [1] * 70], ids=len)
+def test_wgrad_many_tiles_of_different_lengths(tile, t, counts):
+    """More tiles than the workers of any form, groups of very different lengths: every element once, whoever adds it."""
+    m, n = (1030, 2050) if len(counts) < 50 else (130, 264)
+    run_wgrad(TYPES[t], torch.float32, counts, m, n, ints=True)
