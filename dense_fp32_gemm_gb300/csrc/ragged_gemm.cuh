@@ -678,8 +678,8 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
 
   if (warp < kEpiWarp0) {
     if (G::kMoveRegs) ptx::regs_lower<G::kRegsFew>();
-    // ---- warp 0: TMA producer ---------------------------------------------------
-    if (warp == 0) {
+    // ---- warp 0: TMA producer, one thread of it -----------------------------------
+    if (warp == 0 && ptx::elect_one()) {
       int it = 0, s = 0, bf = 0;            // stage and barrier to fill
       // the stage's last use: its barrier, and the parity to wait for (first
       // uses of a stage pass at once, on barriers that nothing has used)
@@ -698,7 +698,6 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
         for (int ks = kb; ks < ke; ++ks, ++it, k += SL) {
           ok = wait_for(ptx::smem_addr(&sh->raw_empty[be]), phase, abort_w, p.status,
                         kDevTimeoutEmpty, p.timeout_ns);
-          ok = __all_sync(kAll, ok);
           if (!ok) break;
           // pair: the even CTA's barrier counts the bytes of both (the odd
           // CTA's loads may complete before it expects them), but for a stage
@@ -707,42 +706,39 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
           const bool clear = kQmn && !G::kConv && ks == clear_at;
           const bool remote = kPair && rank != 0 && !clear;
           if (clear) tail_phase ^= 1u << s;
-          if (ptx::elect_one()) {
-            uint32_t fb = ptx::smem_addr(clear ? &sh->tail_full[s] : &sh->raw_full[bf]);
-            const uint32_t st = raw_base_addr + (uint32_t)(s * G::kRaw);
-            if (remote)
-              fb = ptx::mapa(fb, 0u);
+          uint32_t fb = ptx::smem_addr(clear ? &sh->tail_full[s] : &sh->raw_full[bf]);
+          const uint32_t st = raw_base_addr + (uint32_t)(s * G::kRaw);
+          if (remote)
+            fb = ptx::mapa(fb, 0u);
+          else
+            ptx::mbar_arrive_expect_tx(
+                fb, (uint32_t)(kPair && !clear ? 2 * G::kRaw : G::kRaw));
+          auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, int z) {
+            if (kPair)
+              ptx::tma_load_3d_pair(dst, map, x, y, z, fb);
             else
-              ptx::mbar_arrive_expect_tx(
-                  fb, (uint32_t)(kPair && !clear ? 2 * G::kRaw : G::kRaw));
-            auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, int z) {
-              if (kPair)
-                ptx::tma_load_3d_pair(dst, map, x, y, z, fb);
-              else
-                ptx::tma_load_3d(dst, map, x, y, z, fb);
-            };
+              ptx::tma_load_3d(dst, map, x, y, z, fb);
+          };
 #pragma unroll
-            for (int sub = 0; sub < G::kSub; ++sub) {
-              const int ksub = k + sub * G::kSubK;
-              const uint32_t at = st + (uint32_t)(sub * G::kRawSub);
-              if (p_mn) {
+          for (int sub = 0; sub < G::kSub; ++sub) {
+            const int ksub = k + sub * G::kSubK;
+            const uint32_t at = st + (uint32_t)(sub * G::kRawSub);
+            if (p_mn) {
 #pragma unroll
-                for (int i = 0; i < BP / BOX; ++i)
-                  load(at + (uint32_t)(i * G::kSubK * G::kRawRow), &mapP, p0 + i * BOX, ksub, pe);
-              } else {
-                load(at, &mapP, ksub, p0, pe);
-              }
-              if (kQmn && q_mn) {
+              for (int i = 0; i < BP / BOX; ++i)
+                load(at + (uint32_t)(i * G::kSubK * G::kRawRow), &mapP, p0 + i * BOX, ksub, pe);
+            } else {
+              load(at, &mapP, ksub, p0, pe);
+            }
+            if (kQmn && q_mn) {
 #pragma unroll
-                for (int i = 0; i < G::kRows / BOX; ++i)
-                  load(at + (uint32_t)(G::kRawP + i * G::kSubK * G::kRawRow), &mapQ, q0 + i * BOX,
-                       ksub, 0);
-              } else {
-                load(at + G::kRawP, &mapQ, ksub, qrow, 0);
-              }
+              for (int i = 0; i < G::kRows / BOX; ++i)
+                load(at + (uint32_t)(G::kRawP + i * G::kSubK * G::kRawRow), &mapQ, q0 + i * BOX,
+                     ksub, 0);
+            } else {
+              load(at + G::kRawP, &mapQ, ksub, qrow, 0);
             }
           }
-          __syncwarp();
           if (++s == RS) s = 0;
           if (++bf == RB) bf = 0;
           if (++be == RB) {
@@ -773,8 +769,8 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
             if ((long long)(ptx::global_ns() - t0) > cleanup_bound_ns(p.timeout_ns)) break;
         }
       }
-      __syncwarp();
     }
+    __syncwarp();
     // ---- warp 2: clears the rows past a group's end (weight gradients) -------------
     // A slice that ends inside a 16-row step has rows of the next group in it, up
     // to that step's end (the steps beyond are not issued). They are set to zero
@@ -819,8 +815,8 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
         }
       }
     }
-    // ---- warp 1: MMA issuer (even CTA of a pair) -----------------------------------
-    if (warp == 1 && rank == 0) {
+    // ---- warp 1: MMA issuer (even CTA of a pair), one thread of it ------------------
+    if (warp == 1 && rank == 0 && ptx::elect_one()) {
     // operand tiles: K-major rows of 128 bytes (64 for kF32) in 8-row groups;
     // MN-major chunks of 64 elements x SL rows of k, 128 bytes a row. The
     // descriptors of stage 0 are made once; a stage, a part or a k-step moves
@@ -890,7 +886,6 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
         const uint32_t par = (uint32_t)((acc >> 1) & 1) ^ 1u;
         ok = kPair ? wait_for_pair(eb, par, abort_w, p.status, kDevTimeoutSync, p.timeout_ns)
                    : wait_for(eb, par, abort_w, p.status, kDevTimeoutSync, p.timeout_ns);
-        ok = __all_sync(kAll, ok);
         if (!ok) break;
         tc::fence_after_sync();
         const int k1 = min(ke, k0 + chunk);
@@ -898,21 +893,17 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
           const int rem = klen - ks * SL;   // > 0
           ok = wait_for(ptx::smem_addr(G::kConv ? &sh->op_full[s] : &sh->raw_full[s]), phase,
                         abort_w, p.status, kDevTimeoutFull, p.timeout_ns);
-          ok = __all_sync(kAll, ok);
           if (!ok) break;
           tc::fence_after_sync();
-          if (ptx::elect_one()) {
-            const uint32_t add = ks == k0 ? 0u : 1u;
-            if (rem >= SL) {
+          const uint32_t add = ks == k0 ? 0u : 1u;
+          if (rem >= SL) {
 #pragma unroll
-              for (int kk = 0; kk < SL / 16; ++kk) step(d, s, kk, kk == 0 ? add : 1u);
-            } else {
+            for (int kk = 0; kk < SL / 16; ++kk) step(d, s, kk, kk == 0 ? add : 1u);
+          } else {
 #pragma unroll 1
-              for (int kk = 0; kk * 16 < rem; ++kk) step(d, s, kk, kk == 0 ? add : 1u);
-            }
-            commit(G::kConv ? &sh->op_empty[s] : &sh->raw_empty[s]);
+            for (int kk = 0; kk * 16 < rem; ++kk) step(d, s, kk, kk == 0 ? add : 1u);
           }
-          __syncwarp();
+          commit(G::kConv ? &sh->op_empty[s] : &sh->raw_empty[s]);
           issued_any = true;
           if (++s == OS) {
             s = 0;
@@ -920,26 +911,21 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
           }
         }
         if (!ok) break;
-        if (ptx::elect_one()) commit(&sh->acc_full[buf]);
-        __syncwarp();
+        commit(&sh->acc_full[buf]);
       }
     }
-    const bool aborted = __any_sync(kAll, *abort_w != 0);
-    if (aborted && issued_any) {
+    if (*abort_w != 0 && issued_any) {
       // wait (bounded) until every MMA issued has completed
-      if (ptx::elect_one()) {
-        if (kPair)
-          tc::commit_pair(ptx::smem_addr(&sh->drain));
-        else
-          tc::commit(ptx::smem_addr(&sh->drain));
-      }
-      __syncwarp();
+      if (kPair)
+        tc::commit_pair(ptx::smem_addr(&sh->drain));
+      else
+        tc::commit(ptx::smem_addr(&sh->drain));
       const uint64_t t0 = ptx::global_ns();
       while (!ptx::mbar_try_wait(ptx::smem_addr(&sh->drain), 0u))
         if ((long long)(ptx::global_ns() - t0) > cleanup_bound_ns(p.timeout_ns)) break;
     }
-    __syncwarp();
     }
+    __syncwarp();
   } else if (G::kConv && warp >= kConvWarp0) {
     // ---- converters: raw tiles -> operand tiles ----------------------------------
     if (G::kMoveRegs) ptx::regs_lower<G::kRegsConv>();
