@@ -57,15 +57,16 @@
 //
 // Measured on GB300 (graphs of calls, operands larger than L2 but where noted;
 // peaks: copy 6.78 TB/s, library BF16 product 1945 TFLOP/s):
-//   256 x 2, BF16, 8192 rows in 8 groups, 4096 x 4096: 190 us, 1450 TFLOP/s; with
-//     K = 16384 the rate is 1680. Between them: the first wave's fill, the
-//     epilogues that nothing overlaps, the parts of the last tiles.
+//   256 x 2, BF16, 8192 rows in 8 groups, 4096 x 4096: 174 us in short bursts,
+//     1580 TFLOP/s (tensor pipe 80 % of active cycles), 199 under sustained
+//     power. The rest: ragged edges, the first wave's fill, the parts of the
+//     last tiles. Half the loads from L2 would gain 1-2 %.
 //   16 x 1, BF16: weights of 320 MB stream at 6.2 TB/s. The weights that 16 rows
-//     choose of 32 of 1024 x 2048 (38 MB) take 13.7 us, DRAM's share 5.6: launch,
+//     choose of 32 of 1024 x 2048 (38 MB) take 13.2 us, DRAM's share 5.6: launch,
 //     scan and first loads are some 3 us, the exchange of the parts of cut
 //     tiles 2.5 us.
-//   kF32 128: a slice of 32 in 713 ns, 41 % of the tensor pipe: bound by the
-//     hand-offs between converters, tensor memory and MMAs, not by DRAM.
+//   kF32 128: 2048 rows in 8 groups, 1024 x 2048: 62 us, tensor pipe 48 %: bound by
+//     the hand-offs between converters, tensor memory and MMAs, not by DRAM.
 //   kI8 16: a slice of 64 in 270 ns, bound by the converters' chain; kI8Wide: as
 //     k16, plus 19 us to widen 2 x 4096 x 4096.
 //
