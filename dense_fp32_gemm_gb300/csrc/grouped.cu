@@ -269,19 +269,19 @@ const FormEntry* find_form(int dev, int sms, int src, int bq, int cl, int* worke
 }
 
 // What a tile of each width costs on a worker, in ns: a slice of 64 values of k
-// (measured on GB300, 8192 x 4096 x 4096 over 8 groups for 16-bit operands, one
-// wave of tiles for the others) and its epilogue.
+// (measured on GB300: 8192 x 4096 x 4096 over 8 groups for 16-bit operands, 8192
+// x 2048 x 4096 for FP32, one wave of tiles for integers) and its epilogue.
 struct TileCost {
   int src, bq, cl, slice, epilogue;
 };
 constexpr TileCost kTileCosts[] = {
-    {k16, 16, 1, 200, 600},    {k16, 32, 1, 205, 700},   {k16, 64, 1, 335, 1100},
-    {k16, 128, 1, 342, 1300},  {k16, 256, 1, 415, 2000}, {k16, 256, 2, 390, 2500},
-    {kF32, 16, 1, 490, 600},   {kF32, 32, 1, 500, 700},  {kF32, 64, 1, 1200, 1100},
-    {kF32, 128, 1, 1500, 1300},
+    {k16, 16, 1, 181, 600},    {k16, 32, 1, 184, 700},   {k16, 64, 1, 280, 1100},
+    {k16, 128, 1, 282, 1300},  {k16, 256, 1, 403, 2000}, {k16, 256, 2, 364, 2500},
+    {kF32, 16, 1, 800, 600},   {kF32, 32, 1, 810, 700},  {kF32, 64, 1, 1080, 1100},
+    {kF32, 128, 1, 1300, 1300},
     {kI8, 16, 1, 270, 600},    {kI8, 32, 1, 275, 700},   {kI8, 64, 1, 425, 1100},
     {kI8, 128, 1, 460, 1300},
-    {kI8Wide, 256, 2, 390, 2500},
+    {kI8Wide, 256, 2, 364, 2500},
 };
 // What cutting a tile along k costs, ns: publishing a part and the rendezvous,
 // and reading one part back (a load of L2 for every 32 columns of a warp; four
