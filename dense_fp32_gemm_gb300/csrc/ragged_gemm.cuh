@@ -92,6 +92,11 @@ enum OutType : int { kOutF32 = 0, kOutBf16 = 1, kOutF16 = 2 };
 
 constexpr int BP = 128;            // tile height in p (MMA M)
 constexpr int kMaxGroups = 1024;   // the scanned offsets live in shared memory
+// Slices by which one that has to be cleared is loaded early. Between a pair's
+// CTAs the clearing takes longer than the loads are ahead of the MMAs (8 groups of
+// 1000 x (4096 + 1024): 57.1 us with 0, 53.4 with 2, 52.8 with 3); a single CTA, with fewer
+// stages, loses more by the one that is held (256 columns: 55.5 and 58.6 us).
+__host__ __device__ constexpr int early_slices(int cl) { return cl == 2 ? 3 : 0; }
 constexpr int kEpiWarp0 = 4, kEpiWarps = 8, kEpiThreads = kEpiWarps * 32;
 constexpr int kConvWarp0 = kEpiWarp0 + kEpiWarps, kConvWarps = 8;
 
@@ -220,7 +225,9 @@ struct Unit {
   int e, p0, q0;       // group, first p, first q within the group
   int row0, nq;        // first token row of the group; valid q in the tile
   int kb, ke, klen;    // slices of this unit, contraction length
-  int clear;           // wgrad: the slice whose last rows belong to the next group, or -1
+  // wgrad: the last slice (whose rows are partly the next group's, to be cleared)
+  // is loaded as number `early` of the unit's, the MMAs read it last; else -1
+  int early;
   int c0, parts;       // workers c0 .. c0 + parts - 1 share the tile
 };
 
@@ -287,7 +294,9 @@ struct Walk {
     u.klen = p.K == 0 ? 0 : (p.wgrad ? n : p.K);
     if (u.klen == 0) u.ke = u.kb;   // nothing to add
     // a sum that ends inside a 16-row step of its last slice
-    u.clear = p.wgrad && (u.klen & 15) ? u.klen / SLICE : -1;
+    constexpr int kEarly = early_slices(CL);
+    const int n_k = u.ke - u.kb;
+    u.early = p.wgrad && (u.klen & 15) && n_k > 0 && u.ke == slices ? max(0, n_k - 1 - kEarly) : -1;
     return true;
   }
 };
@@ -526,6 +535,8 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
   // and wider
   constexpr bool kQmn = BQ >= 64;
   static_assert(!kPair || !G::kConv, "pairs read their tiles as TMA wrote them");
+  constexpr bool kReorder = kQmn && !G::kConv && early_slices(CL) > 0;
+  static_assert(RS > early_slices(CL), "a slice loaded early keeps its stage");
   constexpr uint16_t kBoth = 0x3;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw_addr = ptx::smem_addr(smem_raw);
@@ -694,9 +705,11 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
       for (List list(p, sh, worker, workers); ok && list.next(w);) {
         const int p0 = w.p0 + rank * BP, q0 = w.q0 + rank * G::kRows;
         const int pe = wgrad || p.p_shared ? 0 : w.e, qrow = wgrad ? 0 : w.row0 + q0;
-        const int kb = w.kb, ke = w.ke, clear_at = w.clear;
-        int k = w.kb * SL + (wgrad ? w.row0 : 0);
-        for (int ks = kb; ks < ke; ++ks, ++it, k += SL) {
+        const int n = w.ke - w.kb, early = kQmn && !G::kConv ? w.early : -1;
+        const int first_k = w.kb * SL + (wgrad ? w.row0 : 0);
+        for (int i = 0, next = 0; i < n; ++i, ++it) {
+          const bool clear = i == early;
+          const int k = first_k + (clear ? n - 1 : next++) * SL;
           ok = wait_for(ptx::smem_addr(&sh->raw_empty[be]), phase, abort_w, p.status,
                         kDevTimeoutEmpty, p.timeout_ns);
           if (!ok) break;
@@ -704,7 +717,6 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
           // CTA's loads may complete before it expects them), but for a stage
           // that is to be cleared. (A remote arrival for each of the odd CTA's
           // stages took its producer 1300 cycles.)
-          const bool clear = kQmn && !G::kConv && ks == clear_at;
           const bool remote = kPair && rank != 0 && !clear;
           if (clear) tail_phase ^= 1u << s;
           uint32_t fb = ptx::smem_addr(clear ? &sh->tail_full[s] : &sh->raw_full[bf]);
@@ -776,17 +788,17 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     // A slice that ends inside a 16-row step has rows of the next group in it, up
     // to that step's end (the steps beyond are not issued). They are set to zero
     // in both operands (what they hold may be no number) here, ahead of the MMAs:
-    // in the MMA warp a tile's last slice cost it 0.7 to 1.1 us (8 groups of 1009
-    // x (4096 + 1024): 64.1 us, of 1008: 56.9).
+    // in the MMA warp a tile's last slice cost 0.7 to 1.1 us (8 groups of 1009
+    // x (4096 + 1024) 64.1 us, of 1008 56.9; here 52.9 and 50.5).
     if (!G::kConv && kQmn && warp == 2 && p.wgrad) {
       int it = 0;
       uint32_t tail_phase = 0;
       bool ok = true;
       Unit w;
       for (List list(p, sh, worker, workers); ok && list.next(w);) {
+        const int s = (it + w.early) % RS, rem = w.klen - (w.ke - 1) * SL;
         it += w.ke - w.kb;
-        if (w.ke == w.kb || w.ke - 1 != w.clear) continue;
-        const int s = (it - 1) % RS, rem = w.klen - w.clear * SL;
+        if (w.early < 0) continue;
         const uint32_t par = tail_phase >> s & 1u;
         tail_phase ^= 1u << s;
         ok = wait_for(ptx::smem_addr(&sh->tail_full[s]), par, abort_w, p.status, kDevTimeoutFull,
@@ -879,7 +891,9 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     const int chunk = p.chunk / SL;
     Unit w;
     for (List list(p, sh, worker, workers); ok && list.next(w);) {
-      const int kb = w.kb, ke = w.ke, klen = w.klen;
+      const int kb = w.kb, ke = w.ke, klen = w.klen, early = w.early;
+      int early_s = 0, after_s = 0;
+      uint32_t early_phase = 0, after_phase = 0;
       for (int k0 = kb; k0 < ke && ok; k0 += chunk, ++acc) {
         const int buf = acc & 1;
         const uint32_t d = tmem + (uint32_t)(buf * BQ);
@@ -892,6 +906,22 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
         const int k1 = min(ke, k0 + chunk);
         for (int ks = k0; ks < k1; ++ks) {
           const int rem = klen - ks * SL;   // > 0
+          if (kReorder && early >= 0) {
+            if (ks == kb + early) {         // step over the slice loaded early ...
+              early_s = s;
+              early_phase = phase;
+              if (++s == OS) {
+                s = 0;
+                phase ^= 1u;
+              }
+            }
+            if (ks == ke - 1) {             // ... and come back to it
+              after_s = s;
+              after_phase = phase;
+              s = early_s;
+              phase = early_phase;
+            }
+          }
           ok = wait_for(ptx::smem_addr(G::kConv ? &sh->op_full[s] : &sh->raw_full[s]), phase,
                         abort_w, p.status, kDevTimeoutFull, p.timeout_ns);
           if (!ok) break;
@@ -906,7 +936,10 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
           }
           commit(G::kConv ? &sh->op_empty[s] : &sh->raw_empty[s]);
           issued_any = true;
-          if (++s == OS) {
+          if (kReorder && early >= 0 && ks == ke - 1) {
+            s = after_s;
+            phase = after_phase;
+          } else if (++s == OS) {
             s = 0;
             phase ^= 1u;
           }
