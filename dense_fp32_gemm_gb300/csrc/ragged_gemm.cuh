@@ -58,11 +58,11 @@
 // Measured on GB300 (graphs of calls, operands larger than L2 but where noted;
 // peaks: copy 6.78 TB/s, library BF16 product 1945 TFLOP/s):
 //   256 x 2, BF16, 8192 rows in 8 groups, 4096 x 4096: 174 us in short bursts,
-//     1580 TFLOP/s (tensor pipe 80 % of active cycles), 199 under sustained
+//     1580 TFLOP/s (tensor pipe 80 % of active cycles), 202 under sustained
 //     power. The rest: ragged edges, the first wave's fill, the parts of the
 //     last tiles. Half the loads from L2 would gain 1-2 %.
 //   16 x 1, BF16: weights of 320 MB stream at 6.2 TB/s. The weights that 16 rows
-//     choose of 32 of 1024 x 2048 (38 MB) take 13.2 us, DRAM's share 5.6: launch,
+//     choose of 32 of 1024 x 2048 (38 MB) take 13.6 us, DRAM's share 5.6: launch,
 //     scan and first loads are some 3 us, the exchange of the parts of cut
 //     tiles 2.5 us.
 //   kF32 128: 2048 rows in 8 groups, 1024 x 2048: 62 us, tensor pipe 48 %: bound by
