@@ -58,14 +58,14 @@
 // Measured on GB300 (graphs of calls, operands larger than L2 but where noted;
 // peaks: copy 6.78 TB/s, library BF16 product 1945 TFLOP/s):
 //   256 x 2, BF16, 8192 rows in 8 groups, 4096 x 4096: 174 us in short bursts,
-//     1580 TFLOP/s (tensor pipe 80 % of active cycles), 202 under sustained
+//     1580 TFLOP/s (tensor pipe 80 % of active cycles), 195 under sustained
 //     power. The rest: ragged edges, the first wave's fill, the parts of the
 //     last tiles. Half the loads from L2 would gain 1-2 %.
 //   16 x 1, BF16: weights of 320 MB stream at 6.2 TB/s. The weights that 16 rows
-//     choose of 32 of 1024 x 2048 (38 MB) take 13.6 us, DRAM's share 5.6: launch,
+//     choose of 32 of 1024 x 2048 (38 MB) take 13.8 us, DRAM's share 5.6: launch,
 //     scan and first loads are some 3 us, the exchange of the parts of cut
 //     tiles 2.5 us.
-//   kF32 128: 2048 rows in 8 groups, 1024 x 2048: 62 us, tensor pipe 48 %: bound by
+//   kF32 128: 2048 rows in 8 groups, 1024 x 2048: 63 us, tensor pipe 48 %: bound by
 //     the hand-offs between converters, tensor memory and MMAs, not by DRAM.
 //   kI8 16: a slice of 64 in 270 ns, bound by the converters' chain; kI8Wide: as
 //     k16, plus 19 us to widen 2 x 4096 x 4096.
@@ -224,6 +224,7 @@ __device__ __forceinline__ int tile_slices(const Params& p, int rows) {
 struct Unit {
   int e, p0, q0;       // group, first p, first q within the group
   int row0, nq;        // first token row of the group; valid q in the tile
+  int nn;              // columns the MMAs compute: nq rounded up
   int kb, ke, klen;    // slices of this unit, contraction length
   // wgrad: the last slice (whose rows are partly the next group's, to be cleared)
   // is loaded as number `early` of the unit's, the MMAs read it last; else -1
@@ -291,6 +292,7 @@ struct Walk {
     u.p0 = tp * (BP * CL);
     u.q0 = (j - tp * qt) * BQ;
     u.nq = min(BQ, qdim - u.q0);
+    u.nn = min(BQ, cdiv(u.nq, 16 * CL) * (16 * CL));
     u.klen = p.K == 0 ? 0 : (p.wgrad ? n : p.K);
     if (u.klen == 0) u.ke = u.kb;   // nothing to add
     // a sum that ends inside a 16-row step of its last slice
@@ -703,7 +705,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
       const bool p_mn = p.p_mn, q_mn = p.q_mn, wgrad = p.wgrad;
       Unit w;
       for (List list(p, sh, worker, workers); ok && list.next(w);) {
-        const int p0 = w.p0 + rank * BP, q0 = w.q0 + rank * G::kRows;
+        const int p0 = w.p0 + rank * BP, q0 = w.q0 + rank * (w.nn / CL);
         const int pe = wgrad || p.p_shared ? 0 : w.e, qrow = wgrad ? 0 : w.row0 + q0;
         const int n = w.ke - w.kb, early = kQmn && !G::kConv ? w.early : -1;
         const int first_k = w.kb * SL + (wgrad ? w.row0 : 0);
@@ -839,8 +841,6 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     constexpr int OP_Q = G::kConv ? G::kOpQ : G::kRawQ;   // one part
     constexpr uint32_t kStage16 = (G::kConv ? G::kOp : G::kRaw) >> 4;
     const bool a_mn = !G::kConv && p.p_mn, b_mn = kQmn && p.q_mn;   // (tensor memory: K-major)
-    const uint32_t idesc =
-        tc::idesc_f16(BP * CL, BQ, SRC == kF32 || (SRC == k16 && p.bf16), a_mn, b_mn);
     auto desc = [](uint32_t addr, bool mn) {
       return mn ? tc::smem_desc(addr, G::kSubK * 128, 1024, true)
                 : tc::smem_desc(addr, 16, kNarrow ? 512 : 1024, !kNarrow);
@@ -850,7 +850,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     const uint32_t a_step = a_mn ? 2048u >> 4 : 32u >> 4, b_step = b_mn ? 2048u >> 4 : 32u >> 4;
     const uint32_t a_slots = tmem + 2 * BQ;      // P's converted parts
     // the MMAs of k-step kk of stage s
-    auto step = [&](uint32_t d, int s, int kk, uint32_t add) {
+    auto step = [&](uint32_t d, uint32_t idesc, int s, int kk, uint32_t add) {
       constexpr int kSteps = G::kSubK / 16;
       const int sub = kk / kSteps;
       kk -= sub * kSteps;
@@ -892,6 +892,11 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     Unit w;
     for (List list(p, sh, worker, workers); ok && list.next(w);) {
       const int kb = w.kb, ke = w.ke, klen = w.klen, early = w.early;
+      // A ragged tile's MMAs are as narrow as its rows (4096 rows over 16 groups,
+      // 4096 x 2048, under sustained power 78 against 84.6 us). Where converters
+      // set the pace that gains nothing.
+      const uint32_t idesc = tc::idesc_f16(BP * CL, G::kConv ? BQ : w.nn,
+                                           SRC == kF32 || (SRC == k16 && p.bf16), a_mn, b_mn);
       int early_s = 0, after_s = 0;
       uint32_t early_phase = 0, after_phase = 0;
       for (int k0 = kb; k0 < ke && ok; k0 += chunk, ++acc) {
@@ -929,10 +934,10 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
           const uint32_t add = ks == k0 ? 0u : 1u;
           if (rem >= SL) {
 #pragma unroll
-            for (int kk = 0; kk < SL / 16; ++kk) step(d, s, kk, kk == 0 ? add : 1u);
+            for (int kk = 0; kk < SL / 16; ++kk) step(d, idesc, s, kk, kk == 0 ? add : 1u);
           } else {
 #pragma unroll 1
-            for (int kk = 0; kk * 16 < rem; ++kk) step(d, s, kk, kk == 0 ? add : 1u);
+            for (int kk = 0; kk * 16 < rem; ++kk) step(d, idesc, s, kk, kk == 0 ? add : 1u);
           }
           commit(G::kConv ? &sh->op_empty[s] : &sh->raw_empty[s]);
           issued_any = true;
