@@ -58,7 +58,7 @@
 // Measured on GB300 (graphs of calls, operands larger than L2 but where noted;
 // peaks: copy 6.78 TB/s, library BF16 product 1945 TFLOP/s):
 //   256 x 2, BF16, 8192 rows in 8 groups, 4096 x 4096: 174 us in short bursts,
-//     1580 TFLOP/s (tensor pipe 80 % of active cycles), 195 under sustained
+//     1580 TFLOP/s (tensor pipe 73 to 80 % of active cycles), 195 under sustained
 //     power. The rest: ragged edges, the first wave's fill, the parts of the
 //     last tiles. Half the loads from L2 would gain 1-2 %.
 //   16 x 1, BF16: weights of 320 MB stream at 6.2 TB/s. The weights that 16 rows
