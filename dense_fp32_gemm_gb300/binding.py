@@ -415,7 +415,12 @@ def _ld(t, name):
         raise ValueError(f"{name} must be a 2-D float32 tensor")
     if t.size(1) > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must be row-major (unit stride along rows)")
-    return max(t.stride(0), max(t.size(1), 1)) if t.size(0) > 1 else max(t.size(1), 1)
+    least = max(t.size(1), 1)
+    if t.size(0) < 2 or t.numel() == 0:
+        return least
+    if t.stride(0) < least:
+        raise ValueError(f"{name} has overlapping rows (a row stride below the row length)")
+    return t.stride(0)
 
 
 def gemm(A, B, C, alpha=1.0, beta=0.0, stream=None):

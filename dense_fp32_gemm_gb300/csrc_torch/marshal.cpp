@@ -69,14 +69,17 @@ int to_int(int64_t v) {
   return (int)v;
 }
 
-// Row pitch of a row-major matrix (or of the matrices of a 3-D tensor).
+// Row pitch of a row-major matrix (or of the matrices of a 3-D tensor). Rows
+// that overlap (an expanded tensor's have stride 0) have no pitch that the
+// kernels take: read at the row length they would lie past the storage.
 int pitch(const at::Tensor& t, const char* name) {
-  const int64_t d = t.dim(), cols = t.size(d - 1);
+  const int64_t d = t.dim(), cols = t.size(d - 1), least = cols > 1 ? cols : 1;
   if (cols > 1 && t.stride(d - 1) != 1)
     throw Refusal{std::string(name) + " must be row-major (unit stride along rows)"};
-  int64_t p = cols > 1 ? cols : 1;
-  if (t.size(d - 2) > 1 && t.stride(d - 2) > p) p = t.stride(d - 2);
-  return to_int(p);
+  if (t.size(d - 2) < 2 || t.numel() == 0) return to_int(least);
+  if (t.stride(d - 2) < least)
+    throw Refusal{std::string(name) + " has overlapping rows (a row stride below the row length)"};
+  return to_int(t.stride(d - 2));
 }
 
 // Tensors of one call: on one CUDA device, which is made current; its stream.
@@ -161,7 +164,7 @@ PyObject* grouped_gemm(PyObject* const* a) {
   check(W.size(transposed ? 2 : 1) == K, "shape mismatch");
   check(W.scalar_type() == X.scalar_type(), "X and W must have one type");
   const int* bounds = offsets_of(off, E);
-  const int type = type_of(X, "X");
+  const int type = type_of(X, "X"), ldx = pitch(X, "X"), ldw = pitch(W, "W");
   at::Tensor Y;
   if (is_none(a[3])) {
     check(beta == 0.0, "beta needs Y");
@@ -173,11 +176,12 @@ PyObject* grouped_gemm(PyObject* const* a) {
     Y = tensor(a[3], "Y");
     check(Y.dim() == 2 && Y.size(0) == T && Y.size(1) == N, "shape mismatch");
   }
+  const int ldy = pitch(Y, "Y");
   const Launch on(a[8], {&X, &W, &off, &Y});
   const int st = fn.grouped(transposed ? 1 : 0, type, type_of(Y, "Y"), to_int(E), to_int(T),
-                            to_int(N), to_int(K), (float)alpha, X.data_ptr(), pitch(X, "X"),
-                            W.data_ptr(), pitch(W, "W"), E > 1 ? W.stride(0) : 0, bounds,
-                            (float)beta, Y.data_ptr(), pitch(Y, "Y"), on.handle());
+                            to_int(N), to_int(K), (float)alpha, X.data_ptr(), ldx, W.data_ptr(),
+                            ldw, E > 1 ? W.stride(0) : 0, bounds, (float)beta, Y.data_ptr(), ldy,
+                            on.handle());
   if (st != 0) throw Status{st, "sgemm_grouped"};
   return result(a[3], Y);
 }
@@ -191,7 +195,7 @@ PyObject* grouped_wgrad(PyObject* const* a) {
   const int64_t E = off.numel() - 1, T = A.size(0), M = A.size(1), N = B.size(1);
   check(E >= 0, "offsets must hold one bound more than there are groups");
   const int* bounds = offsets_of(off, E);
-  const int type = type_of(A, "A");
+  const int type = type_of(A, "A"), lda = pitch(A, "A"), ldb = pitch(B, "B");
   at::Tensor C;
   if (is_none(a[3])) {
     check(beta == 0.0, "beta needs C");
@@ -203,11 +207,11 @@ PyObject* grouped_wgrad(PyObject* const* a) {
     C = tensor(a[3], "C");
     check(C.dim() == 3 && C.size(0) == E && C.size(1) == M && C.size(2) == N, "shape mismatch");
   }
+  const int ldc = pitch(C, "C");
   const Launch on(a[7], {&A, &B, &off, &C});
   const int st = fn.wgrad(type, type_of(C, "C"), to_int(E), to_int(T), to_int(M), to_int(N),
-                          (float)alpha, A.data_ptr(), pitch(A, "A"), B.data_ptr(), pitch(B, "B"),
-                          bounds, (float)beta, C.data_ptr(), pitch(C, "C"),
-                          E > 1 ? C.stride(0) : 0, on.handle());
+                          (float)alpha, A.data_ptr(), lda, B.data_ptr(), ldb, bounds, (float)beta,
+                          C.data_ptr(), ldc, E > 1 ? C.stride(0) : 0, on.handle());
   if (st != 0) throw Status{st, "sgemm_grouped_wgrad"};
   return result(a[3], C);
 }
@@ -217,10 +221,10 @@ PyObject* i8_quantize(PyObject* const* a) {
   const at::Tensor& X = tensor(a[0], "X");
   check(X.dim() == 2, "X must be 2-D");
   const int64_t M = X.size(0), K = X.size(1);
-  const int type = type_of(X, "X");
-  check(X.is_cuda(), "tensors must be on one CUDA device");
+  const int type = type_of(X, "X"), ldx = pitch(X, "X");
   at::Tensor Q, scale;
   if (is_none(a[1])) {
+    check(X.is_cuda(), "tensors must be on one CUDA device");
     // rows padded to 16 bytes, so that sgemm_i8 reads them in place
     const int64_t ld = (K + 15) / 16 * 16;
     const auto options = X.options().dtype(at::kChar).requires_grad(false);
@@ -228,17 +232,20 @@ PyObject* i8_quantize(PyObject* const* a) {
   } else {
     Q = tensor(a[1], "Q");
   }
-  if (is_none(a[2]))
-    scale = at::empty({M}, X.options().dtype(at::kFloat).requires_grad(false));
-  else
-    scale = tensor(a[2], "scale");
   check(Q.scalar_type() == at::kChar && Q.dim() == 2 && Q.size(0) == M && Q.size(1) == K,
         "Q must be int8 of X's shape");
+  const int ldq = pitch(Q, "Q");
+  if (is_none(a[2])) {
+    check(X.is_cuda(), "tensors must be on one CUDA device");
+    scale = at::empty({M}, X.options().dtype(at::kFloat).requires_grad(false));
+  } else {
+    scale = tensor(a[2], "scale");
+  }
   vector_of(scale, M, "scale must be a contiguous float32 vector with one value a row");
   {
     const Launch on(a[3], {&X, &Q, &scale});
-    const int st = fn.quantize(to_int(M), to_int(K), type, X.data_ptr(), pitch(X, "X"),
-                               static_cast<signed char*>(Q.data_ptr()), pitch(Q, "Q"),
+    const int st = fn.quantize(to_int(M), to_int(K), type, X.data_ptr(), ldx,
+                               static_cast<signed char*>(Q.data_ptr()), ldq,
                                static_cast<float*>(scale.data_ptr()), on.handle());
     if (st != 0) throw Status{st, "sgemm_i8_quantize"};
   }
@@ -260,6 +267,7 @@ PyObject* i8_gemm(PyObject* const* a) {
   const int64_t M = A.size(0), K = A.size(1), N = B.size(0);
   vector_of(sa, M, "scaleA must be a contiguous float32 vector with a value for each row of A");
   vector_of(sb, N, "scaleB must be a contiguous float32 vector with a value for each row of B");
+  const int lda = pitch(A, "A"), ldb = pitch(B, "B");
   at::Tensor C;
   if (is_none(a[4])) {
     check(A.is_cuda(), "tensors must be on one CUDA device");
@@ -270,13 +278,14 @@ PyObject* i8_gemm(PyObject* const* a) {
     C = tensor(a[4], "C");
     check(C.dim() == 2 && C.size(0) == M && C.size(1) == N, "shape mismatch");
   }
+  const int ldc = pitch(C, "C");
   const Launch on(a[6], {&A, &sa, &B, &sb, &C});
   const int st = fn.i8(to_int(M), to_int(N), to_int(K),
-                       static_cast<const signed char*>(A.data_ptr()), pitch(A, "A"),
+                       static_cast<const signed char*>(A.data_ptr()), lda,
                        static_cast<const float*>(sa.data_ptr()),
-                       static_cast<const signed char*>(B.data_ptr()), pitch(B, "B"),
-                       static_cast<const float*>(sb.data_ptr()), type_of(C, "C"), C.data_ptr(),
-                       pitch(C, "C"), on.handle());
+                       static_cast<const signed char*>(B.data_ptr()), ldb,
+                       static_cast<const float*>(sb.data_ptr()), type_of(C, "C"), C.data_ptr(), ldc,
+                       on.handle());
   if (st != 0) throw Status{st, "sgemm_i8"};
   return result(a[4], C);
 }
