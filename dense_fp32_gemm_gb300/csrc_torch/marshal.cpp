@@ -82,6 +82,16 @@ int pitch(const at::Tensor& t, const char* name) {
   return to_int(t.stride(d - 2));
 }
 
+// The matrices of a 3-D result may lie one after another or row by row beside
+// each other; groups that write the same elements would race.
+void check_apart(const at::Tensor& t, int64_t ld) {
+  if (t.size(0) < 2 || t.numel() == 0) return;
+  const int64_t gap = t.stride(0), rows = t.size(1), cols = t.size(2);
+  check(gap >= (rows - 1) * ld + cols ||
+            (gap >= cols && (rows < 2 || ld >= (t.size(0) - 1) * gap + cols)),
+        "the groups' matrices in C overlap");
+}
+
 // Tensors of one call: on one CUDA device, which is made current; its stream.
 class Launch {
  public:
@@ -208,6 +218,7 @@ PyObject* grouped_wgrad(PyObject* const* a) {
     check(C.dim() == 3 && C.size(0) == E && C.size(1) == M && C.size(2) == N, "shape mismatch");
   }
   const int ldc = pitch(C, "C");
+  check_apart(C, ldc);
   const Launch on(a[7], {&A, &B, &off, &C});
   const int st = fn.wgrad(type, type_of(C, "C"), to_int(E), to_int(T), to_int(M), to_int(N),
                           (float)alpha, A.data_ptr(), lda, B.data_ptr(), ldb, bounds, (float)beta,

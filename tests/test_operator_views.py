@@ -72,3 +72,17 @@ def test_views_that_do_not_overlap_keep_their_pitch():
     for x in (mat(4, 8), mat(8, 16)[::2, 3:11], mat(1, 8).expand(1, 8)):
         with pytest.raises(ValueError, match="CUDA device"):
             B.grouped_gemm(x, torch.zeros(2, 6, 8), OFF)
+
+
+def test_wgrad_groups_that_share_elements():
+    a, b = mat(4, 8), mat(4, 6)
+    for c in (mat(8, 6).expand(2, 8, 6), torch.zeros(100).as_strided((2, 8, 6), (47, 6, 1)),
+              torch.zeros(200).as_strided((2, 8, 6), (5, 12, 1)), torch.zeros(200).as_strided((2, 8, 6), (6, 11, 1))):
+        with pytest.raises(ValueError, match="matrices in C overlap"):
+            B.grouped_wgrad(a, b, OFF, C=c)
+    # one after another, and row by row beside each other
+    for c in (torch.zeros(2, 8, 6), torch.zeros(8, 2, 6).transpose(0, 1), torch.zeros(2, 9, 7)[:, 1:, :6],
+              torch.zeros(1, 8, 6).expand(2, 8, 6)[:1]):
+        off = OFF if c.size(0) == 2 else OFF[:2]
+        with pytest.raises(ValueError, match="CUDA device"):
+            B.grouped_wgrad(a, b, off, C=c)
