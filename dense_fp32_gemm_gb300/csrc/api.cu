@@ -66,15 +66,23 @@ struct DeviceInfo {
 };
 std::map<int, DeviceInfo> g_devices;
 
-struct Workspace {
-  void* block = nullptr;
-  size_t bytes = 0;
+// One allocation: the status word, the flags behind it, the scratch behind them.
+struct Block {
+  void* base = nullptr;
   int* status = nullptr;
   uint32_t* flags = nullptr;
-  float* partials = nullptr;
   size_t flag_cap = 0;
+};
+struct Workspace {
+  Block block;
+  float* partials = nullptr;
   size_t partial_cap = 0;  // floats
   uint32_t epoch = 0;
+  // A call captured into a graph has been given the block: the graph holds its
+  // addresses for as long as it lives, so the block is not freed when the
+  // workspace grows but kept in `retired` until sgemm_shutdown().
+  bool captured = false;
+  std::vector<Block> retired;
 };
 std::map<std::pair<int, cudaStream_t>, Workspace> g_workspaces;
 
@@ -127,42 +135,47 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 int get_workspace(int dev, cudaStream_t stream, size_t flags, size_t partial_floats,
                   Workspace** out) {
   Workspace& w = g_workspaces[{dev, stream}];
-  if (w.block == nullptr || w.flag_cap < flags || w.partial_cap < partial_floats) {
+  // (the query fails where another stream's capture makes this one unusable)
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  const bool asked = cudaStreamIsCapturing(stream, &cs) == cudaSuccess;
+  if (!asked) cudaGetLastError();
+  if (w.block.base == nullptr || w.block.flag_cap < flags || w.partial_cap < partial_floats) {
     // allocation is not allowed while the stream is captured into a graph:
     // refuse instead of invalidating the capture
-    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(stream, &cs) != cudaSuccess) {
-      cudaGetLastError();
-      return SGEMM_ERR_CAPTURE;
-    }
-    if (cs != cudaStreamCaptureStatusNone) return SGEMM_ERR_CAPTURE;
-    const size_t fcap = flags > w.flag_cap ? flags : w.flag_cap;
+    if (!asked || cs != cudaStreamCaptureStatusNone) return SGEMM_ERR_CAPTURE;
+    const size_t fcap = flags > w.block.flag_cap ? flags : w.block.flag_cap;
     const size_t pcap = partial_floats > w.partial_cap ? partial_floats : w.partial_cap;
     const size_t status_bytes = 256;
     const size_t flag_bytes = ((fcap * 4 + 255) / 256) * 256;
     const size_t bytes = status_bytes + flag_bytes + pcap * 4;
-    if (w.block != nullptr) {
+    if (w.block.base != nullptr) {
       // the old block may still be in use by queued work on this stream
       if (cudaStreamSynchronize(stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
-      cudaFree(w.block);
-      w.block = nullptr;
+      if (w.captured)
+        w.retired.push_back(w.block);
+      else
+        cudaFree(w.block.base);
+      w.block = Block{};
+      w.partial_cap = 0;
+      w.captured = false;
     }
     void* blk = nullptr;
     if (cudaMalloc(&blk, bytes) != cudaSuccess) {
       cudaGetLastError();
-      w = Workspace{};
       return SGEMM_ERR_ALLOC;
     }
-    if (cudaMemsetAsync(blk, 0, status_bytes + flag_bytes, stream) != cudaSuccess)
+    if (cudaMemsetAsync(blk, 0, status_bytes + flag_bytes, stream) != cudaSuccess) {
+      cudaFree(blk);
       return SGEMM_ERR_LAUNCH;
-    w.block = blk;
-    w.bytes = bytes;
-    w.status = static_cast<int*>(blk);
-    w.flags = reinterpret_cast<uint32_t*>(static_cast<char*>(blk) + status_bytes);
+    }
+    w.block.base = blk;
+    w.block.status = static_cast<int*>(blk);
+    w.block.flags = reinterpret_cast<uint32_t*>(static_cast<char*>(blk) + status_bytes);
+    w.block.flag_cap = fcap;
     w.partials = reinterpret_cast<float*>(static_cast<char*>(blk) + status_bytes + flag_bytes);
-    w.flag_cap = fcap;
     w.partial_cap = pcap;
   }
+  w.captured = w.captured || cs != cudaStreamCaptureStatusNone;
   *out = &w;
   return SGEMM_OK;
 }
@@ -339,8 +352,8 @@ int run_ffma(int opA, int opB, int M, int N, int K, float alpha, const float* A,
   p.sC = sC;
   p.sched = sched;
   p.ws = ws->partials;
-  p.flags = ws->flags;
-  p.status = ws->status;
+  p.flags = ws->block.flags;
+  p.status = ws->block.status;
   p.epoch = ws->epoch;
   p.c_vec = ((reinterpret_cast<uintptr_t>(C) & 15u) == 0) && ((ldc & 3) == 0) &&
             (single || (sC & 3) == 0);
@@ -388,8 +401,8 @@ int library_workspace(int dev, cudaStream_t stream, size_t floats, size_t nflags
   const int st = get_workspace(dev, stream, nflags > 0 ? nflags : 1, floats, &ws);
   if (st != SGEMM_OK) return st;
   *scratch = ws->partials;
-  *status = ws->status;
-  if (flags != nullptr) *flags = ws->flags;
+  *status = ws->block.status;
+  if (flags != nullptr) *flags = ws->block.flags;
   if (epoch != nullptr) {
     if (++ws->epoch == 0) ws->epoch = 1;
     *epoch = ws->epoch;
@@ -500,20 +513,24 @@ SGEMM_API int sgemm_poll_device_status(void* stream_, int* detail) {
   }
   std::lock_guard<std::mutex> lock(g_mutex);
   auto it = g_workspaces.find({dev, stream});
-  if (it == g_workspaces.end() || it->second.status == nullptr) return SGEMM_OK;
+  if (it == g_workspaces.end()) return SGEMM_OK;
   int code = 0;
-  if (cudaMemcpy(&code, it->second.status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
-    return SGEMM_ERR_LAUNCH;
-  if (code != 0) {
-    if (cudaMemset(it->second.status, 0, sizeof(int)) != cudaSuccess) return SGEMM_ERR_LAUNCH;
-    // an aborted launch can leave split-K flags set that no owner consumed
-    if (it->second.flags != nullptr &&
-        cudaMemset(it->second.flags, 0, it->second.flag_cap * 4) != cudaSuccess)
+  // (a graph whose block has been retired reports there)
+  for (size_t i = 0; i <= it->second.retired.size(); ++i) {
+    const Block& b = i == 0 ? it->second.block : it->second.retired[i - 1];
+    if (b.base == nullptr) continue;
+    int got = 0;
+    if (cudaMemcpy(&got, b.status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
       return SGEMM_ERR_LAUNCH;
-    if (detail) *detail = code;
-    return SGEMM_ERR_DEVICE_TIMEOUT;
+    if (got == 0) continue;
+    if (cudaMemset(b.status, 0, sizeof(int)) != cudaSuccess) return SGEMM_ERR_LAUNCH;
+    // an aborted launch can leave split-K flags set that no owner consumed
+    if (cudaMemset(b.flags, 0, b.flag_cap * 4) != cudaSuccess) return SGEMM_ERR_LAUNCH;
+    if (code == 0) code = got;
   }
-  return SGEMM_OK;
+  if (code == 0) return SGEMM_OK;
+  if (detail) *detail = code;
+  return SGEMM_ERR_DEVICE_TIMEOUT;
 }
 
 namespace sgemm_gb300 {
@@ -526,11 +543,10 @@ SGEMM_API void sgemm_shutdown(void) {
   int cur = 0;
   const bool have_cur = cudaGetDevice(&cur) == cudaSuccess;
   for (auto& kv : g_workspaces) {
-    if (kv.second.block) {
-      cudaSetDevice(kv.first.first);
-      cudaDeviceSynchronize();
-      cudaFree(kv.second.block);
-    }
+    cudaSetDevice(kv.first.first);
+    cudaDeviceSynchronize();
+    if (kv.second.block.base) cudaFree(kv.second.block.base);
+    for (const Block& b : kv.second.retired) cudaFree(b.base);
   }
   g_workspaces.clear();
   if (have_cur) cudaSetDevice(cur);
@@ -681,7 +697,7 @@ SGEMM_API int sgemm_diag_wait_timeout(long long timeout_ns, void* stream_) {
   Workspace* ws = nullptr;
   st = get_workspace(dev, stream, 1, 0, &ws);
   if (st != SGEMM_OK) return st;
-  diag_wait_kernel<<<1, 32, 0, stream>>>(ws->status, timeout_ns);
+  diag_wait_kernel<<<1, 32, 0, stream>>>(ws->block.status, timeout_ns);
   return cudaGetLastError() == cudaSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH;
 }
 

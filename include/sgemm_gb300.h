@@ -31,13 +31,17 @@
  * `stream`; the workspace is per (device, stream), so concurrent calls on
  * different streams do not share it. Host-side state is guarded by a mutex.
  *
- * CUDA graphs: sgemm, sgemm_ex, sgemm_strided_batched and sgemm_3xtf32 can be
+ * CUDA graphs: sgemm, sgemm_ex, sgemm_strided_batched, sgemm_3xtf32,
+ * sgemm_grouped, sgemm_grouped_wgrad, sgemm_i8 and sgemm_grad_clip can be
  * captured into a graph and replayed, once a call of at least the same size
  * has run on the capturing stream outside the capture (it sets the device up
  * and sizes the stream's workspace; a call that would have to grow it during
  * capture returns SGEMM_ERR_CAPTURE and launches nothing). The graph keeps
  * the stream's workspace: do not replay it concurrently with other work on
- * that stream's workspace. sgemm_noalloc needs no workspace at all.
+ * that stream's workspace. A later call that needs a larger one gets a new
+ * block; the one that graphs hold stays allocated until sgemm_shutdown(),
+ * after which they must not be replayed. sgemm_noalloc needs no workspace at
+ * all.
  */
 #ifndef SGEMM_GB300_H
 #define SGEMM_GB300_H
