@@ -10,11 +10,12 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_strided.h>
-#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <optional>
 #include <string>
 #include <vector>
 
@@ -48,6 +49,8 @@ struct PythonError {};   // the exception is already set
 void check(bool ok, const char* what) {
   if (!ok) throw Refusal{what};
 }
+
+bool is_none(PyObject* o) { return o == nullptr || o == Py_None; }
 
 const at::Tensor& tensor(PyObject* o, const char* name) {
   if (!THPVariable_Check(o)) throw Refusal{std::string(name) + " must be a tensor"};
@@ -92,26 +95,19 @@ void check_apart(const at::Tensor& t, int64_t ld) {
         "the groups' matrices in C overlap");
 }
 
-// Tensors of one call: on one CUDA device, which is made current; its stream.
+// Tensors of one call: on one CUDA device, which is current for its duration,
+// and so is the stream it was given: a result is allocated as that stream's
+// own (one of the current stream's could still be in use by work queued there,
+// or be handed out again there before the kernel has written it).
 class Launch {
  public:
-  Launch(PyObject* stream, std::initializer_list<const at::Tensor*> tensors) {
-    const at::Tensor& first = **tensors.begin();
-    check(first.is_cuda(), "tensors must be on one CUDA device");
-    const auto device = first.get_device();
-    for (const at::Tensor* t : tensors)
-      check(t->is_cuda() && t->get_device() == device, "tensors must be on one CUDA device");
-    init(stream, device);
+  Launch(PyObject* stream, std::initializer_list<const at::Tensor*> tensors)
+      : Launch(stream, device_of(**tensors.begin())) {
+    for (const at::Tensor* t : tensors) check_device(*t);
   }
-  Launch(PyObject* stream, int device) { init(stream, device); }
-  ~Launch() {
-    if (previous_ >= 0) c10::cuda::set_device((c10::DeviceIndex)previous_);
-  }
-  void* handle() const { return handle_; }
-
- private:
-  void init(PyObject* stream, int device) {
-    if (stream == nullptr || stream == Py_None) {
+  Launch(PyObject* stream, int device) : device_(device) {
+    if (is_none(stream)) {
+      on_device_.emplace((c10::DeviceIndex)device);
       handle_ = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();
     } else {
       PyObject* h = PyObject_GetAttrString(stream, "cuda_stream");
@@ -119,15 +115,24 @@ class Launch {
       handle_ = PyLong_AsVoidPtr(h);
       Py_DECREF(h);
       if (PyErr_Occurred()) throw PythonError{};
-    }
-    const int current = c10::cuda::current_device();
-    if (current != device) {
-      c10::cuda::set_device((c10::DeviceIndex)device);
-      previous_ = current;
+      on_stream_.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle_),
+                                                          (c10::DeviceIndex)device));
     }
   }
+  void* handle() const { return handle_; }
+  void check_device(const at::Tensor& t) const {
+    check(t.is_cuda() && t.get_device() == device_, "tensors must be on one CUDA device");
+  }
+
+ private:
+  static int device_of(const at::Tensor& t) {
+    check(t.is_cuda(), "tensors must be on one CUDA device");
+    return t.get_device();
+  }
+  int device_;
   void* handle_ = nullptr;
-  int previous_ = -1;
+  std::optional<c10::cuda::CUDAGuard> on_device_;
+  std::optional<c10::cuda::CUDAStreamGuard> on_stream_;
 };
 
 at::ScalarType dtype_or(PyObject* o, at::ScalarType other) {
@@ -146,8 +151,6 @@ const int* offsets_of(const at::Tensor& t, int64_t groups) {
 void vector_of(const at::Tensor& t, int64_t n, const char* what) {
   check(t.scalar_type() == at::kFloat && t.dim() == 1 && t.size(0) == n && t.is_contiguous(), what);
 }
-
-bool is_none(PyObject* o) { return o == nullptr || o == Py_None; }
 
 double number(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
@@ -176,22 +179,24 @@ PyObject* grouped_gemm(PyObject* const* a) {
   const int* bounds = offsets_of(off, E);
   const int type = type_of(X, "X"), ldx = pitch(X, "X"), ldw = pitch(W, "W");
   at::Tensor Y;
+  at::ScalarType out = X.scalar_type();
   if (is_none(a[3])) {
     check(beta == 0.0, "beta needs Y");
-    check(X.is_cuda(), "tensors must be on one CUDA device");
-    const at::ScalarType out = dtype_or(a[7], X.scalar_type());
-    type_of(out, "out_dtype");
-    Y = at::empty({T, N}, X.options().dtype(out).requires_grad(false));
+    out = dtype_or(a[7], out);
   } else {
     Y = tensor(a[3], "Y");
     check(Y.dim() == 2 && Y.size(0) == T && Y.size(1) == N, "shape mismatch");
+    pitch(Y, "Y");
+    out = Y.scalar_type();
   }
-  const int ldy = pitch(Y, "Y");
-  const Launch on(a[8], {&X, &W, &off, &Y});
-  const int st = fn.grouped(transposed ? 1 : 0, type, type_of(Y, "Y"), to_int(E), to_int(T),
-                            to_int(N), to_int(K), (float)alpha, X.data_ptr(), ldx, W.data_ptr(),
-                            ldw, E > 1 ? W.stride(0) : 0, bounds, (float)beta, Y.data_ptr(), ldy,
-                            on.handle());
+  const int out_type = type_of(out, "Y");
+  const Launch on(a[8], {&X, &W, &off});
+  if (!Y.defined()) Y = at::empty({T, N}, X.options().dtype(out).requires_grad(false));
+  on.check_device(Y);
+  const int st = fn.grouped(transposed ? 1 : 0, type, out_type, to_int(E), to_int(T), to_int(N),
+                            to_int(K), (float)alpha, X.data_ptr(), ldx, W.data_ptr(), ldw,
+                            E > 1 ? W.stride(0) : 0, bounds, (float)beta, Y.data_ptr(),
+                            pitch(Y, "Y"), on.handle());
   if (st != 0) throw Status{st, "sgemm_grouped"};
   return result(a[3], Y);
 }
@@ -207,22 +212,23 @@ PyObject* grouped_wgrad(PyObject* const* a) {
   const int* bounds = offsets_of(off, E);
   const int type = type_of(A, "A"), lda = pitch(A, "A"), ldb = pitch(B, "B");
   at::Tensor C;
+  at::ScalarType out = A.scalar_type();
   if (is_none(a[3])) {
     check(beta == 0.0, "beta needs C");
-    check(A.is_cuda(), "tensors must be on one CUDA device");
-    const at::ScalarType out = dtype_or(a[6], A.scalar_type());
-    type_of(out, "out_dtype");
-    C = at::empty({E, M, N}, A.options().dtype(out).requires_grad(false));
+    out = dtype_or(a[6], out);
   } else {
     C = tensor(a[3], "C");
     check(C.dim() == 3 && C.size(0) == E && C.size(1) == M && C.size(2) == N, "shape mismatch");
+    check_apart(C, pitch(C, "C"));
+    out = C.scalar_type();
   }
-  const int ldc = pitch(C, "C");
-  check_apart(C, ldc);
-  const Launch on(a[7], {&A, &B, &off, &C});
-  const int st = fn.wgrad(type, type_of(C, "C"), to_int(E), to_int(T), to_int(M), to_int(N),
-                          (float)alpha, A.data_ptr(), lda, B.data_ptr(), ldb, bounds, (float)beta,
-                          C.data_ptr(), ldc, E > 1 ? C.stride(0) : 0, on.handle());
+  const int out_type = type_of(out, "C");
+  const Launch on(a[7], {&A, &B, &off});
+  if (!C.defined()) C = at::empty({E, M, N}, A.options().dtype(out).requires_grad(false));
+  on.check_device(C);
+  const int st = fn.wgrad(type, out_type, to_int(E), to_int(T), to_int(M), to_int(N), (float)alpha,
+                          A.data_ptr(), lda, B.data_ptr(), ldb, bounds, (float)beta, C.data_ptr(),
+                          pitch(C, "C"), E > 1 ? C.stride(0) : 0, on.handle());
   if (st != 0) throw Status{st, "sgemm_grouped_wgrad"};
   return result(a[3], C);
 }
@@ -234,29 +240,30 @@ PyObject* i8_quantize(PyObject* const* a) {
   const int64_t M = X.size(0), K = X.size(1);
   const int type = type_of(X, "X"), ldx = pitch(X, "X");
   at::Tensor Q, scale;
-  if (is_none(a[1])) {
-    check(X.is_cuda(), "tensors must be on one CUDA device");
-    // rows padded to 16 bytes, so that sgemm_i8 reads them in place
-    const int64_t ld = (K + 15) / 16 * 16;
-    const auto options = X.options().dtype(at::kChar).requires_grad(false);
-    Q = ld == K ? at::empty({M, K}, options) : at::empty_strided({M, K}, {ld, 1}, options);
-  } else {
+  if (!is_none(a[1])) {
     Q = tensor(a[1], "Q");
+    check(Q.scalar_type() == at::kChar && Q.dim() == 2 && Q.size(0) == M && Q.size(1) == K,
+          "Q must be int8 of X's shape");
+    pitch(Q, "Q");
   }
-  check(Q.scalar_type() == at::kChar && Q.dim() == 2 && Q.size(0) == M && Q.size(1) == K,
-        "Q must be int8 of X's shape");
-  const int ldq = pitch(Q, "Q");
-  if (is_none(a[2])) {
-    check(X.is_cuda(), "tensors must be on one CUDA device");
-    scale = at::empty({M}, X.options().dtype(at::kFloat).requires_grad(false));
-  } else {
+  if (!is_none(a[2])) {
     scale = tensor(a[2], "scale");
+    vector_of(scale, M, "scale must be a contiguous float32 vector with one value a row");
   }
-  vector_of(scale, M, "scale must be a contiguous float32 vector with one value a row");
   {
-    const Launch on(a[3], {&X, &Q, &scale});
+    const Launch on(a[3], {&X});
+    if (!Q.defined()) {
+      // rows padded to 16 bytes, so that sgemm_i8 reads them in place
+      const int64_t ld = (K + 15) / 16 * 16;
+      const auto options = X.options().dtype(at::kChar).requires_grad(false);
+      Q = ld == K ? at::empty({M, K}, options) : at::empty_strided({M, K}, {ld, 1}, options);
+    }
+    if (!scale.defined())
+      scale = at::empty({M}, X.options().dtype(at::kFloat).requires_grad(false));
+    on.check_device(Q);
+    on.check_device(scale);
     const int st = fn.quantize(to_int(M), to_int(K), type, X.data_ptr(), ldx,
-                               static_cast<signed char*>(Q.data_ptr()), ldq,
+                               static_cast<signed char*>(Q.data_ptr()), pitch(Q, "Q"),
                                static_cast<float*>(scale.data_ptr()), on.handle());
     if (st != 0) throw Status{st, "sgemm_i8_quantize"};
   }
@@ -280,23 +287,25 @@ PyObject* i8_gemm(PyObject* const* a) {
   vector_of(sb, N, "scaleB must be a contiguous float32 vector with a value for each row of B");
   const int lda = pitch(A, "A"), ldb = pitch(B, "B");
   at::Tensor C;
+  at::ScalarType out = at::kBFloat16;
   if (is_none(a[4])) {
-    check(A.is_cuda(), "tensors must be on one CUDA device");
-    const at::ScalarType out = dtype_or(a[5], at::kBFloat16);
-    type_of(out, "out_dtype");
-    C = at::empty({M, N}, A.options().dtype(out).requires_grad(false));
+    out = dtype_or(a[5], out);
   } else {
     C = tensor(a[4], "C");
     check(C.dim() == 2 && C.size(0) == M && C.size(1) == N, "shape mismatch");
+    pitch(C, "C");
+    out = C.scalar_type();
   }
-  const int ldc = pitch(C, "C");
-  const Launch on(a[6], {&A, &sa, &B, &sb, &C});
+  const int out_type = type_of(out, "C");
+  const Launch on(a[6], {&A, &sa, &B, &sb});
+  if (!C.defined()) C = at::empty({M, N}, A.options().dtype(out).requires_grad(false));
+  on.check_device(C);
   const int st = fn.i8(to_int(M), to_int(N), to_int(K),
                        static_cast<const signed char*>(A.data_ptr()), lda,
                        static_cast<const float*>(sa.data_ptr()),
                        static_cast<const signed char*>(B.data_ptr()), ldb,
-                       static_cast<const float*>(sb.data_ptr()), type_of(C, "C"), C.data_ptr(), ldc,
-                       on.handle());
+                       static_cast<const float*>(sb.data_ptr()), out_type, C.data_ptr(),
+                       pitch(C, "C"), on.handle());
   if (st != 0) throw Status{st, "sgemm_i8"};
   return result(a[4], C);
 }
@@ -346,9 +355,9 @@ PyObject* clip_grad_norm(PyObject* const* a) {
       to[i] = o.data_ptr();
     }
   }
+  const Launch on(a[3], device);
   const at::Tensor norm =
       at::empty({}, tensor(grads[0], "gradients").options().dtype(at::kFloat).requires_grad(false));
-  const Launch on(a[3], device);
   const int st = fn.clip((int)n, in.data(), to.data(), sizes.data(), types.data(), (float)max_norm,
                          static_cast<float*>(norm.data_ptr()), on.handle());
   if (st != 0) throw Status{st, "sgemm_grad_clip"};
