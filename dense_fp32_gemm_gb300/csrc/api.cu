@@ -390,13 +390,18 @@ __global__ void diag_wait_kernel(int* status, long long timeout_ns) {
 }  // namespace
 
 // ---- internal hooks for the other entry points of the library -------------
+// The lock that a call holds from taking the workspace to its last launch:
+// another host thread's call on the same stream must neither queue a kernel
+// between two of this one's that hand something on in the workspace, nor grow
+// (and free) the block that this one is about to launch with.
+std::unique_lock<std::mutex> library_lock() { return std::unique_lock<std::mutex>(g_mutex); }
+
 // Scratch of at least `floats` floats (and the status word) in the
-// per-(device, stream) workspace.
+// per-(device, stream) workspace. Called with the lock above held.
 // With nflags > 0 it also returns the flag array and this call's epoch (a
 // value no flag holds before this call publishes it).
 int library_workspace(int dev, cudaStream_t stream, size_t floats, size_t nflags, float** scratch,
                       int** status, uint32_t** flags, uint32_t* epoch) {
-  std::lock_guard<std::mutex> lock(g_mutex);
   Workspace* ws = nullptr;
   const int st = get_workspace(dev, stream, nflags > 0 ? nflags : 1, floats, &ws);
   if (st != SGEMM_OK) return st;

@@ -23,6 +23,7 @@
 #include <stdint.h>
 
 #include <cstring>
+#include <mutex>
 
 #include "../../include/sgemm_gb300.h"
 #include "ptx.cuh"
@@ -31,6 +32,7 @@
 
 namespace sgemm_gb300 {
 
+std::unique_lock<std::mutex> library_lock();
 int library_workspace(int dev, cudaStream_t stream, size_t floats, size_t nflags, float** scratch,
                       int** status, uint32_t** flags, uint32_t* epoch);
 int library_device_sms(int dev, int* sms);
@@ -363,6 +365,7 @@ SGEMM_API int sgemm_grad_clip(int n, const void* const* grads, void* const* out,
   const size_t most = (size_t)lists * sms * ctas_per_sm(4);
   float* ws = nullptr;
   int* status = nullptr;
+  const std::unique_lock<std::mutex> lock = library_lock();   // to the last launch
   st = library_workspace(dev, stream, most * 2, 0, &ws, &status, nullptr, nullptr);
   if (st != SGEMM_OK) return st;
   double* sums = reinterpret_cast<double*>(ws);

@@ -7,12 +7,15 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <mutex>
+
 #include "../../include/sgemm_gb300.h"
 #include "ragged_gemm.cuh"
 
 namespace sgemm_gb300 {
 
 // Provided by api.cu.
+std::unique_lock<std::mutex> library_lock();
 int library_workspace(int dev, cudaStream_t stream, size_t floats, size_t nflags, float** scratch,
                       int** status, uint32_t** flags, uint32_t* epoch);
 int library_device_sms(int dev, int* sms);

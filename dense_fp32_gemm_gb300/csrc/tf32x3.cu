@@ -74,6 +74,7 @@
 namespace sgemm_gb300 {
 
 // Provided by api.cu.
+std::unique_lock<std::mutex> library_lock();
 int library_workspace(int dev, cudaStream_t stream, size_t floats, size_t nflags, float** scratch,
                       int** status, uint32_t** flags, uint32_t* epoch);
 int library_device_sms(int dev, int* sms);
@@ -974,6 +975,7 @@ SGEMM_API int sgemm_3xtf32(int M, int N, int K, float alpha, const float* A, int
   int* status = nullptr;
   uint32_t* flags = nullptr;
   uint32_t epoch = 0;
+  const std::unique_lock<std::mutex> lock = library_lock();   // to the last launch
   st = library_workspace(dev, stream, bt_floats + a_floats + partial_floats, (size_t)ctas, &ws,
                          &status, &flags, &epoch);
   if (st != SGEMM_OK) return st;

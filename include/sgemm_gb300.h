@@ -29,7 +29,9 @@
  *
  * Threading: calls are asynchronous with respect to the host and ordered on
  * `stream`; the workspace is per (device, stream), so concurrent calls on
- * different streams do not share it. Host-side state is guarded by a mutex.
+ * different streams do not share it. Host-side state is guarded by a mutex,
+ * and the launches of one call are queued together: host threads may call on
+ * one stream.
  *
  * CUDA graphs: sgemm, sgemm_ex, sgemm_strided_batched, sgemm_3xtf32,
  * sgemm_grouped, sgemm_grouped_wgrad, sgemm_i8 and sgemm_grad_clip can be
