@@ -66,12 +66,14 @@ struct DeviceInfo {
 };
 std::map<int, DeviceInfo> g_devices;
 
-// One allocation: the status word, the flags behind it, the scratch behind them.
+// One allocation: the status word, the flags of split tiles (a call's epoch
+// marks them), the counters of cut tiles (zero between launches), the scratch.
 struct Block {
   void* base = nullptr;
   int* status = nullptr;
   uint32_t* flags = nullptr;
-  size_t flag_cap = 0;
+  uint32_t* counters = nullptr;
+  size_t flag_cap = 0;         // of either
 };
 struct Workspace {
   Block block;
@@ -147,7 +149,7 @@ int get_workspace(int dev, cudaStream_t stream, size_t flags, size_t partial_flo
     const size_t pcap = partial_floats > w.partial_cap ? partial_floats : w.partial_cap;
     const size_t status_bytes = 256;
     const size_t flag_bytes = ((fcap * 4 + 255) / 256) * 256;
-    const size_t bytes = status_bytes + flag_bytes + pcap * 4;
+    const size_t bytes = status_bytes + 2 * flag_bytes + pcap * 4;
     if (w.block.base != nullptr) {
       // the old block may still be in use by queued work on this stream
       if (cudaStreamSynchronize(stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
@@ -164,15 +166,16 @@ int get_workspace(int dev, cudaStream_t stream, size_t flags, size_t partial_flo
       cudaGetLastError();
       return SGEMM_ERR_ALLOC;
     }
-    if (cudaMemsetAsync(blk, 0, status_bytes + flag_bytes, stream) != cudaSuccess) {
+    if (cudaMemsetAsync(blk, 0, status_bytes + 2 * flag_bytes, stream) != cudaSuccess) {
       cudaFree(blk);
       return SGEMM_ERR_LAUNCH;
     }
     w.block.base = blk;
     w.block.status = static_cast<int*>(blk);
     w.block.flags = reinterpret_cast<uint32_t*>(static_cast<char*>(blk) + status_bytes);
+    w.block.counters = w.block.flags + flag_bytes / 4;
     w.block.flag_cap = fcap;
-    w.partials = reinterpret_cast<float*>(static_cast<char*>(blk) + status_bytes + flag_bytes);
+    w.partials = reinterpret_cast<float*>(static_cast<char*>(blk) + status_bytes + 2 * flag_bytes);
     w.partial_cap = pcap;
   }
   w.captured = w.captured || cs != cudaStreamCaptureStatusNone;
@@ -373,7 +376,8 @@ int run_ffma(int opA, int opB, int M, int N, int K, float alpha, const float* A,
   return SGEMM_OK;
 }
 
-__global__ void diag_wait_kernel(int* status, long long timeout_ns) {
+__global__ void diag_wait_kernel(int* status, uint32_t* flags, uint32_t* counters, int n,
+                                 uint32_t epoch, long long timeout_ns) {
   __shared__ __align__(8) uint64_t bar;
   __shared__ int abort_w;
   if (threadIdx.x == 0) {
@@ -384,6 +388,12 @@ __global__ void diag_wait_kernel(int* status, long long timeout_ns) {
   __syncthreads();
   // phase 0 of `bar` never completes: nothing arrives
   bounded_wait(ptx::smem_addr(&bar), 0u, &abort_w, status, kDevTimeoutFull, timeout_ns);
+  // what launches that give up can leave behind: flags that no owner consumed,
+  // arrivals of which the last never came
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    flags[i] = epoch;
+    counters[i] = 1u;
+  }
 }
 
 
@@ -399,15 +409,17 @@ std::unique_lock<std::mutex> library_lock() { return std::unique_lock<std::mutex
 // Scratch of at least `floats` floats (and the status word) in the
 // per-(device, stream) workspace. Called with the lock above held.
 // With nflags > 0 it also returns the flag array and this call's epoch (a
-// value no flag holds before this call publishes it).
+// value no flag holds before this call publishes it), or the counter array
+// (zeros, unless a launch gave up and its status has not been polled since).
 int library_workspace(int dev, cudaStream_t stream, size_t floats, size_t nflags, float** scratch,
-                      int** status, uint32_t** flags, uint32_t* epoch) {
+                      int** status, uint32_t** flags, uint32_t* epoch, uint32_t** counters) {
   Workspace* ws = nullptr;
   const int st = get_workspace(dev, stream, nflags > 0 ? nflags : 1, floats, &ws);
   if (st != SGEMM_OK) return st;
   *scratch = ws->partials;
   *status = ws->block.status;
   if (flags != nullptr) *flags = ws->block.flags;
+  if (counters != nullptr) *counters = ws->block.counters;
   if (epoch != nullptr) {
     if (++ws->epoch == 0) ws->epoch = 1;
     *epoch = ws->epoch;
@@ -528,9 +540,13 @@ SGEMM_API int sgemm_poll_device_status(void* stream_, int* detail) {
     if (cudaMemcpy(&got, b.status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
       return SGEMM_ERR_LAUNCH;
     if (got == 0) continue;
-    if (cudaMemset(b.status, 0, sizeof(int)) != cudaSuccess) return SGEMM_ERR_LAUNCH;
-    // an aborted launch can leave split-K flags set that no owner consumed
-    if (cudaMemset(b.flags, 0, b.flag_cap * 4) != cudaSuccess) return SGEMM_ERR_LAUNCH;
+    // an aborted launch can leave split-K flags set that no owner consumed, and
+    // arrivals counted of which the last never came (cleared in the stream's
+    // order, ahead of later calls)
+    if (cudaMemsetAsync(b.status, 0, sizeof(int), stream) != cudaSuccess ||
+        cudaMemsetAsync(b.flags, 0, b.flag_cap * 4, stream) != cudaSuccess ||
+        cudaMemsetAsync(b.counters, 0, b.flag_cap * 4, stream) != cudaSuccess)
+      return SGEMM_ERR_LAUNCH;
     if (code == 0) code = got;
   }
   if (code == 0) return SGEMM_OK;
@@ -702,7 +718,8 @@ SGEMM_API int sgemm_diag_wait_timeout(long long timeout_ns, void* stream_) {
   Workspace* ws = nullptr;
   st = get_workspace(dev, stream, 1, 0, &ws);
   if (st != SGEMM_OK) return st;
-  diag_wait_kernel<<<1, 32, 0, stream>>>(ws->block.status, timeout_ns);
+  diag_wait_kernel<<<1, 32, 0, stream>>>(ws->block.status, ws->block.flags, ws->block.counters,
+                                        (int)ws->block.flag_cap, ws->epoch, timeout_ns);
   return cudaGetLastError() == cudaSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH;
 }
 

@@ -34,7 +34,7 @@ namespace sgemm_gb300 {
 
 std::unique_lock<std::mutex> library_lock();
 int library_workspace(int dev, cudaStream_t stream, size_t floats, size_t nflags, float** scratch,
-                      int** status, uint32_t** flags, uint32_t* epoch);
+                      int** status, uint32_t** flags, uint32_t* epoch, uint32_t** counters);
 int library_device_sms(int dev, int* sms);
 
 namespace {
@@ -366,7 +366,8 @@ SGEMM_API int sgemm_grad_clip(int n, const void* const* grads, void* const* out,
   float* ws = nullptr;
   int* status = nullptr;
   const std::unique_lock<std::mutex> lock = library_lock();   // to the last launch
-  st = library_workspace(dev, stream, most * 2, 0, &ws, &status, nullptr, nullptr);
+  st = library_workspace(dev, stream, most * 2, 0, &ws, &status, nullptr, nullptr,
+                         nullptr);
   if (st != SGEMM_OK) return st;
   double* sums = reinterpret_cast<double*>(ws);
   // the first launches write their sums one list after another

@@ -370,10 +370,9 @@ int run(int src, int type, Params p, Operand op_p, Operand op_q, cudaStream_t st
   const size_t pack_q = reads ? op_q.packed_bytes(widen) : 0;
   const size_t partial = (size_t)workers * cl * 2 * BP * bq * 4;
   float* ws = nullptr;
-  uint32_t epoch = 0;
   const std::unique_lock<std::mutex> lock = library_lock();   // to the last launch
   st = library_workspace(dev, stream, (pack_p + pack_q + partial) / 4, (size_t)workers * cl, &ws,
-                         &p.status, &p.counters, &epoch);
+                         &p.status, nullptr, nullptr, &p.counters);
   if (st != SGEMM_OK) return st;
   char* at = reinterpret_cast<char*>(ws);
   if ((pack_p || pack_q) &&

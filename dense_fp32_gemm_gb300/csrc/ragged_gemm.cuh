@@ -120,7 +120,7 @@ struct Params {
   // costs, in 1/16 slices: once, and for each part of the tile
   int cut_least, cut_once, cut_part;
   float* partials;        // two tiles of BQ x 128 floats per CTA
-  uint32_t* counters;     // arrivals at a cut tile, one per CTA, zero between launches
+  uint32_t* counters;     // arrivals at a cut tile, one per CTA, zero unless status is set
   int* status;
   long long timeout_ns;
 };
@@ -596,6 +596,11 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     // scan of the groups: rows, number and slice position of each one's first
     // tile. A group starts at the end of those before it at the earliest, so the
     // groups together have at most T rows whatever the offsets hold.
+    // A launch before this one that gave up may have left arrivals counted,
+    // until its status is polled: then no tile is cut. (CTAs that read the word
+    // on both sides of this launch's own giving up differ in their lists; the
+    // launch has failed by then, and its waits end.)
+    const int gave_up = *const_cast<const volatile int*>(p.status);
     const int ptiles = cdiv(p.P, BP * CL);
     int tiles_before = 0, pos_before = 0, end_before = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
@@ -646,7 +651,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
       // publishing and adding the parts takes
       const int over = tiles % workers;
       int dp = tiles, cutters = workers;
-      if (over != 0) {
+      if (over != 0 && gave_up == 0) {
         const int mean = total / tiles;
         int saved = mean * 16 / workers * (workers - over), parts = 2;
         if (tiles < workers) {

@@ -17,7 +17,7 @@ namespace sgemm_gb300 {
 // Provided by api.cu.
 std::unique_lock<std::mutex> library_lock();
 int library_workspace(int dev, cudaStream_t stream, size_t floats, size_t nflags, float** scratch,
-                      int** status, uint32_t** flags, uint32_t* epoch);
+                      int** status, uint32_t** flags, uint32_t* epoch, uint32_t** counters);
 int library_device_sms(int dev, int* sms);
 void note_last_config(const char* text);
 long long library_wait_timeout_ns();

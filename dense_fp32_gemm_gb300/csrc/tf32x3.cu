@@ -76,7 +76,7 @@ namespace sgemm_gb300 {
 // Provided by api.cu.
 std::unique_lock<std::mutex> library_lock();
 int library_workspace(int dev, cudaStream_t stream, size_t floats, size_t nflags, float** scratch,
-                      int** status, uint32_t** flags, uint32_t* epoch);
+                      int** status, uint32_t** flags, uint32_t* epoch, uint32_t** counters);
 int library_device_sms(int dev, int* sms);
 void note_last_config(const char* text);
 long long library_wait_timeout_ns();
@@ -977,7 +977,7 @@ SGEMM_API int sgemm_3xtf32(int M, int N, int K, float alpha, const float* A, int
   uint32_t epoch = 0;
   const std::unique_lock<std::mutex> lock = library_lock();   // to the last launch
   st = library_workspace(dev, stream, bt_floats + a_floats + partial_floats, (size_t)ctas, &ws,
-                         &status, &flags, &epoch);
+                         &status, &flags, &epoch, nullptr);
   if (st != SGEMM_OK) return st;
   float* bt = ws;
   float* a_copy = bt + bt_floats;

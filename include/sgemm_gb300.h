@@ -399,7 +399,9 @@ int sgemm_schedule_piece(const int* sched, int b, int i, int* out);
  * Diagnostic: launches one CTA that waits on a shared-memory barrier nothing
  * ever arrives on, with a limit of timeout_ns, through the same bounded wait
  * the GEMM kernels use. The wait must run out and record device code 1; read
- * it with sgemm_poll_device_status(). Nothing faults and nothing hangs.
+ * it with sgemm_poll_device_status(). Nothing faults and nothing hangs. It
+ * also leaves the workspace's flags and counters as launches that gave up can
+ * leave them: later calls have to be right all the same, polled or not.
  * The pages are silent.
  */
 int sgemm_diag_wait_timeout(long long timeout_ns, void* stream);
