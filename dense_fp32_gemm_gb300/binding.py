@@ -426,6 +426,7 @@ def _ld(t, name):
 def gemm(A, B, C, alpha=1.0, beta=0.0, stream=None):
     """C <- alpha*A@B + beta*C on CUDA float32 tensors (row-major views with
     any row stride). Raises SgemmError on a non-zero status. Returns C."""
+    import torch
     M, K = A.shape
     K2, N = B.shape
     if K2 != K or tuple(C.shape) != (M, N):
@@ -437,10 +438,14 @@ def gemm(A, B, C, alpha=1.0, beta=0.0, stream=None):
                float(beta), C.data_ptr(), _ld(C, "C"), _stream_handle(stream))
     if st != SGEMM_OK:
         raise SgemmError(st, "sgemm")
+    if not C.is_inference():
+        torch.autograd.graph.increment_version(C)
     return C
 
 
-# (csrc_torch/marshal.cpp: checks, allocation and the C call in native code)
+# (csrc_torch/marshal.cpp: checks, allocation and the C call in native code.
+# Autograd does not see through them: results carry no graph, layers.py has the
+# differentiable form. A tensor that is given to be written counts as changed.)
 @functools.cache
 def _native():
     """The marshalling module, bound to the loaded library."""

@@ -158,9 +158,17 @@ double number(PyObject* o) {
   return v;
 }
 
+// Tells autograd that a given tensor's values have changed: a graph that had
+// saved it for its backward pass refuses to use it. (Inference tensors have no
+// version.)
+void overwritten(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // The given result object, or a wrapper of the new tensor.
 PyObject* result(PyObject* given, const at::Tensor& t) {
   if (!is_none(given)) {
+    overwritten(t);
     Py_INCREF(given);
     return given;
   }
@@ -343,8 +351,9 @@ PyObject* clip_grad_norm(PyObject* const* a) {
     in[i] = to[i] = g.data_ptr();
     sizes[i] = g.numel();
   }
+  const Items written(is_none(a[2]) ? grads.fast : a[2]);
   if (!is_none(a[2])) {
-    const Items out(a[2]);
+    const Items& out = written;
     check(out.size() == n, "out must hold a tensor for every gradient");
     for (Py_ssize_t i = 0; i < n; ++i) {
       const at::Tensor &o = tensor(out[i], "out"), &g = tensor(grads[i], "gradients");
@@ -361,6 +370,7 @@ PyObject* clip_grad_norm(PyObject* const* a) {
   const int st = fn.clip((int)n, in.data(), to.data(), sizes.data(), types.data(), (float)max_norm,
                          static_cast<float*>(norm.data_ptr()), on.handle());
   if (st != 0) throw Status{st, "sgemm_grad_clip"};
+  for (Py_ssize_t i = 0; i < n; ++i) overwritten(tensor(written[i], "out"));
   return THPVariable_Wrap(norm);
 }
 
