@@ -124,7 +124,8 @@ __global__ void __launch_bounds__(kThreads)
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const int step = 16 * blockDim.x, k0 = 16 * threadIdx.x;
-  for (int m = blockIdx.x; m < M; m += gridDim.x) {
+  // (row numbers and places in a row pass 32 bits before they end their loops)
+  for (long long m = blockIdx.x; m < M; m += gridDim.x) {
     const E* x = X + m * ldx;
     uint32_t most = 0;
     Raw<E> h[kHeld];
@@ -132,8 +133,8 @@ __global__ void __launch_bounds__(kThreads)
     for (int i = 0; i < kHeld; ++i) h[i] = load_16<E, V>(x + k0 + i * step, K - k0 - i * step);
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) most = magnitude(h[i], most);
-    for (int k = k0 + kHeld * step; k < K; k += step)
-      most = magnitude(load_16<E, V>(x + k, K - k), most);
+    for (long long k = k0 + kHeld * step; k < K; k += step)
+      most = magnitude(load_16<E, V>(x + k, (int)(K - k)), most);
     most = __reduce_max_sync(0xffffffffu, most);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = most;
@@ -147,8 +148,8 @@ __global__ void __launch_bounds__(kThreads)
     for (int i = 0; i < kHeld; ++i)
       if (k0 + i * step < K)
         put_16(h[i], x + k0 + i * step, s, inv, q + k0 + i * step, K - k0 - i * step);
-    for (int k = k0 + kHeld * step; k < K; k += step)
-      put_16(load_16<E, V>(x + k, K - k), x + k, s, inv, q + k, K - k);
+    for (long long k = k0 + kHeld * step; k < K; k += step)
+      put_16(load_16<E, V>(x + k, (int)(K - k)), x + k, s, inv, q + k, (int)(K - k));
   }
 }
 
@@ -162,7 +163,7 @@ cudaError_t quantize(int M, int K, const void* X, int ldx, signed char* Q, int l
   // Few rows: as many threads as the row has groups, for its latency. Rows that
   // fill the SMs: half as many, so that twice the rows are in flight (a row is
   // a chain of a load, a block-wide maximum and a store).
-  const int groups = (K + 15) / 16, want = M < 4 * sms ? groups : (groups + 1) / 2;
+  const int groups = K / 16 + (K % 16 != 0), want = M < 4 * sms ? groups : (groups + 1) / 2;
   int threads = want < 32 ? 32 : (want + 31) / 32 * 32;
   if (threads > kThreads) threads = kThreads;
   const int fit = sms * (2048 / threads < 32 ? 2048 / threads : 32);
