@@ -39,7 +39,8 @@ struct Pack {
   unsigned char* dst;
   long long ld, stride, ldo, total;   // total: segments of all rows
   const unsigned char* end;           // of the last row
-  int rows, bytes, segments;          // segments: of a row
+  long long bytes;                    // of a row: beyond 32 bits from 2^29 FP32 values on
+  int rows, segments;                 // segments: of a row
   int lanes;                          // 4 .. 32: as many as a short row needs
 };
 constexpr int kPackThreads = 256;
@@ -93,7 +94,8 @@ __global__ void __launch_bounds__(kPackThreads)
       seg = (int)(unit - r * p.segments);
       mat = p.stride == 0 ? 0 : r / p.rows;
     }
-    const int c0 = seg * kPieces * step + lane * 16;   // the thread's first piece: byte of the row
+    // the thread's first piece: byte of the row
+    const long long c0 = (long long)seg * (kPieces * step) + lane * 16;
     const unsigned char* s = p.src + mat * p.stride + (r - mat * p.rows) * p.ld + c0;
     const unsigned at = (unsigned)reinterpret_cast<uintptr_t>(s) & 15u;   // (a segment's lanes agree)
     const unsigned char* base = s - at;
@@ -110,7 +112,7 @@ __global__ void __launch_bounds__(kPackThreads)
     }
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) {
-      const int c = c0 + step * j;
+      const long long c = c0 + step * j;
       if (c >= p.bytes) break;
       uint32_t w[4];
       if (inside[j]) {
@@ -123,9 +125,10 @@ __global__ void __launch_bounds__(kPackThreads)
         }
         w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
         if (c + 16 > p.bytes) {               // the row's end
+          const int left = (int)(p.bytes - c);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int n = p.bytes - c - 4 * k;   // valid bytes from this word on
+            const int n = left - 4 * k;       // valid bytes from this word on
             w[k] &= n >= 4 ? 0xffffffffu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u);
           }
         }
@@ -175,7 +178,7 @@ cudaError_t pack_operands(Operand* a, void* dst_a, Operand* b, void* dst_b, bool
     p[i].total = op.rows * op.batch * p[i].segments;
     p[i].end = p[i].src + (op.batch - 1) * p[i].stride + (op.rows - 1) * p[i].ld + bytes;
     p[i].rows = (int)op.rows;
-    p[i].bytes = (int)bytes;
+    p[i].bytes = bytes;
     total += p[i].total * p[i].lanes;
     if (widen) op.elem = 2;
     op.ptr = dsts[i];

@@ -50,3 +50,20 @@ def test_quantize_longest_row():
     assert float(s) == 1.0
     for c in chunks(MOST):
         assert torch.equal(q[0, c], x[c].to(torch.int8))
+
+
+@pytest.mark.parametrize("k", [2 ** 29 + 5, 2 ** 29 - 3])
+def test_copied_rows_of_two_gigabytes(k):
+    """FP32 rows that have to be copied, of more bytes than 32 bits count (and of just fewer)."""
+    x, w = torch.zeros(2, k, device="cuda"), torch.zeros(1, 1, k, device="cuda")
+    at = torch.tensor([0, 1, 15, 16, 12345, 2 ** 27 + 3, 2 ** 28 - 1, 2 ** 28, 2 ** 29 - 13, k - 6, k - 2, k - 1], device="cuda")
+    w[0, 0, at] = torch.arange(1, len(at) + 1, device="cuda").float()
+    x[0, at] = 1.0
+    x[1, at] = torch.arange(len(at), device="cuda").float()
+    off = torch.tensor([0, 2], dtype=torch.int32, device="cuda")
+    y = B.grouped_gemm(x, w, off)
+    assert "p=copied q=copied" in B.sgemm_last_config()
+    n = len(at)
+    assert y.flatten().tolist() == [n * (n + 1) / 2, sum(i * (i + 1) for i in range(n))]
+    assert B.sgemm_poll_device_status(torch.cuda.current_stream().cuda_stream) == (0, 0)
+    B.sgemm_shutdown()                   # (a workspace of 6 GB)
