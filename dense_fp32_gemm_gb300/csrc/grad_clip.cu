@@ -7,10 +7,10 @@
 // Two launches a list of up to kTable tensors: the squares, then the scaling.
 // The tensors are cut into pieces of 16 or 32 KB that start on 16-byte addresses
 // (the elements before a tensor's first such address form its first, shorter
-// vector), dealt to the CTAs in turn. Squares are summed in FP32 over one
-// thread's share of a piece (16 or 32 values) and in FP64 beyond; every CTA of
-// the second launch adds the first one's per-CTA sums in the same order, so
-// the result does not depend on timing.
+// vector), dealt to the CTAs in turn. Squares are summed in FP32 over at most
+// four vectors of a thread's share of a piece (16 FP32 or 32 16-bit values) and
+// in FP64 beyond; every CTA of the second launch adds the first one's per-CTA
+// sums in the same order, so the result does not depend on timing.
 //
 // Bound by HBM: the gradients are read twice (the norm is not known before all of
 // them have been) and written once, or read once where nothing is clipped.
@@ -173,10 +173,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(VECS))
       whole[j] = lo >= 0 && lo + per <= n;
       if (whole[j]) raw[j] = __ldg(reinterpret_cast<const uint4*>(in + lo * es));
     }
-    float s = 0.f;
+    float part[VECS / 4] = {};
     float x[8];
 #pragma unroll
     for (int j = 0; j < VECS; ++j) {
+      float& s = part[j / 4];
       if (whole[j]) {
         unpack(raw[j], type, x);
 #pragma unroll
@@ -190,9 +191,16 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(VECS))
           }
       }
     }
-    if (s > 1e-30f && s < 1e37f) {
-      total += (double)s;
-    } else if (s != 0.f) {
+    double sum = 0.0;
+    bool plain = true;
+#pragma unroll
+    for (int q = 0; q < VECS / 4; ++q) {
+      sum += (double)part[q];
+      plain = plain && ((part[q] > 1e-30f && part[q] < 1e37f) || part[q] == 0.f);
+    }
+    if (plain) {
+      total += sum;
+    } else {
       // squares near the ends of FP32's range (or no numbers): in FP64
       for (int j = 0; j < VECS; ++j) {
         const long long lo = (v0 + j * kThreads) * per - head;
