@@ -191,19 +191,26 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(VECS))
           }
       }
     }
-    double sum = 0.0;
-    bool plain = true;
+    bool plain[VECS / 4], all = true;
 #pragma unroll
     for (int q = 0; q < VECS / 4; ++q) {
-      sum += (double)part[q];
-      plain = plain && ((part[q] > 1e-30f && part[q] < 1e37f) || part[q] == 0.f);
+      plain[q] = part[q] > 1e-30f && part[q] < 1e37f;
+      if (plain[q]) total += (double)part[q];
+      all = all && plain[q];
     }
-    if (plain) {
-      total += sum;
-    } else {
-      // squares near the ends of FP32's range (or no numbers): in FP64
-      for (int j = 0; j < VECS; ++j) {
-        const long long lo = (v0 + j * kThreads) * per - head;
+    if (!all) {
+      // squares near the ends of FP32's range, or below it (or no numbers): in
+      // FP64, but for vectors of zeros and those beyond the tensor
+      const uint32_t value_bits = type == SGEMM_TYPE_F32 ? 0x7fffffffu : 0x7fff7fffu;
+      unsigned left = 0;
+#pragma unroll
+      for (int j = 0; j < VECS; ++j)
+        if (!plain[j / 4] &&
+            (whole[j] ? ((raw[j].x | raw[j].y | raw[j].z | raw[j].w) & value_bits) != 0u
+                      : (v0 + j * kThreads) * per - head < n))
+          left |= 1u << j;
+      for (; left != 0u; left &= left - 1) {
+        const long long lo = (v0 + (__ffs(left) - 1) * kThreads) * per - head;
         for (int k = 0; k < per; ++k)
           if (lo + k >= 0 && lo + k < n) {
             const double e = (double)elem_f32(in, lo + k, type);

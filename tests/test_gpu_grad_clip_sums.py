@@ -1,4 +1,6 @@
-"""Squares are summed in FP32 over at most 32 values, whatever the piece a
+"""Sums of squares that FP32 cannot hold.
+
+Squares are summed in FP32 over at most 32 values, whatever the piece a
 thread takes (a list of 64 MB and more takes twice as many vectors).
 
 The first value a thread adds is 1, the others' squares are half an ulp of 1,
@@ -28,3 +30,23 @@ def test_norm_of_values_that_round_away(numel, t, vecs):
     want = math.sqrt(sum(float(c.double().square().sum()) for c in g.split(1 << 24)))
     norm = float(B.clip_grad_norm([g], 1e9))
     assert abs(norm - want) <= 20 * 2.0 ** -24 * want
+
+
+@pytest.mark.parametrize("t,value", [(torch.float32, 1e-24), (torch.float32, 1e-38), (torch.float32, 2.0 ** -149),
+                                     (torch.bfloat16, 1e-30), (torch.float32, 1e-15)])
+@pytest.mark.parametrize("numel", [1, 5, 5000, 1 << 25])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_norm_of_values_whose_squares_vanish(t, value, numel, zeros):
+    """Squares below FP32's range count all the same, between zeros too."""
+    g = torch.full((numel,), value, device="cuda").to(t)
+    if zeros:
+        g.view(-1)[: numel // 2] = -0.0
+    want = math.sqrt(float(g.double().square().sum()))
+    norm = float(B.clip_grad_norm([g], 1e9))
+    # (a subnormal norm is rounded to FP32's last place)
+    assert abs(norm - want) <= 20 * 2.0 ** -24 * want + 2.0 ** -150
+
+
+def test_norm_of_zeros():
+    for numel in (3, 10000, 1 << 25):
+        assert float(B.clip_grad_norm([torch.zeros(numel, device="cuda")], 1.0)) == 0.0
