@@ -25,10 +25,10 @@
 //   kI8Wide  the same integers, already as F16 in the workspace.
 //
 // Accumulation. The tensor core adds into FP32 with truncation, an error that
-// grows with the number of instructions. For 32-bit results a tile's sum is
-// therefore cut into chunks of `chunk` k-slices: each goes to one of two
-// tensor-memory accumulators and is added in registers (round to nearest; for
-// kI8 as 32-bit integers) while the other is filled.
+// grows with the number of instructions. A tile's sum is therefore cut into
+// chunks of `chunk` values of k: each goes to one of two tensor-memory
+// accumulators and is added in registers (round to nearest; for kI8 as 32-bit
+// integers) while the other is filled.
 //
 // Kernel forms (CL): single CTAs, or clusters of two on vertically adjacent
 // tiles whose even CTA issues M = 256 MMAs over both (cta_group::2): each CTA

@@ -520,7 +520,8 @@ typedef enum {
  *
  * type is that of X and W, out_type that of Y: FP32 operands give FP32; BF16
  * and F16 operands give any type. Products are accumulated in FP32 and rounded
- * once; FP32 operands are cut into three BF16 parts each (an error below
+ * once (16-bit results of 16-bit operands leave the tensor cores, which
+ * truncate, every 1024 products); FP32 operands are cut into three BF16 parts each (an error below
  * 2^-23 of |x||w| per product). An FP32 operand that is infinite or NaN makes
  * every output it takes part in NaN; BF16 and F16 follow IEEE arithmetic.
  * beta == 0 never reads Y; alpha == 0 or K == 0 never reads X or W.
