@@ -422,17 +422,18 @@ int run(int src, int type, Params p, Operand op_p, Operand op_q, cudaStream_t st
 
 // Values of k per tensor-memory accumulation. Each instruction truncates its
 // sum: with n of them in one accumulation a 32-bit result is off by 1.4e-8 n
-// (2-norm, relative). Measured: 32 (512 values) 4.5e-7 for 16-bit operands, the
-// gradient of 8 groups of 1024 x (4096 + 1024) in 71 us (16: 2.3e-7 and 82 us,
-// all: 1.7e-6 and 68 us); for kF32, six a step, 36 (96 values) 6e-7 (a sum in
-// FP32 of 2048 products: 8e-7). 16-bit results take 64 (1024 values): 1.1e-6, or
-// 5e-6 where all products have one sign, 2 % of F16's own half unit whatever the
-// length. In one accumulation that share grew with it (131072 rows: 1.5e-5, and
-// 8e-5 of one sign); 8192 x 4096 x 4096 over 8 groups took 190 us so, 194 now.
+// (2-norm, relative). Measured: 16 (256 values) 2.3e-7 for 16-bit operands, where
+// a sum in FP32 is off by 3.3e-7; the gradient of 8 groups of 1024 x (4096 + 1024)
+// in 80 us (24: 3.3e-7 and 72 us, 32: 4.5e-7 and 68 us). For kF32, six a step, 36
+// (96 values) 6e-7 (a sum in FP32 of 2048 products: 8e-7). 16-bit results take 64
+// (1024 values): 1.1e-6, or 5e-6 where all products have one sign, 2 % of F16's own
+// half unit whatever the length. In one accumulation that share grew with it
+// (131072 rows: 1.5e-5, and 8e-5 of one sign); 8192 x 4096 x 4096 over 8 groups took
+// 192 us so, 197 now.
 int accumulation_chunk(int src, int out_type) {
   if (src == kF32) return 96;
   if (src == kI8 || src == kI8Wide) return kExactK;
-  return out_type == kOutF32 ? 512 : 1024;
+  return out_type == kOutF32 ? 256 : 1024;
 }
 
 }  // namespace

@@ -548,7 +548,7 @@ int sgemm_grouped(int op, int type, int out_type, int E, int T, int N, int K, fl
  * gradient of weights stored N x K (op T above), with A = X and B = dY of
  * weights stored K x N. An empty group gives beta * C_e (zeros for beta == 0,
  * without reading C). Types, offsets, accuracy and errors as sgemm_grouped();
- * FP32 results of 16-bit operands leave the tensor cores every 512 rows and
+ * FP32 results of 16-bit operands leave the tensor cores every 256 rows and
  * are added in FP32 with rounding to nearest. The C_e must not overlap.
  */
 int sgemm_grouped_wgrad(int type, int out_type, int E, int T, int M, int N, float alpha,

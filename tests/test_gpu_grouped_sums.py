@@ -36,3 +36,37 @@ def test_long_sums_of_one_sign_are_not_short(kind, t, k):
     assert got.dtype == t
     short, rounded = 64 * 2.0 ** -23 + k / 1024 * 2.0 ** -24, k / 1024 * 2.0 ** -24
     assert bool((got >= (ref * (1 - short)).to(t)).all()) and bool((got <= (ref * (1 + rounded)).to(t)).all())
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("k", [512, 1024, 4096])
+@pytest.mark.parametrize("kind", ["rows", "wgrad"])
+def test_sums_that_lose_all_they_can(kind, t, k):
+    """32-bit results. Every 512th product is 1, and of the others one in 16 is just below 2^-23: added
+    to a sum of 1 or more it is truncated away, in one accumulation 15 times in 256 values, 31 times in 512."""
+    t = TYPES[t]
+    a = torch.zeros(k, dtype=torch.float64)
+    a[::16] = 2.0 ** -11
+    a[::512] = 1.0
+    b = torch.where(a == 1.0, 1.0, 2.0 ** -12 * 255 / 256).double()
+    ref = float(a @ b)
+    a, b = a.to(t).cuda(), b.to(t).cuda()
+    if kind == "rows":
+        off = torch.tensor([0, 256], dtype=torch.int32, device="cuda")
+        got = B.grouped_gemm(a.repeat(256, 1), b.repeat(1, 4096, 1), off, out_dtype=torch.float32)
+    else:
+        off = torch.tensor([0, k], dtype=torch.int32, device="cuda")
+        got = B.grouped_wgrad(a[:, None].repeat(1, 4096), b[:, None].repeat(1, 264), off, out_dtype=torch.float32)
+    assert bool(((got.double() - ref).abs() <= (16 * 2.0 ** -23 + k / 256 * 2.0 ** -24) * ref).all())
+
+
+def test_weight_gradient_is_no_less_exact_than_a_sum_in_fp32():
+    g = torch.Generator(device="cuda").manual_seed(1)
+    a, b = (torch.randn(2048, n, generator=g, device="cuda").bfloat16() for n in (1024, 512))
+    off = torch.tensor([0, 2048], dtype=torch.int32, device="cuda")
+    ref = a.double().mT @ b.double()
+    error = lambda y: float((y.double() - ref).norm() / ref.norm())  # noqa: E731
+    plain = torch.zeros_like(ref, dtype=torch.float32)
+    for r in range(2048):                # one product after another
+        plain.addr_(a[r].float(), b[r].float())
+    assert error(B.grouped_wgrad(a, b, off, out_dtype=torch.float32)[0]) <= error(plain)
