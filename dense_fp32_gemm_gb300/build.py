@@ -13,7 +13,8 @@ library from another configuration list (the tuner's candidate set) without
 touching the product library.
 
 Beside it, csrc_torch/marshal.cpp (the torch conveniences of binding.py) is
-compiled with the host compiler against the installed torch.
+compiled with the host compiler against the installed torch, if there is one;
+the library needs neither.
 """
 from __future__ import annotations
 
@@ -52,27 +53,40 @@ SGEMM_GB300_DEFINE_CONFIG({name})
 MARSHAL_SOURCE = os.path.join(HERE, "csrc_torch", "marshal.cpp")
 
 
+def torch_dir() -> str | None:
+    """Where torch is installed (it is not imported); None without it."""
+    spec = importlib.util.find_spec("torch")
+    return None if spec is None else spec.submodule_search_locations[0]
+
+
 def marshal_path() -> str:
-    """The torch marshalling module built for the installed torch (another
-    version needs another build)."""
-    version = importlib.metadata.version("torch").replace("+", "_")
-    return os.path.join(OUT_DIR, f"_marshal_{version}.so")
+    """The torch marshalling module built for the installed torch and this
+    Python (another version of either needs another build)."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:   # (installed without metadata)
+        import torch
+        version = torch.__version__
+    soabi = sysconfig.get_config_var("SOABI")
+    return os.path.join(OUT_DIR, f"_marshal_{version.replace('+', '_')}.{soabi}.so")
 
 
-def build_marshal() -> str:
+def build_marshal() -> str | None:
     """Compile csrc_torch/marshal.cpp against the installed torch, if it or the
-    torch version changed."""
+    torch or Python version changed; None without torch."""
+    torch_at = torch_dir()
+    if torch_at is None:
+        return None
     path = marshal_path()
     if not _stale(path, [MARSHAL_SOURCE]):
         return path
     os.makedirs(OUT_DIR, exist_ok=True)
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
-    includes = [sysconfig.get_paths()["include"], os.path.join(torch_dir, "include"),
-                os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), cuda]
+    includes = [sysconfig.get_paths()["include"], os.path.join(torch_at, "include"),
+                os.path.join(torch_at, "include", "torch", "csrc", "api", "include"), cuda]
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden"]
     cmd += [f"-I{d}" for d in includes]
-    cmd += [MARSHAL_SOURCE, "-o", path + ".tmp", "-L" + os.path.join(torch_dir, "lib"),
+    cmd += [MARSHAL_SOURCE, "-o", path + ".tmp", "-L" + os.path.join(torch_at, "lib"),
             "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -170,8 +184,6 @@ def build(verbose: bool = False, jobs: int | None = None, config_list: str | Non
         # (a candidate build of the tuner takes the product's marshalling module)
         marshal = ex.submit(build_marshal) if out_dir == OUT_DIR else None
         list(ex.map(compile_one, zip(srcs, objs)))
-        if marshal is not None:
-            marshal.result()
     if verbose:
         for src, log in sorted(logs.items()):
             print(f"== {os.path.basename(src)}\n{log}", file=sys.stderr)
@@ -182,6 +194,8 @@ def build(verbose: bool = False, jobs: int | None = None, config_list: str | Non
         tmp = lib_path + ".tmp"
         subprocess.check_call([tool, "-shared", "-cudart", "static"] + ARCH + objs + ["-o", tmp])
         os.replace(tmp, lib_path)
+    if marshal is not None:
+        marshal.result()          # its failure leaves the library built
     return lib_path
 
 
