@@ -286,6 +286,14 @@ constexpr TileCost kTileCosts[] = {
     {kI8, 128, 1, 460, 1300},
     {kI8Wide, 256, 2, 364, 2500},
 };
+// The costs of a form: those of its own number of CTAs (integers that have been
+// widened cost what F16 operands do).
+TileCost tile_cost(int src, int bq, int cl) {
+  const int as = src == kI8Wide ? k16 : src;
+  for (const TileCost& c : kTileCosts)
+    if (c.src == as && c.bq == bq && c.cl == cl) return c;
+  return kTileCosts[0];   // (every built form has its entry)
+}
 // What cutting a tile along k costs, ns: publishing a part and the rendezvous,
 // and reading one part back (a load of L2 for every 32 columns of a warp; four
 // narrow parts go in one).
@@ -385,9 +393,8 @@ int run(int src, int type, Params p, Operand op_p, Operand op_q, cudaStream_t st
     return SGEMM_ERR_LAUNCH;
   }
   p.partials = reinterpret_cast<float*>(at + pack_p + pack_q);
-  for (const TileCost& c : kTileCosts) {
-    if (c.src != src || c.bq != bq) continue;
-    const double ns = (double)c.slice * slice / 64;
+  {
+    const double ns = (double)tile_cost(src, bq, cl).slice * slice / 64;
     const double sum = (double)(p.wgrad ? p.T / p.E : p.K) / slice;
     p.cut_least = cut_least(sum < 1 ? 1 : sum, (int)ns, bq);
     p.cut_once = (int)(16 * cut_once(bq) / ns) + 1;
