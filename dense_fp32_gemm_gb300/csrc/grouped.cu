@@ -309,8 +309,8 @@ int cut_least(double sum, int slice, int bq) {
 
 // The tile of a call: the one whose list takes least time on the workers it
 // has, by the costs above. The host does not know the groups' sizes: they are
-// taken to be equal but for half a tile of raggedness each.
-Form choose_tile(int src, const Params& p, int sms) {
+// taken to be equal but for half a tile of raggedness each. *ns: that time.
+Form choose_tile(int src, const Params& p, int sms, double* ns) {
   Form best{src, 0, 1};
   double least = 0;
   for (const TileCost& c : kTileCosts) {
@@ -339,7 +339,22 @@ Form choose_tile(int src, const Params& p, int sms) {
       best = Form{src, c.bq, c.cl};
     }
   }
+  *ns = least;
   return best;
+}
+
+// Whether an 8-bit product widens its operands to F16 first, for the widest
+// tiles, or converts them tile by tile: by the times above, the widening at 4 us
+// and 0.65 ns for 1000 values, the copies that the other form may need at 3 us
+// and 0.3. Measured on both sides, us (tile by tile / widened): 512 x 4096 x 4096
+// 32 / 49, 768 47 / 39, 2048 102 / 63; 2048 x 1024 x 4096 32 / 44; 256 x 8191 x 1000
+// (copied) 17 / 21, 384 24 / 22; 512 x 14336 x 4096 86 / 94, 768 131 / 107; 2048 x
+// 512 x 512 9 / 15. Of 54 such sizes it takes the faster side of all.
+bool widen_first(const Params& p, int sms, double tiles_ns, double copied, double values) {
+  double ns = 0;
+  choose_tile(kI8Wide, p, sms, &ns);
+  if (copied > 0) tiles_ns += 3000 + 0.3e-3 * copied;
+  return ns + 4000 + 0.65e-3 * values < tiles_ns;
 }
 
 // The operands as stored. Fills the maps (copying what TMA cannot read), the
@@ -355,10 +370,20 @@ int run(int src, int type, Params p, Operand op_p, Operand op_q, cudaStream_t st
   if (st != SGEMM_OK) return st;
   if (tensor_map_encode() == nullptr) return SGEMM_ERR_LAUNCH;
 
-  const Form t = choose_tile(src, p, sms);
+  const int width = g_width.load(), ctas = g_ctas.load();
+  double ns = 0;
+  Form t = choose_tile(src, p, sms, &ns);
+  if (src == kI8) {
+    const double vp = (double)op_p.rows * op_p.cols, vq = (double)op_q.rows * op_q.cols;
+    const double copied = (op_p.direct() ? 0 : vp) + (op_q.direct() ? 0 : vq);
+    // (256 columns are built for widened operands only)
+    if (width > 0 ? width == 256 : widen_first(p, sms, ns, copied, vp + vq)) {
+      src = kI8Wide;
+      t = choose_tile(src, p, sms, &ns);
+    }
+  }
   int workers = 0;
   const FormEntry* form = nullptr;
-  const int width = g_width.load(), ctas = g_ctas.load();
   if (width > 0 && (!p.wgrad || width >= 64)) form = find_form(dev, sms, src, width, ctas, &workers);
   if (form == nullptr) form = find_form(dev, sms, t.src, t.bq, t.cl, &workers);
   if (form == nullptr && t.cl == 2) form = find_form(dev, sms, t.src, t.bq, 1, &workers);
@@ -563,11 +588,7 @@ SGEMM_API int sgemm_i8(int M, int N, int K, const signed char* A, int lda, const
   p.scale_q = scaleA;
   p.chunk = ragged::accumulation_chunk(ragged::kI8, out_type);
   const Operand w{B, 1, N, K, ldb, 0, 1}, x{A, 1, M, K, lda, 0, 1};
-  // Many rows: both operands are widened to F16 first and the widest tiles run
-  // (4 bytes written and read per weight, against converting a weight tile
-  // once for every 128 rows).
-  const int src = M >= 512 ? ragged::kI8Wide : ragged::kI8;
-  return ragged::run(src, SGEMM_TYPE_F16, p, w, x, static_cast<cudaStream_t>(stream), "i8");
+  return ragged::run(ragged::kI8, SGEMM_TYPE_F16, p, w, x, static_cast<cudaStream_t>(stream), "i8");
 }
 
 SGEMM_API int sgemm_grouped_set_tile(int width, int ctas) {
