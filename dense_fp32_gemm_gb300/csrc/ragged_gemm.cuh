@@ -695,6 +695,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     __syncthreads();  // every role sees the abort word
   }
 
+  bool issued_any = false;   // this thread has issued MMAs
   if (warp < kEpiWarp0) {
     if (G::kMoveRegs) ptx::regs_lower<G::kRegsFew>();
     // ---- warp 0: TMA producer, one thread of it -----------------------------------
@@ -892,7 +893,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     };
     int acc = 0, s = 0;
     uint32_t phase = 0;       // parity of the full barriers to wait for
-    bool issued_any = false, ok = true;
+    bool ok = true;
     const int chunk = p.chunk / SL;
     Unit w;
     for (List list(p, sh, worker, workers); ok && list.next(w);) {
@@ -957,16 +958,6 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
         if (!ok) break;
         commit(&sh->acc_full[buf]);
       }
-    }
-    if (*abort_w != 0 && issued_any) {
-      // wait (bounded) until every MMA issued has completed
-      if (kPair)
-        tc::commit_pair(ptx::smem_addr(&sh->drain));
-      else
-        tc::commit(ptx::smem_addr(&sh->drain));
-      const uint64_t t0 = ptx::global_ns();
-      while (!ptx::mbar_try_wait(ptx::smem_addr(&sh->drain), 0u))
-        if ((long long)(ptx::global_ns() - t0) > cleanup_bound_ns(p.timeout_ns)) break;
     }
     }
     __syncwarp();
@@ -1215,6 +1206,20 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
 
   tc::fence_before_sync();
   __syncthreads();
+  // A CTA that gives up waits (bounded) until every MMA it issued has completed:
+  // here, since any role may be the one that gives up, with the last MMAs in
+  // flight and their issuer done. (Where none has, the epilogue has waited for
+  // all of them.)
+  if (issued_any && *abort_w != 0) {
+    if (kPair)
+      tc::commit_pair(ptx::smem_addr(&sh->drain));
+    else
+      tc::commit(ptx::smem_addr(&sh->drain));
+    const uint64_t t0 = ptx::global_ns();
+    while (!ptx::mbar_try_wait(ptx::smem_addr(&sh->drain), 0u))
+      if ((long long)(ptx::global_ns() - t0) > cleanup_bound_ns(p.timeout_ns)) break;
+  }
+  __syncwarp();
   // the even CTA's MMAs write the odd CTA's tensor memory and read its shared
   // memory: the pair frees its tensor memory together, once both are done
   if (kPair) ptx::cluster_sync();
