@@ -499,8 +499,9 @@ __global__ void __launch_bounds__(NT, 1)
         else
           tc::commit(ptx::smem_addr(&bar->tmem_full[buf]));
       }
-      if (*abort_w && issued_any) {
-        // wait (bounded) until every MMA issued has completed
+      if (issued_any) {
+        // wait (bounded) until every MMA issued has completed: whichever role
+        // gives up, and however late, the CTA does not end before
         if (TWO_SM)
           tc::commit_pair(ptx::smem_addr(&bar->drain));
         else
