@@ -202,7 +202,7 @@ struct Shared {
   uint32_t tmem;
   int abort;
   int last;                     // this CTA arrived last at its cut tile
-  int tiles, dp;                // tiles; how many of them are dealt out whole
+  int dp;                       // tiles that are dealt out whole
   int base, len, cutters;       // slices dealt out: first position, number, workers
   // the scanned groups: first row, rows, number and slice position of the first tile
   int row0[kMaxGroups], rows[kMaxGroups], first[kMaxGroups], pos[kMaxGroups];
@@ -645,7 +645,6 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     __syncwarp();
     if (lane == 0) {
       const int tiles = tiles_before, total = pos_before;
-      sh->tiles = tiles;
       // whole waves first; what is left, one to two waves (or, with fewer tiles
       // than workers, all of them), by slices, unless that saves less time than
       // publishing and adding the parts takes

@@ -58,13 +58,9 @@ bool encode_operand(CUtensorMap* map, const Operand& op, CUtensorMapDataType typ
 struct Form {
   int src, bq, cl;
 };
-// Makes the kernel of a form ready on a device and gives the workers that are
-// resident at once (0: the form is not built, or pairs cannot run); launches it.
-cudaError_t form_workers(int dev, int sms, const Form& f, int* workers);
-cudaError_t form_launch(const Form& f, int workers, const Params& p, const CUtensorMap& mp,
-                        const CUtensorMap& mq, cudaStream_t stream);
-
-// One entry of the table of built kernels (a translation unit per source).
+// One entry of the table of built kernels (a translation unit per source):
+// makes the kernel ready on the current device and gives the workers that are
+// resident at once (0: pairs cannot run); launches it.
 struct FormEntry {
   Form form;
   cudaError_t (*prepare)(int sms, int* workers);
