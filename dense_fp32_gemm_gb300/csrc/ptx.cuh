@@ -95,10 +95,10 @@ __device__ __forceinline__ void fence_proxy_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// True in one lane of a converged warp, always the same one. (The compiler
-// knows that the branch on it has one thread; on `lane == 0` it does not, and
-// issues each bulk copy or tensor instruction in it through a loop over the
-// active lanes.)
+// True in one lane of a converged warp, always the same one. (Issue loops in a
+// branch on it ran faster than on `lane == 0` with a warp-wide vote a slice: 8192
+// x 4096 x 4096 BF16 over 8 groups 174 against 179 us, FP32 2048 x 1024 x 2048 61
+// against 65.)
 __device__ __forceinline__ bool elect_one() {
   uint32_t is;
   asm volatile(

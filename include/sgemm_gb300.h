@@ -36,14 +36,15 @@
  * CUDA graphs: sgemm, sgemm_ex, sgemm_strided_batched, sgemm_3xtf32,
  * sgemm_grouped, sgemm_grouped_wgrad, sgemm_i8 and sgemm_grad_clip can be
  * captured into a graph and replayed, once a call of at least the same size
- * has run on the capturing stream outside the capture (it sets the device up
- * and sizes the stream's workspace; a call that would have to grow it during
- * capture returns SGEMM_ERR_CAPTURE and launches nothing). The graph keeps
- * the stream's workspace: do not replay it concurrently with other work on
- * that stream's workspace. A later call that needs a larger one gets a new
- * block; the one that graphs hold stays allocated until sgemm_shutdown(),
- * after which they must not be replayed. sgemm_noalloc needs no workspace at
- * all.
+ * (for the grouped and 8-bit calls, whose workspace goes by the tile that
+ * their sizes choose: of the same sizes) has run on the capturing stream
+ * outside the capture (it sets the device up and sizes the stream's workspace;
+ * a call that would have to grow it during capture returns SGEMM_ERR_CAPTURE
+ * and launches nothing). The graph keeps the stream's workspace: do not replay
+ * it concurrently with other work on that stream's workspace. A later call
+ * that needs a larger one gets a new block; the one that graphs hold stays
+ * allocated until sgemm_shutdown(), after which they must not be replayed.
+ * sgemm_noalloc needs no workspace at all.
  */
 #ifndef SGEMM_GB300_H
 #define SGEMM_GB300_H
@@ -61,7 +62,7 @@ typedef enum {
   SGEMM_ERR_LAUNCH = -5,            /* CUDA runtime error while launching         */
   SGEMM_ERR_DEVICE_TIMEOUT = -6,    /* a kernel gave up on a bounded wait         */
   SGEMM_ERR_ALLOC = -7,             /* workspace allocation failed                */
-  SGEMM_ERR_MISALIGNED = -8,        /* a matrix pointer is not 4-byte aligned     */
+  SGEMM_ERR_MISALIGNED = -8,        /* a pointer is not aligned to its element type (4 bytes for FP32) */
   SGEMM_ERR_INVALID_VALUE = -9,     /* other invalid argument (config id, buffer) */
   SGEMM_ERR_NOALLOC_CAPACITY = -10, /* sgemm_noalloc: problem needs more scratch
                                        than its fixed buffer holds             */
