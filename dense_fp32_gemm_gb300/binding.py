@@ -413,6 +413,8 @@ def _stream_handle(stream):
 def _ld(t, name):
     if t.dim() != 2 or t.dtype.__repr__() != "torch.float32":
         raise ValueError(f"{name} must be a 2-D float32 tensor")
+    if t.is_neg():
+        raise ValueError(f"{name} is a negated view: call resolve_neg() first")
     if t.size(1) > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must be row-major (unit stride along rows)")
     least = max(t.size(1), 1)

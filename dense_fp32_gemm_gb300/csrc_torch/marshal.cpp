@@ -65,7 +65,11 @@ int type_of(at::ScalarType t, const char* name) {
     default: throw Refusal{std::string(name) + " must be float32, bfloat16 or float16"};
   }
 }
-int type_of(const at::Tensor& t, const char* name) { return type_of(t.scalar_type(), name); }
+int type_of(const at::Tensor& t, const char* name) {
+  // (the imaginary part of a conjugate: what is stored has the other sign)
+  if (t.is_neg()) throw Refusal{std::string(name) + " is a negated view: call resolve_neg() first"};
+  return type_of(t.scalar_type(), name);
+}
 
 int to_int(int64_t v) {
   check(v >= 0 && v <= 0x7fffffff, "sizes must be below 2^31");
@@ -149,7 +153,8 @@ const int* offsets_of(const at::Tensor& t, int64_t groups) {
 }
 
 void vector_of(const at::Tensor& t, int64_t n, const char* what) {
-  check(t.scalar_type() == at::kFloat && t.dim() == 1 && t.size(0) == n && t.is_contiguous(), what);
+  check(t.scalar_type() == at::kFloat && t.dim() == 1 && t.size(0) == n && t.is_contiguous() &&
+            !t.is_neg(), what);
 }
 
 double number(PyObject* o) {
@@ -186,6 +191,7 @@ PyObject* grouped_gemm(PyObject* const* a) {
   check(W.scalar_type() == X.scalar_type(), "X and W must have one type");
   const int* bounds = offsets_of(off, E);
   const int type = type_of(X, "X"), ldx = pitch(X, "X"), ldw = pitch(W, "W");
+  type_of(W, "W");
   at::Tensor Y;
   at::ScalarType out = X.scalar_type();
   if (is_none(a[3])) {
@@ -195,6 +201,7 @@ PyObject* grouped_gemm(PyObject* const* a) {
     Y = tensor(a[3], "Y");
     check(Y.dim() == 2 && Y.size(0) == T && Y.size(1) == N, "shape mismatch");
     pitch(Y, "Y");
+    type_of(Y, "Y");
     out = Y.scalar_type();
   }
   const int out_type = type_of(out, "Y");
@@ -219,6 +226,7 @@ PyObject* grouped_wgrad(PyObject* const* a) {
   check(E >= 0, "offsets must hold one bound more than there are groups");
   const int* bounds = offsets_of(off, E);
   const int type = type_of(A, "A"), lda = pitch(A, "A"), ldb = pitch(B, "B");
+  type_of(B, "B");
   at::Tensor C;
   at::ScalarType out = A.scalar_type();
   if (is_none(a[3])) {
@@ -228,6 +236,7 @@ PyObject* grouped_wgrad(PyObject* const* a) {
     C = tensor(a[3], "C");
     check(C.dim() == 3 && C.size(0) == E && C.size(1) == M && C.size(2) == N, "shape mismatch");
     check_apart(C, pitch(C, "C"));
+    type_of(C, "C");
     out = C.scalar_type();
   }
   const int out_type = type_of(out, "C");
@@ -302,6 +311,7 @@ PyObject* i8_gemm(PyObject* const* a) {
     C = tensor(a[4], "C");
     check(C.dim() == 2 && C.size(0) == M && C.size(1) == N, "shape mismatch");
     pitch(C, "C");
+    type_of(C, "C");
     out = C.scalar_type();
   }
   const int out_type = type_of(out, "C");
@@ -359,6 +369,7 @@ PyObject* clip_grad_norm(PyObject* const* a) {
       const at::Tensor &o = tensor(out[i], "out"), &g = tensor(grads[i], "gradients");
       check(o.is_cuda() && o.get_device() == device, "gradients must be on one CUDA device");
       check(o.is_contiguous(), "gradients must be contiguous");
+      type_of(o, "out");
       check(o.scalar_type() == g.scalar_type() && o.sizes() == g.sizes(),
             "out must have the gradients' types and shapes");
       to[i] = o.data_ptr();

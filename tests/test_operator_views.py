@@ -74,6 +74,25 @@ def test_views_that_do_not_overlap_keep_their_pitch():
             B.grouped_gemm(x, torch.zeros(2, 6, 8), OFF)
 
 
+def negated(*shape):
+    """A view whose values are the stored ones with the other sign, one column of each row."""
+    z = torch.ones(*shape, 2, dtype=torch.complex64)
+    return z.conj().imag[..., :1]
+
+
+def test_negated_views():
+    """What the kernels would read of them has the wrong sign."""
+    x, w, n1 = mat(4, 1), torch.zeros(2, 1, 1), negated(4)
+    assert n1.is_neg() and n1.shape == (4, 1)
+    for call in (lambda: B.grouped_gemm(n1, w, OFF), lambda: B.grouped_gemm(x, negated(2, 1), OFF),
+                 lambda: B.grouped_gemm(x, w, OFF, Y=n1), lambda: B.grouped_wgrad(n1, x, OFF),
+                 lambda: B.grouped_wgrad(x, n1, OFF), lambda: B.grouped_wgrad(x, x, OFF, C=negated(2, 1)),
+                 lambda: B.i8_quantize(n1), lambda: B._ld(n1, "A"),
+                 lambda: B.i8_gemm(x.to(torch.int8), torch.zeros(4), mat(1, 1, torch.int8), torch.zeros(1), C=n1)):
+        with pytest.raises(ValueError, match="negated view"):
+            call()
+
+
 def test_wgrad_groups_that_share_elements():
     a, b = mat(4, 8), mat(4, 6)
     for c in (mat(8, 6).expand(2, 8, 6), torch.zeros(100).as_strided((2, 8, 6), (47, 6, 1)),
