@@ -15,8 +15,9 @@
 // Bound by HBM: the gradients are read twice (the norm is not known before all of
 // them have been) and written once, or read once where nothing is clipped.
 // 400 M BF16 values: 396 us, 6.1 TB/s of 2.4 GB (measured copy: 6.78 TB/s);
-// 60 M FP32 values below the bound: 45 us, 5.3 TB/s; 48 tensors of 1 M FP32
-// values in all: 10.7 us a call, the two launches.
+// 60 M FP32 values below the bound: 47 us, 5.1 TB/s; 48 tensors of 1 M FP32
+// values in all: 10.8 us a call, the two launches. Gradients of zeros only, whose
+// sums have to be told from squares that vanish: 268 MB in 56 us, others in 48.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

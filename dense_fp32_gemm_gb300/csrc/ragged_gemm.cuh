@@ -57,11 +57,13 @@
 //
 // Measured on GB300 (graphs of calls, operands larger than L2 but where noted;
 // peaks: copy 6.78 TB/s, library BF16 product 1945 TFLOP/s):
-//   256 x 2, BF16, 8192 rows in 8 groups, 4096 x 4096: 174 us in short bursts,
-//     1580 TFLOP/s (tensor pipe 73 to 80 % of active cycles), 195 under sustained
-//     power. The rest: ragged edges, the first wave's fill, the parts of the
-//     last tiles. Half the loads from L2 would gain 1-2 %.
-//   16 x 1, BF16: weights of 320 MB stream at 6.2 TB/s. The weights that 16 rows
+//   256 x 2, BF16, 8192 rows in 8 groups, 4096 x 4096: 198 us, 1390 TFLOP/s under
+//     sustained power, 179 in bursts of 2 ms (tensor pipe 68 % of active cycles).
+//     The rest: ragged edges, the first wave's fill, the parts of the last tiles,
+//     the accumulators' reads (2 %). Half the loads from L2 would gain 1-2 %.
+//     The weight gradient of 8 groups of 1024 x (4096 + 1024) in FP32: 80 us, the
+//     reads of the accumulators every 256 rows beside the MMAs 12 of them.
+//   16 x 1, BF16: weights of 335 MB stream at 6.0 TB/s. The weights that 16 rows
 //     choose of 32 of 1024 x 2048 (38 MB) take 13.8 us, DRAM's share 5.6: launch,
 //     scan and first loads are some 3 us, the exchange of the parts of cut
 //     tiles 2.5 us.
@@ -95,7 +97,8 @@ constexpr int kMaxGroups = 1024;   // the scanned offsets live in shared memory
 // Slices by which one that has to be cleared is loaded early. Between a pair's
 // CTAs the clearing takes longer than the loads are ahead of the MMAs (8 groups of
 // 1000 x (4096 + 1024): 57.1 us with 0, 53.4 with 2, 52.8 with 3); a single CTA, with fewer
-// stages, loses more by the one that is held (256 columns: 55.5 and 58.6 us).
+// stages, loses more by the one that is held (256 columns: 55.5 and 58.6 us). All
+// with accumulations of 512 rows; of 256, as they are, the first takes 73 us.
 __host__ __device__ constexpr int early_slices(int cl) { return cl == 2 ? 3 : 0; }
 constexpr int kEpiWarp0 = 4, kEpiWarps = 8, kEpiThreads = kEpiWarps * 32;
 constexpr int kConvWarp0 = kEpiWarp0 + kEpiWarps, kConvWarps = 8;
@@ -796,7 +799,8 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     // to that step's end (the steps beyond are not issued). They are set to zero
     // in both operands (what they hold may be no number) here, ahead of the MMAs:
     // in the MMA warp a tile's last slice cost 0.7 to 1.1 us (8 groups of 1009
-    // x (4096 + 1024) 64.1 us, of 1008 56.9; here 52.9 and 50.5).
+    // x (4096 + 1024) 64.1 us, of 1008 56.9; here 52.9 and 50.5, with accumulations
+    // of 512 rows; 73.5 and 71.6 with those of 256).
     if (!G::kConv && kQmn && warp == 2 && p.wgrad) {
       int it = 0;
       uint32_t tail_phase = 0;
