@@ -106,6 +106,9 @@ def lib() -> ctypes.CDLL:
                 "sgemm_i8": (I, [I, I, I, P, I, P, P, I, P, I, P, I, P]),
                 "sgemm_grouped_set_tile": (I, [I, I]),
                 "sgemm_grad_clip": (I, [I, P, P, P, P, F, P, P]),
+                "sgemm_rms_norm": (I, [I, I, I, P, I, P, I, P, I, F, P, I, P, I, P, P]),
+                "sgemm_rms_norm_i8": (I, [I, I, I, P, I, P, I, P, I, F, P, I, P, I, P, P]),
+                "sgemm_rms_norm_grad": (I, [I, I, I, P, I, P, I, P, I, P, P, I, P, I, P, P]),
                 "sgemm_strided_batched": (I, [I, I, I, I, I, F, P, I, LL, P, I, LL, F, P, I, LL,
                                               I, P]),
             }
@@ -403,6 +406,31 @@ def sgemm_grad_clip(grads, out, sizes, types, max_norm, norm, stream=None) -> in
                                  (ctypes.c_int * n)(*types), max_norm, norm, stream)
 
 
+# ---- the output end of a model: norm, ... -------------------------------------------
+def sgemm_rms_norm(M, N, type, X, ldx, R, ldr, weight, weight_type, eps, H, ldh, Y, ldy, rstd=None,
+                   stream=None) -> int:
+    """H = X + R (R None: X itself), Y = H / sqrt(mean(H^2) + eps) * weight row by
+    row; rstd (may be None) receives 1 / sqrt(...). Returns the status code."""
+    return lib().sgemm_rms_norm(M, N, type, X, ldx, R, ldr, weight, weight_type, eps, H, ldh, Y, ldy,
+                                rstd, stream)
+
+
+def sgemm_rms_norm_i8(M, N, type, X, ldx, R, ldr, weight, weight_type, eps, H, ldh, Q, ldq, scale,
+                      stream=None) -> int:
+    """The same with the norm as 8-bit integers Q and one FP32 scale a row.
+    Returns the status code."""
+    return lib().sgemm_rms_norm_i8(M, N, type, X, ldx, R, ldr, weight, weight_type, eps, H, ldh, Q,
+                                   ldq, scale, stream)
+
+
+def sgemm_rms_norm_grad(M, N, type, dY, lddy, H, ldh, weight, weight_type, rstd, dH, lddh, dX, lddx,
+                        dweight, stream=None) -> int:
+    """Gradients of sgemm_rms_norm; dH, dX and dweight may be None. Returns the
+    status code."""
+    return lib().sgemm_rms_norm_grad(M, N, type, dY, lddy, H, ldh, weight, weight_type, rstd, dH,
+                                     lddh, dX, lddx, dweight, stream)
+
+
 # ---- torch conveniences (marshalling only) ------------------------------------------
 def _stream_handle(stream):
     import torch
@@ -460,8 +488,9 @@ def _native():
     loader = importlib.machinery.ExtensionFileLoader("_marshal", path)
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
     loader.exec_module(module)
-    names = ("sgemm_grouped", "sgemm_grouped_wgrad", "sgemm_i8_quantize", "sgemm_i8", "sgemm_grad_clip")
-    module.bind(*(ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in names), SgemmError)
+    names = ("sgemm_grouped", "sgemm_grouped_wgrad", "sgemm_i8_quantize", "sgemm_i8", "sgemm_grad_clip",
+             "sgemm_rms_norm", "sgemm_rms_norm_i8", "sgemm_rms_norm_grad")
+    module.bind(tuple(ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in names), SgemmError)
     return module
 
 
@@ -501,3 +530,25 @@ def clip_grad_norm(grads, max_norm, out=None, stream=None):
     together, before clipping; out[i] = grads[i] * min(1, max_norm / (norm +
     1e-6)), in place without `out`."""
     return _native().clip_grad_norm(grads, max_norm, out, stream)
+
+
+def rms_norm(X, weight, residual=None, eps=1e-6, Y=None, H=None, rstd=None, stream=None):
+    """(Y, H, rstd): H = X + residual in X's type (X itself without a residual),
+    rstd = 1 / sqrt(mean(H^2) + eps) of each row in float32, Y = H * rstd *
+    weight. weight is of X's type or float32. Y and H may be X or the residual
+    itself."""
+    return _native().rms_norm(X, weight, residual, eps, Y, H, rstd, stream)
+
+
+def rms_norm_i8(X, weight, residual=None, eps=1e-6, Q=None, scale=None, H=None, stream=None):
+    """(Q, scale, H): the same norm as 8-bit integers with one float32 scale a row,
+    as i8_gemm takes them: Q * scale[:, None] stands for H * rstd * weight. A new
+    Q has rows padded to 16 bytes."""
+    return _native().rms_norm_i8(X, weight, residual, eps, Q, scale, H, stream)
+
+
+def rms_norm_grad(dY, H, weight, rstd, dH=None, dX=None, dweight=None, want=(True, True), stream=None):
+    """(dX, dweight): gradients of rms_norm. dX is that of X and of the residual
+    alike; dH is the gradient that reaches H itself. What is not wanted is None."""
+    return _native().rms_norm_grad(dY, H, weight, rstd, dH, dX, dweight, bool(want[0]), bool(want[1]),
+                                   stream)

@@ -1,0 +1,643 @@
+// rms_norm.cu -- sgemm_rms_norm, sgemm_rms_norm_i8 and sgemm_rms_norm_grad:
+// the residual's addition and the root-mean-square norm of its rows, with an
+// output in the input's type or in 8-bit integers with a scale a row, and the
+// gradients.
+//
+// Mathematics, a row of N values at a time:
+//   h = x + r, rounded to the type of x (the sum that the next layer adds to)
+//   rstd = 1 / sqrt(mean(h^2) + eps),  n = h rstd
+//   y = n w
+//   8 bits: u = h w in FP32, step = max|u| / 127, q = rint(u / step), scale =
+//     step rstd. The factor rstd is common to a row, so q does not depend on
+//     it (nor on the order of its sum), and one pass over the row gives both
+//     the sum of squares and the maximum.
+//   gradients of y and h (dy, dh):  dn = dy w,  c = mean(dn n),
+//     dx = dr = rstd (dn - n c) + dh,  dw = sum over rows of dy n.
+#include <cuda_runtime.h>
+#include <cmath>
+#include <mutex>
+#include <stdint.h>
+
+#include "../../include/sgemm_gb300.h"
+#include "elements.cuh"
+#include "ptx.cuh"
+
+#define SGEMM_API extern "C" __attribute__((visibility("default")))
+
+namespace sgemm_gb300 {
+
+int library_device_sms(int dev, int* sms);
+std::unique_lock<std::mutex> library_lock();
+int library_workspace(int dev, cudaStream_t stream, size_t floats, size_t nflags, float** scratch,
+                      int** status, uint32_t** flags, uint32_t* epoch, uint32_t** counters);
+
+namespace rows {
+namespace {
+
+constexpr int kMaxThreads = 512;
+constexpr uint32_t kAll = 0xffffffffu;
+
+struct NormArgs {
+  int M, N;
+  const void *x, *r, *w;   // r: null without a residual
+  long long ldx, ldr;
+  void* h;                 // null: not stored (then r is null)
+  long long ldh;
+  void* y;                 // E, or signed char (8 bits)
+  long long ldy;
+  float* rstd;             // may be null
+  float* scale;            // 8 bits
+  float eps;
+  int wide_q;              // 8 bits: rows of q aligned to a piece's integers
+};
+
+// Sum and maximum over the block, the same in every thread and in a fixed
+// order. `buf` alternates between the two halves of the array from one call to
+// the next, so one barrier a call is enough.
+struct Reduced {
+  float sum;
+  uint32_t most;
+};
+__device__ __forceinline__ Reduced reduce(float sum, uint32_t most, float2 (*part)[kMaxThreads / 32],
+                                          int& buf) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+  most = __reduce_max_sync(kAll, most);
+  const int warps = (int)blockDim.x >> 5;
+  if (warps == 1) return {sum, most};
+  if ((threadIdx.x & 31) == 0)
+    part[buf][threadIdx.x >> 5] = make_float2(sum, __uint_as_float(most));
+  __syncthreads();
+  sum = 0.f;
+  most = 0;
+  for (int i = 0; i < warps; ++i) {
+    const float2 p = part[buf][i];
+    sum += p.x;
+    most = max(most, __float_as_uint(p.y));
+  }
+  buf ^= 1;
+  return {sum, most};
+}
+
+// q = rint(u / step), the quotient rounded to FP32 first. u * inv, inv = 1 /
+// step, is within 2^-22 of it (relative; |u / step| <= 127), so the two round to
+// the same integer unless the product lies that near to the middle of two.
+__device__ __forceinline__ int quotient(float u, float step, float inv) {
+  const float t = u * inv, n = rintf(t);
+  // (also for no number)
+  if (!(fabsf(t - n) <= 0.5f - 1e-4f) || !(inv < 1e37f))
+    // (a step below FP32's normal numbers may be far below max|u| / 127)
+    return __float2int_rn(fminf(fmaxf(__fdiv_rn(u, step), -127.f), 127.f));
+  return (int)n;
+}
+
+// A row per block, in pieces of VW elements (16 bytes, or one element where
+// something is not aligned). Up to HELD pieces a thread stay in registers
+// between the pass that sums and the pass that writes; what is left of a longer
+// row is read again (the thread's own h, or x).
+template <typename E, typename W, int VW, int HELD, bool I8>
+__global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a) {
+  __shared__ float2 part[2][kMaxThreads / 32];
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const E* x = static_cast<const E*>(a.x);
+  const E* r = static_cast<const E*>(a.r);
+  const W* w = static_cast<const W*>(a.w);
+  E* h = static_cast<E*>(a.h);
+  // (places in a row pass 32 bits before they end their loops)
+  const long long step_c = (long long)blockDim.x * VW, c0 = threadIdx.x * VW, N = a.N;
+  const float inv_n = 1.f / (float)a.N;
+  int buf = 0;
+  for (long long m = blockIdx.x; m < a.M; m += gridDim.x) {
+    float sum = 0.f;
+    uint32_t most = 0;
+    auto take = [&](long long c) {
+      Piece<E, VW> p = load<E, VW>(x + m * a.ldx + c);
+      if (r != nullptr) {
+        const Piece<E, VW> q = load<E, VW>(r + m * a.ldr + c);
+#pragma unroll
+        for (int j = 0; j < VW; ++j) p.e[j] = from_f32<E>(to_f32(p.e[j]) + to_f32(q.e[j]));
+      }
+      return p;
+    };
+    auto add = [&](const Piece<E, VW>& p, long long c) {
+      if (h != nullptr) store<E, VW>(h + m * a.ldh + c, p);
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < VW; ++j) s = fmaf(to_f32(p.e[j]), to_f32(p.e[j]), s);
+      sum += s;
+      if (I8) {
+        float v[VW];
+        load_vector<W, VW>(w + c, v);
+        // as bits: a NaN is above infinity, so either survives
+#pragma unroll
+        for (int j = 0; j < VW; ++j)
+          most = max(most, __float_as_uint(to_f32(p.e[j]) * v[j]) & 0x7fffffffu);
+      }
+    };
+    Piece<E, VW> held[HELD];
+#pragma unroll
+    for (int i = 0; i < HELD; ++i)
+      if (c0 + i * step_c < N) held[i] = take(c0 + i * step_c);
+#pragma unroll
+    for (int i = 0; i < HELD; ++i)
+      if (c0 + i * step_c < N) add(held[i], c0 + i * step_c);
+    for (long long c = c0 + HELD * step_c; c < N; c += step_c) add(take(c), c);
+    // the row's values once more: those that were not held from h, or x
+    auto each = [&](auto&& f) {
+#pragma unroll
+      for (int i = 0; i < HELD; ++i)
+        if (c0 + i * step_c < N) f(held[i], c0 + i * step_c);
+      for (long long c = c0 + HELD * step_c; c < N; c += step_c)
+        f(load<E, VW>(h != nullptr ? h + m * a.ldh + c : x + m * a.ldx + c), c);
+    };
+    Reduced t = reduce(sum, most, part, buf);
+    // Squares beyond FP32's range (values above 1e19): once more on values that
+    // are scaled down. eps is at least 1e-30, so squares below the range do not count.
+    float down = 1.f;
+    if (!(t.sum <= 3e38f)) {
+      down = 0x1p-70f;
+      sum = 0.f;
+      each([&](const Piece<E, VW>& p, long long) {
+#pragma unroll
+        for (int j = 0; j < VW; ++j) {
+          const float v = to_f32(p.e[j]) * down;
+          sum = fmaf(v, v, sum);
+        }
+      });
+      t.sum = reduce(sum, 0, part, buf).sum;
+    }
+    const float rstd = 1.f / sqrtf(t.sum * inv_n + a.eps * down * down);
+    if (threadIdx.x == 0 && a.rstd != nullptr) a.rstd[m] = rstd * down;
+    if (!I8) {
+      E* y = static_cast<E*>(a.y) + m * a.ldy;
+      each([&](const Piece<E, VW>& p, long long c) {
+        float v[VW];
+        load_vector<W, VW>(w + c, v);
+        Piece<E, VW> o;
+#pragma unroll
+        for (int j = 0; j < VW; ++j) o.e[j] = from_f32<E>(to_f32(p.e[j]) * down * rstd * v[j]);
+        store<E, VW>(y + c, o);
+      });
+    } else {
+      const float step = __fdiv_rn(__uint_as_float(t.most), 127.f);
+      const float inv = step > 0.f ? 1.f / step : 0.f;
+      const bool none = !(step > 0.f && step <= 3e38f);   // zeros, or no numbers
+      if (threadIdx.x == 0) a.scale[m] = step * down * rstd;
+      signed char* q = static_cast<signed char*>(a.y) + m * a.ldy;
+      each([&](const Piece<E, VW>& p, long long c) {
+        float v[VW];
+        load_vector<W, VW>(w + c, v);
+        uint32_t b[VW];
+#pragma unroll
+        for (int j = 0; j < VW; ++j)
+          b[j] = none ? 0u : (uint32_t)quotient(to_f32(p.e[j]) * v[j], step, inv) & 0xffu;
+        if (VW > 1 && a.wide_q) {
+          uint32_t o[VW / 4 > 0 ? VW / 4 : 1];
+#pragma unroll
+          for (int j = 0; j < VW / 4; ++j)
+            o[j] = b[4 * j] | b[4 * j + 1] << 8 | b[4 * j + 2] << 16 | b[4 * j + 3] << 24;
+          if constexpr (VW == 8)
+            *reinterpret_cast<uint2*>(q + c) = make_uint2(o[0], o[1]);
+          else
+            *reinterpret_cast<uint32_t*>(q + c) = o[0];
+        } else {
+#pragma unroll
+          for (int j = 0; j < VW; ++j) q[c + j] = (signed char)b[j];
+        }
+      });
+    }
+  }
+}
+
+struct GradArgs {
+  int M, N;
+  const void *dy, *h, *w, *dh;   // dh: may be null
+  long long lddy, ldh, lddh;
+  const float* rstd;
+  void* dx;                      // may be null
+  long long lddx;
+  float* partial;                // gridDim.x rows of N sums for dw; null: not formed here
+};
+
+// A row per block at a time, every thread at the same places in each, so that
+// its part of dw stays in registers over all rows of the block. DW: the row
+// fits into HELD pieces a thread and dw's parts are formed.
+template <typename E, typename W, int VW, int HELD, bool DW>
+__global__ void __launch_bounds__(kMaxThreads) norm_grad_kernel(const GradArgs a) {
+  __shared__ float2 part[2][kMaxThreads / 32];
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const E* dy = static_cast<const E*>(a.dy);
+  const E* h = static_cast<const E*>(a.h);
+  const E* dh = static_cast<const E*>(a.dh);
+  const W* w = static_cast<const W*>(a.w);
+  E* dx = static_cast<E*>(a.dx);
+  const long long step_c = (long long)blockDim.x * VW, c0 = threadIdx.x * VW, N = a.N;
+  const float inv_n = 1.f / (float)a.N;
+  int buf = 0;
+  float dw[DW ? HELD : 1][VW];
+#pragma unroll
+  for (int i = 0; i < (DW ? HELD : 1); ++i)
+#pragma unroll
+    for (int j = 0; j < VW; ++j) dw[i][j] = 0.f;
+  for (long long m = blockIdx.x; m < a.M; m += gridDim.x) {
+    const float rstd = a.rstd[m];
+    Piece<E, VW> g[HELD], v[HELD], d[HELD];
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+      const long long c = c0 + i * step_c;
+      if (c >= N) continue;
+      g[i] = load<E, VW>(dy + m * a.lddy + c);
+      v[i] = load<E, VW>(h + m * a.ldh + c);
+      if (dh != nullptr) d[i] = load<E, VW>(dh + m * a.lddh + c);
+    }
+    float sum = 0.f;
+    auto add = [&](const Piece<E, VW>& g, const Piece<E, VW>& v, long long c) {
+      float wv[VW], s = 0.f;
+      load_vector<W, VW>(w + c, wv);
+#pragma unroll
+      for (int j = 0; j < VW; ++j)
+        s = fmaf(to_f32(g.e[j]) * wv[j], to_f32(v.e[j]) * rstd, s);
+      sum += s;
+    };
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+      const long long c = c0 + i * step_c;
+      if (c >= N) continue;
+      add(g[i], v[i], c);
+      if (DW) {
+#pragma unroll
+        for (int j = 0; j < VW; ++j)
+          dw[i][j] = fmaf(to_f32(g[i].e[j]), to_f32(v[i].e[j]) * rstd, dw[i][j]);
+      }
+    }
+    if (!DW)
+      for (long long c = c0 + HELD * step_c; c < N; c += step_c)
+        add(load<E, VW>(dy + m * a.lddy + c), load<E, VW>(h + m * a.ldh + c), c);
+    if (dx == nullptr) continue;
+    const float mean = reduce(sum, 0, part, buf).sum * inv_n;
+    auto put = [&](const Piece<E, VW>& g, const Piece<E, VW>& v, const Piece<E, VW>& d, long long c) {
+      float wv[VW];
+      load_vector<W, VW>(w + c, wv);
+      Piece<E, VW> o;
+#pragma unroll
+      for (int j = 0; j < VW; ++j) {
+        const float t = rstd * fmaf(-mean, to_f32(v.e[j]) * rstd, to_f32(g.e[j]) * wv[j]);
+        o.e[j] = from_f32<E>(dh != nullptr ? t + to_f32(d.e[j]) : t);
+      }
+      store<E, VW>(dx + m * a.lddx + c, o);
+    };
+#pragma unroll
+    for (int i = 0; i < HELD; ++i)
+      if (c0 + i * step_c < N) put(g[i], v[i], d[i], c0 + i * step_c);
+    if (!DW)
+      for (long long c = c0 + HELD * step_c; c < N; c += step_c)
+        put(load<E, VW>(dy + m * a.lddy + c), load<E, VW>(h + m * a.ldh + c),
+            dh != nullptr ? load<E, VW>(dh + m * a.lddh + c) : Piece<E, VW>{}, c);
+  }
+  if (DW && a.partial != nullptr) {
+    float* p = a.partial + blockIdx.x * N;
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+      const long long c = c0 + i * step_c;
+      if (c >= N) continue;
+      if constexpr (VW == 1) {
+        p[c] = dw[i][0];
+      } else {
+#pragma unroll
+        for (int j = 0; j < VW; j += 4)
+          *reinterpret_cast<float4*>(p + c + j) =
+              make_float4(dw[i][j], dw[i][j + 1], dw[i][j + 2], dw[i][j + 3]);
+      }
+    }
+  }
+}
+
+// Rows too long for registers: dw's parts a column a thread, over the rows of a
+// slab (slab s has the rows s, s + slabs, ...).
+constexpr int kColumnThreads = 256;
+template <typename E>
+__global__ void __launch_bounds__(kColumnThreads) column_kernel(const GradArgs a, int slabs) {
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const long long columns = (a.N + kColumnThreads - 1ll) / kColumnThreads;
+  for (long long b = blockIdx.x; b < columns * slabs; b += gridDim.x) {
+    const long long slab = b / columns, c = (b - slab * columns) * kColumnThreads + threadIdx.x;
+    if (c >= a.N) continue;
+    const E* dy = static_cast<const E*>(a.dy) + c;
+    const E* h = static_cast<const E*>(a.h) + c;
+    float sum = 0.f;
+#pragma unroll 4
+    for (long long m = slab; m < a.M; m += slabs)
+      sum = fmaf(to_f32(dy[m * a.lddy]), to_f32(h[m * a.ldh]) * a.rstd[m], sum);
+    a.partial[slab * a.N + c] = sum;
+  }
+}
+
+// dw[c] = sum of the parts in their order: 32 columns a block, 8 threads a
+// column, each the parts of its own residue.
+constexpr int kSumLanes = 8;
+template <typename W>
+__global__ void __launch_bounds__(32 * kSumLanes)
+    sum_kernel(const float* partial, int parts, int N, W* dw) {
+  __shared__ float s[kSumLanes][32];
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
+  for (long long c0 = blockIdx.x * 32ll; c0 < N; c0 += gridDim.x * 32ll) {
+    const long long c = c0 + lane;
+    float sum = 0.f;
+    if (c < N) {
+#pragma unroll 8
+      for (int p = group; p < parts; p += kSumLanes) sum += __ldcg(partial + (long long)p * N + c);
+    }
+    s[group][lane] = sum;
+    __syncthreads();
+    if (group == 0 && c < N) {
+#pragma unroll
+      for (int g = 1; g < kSumLanes; ++g) sum += s[g][lane];
+      dw[c] = from_f32<W>(sum);
+    }
+    __syncthreads();
+  }
+}
+
+template <typename... A>
+cudaError_t launch(void (*kernel)(A...), long long blocks, int threads, cudaStream_t stream,
+                   std::common_type_t<A>... args) {
+  cudaLaunchConfig_t lc = {};
+  cudaLaunchAttribute la[1];
+  la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  la[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.gridDim = dim3((unsigned)blocks);
+  lc.blockDim = dim3((unsigned)threads);
+  lc.stream = stream;
+  lc.attrs = la;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, kernel, args...);
+}
+
+// Threads of a row: a piece each while that leaves SMs idle otherwise (few
+// rows: latency), else as many pieces as are held, at most kMaxThreads.
+int threads_of(long long pieces, int held, bool few) {
+  const long long want = few ? pieces : (pieces + held - 1) / held;
+  const long long t = (want + 31) / 32 * 32;
+  return (int)(t < 32 ? 32 : (t > kMaxThreads ? kMaxThreads : t));
+}
+int blocks_of(int M, int threads, int sms, int per_sm) {
+  const int fit = sms * (per_sm * 256 / threads > 0 ? per_sm * 256 / threads : 1);
+  return M < fit ? M : fit;
+}
+
+bool aligned(const void* p, long long ld, int elem, int bytes) {
+  return p == nullptr ||
+         ((reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0 && ld * elem % bytes == 0);
+}
+
+// HELD of both kernels: 2 pieces where a row has at most that for every thread
+// of half a block, else 4; 8 single elements.
+template <typename E, typename W, bool I8>
+cudaError_t forward(NormArgs a, int sms, cudaStream_t stream) {
+  constexpr int VW = 16 / (int)sizeof(E);
+  const bool vec = aligned(a.x, a.ldx, sizeof(E), 16) && aligned(a.r, a.ldr, sizeof(E), 16) &&
+                   aligned(a.h, a.ldh, sizeof(E), 16) && aligned(a.w, 0, sizeof(W), 16) &&
+                   a.N % VW == 0 && (I8 || aligned(a.y, a.ldy, sizeof(E), 16));
+  a.wide_q = I8 && aligned(a.y, a.ldy, 1, VW);
+  const bool few = a.M < 2 * sms;
+  if (!vec) {
+    const int t = threads_of(a.N, 8, few);
+    return launch(norm_kernel<E, W, 1, 8, I8>, blocks_of(a.M, t, sms, 6), t, stream, a);
+  }
+  const long long pieces = a.N / VW;
+  if (pieces <= 2 * 256 || (few && pieces <= 2 * kMaxThreads)) {
+    const int t = threads_of(pieces, 2, few);
+    return launch(norm_kernel<E, W, VW, 2, I8>, blocks_of(a.M, t, sms, 6), t, stream, a);
+  }
+  const int t = threads_of(pieces, 4, few);
+  return launch(norm_kernel<E, W, VW, 4, I8>, blocks_of(a.M, t, sms, 4), t, stream, a);
+}
+
+template <typename E, typename W>
+cudaError_t backward(GradArgs a, W* dw, float* partial, int blocks, int sms, cudaStream_t stream,
+                     int threads, bool vec, int held) {
+  constexpr int VW = 16 / (int)sizeof(E);
+  a.partial = partial;
+  cudaError_t e = cudaSuccess;
+  if (held != 0) {
+    e = !vec ? launch(norm_grad_kernel<E, W, 1, 8, true>, blocks, threads, stream, a)
+        : held == 2 ? launch(norm_grad_kernel<E, W, VW, 2, true>, blocks, threads, stream, a)
+                    : launch(norm_grad_kernel<E, W, VW, 4, true>, blocks, threads, stream, a);
+  } else {
+    if (a.dx != nullptr)
+      e = vec ? launch(norm_grad_kernel<E, W, VW, 4, false>, blocks_of(a.M, threads, sms, 4), threads, stream, a)
+              : launch(norm_grad_kernel<E, W, 1, 8, false>, blocks_of(a.M, threads, sms, 4), threads, stream, a);
+    if (e == cudaSuccess && dw != nullptr) {
+      const long long all = (a.N + kColumnThreads - 1ll) / kColumnThreads * blocks;
+      e = launch(column_kernel<E>, all < sms * 8ll ? all : sms * 8ll, kColumnThreads, stream, a, blocks);
+    }
+  }
+  if (e == cudaSuccess && dw != nullptr) {
+    const long long all = (a.N + 31ll) / 32;
+    e = launch(sum_kernel<W>, all < sms * 8ll ? all : sms * 8ll, 32 * kSumLanes, stream,
+               static_cast<const float*>(partial), blocks, a.N, dw);
+  }
+  return e;
+}
+
+int elem_bytes(int type) { return type == SGEMM_TYPE_F32 ? 4 : 2; }
+bool type_ok(int type) {
+  return type == SGEMM_TYPE_F32 || type == SGEMM_TYPE_BF16 || type == SGEMM_TYPE_F16;
+}
+bool misaligned(const void* p, int bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) != 0;
+}
+
+int device(int* sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return SGEMM_ERR_LAUNCH;
+  }
+  return library_device_sms(dev, sms);
+}
+
+int done(cudaError_t e) {
+  if (e == cudaSuccess) return SGEMM_OK;
+  cudaGetLastError();
+  return SGEMM_ERR_LAUNCH;
+}
+
+template <bool I8>
+int run_forward(int type, int weight_type, const NormArgs& a, cudaStream_t stream) {
+  int sms = 0;
+  const int st = device(&sms);
+  if (st != SGEMM_OK) return st;
+  using B = __nv_bfloat16;
+  if (type == SGEMM_TYPE_F32) return done(forward<float, float, I8>(a, sms, stream));
+  if (type == SGEMM_TYPE_BF16)
+    return done(weight_type == SGEMM_TYPE_F32 ? forward<B, float, I8>(a, sms, stream)
+                                              : forward<B, B, I8>(a, sms, stream));
+  return done(weight_type == SGEMM_TYPE_F32 ? forward<__half, float, I8>(a, sms, stream)
+                                            : forward<__half, __half, I8>(a, sms, stream));
+}
+
+// Checks that the three calls share; `ld`s are of the matrices that are given.
+int check(int M, int N, int type, int weight_type) {
+  if (!type_ok(type) || (weight_type != type && weight_type != SGEMM_TYPE_F32))
+    return SGEMM_ERR_INVALID_VALUE;
+  return M < 0 || N < 0 ? SGEMM_ERR_INVALID_DIM : SGEMM_OK;
+}
+bool short_ld(const void* p, int ld, int N) { return p != nullptr && ld < (N > 1 ? N : 1); }
+bool eps_ok(float eps) { return eps >= 1e-30f && eps <= 3e38f; }
+
+}  // namespace
+}  // namespace rows
+}  // namespace sgemm_gb300
+
+using namespace sgemm_gb300;
+
+SGEMM_API int sgemm_rms_norm(int M, int N, int type, const void* X, int ldx, const void* R, int ldr,
+                             const void* weight, int weight_type, float eps, void* H, int ldh,
+                             void* Y, int ldy, float* rstd, void* stream) {
+  int st = rows::check(M, N, type, weight_type);
+  if (st != SGEMM_OK) return st;
+  if (!rows::eps_ok(eps)) return SGEMM_ERR_INVALID_VALUE;
+  const int least = N > 1 ? N : 1;
+  if (ldx < least || ldy < least || rows::short_ld(R, ldr, N) || rows::short_ld(H, ldh, N))
+    return SGEMM_ERR_INVALID_LD;
+  if (M == 0 || N == 0) return SGEMM_OK;
+  if (X == nullptr || weight == nullptr || Y == nullptr || (R != nullptr && H == nullptr))
+    return SGEMM_ERR_NULL_PTR;
+  const int eb = rows::elem_bytes(type);
+  if (rows::misaligned(X, eb) || rows::misaligned(R, eb) || rows::misaligned(H, eb) ||
+      rows::misaligned(Y, eb) || rows::misaligned(weight, rows::elem_bytes(weight_type)) ||
+      rows::misaligned(rstd, 4))
+    return SGEMM_ERR_MISALIGNED;
+  rows::NormArgs a = {};
+  a.M = M;
+  a.N = N;
+  a.x = X;
+  a.ldx = ldx;
+  a.r = R;
+  a.ldr = ldr;
+  a.w = weight;
+  a.h = R != nullptr ? H : nullptr;
+  a.ldh = ldh;
+  a.y = Y;
+  a.ldy = ldy;
+  a.rstd = rstd;
+  a.eps = eps;
+  return rows::run_forward<false>(type, weight_type, a, static_cast<cudaStream_t>(stream));
+}
+
+SGEMM_API int sgemm_rms_norm_i8(int M, int N, int type, const void* X, int ldx, const void* R,
+                                int ldr, const void* weight, int weight_type, float eps, void* H,
+                                int ldh, signed char* Q, int ldq, float* scale, void* stream) {
+  int st = rows::check(M, N, type, weight_type);
+  if (st != SGEMM_OK) return st;
+  if (!rows::eps_ok(eps)) return SGEMM_ERR_INVALID_VALUE;
+  const int least = N > 1 ? N : 1;
+  if (ldx < least || ldq < least || rows::short_ld(R, ldr, N) || rows::short_ld(H, ldh, N))
+    return SGEMM_ERR_INVALID_LD;
+  if (M == 0 || N == 0) return SGEMM_OK;
+  if (X == nullptr || weight == nullptr || Q == nullptr || scale == nullptr ||
+      (R != nullptr && H == nullptr))
+    return SGEMM_ERR_NULL_PTR;
+  const int eb = rows::elem_bytes(type);
+  if (rows::misaligned(X, eb) || rows::misaligned(R, eb) || rows::misaligned(H, eb) ||
+      rows::misaligned(weight, rows::elem_bytes(weight_type)) || rows::misaligned(scale, 4))
+    return SGEMM_ERR_MISALIGNED;
+  rows::NormArgs a = {};
+  a.M = M;
+  a.N = N;
+  a.x = X;
+  a.ldx = ldx;
+  a.r = R;
+  a.ldr = ldr;
+  a.w = weight;
+  a.h = R != nullptr ? H : nullptr;
+  a.ldh = ldh;
+  a.y = Q;
+  a.ldy = ldq;
+  a.scale = scale;
+  a.eps = eps;
+  return rows::run_forward<true>(type, weight_type, a, static_cast<cudaStream_t>(stream));
+}
+
+SGEMM_API int sgemm_rms_norm_grad(int M, int N, int type, const void* dY, int lddy, const void* H,
+                                  int ldh, const void* weight, int weight_type, const float* rstd,
+                                  const void* dH, int lddh, void* dX, int lddx, void* dweight,
+                                  void* stream_) {
+  int st = rows::check(M, N, type, weight_type);
+  if (st != SGEMM_OK) return st;
+  const int least = N > 1 ? N : 1;
+  if (lddy < least || ldh < least || rows::short_ld(dH, lddh, N) || rows::short_ld(dX, lddx, N))
+    return SGEMM_ERR_INVALID_LD;
+  if (N == 0 || (dX == nullptr && dweight == nullptr)) return SGEMM_OK;
+  if (M > 0 && (dY == nullptr || H == nullptr || weight == nullptr || rstd == nullptr))
+    return SGEMM_ERR_NULL_PTR;
+  const int eb = rows::elem_bytes(type), wb = rows::elem_bytes(weight_type);
+  if (rows::misaligned(dY, eb) || rows::misaligned(H, eb) || rows::misaligned(dH, eb) ||
+      rows::misaligned(dX, eb) || rows::misaligned(weight, wb) || rows::misaligned(dweight, wb) ||
+      rows::misaligned(rstd, 4))
+    return SGEMM_ERR_MISALIGNED;
+  int sms = 0, dev = 0;
+  st = rows::device(&sms);
+  if (st != SGEMM_OK) return st;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if (M == 0) {   // no rows: dweight is zero
+    if (dweight == nullptr) return SGEMM_OK;
+    return rows::done(cudaMemsetAsync(dweight, 0, (size_t)N * wb, stream));
+  }
+  rows::GradArgs a = {};
+  a.M = M;
+  a.N = N;
+  a.dy = dY;
+  a.lddy = lddy;
+  a.h = H;
+  a.ldh = ldh;
+  a.w = weight;
+  a.rstd = rstd;
+  a.dh = dX != nullptr ? dH : nullptr;
+  a.lddh = lddh;
+  a.dx = dX;
+  a.lddx = lddx;
+  const int vw = 16 / eb;
+  const bool vec = rows::aligned(dY, lddy, eb, 16) && rows::aligned(H, ldh, eb, 16) &&
+                   rows::aligned(dH, lddh, eb, 16) && rows::aligned(dX, lddx, eb, 16) &&
+                   rows::aligned(weight, 0, wb, 16) && N % vw == 0;
+  const long long pieces = vec ? N / vw : N;
+  // pieces that a thread holds of a row; 0: the row is too long for that
+  const int held = !vec ? (pieces <= 8 * rows::kMaxThreads ? 8 : 0)
+                        : (pieces <= 2 * 256 ? 2 : (pieces <= 4 * rows::kMaxThreads ? 4 : 0));
+  const int threads = rows::threads_of(pieces, held == 0 ? (vec ? 4 : 8) : held, M < 2 * sms);
+  // blocks (each makes a part of dw), or slabs of rows
+  int blocks = 0;
+  if (held != 0) {
+    blocks = rows::blocks_of(M, threads, sms, held == 2 ? 4 : 2);
+  } else {
+    const int fill = sms * 8 / (int)((N + rows::kColumnThreads - 1ll) / rows::kColumnThreads) + 1;
+    blocks = M < fill ? M : fill;
+  }
+  std::unique_lock<std::mutex> lock;
+  float* partial = nullptr;
+  if (dweight != nullptr) {
+    if (cudaGetDevice(&dev) != cudaSuccess) return rows::done(cudaErrorInvalidDevice);
+    lock = library_lock();   // to the last launch
+    int* status = nullptr;
+    st = library_workspace(dev, stream, (size_t)blocks * N, 0, &partial, &status, nullptr, nullptr,
+                           nullptr);
+    if (st != SGEMM_OK) return st;
+  }
+  using B = __nv_bfloat16;
+  auto go = [&](auto e, auto w) {
+    using E = decltype(e);
+    using W = decltype(w);
+    return rows::done(rows::backward<E, W>(a, static_cast<W*>(dweight), partial, blocks, sms, stream,
+                                           threads, vec, held));
+  };
+  if (type == SGEMM_TYPE_F32) return go(0.f, 0.f);
+  if (type == SGEMM_TYPE_BF16) return weight_type == SGEMM_TYPE_F32 ? go(B{}, 0.f) : go(B{}, B{});
+  return weight_type == SGEMM_TYPE_F32 ? go(__half{}, 0.f) : go(__half{}, __half{});
+}

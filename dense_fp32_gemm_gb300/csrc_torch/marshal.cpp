@@ -33,6 +33,12 @@ struct Functions {
             const float*, int, void*, int, void*);
   int (*clip)(int, const void* const*, void* const*, const long long*, const int*, float, float*,
               void*);
+  int (*norm)(int, int, int, const void*, int, const void*, int, const void*, int, float, void*, int,
+              void*, int, float*, void*);
+  int (*norm_i8)(int, int, int, const void*, int, const void*, int, const void*, int, float, void*,
+                 int, signed char*, int, float*, void*);
+  int (*norm_grad)(int, int, int, const void*, int, const void*, int, const void*, int, const float*,
+                   const void*, int, void*, int, void*, void*);
 } fn;
 PyObject* g_error = nullptr;   // SgemmError(status, name)
 
@@ -250,6 +256,14 @@ PyObject* grouped_wgrad(PyObject* const* a) {
   return result(a[3], C);
 }
 
+// 8-bit integers of X's shape, rows padded to 16 bytes, so that sgemm_i8 reads
+// them in place.
+at::Tensor padded_i8(const at::Tensor& X) {
+  const int64_t M = X.size(0), K = X.size(1), ld = (K + 15) / 16 * 16;
+  const auto options = X.options().dtype(at::kChar).requires_grad(false);
+  return ld == K ? at::empty({M, K}, options) : at::empty_strided({M, K}, {ld, 1}, options);
+}
+
 // (X, Q, scale, stream)
 PyObject* i8_quantize(PyObject* const* a) {
   const at::Tensor& X = tensor(a[0], "X");
@@ -269,12 +283,7 @@ PyObject* i8_quantize(PyObject* const* a) {
   }
   {
     const Launch on(a[3], {&X});
-    if (!Q.defined()) {
-      // rows padded to 16 bytes, so that sgemm_i8 reads them in place
-      const int64_t ld = (K + 15) / 16 * 16;
-      const auto options = X.options().dtype(at::kChar).requires_grad(false);
-      Q = ld == K ? at::empty({M, K}, options) : at::empty_strided({M, K}, {ld, 1}, options);
-    }
+    if (!Q.defined()) Q = padded_i8(X);
     if (!scale.defined())
       scale = at::empty({M}, X.options().dtype(at::kFloat).requires_grad(false));
     on.check_device(Q);
@@ -326,6 +335,187 @@ PyObject* i8_gemm(PyObject* const* a) {
                        pitch(C, "C"), on.handle());
   if (st != 0) throw Status{st, "sgemm_i8"};
   return result(a[4], C);
+}
+
+// A tuple of n objects; takes their references.
+template <typename... O>
+PyObject* tuple_of(O*... objects) {
+  PyObject* all[] = {objects...};
+  bool ok = true;
+  for (PyObject* o : all) ok = ok && o != nullptr;
+  PyObject* t = ok ? PyTuple_New(sizeof...(O)) : nullptr;
+  if (t == nullptr) {
+    for (PyObject* o : all) Py_XDECREF(o);
+    throw PythonError{};
+  }
+  for (size_t i = 0; i < sizeof...(O); ++i) PyTuple_SET_ITEM(t, (Py_ssize_t)i, all[i]);
+  return t;
+}
+
+// A matrix of X's shape and type that was given as `name`.
+void like(const at::Tensor& t, const at::Tensor& X, const char* name) {
+  if (t.scalar_type() != X.scalar_type() || t.dim() != 2 || t.size(0) != X.size(0) ||
+      t.size(1) != X.size(1))
+    throw Refusal{std::string(name) + " must have the shape and type of X"};
+  type_of(t, name);
+  pitch(t, name);
+}
+
+// The norm's weight: its type.
+int weight_of(const at::Tensor& w, const at::Tensor& X) {
+  check(w.dim() == 1 && w.size(0) == X.size(1) && w.is_contiguous(),
+        "weight must be a contiguous vector with a value for each column");
+  check(w.scalar_type() == X.scalar_type() || w.scalar_type() == at::kFloat,
+        "weight must be of X's type or float32");
+  return type_of(w, "weight");
+}
+
+// What rms_norm and rms_norm_i8 share: X, the residual and where their sum goes.
+struct Rows {
+  const at::Tensor &X, &weight;
+  at::Tensor R, H;
+  int type, weight_type, ldx, ldr = 1, M, N;
+  Rows(PyObject* x, PyObject* w, PyObject* residual, PyObject* h)
+      : X(tensor(x, "X")), weight(tensor(w, "weight")) {
+    check(X.dim() == 2, "X must be 2-D");
+    type = type_of(X, "X");
+    ldx = pitch(X, "X");
+    M = to_int(X.size(0));
+    N = to_int(X.size(1));
+    weight_type = weight_of(weight, X);
+    ldr = N > 1 ? N : 1;
+    if (!is_none(residual)) {
+      R = tensor(residual, "residual");
+      like(R, X, "residual");
+      ldr = pitch(R, "residual");
+    }
+    if (!is_none(h)) {
+      check(R.defined(), "H needs a residual");
+      H = tensor(h, "H");
+      like(H, X, "H");
+    }
+  }
+  // (within the call's Launch) the sum's matrix, allocated if none was given
+  void place(const Launch& on) {
+    if (!R.defined()) return;
+    on.check_device(R);
+    if (!H.defined()) H = at::empty({X.size(0), X.size(1)}, X.options().requires_grad(false));
+    on.check_device(H);
+  }
+  void* h() const { return H.defined() ? H.data_ptr() : nullptr; }
+  int ldh() const { return H.defined() ? pitch(H, "H") : (N > 1 ? N : 1); }
+  const void* r() const { return R.defined() ? R.data_ptr() : nullptr; }
+  // the sum as an object: X itself without a residual
+  PyObject* sum(PyObject* x, PyObject* given) const {
+    if (R.defined()) return result(given, H);
+    Py_INCREF(x);
+    return x;
+  }
+};
+
+// (X, weight, residual, eps, Y, H, rstd, stream)
+PyObject* rms_norm(PyObject* const* a) {
+  Rows in(a[0], a[1], a[2], a[5]);
+  const double eps = number(a[3]);
+  at::Tensor Y, rstd;
+  if (!is_none(a[4])) {
+    Y = tensor(a[4], "Y");
+    like(Y, in.X, "Y");
+  }
+  if (!is_none(a[6])) {
+    rstd = tensor(a[6], "rstd");
+    vector_of(rstd, in.M, "rstd must be a contiguous float32 vector with one value a row");
+  }
+  {
+    const Launch on(a[7], {&in.X, &in.weight});
+    in.place(on);
+    if (!Y.defined()) Y = at::empty({in.M, in.N}, in.X.options().requires_grad(false));
+    if (!rstd.defined())
+      rstd = at::empty({in.M}, in.X.options().dtype(at::kFloat).requires_grad(false));
+    on.check_device(Y);
+    on.check_device(rstd);
+    const int st = fn.norm(in.M, in.N, in.type, in.X.data_ptr(), in.ldx, in.r(), in.ldr,
+                           in.weight.data_ptr(), in.weight_type, (float)eps, in.h(), in.ldh(),
+                           Y.data_ptr(), pitch(Y, "Y"), static_cast<float*>(rstd.data_ptr()),
+                           on.handle());
+    if (st != 0) throw Status{st, "sgemm_rms_norm"};
+  }
+  return tuple_of(result(a[4], Y), in.sum(a[0], a[5]), result(a[6], rstd));
+}
+
+// (X, weight, residual, eps, Q, scale, H, stream)
+PyObject* rms_norm_i8(PyObject* const* a) {
+  Rows in(a[0], a[1], a[2], a[6]);
+  const double eps = number(a[3]);
+  at::Tensor Q, scale;
+  if (!is_none(a[4])) {
+    Q = tensor(a[4], "Q");
+    check(Q.scalar_type() == at::kChar && Q.dim() == 2 && Q.size(0) == in.M && Q.size(1) == in.N,
+          "Q must be int8 of X's shape");
+    pitch(Q, "Q");
+  }
+  if (!is_none(a[5])) {
+    scale = tensor(a[5], "scale");
+    vector_of(scale, in.M, "scale must be a contiguous float32 vector with one value a row");
+  }
+  {
+    const Launch on(a[7], {&in.X, &in.weight});
+    in.place(on);
+    if (!Q.defined()) Q = padded_i8(in.X);
+    if (!scale.defined())
+      scale = at::empty({in.M}, in.X.options().dtype(at::kFloat).requires_grad(false));
+    on.check_device(Q);
+    on.check_device(scale);
+    const int st = fn.norm_i8(in.M, in.N, in.type, in.X.data_ptr(), in.ldx, in.r(), in.ldr,
+                              in.weight.data_ptr(), in.weight_type, (float)eps, in.h(), in.ldh(),
+                              static_cast<signed char*>(Q.data_ptr()), pitch(Q, "Q"),
+                              static_cast<float*>(scale.data_ptr()), on.handle());
+    if (st != 0) throw Status{st, "sgemm_rms_norm_i8"};
+  }
+  return tuple_of(result(a[4], Q), result(a[5], scale), in.sum(a[0], a[6]));
+}
+
+// (dY, H, weight, rstd, dH, dX, dweight, want dX, want dweight, stream)
+PyObject* rms_norm_grad(PyObject* const* a) {
+  const at::Tensor &dY = tensor(a[0], "dY"), &H = tensor(a[1], "H"), &w = tensor(a[2], "weight"),
+                   &rstd = tensor(a[3], "rstd");
+  check(H.dim() == 2, "H must be 2-D");
+  const int type = type_of(H, "H"), ldh = pitch(H, "H");
+  like(dY, H, "dY");
+  const int weight_type = weight_of(w, H), M = to_int(H.size(0)), N = to_int(H.size(1));
+  vector_of(rstd, M, "rstd must be a contiguous float32 vector with one value a row");
+  const bool want_x = a[7] == Py_True, want_w = a[8] == Py_True;
+  at::Tensor dH, dX, dw;
+  if (!is_none(a[4])) {
+    dH = tensor(a[4], "dH");
+    like(dH, H, "dH");
+  }
+  if (want_x && !is_none(a[5])) {
+    dX = tensor(a[5], "dX");
+    like(dX, H, "dX");
+  }
+  if (want_w && !is_none(a[6])) {
+    dw = tensor(a[6], "dweight");
+    check(dw.dim() == 1 && dw.size(0) == N && dw.is_contiguous() && !dw.is_neg() &&
+              dw.scalar_type() == w.scalar_type(), "dweight must have the shape and type of weight");
+  }
+  const int least = N > 1 ? N : 1;
+  {
+    const Launch on(a[9], {&dY, &H, &w, &rstd});
+    if (dH.defined()) on.check_device(dH);
+    if (want_x && !dX.defined()) dX = at::empty({M, N}, H.options().requires_grad(false));
+    if (want_w && !dw.defined()) dw = at::empty({N}, w.options().requires_grad(false));
+    if (want_x) on.check_device(dX);
+    if (want_w) on.check_device(dw);
+    const int st = fn.norm_grad(
+        M, N, type, dY.data_ptr(), pitch(dY, "dY"), H.data_ptr(), ldh, w.data_ptr(), weight_type,
+        static_cast<const float*>(rstd.data_ptr()), dH.defined() ? dH.data_ptr() : nullptr,
+        dH.defined() ? pitch(dH, "dH") : least, want_x ? dX.data_ptr() : nullptr,
+        want_x ? pitch(dX, "dX") : least, want_w ? dw.data_ptr() : nullptr, on.handle());
+    if (st != 0) throw Status{st, "sgemm_rms_norm_grad"};
+  }
+  return tuple_of(want_x ? result(a[5], dX) : Py_NewRef(Py_None),
+                  want_w ? result(a[6], dw) : Py_NewRef(Py_None));
 }
 
 // Holds a list or tuple of the items of any iterable.
@@ -406,16 +596,28 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   return nullptr;
 }
 
-// (grouped, wgrad, quantize, i8, clip addresses, the exception class)
+// (addresses of the C functions, in the order of Functions, the exception class)
 PyObject* bind(PyObject*, PyObject* args) {
-  unsigned long long p[5];
-  PyObject* error;
-  if (!PyArg_ParseTuple(args, "KKKKKO", &p[0], &p[1], &p[2], &p[3], &p[4], &error)) return nullptr;
+  constexpr int kFunctions = 8;
+  PyObject *addresses, *error;
+  if (!PyArg_ParseTuple(args, "O!O", &PyTuple_Type, &addresses, &error)) return nullptr;
+  if (PyTuple_GET_SIZE(addresses) != kFunctions) {
+    PyErr_SetString(PyExc_ValueError, "wrong number of functions");
+    return nullptr;
+  }
+  unsigned long long p[kFunctions];
+  for (int i = 0; i < kFunctions; ++i) {
+    p[i] = PyLong_AsUnsignedLongLong(PyTuple_GET_ITEM(addresses, i));
+    if (PyErr_Occurred()) return nullptr;
+  }
   fn.grouped = reinterpret_cast<decltype(fn.grouped)>(p[0]);
   fn.wgrad = reinterpret_cast<decltype(fn.wgrad)>(p[1]);
   fn.quantize = reinterpret_cast<decltype(fn.quantize)>(p[2]);
   fn.i8 = reinterpret_cast<decltype(fn.i8)>(p[3]);
   fn.clip = reinterpret_cast<decltype(fn.clip)>(p[4]);
+  fn.norm = reinterpret_cast<decltype(fn.norm)>(p[5]);
+  fn.norm_i8 = reinterpret_cast<decltype(fn.norm_i8)>(p[6]);
+  fn.norm_grad = reinterpret_cast<decltype(fn.norm_grad)>(p[7]);
   Py_INCREF(error);
   Py_XDECREF(g_error);
   g_error = error;
@@ -431,6 +633,9 @@ PyMethodDef methods[] = {
     SGEMM_GB300_METHOD(i8_quantize, 4),
     SGEMM_GB300_METHOD(i8_gemm, 7),
     SGEMM_GB300_METHOD(clip_grad_norm, 4),
+    SGEMM_GB300_METHOD(rms_norm, 8),
+    SGEMM_GB300_METHOD(rms_norm_i8, 8),
+    SGEMM_GB300_METHOD(rms_norm_grad, 10),
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -1,9 +1,13 @@
-"""The linear layer of a set of experts as torch autograd sees it: the three
-grouped products of binding.py behind one function. Each product's gradients
-are products of the same kinds, so derivatives of any order come out."""
+"""The operators of binding.py as torch autograd sees them.
+
+The linear layer of a set of experts: the three grouped products behind one
+function. Each product's gradients are products of the same kinds, so
+derivatives of any order come out. The norm and the loss of the output end have
+first derivatives; asking for a second raises."""
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import binding
 
@@ -56,3 +60,42 @@ def expert_linear(x, weight, offsets):
     device that cover every row of x. Differentiable in x and weight, any
     number of times."""
     return _Rows.apply(x, weight, offsets, "T")
+
+
+class _Norm(torch.autograd.Function):
+    """(y, h) of binding.rms_norm on rows."""
+
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        ctx.set_materialize_grads(False)
+        y, h, rstd = binding.rms_norm(x, weight, residual=residual, eps=eps)
+        ctx.save_for_backward(h, weight, rstd)
+        ctx.with_residual = residual is not None
+        return (y, h) if ctx.with_residual else y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh=None):
+        h, weight, rstd = ctx.saved_tensors
+        need_x, need_w, need_r = ctx.needs_input_grad[:3]
+        dx, dw = dh, None
+        if dy is None:              # only h was used
+            dw = torch.zeros_like(weight) if need_w else None
+        else:
+            dx, dw = binding.rms_norm_grad(dy.contiguous(), h, weight, rstd,
+                                           dH=None if dh is None else dh.contiguous(),
+                                           want=(need_x or need_r, need_w))
+        return dx if need_x else None, dw, dx if need_r else None, None
+
+
+def rms_norm(x, weight, residual=None, eps=1e-6):
+    """h / sqrt(mean(h^2) + eps) * weight over the last dimension, h = x +
+    residual; with a residual (y, h) is returned. Differentiable once in x,
+    weight and residual."""
+    rows = x.reshape(-1, x.shape[-1])
+    if residual is None:
+        return _Norm.apply(rows, weight, None, eps).view(x.shape)
+    if residual.shape != x.shape:
+        raise ValueError("residual must have the shape of x")
+    y, h = _Norm.apply(rows, weight, residual.reshape(rows.shape), eps)
+    return y.view(x.shape), h.view(x.shape)

@@ -612,6 +612,58 @@ int sgemm_grouped_set_tile(int width, int ctas);
 int sgemm_grad_clip(int n, const void* const* grads, void* const* out, const long long* sizes,
                     const int* types, float max_norm, float* norm, void* stream);
 
+/*
+ * The output end of a language model: the residual's addition with the norm of
+ * its rows, what follows it in training (the loss over the vocabulary) and in
+ * serving (8-bit and 4-bit products). The pages have none of these.
+ */
+
+/*
+ * H = X + R rounded to `type` (R == NULL: H is X, and the argument H is not
+ * used), and row by row
+ *   rstd = 1 / sqrt(mean(H^2) + eps),   Y = H * rstd * weight.
+ * X, R, H and Y are M x N of `type`, weight has N values of weight_type (`type`
+ * or FP32), rstd (may be NULL) M FP32 values. Sums and products are FP32, Y is
+ * rounded once. eps is at least 1e-30. A row with an infinity or a NaN gives
+ * what the formula gives. Y and H may be X or R themselves (the same address and
+ * pitch); otherwise they must not overlap what is read, nor each other. N == 0
+ * or M == 0 does nothing. Any leading dimensions (>= max(1, N)) and element
+ * alignment; rows that start on 16 bytes are faster. Capturable without any
+ * call before.
+ * Returns SGEMM_ERR_INVALID_VALUE (type, eps), _INVALID_DIM, _INVALID_LD,
+ * _NULL_PTR, _MISALIGNED as sgemm().
+ */
+int sgemm_rms_norm(int M, int N, int type, const void* X, int ldx, const void* R, int ldr,
+                   const void* weight, int weight_type, float eps, void* H, int ldh, void* Y,
+                   int ldy, float* rstd, void* stream);
+
+/*
+ * The same norm as 8-bit integers with one scale a row, as sgemm_i8 takes them:
+ * with u = H * weight in FP32,
+ *   step = max_n |u[m, n]| / 127,  Q = u / step rounded to the nearest integer
+ *   (ties to even) within +-127,  scale[m] = step * rstd[m];
+ * both quotients are rounded to FP32. A row of zeros has scale 0 and zeros. A row
+ * with an infinity or a NaN has a NaN for its scale (an infinity where only a
+ * product u overflows), so its products are no numbers. H may be X or R
+ * themselves. Errors as sgemm_rms_norm().
+ */
+int sgemm_rms_norm_i8(int M, int N, int type, const void* X, int ldx, const void* R, int ldr,
+                      const void* weight, int weight_type, float eps, void* H, int ldh,
+                      signed char* Q, int ldq, float* scale, void* stream);
+
+/*
+ * Gradients of sgemm_rms_norm, with n = H * rstd and d = dY * weight:
+ *   dX = rstd * (d - n * mean(d * n)) + dH,   dweight = sum over rows of dY * n.
+ * dX is the gradient of X and of R alike. dH (may be NULL) is the gradient that
+ * reaches H itself. dX or dweight (of weight_type) may be NULL: not formed. dX
+ * may be dY, H or dH itself. dweight is summed in FP32 in an order that depends
+ * on the sizes only, and rounded once; M == 0 sets it to zeros. Workspace and
+ * capture as for sgemm(); errors as sgemm_rms_norm().
+ */
+int sgemm_rms_norm_grad(int M, int N, int type, const void* dY, int lddy, const void* H, int ldh,
+                        const void* weight, int weight_type, const float* rstd, const void* dH,
+                        int lddh, void* dX, int lddx, void* dweight, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

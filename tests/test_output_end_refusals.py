@@ -1,0 +1,72 @@
+"""Argument checks of the output end's calls: they return before any device call,
+so they run without a GPU."""
+import pytest
+import torch
+
+from dense_fp32_gemm_gb300 import binding as B
+from dense_fp32_gemm_gb300 import layers
+
+F32, BF16, F16 = B.SGEMM_TYPE_F32, B.SGEMM_TYPE_BF16, B.SGEMM_TYPE_F16
+OK, VALUE, DIM, LD = B.SGEMM_OK, B.SGEMM_ERR_INVALID_VALUE, B.SGEMM_ERR_INVALID_DIM, B.SGEMM_ERR_INVALID_LD
+NULL, ALIGN = B.SGEMM_ERR_NULL_PTR, B.SGEMM_ERR_MISALIGNED
+
+
+NORM = dict(M=4, N=16, type=BF16, X=256, ldx=16, R=256, ldr=16, weight=256, weight_type=F32, eps=1e-6, H=256, ldh=16)
+NORM_CASES = [
+    (dict(type=3), VALUE), (dict(weight_type=F16), VALUE), (dict(weight_type=7), VALUE), (dict(eps=0.0), VALUE),
+    (dict(eps=-1.0), VALUE), (dict(eps=float("nan")), VALUE), (dict(eps=float("inf")), VALUE), (dict(M=-1), DIM),
+    (dict(N=-1), DIM), (dict(ldx=15), LD), (dict(ldr=15), LD), (dict(ldh=15), LD), (dict(X=None), NULL),
+    (dict(weight=None), NULL), (dict(H=None), NULL), (dict(X=257), ALIGN), (dict(R=257), ALIGN), (dict(H=257), ALIGN),
+    (dict(weight=258), ALIGN), (dict(M=0, X=None), OK), (dict(N=0, X=None), OK)]
+
+
+@pytest.mark.parametrize("kw,want", NORM_CASES + [
+    (dict(Y=None), NULL), (dict(Y=257), ALIGN), (dict(ldy=15), LD), (dict(rstd=258), ALIGN)])
+def test_rms_norm(kw, want):
+    assert B.sgemm_rms_norm(**(dict(NORM, Y=256, ldy=16, rstd=256) | kw)) == want
+
+
+@pytest.mark.parametrize("kw,want", NORM_CASES + [
+    (dict(Q=None), NULL), (dict(scale=None), NULL), (dict(scale=258), ALIGN), (dict(ldq=15), LD)])
+def test_rms_norm_i8(kw, want):
+    assert B.sgemm_rms_norm_i8(**(dict(NORM, Q=257, ldq=16, scale=256) | kw)) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(type=3), VALUE), (dict(weight_type=F16), VALUE), (dict(M=-1), DIM), (dict(N=-1), DIM), (dict(lddy=15), LD),
+    (dict(ldh=15), LD), (dict(lddh=15), LD), (dict(lddx=15), LD), (dict(dY=None), NULL), (dict(H=None), NULL),
+    (dict(weight=None), NULL), (dict(rstd=None), NULL), (dict(dY=257), ALIGN), (dict(H=257), ALIGN),
+    (dict(dH=257), ALIGN), (dict(dX=257), ALIGN), (dict(dweight=258), ALIGN), (dict(rstd=258), ALIGN),
+    (dict(dX=None, dweight=None), OK), (dict(N=0, dY=None), OK)])
+def test_rms_norm_grad(kw, want):
+    a = dict(M=4, N=16, type=BF16, dY=256, lddy=16, H=256, ldh=16, weight=256, weight_type=F32, rstd=256, dH=256,
+             lddh=16, dX=256, lddx=16, dweight=256)
+    assert B.sgemm_rms_norm_grad(**(a | kw)) == want
+
+
+def test_torch_norm_refuses():
+    x, w, s = torch.zeros(4, 8), torch.zeros(8), torch.zeros(4)
+    wide = torch.zeros(1, 8).expand(4, 8)
+    for args, kw in [((x, w), {}),                                         # not on a GPU
+                     ((x[0], w), {}), ((x.double(), w.double()), {}), ((x, w[:7]), {}), ((x, w.half()), {}),
+                     ((x, torch.zeros(16)[::2]), {}), ((wide, w), {}), ((x.t(), s), {}), ((x, w), dict(residual=x[:3])),
+                     ((x, w), dict(residual=x.half())), ((x, w), dict(residual=wide)), ((x, w), dict(H=x)),
+                     ((x, w), dict(residual=x, H=x[:, :7]))]:
+        for f in (B.rms_norm, B.rms_norm_i8):
+            with pytest.raises(ValueError):
+                f(*args, **kw)
+    for kw in (dict(Y=x[:3]), dict(Y=x.half()), dict(Y=wide), dict(rstd=s[:3]), dict(rstd=s.double())):
+        with pytest.raises(ValueError):
+            B.rms_norm(x, w, **kw)
+    for kw in (dict(Q=x), dict(scale=s[:3]), dict(Q=torch.zeros(4, 7, dtype=torch.int8))):
+        with pytest.raises(ValueError):
+            B.rms_norm_i8(x, w, **kw)
+    for args, kw in [((x, x, w, s), {}), ((x[:3], x, w, s), {}), ((x.half(), x, w, s), {}), ((x, x, w, s[:3]), {}),
+                     ((x, x, w[:7], s), {}), ((x, x, w, s), dict(dH=x[:3])), ((x, x, w, s), dict(dX=x.half())),
+                     ((x, x, w, s), dict(dweight=w[:7])), ((wide, x, w, s), {})]:
+        with pytest.raises(ValueError):
+            B.rms_norm_grad(*args, **kw)
+    with pytest.raises(ValueError):
+        layers.rms_norm(x, w, residual=x[:3])
+    with pytest.raises(TypeError):
+        B.rms_norm(x, w, eps="small")
