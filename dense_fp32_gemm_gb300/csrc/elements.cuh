@@ -23,31 +23,87 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
-// VW neighbouring elements of a row.
+// VW neighbouring elements of a row, as 32-bit words where there are several
+// (two 16-bit elements a word; element by element the compiler took twice the
+// registers).
 template <typename E, int VW>
-struct __align__(VW * sizeof(E)) Piece {
-  E e[VW];
+struct Piece {
+  static constexpr int kWords = VW * (int)sizeof(E) / 4;
+  static_assert(kWords == 4, "pieces of 16 bytes or of one element");
+  uint4 w;
+};
+template <typename E>
+struct Piece<E, 1> {
+  E e;
 };
 
 // Loads that are read once; the memory may be written later in the same kernel.
 template <typename E, int VW>
 __device__ __forceinline__ Piece<E, VW> load(const E* p) {
-  constexpr int kBytes = VW * (int)sizeof(E);
-  static_assert(kBytes == 16 || VW == 1, "pieces of 16 bytes or of one element");
   Piece<E, VW> r;
-  if constexpr (kBytes == 16)
-    *reinterpret_cast<uint4*>(&r) = __ldcs(reinterpret_cast<const uint4*>(p));
+  if constexpr (VW == 1)
+    r.e = *p;
   else
-    r.e[0] = *p;
+    r.w = __ldcs(reinterpret_cast<const uint4*>(p));
   return r;
 }
 template <typename E, int VW>
 __device__ __forceinline__ void store(E* p, const Piece<E, VW>& r) {
-  if constexpr (VW * sizeof(E) == 16)
-    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(&r);
+  if constexpr (VW == 1)
+    *p = r.e;
   else
-    *p = r.e[0];
+    *reinterpret_cast<uint4*>(p) = r.w;
 }
+
+__device__ __forceinline__ float2 unpack2(uint32_t w, __nv_bfloat16) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w, __half) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The elements as FP32, and FP32 values rounded to elements.
+template <typename E, int VW>
+__device__ __forceinline__ void unpack(const Piece<E, VW>& p, float (&v)[VW]) {
+  if constexpr (VW == 1) {
+    v[0] = to_f32(p.e);
+  } else {
+    const uint32_t w[4] = {p.w.x, p.w.y, p.w.z, p.w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (VW == 4) {
+        v[i] = __uint_as_float(w[i]);
+      } else {
+        const float2 f = unpack2(w[i], E{});
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+      }
+    }
+  }
+}
+template <typename E, int VW>
+__device__ __forceinline__ Piece<E, VW> pack(const float (&v)[VW]) {
+  Piece<E, VW> p;
+  if constexpr (VW == 1) {
+    p.e = from_f32<E>(v[0]);
+  } else if constexpr (VW == 4) {
+    p.w = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                     __float_as_uint(v[3]));
+  } else {
+    p.w = make_uint4(pack2(v[0], v[1], E{}), pack2(v[2], v[3], E{}), pack2(v[4], v[5], E{}),
+                     pack2(v[6], v[7], E{}));
+  }
+  return p;
+}
+
 // VW values of a vector that no kernel of the call writes, as FP32; 16-byte
 // aligned where VW > 1.
 template <typename W, int VW>
@@ -71,9 +127,16 @@ __device__ __forceinline__ void load_vector(const W* p, float (&v)[VW]) {
         w[i + 3] = a.w;
       }
     }
-    const W* e = reinterpret_cast<const W*>(w);
 #pragma unroll
-    for (int i = 0; i < VW; ++i) v[i] = to_f32(e[i]);
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(W) == 4) {
+        v[i] = __uint_as_float(w[i]);
+      } else {
+        const float2 f = unpack2(w[i], W{});
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+      }
+    }
   }
 }
 

@@ -35,6 +35,8 @@ namespace rows {
 namespace {
 
 constexpr int kMaxThreads = 512;
+// Pieces of a row that a thread holds: of 16 bytes, or single elements.
+__host__ __device__ constexpr int held_of(int vw) { return vw > 1 ? 4 : 8; }
 constexpr uint32_t kAll = 0xffffffffu;
 
 struct NormArgs {
@@ -58,11 +60,12 @@ struct Reduced {
   float sum;
   uint32_t most;
 };
+template <bool MOST>
 __device__ __forceinline__ Reduced reduce(float sum, uint32_t most, float2 (*part)[kMaxThreads / 32],
                                           int& buf) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
-  most = __reduce_max_sync(kAll, most);
+  if (MOST) most = __reduce_max_sync(kAll, most);
   const int warps = (int)blockDim.x >> 5;
   if (warps == 1) return {sum, most};
   if ((threadIdx.x & 31) == 0)
@@ -73,30 +76,47 @@ __device__ __forceinline__ Reduced reduce(float sum, uint32_t most, float2 (*par
   for (int i = 0; i < warps; ++i) {
     const float2 p = part[buf][i];
     sum += p.x;
-    most = max(most, __float_as_uint(p.y));
+    if (MOST) most = max(most, __float_as_uint(p.y));
   }
   buf ^= 1;
   return {sum, most};
 }
 
-// q = rint(u / step), the quotient rounded to FP32 first. u * inv, inv = 1 /
-// step, is within 2^-22 of it (relative; |u / step| <= 127), so the two round to
-// the same integer unless the product lies that near to the middle of two.
-__device__ __forceinline__ int quotient(float u, float step, float inv) {
-  const float t = u * inv, n = rintf(t);
-  // (also for no number)
-  if (!(fabsf(t - n) <= 0.5f - 1e-4f) || !(inv < 1e37f))
-    // (a step below FP32's normal numbers may be far below max|u| / 127)
-    return __float2int_rn(fminf(fmaxf(__fdiv_rn(u, step), -127.f), 127.f));
-  return (int)n;
+// q = rint(u / step), the quotient rounded to FP32 first, in the low bytes of
+// b. u * inv, inv = 1 / step, is within 2^-22 of the quotient (relative; |u /
+// step| <= 127), so the two round to the same integer unless the product lies
+// that near to the middle of two. Adding 1.5 * 2^23 rounds to the nearest
+// integer, ties to even, and leaves it in the sum's low byte. Where one value of
+// the piece lies near a middle (or 1 / step is no number to multiply by, or u
+// is none), all are divided.
+template <int VW>
+__device__ __forceinline__ void quotients(const float (&u)[VW], float step, float inv,
+                                          uint32_t (&b)[VW]) {
+  constexpr float kMagic = 12582912.f;
+  bool near = false;
+#pragma unroll
+  for (int j = 0; j < VW; ++j) {
+    const float v = u[j] * inv, t = v + kMagic;
+    near = near || !(fabsf(v - (t - kMagic)) <= 0.5f - 1e-4f);
+    b[j] = __float_as_uint(t);
+  }
+  if (near) {
+#pragma unroll
+    for (int j = 0; j < VW; ++j)
+      // (a step below FP32's normal numbers may be far below max|u| / 127)
+      b[j] = (uint32_t)__float2int_rn(fminf(fmaxf(__fdiv_rn(u[j], step), -127.f), 127.f));
+  }
 }
 
 // A row per block, in pieces of VW elements (16 bytes, or one element where
-// something is not aligned). Up to HELD pieces a thread stay in registers
-// between the pass that sums and the pass that writes; what is left of a longer
-// row is read again (the thread's own h, or x).
-template <typename E, typename W, int VW, int HELD, bool I8>
+// something is not aligned). Up to
+// HELD pieces a thread stay in registers
+// between the pass that sums and the pass that writes, and those of the block's
+// next row are loaded ahead; what is left of a longer row is read again (the
+// thread's own h, or x).
+template <typename E, typename W, int VW, bool I8>
 __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a) {
+  constexpr int HELD = held_of(VW);
   __shared__ float2 part[2][kMaxThreads / 32];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
@@ -104,27 +124,38 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a) {
   const E* r = static_cast<const E*>(a.r);
   const W* w = static_cast<const W*>(a.w);
   E* h = static_cast<E*>(a.h);
-  // (places in a row pass 32 bits before they end their loops)
-  const long long step_c = (long long)blockDim.x * VW, c0 = threadIdx.x * VW, N = a.N;
+  // (places in a row pass 2^31 before they end their loops, not 2^32)
+  const unsigned step_c = blockDim.x * VW, c0 = threadIdx.x * VW, N = (unsigned)a.N;
   const float inv_n = 1.f / (float)a.N;
   int buf = 0;
+  Piece<E, VW> held[HELD], ahead[HELD];      // x, then h; the residual
+  auto fetch = [&](long long m) {
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+      const unsigned c = c0 + i * step_c;
+      if (c >= N) continue;
+      held[i] = load<E, VW>(x + m * a.ldx + c);
+      if (r != nullptr) ahead[i] = load<E, VW>(r + m * a.ldr + c);
+    }
+  };
+  auto sum_of = [&](const Piece<E, VW>& p, const Piece<E, VW>& q) {
+    float s[VW], t[VW];
+    unpack(p, s);
+    unpack(q, t);
+#pragma unroll
+    for (int j = 0; j < VW; ++j) s[j] += t[j];
+    return pack<E, VW>(s);
+  };
+  fetch(blockIdx.x);
   for (long long m = blockIdx.x; m < a.M; m += gridDim.x) {
     float sum = 0.f;
     uint32_t most = 0;
-    auto take = [&](long long c) {
-      Piece<E, VW> p = load<E, VW>(x + m * a.ldx + c);
-      if (r != nullptr) {
-        const Piece<E, VW> q = load<E, VW>(r + m * a.ldr + c);
-#pragma unroll
-        for (int j = 0; j < VW; ++j) p.e[j] = from_f32<E>(to_f32(p.e[j]) + to_f32(q.e[j]));
-      }
-      return p;
-    };
-    auto add = [&](const Piece<E, VW>& p, long long c) {
+    auto add = [&](const Piece<E, VW>& p, unsigned c) {
       if (h != nullptr) store<E, VW>(h + m * a.ldh + c, p);
-      float s = 0.f;
+      float f[VW], s = 0.f;
+      unpack(p, f);
 #pragma unroll
-      for (int j = 0; j < VW; ++j) s = fmaf(to_f32(p.e[j]), to_f32(p.e[j]), s);
+      for (int j = 0; j < VW; ++j) s = fmaf(f[j], f[j], s);
       sum += s;
       if (I8) {
         float v[VW];
@@ -132,78 +163,88 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a) {
         // as bits: a NaN is above infinity, so either survives
 #pragma unroll
         for (int j = 0; j < VW; ++j)
-          most = max(most, __float_as_uint(to_f32(p.e[j]) * v[j]) & 0x7fffffffu);
+          most = max(most, __float_as_uint(f[j] * v[j]) & 0x7fffffffu);
       }
     };
-    Piece<E, VW> held[HELD];
+    Piece<E, VW> row[HELD];
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) row[i] = r != nullptr ? sum_of(held[i], ahead[i]) : held[i];
+    if (m + gridDim.x < a.M) fetch(m + gridDim.x);
 #pragma unroll
     for (int i = 0; i < HELD; ++i)
-      if (c0 + i * step_c < N) held[i] = take(c0 + i * step_c);
-#pragma unroll
-    for (int i = 0; i < HELD; ++i)
-      if (c0 + i * step_c < N) add(held[i], c0 + i * step_c);
-    for (long long c = c0 + HELD * step_c; c < N; c += step_c) add(take(c), c);
+      if (c0 + i * step_c < N) add(row[i], c0 + i * step_c);
+    for (unsigned c = c0 + HELD * step_c; c < N; c += step_c) {
+      Piece<E, VW> p = load<E, VW>(x + m * a.ldx + c);
+      if (r != nullptr) p = sum_of(p, load<E, VW>(r + m * a.ldr + c));
+      add(p, c);
+    }
     // the row's values once more: those that were not held from h, or x
     auto each = [&](auto&& f) {
 #pragma unroll
       for (int i = 0; i < HELD; ++i)
-        if (c0 + i * step_c < N) f(held[i], c0 + i * step_c);
-      for (long long c = c0 + HELD * step_c; c < N; c += step_c)
+        if (c0 + i * step_c < N) f(row[i], c0 + i * step_c);
+      for (unsigned c = c0 + HELD * step_c; c < N; c += step_c)
         f(load<E, VW>(h != nullptr ? h + m * a.ldh + c : x + m * a.ldx + c), c);
     };
-    Reduced t = reduce(sum, most, part, buf);
+    Reduced t = reduce<I8>(sum, most, part, buf);
     // Squares beyond FP32's range (values above 1e19): once more on values that
     // are scaled down. eps is at least 1e-30, so squares below the range do not count.
     float down = 1.f;
     if (!(t.sum <= 3e38f)) {
       down = 0x1p-70f;
       sum = 0.f;
-      each([&](const Piece<E, VW>& p, long long) {
+      each([&](const Piece<E, VW>& p, unsigned) {
+        float f[VW];
+        unpack(p, f);
 #pragma unroll
-        for (int j = 0; j < VW; ++j) {
-          const float v = to_f32(p.e[j]) * down;
-          sum = fmaf(v, v, sum);
-        }
+        for (int j = 0; j < VW; ++j) sum = fmaf(f[j] * down, f[j] * down, sum);
       });
-      t.sum = reduce(sum, 0, part, buf).sum;
+      t.sum = reduce<false>(sum, 0, part, buf).sum;
     }
-    const float rstd = 1.f / sqrtf(t.sum * inv_n + a.eps * down * down);
-    if (threadIdx.x == 0 && a.rstd != nullptr) a.rstd[m] = rstd * down;
+    // (below FP32's normal numbers where the values are above 8e37: 21 bits are left)
+    const float rstd = rsqrtf(t.sum * inv_n + a.eps * down * down) * down;
+    if (threadIdx.x == 0 && a.rstd != nullptr) a.rstd[m] = rstd;
     if (!I8) {
       E* y = static_cast<E*>(a.y) + m * a.ldy;
-      each([&](const Piece<E, VW>& p, long long c) {
-        float v[VW];
+      each([&](const Piece<E, VW>& p, unsigned c) {
+        float v[VW], f[VW];
         load_vector<W, VW>(w + c, v);
-        Piece<E, VW> o;
+        unpack(p, f);
 #pragma unroll
-        for (int j = 0; j < VW; ++j) o.e[j] = from_f32<E>(to_f32(p.e[j]) * down * rstd * v[j]);
-        store<E, VW>(y + c, o);
+        for (int j = 0; j < VW; ++j) f[j] = f[j] * rstd * v[j];
+        store<E, VW>(y + c, pack<E, VW>(f));
       });
     } else {
       const float step = __fdiv_rn(__uint_as_float(t.most), 127.f);
-      const float inv = step > 0.f ? 1.f / step : 0.f;
+      // (1 / step has to be a number: else every value is divided)
+      const float inv = step > 1e-37f ? __frcp_rn(step) : __uint_as_float(0x7fc00000u);
       const bool none = !(step > 0.f && step <= 3e38f);   // zeros, or no numbers
-      if (threadIdx.x == 0) a.scale[m] = step * down * rstd;
+      if (threadIdx.x == 0) a.scale[m] = step * rstd;
       signed char* q = static_cast<signed char*>(a.y) + m * a.ldy;
-      each([&](const Piece<E, VW>& p, long long c) {
-        float v[VW];
-        load_vector<W, VW>(w + c, v);
+      each([&](const Piece<E, VW>& p, unsigned c) {
+        float u[VW], f[VW];
+        load_vector<W, VW>(w + c, u);
+        unpack(p, f);
         uint32_t b[VW];
 #pragma unroll
-        for (int j = 0; j < VW; ++j)
-          b[j] = none ? 0u : (uint32_t)quotient(to_f32(p.e[j]) * v[j], step, inv) & 0xffu;
+        for (int j = 0; j < VW; ++j) {
+          u[j] *= f[j];
+          b[j] = 0u;
+        }
+        if (!none) quotients<VW>(u, step, inv, b);
         if (VW > 1 && a.wide_q) {
           uint32_t o[VW / 4 > 0 ? VW / 4 : 1];
 #pragma unroll
           for (int j = 0; j < VW / 4; ++j)
-            o[j] = b[4 * j] | b[4 * j + 1] << 8 | b[4 * j + 2] << 16 | b[4 * j + 3] << 24;
+            o[j] = __byte_perm(__byte_perm(b[4 * j], b[4 * j + 1], 0x0040),
+                               __byte_perm(b[4 * j + 2], b[4 * j + 3], 0x0040), 0x5410);
           if constexpr (VW == 8)
             *reinterpret_cast<uint2*>(q + c) = make_uint2(o[0], o[1]);
           else
             *reinterpret_cast<uint32_t*>(q + c) = o[0];
         } else {
 #pragma unroll
-          for (int j = 0; j < VW; ++j) q[c + j] = (signed char)b[j];
+          for (int j = 0; j < VW; ++j) q[c + j] = (signed char)(b[j] & 0xffu);
         }
       });
     }
@@ -223,8 +264,9 @@ struct GradArgs {
 // A row per block at a time, every thread at the same places in each, so that
 // its part of dw stays in registers over all rows of the block. DW: the row
 // fits into HELD pieces a thread and dw's parts are formed.
-template <typename E, typename W, int VW, int HELD, bool DW>
+template <typename E, typename W, int VW, bool DW>
 __global__ void __launch_bounds__(kMaxThreads) norm_grad_kernel(const GradArgs a) {
+  constexpr int HELD = held_of(VW);
   __shared__ float2 part[2][kMaxThreads / 32];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
@@ -233,7 +275,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_grad_kernel(const GradArgs a
   const E* dh = static_cast<const E*>(a.dh);
   const W* w = static_cast<const W*>(a.w);
   E* dx = static_cast<E*>(a.dx);
-  const long long step_c = (long long)blockDim.x * VW, c0 = threadIdx.x * VW, N = a.N;
+  const unsigned step_c = blockDim.x * VW, c0 = threadIdx.x * VW, N = (unsigned)a.N;
   const float inv_n = 1.f / (float)a.N;
   int buf = 0;
   float dw[DW ? HELD : 1][VW];
@@ -246,61 +288,66 @@ __global__ void __launch_bounds__(kMaxThreads) norm_grad_kernel(const GradArgs a
     Piece<E, VW> g[HELD], v[HELD], d[HELD];
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
-      const long long c = c0 + i * step_c;
+      const unsigned c = c0 + i * step_c;
       if (c >= N) continue;
       g[i] = load<E, VW>(dy + m * a.lddy + c);
       v[i] = load<E, VW>(h + m * a.ldh + c);
       if (dh != nullptr) d[i] = load<E, VW>(dh + m * a.lddh + c);
     }
     float sum = 0.f;
-    auto add = [&](const Piece<E, VW>& g, const Piece<E, VW>& v, long long c) {
-      float wv[VW], s = 0.f;
+    auto add = [&](const Piece<E, VW>& g, const Piece<E, VW>& v, unsigned c) {
+      float wv[VW], gf[VW], vf[VW], s = 0.f;
       load_vector<W, VW>(w + c, wv);
+      unpack(g, gf);
+      unpack(v, vf);
 #pragma unroll
-      for (int j = 0; j < VW; ++j)
-        s = fmaf(to_f32(g.e[j]) * wv[j], to_f32(v.e[j]) * rstd, s);
+      for (int j = 0; j < VW; ++j) s = fmaf(gf[j] * wv[j], vf[j] * rstd, s);
       sum += s;
     };
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
-      const long long c = c0 + i * step_c;
+      const unsigned c = c0 + i * step_c;
       if (c >= N) continue;
       add(g[i], v[i], c);
       if (DW) {
+        float gf[VW], vf[VW];
+        unpack(g[i], gf);
+        unpack(v[i], vf);
 #pragma unroll
-        for (int j = 0; j < VW; ++j)
-          dw[i][j] = fmaf(to_f32(g[i].e[j]), to_f32(v[i].e[j]) * rstd, dw[i][j]);
+        for (int j = 0; j < VW; ++j) dw[i][j] = fmaf(gf[j], vf[j] * rstd, dw[i][j]);
       }
     }
     if (!DW)
-      for (long long c = c0 + HELD * step_c; c < N; c += step_c)
+      for (unsigned c = c0 + HELD * step_c; c < N; c += step_c)
         add(load<E, VW>(dy + m * a.lddy + c), load<E, VW>(h + m * a.ldh + c), c);
     if (dx == nullptr) continue;
-    const float mean = reduce(sum, 0, part, buf).sum * inv_n;
-    auto put = [&](const Piece<E, VW>& g, const Piece<E, VW>& v, const Piece<E, VW>& d, long long c) {
-      float wv[VW];
+    const float mean = reduce<false>(sum, 0, part, buf).sum * inv_n;
+    auto put = [&](const Piece<E, VW>& g, const Piece<E, VW>& v, const Piece<E, VW>& d, unsigned c) {
+      float wv[VW], gf[VW], vf[VW], df[VW];
       load_vector<W, VW>(w + c, wv);
-      Piece<E, VW> o;
+      unpack(g, gf);
+      unpack(v, vf);
+      unpack(d, df);
 #pragma unroll
       for (int j = 0; j < VW; ++j) {
-        const float t = rstd * fmaf(-mean, to_f32(v.e[j]) * rstd, to_f32(g.e[j]) * wv[j]);
-        o.e[j] = from_f32<E>(dh != nullptr ? t + to_f32(d.e[j]) : t);
+        const float t = rstd * fmaf(-mean, vf[j] * rstd, gf[j] * wv[j]);
+        gf[j] = dh != nullptr ? t + df[j] : t;
       }
-      store<E, VW>(dx + m * a.lddx + c, o);
+      store<E, VW>(dx + m * a.lddx + c, pack<E, VW>(gf));
     };
 #pragma unroll
     for (int i = 0; i < HELD; ++i)
       if (c0 + i * step_c < N) put(g[i], v[i], d[i], c0 + i * step_c);
     if (!DW)
-      for (long long c = c0 + HELD * step_c; c < N; c += step_c)
+      for (unsigned c = c0 + HELD * step_c; c < N; c += step_c)
         put(load<E, VW>(dy + m * a.lddy + c), load<E, VW>(h + m * a.ldh + c),
             dh != nullptr ? load<E, VW>(dh + m * a.lddh + c) : Piece<E, VW>{}, c);
   }
   if (DW && a.partial != nullptr) {
-    float* p = a.partial + blockIdx.x * N;
+    float* p = a.partial + (long long)blockIdx.x * a.N;
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
-      const long long c = c0 + i * step_c;
+      const unsigned c = c0 + i * step_c;
       if (c >= N) continue;
       if constexpr (VW == 1) {
         p[c] = dw[i][0];
@@ -379,14 +426,15 @@ cudaError_t launch(void (*kernel)(A...), long long blocks, int threads, cudaStre
 }
 
 // Threads of a row: a piece each while that leaves SMs idle otherwise (few
-// rows: latency), else as many pieces as are held, at most kMaxThreads.
+// rows: latency), else as many pieces as are held.
 int threads_of(long long pieces, int held, bool few) {
   const long long want = few ? pieces : (pieces + held - 1) / held;
   const long long t = (want + 31) / 32 * 32;
   return (int)(t < 32 ? 32 : (t > kMaxThreads ? kMaxThreads : t));
 }
-int blocks_of(int M, int threads, int sms, int per_sm) {
-  const int fit = sms * (per_sm * 256 / threads > 0 ? per_sm * 256 / threads : 1);
+// Blocks: a row each, or as many as fill the SMs (`threads_per_sm` resident).
+int blocks_of(int M, int threads, int sms, int threads_per_sm) {
+  const int fit = sms * (threads_per_sm / threads < 32 ? threads_per_sm / threads : 32);
   return M < fit ? M : fit;
 }
 
@@ -395,8 +443,6 @@ bool aligned(const void* p, long long ld, int elem, int bytes) {
          ((reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0 && ld * elem % bytes == 0);
 }
 
-// HELD of both kernels: 2 pieces where a row has at most that for every thread
-// of half a block, else 4; 8 single elements.
 template <typename E, typename W, bool I8>
 cudaError_t forward(NormArgs a, int sms, cudaStream_t stream) {
   constexpr int VW = 16 / (int)sizeof(E);
@@ -405,33 +451,27 @@ cudaError_t forward(NormArgs a, int sms, cudaStream_t stream) {
                    a.N % VW == 0 && (I8 || aligned(a.y, a.ldy, sizeof(E), 16));
   a.wide_q = I8 && aligned(a.y, a.ldy, 1, VW);
   const bool few = a.M < 2 * sms;
-  if (!vec) {
-    const int t = threads_of(a.N, 8, few);
-    return launch(norm_kernel<E, W, 1, 8, I8>, blocks_of(a.M, t, sms, 6), t, stream, a);
-  }
-  const long long pieces = a.N / VW;
-  if (pieces <= 2 * 256 || (few && pieces <= 2 * kMaxThreads)) {
-    const int t = threads_of(pieces, 2, few);
-    return launch(norm_kernel<E, W, VW, 2, I8>, blocks_of(a.M, t, sms, 6), t, stream, a);
-  }
-  const int t = threads_of(pieces, 4, few);
-  return launch(norm_kernel<E, W, VW, 4, I8>, blocks_of(a.M, t, sms, 4), t, stream, a);
+  const long long pieces = vec ? a.N / VW : a.N;
+  const int t = threads_of(pieces, held_of(vec ? VW : 1), few);
+  return launch(vec ? norm_kernel<E, W, VW, I8> : norm_kernel<E, W, 1, I8>,
+                blocks_of(a.M, t, sms, 512), t, stream, a);
 }
 
+// `blocks` make a part of dw each: of norm_grad_kernel where a row is `held`, else
+// slabs of column_kernel.
 template <typename E, typename W>
 cudaError_t backward(GradArgs a, W* dw, float* partial, int blocks, int sms, cudaStream_t stream,
-                     int threads, bool vec, int held) {
+                     int threads, bool vec, bool held) {
   constexpr int VW = 16 / (int)sizeof(E);
   a.partial = partial;
   cudaError_t e = cudaSuccess;
-  if (held != 0) {
-    e = !vec ? launch(norm_grad_kernel<E, W, 1, 8, true>, blocks, threads, stream, a)
-        : held == 2 ? launch(norm_grad_kernel<E, W, VW, 2, true>, blocks, threads, stream, a)
-                    : launch(norm_grad_kernel<E, W, VW, 4, true>, blocks, threads, stream, a);
+  if (held) {
+    e = launch(vec ? norm_grad_kernel<E, W, VW, true> : norm_grad_kernel<E, W, 1, true>, blocks,
+               threads, stream, a);
   } else {
     if (a.dx != nullptr)
-      e = vec ? launch(norm_grad_kernel<E, W, VW, 4, false>, blocks_of(a.M, threads, sms, 4), threads, stream, a)
-              : launch(norm_grad_kernel<E, W, 1, 8, false>, blocks_of(a.M, threads, sms, 4), threads, stream, a);
+      e = launch(vec ? norm_grad_kernel<E, W, VW, false> : norm_grad_kernel<E, W, 1, false>,
+                 blocks_of(a.M, threads, sms, 512), threads, stream, a);
     if (e == cudaSuccess && dw != nullptr) {
       const long long all = (a.N + kColumnThreads - 1ll) / kColumnThreads * blocks;
       e = launch(column_kernel<E>, all < sms * 8ll ? all : sms * 8ll, kColumnThreads, stream, a, blocks);
@@ -608,14 +648,12 @@ SGEMM_API int sgemm_rms_norm_grad(int M, int N, int type, const void* dY, int ld
                    rows::aligned(dH, lddh, eb, 16) && rows::aligned(dX, lddx, eb, 16) &&
                    rows::aligned(weight, 0, wb, 16) && N % vw == 0;
   const long long pieces = vec ? N / vw : N;
-  // pieces that a thread holds of a row; 0: the row is too long for that
-  const int held = !vec ? (pieces <= 8 * rows::kMaxThreads ? 8 : 0)
-                        : (pieces <= 2 * 256 ? 2 : (pieces <= 4 * rows::kMaxThreads ? 4 : 0));
-  const int threads = rows::threads_of(pieces, held == 0 ? (vec ? 4 : 8) : held, M < 2 * sms);
-  // blocks (each makes a part of dw), or slabs of rows
+  const int most = rows::held_of(vec ? vw : 1);
+  const bool held = pieces <= most * rows::kMaxThreads;
+  const int threads = rows::threads_of(pieces, most, M < 2 * sms);
   int blocks = 0;
-  if (held != 0) {
-    blocks = rows::blocks_of(M, threads, sms, held == 2 ? 4 : 2);
+  if (held) {
+    blocks = rows::blocks_of(M, threads, sms, 512);
   } else {
     const int fill = sms * 8 / (int)((N + rows::kColumnThreads - 1ll) / rows::kColumnThreads) + 1;
     blocks = M < fill ? M : fill;
