@@ -109,6 +109,8 @@ def lib() -> ctypes.CDLL:
                 "sgemm_rms_norm": (I, [I, I, I, P, I, P, I, P, I, F, P, I, P, I, P, P]),
                 "sgemm_rms_norm_i8": (I, [I, I, I, P, I, P, I, P, I, F, P, I, P, I, P, P]),
                 "sgemm_rms_norm_grad": (I, [I, I, I, P, I, P, I, P, I, P, P, I, P, I, P, P]),
+                "sgemm_linear_ce": (I, [I, I, I, I, P, I, P, I, P, LL, P, P, P]),
+                "sgemm_linear_ce_grad": (I, [I, I, I, I, P, I, P, I, P, LL, P, P, P, I, P, I, P]),
                 "sgemm_strided_batched": (I, [I, I, I, I, I, F, P, I, LL, P, I, LL, F, P, I, LL,
                                               I, P]),
             }
@@ -406,7 +408,7 @@ def sgemm_grad_clip(grads, out, sizes, types, max_norm, norm, stream=None) -> in
                                  (ctypes.c_int * n)(*types), max_norm, norm, stream)
 
 
-# ---- the output end of a model: norm, ... -------------------------------------------
+# ---- the output end of a model: norm, loss over the vocabulary ----------------------
 def sgemm_rms_norm(M, N, type, X, ldx, R, ldr, weight, weight_type, eps, H, ldh, Y, ldy, rstd=None,
                    stream=None) -> int:
     """H = X + R (R None: X itself), Y = H / sqrt(mean(H^2) + eps) * weight row by
@@ -429,6 +431,21 @@ def sgemm_rms_norm_grad(M, N, type, dY, lddy, H, ldh, weight, weight_type, rstd,
     status code."""
     return lib().sgemm_rms_norm_grad(M, N, type, dY, lddy, H, ldh, weight, weight_type, rstd, dH,
                                      lddh, dX, lddx, dweight, stream)
+
+
+def sgemm_linear_ce(type, T, V, H, X, ldx, W, ldw, target, ignore_index, loss, lse=None, stream=None) -> int:
+    """loss[t] = log(sum_v exp(X[t] . W[v])) - X[t] . W[target[t]], 0 where the
+    target is ignore_index; lse (may be None) receives the logarithms. Returns
+    the status code."""
+    return lib().sgemm_linear_ce(type, T, V, H, X, ldx, W, ldw, target, ignore_index, loss, lse, stream)
+
+
+def sgemm_linear_ce_grad(type, T, V, H, X, ldx, W, ldw, target, ignore_index, lse, dloss, dX, lddx, dW,
+                         lddw, stream=None) -> int:
+    """Gradients of sgemm_linear_ce for dloss; dX or dW may be None. Returns the
+    status code."""
+    return lib().sgemm_linear_ce_grad(type, T, V, H, X, ldx, W, ldw, target, ignore_index, lse, dloss,
+                                      dX, lddx, dW, lddw, stream)
 
 
 # ---- torch conveniences (marshalling only) ------------------------------------------
@@ -489,7 +506,8 @@ def _native():
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
     loader.exec_module(module)
     names = ("sgemm_grouped", "sgemm_grouped_wgrad", "sgemm_i8_quantize", "sgemm_i8", "sgemm_grad_clip",
-             "sgemm_rms_norm", "sgemm_rms_norm_i8", "sgemm_rms_norm_grad")
+             "sgemm_rms_norm", "sgemm_rms_norm_i8", "sgemm_rms_norm_grad", "sgemm_linear_ce",
+             "sgemm_linear_ce_grad")
     module.bind(tuple(ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in names), SgemmError)
     return module
 
@@ -552,3 +570,19 @@ def rms_norm_grad(dY, H, weight, rstd, dH=None, dX=None, dweight=None, want=(Tru
     alike; dH is the gradient that reaches H itself. What is not wanted is None."""
     return _native().rms_norm_grad(dY, H, weight, rstd, dH, dX, dweight, bool(want[0]), bool(want[1]),
                                    stream)
+
+
+def linear_cross_entropy(X, W, target, ignore_index=-100, loss=None, lse=None, stream=None):
+    """(loss, lse), float32 with a value for each row of X: the softmax cross
+    entropy of the logits X @ W.T with the words target (int64), 0 where target
+    is ignore_index, and the logarithm of the sum of the logits' exponentials.
+    The logits are not kept. A target that is no word gives NaN."""
+    return _native().linear_cross_entropy(X, W, target, ignore_index, loss, lse, stream)
+
+
+def linear_cross_entropy_grad(X, W, target, lse, dloss, ignore_index=-100, dX=None, dW=None,
+                              want=(True, True), stream=None):
+    """(dX, dW): gradients of linear_cross_entropy for dloss, the gradient of each
+    row's loss (float32). What is not wanted is None."""
+    return _native().linear_cross_entropy_grad(X, W, target, lse, dloss, ignore_index, dX, dW,
+                                               bool(want[0]), bool(want[1]), stream)

@@ -232,7 +232,7 @@ bool misaligned(const void* p, int bytes) {
 }
 
 // The built kernels, and per device what prepare() said of each.
-constexpr int kMaxDevices = 64, kMaxForms = 24;
+constexpr int kMaxDevices = 64, kMaxForms = 32;
 struct Built {
   bool ready;
   int workers;
@@ -247,7 +247,9 @@ const FormEntry* form_entry(int i) {
   i -= kNumForms16;
   if (i < kNumFormsF32) return &kFormsF32[i];
   i -= kNumFormsF32;
-  return i < kNumFormsI8 ? &kFormsI8[i] : nullptr;
+  if (i < kNumFormsI8) return &kFormsI8[i];
+  i -= kNumFormsI8;
+  return i < kNumFormsLoss ? &kFormsLoss[i] : nullptr;
 }
 
 // The entry of a form and its resident workers on `dev` (null: not built or,
@@ -286,10 +288,13 @@ constexpr TileCost kTileCosts[] = {
     {kI8, 128, 1, 460, 1300},
     {kI8Wide, 256, 2, 364, 2500},
 };
-// The costs of a form: those of its own number of CTAs (integers that have been
-// widened cost what F16 operands do).
+// Integers that have been widened cost what F16 operands do, and so do the
+// products of a loss (built from 64 columns on).
+bool loss(int src) { return src == kLse || src == kGrad; }
+int cost_source(int src) { return src == kI8Wide || loss(src) ? k16 : src; }
+// The costs of a form: those of its own number of CTAs.
 TileCost tile_cost(int src, int bq, int cl) {
-  const int as = src == kI8Wide ? k16 : src;
+  const int as = cost_source(src);
   for (const TileCost& c : kTileCosts)
     if (c.src == as && c.bq == bq && c.cl == cl) return c;
   return kTileCosts[0];   // (every built form has its entry)
@@ -314,7 +319,7 @@ Form choose_tile(int src, const Params& p, int sms, double* ns) {
   Form best{src, 0, 1};
   double least = 0;
   for (const TileCost& c : kTileCosts) {
-    if (c.src != src || (p.wgrad && c.bq < 64)) continue;
+    if (c.src != (loss(src) ? k16 : src) || ((p.wgrad || loss(src)) && c.bq < 64)) continue;
     const int workers = sms / c.cl;
     const double groups = p.E < p.T ? p.E : (p.T > 0 ? p.T : 1);
     const double q = p.wgrad ? (double)p.E * cdiv(p.Q, c.bq)
@@ -357,38 +362,36 @@ bool widen_first(const Params& p, int sms, double tiles_ns, double copied, doubl
   return ns + 4000 + 0.65e-3 * values < tiles_ns;
 }
 
-// The operands as stored. Fills the maps (copying what TMA cannot read), the
-// workspace fields of `p`, and launches.
-int run(int src, int type, Params p, Operand op_p, Operand op_q, cudaStream_t stream,
-        const char* what) {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) {
+}  // namespace
+
+int plan(int src, int type, const Params& p, const Operand& op_p, const Operand& op_q, Plan* out) {
+  Plan r = {};
+  if (cudaGetDevice(&r.dev) != cudaSuccess) {
     cudaGetLastError();
     return SGEMM_ERR_LAUNCH;
   }
-  int st = library_device_sms(dev, &sms);
+  const int st = library_device_sms(r.dev, &r.sms);
   if (st != SGEMM_OK) return st;
   if (tensor_map_encode() == nullptr) return SGEMM_ERR_LAUNCH;
 
   const int width = g_width.load(), ctas = g_ctas.load();
   double ns = 0;
-  Form t = choose_tile(src, p, sms, &ns);
+  Form t = choose_tile(src, p, r.sms, &ns);
   if (src == kI8) {
     const double vp = (double)op_p.rows * op_p.cols, vq = (double)op_q.rows * op_q.cols;
     const double copied = (op_p.direct() ? 0 : vp) + (op_q.direct() ? 0 : vq);
     // (256 columns are built for widened operands only)
-    if (width > 0 ? width == 256 : widen_first(p, sms, ns, copied, vp + vq)) {
+    if (width > 0 ? width == 256 : widen_first(p, r.sms, ns, copied, vp + vq)) {
       src = kI8Wide;
-      t = choose_tile(src, p, sms, &ns);
+      t = choose_tile(src, p, r.sms, &ns);
     }
   }
-  int workers = 0;
-  const FormEntry* form = nullptr;
-  if (width > 0 && (!p.wgrad || width >= 64)) form = find_form(dev, sms, src, width, ctas, &workers);
-  if (form == nullptr) form = find_form(dev, sms, t.src, t.bq, t.cl, &workers);
-  if (form == nullptr && t.cl == 2) form = find_form(dev, sms, t.src, t.bq, 1, &workers);
-  if (form == nullptr) return SGEMM_ERR_LAUNCH;
-  const int bq = form->form.bq, cl = form->form.cl;
+  if (width > 0 && (!p.wgrad || width >= 64))
+    r.form = find_form(r.dev, r.sms, src, width, ctas, &r.workers);
+  if (r.form == nullptr) r.form = find_form(r.dev, r.sms, t.src, t.bq, t.cl, &r.workers);
+  if (r.form == nullptr && t.cl == 2) r.form = find_form(r.dev, r.sms, t.src, t.bq, 1, &r.workers);
+  if (r.form == nullptr) return SGEMM_ERR_LAUNCH;
+  const int bq = r.form->form.bq, cl = r.form->form.cl;
 
   // tiles and k-slices are numbered with 32-bit integers
   const int sub_k = src == kF32 ? 32 : 64, slice = bq <= 32 ? 2 * sub_k : sub_k;
@@ -400,57 +403,81 @@ int run(int src, int type, Params p, Operand op_p, Operand op_q, cudaStream_t st
               : tiles * (cdiv(p.K, slice) + 1);
   if (tiles > 0x7fffffffLL || slices > 0x7fffffffLL) return SGEMM_ERR_INVALID_DIM;
 
-  const bool reads = p.K > 0;
-  const bool widen = src == kI8Wide;
-  const size_t pack_p = reads ? op_p.packed_bytes(widen) : 0;
-  const size_t pack_q = reads ? op_q.packed_bytes(widen) : 0;
-  const size_t partial = (size_t)workers * cl * 2 * BP * bq * 4;
-  float* ws = nullptr;
-  const std::unique_lock<std::mutex> lock = library_lock();   // to the last launch
-  st = library_workspace(dev, stream, (pack_p + pack_q + partial) / 4, (size_t)workers * cl, &ws,
-                         &p.status, nullptr, nullptr, &p.counters);
-  if (st != SGEMM_OK) return st;
-  char* at = reinterpret_cast<char*>(ws);
-  if ((pack_p || pack_q) &&
-      pack_operands(&op_p, pack_p ? at : nullptr, &op_q, pack_q ? at + pack_p : nullptr, widen, sms,
-                    stream) != cudaSuccess) {
+  const bool reads = p.K > 0, widen = src == kI8Wide;
+  r.src = src;
+  r.type = type;
+  r.slice = slice;
+  r.pack_p = reads ? op_p.packed_bytes(widen) : 0;
+  r.pack_q = reads ? op_q.packed_bytes(widen) : 0;
+  r.partial = (size_t)r.workers * cl * 2 * BP * bq * 4;
+  *out = r;
+  return SGEMM_OK;
+}
+
+int launch(const Plan& r, Params p, Operand op_p, Operand op_q, char* at, cudaStream_t stream,
+           const char* what) {
+  const int src = r.src, bq = r.form->form.bq, cl = r.form->form.cl;
+  if ((r.pack_p || r.pack_q) &&
+      pack_operands(&op_p, r.pack_p ? at : nullptr, &op_q, r.pack_q ? at + r.pack_p : nullptr,
+                    src == kI8Wide, r.sms, stream) != cudaSuccess) {
     cudaGetLastError();
     return SGEMM_ERR_LAUNCH;
   }
-  p.partials = reinterpret_cast<float*>(at + pack_p + pack_q);
+  p.partials = reinterpret_cast<float*>(at + r.pack_p + r.pack_q);
   {
-    const double ns = (double)tile_cost(src, bq, cl).slice * slice / 64;
-    const double sum = (double)(p.wgrad ? p.T / p.E : p.K) / slice;
+    const double ns = (double)tile_cost(src, bq, cl).slice * r.slice / 64;
+    const double sum = (double)(p.wgrad ? p.T / p.E : p.K) / r.slice;
     p.cut_least = cut_least(sum < 1 ? 1 : sum, (int)ns, bq);
     p.cut_once = (int)(16 * cut_once(bq) / ns) + 1;
     p.cut_part = (int)(16 * cut_part(bq) / ns) + 1;
   }
   p.timeout_ns = library_wait_timeout_ns();
 
+  const int sub_k = src == kF32 ? 32 : 64;
   CUtensorMap mp = {}, mq = {};
-  if (reads) {
+  if (p.K > 0) {
     const CUtensorMapDataType dt =
         src == kI8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                   : (type == SGEMM_TYPE_F32
+                   : (r.type == SGEMM_TYPE_F32
                           ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                          : (type == SGEMM_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT16));
+                          : (r.type == SGEMM_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16));
     const int row_bytes = src == kI8 ? 64 : 128;
     if (!encode_operand(&mp, op_p, dt, row_bytes, p.p_mn ? sub_k : BP) ||
         !encode_operand(&mq, op_q, dt, row_bytes, p.q_mn ? sub_k : bq / cl))
       return SGEMM_ERR_LAUNCH;
   }
-  if (form->launch(workers, p, mp, mq, stream) != cudaSuccess) {
+  if (r.form->launch(r.workers, p, mp, mq, stream) != cudaSuccess) {
     cudaGetLastError();
     return SGEMM_ERR_LAUNCH;
   }
   char text[160];
   snprintf(text, sizeof(text), "%s_%s_%dx%dx%d cluster=%d grid=%d%s%s", what,
-           src == k16 ? (type == SGEMM_TYPE_BF16 ? "bf16" : "f16") : (src == kF32 ? "f32" : "i8"),
-           BP * cl, bq, slice, cl, workers * cl, pack_p ? " p=copied" : "", pack_q ? " q=copied" : "");
+           src == k16 || loss(src) ? (r.type == SGEMM_TYPE_BF16 ? "bf16" : "f16")
+                                   : (src == kF32 ? "f32" : "i8"),
+           BP * cl, bq, r.slice, cl, r.workers * cl, r.pack_p ? " p=copied" : "",
+           r.pack_q ? " q=copied" : "");
   note_last_config(text);
   return SGEMM_OK;
 }
+
+namespace {
+
+// The operands as stored. Plans the call, takes the workspace and launches.
+int run(int src, int type, Params p, const Operand& op_p, const Operand& op_q, cudaStream_t stream,
+        const char* what) {
+  Plan r = {};
+  int st = plan(src, type, p, op_p, op_q, &r);
+  if (st != SGEMM_OK) return st;
+  float* ws = nullptr;
+  const std::unique_lock<std::mutex> lock = library_lock();   // to the last launch
+  st = library_workspace(r.dev, stream, r.bytes() / 4, r.counters(), &ws, &p.status, nullptr,
+                         nullptr, &p.counters);
+  if (st != SGEMM_OK) return st;
+  return launch(r, p, op_p, op_q, reinterpret_cast<char*>(ws), stream, what);
+}
+
+}  // namespace
 
 // Values of k per tensor-memory accumulation. Each instruction truncates its
 // sum: with n of them in one accumulation a 32-bit result is off by 1.4e-8 n
@@ -468,7 +495,6 @@ int accumulation_chunk(int src, int out_type) {
   return out_type == kOutF32 ? 256 : 1024;
 }
 
-}  // namespace
 }  // namespace ragged
 }  // namespace sgemm_gb300
 

@@ -1,0 +1,592 @@
+// linear_ce.cu -- sgemm_linear_ce and sgemm_linear_ce_grad: softmax cross
+// entropy of the logits X W^T over a vocabulary, and its gradients, without
+// keeping the logits.
+//
+// Mathematics, for token t with target word a and upstream gradient d:
+//   z_v = x_t . w_v,  lse = log sum_v exp z_v,  loss = lse - z_a
+//   g_v = (exp(z_v - lse) - [v == a]) d;   dX = G W,  dW = G^T X.
+// The vocabulary is taken in pieces. 16-bit operands: the product's epilogue
+// holds a token's logits in registers (ragged_kernel, kLse and kGrad), from
+// which the loss takes the largest and the sum of exponentials of each tile,
+// and the gradient pass, which forms the logits once more, writes a piece of G
+// in the operands' type. FP32 operands: a piece of the logits is written in
+// FP32, reduced or transformed in place by the kernels below.
+//
+// G in 16 bits: each of its values is off by half a unit, some 2^-9 (BF16) or
+// 2^-12 of it, as if the operands of the two products had been rounded, which
+// they are; in dX and dW these errors add up as random ones do. So that small
+// gradients keep their bits in F16, rows are scaled by d / max|d|, times 2^14 in
+// F16 (values up to 2^14; a probability of 10^-5 is a normal number), and the
+// products by the inverse.
+//
+// Operations: 2 T V H forward; 6 T V H for the gradients, 2 of which form the
+// logits again (in exchange a piece of G is all that is ever stored).
+#include <cuda_runtime.h>
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+
+#include "../../include/sgemm_gb300.h"
+#include "elements.cuh"
+#include "ragged_launch.cuh"
+
+#define SGEMM_API extern "C" __attribute__((visibility("default")))
+
+namespace sgemm_gb300 {
+namespace loss {
+namespace {
+
+using ragged::Operand;
+using ragged::Params;
+
+// A piece of the vocabulary: as many words as keep what is stored of it (G, or
+// FP32 logits) within this, at least kLeastWords. Each piece costs some 10 us of
+// launches and ragged last waves; 4096 tokens have 65536 words a piece.
+constexpr size_t kPieceBytes = 512u << 20;
+constexpr int kLeastWords = 2048;
+// Statistics of a piece (16 bits): 8 bytes for each token and half tile.
+constexpr size_t kStatsBytes = 256u << 20;
+
+constexpr float kLeast = -3.402823466e38f;
+constexpr uint32_t kAll = 0xffffffffu;
+
+// (most, sum) of two disjoint sets of logits.
+__device__ __forceinline__ float2 merge(float2 a, float2 b) {
+  const float m = fmaxf(a.x, b.x);
+  return make_float2(m, a.y * expf(a.x - m) + b.y * expf(b.x - m));
+}
+
+// The parts of a piece and what the pieces before gave, token by token: 32
+// tokens a block, kGroups threads a token.
+constexpr int kGroups = 8;
+struct Join {
+  int T, V, parts;
+  const float2* stats;        // [part][token]
+  float2* state;              // [token]: of the pieces so far
+  int first, last;
+  const long long* target;
+  long long ignore;
+  const float* at_target;
+  float *loss, *lse;
+};
+__global__ void __launch_bounds__(32 * kGroups) join_kernel(const Join a) {
+  __shared__ float2 part[kGroups][32];
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
+  for (long long t0 = blockIdx.x * 32ll; t0 < a.T; t0 += gridDim.x * 32ll) {
+    const long long t = t0 + lane;
+    float2 s = make_float2(kLeast, 0.f);
+    if (t < a.T) {
+      // (most first, then the sums: one exponential a part, loads that do not wait)
+      float most = kLeast;
+#pragma unroll 8
+      for (int p = group; p < a.parts; p += kGroups)
+        most = fmaxf(most, __ldg(&a.stats[(long long)p * a.T + t].x));
+      float sum = 0.f;
+#pragma unroll 8
+      for (int p = group; p < a.parts; p += kGroups) {
+        const float2 v = __ldg(&a.stats[(long long)p * a.T + t]);
+        sum += v.y * expf(v.x - most);
+      }
+      s = make_float2(most, sum);
+    }
+    part[group][lane] = s;
+    __syncthreads();
+    if (group == 0 && t < a.T) {
+#pragma unroll
+      for (int g = 1; g < kGroups; ++g) s = merge(s, part[g][lane]);
+      if (!a.first) s = merge(a.state[t], s);
+      if (!a.last) {
+        a.state[t] = s;
+      } else {
+        const float lse = s.x + logf(s.y);
+        const long long word = a.target[t];
+        if (a.lse != nullptr) a.lse[t] = lse;
+        // a word that is none has no loss: NaN says so
+        a.loss[t] = word == a.ignore ? 0.f
+                    : word < 0 || word >= a.V ? __uint_as_float(0x7fc00000u)
+                                              : lse - a.at_target[t];
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Factors of the tokens' gradients: d / c * unit, c the largest |d| (1 where
+// that is 0 or no number), and c / unit, the factor of the products. 0 for a
+// token that is not counted, NaN for one whose target is no word. One block.
+constexpr int kScaleThreads = 1024;
+__global__ void __launch_bounds__(kScaleThreads)
+    scale_kernel(int T, int V, const long long* target, long long ignore, const float* d,
+                 float unit, float* row_scale, float* alpha) {
+  __shared__ float part[kScaleThreads / 32];
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  float most = 0.f;
+  for (long long t = threadIdx.x; t < T; t += kScaleThreads)
+    if (target[t] != ignore) most = fmaxf(most, fabsf(d[t]));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, o));
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = most;
+  __syncthreads();
+  most = 0.f;
+  for (int i = 0; i < kScaleThreads / 32; ++i) most = fmaxf(most, part[i]);
+  const float c = most > 0.f && most <= 3e38f ? most : 1.f;
+  for (long long t = threadIdx.x; t < T; t += kScaleThreads) {
+    const long long word = target[t];
+    row_scale[t] = word == ignore              ? 0.f
+                   : word < 0 || word >= V ? __uint_as_float(0x7fc00000u)
+                                           : d[t] / c * unit;
+  }
+  if (threadIdx.x == 0) *alpha = c / unit;
+}
+
+// FP32: statistics of a piece of logits, a row per block.
+constexpr int kRowThreads = 256;
+__global__ void __launch_bounds__(kRowThreads)
+    stats_kernel(int T, int n, const float* z, long long ldz, const long long* target, int col0,
+                 float2* stats, float* at_target) {
+  __shared__ float2 part[kRowThreads / 32];
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  for (long long t = blockIdx.x; t < T; t += gridDim.x) {
+    const float* row = z + t * ldz;
+    float2 s = make_float2(kLeast, 0.f);
+    for (int c0 = threadIdx.x; c0 < n; c0 += 8 * kRowThreads) {
+      float v[8], m = s.x;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = c0 + i * kRowThreads < n ? __ldcg(row + c0 + i * kRowThreads) : -INFINITY;
+        m = fmaxf(m, v[i]);
+      }
+      float sum = s.y * expf(s.x - m);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += expf(v[i] - m);
+      s = make_float2(m, sum);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      s = merge(s, make_float2(__shfl_xor_sync(kAll, s.x, o), __shfl_xor_sync(kAll, s.y, o)));
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+      for (int w = 1; w < kRowThreads / 32; ++w) s = merge(s, part[w]);
+      stats[t] = s;
+      const long long rel = target[t] - col0;
+      if (rel >= 0 && rel < n) at_target[t] = row[rel];
+    }
+    __syncthreads();
+  }
+}
+
+// FP32: a piece of logits into G, in place.
+__global__ void __launch_bounds__(kRowThreads)
+    gradient_kernel(int T, int n, float* z, long long ldz, const long long* target, int col0,
+                    const float* lse, const float* row_scale) {
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const long long blocks = (n + 4ll * kRowThreads - 1) / (4 * kRowThreads);   // of a row
+  for (long long b = blockIdx.x; b < blocks * T; b += gridDim.x) {
+    const long long t = b / blocks;
+    const long long c0 = (b - t * blocks) * (4 * kRowThreads) + threadIdx.x;
+    float* row = z + t * ldz;
+    const float l = lse[t], s = row_scale[t];
+    const long long a = target[t] - col0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const long long c = c0 + i * kRowThreads;
+      if (c >= n) break;
+      const float e = expf(row[c] - l);
+      row[c] = s == 0.f ? 0.f : (c == a ? e - 1.f : e) * s;
+    }
+  }
+}
+
+// Rows of FP32 sums to the gradient's type.
+template <typename E>
+__global__ void __launch_bounds__(kRowThreads)
+    round_kernel(int T, int H, const float* sums, E* out, long long ldo) {
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const long long blocks = (H + 4ll * kRowThreads - 1) / (4 * kRowThreads);
+  for (long long b = blockIdx.x; b < blocks * T; b += gridDim.x) {
+    const long long t = b / blocks;
+    const long long c0 = (b - t * blocks) * (4 * kRowThreads) + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const long long c = c0 + i * kRowThreads;
+      if (c < H) out[t * ldo + c] = rows::from_f32<E>(__ldcg(sums + t * H + c));
+    }
+  }
+}
+
+template <typename... A>
+cudaError_t start(void (*kernel)(A...), long long blocks, int threads, cudaStream_t stream,
+                  std::common_type_t<A>... args) {
+  cudaLaunchConfig_t lc = {};
+  cudaLaunchAttribute la[1];
+  la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  la[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.gridDim = dim3((unsigned)blocks);
+  lc.blockDim = dim3((unsigned)threads);
+  lc.stream = stream;
+  lc.attrs = la;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, kernel, args...);
+}
+int done(cudaError_t e) {
+  if (e == cudaSuccess) return SGEMM_OK;
+  cudaGetLastError();
+  return SGEMM_ERR_LAUNCH;
+}
+long long at_most(long long a, long long b) { return a < b ? a : b; }
+size_t padded(size_t bytes) { return (bytes + 255) / 256 * 256; }
+
+// What both calls are given (checked), and the products they are made of.
+struct Problem {
+  int type, T, V, H;
+  const void *X, *W;
+  int ldx, ldw;
+  const long long* target;
+  long long ignore;
+
+  int elem() const { return type == SGEMM_TYPE_F32 ? 4 : 2; }
+  bool f32() const { return type == SGEMM_TYPE_F32; }
+  Operand x() const { return Operand{X, elem(), T, H, ldx, 0, 1}; }
+  Operand words(int v0, int n) const {
+    return Operand{static_cast<const char*>(W) + (size_t)v0 * ldw * elem(), elem(), n, H, ldw, 0, 1};
+  }
+  // words of a piece: equal pieces of whole tiles
+  int piece(size_t bytes_per_word, size_t most) const {
+    if (V == 0) return 1;
+    size_t n = bytes_per_word == 0 ? (size_t)V : most / bytes_per_word;
+    if (n < (size_t)kLeastWords) n = kLeastWords;
+    if (n >= (size_t)V) return V;
+    const long long pieces = (V + (long long)n - 1) / (long long)n;
+    return (int)at_most(V, ((V + pieces - 1) / pieces + 255) / 256 * 256);
+  }
+  // logits of n words: 16 bits, a token a lane (kLse, kGrad) ...
+  Params per_token(int n, int v0) const {
+    Params p = {};
+    p.E = 1;
+    p.T = n;
+    p.P = T;
+    p.K = H;
+    p.bf16 = type == SGEMM_TYPE_BF16;
+    p.alpha = 1.f;
+    p.chunk = ragged::accumulation_chunk(ragged::k16, SGEMM_TYPE_BF16);
+    p.target = target;
+    p.col0 = v0;
+    return p;
+  }
+  // ... FP32, written as they are
+  Params plain(int n, float* z, long long ldz) const {
+    Params p = {};
+    p.E = 1;
+    p.T = T;
+    p.P = n;
+    p.K = H;
+    p.out = z;
+    p.ldo = ldz;
+    p.out_type = SGEMM_TYPE_F32;
+    p.alpha = 1.f;
+    p.chunk = ragged::accumulation_chunk(ragged::kF32, SGEMM_TYPE_F32);
+    return p;
+  }
+};
+
+// Bytes of the workspace, handed out one after another.
+struct Carve {
+  size_t used = 0;
+  size_t take(size_t bytes) {
+    const size_t at = used;
+    used += padded(bytes);
+    return at;
+  }
+};
+
+int check(int type, int T, int V, int H, const void* X, int ldx, const void* W, int ldw,
+          const long long* target) {
+  if (type != SGEMM_TYPE_F32 && type != SGEMM_TYPE_BF16 && type != SGEMM_TYPE_F16)
+    return SGEMM_ERR_INVALID_VALUE;
+  if (T < 0 || V < 0 || H < 0) return SGEMM_ERR_INVALID_DIM;
+  const int least = H > 1 ? H : 1;
+  if (ldx < least || ldw < least) return SGEMM_ERR_INVALID_LD;
+  if (T > 0 && target == nullptr) return SGEMM_ERR_NULL_PTR;
+  if (T > 0 && V > 0 && H > 0 && (X == nullptr || W == nullptr)) return SGEMM_ERR_NULL_PTR;
+  const uintptr_t mask = type == SGEMM_TYPE_F32 ? 3u : 1u;
+  if (((reinterpret_cast<uintptr_t>(X) | reinterpret_cast<uintptr_t>(W)) & mask) ||
+      (reinterpret_cast<uintptr_t>(target) & 7u))
+    return SGEMM_ERR_MISALIGNED;
+  return SGEMM_OK;
+}
+bool odd(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
+
+int forward(const Problem& q, float* loss, float* lse, cudaStream_t stream) {
+  const int T = q.T, V = q.V;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return done(cudaErrorInvalidDevice);
+  int st = library_device_sms(dev, &sms);
+  if (st != SGEMM_OK) return st;
+  // statistics of a piece: one part for a piece of FP32 logits, else two for
+  // each tile of at least 64 words
+  const int n = q.f32() ? q.piece((size_t)T * 4, kPieceBytes) : q.piece((size_t)T / 4 + 1, kStatsBytes);
+  const int most_parts = q.f32() ? 1 : 2 * ragged::cdiv(n, 64);
+  const long long ldz = (n + 3) / 4 * 4;
+  Carve ws;
+  const size_t at_state = ws.take((size_t)T * 8), at_z = ws.take((size_t)T * 4);
+  const size_t at_stats = ws.take((size_t)T * 8 * most_parts);
+  const size_t at_logits = ws.take(q.f32() ? (size_t)T * ldz * 4 : 0);
+
+  // (the first piece is the largest; the others run by its plan)
+  ragged::Plan first = {};
+  const Operand x = q.x();
+  const int n0 = n < V ? n : V;
+  if (V > 0) {
+    st = q.f32() ? ragged::plan(ragged::kF32, q.type, q.plain(n0, nullptr, ldz), q.words(0, n0), x, &first)
+                 : ragged::plan(ragged::kLse, q.type, q.per_token(n0, 0), x, q.words(0, n0), &first);
+    if (st != SGEMM_OK) return st;
+  }
+  float* base = nullptr;
+  int* status = nullptr;
+  uint32_t* counters = nullptr;
+  const std::unique_lock<std::mutex> lock = library_lock();   // to the last launch
+  st = library_workspace(dev, stream, (ws.used + (V > 0 ? first.bytes() : 0)) / 4,
+                         V > 0 ? first.counters() : 1, &base, &status, nullptr, nullptr, &counters);
+  if (st != SGEMM_OK) return st;
+  char* at = reinterpret_cast<char*>(base);
+  float2* stats = reinterpret_cast<float2*>(at + at_stats);
+  float* at_target = reinterpret_cast<float*>(at + at_z);
+  float* z = reinterpret_cast<float*>(at + at_logits);
+
+  Join join = {};
+  join.T = T;
+  join.V = V;
+  join.stats = stats;
+  join.state = reinterpret_cast<float2*>(at + at_state);
+  join.target = q.target;
+  join.ignore = q.ignore;
+  join.at_target = at_target;
+  join.loss = loss;
+  join.lse = lse;
+  const long long join_blocks = at_most((T + 31ll) / 32, sms * 8ll);
+  int v0 = 0;
+  do {
+    const int m = (int)at_most(n, V - v0);
+    if (m > 0) {
+      Params p = q.f32() ? q.plain(m, z, ldz) : q.per_token(m, v0);
+      p.status = status;
+      p.counters = counters;
+      p.stats = stats;
+      p.at_target = at_target;
+      const Operand w = q.words(v0, m);
+      if (q.f32()) {
+        st = ragged::launch(first, p, w, x, at + ws.used, stream, "linear_ce");
+        if (st != SGEMM_OK) return st;
+        st = done(start(stats_kernel, at_most(T, sms * 8ll), kRowThreads, stream, T, m,
+                        static_cast<const float*>(z), ldz, q.target, v0, stats, at_target));
+        join.parts = 1;
+      } else {
+        st = ragged::launch(first, p, x, w, at + ws.used, stream, "linear_ce");
+        join.parts = 2 * ragged::cdiv(m, first.form->form.bq);
+      }
+      if (st != SGEMM_OK) return st;
+    }
+    join.first = v0 == 0;
+    v0 += m;
+    join.last = v0 >= V;
+    st = done(start(join_kernel, join_blocks, 32 * kGroups, stream, join));
+    if (st != SGEMM_OK) return st;
+  } while (v0 < V);
+  return SGEMM_OK;
+}
+
+int backward(const Problem& q, const float* lse, const float* dloss, void* dX, int lddx, void* dW,
+             int lddw, cudaStream_t stream) {
+  const int T = q.T, V = q.V, H = q.H, elem = q.elem();
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return done(cudaErrorInvalidDevice);
+  int st = library_device_sms(dev, &sms);
+  if (st != SGEMM_OK) return st;
+  const int n = q.piece((size_t)T * elem, kPieceBytes);
+  const int n0 = n < V ? n : V;
+  const bool sums = dX != nullptr && !q.f32() && n < V;   // dX is added up in FP32
+  const int per16 = 16 / elem;
+  const long long ldg = (n + per16 - 1) / per16 * per16;
+  Carve ws;
+  const size_t at_scale = ws.take((size_t)T * 4), at_alpha = ws.take(4);
+  const size_t at_g = ws.take((size_t)T * ldg * elem);
+  const size_t at_sums = ws.take(sums ? (size_t)T * H * 4 : 0);
+
+  const int src = q.f32() ? ragged::kF32 : ragged::k16;
+  const Operand x = q.x();
+  auto gradient = [&](int m, int v0, void* g) {
+    Params p = q.f32() ? q.plain(m, static_cast<float*>(g), ldg) : q.per_token(m, v0);
+    p.out = g;
+    p.ldo = ldg;
+    return p;
+  };
+  // dX = G W: W stored with the words, the contraction, as its rows
+  auto input = [&](int m, int v0, float* acc) {
+    Params p = {};
+    p.E = 1;
+    p.T = T;
+    p.P = H;
+    p.K = m;
+    p.p_mn = 1;
+    p.bf16 = q.type == SGEMM_TYPE_BF16;
+    p.out = acc != nullptr ? acc : dX;
+    p.ldo = acc != nullptr ? H : lddx;
+    p.out_type = acc != nullptr ? SGEMM_TYPE_F32 : q.type;
+    p.alpha = 1.f;
+    p.beta = v0 > 0 ? 1.f : 0.f;
+    p.chunk = ragged::accumulation_chunk(src, q.type);
+    return p;
+  };
+  // dW = G^T X
+  auto weight = [&](int m, int v0) {
+    Params p = {};
+    p.wgrad = 1;
+    p.E = 1;
+    p.T = T;
+    p.P = H;
+    p.Q = m;
+    p.K = T;
+    p.p_mn = p.q_mn = 1;
+    p.bf16 = q.type == SGEMM_TYPE_BF16;
+    p.out = static_cast<char*>(dW) + (size_t)v0 * lddw * elem;
+    p.ldo = lddw;
+    p.out_type = q.type;
+    p.alpha = 1.f;
+    p.chunk = ragged::accumulation_chunk(src, q.type);
+    return p;
+  };
+  auto g_of = [&](void* g, int m) { return Operand{g, elem, T, m, ldg, 0, 1}; };
+
+  // (the first piece is the largest; the others run by its plans. Of where G will
+  // lie only the alignment counts, which any multiple of 256 has)
+  void* somewhere = reinterpret_cast<void*>(256);
+  ragged::Plan plans[3] = {};
+  size_t most = 0, most_counters = 1;
+  for (int i = 0; V > 0 && i < 3; ++i) {
+    if ((i == 1 && dX == nullptr) || (i == 2 && dW == nullptr)) continue;
+    if (i == 0)
+      st = q.f32() ? ragged::plan(src, q.type, gradient(n0, 0, somewhere), q.words(0, n0), x, &plans[i])
+                   : ragged::plan(ragged::kGrad, q.type, gradient(n0, 0, somewhere), x, q.words(0, n0), &plans[i]);
+    else if (i == 1)
+      st = ragged::plan(src, q.type, input(n0, 0, nullptr), q.words(0, n0), g_of(somewhere, n0), &plans[i]);
+    else
+      st = ragged::plan(src, q.type, weight(n0, 0), x, g_of(somewhere, n0), &plans[i]);
+    if (st != SGEMM_OK) return st;
+    most = std::max(most, plans[i].bytes());
+    most_counters = std::max(most_counters, plans[i].counters());
+  }
+  float* base = nullptr;
+  int* status = nullptr;
+  uint32_t* counters = nullptr;
+  const std::unique_lock<std::mutex> lock = library_lock();   // to the last launch
+  st = library_workspace(dev, stream, (ws.used + most) / 4, most_counters, &base, &status, nullptr,
+                         nullptr, &counters);
+  if (st != SGEMM_OK) return st;
+  char* at = reinterpret_cast<char*>(base);
+  float* row_scale = reinterpret_cast<float*>(at + at_scale);
+  float* alpha = reinterpret_cast<float*>(at + at_alpha);
+  void* g = at + at_g;
+  float* acc = sums ? reinterpret_cast<float*>(at + at_sums) : nullptr;
+  char* rest = at + ws.used;
+
+  st = done(start(scale_kernel, 1, kScaleThreads, stream, T, V, q.target, q.ignore, dloss,
+                  q.type == SGEMM_TYPE_F16 ? 16384.f : 1.f, row_scale, alpha));
+  if (st != SGEMM_OK) return st;
+  for (int v0 = 0; v0 < V; v0 += n) {
+    const int m = (int)at_most(n, V - v0);
+    auto with = [&](Params p) {
+      p.status = status;
+      p.counters = counters;
+      return p;
+    };
+    Params p = with(gradient(m, v0, g));
+    const Operand w = q.words(v0, m);
+    if (q.f32()) {
+      st = ragged::launch(plans[0], p, w, x, rest, stream, "linear_ce_grad");
+      if (st != SGEMM_OK) return st;
+      const long long blocks = (m + 4ll * kRowThreads - 1) / (4 * kRowThreads) * T;
+      st = done(start(gradient_kernel, at_most(blocks, sms * 8ll), kRowThreads, stream, T, m,
+                      static_cast<float*>(g), ldg, q.target, v0, lse,
+                      static_cast<const float*>(row_scale)));
+    } else {
+      p.lse = lse;
+      p.row_scale = row_scale;
+      st = ragged::launch(plans[0], p, x, w, rest, stream, "linear_ce_grad");
+    }
+    if (st != SGEMM_OK) return st;
+    if (dX != nullptr) {
+      p = with(input(m, v0, acc));
+      p.alpha_dev = alpha;
+      st = ragged::launch(plans[1], p, w, g_of(g, m), rest, stream, "linear_ce_dx");
+      if (st != SGEMM_OK) return st;
+    }
+    if (dW != nullptr) {
+      p = with(weight(m, v0));
+      p.alpha_dev = alpha;
+      st = ragged::launch(plans[2], p, x, g_of(g, m), rest, stream, "linear_ce_dw");
+      if (st != SGEMM_OK) return st;
+    }
+  }
+  if (sums) {
+    const long long blocks = at_most((H + 4ll * kRowThreads - 1) / (4 * kRowThreads) * T, sms * 8ll);
+    const float* s = acc;
+    st = q.type == SGEMM_TYPE_BF16
+             ? done(start(round_kernel<__nv_bfloat16>, blocks, kRowThreads, stream, T, H, s,
+                          static_cast<__nv_bfloat16*>(dX), (long long)lddx))
+             : done(start(round_kernel<__half>, blocks, kRowThreads, stream, T, H, s,
+                          static_cast<__half*>(dX), (long long)lddx));
+  }
+  return st;
+}
+
+// Rows of zeros.
+int clear(void* p, int rows, int cols, int ld, int elem, cudaStream_t stream) {
+  if (p == nullptr || rows == 0 || cols == 0) return SGEMM_OK;
+  return done(cudaMemset2DAsync(p, (size_t)ld * elem, 0, (size_t)cols * elem, rows, stream));
+}
+
+}  // namespace
+}  // namespace loss
+}  // namespace sgemm_gb300
+
+using namespace sgemm_gb300;
+
+SGEMM_API int sgemm_linear_ce(int type, int T, int V, int H, const void* X, int ldx, const void* W,
+                              int ldw, const long long* target, long long ignore_index, float* loss,
+                              float* lse, void* stream) {
+  const int st = loss::check(type, T, V, H, X, ldx, W, ldw, target);
+  if (st != SGEMM_OK) return st;
+  if (T == 0) return SGEMM_OK;
+  if (loss == nullptr) return SGEMM_ERR_NULL_PTR;
+  if (loss::odd(loss, 4) || loss::odd(lse, 4)) return SGEMM_ERR_MISALIGNED;
+  const loss::Problem q{type, T, V, H, X, W, ldx, ldw, target, ignore_index};
+  return loss::forward(q, loss, lse, static_cast<cudaStream_t>(stream));
+}
+
+SGEMM_API int sgemm_linear_ce_grad(int type, int T, int V, int H, const void* X, int ldx,
+                                   const void* W, int ldw, const long long* target,
+                                   long long ignore_index, const float* lse, const float* dloss,
+                                   void* dX, int lddx, void* dW, int lddw, void* stream_) {
+  const int st = loss::check(type, T, V, H, X, ldx, W, ldw, target);
+  if (st != SGEMM_OK) return st;
+  const int least = H > 1 ? H : 1;
+  if ((dX != nullptr && lddx < least) || (dW != nullptr && lddw < least)) return SGEMM_ERR_INVALID_LD;
+  const int elem = type == SGEMM_TYPE_F32 ? 4 : 2;
+  if (loss::odd(dX, elem) || loss::odd(dW, elem) || loss::odd(lse, 4) || loss::odd(dloss, 4))
+    return SGEMM_ERR_MISALIGNED;
+  if (T > 0 && (lse == nullptr || dloss == nullptr)) return SGEMM_ERR_NULL_PTR;
+  if (H == 0 || (dX == nullptr && dW == nullptr)) return SGEMM_OK;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if (T == 0) return loss::clear(dW, V, H, lddw, elem, stream);
+  if (V == 0) return loss::clear(dX, T, H, lddx, elem, stream);
+  const loss::Problem q{type, T, V, H, X, W, ldx, ldw, target, ignore_index};
+  return loss::backward(q, lse, dloss, dX, lddx, dW, lddw, stream);
+}

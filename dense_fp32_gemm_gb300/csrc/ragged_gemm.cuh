@@ -1,5 +1,6 @@
 // ragged_gemm.cuh -- tensor-core products of ragged groups: one kernel behind
-// sgemm_grouped, sgemm_grouped_wgrad and sgemm_i8.
+// sgemm_grouped, sgemm_grouped_wgrad, sgemm_i8 and (one group, an epilogue that
+// reduces or transforms the product) sgemm_linear_ce.
 //
 // Mathematics. A group e owns the token rows [off_e, off_e + n_e). The kernel
 // forms tiles of D[p, q] = sum_k P_e[p, k] Q_e[q, k], where p runs along the
@@ -22,7 +23,10 @@
 //         sm_103a has no integer tensor instruction of this generation. A
 //         product is at most 2^14, so the FP32 sums of 1024 products are
 //         exact integers;
-//   kI8Wide  the same integers, already as F16 in the workspace.
+//   kI8Wide  the same integers, already as F16 in the workspace;
+//   kLse, kGrad  as k16, p = token and q = word of a vocabulary (X is the P side):
+//         a thread has a token's logits, of which kLse keeps the largest and
+//         the sum of exponentials, and kGrad writes the loss's gradient.
 //
 // Accumulation. The tensor core adds into FP32 with truncation, an error that
 // grows with the number of instructions. A tile's sum is therefore cut into
@@ -89,7 +93,7 @@
 namespace sgemm_gb300 {
 namespace ragged {
 
-enum Src : int { k16 = 0, kF32 = 1, kI8 = 2, kI8Wide = 3 };
+enum Src : int { k16 = 0, kF32 = 1, kI8 = 2, kI8Wide = 3, kLse = 4, kGrad = 5 };
 enum OutType : int { kOutF32 = 0, kOutBf16 = 1, kOutF16 = 2 };
 
 constexpr int BP = 128;            // tile height in p (MMA M)
@@ -116,8 +120,16 @@ struct Params {
   long long ldo, stride_o;  // row pitch; pitch between the groups' outputs (wgrad)
   int out_type;
   float alpha, beta;
+  const float* alpha_dev; // rows, wgrad: a factor of alpha on the device; may be null
   const float* scale_p;   // kI8: scales of p and q
   const float* scale_q;
+  // kLse, kGrad: the words are col0 .. col0 + T - 1 of the vocabulary
+  const long long* target;  // a word for each token
+  int col0;
+  float2* stats;          // kLse: (largest logit, sum of exp(logit - it)), [tile of q][half][token]
+  float* at_target;       // kLse: the target's logit
+  const float* lse;       // kGrad: log of the sum of exponentials over the vocabulary
+  const float* row_scale; // kGrad: factor of a token's gradient (0: all of it is 0)
   int chunk;              // values of k per tensor-memory accumulation (a multiple of the slice)
   // when tiles are cut along k: the slices a part has at least, and what a cut
   // costs, in 1/16 slices: once, and for each part of the tile
@@ -493,6 +505,77 @@ __device__ __forceinline__ void from_f32(float* d, float v) { *d = v; }
 __device__ __forceinline__ void from_f32(__nv_bfloat16* d, float v) { *d = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void from_f32(__half* d, float v) { *d = __float2half_rn(v); }
 
+constexpr float kLog2e = 1.44269504f;
+
+// 2^v: the hardware's approximation, off by 2^-22 (relative).
+__device__ __forceinline__ float exp2_fast(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// kLse: a token's logits, some columns at a time. The sum is of exp(logit -
+// most); most is a number whatever the logits are, so columns of -infinity add
+// nothing and a NaN or +infinity among them makes the sum NaN or infinite.
+struct Softmax {
+  float most = -3.402823466e38f, sum = 0.f, at_target = 0.f;
+  template <int N>
+  __device__ __forceinline__ void add(const float (&z)[N], int n, int target) {
+    float m = most;
+    if (n >= N) {
+#pragma unroll
+      for (int c = 0; c < N; ++c) m = fmaxf(m, z[c]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < N; ++c) m = fmaxf(m, c < n ? z[c] : m);
+    }
+    // (differences first: one fused product would round the largest's, too)
+    float s0 = sum * exp2_fast((most - m) * kLog2e), s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+    for (int c = 0; c < N; c += 4) {
+      auto term = [&](int i) { return c + i < n ? exp2_fast((z[c + i] - m) * kLog2e) : 0.f; };
+      s0 += term(0);
+      s1 += term(1);
+      s2 += term(2);
+      s3 += term(3);
+    }
+    most = m;
+    sum = (s0 + s1) + (s2 + s3);
+    if ((unsigned)target < (unsigned)N) {
+#pragma unroll
+      for (int c = 0; c < N; ++c) at_target = c == target ? z[c] : at_target;
+    }
+  }
+};
+
+// kGrad: (exp(logit - lse) - [c == target]) * scale of N neighbouring words of a
+// token, n of them inside, to `out` (16-byte aligned).
+template <int N, typename T>
+__device__ __forceinline__ void write_gradient(T* out, const float (&z)[N], float lse, float scale,
+                                               int target, int n) {
+  static_assert(N % 8 == 0 && sizeof(T) == 2, "pieces of 16 bytes");
+#pragma unroll
+  for (int c0 = 0; c0 < N; c0 += 8) {
+    float g[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float e = exp2_fast((z[c0 + i] - lse) * kLog2e);
+      g[i] = scale == 0.f ? 0.f : (c0 + i == target ? e - 1.f : e) * scale;
+    }
+    if (c0 + 8 <= n) {
+      uint4 v;
+      T* t = reinterpret_cast<T*>(&v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) from_f32(t + i, g[i]);
+      *reinterpret_cast<uint4*>(out + c0) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c0 + i < n) from_f32(out + c0 + i, g[i]);
+    }
+  }
+}
+
 // Part of a thread's column of the tile: `n` valid values (of HC) at pitch ld,
 // `live` when its p is inside the output. A warp writes 32 neighbours at a
 // time. The element type, the full column and beta are decided once for all
@@ -535,7 +618,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
   using List = Walk<G::kSlice, BQ, CL>;
   constexpr int SL = G::kSlice;
   constexpr int RS = G::kRawStages, RB = G::kRawBars, OS = G::kConv ? G::kOpStages : RS;
-  constexpr bool kPair = CL == 2;
+  constexpr bool kPair = CL == 2, kLoss = SRC == kLse || SRC == kGrad;
   // weight gradients (Q stored with k as its slow dimension) take tiles of 64
   // and wider
   constexpr bool kQmn = BQ >= 64;
@@ -905,7 +988,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
       // 4096 x 2048, under sustained power 78 against 84.6 us). Where converters
       // set the pace that gains nothing.
       const uint32_t idesc = tc::idesc_f16(BP * CL, G::kConv ? BQ : w.nn,
-                                           SRC == kF32 || (SRC == k16 && p.bf16), a_mn, b_mn);
+                                           SRC == kF32 || (!G::kInt && p.bf16), a_mn, b_mn);
       int early_s = 0, after_s = 0;
       uint32_t early_phase = 0, after_phase = 0;
       for (int k0 = kb; k0 < ke && ok; k0 += chunk, ++acc) {
@@ -1040,12 +1123,39 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
       const int nq = w.nq - half * HC;                 // valid columns of this warp (may be <= 0)
       const int pp = w.p0 + rank * BP + pr;
       const bool live = pp < p.P;
-      const float sp = !G::kInt ? p.alpha : (live ? p.scale_p[pp] : 0.f);
+      const float sp = G::kInt ? (live ? p.scale_p[pp] : 0.f)
+                               : (p.alpha_dev == nullptr ? p.alpha : p.alpha * __ldg(p.alpha_dev));
       const long long row = (long long)(p.wgrad ? 0 : w.row0) + w.q0 + half * HC;
       const long long at = (p.wgrad ? (long long)w.e * p.stride_o : 0ll) + row * p.ldo + pp;
-      // writes the sums of N columns from column c0 on
+      // kLse, kGrad: the target's column among this warp's (any other value: not there)
+      int target = -1;
+      float lse = 0.f, row_scale = 0.f;
+      Softmax softmax;
+      if (kLoss && live) {
+        const long long rel = p.target[pp] - p.col0 - (w.q0 + half * HC);
+        target = rel >= 0 && rel < min(nq, HC) ? (int)rel : -1;
+        if (SRC == kGrad) {
+          lse = p.lse[pp];
+          row_scale = p.row_scale[pp];
+        }
+      }
+      // writes (kLse: takes in) the sums of N columns from column c0 on
       auto write = [&](const auto& sums, int c0) {
         constexpr int N = sizeof(sums) / sizeof(float);
+        if constexpr (SRC == kLse) {
+          softmax.add(sums, nq - c0, target < 0 ? -1 : target - c0);
+          return;
+        }
+        if constexpr (SRC == kGrad) {
+          const long long a = (long long)pp * p.ldo + w.q0 + half * HC + c0;
+          const int t = target < 0 ? -1 : target - c0;
+          if (!live) return;
+          if (p.bf16)
+            write_gradient<N>(static_cast<__nv_bfloat16*>(p.out) + a, sums, lse, row_scale, t, nq - c0);
+          else
+            write_gradient<N>(static_cast<__half*>(p.out) + a, sums, lse, row_scale, t, nq - c0);
+          return;
+        }
         const float* sq = G::kInt ? p.scale_q + row + c0 : nullptr;
         const long long a = at + c0 * p.ldo;
         if (p.out_type == kOutF32)
@@ -1057,6 +1167,12 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
         else
           write_column<G::kInt, N>(static_cast<__half*>(p.out) + a, p.ldo, sums, sp, sq, p.beta,
                                    nq - c0, live);
+      };
+      // once all of this warp's columns are written
+      auto finish = [&] {
+        if (SRC != kLse || !live) return;
+        p.stats[(2ll * (w.q0 / BQ) + half) * p.P + pp] = make_float2(softmax.most, softmax.sum);
+        if (target >= 0) p.at_target[pp] = softmax.at_target;
       };
       // CH columns of the accumulator in use; integers as such, in the same registers
       auto load = [&](int c0, float (&v)[CH]) {
@@ -1123,6 +1239,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
             write(v, c0);
           }
         }
+        if (w.parts <= 1) finish();
         release();
       } else {
         float sum[HC];
@@ -1151,8 +1268,9 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
 #pragma unroll
           for (int c = 0; c < HC; ++c)
             if (c < nq) __stcg(part + c * BP, sum[c]);
-        } else if (nq > 0) {
-          write(sum, 0);
+        } else {
+          if (nq > 0) write(sum, 0);
+          finish();
         }
       }
       if (w.parts > 1) {
@@ -1203,6 +1321,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
           }
           write(sum, c0);
         }
+        finish();
       }
     }
   }

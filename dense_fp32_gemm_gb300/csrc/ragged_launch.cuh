@@ -67,8 +67,25 @@ struct FormEntry {
   cudaError_t (*launch)(int workers, const Params& p, const CUtensorMap& mp, const CUtensorMap& mq,
                         cudaStream_t stream);
 };
-extern const FormEntry kForms16[], kFormsF32[], kFormsI8[];
-extern const int kNumForms16, kNumFormsF32, kNumFormsI8;
+extern const FormEntry kForms16[], kFormsF32[], kFormsI8[], kFormsLoss[];
+extern const int kNumForms16, kNumFormsF32, kNumFormsI8, kNumFormsLoss;
+
+// A call of the kernel, decided but not launched (grouped.cu): its form, and
+// what it takes of the workspace, in bytes.
+struct Plan {
+  int dev, sms, src, type;
+  const FormEntry* form;
+  int workers, slice;
+  size_t pack_p, pack_q, partial;
+  size_t bytes() const { return pack_p + pack_q + partial; }
+  size_t counters() const { return (size_t)workers * form->form.cl; }
+};
+int plan(int src, int type, const Params& p, const Operand& op_p, const Operand& op_q, Plan* out);
+// Launches it with its part of the workspace at `at` (256-byte aligned) and the
+// workspace's status and counters in `p`. The library's lock is held.
+int launch(const Plan& plan, Params p, Operand op_p, Operand op_q, char* at, cudaStream_t stream,
+           const char* what);
+int accumulation_chunk(int src, int out_type);
 
 template <int SRC, int BQ, int CL>
 struct FormOf {

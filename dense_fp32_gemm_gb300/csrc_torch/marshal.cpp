@@ -39,6 +39,10 @@ struct Functions {
                  int, signed char*, int, float*, void*);
   int (*norm_grad)(int, int, int, const void*, int, const void*, int, const void*, int, const float*,
                    const void*, int, void*, int, void*, void*);
+  int (*ce)(int, int, int, int, const void*, int, const void*, int, const long long*, long long,
+            float*, float*, void*);
+  int (*ce_grad)(int, int, int, int, const void*, int, const void*, int, const long long*, long long,
+                 const float*, const float*, void*, int, void*, int, void*);
 } fn;
 PyObject* g_error = nullptr;   // SgemmError(status, name)
 
@@ -352,11 +356,11 @@ PyObject* tuple_of(O*... objects) {
   return t;
 }
 
-// A matrix of X's shape and type that was given as `name`.
-void like(const at::Tensor& t, const at::Tensor& X, const char* name) {
+// A matrix that was given as `name`: of X's shape and type.
+void like(const at::Tensor& t, const at::Tensor& X, const char* name, const char* of = "X") {
   if (t.scalar_type() != X.scalar_type() || t.dim() != 2 || t.size(0) != X.size(0) ||
       t.size(1) != X.size(1))
-    throw Refusal{std::string(name) + " must have the shape and type of X"};
+    throw Refusal{std::string(name) + " must have the shape and type of " + of};
   type_of(t, name);
   pitch(t, name);
 }
@@ -481,18 +485,18 @@ PyObject* rms_norm_grad(PyObject* const* a) {
                    &rstd = tensor(a[3], "rstd");
   check(H.dim() == 2, "H must be 2-D");
   const int type = type_of(H, "H"), ldh = pitch(H, "H");
-  like(dY, H, "dY");
+  like(dY, H, "dY", "H");
   const int weight_type = weight_of(w, H), M = to_int(H.size(0)), N = to_int(H.size(1));
   vector_of(rstd, M, "rstd must be a contiguous float32 vector with one value a row");
   const bool want_x = a[7] == Py_True, want_w = a[8] == Py_True;
   at::Tensor dH, dX, dw;
   if (!is_none(a[4])) {
     dH = tensor(a[4], "dH");
-    like(dH, H, "dH");
+    like(dH, H, "dH", "H");
   }
   if (want_x && !is_none(a[5])) {
     dX = tensor(a[5], "dX");
-    like(dX, H, "dX");
+    like(dX, H, "dX", "H");
   }
   if (want_w && !is_none(a[6])) {
     dw = tensor(a[6], "dweight");
@@ -516,6 +520,93 @@ PyObject* rms_norm_grad(PyObject* const* a) {
   }
   return tuple_of(want_x ? result(a[5], dX) : Py_NewRef(Py_None),
                   want_w ? result(a[6], dw) : Py_NewRef(Py_None));
+}
+
+// What both calls of the loss share.
+struct Loss {
+  const at::Tensor &X, &W, &target;
+  long long ignore;
+  int type, T, V, H, ldx, ldw;
+  Loss(PyObject* x, PyObject* w, PyObject* words, PyObject* ignored)
+      : X(tensor(x, "X")), W(tensor(w, "W")), target(tensor(words, "target")) {
+    check(X.dim() == 2 && W.dim() == 2 && X.size(1) == W.size(1), "X and W must be 2-D with rows of one length");
+    check(X.scalar_type() == W.scalar_type(), "X and W must have one type");
+    type = type_of(X, "X");
+    type_of(W, "W");
+    ldx = pitch(X, "X");
+    ldw = pitch(W, "W");
+    T = to_int(X.size(0));
+    V = to_int(W.size(0));
+    H = to_int(X.size(1));
+    check(target.scalar_type() == at::kLong && target.dim() == 1 && target.size(0) == T &&
+              target.is_contiguous(), "target must be a contiguous int64 vector with a word for each row of X");
+    ignore = PyLong_AsLongLong(ignored);
+    if (ignore == -1 && PyErr_Occurred()) throw PythonError{};
+  }
+  const long long* words() const { return static_cast<const long long*>(target.data_ptr()); }
+  at::Tensor row_values() const { return at::empty({T}, X.options().dtype(at::kFloat).requires_grad(false)); }
+};
+
+// (X, W, target, ignore_index, loss, lse, stream)
+PyObject* linear_cross_entropy(PyObject* const* a) {
+  const Loss in(a[0], a[1], a[2], a[3]);
+  at::Tensor loss, lse;
+  if (!is_none(a[4])) {
+    loss = tensor(a[4], "loss");
+    vector_of(loss, in.T, "loss must be a contiguous float32 vector with one value a row");
+  }
+  if (!is_none(a[5])) {
+    lse = tensor(a[5], "lse");
+    vector_of(lse, in.T, "lse must be a contiguous float32 vector with one value a row");
+  }
+  {
+    const Launch on(a[6], {&in.X, &in.W, &in.target});
+    if (!loss.defined()) loss = in.row_values();
+    if (!lse.defined()) lse = in.row_values();
+    on.check_device(loss);
+    on.check_device(lse);
+    const int st = fn.ce(in.type, in.T, in.V, in.H, in.X.data_ptr(), in.ldx, in.W.data_ptr(), in.ldw,
+                         in.words(), in.ignore, static_cast<float*>(loss.data_ptr()),
+                         static_cast<float*>(lse.data_ptr()), on.handle());
+    if (st != 0) throw Status{st, "sgemm_linear_ce"};
+  }
+  return tuple_of(result(a[4], loss), result(a[5], lse));
+}
+
+// (X, W, target, lse, dloss, ignore_index, dX, dW, want dX, want dW, stream)
+PyObject* linear_cross_entropy_grad(PyObject* const* a) {
+  const Loss in(a[0], a[1], a[2], a[5]);
+  const at::Tensor &lse = tensor(a[3], "lse"), &dloss = tensor(a[4], "dloss");
+  vector_of(lse, in.T, "lse must be a contiguous float32 vector with one value a row");
+  vector_of(dloss, in.T, "dloss must be a contiguous float32 vector with one value a row");
+  const bool want_x = a[8] == Py_True, want_w = a[9] == Py_True;
+  at::Tensor dX, dW;
+  if (want_x && !is_none(a[6])) {
+    dX = tensor(a[6], "dX");
+    like(dX, in.X, "dX", "X");
+  }
+  if (want_w && !is_none(a[7])) {
+    dW = tensor(a[7], "dW");
+    like(dW, in.W, "dW", "W");
+  }
+  const int least = in.H > 1 ? in.H : 1;
+  {
+    const Launch on(a[10], {&in.X, &in.W, &in.target, &lse, &dloss});
+    const auto options = in.X.options().requires_grad(false);
+    if (want_x && !dX.defined()) dX = at::empty({in.T, in.H}, options);
+    if (want_w && !dW.defined()) dW = at::empty({in.V, in.H}, options);
+    if (want_x) on.check_device(dX);
+    if (want_w) on.check_device(dW);
+    const int st = fn.ce_grad(
+        in.type, in.T, in.V, in.H, in.X.data_ptr(), in.ldx, in.W.data_ptr(), in.ldw, in.words(),
+        in.ignore, static_cast<const float*>(lse.data_ptr()),
+        static_cast<const float*>(dloss.data_ptr()), want_x ? dX.data_ptr() : nullptr,
+        want_x ? pitch(dX, "dX") : least, want_w ? dW.data_ptr() : nullptr,
+        want_w ? pitch(dW, "dW") : least, on.handle());
+    if (st != 0) throw Status{st, "sgemm_linear_ce_grad"};
+  }
+  return tuple_of(want_x ? result(a[6], dX) : Py_NewRef(Py_None),
+                  want_w ? result(a[7], dW) : Py_NewRef(Py_None));
 }
 
 // Holds a list or tuple of the items of any iterable.
@@ -598,7 +689,7 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
 
 // (addresses of the C functions, in the order of Functions, the exception class)
 PyObject* bind(PyObject*, PyObject* args) {
-  constexpr int kFunctions = 8;
+  constexpr int kFunctions = 10;
   PyObject *addresses, *error;
   if (!PyArg_ParseTuple(args, "O!O", &PyTuple_Type, &addresses, &error)) return nullptr;
   if (PyTuple_GET_SIZE(addresses) != kFunctions) {
@@ -618,6 +709,8 @@ PyObject* bind(PyObject*, PyObject* args) {
   fn.norm = reinterpret_cast<decltype(fn.norm)>(p[5]);
   fn.norm_i8 = reinterpret_cast<decltype(fn.norm_i8)>(p[6]);
   fn.norm_grad = reinterpret_cast<decltype(fn.norm_grad)>(p[7]);
+  fn.ce = reinterpret_cast<decltype(fn.ce)>(p[8]);
+  fn.ce_grad = reinterpret_cast<decltype(fn.ce_grad)>(p[9]);
   Py_INCREF(error);
   Py_XDECREF(g_error);
   g_error = error;
@@ -636,6 +729,8 @@ PyMethodDef methods[] = {
     SGEMM_GB300_METHOD(rms_norm, 8),
     SGEMM_GB300_METHOD(rms_norm_i8, 8),
     SGEMM_GB300_METHOD(rms_norm_grad, 10),
+    SGEMM_GB300_METHOD(linear_cross_entropy, 7),
+    SGEMM_GB300_METHOD(linear_cross_entropy_grad, 11),
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -99,3 +99,41 @@ def rms_norm(x, weight, residual=None, eps=1e-6):
         raise ValueError("residual must have the shape of x")
     y, h = _Norm.apply(rows, weight, residual.reshape(rows.shape), eps)
     return y.view(x.shape), h.view(x.shape)
+
+
+class _CrossEntropy(torch.autograd.Function):
+    """binding.linear_cross_entropy's loss of each row."""
+
+    @staticmethod
+    def forward(ctx, x, w, target, ignore_index):
+        loss, lse = binding.linear_cross_entropy(x, w, target, ignore_index=ignore_index)
+        ctx.save_for_backward(x, w, target, lse)
+        ctx.ignore_index = ignore_index
+        return loss
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dloss):
+        x, w, target, lse = ctx.saved_tensors
+        dx, dw = binding.linear_cross_entropy_grad(x, w, target, lse, dloss.contiguous(),
+                                                   ignore_index=ctx.ignore_index,
+                                                   want=ctx.needs_input_grad[:2])
+        return dx, dw, None, None
+
+
+def linear_cross_entropy(x, weight, target, ignore_index=-100, reduction="mean"):
+    """Softmax cross entropy of x @ weight.T with the words `target` (int64, the
+    leading dimensions of x), without keeping the logits. Rows whose target is
+    ignore_index are not counted. reduction: "mean" over the counted rows (0 if
+    there are none), "sum", or "none" (a value a row). Differentiable once in x
+    and weight."""
+    if reduction not in ("mean", "sum", "none"):
+        raise ValueError('reduction must be "mean", "sum" or "none"')
+    if target.shape != x.shape[:-1]:
+        raise ValueError("target must have the leading dimensions of x")
+    loss = _CrossEntropy.apply(x.reshape(-1, x.shape[-1]), weight, target.reshape(-1).contiguous(), ignore_index)
+    if reduction == "none":
+        return loss.view(target.shape)
+    if reduction == "sum":
+        return loss.sum()
+    return loss.sum() / (target != ignore_index).sum().clamp(min=1)

@@ -664,6 +664,42 @@ int sgemm_rms_norm_grad(int M, int N, int type, const void* dY, int lddy, const 
                         const void* weight, int weight_type, const float* rstd, const void* dH,
                         int lddh, void* dX, int lddx, void* dweight, void* stream);
 
+/*
+ * Softmax cross entropy over a vocabulary without keeping the logits. With z[t,
+ * v] = X[t] . W[v], X being T x H and W V x H of `type`, row-major:
+ *   lse[t] = log(sum_v exp(z[t, v])),   loss[t] = lse[t] - z[t, target[t]];
+ * target has T 64-bit integers on the device. loss[t] is 0 where target[t] is
+ * ignore_index, and NaN where it is neither that nor in 0 .. V - 1. lse (may be
+ * NULL) is written for every row. Both are FP32, and so are the logits and the
+ * sums: 16-bit operands are multiplied exactly and leave the tensor cores every
+ * 1024 products, FP32 ones as in sgemm_grouped(). Logits of -infinity have no
+ * share; a NaN or +infinity among a row's makes its loss NaN.
+ * The vocabulary is taken in pieces, so that the workspace stays below 256 MB
+ * beside the products' own (FP32: 512 MB), or the statistics (logits) of 2048
+ * words at a time. Any leading dimensions (>= max(1, H)) and element
+ * alignment; operands whose rows are not multiples of 16 bytes are copied piece
+ * by piece. Workspace, capture, device status and errors as sgemm().
+ */
+int sgemm_linear_ce(int type, int T, int V, int H, const void* X, int ldx, const void* W, int ldw,
+                    const long long* target, long long ignore_index, float* loss, float* lse,
+                    void* stream);
+
+/*
+ * Gradients of sgemm_linear_ce: with dloss[t] the gradient of loss[t] and
+ *   G[t, v] = (exp(z[t, v] - lse[t]) - (v == target[t])) * dloss[t]
+ * (0 where target[t] is ignore_index, NaN where it is no word),
+ *   dX = G W (T x H),   dW = G^T X (V x H), of `type`; either may be NULL.
+ * The logits are formed once more; a piece of G at a time is held in `type`,
+ * scaled by a power of two and max|dloss| so that F16 keeps small ones. Sums are
+ * FP32, rounded once. X must hold numbers in rows that are not counted, too (0
+ * times none is none). dX and dW must not overlap X, W or each other. Workspace:
+ * 512 MB (or 2048 words of G) beside the products' own, and T x H FP32 sums
+ * where G takes several pieces. Errors as sgemm_linear_ce().
+ */
+int sgemm_linear_ce_grad(int type, int T, int V, int H, const void* X, int ldx, const void* W,
+                         int ldw, const long long* target, long long ignore_index, const float* lse,
+                         const float* dloss, void* dX, int lddx, void* dW, int lddw, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -70,3 +70,42 @@ def test_torch_norm_refuses():
         layers.rms_norm(x, w, residual=x[:3])
     with pytest.raises(TypeError):
         B.rms_norm(x, w, eps="small")
+
+
+CE = dict(type=BF16, T=4, V=10, H=16, X=256, ldx=16, W=256, ldw=16, target=256, ignore_index=-100)
+CE_CASES = [
+    (dict(type=3), VALUE), (dict(T=-1), DIM), (dict(V=-1), DIM), (dict(H=-1), DIM), (dict(ldx=15), LD),
+    (dict(ldw=15), LD), (dict(X=None), NULL), (dict(W=None), NULL), (dict(target=None), NULL), (dict(X=257), ALIGN),
+    (dict(W=257), ALIGN), (dict(type=F32, X=258), ALIGN), (dict(target=260), ALIGN)]
+
+
+@pytest.mark.parametrize("kw,want", CE_CASES + [
+    (dict(loss=None), NULL), (dict(loss=258), ALIGN), (dict(lse=258), ALIGN), (dict(T=0, target=None), OK)])
+def test_linear_ce(kw, want):
+    assert B.sgemm_linear_ce(**(dict(CE, loss=256, lse=256) | kw)) == want
+
+
+@pytest.mark.parametrize("kw,want", CE_CASES + [
+    (dict(lse=None), NULL), (dict(dloss=None), NULL), (dict(lddx=15), LD), (dict(lddw=15), LD), (dict(lse=258), ALIGN),
+    (dict(dloss=258), ALIGN), (dict(dX=257), ALIGN), (dict(dW=257), ALIGN), (dict(dX=None, dW=None), OK),
+    (dict(H=0), OK)])
+def test_linear_ce_grad(kw, want):
+    a = dict(CE, lse=256, dloss=256, dX=256, lddx=16, dW=256, lddw=16)
+    assert B.sgemm_linear_ce_grad(**(a | kw)) == want
+
+
+def test_torch_loss_refuses():
+    x, w, t, s = torch.zeros(4, 8), torch.zeros(6, 8), torch.zeros(4, dtype=torch.int64), torch.zeros(4)
+    wide = torch.zeros(1, 8).expand(4, 8)
+    for args, kw in [((x, w, t), {}),                                      # not on a GPU
+                     ((x[0], w, t), {}), ((x, w[:, :7], t), {}), ((x, w.half(), t), {}), ((x.double(), w.double(), t), {}),
+                     ((x, w, t[:3]), {}), ((x, w, t.int()), {}), ((x, w, t[:, None]), {}), ((wide, w, t), {}),
+                     ((x, w.t(), t), {}), ((x, w, t), dict(loss=s[:3])), ((x, w, t), dict(lse=s.double()))]:
+        with pytest.raises(ValueError):
+            B.linear_cross_entropy(*args, **kw)
+    for args, kw in [((x, w, t, s, s), {}), ((x, w, t, s[:3], s), {}), ((x, w, t, s, s.double()), {}),
+                     ((x, w, t, s, s), dict(dX=w)), ((x, w, t, s, s), dict(dW=x)), ((x, w, t, s, s), dict(dX=wide))]:
+        with pytest.raises(ValueError):
+            B.linear_cross_entropy_grad(*args, **kw)
+    with pytest.raises(TypeError):
+        B.linear_cross_entropy(x, w, t, ignore_index=None)
