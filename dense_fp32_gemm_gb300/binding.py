@@ -111,6 +111,9 @@ def lib() -> ctypes.CDLL:
                 "sgemm_rms_norm_grad": (I, [I, I, I, P, I, P, I, P, I, P, P, I, P, I, P, P]),
                 "sgemm_linear_ce": (I, [I, I, I, I, P, I, P, I, P, LL, P, P, P]),
                 "sgemm_linear_ce_grad": (I, [I, I, I, I, P, I, P, I, P, LL, P, P, P, I, P, I, P]),
+                "sgemm_mx4_quantize": (I, [I, I, I, P, I, P, I, P, P]),
+                "sgemm_mx4_dequantize": (I, [I, I, P, I, P, I, P, I, P]),
+                "sgemm_mx4": (I, [I, I, I, P, I, P, P, I, P, I, P, I, P]),
                 "sgemm_strided_batched": (I, [I, I, I, I, I, F, P, I, LL, P, I, LL, F, P, I, LL,
                                               I, P]),
             }
@@ -448,6 +451,24 @@ def sgemm_linear_ce_grad(type, T, V, H, X, ldx, W, ldw, target, ignore_index, ls
                                       dX, lddx, dW, lddw, stream)
 
 
+# ---- 4-bit floating point in blocks of 32 with a power of two each ------------------
+def sgemm_mx4_quantize(M, K, type, X, ldx, Q, ldq, scale, stream=None) -> int:
+    """Rows of X to 4-bit codes Q (16 bytes for every 32 values) and the blocks'
+    powers in tiles of 128 rows x 4 blocks. Returns the status code."""
+    return lib().sgemm_mx4_quantize(M, K, type, X, ldx, Q, ldq, scale, stream)
+
+
+def sgemm_mx4_dequantize(M, K, Q, ldq, scale, type, X, ldx, stream=None) -> int:
+    """The values that Q and scale stand for. Returns the status code."""
+    return lib().sgemm_mx4_dequantize(M, K, Q, ldq, scale, type, X, ldx, stream)
+
+
+def sgemm_mx4(M, N, K, A, lda, scaleA, B, ldb, scaleB, out_type, C, ldc, stream=None) -> int:
+    """C = A B^T on 4-bit codes with their blocks' powers (B is N x K). Returns the
+    status code."""
+    return lib().sgemm_mx4(M, N, K, A, lda, scaleA, B, ldb, scaleB, out_type, C, ldc, stream)
+
+
 # ---- torch conveniences (marshalling only) ------------------------------------------
 def _stream_handle(stream):
     import torch
@@ -507,7 +528,7 @@ def _native():
     loader.exec_module(module)
     names = ("sgemm_grouped", "sgemm_grouped_wgrad", "sgemm_i8_quantize", "sgemm_i8", "sgemm_grad_clip",
              "sgemm_rms_norm", "sgemm_rms_norm_i8", "sgemm_rms_norm_grad", "sgemm_linear_ce",
-             "sgemm_linear_ce_grad")
+             "sgemm_linear_ce_grad", "sgemm_mx4_quantize", "sgemm_mx4_dequantize", "sgemm_mx4")
     module.bind(tuple(ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in names), SgemmError)
     return module
 
@@ -586,3 +607,36 @@ def linear_cross_entropy_grad(X, W, target, lse, dloss, ignore_index=-100, dX=No
     row's loss (float32). What is not wanted is None."""
     return _native().linear_cross_entropy_grad(X, W, target, lse, dloss, ignore_index, dX, dW,
                                                bool(want[0]), bool(want[1]), stream)
+
+
+def mx4_quantize(X, Q=None, scale=None, stream=None):
+    """(Q, scale): the rows of X as 4-bit floating point (E2M1) in blocks of 32
+    values with a power of two each. Q is uint8, (rows, 16 * blocks), the first
+    of two values in a byte's low half; scale is uint8, the biased powers in the
+    tiles that mx4_gemm reads (see mx4_tile_scales)."""
+    return _native().mx4_quantize(X, Q, scale, stream)
+
+
+def mx4_dequantize(Q, scale, K, X=None, out_dtype=None, stream=None):
+    """The (rows, K) values that Q and scale stand for, as out_dtype (default
+    bfloat16)."""
+    return _native().mx4_dequantize(Q, scale, K, X, out_dtype, stream)
+
+
+def mx4_gemm(A, scaleA, B, scaleB, C=None, out_dtype=None, stream=None):
+    """C = A @ B.T on the 4-bit values of A (M rows) and B (N rows), added up in
+    FP32. Without C a new tensor of out_dtype (default bfloat16) is returned."""
+    return _native().mx4_gemm(A, scaleA, B, scaleB, C, out_dtype, stream)
+
+
+def mx4_tile_scales(scales):
+    """Biased powers of two, uint8 (rows, blocks), as the vector that mx4_gemm
+    reads: tiles of 128 rows x 4 blocks of 512 bytes, row of tiles after row of
+    tiles; in a tile row r and block b stand at (r % 32) * 16 + (r // 32) * 4 + b.
+    Places that belong to no block are 0."""
+    import torch
+    if scales.dim() != 2 or scales.dtype != torch.uint8:
+        raise ValueError("scales must be a 2-D uint8 tensor")
+    rows, blocks = scales.shape
+    tiles = torch.nn.functional.pad(scales, (0, -blocks % 4, 0, -rows % 128))
+    return tiles.view((rows + 127) // 128, 4, 32, (blocks + 3) // 4, 4).permute(0, 3, 2, 1, 4).reshape(-1)

@@ -364,6 +364,11 @@ bool widen_first(const Params& p, int sms, double tiles_ns, double copied, doubl
 
 }  // namespace
 
+void forced_tile(int* width, int* ctas) {
+  *width = g_width.load();
+  *ctas = g_ctas.load();
+}
+
 int plan(int src, int type, const Params& p, const Operand& op_p, const Operand& op_q, Plan* out) {
   Plan r = {};
   if (cudaGetDevice(&r.dev) != cudaSuccess) {

@@ -1,0 +1,693 @@
+// mx4_gemm.cu -- sgemm_mx4: the product of two matrices of 4-bit floating point
+// with a power of two for every 32 values of k, on the block-scaled tensor-core
+// instruction (tcgen05.mma kind::mxf4).
+//
+// Mathematics: C[m, n] = sum_k A[m, k] B[n, k] 2^(sA[m, k / 32] + sB[n, k / 32] -
+// 254). A product of two codes and its powers is exact; the tensor core adds them
+// up in FP32.
+//
+// The 128 lanes of the instruction are output features (rows of B: P below), its
+// columns are tokens (rows of A: Q), so a few tokens cost a narrow tile while the
+// weights stream through full ones. A slice is 256 values of k, 128 bytes a row,
+// four instructions. Its scales arrive by TMA beside the codes, as the 512-byte
+// tiles of 128 rows x 4 blocks that they are stored in, and are copied to tensor
+// memory by tcgen05.cp in the stream of the MMAs.
+//
+// Tensor memory of a 256-wide tile: two accumulators do not fit beside the
+// scales, so the second starts 64 columns before the first one's end. The
+// epilogue reads the shared columns of a full accumulator first, and the next
+// tile's MMAs start as soon as it has.
+//
+// Roles: warp 0 issues the loads, warp 1 the scales' copies and the MMAs, warps
+// 4-11 read the accumulators (two warps a lane quarter, each half of the columns)
+// and write. CL = 2: pairs of CTAs on vertically adjacent tiles, whose even CTA
+// issues M = 256 MMAs over both; each holds its 128 rows of P, half of Q's rows
+// and all of Q's scales.
+//
+// Schedule: whole tiles in turn; where there are fewer tiles than workers each is
+// cut into `split` ranges of k, whose last worker to arrive adds the parts in the
+// order of k (no CTA waits for another).
+//
+// Every wait is bounded; a CTA that gives up drains its copies and MMAs, frees
+// its tensor memory and returns.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <algorithm>
+#include <atomic>
+#include <cstdio>
+#include <mutex>
+
+#include "../../include/sgemm_gb300.h"
+#include "ragged_launch.cuh"
+
+#define SGEMM_API extern "C" __attribute__((visibility("default")))
+
+namespace sgemm_gb300 {
+namespace mx4 {
+namespace {
+
+constexpr int BP = 128;                    // rows of P in a CTA
+constexpr int kSliceK = 256, kRow = 128;   // values of k in a slice, their bytes
+constexpr int kEpiWarp0 = 4, kEpiWarps = 8, kThreads = (kEpiWarp0 + kEpiWarps) * 32;
+constexpr uint32_t kAll = 0xffffffffu;
+
+struct Params {
+  int P, Q, K;              // features, tokens, values of k
+  int split;                // ranges of k that a tile is cut into
+  int chunk;                // slices of one accumulation
+  void* out;
+  long long ldo;
+  int out_type;
+  float* partials;          // a tile for each unit: BQ columns of CL * BP
+  uint32_t* counters;       // arrivals at a tile, zero unless status is set
+  int* status;
+  long long timeout_ns;
+};
+
+template <int BQ, int CL>
+struct Geo {
+  static constexpr int kRowsQ = BQ / CL;                       // rows of Q in a CTA
+  static constexpr int kTilesQ = (BQ + 127) / 128;             // scale tiles of Q
+  static constexpr int kP = BP * kRow, kQ = kRowsQ * kRow;
+  static constexpr int kScaleP = 1024, kScaleQ = 1024 * kTilesQ;   // two blocks of 4 each
+  static constexpr int kStage = kP + kQ + kScaleP + kScaleQ;
+  static constexpr int kRegion = 208 * 1024;
+  static constexpr int kFit = kRegion / kStage;
+  static constexpr int kStages = kFit < 10 ? kFit : 10;
+  static_assert(kStage % 1024 == 0 && kStages >= 3, "stages");
+  // columns of a slice's scales, and where things lie in tensor memory
+  static constexpr int kCols = 8 + 8 * kTilesQ;
+  static constexpr bool kShare = BQ == 256;                    // accumulators share columns
+  static constexpr int kShared = kShare ? 64 : 0;
+  static constexpr int kSecond = BQ - kShared;                 // the second accumulator
+  static constexpr int kScales = 2 * BQ - kShared;             // two slices' scales
+  static constexpr int kUsed = kScales + 2 * kCols;
+  static constexpr int kTmem = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+  static_assert(kUsed <= 512, "tensor memory");
+};
+
+struct Shared {
+  uint64_t full[10], empty[10];
+  uint64_t acc_full[2], acc_empty[2], acc_part[2];
+  uint64_t drain, epi_sync;
+  uint32_t tmem;
+  int abort, last, split;
+};
+constexpr int kSmem = 1024 + 208 * 1024 + 512;
+static_assert(sizeof(Shared) <= 512 && kSmem <= 227 * 1024, "shared memory");
+
+using ragged::cdiv;
+using ragged::wait_for;
+using ragged::wait_for_pair;
+
+// A part of a worker's list: slices kb .. ke of the tile (p0, q0).
+struct Unit {
+  int tile, part, p0, q0, nq, nn, kb, ke;
+};
+
+template <int BQ, int CL>
+__global__ void __launch_bounds__(kThreads, 1)
+    mx4_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap map_p,
+               const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_sp,
+               const __grid_constant__ CUtensorMap map_sq) {
+  using G = Geo<BQ, CL>;
+  constexpr bool kPair = CL == 2;
+  constexpr int S = G::kStages;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw_addr = ptx::smem_addr(smem_raw);
+  unsigned char* base = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  const uint32_t base_addr = ptx::smem_addr(base);
+  Shared* sh = reinterpret_cast<Shared*>(base + G::kRegion);
+  volatile int* abort_w = &sh->abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = kPair ? (int)ptx::cluster_ctarank() : 0;
+  const int worker = (int)blockIdx.x / CL, workers = (int)gridDim.x / CL;
+
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      ptx::mbar_init(ptx::smem_addr(&sh->full[s]), 1);
+      ptx::mbar_init(ptx::smem_addr(&sh->empty[s]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(ptx::smem_addr(&sh->acc_full[i]), 1);
+      ptx::mbar_init(ptx::smem_addr(&sh->acc_empty[i]), CL * kEpiWarps);
+      ptx::mbar_init(ptx::smem_addr(&sh->acc_part[i]), CL * kEpiWarps / 2);
+    }
+    ptx::mbar_init(ptx::smem_addr(&sh->drain), 1);
+    ptx::mbar_init(ptx::smem_addr(&sh->epi_sync), kEpiWarps * 32);
+    sh->abort = 0;
+    ptx::mbar_fence_init();
+    ptx::tma_prefetch_desc(&map_p);
+    ptx::tma_prefetch_desc(&map_q);
+    ptx::tma_prefetch_desc(&map_sp);
+    ptx::tma_prefetch_desc(&map_sq);
+  }
+  if (warp == 1) {
+    tc::tmem_alloc<CL>(ptx::smem_addr(&sh->tmem), G::kTmem);
+    tc::tmem_relinquish<CL>();
+  }
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  // A launch before this one that gave up may have left arrivals counted, until
+  // its status is polled: then no tile is cut.
+  if (tid == 0) sh->split = *const_cast<const volatile int*>(p.status) != 0 ? 1 : p.split;
+  tc::fence_before_sync();
+  __syncthreads();
+  if (kPair) ptx::cluster_sync();
+  tc::fence_after_sync();
+  const uint32_t tmem = sh->tmem;
+  if (kPair) {
+    if (tid == 0) {
+      const uint32_t peer =
+          ptx::ld_shared_cluster(ptx::mapa(ptx::smem_addr(&sh->tmem), (uint32_t)(rank ^ 1)));
+      // (the two read the status one after another: a pair takes one's word)
+      const uint32_t cut =
+          ptx::ld_shared_cluster(ptx::mapa(ptx::smem_addr(&sh->split), 0u));
+      if (peer != tmem) {
+        *abort_w = 1;
+        atomicCAS(p.status, 0, (int)kDevTmemMismatch);
+      }
+      sh->last = (int)cut;
+    }
+    __syncthreads();
+  }
+  const int split = kPair ? sh->last : sh->split;
+  __syncthreads();          // `last` is the epilogue's from here on
+  const int slices = cdiv(p.K, kSliceK), tiles_q = cdiv(p.Q, BQ);
+  const int units = cdiv(p.P, BP * CL) * tiles_q * split;
+  auto unit = [&](int i) {
+    Unit u;
+    u.tile = i / split;
+    u.part = i - u.tile * split;
+    const int tp = u.tile / tiles_q;      // q fastest: workers running together share weight tiles
+    u.p0 = tp * (BP * CL);
+    u.q0 = (u.tile - tp * tiles_q) * BQ;
+    u.nq = min(BQ, p.Q - u.q0);
+    u.nn = min(BQ, cdiv(u.nq, 16 * CL) * (16 * CL));
+    u.kb = (int)((long long)slices * u.part / split);
+    u.ke = (int)((long long)slices * (u.part + 1) / split);
+    return u;
+  };
+
+  bool issued_any = false;
+  if (warp == 0) {
+    // ---- loads, one thread -------------------------------------------------------
+    if (ptx::elect_one()) {
+      int it = 0;
+      bool ok = true;
+      for (int i = worker; ok && i < units; i += workers) {
+        const Unit u = unit(i);
+        const int p0 = u.p0 + rank * BP, q0 = u.q0 + rank * (u.nn / CL);
+        for (int ks = u.kb; ks < u.ke; ++ks, ++it) {
+          const int s = it % S;
+          ok = wait_for(ptx::smem_addr(&sh->empty[s]), (uint32_t)((it / S) & 1) ^ 1u, abort_w,
+                        p.status, kDevTimeoutEmpty, p.timeout_ns);
+          if (!ok) break;
+          // pair: the even CTA's barrier counts the bytes of both
+          uint32_t fb = ptx::smem_addr(&sh->full[s]);
+          const uint32_t st = base_addr + (uint32_t)(s * G::kStage);
+          if (kPair && rank != 0)
+            fb = ptx::mapa(fb, 0u);
+          else
+            ptx::mbar_arrive_expect_tx(fb, (uint32_t)(CL * G::kStage));
+          auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y) {
+            if (kPair)
+              ptx::tma_load_3d_pair(dst, map, x, y, 0, fb);
+            else
+              ptx::tma_load_3d(dst, map, x, y, 0, fb);
+          };
+          load(st, &map_p, ks * kRow, p0);
+          load(st + G::kP, &map_q, ks * kRow, q0);
+          load(st + G::kP + G::kQ, &map_sp, ks * 256, p0 >> 7);
+          load(st + G::kP + G::kQ + G::kScaleP, &map_sq, ks * 256, u.q0 >> 7);
+        }
+      }
+      // nothing may land after the CTA is gone (the odd CTA's loads signal the
+      // even one's barriers: they have landed once its MMAs have read them)
+      const uint64_t t0 = ptx::global_ns();
+      if (!kPair || rank == 0) {
+        for (int j = it - 1; j >= 0 && j >= it - S; --j)
+          while (!ptx::mbar_try_wait(ptx::smem_addr(&sh->full[j % S]), (uint32_t)((j / S) & 1)))
+            if ((long long)(ptx::global_ns() - t0) > cleanup_bound_ns(p.timeout_ns)) break;
+      }
+      if (kPair) {
+        for (int j = it; j < it + S; ++j)
+          while (!ptx::mbar_try_wait(ptx::smem_addr(&sh->empty[j % S]), (uint32_t)((j / S) & 1) ^ 1u))
+            if ((long long)(ptx::global_ns() - t0) > cleanup_bound_ns(p.timeout_ns)) break;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---- scales to tensor memory and MMAs, one thread of the even CTA ---------------
+    if (rank == 0 && ptx::elect_one()) {
+      auto commit = [&](uint64_t* bar) {
+        if (kPair)
+          tc::commit_pair_multicast(ptx::smem_addr(bar), (uint16_t)0x3);
+        else
+          tc::commit(ptx::smem_addr(bar));
+      };
+      auto wait_acc = [&](uint64_t* bar, uint32_t parity) {
+        return kPair ? wait_for_pair(ptx::smem_addr(bar), parity, abort_w, p.status, kDevTimeoutSync,
+                                     p.timeout_ns)
+                     : wait_for(ptx::smem_addr(bar), parity, abort_w, p.status, kDevTimeoutSync,
+                                p.timeout_ns);
+      };
+      const uint64_t a_desc = tc::smem_desc(base_addr, 16, 1024, true);
+      const uint64_t b_desc = tc::smem_desc(base_addr + G::kP, 16, 1024, true);
+      int it = 0, acc = 0;
+      bool ok = true;
+      for (int i = worker; ok && i < units; i += workers) {
+        const Unit u = unit(i);
+        const uint32_t idesc[2] = {tc::idesc_mx4(BP * CL, u.nn, 0), tc::idesc_mx4(BP * CL, u.nn, 2)};
+        for (int k0 = u.kb; k0 < u.ke && ok; k0 += p.chunk, ++acc) {
+          const int buf = acc & 1;
+          ok = wait_acc(&sh->acc_empty[buf], (uint32_t)((acc >> 1) & 1) ^ 1u);
+          if (ok && G::kShare && acc > 0)
+            ok = wait_acc(&sh->acc_part[buf ^ 1], (uint32_t)(((acc - 1) >> 1) & 1));
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint32_t d = tmem + (uint32_t)(buf * G::kSecond);
+          const int k1 = min(u.ke, k0 + p.chunk);
+          for (int ks = k0; ks < k1; ++ks, ++it) {
+            const int s = it % S;
+            ok = wait_for(ptx::smem_addr(&sh->full[s]), (uint32_t)((it / S) & 1), abort_w, p.status,
+                          kDevTimeoutFull, p.timeout_ns);
+            // the MMAs that read this slot of scales, two slices ago, have completed
+            if (ok && it >= 2)
+              ok = wait_for(ptx::smem_addr(&sh->empty[(it - 2) % S]), (uint32_t)(((it - 2) / S) & 1),
+                            abort_w, p.status, kDevTimeoutEmpty, p.timeout_ns);
+            if (!ok) break;
+            tc::fence_after_sync();
+            const uint32_t st = (uint32_t)(s * G::kStage);
+            const uint32_t scales = base_addr + st + G::kP + G::kQ;
+            const uint32_t sp = tmem + (uint32_t)(G::kScales + (it & 1) * G::kCols), sq = sp + 8;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              tc::copy_scales<CL>(sp + h * 4, scales + h * 512);
+#pragma unroll
+              for (int t = 0; t < G::kTilesQ; ++t)
+                tc::copy_scales<CL>(sq + (h * G::kTilesQ + t) * 4,
+                                    scales + G::kScaleP + t * 1024 + h * 512);
+            }
+            const int steps = min(4, cdiv(p.K - ks * kSliceK, 64));
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              if (kk < steps)
+                tc::mma_mx4<CL>(d, a_desc + (st >> 4) + kk * 2, b_desc + (st >> 4) + kk * 2,
+                                idesc[kk & 1], sp + (kk >> 1) * 4, sq + (kk >> 1) * (G::kTilesQ * 4),
+                                ks > k0 || kk > 0 ? 1u : 0u);
+            commit(&sh->empty[s]);
+            issued_any = true;
+          }
+          if (!ok) break;
+          commit(&sh->acc_full[buf]);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp >= kEpiWarp0) {
+    // ---- epilogue ------------------------------------------------------------------
+    constexpr int HC = BQ / 2, CH = HC < 32 ? HC : 32;
+    const int quarter = warp & 3, half = (warp - kEpiWarp0) >> 2;
+    const int pr = quarter * 32 + lane;
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    // the tile's column of this warp's c-th, c a multiple of CH: where
+    // accumulators share columns those come first
+    auto column = [&](int c) { return half * HC + (G::kShare && half != 0 ? (c + HC / 2) % HC : c); };
+    uint32_t sync_phase = 0;
+    auto epi_sync = [&]() -> bool {
+      ptx::mbar_arrive(ptx::smem_addr(&sh->epi_sync));
+      const bool ok = wait_for(ptx::smem_addr(&sh->epi_sync), sync_phase, abort_w, p.status,
+                               kDevTimeoutSync, p.timeout_ns);
+      sync_phase ^= 1u;
+      return __all_sync(kAll, ok);
+    };
+    auto arrive = [&](uint64_t* bar) {
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (kPair && rank != 0)
+          ptx::mbar_arrive_remote(ptx::mapa(ptx::smem_addr(bar), 0u));
+        else
+          ptx::mbar_arrive(ptx::smem_addr(bar));
+      }
+    };
+    int acc = 0;
+    bool ok = true;
+    for (int i = worker; ok && i < units; i += workers) {
+      const Unit u = unit(i);
+      const int pp = u.p0 + rank * BP + pr;
+      const bool live = pp < p.P;
+      auto write = [&](const float (&v)[CH], int c) {
+        const int n = u.nq - c;                        // valid columns from the tile's c-th on
+        const long long at = (long long)(u.q0 + c) * p.ldo + pp;
+        if (p.out_type == SGEMM_TYPE_F32)
+          ragged::write_column<false, CH>(static_cast<float*>(p.out) + at, p.ldo, v, 1.f, nullptr,
+                                          0.f, n, live);
+        else if (p.out_type == SGEMM_TYPE_BF16)
+          ragged::write_column<false, CH>(static_cast<__nv_bfloat16*>(p.out) + at, p.ldo, v, 1.f,
+                                          nullptr, 0.f, n, live);
+        else
+          ragged::write_column<false, CH>(static_cast<__half*>(p.out) + at, p.ldo, v, 1.f, nullptr,
+                                          0.f, n, live);
+      };
+      auto load = [&](int c, float (&v)[CH]) {
+        uint32_t* r = reinterpret_cast<uint32_t*>(v);
+        const uint32_t src = tmem + lane_base + (uint32_t)((acc & 1) * G::kSecond + column(c));
+        if constexpr (CH == 8) {
+          tc::tmem_ld8(src, *reinterpret_cast<uint32_t(*)[8]>(r));
+        } else {
+#pragma unroll
+          for (int j = 0; j < CH; j += 16)
+            tc::tmem_ld16(src + (uint32_t)j, *reinterpret_cast<uint32_t(*)[16]>(r + j));
+        }
+        tc::tmem_wait_ld();
+      };
+      auto acquire = [&]() -> bool {
+        const bool full = wait_for(ptx::smem_addr(&sh->acc_full[acc & 1]), (uint32_t)((acc >> 1) & 1),
+                                   abort_w, p.status, kDevTimeoutFull, p.timeout_ns);
+        const bool all = __all_sync(kAll, full);
+        tc::fence_after_sync();
+        return all;
+      };
+      // the columns that both accumulators have are read: the second half's first
+      // 64 of the first, the first half's of the second
+      auto shared_read = [&] {
+        if (G::kShare && half == ((acc & 1) ^ 1)) arrive(&sh->acc_part[acc & 1]);
+      };
+      auto release = [&] {
+        arrive(&sh->acc_empty[acc & 1]);
+        ++acc;
+      };
+      float* part = p.partials + ((long long)i * CL + rank) * (BP * BQ) + pr;
+      if (u.ke - u.kb <= p.chunk) {
+        // one accumulation: from tensor memory to its place
+        ok = acquire();
+        if (!ok) break;
+#pragma unroll 1
+        for (int c0 = 0; c0 < HC; c0 += CH) {
+          const int c = column(c0);
+          if (c < u.nq) {
+            float v[CH];
+            load(c0, v);
+            if (split > 1) {
+#pragma unroll
+              for (int j = 0; j < CH; ++j)
+                if (c + j < u.nq) __stcg(part + (c + j) * BP, v[j]);
+            } else {
+              write(v, c);
+            }
+          }
+          if (c0 + CH == HC / 2) shared_read();
+        }
+        release();
+      } else {
+        float sum[HC];
+#pragma unroll
+        for (int c = 0; c < HC; ++c) sum[c] = 0.f;
+        for (int k0 = u.kb; k0 < u.ke; k0 += p.chunk) {
+          ok = acquire();
+          if (!ok) break;
+#pragma unroll
+          for (int c0 = 0; c0 < HC; c0 += CH) {
+            if (column(c0) < u.nq) {                   // (the whole warp)
+              float v[CH];
+              load(c0, v);
+#pragma unroll
+              for (int j = 0; j < CH; ++j) sum[c0 + j] += v[j];
+            }
+            if (c0 + CH == HC / 2) shared_read();
+          }
+          release();
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int c0 = 0; c0 < HC; c0 += CH) {
+          const int c = column(c0);
+          if (c >= u.nq) continue;
+          if (split > 1) {
+#pragma unroll
+            for (int j = 0; j < CH; ++j)
+              if (c + j < u.nq) __stcg(part + (c + j) * BP, sum[c0 + j]);
+          } else {
+            float v[CH];
+#pragma unroll
+            for (int j = 0; j < CH; ++j) v[j] = sum[c0 + j];
+            write(v, c);
+          }
+        }
+      }
+      if (split > 1) {
+        // the last worker to arrive adds the parts in the order of k
+        __threadfence();
+        ok = epi_sync();
+        if (!ok) break;
+        if (warp == kEpiWarp0 && lane == 0) {
+          uint32_t* counter = p.counters + u.tile * CL + rank;
+          const int last = atomicAdd(counter, 1u) == (uint32_t)(split - 1);
+          if (last) *counter = 0u;                     // ready for the next launch
+          __threadfence();
+          sh->last = last;
+        }
+        ok = epi_sync();
+        if (!ok) break;
+        if (!*reinterpret_cast<volatile int*>(&sh->last)) continue;
+        __threadfence();
+        const float* first = p.partials + ((long long)u.tile * split * CL + rank) * (BP * BQ) + pr;
+        constexpr int LP = 32 / CH;                    // parts loaded at a time
+#pragma unroll 1
+        for (int c0 = 0; c0 < HC; c0 += CH) {
+          const int c = column(c0);
+          if (c >= u.nq) continue;
+          float v[CH];
+#pragma unroll
+          for (int j = 0; j < CH; ++j) v[j] = 0.f;
+#pragma unroll 1
+          for (int i0 = 0; i0 < split; i0 += LP) {
+            float x[LP][CH];
+#pragma unroll
+            for (int l = 0; l < LP; ++l)
+#pragma unroll
+              for (int j = 0; j < CH; ++j)
+                x[l][j] = i0 + l < split && c + j < u.nq
+                              ? __ldcg(first + (long long)(i0 + l) * CL * (BP * BQ) + (c + j) * BP)
+                              : 0.f;
+#pragma unroll
+            for (int l = 0; l < LP; ++l)
+#pragma unroll
+              for (int j = 0; j < CH; ++j) v[j] += x[l][j];
+          }
+          write(v, c);
+        }
+      }
+    }
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  // a CTA that gives up waits (bounded) for every MMA it issued
+  if (issued_any && *abort_w != 0) {
+    if (kPair)
+      tc::commit_pair(ptx::smem_addr(&sh->drain));
+    else
+      tc::commit(ptx::smem_addr(&sh->drain));
+    const uint64_t t0 = ptx::global_ns();
+    while (!ptx::mbar_try_wait(ptx::smem_addr(&sh->drain), 0u))
+      if ((long long)(ptx::global_ns() - t0) > cleanup_bound_ns(p.timeout_ns)) break;
+  }
+  __syncwarp();
+  if (kPair) ptx::cluster_sync();
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc<CL>(tmem, G::kTmem);
+  }
+}
+
+// ---- host ---------------------------------------------------------------------------
+struct Form {
+  int bq, cl;
+  const void* kernel;
+};
+#define SGEMM_GB300_MX4(BQ, CL) {BQ, CL, reinterpret_cast<const void*>(&mx4_kernel<BQ, CL>)}
+const Form kForms[] = {SGEMM_GB300_MX4(16, 1),  SGEMM_GB300_MX4(32, 1),  SGEMM_GB300_MX4(64, 1),
+                       SGEMM_GB300_MX4(128, 1), SGEMM_GB300_MX4(256, 1), SGEMM_GB300_MX4(256, 2)};
+constexpr int kNumForms = sizeof(kForms) / sizeof(kForms[0]), kMaxDevices = 64;
+struct Built {
+  bool ready;
+  int workers;
+};
+std::mutex g_mutex;
+Built g_built[kMaxDevices][kNumForms];
+
+cudaLaunchConfig_t config(const Form& f, int workers, cudaLaunchAttribute (&la)[2], cudaStream_t stream) {
+  la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  la[0].val.programmaticStreamSerializationAllowed = 1;
+  la[1].id = cudaLaunchAttributeClusterDimension;
+  la[1].val.clusterDim.x = f.cl;
+  la[1].val.clusterDim.y = 1;
+  la[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)(workers * f.cl));
+  lc.blockDim = dim3(kThreads);
+  lc.dynamicSmemBytes = kSmem;
+  lc.stream = stream;
+  lc.attrs = la;
+  lc.numAttrs = f.cl == 2 ? 2 : 1;
+  return lc;
+}
+
+// Workers of a form that are resident at once (0: it cannot run).
+int workers_of(int dev, int sms, int i) {
+  if (dev < 0 || dev >= kMaxDevices) return 0;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  Built& b = g_built[dev][i];
+  if (b.ready) return b.workers;
+  const Form& f = kForms[i];
+  if (cudaFuncSetAttribute(f.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  b.workers = sms;
+  if (f.cl == 2) {
+    cudaLaunchAttribute la[2];
+    cudaLaunchConfig_t lc = config(f, sms / 2 > 0 ? sms / 2 : 1, la, nullptr);
+    lc.attrs = la + 1;
+    lc.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&b.workers, f.kernel, &lc) != cudaSuccess) {
+      cudaGetLastError();
+      b.workers = 0;
+    }
+  }
+  b.ready = true;
+  return b.workers;
+}
+
+// Maps: codes as bytes, boxes of 128 bytes x rows; scales as 32-bit words, a row
+// of tiles a row, boxes of two tiles x `rows`.
+bool encode(CUtensorMap* map, const void* ptr, bool scales, long long cols, long long rows,
+            long long pitch, int box_rows) {
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, 1};
+  cuuint64_t strides[2] = {(cuuint64_t)pitch, (cuuint64_t)(pitch * rows)};
+  cuuint32_t box[3] = {scales ? 256u : (cuuint32_t)kRow, (cuuint32_t)box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  auto call = [&] {
+    return ragged::tensor_map_encode()(
+               map, scales ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+               const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               scales ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (call()) return true;
+  int dev = 0;   // (a host thread without a context: see ragged::encode_operand)
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && call();
+}
+
+// The tile: as wide as the tokens up to 128, else the pair's.
+int choose(int M, int N) {
+  if (M <= 16) return 0;
+  if (M <= 32) return 1;
+  if (M <= 64) return 2;
+  if (M <= 128) return 3;
+  return 5;
+}
+
+int run(int M, int N, int K, const void* A, int lda, const void* SA, const void* B, int ldb,
+        const void* SB, int out_type, void* C, int ldc, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return SGEMM_ERR_LAUNCH;
+  }
+  int st = library_device_sms(dev, &sms);
+  if (st != SGEMM_OK) return st;
+  if (ragged::tensor_map_encode() == nullptr) return SGEMM_ERR_LAUNCH;
+  int i = choose(M, N), workers = 0;
+  int width = 0, ctas = 0;
+  ragged::forced_tile(&width, &ctas);
+  for (int j = 0; width > 0 && j < kNumForms; ++j)
+    // (a narrow tile has the scales of its first 128 rows only at their start)
+    if (kForms[j].bq == width && kForms[j].cl == ctas && (width >= 128 || M <= width)) i = j;
+  workers = workers_of(dev, sms, i);
+  if (workers == 0 && kForms[i].cl == 2) workers = workers_of(dev, sms, --i);
+  if (workers == 0) return SGEMM_ERR_LAUNCH;
+  const Form& f = kForms[i];
+
+  const long long tiles = (long long)cdiv(N, BP * f.cl) * cdiv(M, f.bq);
+  if (tiles > 0x7fffffffLL / 64) return SGEMM_ERR_INVALID_DIM;
+  const int slices = cdiv(K, kSliceK);
+  Params p = {};
+  p.P = N;
+  p.Q = M;
+  p.K = K;
+  p.split = 1;
+  if (tiles < workers) p.split = (int)std::min<long long>(workers / tiles, std::max(1, slices / 2));
+  p.chunk = out_type == SGEMM_TYPE_F32 ? 8 : 32;
+  p.out = C;
+  p.ldo = ldc;
+  p.out_type = out_type;
+  const size_t partial = p.split > 1 ? (size_t)tiles * p.split * f.cl * BP * f.bq : 1;
+  float* ws = nullptr;
+  const std::unique_lock<std::mutex> lock = library_lock();   // to the launch
+  st = library_workspace(dev, stream, partial, (size_t)workers * f.cl, &ws, &p.status, nullptr,
+                         nullptr, &p.counters);
+  if (st != SGEMM_OK) return st;
+  p.partials = ws;
+  p.timeout_ns = library_wait_timeout_ns();
+
+  const long long blocks = (K + 31ll) / 32, tiles_k = (blocks + 3) / 4;
+  CUtensorMap mp = {}, mq = {}, msp = {}, msq = {};
+  if (!encode(&mp, B, false, blocks * 16, N, ldb, BP) ||
+      !encode(&mq, A, false, blocks * 16, M, lda, f.bq / f.cl) ||
+      !encode(&msp, SB, true, tiles_k * 128, (N + 127ll) / 128, tiles_k * 512, 1) ||
+      !encode(&msq, SA, true, tiles_k * 128, (M + 127ll) / 128, tiles_k * 512, (f.bq + 127) / 128))
+    return SGEMM_ERR_LAUNCH;
+  const int used = (int)std::min<long long>(workers, tiles * p.split);
+  cudaLaunchAttribute la[2];
+  const cudaLaunchConfig_t lc = config(f, used, la, stream);
+  void* args[] = {&p, &mp, &mq, &msp, &msq};
+  if (cudaLaunchKernelExC(&lc, f.kernel, args) != cudaSuccess) {
+    cudaGetLastError();
+    return SGEMM_ERR_LAUNCH;
+  }
+  char text[160];
+  snprintf(text, sizeof(text), "mx4_%dx%dx%d cluster=%d grid=%d split=%d", BP * f.cl, f.bq, kSliceK,
+           f.cl, used * f.cl, p.split);
+  note_last_config(text);
+  return SGEMM_OK;
+}
+
+// K == 0: zeros.
+int clear(int M, int N, int out_type, void* C, int ldc, cudaStream_t stream) {
+  const size_t e = out_type == SGEMM_TYPE_F32 ? 4 : 2;
+  if (cudaMemset2DAsync(C, ldc * e, 0, N * e, M, stream) == cudaSuccess) return SGEMM_OK;
+  cudaGetLastError();
+  return SGEMM_ERR_LAUNCH;
+}
+
+}  // namespace
+}  // namespace mx4
+}  // namespace sgemm_gb300
+
+using namespace sgemm_gb300;
+
+SGEMM_API int sgemm_mx4(int M, int N, int K, const unsigned char* A, int lda,
+                        const unsigned char* scaleA, const unsigned char* B, int ldb,
+                        const unsigned char* scaleB, int out_type, void* C, int ldc, void* stream_) {
+  if (out_type != SGEMM_TYPE_F32 && out_type != SGEMM_TYPE_BF16 && out_type != SGEMM_TYPE_F16)
+    return SGEMM_ERR_INVALID_VALUE;
+  if (M < 0 || N < 0 || K < 0) return SGEMM_ERR_INVALID_DIM;
+  const long long bytes = (K + 31ll) / 32 * 16;
+  if (lda < bytes || ldb < bytes || lda % 16 != 0 || ldb % 16 != 0 || ldc < (N > 1 ? N : 1))
+    return SGEMM_ERR_INVALID_LD;
+  if (M == 0 || N == 0) return SGEMM_OK;
+  if (C == nullptr || (K > 0 && (A == nullptr || B == nullptr || scaleA == nullptr || scaleB == nullptr)))
+    return SGEMM_ERR_NULL_PTR;
+  const uintptr_t in = reinterpret_cast<uintptr_t>(A) | reinterpret_cast<uintptr_t>(B) |
+                       reinterpret_cast<uintptr_t>(scaleA) | reinterpret_cast<uintptr_t>(scaleB);
+  if ((K > 0 && (in & 15u)) ||
+      (reinterpret_cast<uintptr_t>(C) & (out_type == SGEMM_TYPE_F32 ? 3u : 1u)))
+    return SGEMM_ERR_MISALIGNED;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if (K == 0) return mx4::clear(M, N, out_type, C, ldc, stream);
+  return mx4::run(M, N, K, A, lda, scaleA, B, ldb, scaleB, out_type, C, ldc, stream);
+}

@@ -86,6 +86,8 @@ int plan(int src, int type, const Params& p, const Operand& op_p, const Operand&
 int launch(const Plan& plan, Params p, Operand op_p, Operand op_q, char* at, cudaStream_t stream,
            const char* what);
 int accumulation_chunk(int src, int out_type);
+// What sgemm_grouped_set_tile asked for (width 0: nothing).
+void forced_tile(int* width, int* ctas);
 
 template <int SRC, int BQ, int CL>
 struct FormOf {

@@ -259,5 +259,58 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t smem_addr, uint32_t lead_
   return d;
 }
 
+// ---- kind::mxf4: 4-bit floats (E2M1) with a power of two (UE8M0) for every 32 --
+// D (+)= A B over 64 values of K. The scales are in tensor memory: of 128 rows x
+// 4 blocks a tile of 4 columns, row r at lane r % 32 (in all four quarters of
+// the lanes) of column r / 32, a byte for each block; `idesc` says which two
+// bytes this step uses.
+template <int CG>
+__device__ __forceinline__ void mma_mx4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                        uint32_t idesc, uint32_t a_scale, uint32_t b_scale,
+                                        uint32_t accumulate) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(a_scale), "r"(b_scale)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(a_scale), "r"(b_scale)
+        : "memory");
+}
+
+// Instruction descriptor of kind::mxf4, both operands K-major: scale bytes of B
+// (bits 4-5: 0 or 2, the first of the two), A and B format (7-9 and 10-11: 1 =
+// E2M1), N >> 3 (17-22), scale format (23: 1 = UE8M0), M >> 7 (27-28), scale
+// bytes of A (29-30), K of 64 values (31: 0).
+__host__ __device__ constexpr uint32_t idesc_mx4(int M, int N, int scale_byte) {
+  return ((uint32_t)scale_byte << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
+         (1u << 23) | ((uint32_t)(M >> 7) << 27) | ((uint32_t)scale_byte << 29);
+}
+
+// Copies a tile of 32 rows of 16 bytes, one after another in shared memory (512
+// bytes at a 16-byte boundary), to 4 columns of each quarter of tensor memory's
+// lanes; CG = 2: in both CTAs of the pair, from the same offset of each one's
+// shared memory. In order with the MMAs that the same thread issues after it.
+template <int CG>
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t smem_addr) {
+  // no swizzle: groups of 8 rows of 16 bytes, 128 bytes apart
+  const uint64_t desc = (uint64_t)((smem_addr >> 4) & 0x3FFFu) | (uint64_t)(128u >> 4) << 32 |
+                        (uint64_t)1u << 46;
+  if constexpr (CG == 1)
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                 : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                 : "memory");
+}
+
 }  // namespace tc
 }  // namespace sgemm_gb300

@@ -43,6 +43,11 @@ struct Functions {
             float*, float*, void*);
   int (*ce_grad)(int, int, int, int, const void*, int, const void*, int, const long long*, long long,
                  const float*, const float*, void*, int, void*, int, void*);
+  int (*mx4_quantize)(int, int, int, const void*, int, unsigned char*, int, unsigned char*, void*);
+  int (*mx4_dequantize)(int, int, const unsigned char*, int, const unsigned char*, int, void*, int,
+                        void*);
+  int (*mx4)(int, int, int, const unsigned char*, int, const unsigned char*, const unsigned char*, int,
+             const unsigned char*, int, void*, int, void*);
 } fn;
 PyObject* g_error = nullptr;   // SgemmError(status, name)
 
@@ -609,6 +614,125 @@ PyObject* linear_cross_entropy_grad(PyObject* const* a) {
                   want_w ? result(a[7], dW) : Py_NewRef(Py_None));
 }
 
+// A matrix of 4-bit codes: rows of whole blocks of 16 bytes at 16-byte
+// boundaries.
+const at::Tensor& codes_of(const at::Tensor& t, const char* name) {
+  if (t.scalar_type() != at::kByte || t.dim() != 2 || t.size(1) % 16 != 0)
+    throw Refusal{std::string(name) + " must be a 2-D uint8 tensor with 16 bytes for every 32 values"};
+  if (pitch(t, name) % 16 != 0 && t.size(0) > 1 && t.numel() > 0)
+    throw Refusal{std::string(name) + " must have rows at multiples of 16 bytes"};
+  return t;
+}
+int code_pitch(const at::Tensor& t, const char* name) {
+  const int p = pitch(t, name);
+  return t.size(1) == 0 ? 16 : p;       // (a pitch of 1 has no meaning here)
+}
+int64_t scale_bytes(int64_t rows, int64_t blocks) { return (rows + 127) / 128 * ((blocks + 3) / 4) * 512; }
+const unsigned char* scales_of(const at::Tensor& t, int64_t rows, int64_t blocks, const char* name) {
+  if (t.scalar_type() != at::kByte || t.dim() != 1 || !t.is_contiguous() ||
+      t.numel() != scale_bytes(rows, blocks))
+    throw Refusal{std::string(name) + " must be a contiguous uint8 vector with 512 bytes for every 128 rows x 4 blocks"};
+  return static_cast<const unsigned char*>(t.data_ptr());
+}
+
+// (X, Q, scale, stream)
+PyObject* mx4_quantize(PyObject* const* a) {
+  const at::Tensor& X = tensor(a[0], "X");
+  check(X.dim() == 2, "X must be 2-D");
+  const int M = to_int(X.size(0)), K = to_int(X.size(1));
+  const int64_t blocks = ((int64_t)K + 31) / 32;
+  const int type = type_of(X, "X"), ldx = pitch(X, "X");
+  at::Tensor Q, scale;
+  if (!is_none(a[1])) {
+    Q = codes_of(tensor(a[1], "Q"), "Q");
+    check(Q.size(0) == M && Q.size(1) == blocks * 16, "Q must have a row of whole blocks for each of X");
+  }
+  if (!is_none(a[2])) {
+    scale = tensor(a[2], "scale");
+    scales_of(scale, M, blocks, "scale");
+  }
+  {
+    const Launch on(a[3], {&X});
+    const auto options = X.options().dtype(at::kByte).requires_grad(false);
+    if (!Q.defined()) Q = at::empty({M, blocks * 16}, options);
+    if (!scale.defined()) scale = at::empty({scale_bytes(M, blocks)}, options);
+    on.check_device(Q);
+    on.check_device(scale);
+    const int st = fn.mx4_quantize(M, K, type, X.data_ptr(), ldx,
+                                   static_cast<unsigned char*>(Q.data_ptr()), code_pitch(Q, "Q"),
+                                   static_cast<unsigned char*>(scale.data_ptr()), on.handle());
+    if (st != 0) throw Status{st, "sgemm_mx4_quantize"};
+  }
+  return tuple_of(result(a[1], Q), result(a[2], scale));
+}
+
+// (Q, scale, K, X, out_dtype, stream)
+PyObject* mx4_dequantize(PyObject* const* a) {
+  const at::Tensor &Q = codes_of(tensor(a[0], "Q"), "Q"), &scale = tensor(a[1], "scale");
+  const long long k = PyLong_AsLongLong(a[2]);
+  if (k == -1 && PyErr_Occurred()) throw PythonError{};
+  const int M = to_int(Q.size(0)), K = to_int(k);
+  check((k + 31) / 32 * 16 == Q.size(1), "K values are not the blocks of Q");
+  scales_of(scale, M, Q.size(1) / 16, "scale");
+  at::Tensor X;
+  at::ScalarType out = at::kBFloat16;
+  if (is_none(a[3])) {
+    out = dtype_or(a[4], out);
+  } else {
+    X = tensor(a[3], "X");
+    check(X.dim() == 2 && X.size(0) == M && X.size(1) == K, "shape mismatch");
+    pitch(X, "X");
+    type_of(X, "X");
+    out = X.scalar_type();
+  }
+  const int type = type_of(out, "X");
+  {
+    const Launch on(a[5], {&Q, &scale});
+    if (!X.defined()) X = at::empty({M, K}, Q.options().dtype(out).requires_grad(false));
+    on.check_device(X);
+    const int st = fn.mx4_dequantize(M, K, static_cast<const unsigned char*>(Q.data_ptr()),
+                                     code_pitch(Q, "Q"),
+                                     static_cast<const unsigned char*>(scale.data_ptr()), type,
+                                     X.data_ptr(), pitch(X, "X"), on.handle());
+    if (st != 0) throw Status{st, "sgemm_mx4_dequantize"};
+  }
+  return result(a[3], X);
+}
+
+// (A, scaleA, B, scaleB, C, out_dtype, stream)
+PyObject* mx4_gemm(PyObject* const* a) {
+  const at::Tensor &A = codes_of(tensor(a[0], "A"), "A"), &sa = tensor(a[1], "scaleA"),
+                   &B = codes_of(tensor(a[2], "B"), "B"), &sb = tensor(a[3], "scaleB");
+  check(A.size(1) == B.size(1), "shape mismatch");
+  const int64_t blocks = A.size(1) / 16;
+  const int M = to_int(A.size(0)), N = to_int(B.size(0)), K = to_int(blocks * 32);
+  const unsigned char *scale_a = scales_of(sa, M, blocks, "scaleA"),
+                      *scale_b = scales_of(sb, N, blocks, "scaleB");
+  at::Tensor C;
+  at::ScalarType out = at::kBFloat16;
+  if (is_none(a[4])) {
+    out = dtype_or(a[5], out);
+  } else {
+    C = tensor(a[4], "C");
+    check(C.dim() == 2 && C.size(0) == M && C.size(1) == N, "shape mismatch");
+    pitch(C, "C");
+    type_of(C, "C");
+    out = C.scalar_type();
+  }
+  const int out_type = type_of(out, "C");
+  {
+    const Launch on(a[6], {&A, &sa, &B, &sb});
+    if (!C.defined()) C = at::empty({M, N}, A.options().dtype(out).requires_grad(false));
+    on.check_device(C);
+    const int st = fn.mx4(M, N, K, static_cast<const unsigned char*>(A.data_ptr()), code_pitch(A, "A"),
+                          scale_a, static_cast<const unsigned char*>(B.data_ptr()),
+                          code_pitch(B, "B"), scale_b, out_type, C.data_ptr(), pitch(C, "C"),
+                          on.handle());
+    if (st != 0) throw Status{st, "sgemm_mx4"};
+  }
+  return result(a[4], C);
+}
+
 // Holds a list or tuple of the items of any iterable.
 struct Items {
   PyObject* fast;
@@ -689,7 +813,7 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
 
 // (addresses of the C functions, in the order of Functions, the exception class)
 PyObject* bind(PyObject*, PyObject* args) {
-  constexpr int kFunctions = 10;
+  constexpr int kFunctions = 13;
   PyObject *addresses, *error;
   if (!PyArg_ParseTuple(args, "O!O", &PyTuple_Type, &addresses, &error)) return nullptr;
   if (PyTuple_GET_SIZE(addresses) != kFunctions) {
@@ -711,6 +835,9 @@ PyObject* bind(PyObject*, PyObject* args) {
   fn.norm_grad = reinterpret_cast<decltype(fn.norm_grad)>(p[7]);
   fn.ce = reinterpret_cast<decltype(fn.ce)>(p[8]);
   fn.ce_grad = reinterpret_cast<decltype(fn.ce_grad)>(p[9]);
+  fn.mx4_quantize = reinterpret_cast<decltype(fn.mx4_quantize)>(p[10]);
+  fn.mx4_dequantize = reinterpret_cast<decltype(fn.mx4_dequantize)>(p[11]);
+  fn.mx4 = reinterpret_cast<decltype(fn.mx4)>(p[12]);
   Py_INCREF(error);
   Py_XDECREF(g_error);
   g_error = error;
@@ -731,6 +858,9 @@ PyMethodDef methods[] = {
     SGEMM_GB300_METHOD(rms_norm_grad, 10),
     SGEMM_GB300_METHOD(linear_cross_entropy, 7),
     SGEMM_GB300_METHOD(linear_cross_entropy_grad, 11),
+    SGEMM_GB300_METHOD(mx4_quantize, 4),
+    SGEMM_GB300_METHOD(mx4_dequantize, 6),
+    SGEMM_GB300_METHOD(mx4_gemm, 7),
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -582,7 +582,8 @@ int sgemm_i8(int M, int N, int K, const signed char* A, int lda, const float* sc
              void* stream);
 
 /*
- * Tile of later sgemm_grouped, sgemm_grouped_wgrad and sgemm_i8 calls
+ * Tile of later sgemm_grouped, sgemm_grouped_wgrad, sgemm_i8, sgemm_linear_ce and
+ * sgemm_mx4 calls
  * (process-wide; for measurements and tests): `width` token rows (wgrad: rows
  * of C) by 128 output columns on one CTA (ctas = 1), or by 256 on a pair of CTAs
  * that share their MMAs (ctas = 2). width 0 restores the choice by size. A call
@@ -699,6 +700,51 @@ int sgemm_linear_ce(int type, int T, int V, int H, const void* X, int ldx, const
 int sgemm_linear_ce_grad(int type, int T, int V, int H, const void* X, int ldx, const void* W,
                          int ldw, const long long* target, long long ignore_index, const float* lse,
                          const float* dloss, void* dX, int lddx, void* dW, int lddw, void* stream);
+
+/*
+ * Rows of X (M x K, of `type`) to 4-bit floating point (E2M1: 0, 0.5, 1, 1.5, 2,
+ * 3, 4, 6 and their negatives) in blocks of 32 values with a power of two each:
+ * the power is floor(log2(max|x|)) - 2, at least -127, and x / 2^power is rounded
+ * to the nearest of those values, ties to the even code, beyond 6 to 6. All of
+ * this is exact, whatever the order of the work.
+ *
+ * Q has M rows of 16 bytes for each block, ldq bytes apart (a multiple of 16, at
+ * least 16 * ceil(K / 32)): value 2i of a block in the low half of byte i, its
+ * sign in the half's highest bit. Values past the row's end are zeros.
+ *
+ * scale holds power + 127 as a byte for each block, in the order in which the
+ * tensor cores read them: tiles of 128 rows x 4 blocks, 512 bytes each, all of
+ * the first 128 rows' tiles first; in a tile row r and block b stand at (r % 32)
+ * * 16 + (r / 32) * 4 + b. It has 512 * ceil(M / 128) * ceil(ceil(K / 32) / 4)
+ * bytes; places that belong to no block are set to 0. A block of zeros has 0. A
+ * block with an infinity or a NaN has 255, which stands for NaN.
+ *
+ * Q and scale start on 16 bytes; X at any element, with any ldx >= max(1, K).
+ * M == 0 or K == 0 does nothing. Capturable without any call before. Errors as
+ * sgemm().
+ */
+int sgemm_mx4_quantize(int M, int K, int type, const void* X, int ldx, unsigned char* Q, int ldq,
+                       unsigned char* scale, void* stream);
+
+/* The values that Q and scale stand for, rounded to `type`: M x K. Errors as
+ * sgemm_mx4_quantize(). */
+int sgemm_mx4_dequantize(int M, int K, const unsigned char* Q, int ldq, const unsigned char* scale,
+                         int type, void* X, int ldx, void* stream);
+
+/*
+ * C[m, n] = sum_k A[m, k] * B[n, k]: A is M x K and B N x K (a channel per row),
+ * codes and scales as sgemm_mx4_quantize() writes them; C is M x N of out_type.
+ * Products are exact and added up in FP32 on the tensor cores (which truncate;
+ * sums leave them every 8192 values of k, FP32 results every 2048), rounded
+ * once. A scale of 255 makes every sum that its block takes part in NaN. The
+ * scales' places that belong to no block must not be 255. K == 0 gives zeros.
+ * lda and ldb are in bytes (multiples of 16); A, B and the scales start on 16
+ * bytes; C at any element with any ldc >= max(1, N). C must not overlap the
+ * operands. Workspace, capture, device status and errors as sgemm().
+ */
+int sgemm_mx4(int M, int N, int K, const unsigned char* A, int lda, const unsigned char* scaleA,
+              const unsigned char* B, int ldb, const unsigned char* scaleB, int out_type, void* C,
+              int ldc, void* stream);
 
 #ifdef __cplusplus
 }

@@ -109,3 +109,49 @@ def test_torch_loss_refuses():
             B.linear_cross_entropy_grad(*args, **kw)
     with pytest.raises(TypeError):
         B.linear_cross_entropy(x, w, t, ignore_index=None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(type=3), VALUE), (dict(M=-1), DIM), (dict(K=-1), DIM), (dict(ldx=39), LD), (dict(ldq=16), LD),
+    (dict(ldq=40), LD), (dict(X=None), NULL), (dict(Q=None), NULL), (dict(scale=None), NULL), (dict(X=257), ALIGN),
+    (dict(Q=264), ALIGN), (dict(scale=264), ALIGN), (dict(M=0, X=None), OK), (dict(K=0, X=None), OK)])
+def test_mx4_quantize(kw, want):
+    a = dict(M=4, K=40, type=BF16, X=256, ldx=40, Q=256, ldq=32, scale=256) | kw
+    assert B.sgemm_mx4_quantize(**a) == want
+    assert B.sgemm_mx4_dequantize(a["M"], a["K"], a["Q"], a["ldq"], a["scale"], a["type"], a["X"], a["ldx"]) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(out_type=3), VALUE), (dict(M=-1), DIM), (dict(N=-1), DIM), (dict(K=-1), DIM), (dict(lda=16), LD),
+    (dict(ldb=40), LD), (dict(ldc=7), LD), (dict(A=None), NULL), (dict(B=None), NULL), (dict(scaleA=None), NULL),
+    (dict(scaleB=None), NULL), (dict(C=None), NULL), (dict(A=264), ALIGN), (dict(B=264), ALIGN),
+    (dict(scaleA=264), ALIGN), (dict(scaleB=257), ALIGN), (dict(C=257), ALIGN), (dict(out_type=F32, C=258), ALIGN),
+    (dict(M=0, A=None), OK), (dict(N=0, C=None), OK)])
+def test_mx4(kw, want):
+    a = dict(M=4, N=8, K=40, A=256, lda=32, scaleA=256, B=256, ldb=32, scaleB=256, out_type=BF16, C=256, ldc=8)
+    assert B.sgemm_mx4(**(a | kw)) == want
+
+
+def test_torch_mx4_refuses():
+    x = torch.zeros(4, 40)
+    q, s = torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8)
+    for args, kw in [((x,), {}), ((x[0],), {}), ((x.double(),), {}), ((x.t(),), {}), ((x,), dict(Q=q[:, :16])),
+                     ((x,), dict(Q=q.to(torch.int8))), ((x,), dict(scale=s[:256])),
+                     ((torch.zeros(1, 40).expand(4, 40),), {})]:
+        with pytest.raises(ValueError):
+            B.mx4_quantize(*args, **kw)
+    odd = torch.zeros(4, 40, dtype=torch.uint8)[:, :32]
+    for args, kw in [((q, s, 40), {}), ((q, s, 30), {}), ((q, s, 70), {}), ((q, s[:256], 40), {}), ((odd, s, 40), {}),
+                     ((q, s, 40), dict(X=x[:3])), ((q, s, 40), dict(out_dtype=torch.float64))]:
+        with pytest.raises(ValueError):
+            B.mx4_dequantize(*args, **kw)
+    for args, kw in [((q, s, q, s), {}), ((q[:, :16], s, q, s), {}), ((q, s[:256], q, s), {}), ((odd, s, q, s), {}),
+                     ((q, s, q, s), dict(C=x)), ((q, s, q, s), dict(out_dtype=torch.int8)),
+                     ((q.to(torch.int8), s, q, s), {})]:
+        with pytest.raises(ValueError):
+            B.mx4_gemm(*args, **kw)
+    for bad in (s, x):
+        with pytest.raises(ValueError):
+            B.mx4_tile_scales(bad)
+    t = B.mx4_tile_scales(torch.arange(200, dtype=torch.uint8).view(40, 5))
+    assert t.shape == (1024,) and int(t[(33 % 32) * 16 + 4 + 2]) == 33 * 5 + 2 and int(t[512 + 7 * 16]) == 7 * 5 + 4
