@@ -13,10 +13,12 @@
 // tiles of 128 rows x 4 blocks that they are stored in, and are copied to tensor
 // memory by tcgen05.cp in the stream of the MMAs.
 //
-// Tensor memory of a 256-wide tile: two accumulators do not fit beside the
-// scales, so the second starts 64 columns before the first one's end. The
-// epilogue reads the shared columns of a full accumulator first, and the next
-// tile's MMAs start as soon as it has.
+// Tensor memory. Each slice's scales have columns of their own until its MMAs are
+// done: with two slices' worth the issuer waited for MMAs that had just been
+// queued (8192 x 8192 x 8192 264 us, 172 without that wait). Beside them two
+// 256-wide accumulators do not fit, so the second one's first half is the first
+// one's second. The epilogue takes its columns into registers before it writes
+// any, and the next tile's MMAs start once the shared half is read.
 //
 // Roles: warp 0 issues the loads, warp 1 the scales' copies and the MMAs, warps
 // 4-11 read the accumulators (two warps a lane quarter, each half of the columns)
@@ -58,6 +60,7 @@ struct Params {
   void* out;
   long long ldo;
   int out_type;
+  int tma_out;              // C's rows are at multiples of 16 bytes: written by TMA
   float* partials;          // a tile for each unit: BQ columns of CL * BP
   uint32_t* counters;       // arrivals at a tile, zero unless status is set
   int* status;
@@ -71,17 +74,26 @@ struct Geo {
   static constexpr int kP = BP * kRow, kQ = kRowsQ * kRow;
   static constexpr int kScaleP = 1024, kScaleQ = 1024 * kTilesQ;   // two blocks of 4 each
   static constexpr int kStage = kP + kQ + kScaleP + kScaleQ;
-  static constexpr int kRegion = 208 * 1024;
+  // wide tiles: the epilogue's pieces of 32 x 32 on their way out, 4 KB a warp
+  static constexpr bool kStaged = BQ >= 128;
+  static constexpr int kRegion = (kStaged ? 176 : 208) * 1024;
   static constexpr int kFit = kRegion / kStage;
   static constexpr int kStages = kFit < 10 ? kFit : 10;
   static_assert(kStage % 1024 == 0 && kStages >= 3, "stages");
   // columns of a slice's scales, and where things lie in tensor memory
   static constexpr int kCols = 8 + 8 * kTilesQ;
-  static constexpr bool kShare = BQ == 256;                    // accumulators share columns
-  static constexpr int kShared = kShare ? 64 : 0;
-  static constexpr int kSecond = BQ - kShared;                 // the second accumulator
-  static constexpr int kScales = 2 * BQ - kShared;             // two slices' scales
-  static constexpr int kUsed = kScales + 2 * kCols;
+  static constexpr bool kShare = BQ == 256;                    // accumulators share a half
+  static constexpr int kSecond = kShare ? BQ / 2 : BQ;         // the second accumulator
+  static constexpr int kScales = kSecond + BQ;
+  static constexpr int kSlotFit = (512 - kScales) / kCols;
+  static constexpr int kSlots = kSlotFit < kStages ? kSlotFit : kStages;   // slices' scales
+  static constexpr int kUsed = kScales + kSlots * kCols;
+  // A thread of a wide tile's epilogue holds 128 sums: it needs more registers
+  // than the launch gives every thread, so the other warps give some up.
+  static constexpr bool kMoveRegs = BQ == 256;
+  static constexpr int kRegs = 168, kRegsFew = 72, kRegsMany = 216;
+  static_assert(128 * kRegsFew + 256 * kRegsMany <= kThreads * kRegs && kThreads * kRegs <= 65536,
+                "register shares");
   static constexpr int kTmem = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
   static_assert(kUsed <= 512, "tensor memory");
 };
@@ -93,6 +105,7 @@ struct Shared {
   uint32_t tmem;
   int abort, last, split;
 };
+constexpr int kOut = 4096;                 // of a warp
 constexpr int kSmem = 1024 + 208 * 1024 + 512;
 static_assert(sizeof(Shared) <= 512 && kSmem <= 227 * 1024, "shared memory");
 
@@ -109,7 +122,8 @@ template <int BQ, int CL>
 __global__ void __launch_bounds__(kThreads, 1)
     mx4_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap map_p,
                const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_sp,
-               const __grid_constant__ CUtensorMap map_sq) {
+               const __grid_constant__ CUtensorMap map_sq,
+               const __grid_constant__ CUtensorMap map_out) {
   using G = Geo<BQ, CL>;
   constexpr bool kPair = CL == 2;
   constexpr int S = G::kStages;
@@ -117,7 +131,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t raw_addr = ptx::smem_addr(smem_raw);
   unsigned char* base = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   const uint32_t base_addr = ptx::smem_addr(base);
-  Shared* sh = reinterpret_cast<Shared*>(base + G::kRegion);
+  Shared* sh = reinterpret_cast<Shared*>(base + 208 * 1024);
+  static_assert(!G::kStaged || G::kRegion + kEpiWarps * kOut <= 208 * 1024, "staged output");
   volatile int* abort_w = &sh->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = kPair ? (int)ptx::cluster_ctarank() : 0;
@@ -141,6 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tma_prefetch_desc(&map_q);
     ptx::tma_prefetch_desc(&map_sp);
     ptx::tma_prefetch_desc(&map_sq);
+    if (G::kStaged && p.tma_out) ptx::tma_prefetch_desc(&map_out);
   }
   if (warp == 1) {
     tc::tmem_alloc<CL>(ptx::smem_addr(&sh->tmem), G::kTmem);
@@ -190,6 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   bool issued_any = false;
+  if (G::kMoveRegs && warp < kEpiWarp0) ptx::regs_lower<G::kRegsFew>();
   if (warp == 0) {
     // ---- loads, one thread -------------------------------------------------------
     if (ptx::elect_one()) {
@@ -272,15 +289,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int s = it % S;
             ok = wait_for(ptx::smem_addr(&sh->full[s]), (uint32_t)((it / S) & 1), abort_w, p.status,
                           kDevTimeoutFull, p.timeout_ns);
-            // the MMAs that read this slot of scales, two slices ago, have completed
-            if (ok && it >= 2)
-              ok = wait_for(ptx::smem_addr(&sh->empty[(it - 2) % S]), (uint32_t)(((it - 2) / S) & 1),
-                            abort_w, p.status, kDevTimeoutEmpty, p.timeout_ns);
+            // the MMAs that read this slot of scales have completed (with a slot
+            // for every stage they have: the stage has been loaded again)
+            constexpr int kSlots = G::kSlots;
+            if (kSlots < S && ok && it >= kSlots)
+              ok = wait_for(ptx::smem_addr(&sh->empty[(it - kSlots) % S]),
+                            (uint32_t)(((it - kSlots) / S) & 1), abort_w, p.status,
+                            kDevTimeoutEmpty, p.timeout_ns);
             if (!ok) break;
             tc::fence_after_sync();
             const uint32_t st = (uint32_t)(s * G::kStage);
             const uint32_t scales = base_addr + st + G::kP + G::kQ;
-            const uint32_t sp = tmem + (uint32_t)(G::kScales + (it & 1) * G::kCols), sq = sp + 8;
+            const uint32_t sp = tmem + (uint32_t)(G::kScales + it % G::kSlots * G::kCols), sq = sp + 8;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               tc::copy_scales<CL>(sp + h * 4, scales + h * 512);
@@ -307,13 +327,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp >= kEpiWarp0) {
     // ---- epilogue ------------------------------------------------------------------
+    if (G::kMoveRegs) ptx::regs_raise<G::kRegsMany>();
     constexpr int HC = BQ / 2, CH = HC < 32 ? HC : 32;
     const int quarter = warp & 3, half = (warp - kEpiWarp0) >> 2;
     const int pr = quarter * 32 + lane;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    // the tile's column of this warp's c-th, c a multiple of CH: where
-    // accumulators share columns those come first
-    auto column = [&](int c) { return half * HC + (G::kShare && half != 0 ? (c + HC / 2) % HC : c); };
+    const int col0 = half * HC;                        // this warp's columns of the tile
     uint32_t sync_phase = 0;
     auto epi_sync = [&]() -> bool {
       ptx::mbar_arrive(ptx::smem_addr(&sh->epi_sync));
@@ -332,28 +351,78 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mbar_arrive(ptx::smem_addr(bar));
       }
     };
-    int acc = 0;
+    int acc = 0, boxes = 0;
     bool ok = true;
     for (int i = worker; ok && i < units; i += workers) {
       const Unit u = unit(i);
       const int pp = u.p0 + rank * BP + pr;
       const bool live = pp < p.P;
+      // v: this lane's feature of the tile's columns c .. c + CH - 1
       auto write = [&](const float (&v)[CH], int c) {
         const int n = u.nq - c;                        // valid columns from the tile's c-th on
-        const long long at = (long long)(u.q0 + c) * p.ldo + pp;
-        if (p.out_type == SGEMM_TYPE_F32)
-          ragged::write_column<false, CH>(static_cast<float*>(p.out) + at, p.ldo, v, 1.f, nullptr,
-                                          0.f, n, live);
-        else if (p.out_type == SGEMM_TYPE_BF16)
-          ragged::write_column<false, CH>(static_cast<__nv_bfloat16*>(p.out) + at, p.ldo, v, 1.f,
-                                          nullptr, 0.f, n, live);
-        else
-          ragged::write_column<false, CH>(static_cast<__half*>(p.out) + at, p.ldo, v, 1.f, nullptr,
-                                          0.f, n, live);
+        if constexpr (G::kStaged) {
+          // token by token into the warp's buffer (16 bits: one of two, in turn),
+          // then out as one box; lane by lane where C's rows do not allow that
+          const bool f32 = p.out_type == SGEMM_TYPE_F32;
+          unsigned char* buf = base + G::kRegion + (warp - kEpiWarp0) * kOut;
+          if (f32) {
+            ptx::bulk_wait_read<0>();
+          } else {
+            ptx::bulk_wait_read<1>();
+            buf += (boxes & 1) * (kOut / 2);
+          }
+          __syncwarp();
+          if (f32) {
+            float* o = reinterpret_cast<float*>(buf) + lane;
+#pragma unroll
+            for (int j = 0; j < CH; ++j) o[j * 32] = v[j];
+          } else if (p.out_type == SGEMM_TYPE_BF16) {
+            __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(buf) + lane;
+#pragma unroll
+            for (int j = 0; j < CH; ++j) o[j * 32] = __float2bfloat16_rn(v[j]);
+          } else {
+            __half* o = reinterpret_cast<__half*>(buf) + lane;
+#pragma unroll
+            for (int j = 0; j < CH; ++j) o[j * 32] = __float2half_rn(v[j]);
+          }
+          if (p.tma_out) {
+            ptx::fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+              if (pp < p.P)
+                ptx::tma_store_3d(&map_out, ptx::smem_addr(buf), pp, u.q0 + c, 0);
+              ptx::bulk_commit();
+            }
+          } else {
+            __syncwarp();
+            const long long at = (long long)(u.q0 + c) * p.ldo + pp;
+#pragma unroll 4
+            for (int j = 0; j < min(n, CH); ++j) {
+              if (!live) continue;
+              if (f32)
+                static_cast<float*>(p.out)[at + j * p.ldo] = reinterpret_cast<float*>(buf)[j * 32 + lane];
+              else
+                static_cast<uint16_t*>(p.out)[at + j * p.ldo] =
+                    reinterpret_cast<uint16_t*>(buf)[j * 32 + lane];
+            }
+          }
+          ++boxes;
+        } else {
+          const long long at = (long long)(u.q0 + c) * p.ldo + pp;
+          if (p.out_type == SGEMM_TYPE_F32)
+            ragged::write_column<false, CH>(static_cast<float*>(p.out) + at, p.ldo, v, 1.f, nullptr,
+                                            0.f, n, live);
+          else if (p.out_type == SGEMM_TYPE_BF16)
+            ragged::write_column<false, CH>(static_cast<__nv_bfloat16*>(p.out) + at, p.ldo, v, 1.f,
+                                            nullptr, 0.f, n, live);
+          else
+            ragged::write_column<false, CH>(static_cast<__half*>(p.out) + at, p.ldo, v, 1.f, nullptr,
+                                            0.f, n, live);
+        }
       };
       auto load = [&](int c, float (&v)[CH]) {
         uint32_t* r = reinterpret_cast<uint32_t*>(v);
-        const uint32_t src = tmem + lane_base + (uint32_t)((acc & 1) * G::kSecond + column(c));
+        const uint32_t src = tmem + lane_base + (uint32_t)((acc & 1) * G::kSecond + col0 + c);
         if constexpr (CH == 8) {
           tc::tmem_ld8(src, *reinterpret_cast<uint32_t(*)[8]>(r));
         } else {
@@ -370,35 +439,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_after_sync();
         return all;
       };
-      // the columns that both accumulators have are read: the second half's first
-      // 64 of the first, the first half's of the second
-      auto shared_read = [&] {
-        if (G::kShare && half == ((acc & 1) ^ 1)) arrive(&sh->acc_part[acc & 1]);
-      };
       auto release = [&] {
+        // the half that both accumulators have: the first one's second
+        if (G::kShare && half == ((acc & 1) ^ 1)) arrive(&sh->acc_part[acc & 1]);
         arrive(&sh->acc_empty[acc & 1]);
         ++acc;
       };
       float* part = p.partials + ((long long)i * CL + rank) * (BP * BQ) + pr;
-      if (u.ke - u.kb <= p.chunk) {
-        // one accumulation: from tensor memory to its place
+      if (!G::kShare && u.ke - u.kb <= p.chunk) {
+        // one accumulation: from tensor memory to its place, in a rolled loop (a
+        // tile's first pass through unrolled code waits for the instructions)
         ok = acquire();
         if (!ok) break;
 #pragma unroll 1
         for (int c0 = 0; c0 < HC; c0 += CH) {
-          const int c = column(c0);
-          if (c < u.nq) {
-            float v[CH];
-            load(c0, v);
-            if (split > 1) {
+          const int c = col0 + c0;
+          if (c >= u.nq) break;
+          float v[CH];
+          load(c0, v);
+          if (split > 1) {
 #pragma unroll
-              for (int j = 0; j < CH; ++j)
-                if (c + j < u.nq) __stcg(part + (c + j) * BP, v[j]);
-            } else {
-              write(v, c);
-            }
+            for (int j = 0; j < CH; ++j)
+              if (c + j < u.nq) __stcg(part + (c + j) * BP, v[j]);
+          } else {
+            write(v, c);
           }
-          if (c0 + CH == HC / 2) shared_read();
         }
         release();
       } else {
@@ -410,20 +475,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
 #pragma unroll
           for (int c0 = 0; c0 < HC; c0 += CH) {
-            if (column(c0) < u.nq) {                   // (the whole warp)
+            if (col0 + c0 < u.nq) {                    // (the whole warp)
               float v[CH];
               load(c0, v);
 #pragma unroll
               for (int j = 0; j < CH; ++j) sum[c0 + j] += v[j];
             }
-            if (c0 + CH == HC / 2) shared_read();
           }
           release();
         }
         if (!ok) break;
 #pragma unroll
         for (int c0 = 0; c0 < HC; c0 += CH) {
-          const int c = column(c0);
+          const int c = col0 + c0;
           if (c >= u.nq) continue;
           if (split > 1) {
 #pragma unroll
@@ -457,8 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int LP = 32 / CH;                    // parts loaded at a time
 #pragma unroll 1
         for (int c0 = 0; c0 < HC; c0 += CH) {
-          const int c = column(c0);
-          if (c >= u.nq) continue;
+          const int c = col0 + c0;
+          if (c >= u.nq) break;
           float v[CH];
 #pragma unroll
           for (int j = 0; j < CH; ++j) v[j] = 0.f;
@@ -481,6 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    if (G::kStaged) ptx::bulk_wait();                  // the buffers are read, C is written
   }
 
   tc::fence_before_sync();
@@ -562,24 +627,39 @@ int workers_of(int dev, int sms, int i) {
   return b.workers;
 }
 
-// Maps: codes as bytes, boxes of 128 bytes x rows; scales as 32-bit words, a row
-// of tiles a row, boxes of two tiles x `rows`.
-bool encode(CUtensorMap* map, const void* ptr, bool scales, long long cols, long long rows,
-            long long pitch, int box_rows) {
+bool encode(CUtensorMap* map, CUtensorMapDataType type, const void* ptr, long long cols,
+            long long rows, long long pitch, int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
   cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, 1};
   cuuint64_t strides[2] = {(cuuint64_t)pitch, (cuuint64_t)(pitch * rows)};
-  cuuint32_t box[3] = {scales ? 256u : (cuuint32_t)kRow, (cuuint32_t)box_rows, 1};
+  cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   auto call = [&] {
-    return ragged::tensor_map_encode()(
-               map, scales ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
-               const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               scales ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return ragged::tensor_map_encode()(map, type, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                                       CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
   if (call()) return true;
   int dev = 0;   // (a host thread without a context: see ragged::encode_operand)
   return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && call();
+}
+// Codes as bytes, boxes of 128 bytes x `box_rows`.
+bool encode_codes(CUtensorMap* map, const void* ptr, long long bytes, long long rows, int ld, int box_rows) {
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, ptr, bytes, rows, ld, kRow, box_rows,
+                CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// Scales as 32-bit words, a row of tiles a row, boxes of two tiles x `box_rows`.
+bool encode_scales(CUtensorMap* map, const void* ptr, long long rows, long long tiles_k, int box_rows) {
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, ptr, tiles_k * 128, (rows + 127) / 128,
+                tiles_k * 512, 256, box_rows, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+// The output, boxes of 32 features x 32 tokens.
+bool encode_out(CUtensorMap* map, const void* ptr, int type, long long n, long long m, long long pitch) {
+  return encode(map,
+                type == SGEMM_TYPE_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                : type == SGEMM_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                ptr, n, m, pitch, 32, 32, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 // The tile: as wide as the tokens up to 128, else the pair's.
@@ -635,16 +715,18 @@ int run(int M, int N, int K, const void* A, int lda, const void* SA, const void*
   p.timeout_ns = library_wait_timeout_ns();
 
   const long long blocks = (K + 31ll) / 32, tiles_k = (blocks + 3) / 4;
-  CUtensorMap mp = {}, mq = {}, msp = {}, msq = {};
-  if (!encode(&mp, B, false, blocks * 16, N, ldb, BP) ||
-      !encode(&mq, A, false, blocks * 16, M, lda, f.bq / f.cl) ||
-      !encode(&msp, SB, true, tiles_k * 128, (N + 127ll) / 128, tiles_k * 512, 1) ||
-      !encode(&msq, SA, true, tiles_k * 128, (M + 127ll) / 128, tiles_k * 512, (f.bq + 127) / 128))
+  CUtensorMap mp = {}, mq = {}, msp = {}, msq = {}, mo = {};
+  if (!encode_codes(&mp, B, blocks * 16, N, ldb, BP) ||
+      !encode_codes(&mq, A, blocks * 16, M, lda, f.bq / f.cl) ||
+      !encode_scales(&msp, SB, N, tiles_k, 1) || !encode_scales(&msq, SA, M, tiles_k, (f.bq + 127) / 128))
     return SGEMM_ERR_LAUNCH;
+  const int elem = out_type == SGEMM_TYPE_F32 ? 4 : 2;
+  p.tma_out = (reinterpret_cast<uintptr_t>(C) & 15u) == 0 && (long long)ldc * elem % 16 == 0;
+  if (p.tma_out && !encode_out(&mo, C, out_type, N, M, (long long)ldc * elem)) return SGEMM_ERR_LAUNCH;
   const int used = (int)std::min<long long>(workers, tiles * p.split);
   cudaLaunchAttribute la[2];
   const cudaLaunchConfig_t lc = config(f, used, la, stream);
-  void* args[] = {&p, &mp, &mq, &msp, &msq};
+  void* args[] = {&p, &mp, &mq, &msp, &msq, &mo};
   if (cudaLaunchKernelExC(&lc, f.kernel, args) != cudaSuccess) {
     cudaGetLastError();
     return SGEMM_ERR_LAUNCH;

@@ -44,130 +44,177 @@ struct Args {
   unsigned char* scale;
 };
 
+// A warp's share: a piece of a row (whole groups of 4 blocks), whose loads are
+// all in flight before the first is used. Numbered row by row; the division is
+// done in 32 bits where the numbers allow it (in 64 it took most of the time).
+struct Share {
+  long long m;
+  int piece;
+};
+__device__ __forceinline__ Share share_of(long long i, int pieces) {
+  if (i <= 0xffffffffll) {
+    const unsigned m = (unsigned)i / (unsigned)pieces;
+    return {m, (int)((unsigned)i - m * (unsigned)pieces)};
+  }
+  const long long m = i / pieces;
+  return {m, (int)(i - m * pieces)};
+}
+
+// The byte of a block whose largest magnitude has these bits (255: no number
+// among them), and the factor that brings its values to units.
+__device__ __forceinline__ uint32_t power_of(uint32_t most) {
+  const int e = (int)(most >> 23);
+  return e == 255 ? 255u : (uint32_t)max(e - 2, 0);
+}
+__device__ __forceinline__ float units_of(uint32_t s) {
+  return __uint_as_float((254u - min(s, 252u)) << 23);   // 1 / 2^(s - 127)
+}
+
 // VW neighbours a thread (16 bytes of X, or one element), so a block of 32 is 32
 // / VW lanes, and a warp takes VW blocks at a time. All of the scales' tiles are
 // written: zeros where they belong to no block.
+constexpr int kAhead = 4;                              // pieces of a thread
+constexpr int values_of(int vw) { return vw > 1 ? 32 * vw * kAhead : 128; }   // of a warp's share
 template <typename E, int VW>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(const Args a) {
-  constexpr int kLanes = 32 / VW;          // of a block
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
-  // groups of 4 blocks, 128 values, of the rows and of those that fill up their tiles
-  const long long groups = (long long)a.block_tiles * ((a.M + 127ll) / 128 * 128);
-  constexpr int kAtOnce = VW > 1 ? 32 / (4 * kLanes) : 1;       // groups of a warp
+  constexpr int kValues = values_of(VW);
+  const int pieces = (int)((a.block_tiles * 128ll + kValues - 1) / kValues);
+  // (the rows that fill up the scales' tiles have zeros, too)
+  const long long all = (a.M + 127ll) / 128 * 128 * pieces;
   const long long warps = (long long)gridDim.x * (kThreads / 32);
-  for (long long g0 = (blockIdx.x * (long long)(kThreads / 32) + (threadIdx.x >> 5)) * kAtOnce;
-       g0 < groups; g0 += warps * kAtOnce) {
+  for (long long i = blockIdx.x * (long long)(kThreads / 32) + (threadIdx.x >> 5); i < all; i += warps) {
+    const Share sh = share_of(i, pieces);
+    const bool row = sh.m < a.M;
+    const E* x = static_cast<const E*>(a.x) + sh.m * a.ldx;
+    unsigned char* q = a.q + sh.m * a.ldq;
+    const long long k0 = (long long)sh.piece * kValues;
     if constexpr (VW > 1) {
-      const long long g = g0 + lane / (4 * kLanes);
-      const bool in = g < groups;
-      const long long m = in ? g / a.block_tiles : 0;
-      const int tile = in ? (int)(g - m * a.block_tiles) : 0;
-      const int l = lane & (4 * kLanes - 1);                    // within the group
-      const long long k = tile * 128ll + l * VW;
-      float v[VW];
+      constexpr int kLanes = 32 / VW;                  // of a block
+      rows::Piece<E, VW> in[kAhead];
 #pragma unroll
-      for (int i = 0; i < VW; ++i) v[i] = 0.f;
-      // (K is a multiple of VW here)
-      if (in && m < a.M && k < a.K)
-        rows::unpack(rows::load<E, VW>(static_cast<const E*>(a.x) + m * a.ldx + k), v);
-      uint32_t most = 0;
-#pragma unroll
-      for (int i = 0; i < VW; ++i) most = max(most, __float_as_uint(v[i]) & 0x7fffffffu);
-#pragma unroll
-      for (int d = 1; d < kLanes; d <<= 1) most = max(most, __shfl_xor_sync(kAll, most, d));
-      const int e = (int)(most >> 23);                          // 255: no number among them
-      const uint32_t s = e == 255 ? 255u : (uint32_t)max(e - 2, 0);
-      const float unit = __uint_as_float((254u - min(s, 252u)) << 23);   // 1 / 2^(s - 127)
-      uint32_t w = 0;
-#pragma unroll
-      for (int i = 0; i < VW; i += 2)
-        w |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(v[i] * unit, v[i + 1] * unit), __NV_E2M1,
-                                                cudaRoundNearest) << (4 * i);
-      // the row's blocks are whole: past its end there are zeros
-      if (in && m < a.M && k < a.blocks * 32ll) {
-        unsigned char* q = a.q + m * a.ldq + k / 2;
-        if constexpr (VW == 8)
-          *reinterpret_cast<uint32_t*>(q) = w;
-        else
-          *reinterpret_cast<uint16_t*>(q) = (uint16_t)w;
+      for (int j = 0; j < kAhead; ++j) {
+        const long long k = k0 + j * (32 * VW) + lane * VW;
+        if (row && k < a.K) in[j] = rows::load<E, VW>(x + k);   // (K is a multiple of VW here)
       }
-      // the group's four bytes, by its first lane (past the row's end: 0)
-      uint32_t word = s & 0xffu;
-      word = m < a.M && tile * 4 + l / kLanes < a.blocks ? word : 0u;
-      const int first = lane & ~(4 * kLanes - 1);
-      const uint32_t b1 = __shfl_sync(kAll, word, first + kLanes),
-                     b2 = __shfl_sync(kAll, word, first + 2 * kLanes),
-                     b3 = __shfl_sync(kAll, word, first + 3 * kLanes);
-      if (in && l == 0)
-        *reinterpret_cast<uint32_t*>(a.scale + scale_place(m, tile * 4, a.block_tiles)) =
-            word | b1 << 8 | b2 << 16 | b3 << 24;
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const long long k = k0 + j * (32 * VW) + lane * VW;
+        if (k - lane * VW >= a.block_tiles * 128ll) break;      // (the whole warp)
+        float v[VW];
+#pragma unroll
+        for (int c = 0; c < VW; ++c) v[c] = 0.f;
+        if (row && k < a.K) rows::unpack(in[j], v);
+        uint32_t most = 0;
+#pragma unroll
+        for (int c = 0; c < VW; ++c) most = max(most, __float_as_uint(v[c]) & 0x7fffffffu);
+#pragma unroll
+        for (int d = 1; d < kLanes; d <<= 1) most = max(most, __shfl_xor_sync(kAll, most, d));
+        const uint32_t s = power_of(most);
+        const float unit = units_of(s);
+        uint32_t w = 0;
+#pragma unroll
+        for (int c = 0; c < VW; c += 2)
+          w |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(v[c] * unit, v[c + 1] * unit),
+                                                  __NV_E2M1, cudaRoundNearest) << (4 * c);
+        // the row's blocks are whole: past its end there are zeros
+        const bool block = row && k < a.blocks * 32ll;
+        if (block) {
+          if constexpr (VW == 8)
+            *reinterpret_cast<uint32_t*>(q + k / 2) = w;
+          else
+            *reinterpret_cast<uint16_t*>(q + k / 2) = (uint16_t)w;
+        }
+        // a group's four bytes, by its first lane
+        const uint32_t byte = block ? s : 0u;
+        const int first = lane & ~(4 * kLanes - 1);
+        const uint32_t word = byte | __shfl_sync(kAll, byte, first + kLanes) << 8 |
+                              __shfl_sync(kAll, byte, first + 2 * kLanes) << 16 |
+                              __shfl_sync(kAll, byte, first + 3 * kLanes) << 24;
+        if (lane == first && k < a.block_tiles * 128ll)
+          *reinterpret_cast<uint32_t*>(a.scale + scale_place(sh.m, (int)(k / 32), a.block_tiles)) = word;
+      }
     } else {
-      const long long m = g0 / a.block_tiles;
-      const int tile = (int)(g0 - m * a.block_tiles);
-      const E* x = static_cast<const E*>(a.x) + m * a.ldx;
       uint32_t word = 0;
       float v[4];
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const long long k = (tile * 4ll + b) * 32 + lane;
-        v[b] = m < a.M && k < a.K ? to_f32(x[k]) : 0.f;
+        const long long k = k0 + b * 32 + lane;
+        v[b] = row && k < a.K ? to_f32(x[k]) : 0.f;
       }
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const long long k = (tile * 4ll + b) * 32 + lane;
-        const int e = (int)(__reduce_max_sync(kAll, __float_as_uint(v[b]) & 0x7fffffffu) >> 23);
-        const uint32_t s = e == 255 ? 255u : (uint32_t)max(e - 2, 0);
-        const float unit = __uint_as_float((254u - min(s, 252u)) << 23);
+        const long long k = k0 + b * 32 + lane;
+        const uint32_t s = power_of(__reduce_max_sync(kAll, __float_as_uint(v[b]) & 0x7fffffffu));
+        const float unit = units_of(s);
         const float next = __shfl_down_sync(kAll, v[b], 1);
-        if (m < a.M && tile * 4 + b < a.blocks) {
+        if (row && k - lane < a.blocks * 32ll) {
           word |= s << (8 * b);
           if (!(lane & 1))
-            a.q[m * a.ldq + k / 2] = (unsigned char)__nv_cvt_float2_to_fp4x2(
-                make_float2(v[b] * unit, next * unit), __NV_E2M1, cudaRoundNearest);
+            q[k / 2] = (unsigned char)__nv_cvt_float2_to_fp4x2(make_float2(v[b] * unit, next * unit),
+                                                               __NV_E2M1, cudaRoundNearest);
         }
       }
       if (lane == 0)
-        *reinterpret_cast<uint32_t*>(a.scale + scale_place(m, tile * 4, a.block_tiles)) = word;
+        *reinterpret_cast<uint32_t*>(a.scale + scale_place(sh.m, sh.piece * 4, a.block_tiles)) = word;
     }
   }
 }
 
 // Values of a block: the code's value times the block's power, rounded to E. A
-// scale of 255 makes them NaN. Eight codes (4 bytes) a thread.
+// scale of 255 makes them NaN. Eight codes (4 bytes) a thread at a time.
 template <typename E>
 __global__ void __launch_bounds__(kThreads)
     dequantize_kernel(const Args a, E* x, long long ldx, int wide) {
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  const long long pieces = (a.K + 7ll) / 8, all = pieces * a.M;
-  for (long long i = blockIdx.x * (long long)kThreads + threadIdx.x; i < all;
-       i += (long long)gridDim.x * kThreads) {
-    const long long m = i / pieces, k = (i - m * pieces) * 8;
-    const unsigned char* q = a.q + m * a.ldq + k / 2;
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(q);     // (rows are whole blocks)
-    const uint32_t s = a.scale[scale_place(m, (int)(k / 32), a.block_tiles)];
-    // 2^(s - 127): below the normal numbers for s = 0, NaN for 255
-    const float unit = s == 0 ? 0x1p-127f : __uint_as_float(s == 255 ? 0x7fc00000u : s << 23);
-    float v[8];
+  constexpr int kValues = 32 * 8 * kAhead;
+  const int lane = threadIdx.x & 31, pieces = (int)((a.K + (long long)kValues - 1) / kValues);
+  const long long all = (long long)a.M * pieces, warps = (long long)gridDim.x * (kThreads / 32);
+  for (long long i = blockIdx.x * (long long)(kThreads / 32) + (threadIdx.x >> 5); i < all; i += warps) {
+    const Share sh = share_of(i, pieces);
+    const long long k0 = (long long)sh.piece * kValues + lane * 8;
+    const unsigned char* q = a.q + sh.m * a.ldq;
+    uint32_t w[kAhead], s[kAhead];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t c = w >> (4 * j) & 15u, e = c >> 1 & 3u, f = c & 1u;
-      // E2M1: 0 and 0.5, then (1 + f / 2) 2^(e - 1)
-      const float mag = e == 0 ? 0.5f * (float)f : __uint_as_float((126u + e) << 23 | f << 22);
-      v[j] = (c & 8u ? -mag : mag) * unit;
+    for (int j = 0; j < kAhead; ++j) {
+      const long long k = k0 + j * 256;
+      if (k >= a.K) continue;
+      w[j] = __ldcs(reinterpret_cast<const uint32_t*>(q + k / 2));   // (rows are whole blocks)
+      s[j] = a.scale[scale_place(sh.m, (int)(k / 32), a.block_tiles)];
     }
-    E* o = x + m * ldx + k;
-    if (wide && k + 8 <= a.K) {
-      constexpr int VW = 16 / (int)sizeof(E);
 #pragma unroll
-      for (int j = 0; j < 8; j += VW)
-        rows::store<E, VW>(o + j, rows::pack<E, VW>(*reinterpret_cast<const float(*)[VW]>(v + j)));
-    } else {
+    for (int j = 0; j < kAhead; ++j) {
+      const long long k = k0 + j * 256;
+      if (k >= a.K) continue;
+      // 2^(s - 127): below the normal numbers for s = 0, NaN for 255
+      const float unit =
+          s[j] == 0 ? 0x1p-127f : __uint_as_float(s[j] == 255 ? 0x7fc00000u : s[j] << 23);
+      float v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (k + j < a.K) o[j] = from_f32<E>(v[j]);
+      for (int c = 0; c < 8; ++c) {
+        const uint32_t code = w[j] >> (4 * c) & 15u, e = code >> 1 & 3u, f = code & 1u;
+        // E2M1: 0 and 0.5, then (1 + f / 2) 2^(e - 1)
+        const float mag = e == 0 ? 0.5f * (float)f : __uint_as_float((126u + e) << 23 | f << 22);
+        v[c] = (code & 8u ? -mag : mag) * unit;
+      }
+      E* o = x + sh.m * ldx + k;
+      if (wide && k + 8 <= a.K) {
+        constexpr int VW = 16 / (int)sizeof(E);
+#pragma unroll
+        for (int c = 0; c < 8; c += VW) {
+          float part[VW];
+#pragma unroll
+          for (int d = 0; d < VW; ++d) part[d] = v[c + d];
+          rows::store<E, VW>(o + c, rows::pack<E, VW>(part));
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (k + c < a.K) o[c] = from_f32<E>(v[c]);
+      }
     }
   }
 }
@@ -190,19 +237,21 @@ cudaError_t start(void (*kernel)(A...), long long blocks, int sms, cudaStream_t 
 template <typename E>
 cudaError_t quantize(const Args& a, int sms, cudaStream_t stream) {
   constexpr int VW = 16 / (int)sizeof(E);
-  const long long groups = (long long)a.block_tiles * ((a.M + 127ll) / 128 * 128);
   const bool vec = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && a.ldx * sizeof(E) % 16 == 0 &&
                    a.K % VW == 0;
-  const long long per_block = (kThreads / 32) * (vec ? VW / 4 : 1);
+  const int values = values_of(vec ? VW : 1);
+  const long long shares = (a.M + 127ll) / 128 * 128 * ((a.block_tiles * 128ll + values - 1) / values);
   return start(vec ? quantize_kernel<E, VW> : quantize_kernel<E, 1>,
-               (groups + per_block - 1) / per_block, sms, stream, a);
+               (shares + kThreads / 32 - 1) / (kThreads / 32), sms, stream, a);
 }
 
 template <typename E>
 cudaError_t dequantize(const Args& a, void* x, long long ldx, int sms, cudaStream_t stream) {
   const bool wide = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && ldx * sizeof(E) % 16 == 0;
-  return start(dequantize_kernel<E>, ((a.K + 7ll) / 8 * a.M + kThreads - 1) / kThreads, sms, stream,
-               a, static_cast<E*>(x), ldx, (int)wide);
+  constexpr int kValues = 32 * 8 * kAhead;
+  const long long shares = (a.K + (long long)kValues - 1) / kValues * a.M;
+  return start(dequantize_kernel<E>, (shares + kThreads / 32 - 1) / (kThreads / 32), sms, stream, a,
+               static_cast<E*>(x), ldx, (int)wide);
 }
 
 bool type_ok(int type) {
