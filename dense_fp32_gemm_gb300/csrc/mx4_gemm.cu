@@ -26,20 +26,22 @@
 // issues M = 256 MMAs over both; each holds its 128 rows of P, half of Q's rows
 // and all of Q's scales.
 //
-// Schedule: whole tiles in turn; where there are fewer tiles than workers each is
-// cut into `split` ranges of k, whose last worker to arrive adds the parts in the
-// order of k (no CTA waits for another).
+// Schedule: whole tiles in turn. Where there are few tiles each is cut into 2, 4
+// or 8 ranges of k, one for each CTA of a cluster (SPLIT). They leave their parts
+// in their shared memory, and each adds some of the columns over all of them, in
+// the order of k. (Through L2, by the last of them to arrive, the exchange of two
+// 128 x 256 tiles took 9 us.)
 //
 // Every wait is bounded; a CTA that gives up drains its copies and MMAs, frees
 // its tensor memory and returns.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <algorithm>
-#include <atomic>
 #include <cstdio>
 #include <mutex>
 
 #include "../../include/sgemm_gb300.h"
+#include "elements.cuh"
 #include "ragged_launch.cuh"
 
 #define SGEMM_API extern "C" __attribute__((visibility("default")))
@@ -55,14 +57,11 @@ constexpr uint32_t kAll = 0xffffffffu;
 
 struct Params {
   int P, Q, K;              // features, tokens, values of k
-  int split;                // ranges of k that a tile is cut into
   int chunk;                // slices of one accumulation
   void* out;
   long long ldo;
   int out_type;
   int tma_out;              // C's rows are at multiples of 16 bytes: written by TMA
-  float* partials;          // a tile for each unit: BQ columns of CL * BP
-  uint32_t* counters;       // arrivals at a tile, zero unless status is set
   int* status;
   long long timeout_ns;
 };
@@ -101,9 +100,9 @@ struct Geo {
 struct Shared {
   uint64_t full[10], empty[10];
   uint64_t acc_full[2], acc_empty[2], acc_part[2];
-  uint64_t drain, epi_sync;
+  uint64_t drain;
   uint32_t tmem;
-  int abort, last, split;
+  int abort;
 };
 constexpr int kOut = 4096;                 // of a warp
 constexpr int kSmem = 1024 + 208 * 1024 + 512;
@@ -113,12 +112,19 @@ using ragged::cdiv;
 using ragged::wait_for;
 using ragged::wait_for_pair;
 
-// A part of a worker's list: slices kb .. ke of the tile (p0, q0).
+// Part of a worker's list: slices kb .. ke of the tile (p0, q0).
 struct Unit {
-  int tile, part, p0, q0, nq, nn, kb, ke;
+  int p0, q0, nq, nn, kb, ke;
 };
 
-template <int BQ, int CL>
+template <typename T>
+__device__ __forceinline__ void put(T* out, long long at, int n, const float (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < n) out[at + i] = rows::from_f32<T>(v[i]);
+}
+
+template <int BQ, int CL, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     mx4_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap map_p,
                const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_sp,
@@ -126,6 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                const __grid_constant__ CUtensorMap map_out) {
   using G = Geo<BQ, CL>;
   constexpr bool kPair = CL == 2;
+  static_assert(!SPLIT || (!kPair && BQ <= 128 && BQ * BP * 4 <= G::kRegion), "cut tiles");
   constexpr int S = G::kStages;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw_addr = ptx::smem_addr(smem_raw);
@@ -136,7 +143,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_w = &sh->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = kPair ? (int)ptx::cluster_ctarank() : 0;
-  const int worker = (int)blockIdx.x / CL, workers = (int)gridDim.x / CL;
+  const int split = SPLIT ? (int)ptx::cluster_nctarank() : 1;
+  const int part = SPLIT ? (int)ptx::cluster_ctarank() : 0;
+  const int worker = (int)blockIdx.x / (SPLIT ? split : CL), workers = (int)gridDim.x / (SPLIT ? split : CL);
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
@@ -149,7 +158,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(ptx::smem_addr(&sh->acc_part[i]), CL * kEpiWarps / 2);
     }
     ptx::mbar_init(ptx::smem_addr(&sh->drain), 1);
-    ptx::mbar_init(ptx::smem_addr(&sh->epi_sync), kEpiWarps * 32);
     sh->abort = 0;
     ptx::mbar_fence_init();
     ptx::tma_prefetch_desc(&map_p);
@@ -164,9 +172,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  // A launch before this one that gave up may have left arrivals counted, until
-  // its status is polled: then no tile is cut.
-  if (tid == 0) sh->split = *const_cast<const volatile int*>(p.status) != 0 ? 1 : p.split;
   tc::fence_before_sync();
   __syncthreads();
   if (kPair) ptx::cluster_sync();
@@ -176,32 +181,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
       const uint32_t peer =
           ptx::ld_shared_cluster(ptx::mapa(ptx::smem_addr(&sh->tmem), (uint32_t)(rank ^ 1)));
-      // (the two read the status one after another: a pair takes one's word)
-      const uint32_t cut =
-          ptx::ld_shared_cluster(ptx::mapa(ptx::smem_addr(&sh->split), 0u));
       if (peer != tmem) {
         *abort_w = 1;
         atomicCAS(p.status, 0, (int)kDevTmemMismatch);
       }
-      sh->last = (int)cut;
     }
-    __syncthreads();
+    __syncthreads();  // every role sees the abort word
   }
-  const int split = kPair ? sh->last : sh->split;
-  __syncthreads();          // `last` is the epilogue's from here on
   const int slices = cdiv(p.K, kSliceK), tiles_q = cdiv(p.Q, BQ);
-  const int units = cdiv(p.P, BP * CL) * tiles_q * split;
+  const int tiles = cdiv(p.P, BP * CL) * tiles_q;
   auto unit = [&](int i) {
     Unit u;
-    u.tile = i / split;
-    u.part = i - u.tile * split;
-    const int tp = u.tile / tiles_q;      // q fastest: workers running together share weight tiles
+    const int tp = i / tiles_q;           // q fastest: workers running together share weight tiles
     u.p0 = tp * (BP * CL);
-    u.q0 = (u.tile - tp * tiles_q) * BQ;
+    u.q0 = (i - tp * tiles_q) * BQ;
     u.nq = min(BQ, p.Q - u.q0);
     u.nn = min(BQ, cdiv(u.nq, 16 * CL) * (16 * CL));
-    u.kb = (int)((long long)slices * u.part / split);
-    u.ke = (int)((long long)slices * (u.part + 1) / split);
+    u.kb = SPLIT ? (int)((long long)slices * part / split) : 0;
+    u.ke = SPLIT ? (int)((long long)slices * (part + 1) / split) : slices;
     return u;
   };
 
@@ -212,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ptx::elect_one()) {
       int it = 0;
       bool ok = true;
-      for (int i = worker; ok && i < units; i += workers) {
+      for (int i = worker; ok && i < tiles; i += workers) {
         const Unit u = unit(i);
         const int p0 = u.p0 + rank * BP, q0 = u.q0 + rank * (u.nn / CL);
         for (int ks = u.kb; ks < u.ke; ++ks, ++it) {
@@ -273,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t b_desc = tc::smem_desc(base_addr + G::kP, 16, 1024, true);
       int it = 0, acc = 0;
       bool ok = true;
-      for (int i = worker; ok && i < units; i += workers) {
+      for (int i = worker; ok && i < tiles; i += workers) {
         const Unit u = unit(i);
         const uint32_t idesc[2] = {tc::idesc_mx4(BP * CL, u.nn, 0), tc::idesc_mx4(BP * CL, u.nn, 2)};
         for (int k0 = u.kb; k0 < u.ke && ok; k0 += p.chunk, ++acc) {
@@ -333,14 +330,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pr = quarter * 32 + lane;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     const int col0 = half * HC;                        // this warp's columns of the tile
-    uint32_t sync_phase = 0;
-    auto epi_sync = [&]() -> bool {
-      ptx::mbar_arrive(ptx::smem_addr(&sh->epi_sync));
-      const bool ok = wait_for(ptx::smem_addr(&sh->epi_sync), sync_phase, abort_w, p.status,
-                               kDevTimeoutSync, p.timeout_ns);
-      sync_phase ^= 1u;
-      return __all_sync(kAll, ok);
-    };
     auto arrive = [&](uint64_t* bar) {
       tc::fence_before_sync();
       __syncwarp();
@@ -353,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     int acc = 0, boxes = 0;
     bool ok = true;
-    for (int i = worker; ok && i < units; i += workers) {
+    for (int i = worker; ok && i < tiles; i += workers) {
       const Unit u = unit(i);
       const int pp = u.p0 + rank * BP + pr;
       const bool live = pp < p.P;
@@ -445,7 +434,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         arrive(&sh->acc_empty[acc & 1]);
         ++acc;
       };
-      float* part = p.partials + ((long long)i * CL + rank) * (BP * BQ) + pr;
+      // a cut tile's part: column after column of 128 lanes, where the stages were
+      auto keep = [&](const float (&v)[CH], int c) {
+        float* o = reinterpret_cast<float*>(base) + c * BP + pr;
+#pragma unroll
+        for (int j = 0; j < CH; ++j) o[j * BP] = v[j];
+      };
       if (!G::kShare && u.ke - u.kb <= p.chunk) {
         // one accumulation: from tensor memory to its place, in a rolled loop (a
         // tile's first pass through unrolled code waits for the instructions)
@@ -457,13 +451,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (c >= u.nq) break;
           float v[CH];
           load(c0, v);
-          if (split > 1) {
-#pragma unroll
-            for (int j = 0; j < CH; ++j)
-              if (c + j < u.nq) __stcg(part + (c + j) * BP, v[j]);
-          } else {
+          if (SPLIT)
+            keep(v, c);
+          else
             write(v, c);
-          }
         }
         release();
       } else {
@@ -489,63 +480,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c0 = 0; c0 < HC; c0 += CH) {
           const int c = col0 + c0;
           if (c >= u.nq) continue;
-          if (split > 1) {
-#pragma unroll
-            for (int j = 0; j < CH; ++j)
-              if (c + j < u.nq) __stcg(part + (c + j) * BP, sum[c0 + j]);
-          } else {
-            float v[CH];
-#pragma unroll
-            for (int j = 0; j < CH; ++j) v[j] = sum[c0 + j];
-            write(v, c);
-          }
-        }
-      }
-      if (split > 1) {
-        // the last worker to arrive adds the parts in the order of k
-        __threadfence();
-        ok = epi_sync();
-        if (!ok) break;
-        if (warp == kEpiWarp0 && lane == 0) {
-          uint32_t* counter = p.counters + u.tile * CL + rank;
-          const int last = atomicAdd(counter, 1u) == (uint32_t)(split - 1);
-          if (last) *counter = 0u;                     // ready for the next launch
-          __threadfence();
-          sh->last = last;
-        }
-        ok = epi_sync();
-        if (!ok) break;
-        if (!*reinterpret_cast<volatile int*>(&sh->last)) continue;
-        __threadfence();
-        const float* first = p.partials + ((long long)u.tile * split * CL + rank) * (BP * BQ) + pr;
-        constexpr int LP = 32 / CH;                    // parts loaded at a time
-#pragma unroll 1
-        for (int c0 = 0; c0 < HC; c0 += CH) {
-          const int c = col0 + c0;
-          if (c >= u.nq) break;
           float v[CH];
 #pragma unroll
-          for (int j = 0; j < CH; ++j) v[j] = 0.f;
-#pragma unroll 1
-          for (int i0 = 0; i0 < split; i0 += LP) {
-            float x[LP][CH];
-#pragma unroll
-            for (int l = 0; l < LP; ++l)
-#pragma unroll
-              for (int j = 0; j < CH; ++j)
-                x[l][j] = i0 + l < split && c + j < u.nq
-                              ? __ldcg(first + (long long)(i0 + l) * CL * (BP * BQ) + (c + j) * BP)
-                              : 0.f;
-#pragma unroll
-            for (int l = 0; l < LP; ++l)
-#pragma unroll
-              for (int j = 0; j < CH; ++j) v[j] += x[l][j];
-          }
-          write(v, c);
+          for (int j = 0; j < CH; ++j) v[j] = sum[c0 + j];
+          if (SPLIT)
+            keep(v, c);
+          else
+            write(v, c);
         }
       }
     }
-    if (G::kStaged) ptx::bulk_wait();                  // the buffers are read, C is written
+    if (G::kStaged && !SPLIT) ptx::bulk_wait();                  // the buffers are read, C is written
   }
 
   tc::fence_before_sync();
@@ -566,65 +511,106 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_after_sync();
     tc::tmem_dealloc<CL>(tmem, G::kTmem);
   }
+  if constexpr (SPLIT) {
+    // every thread of every CTA of the cluster comes here, whoever gave up
+    ptx::cluster_sync();
+    const Unit u = unit(worker);
+    // a warp a column, four features a lane
+    for (int c = part + split * warp; c < u.nq; c += split * (kThreads / 32)) {
+      const uint32_t at = base_addr + (uint32_t)(c * BP + lane * 4) * 4u;
+      float4 x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < split) x[i] = ptx::ld_shared_cluster_v4(ptx::mapa(at, (uint32_t)i));
+      float4 s = x[0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i)
+        if (i < split) {
+          s.x += x[i].x;
+          s.y += x[i].y;
+          s.z += x[i].z;
+          s.w += x[i].w;
+        }
+      const float v[4] = {s.x, s.y, s.z, s.w};
+      const int pp = u.p0 + lane * 4, n = min(4, p.P - pp);
+      const long long o = (long long)(u.q0 + c) * p.ldo + pp;
+      if (p.out_type == SGEMM_TYPE_F32)
+        put(static_cast<float*>(p.out), o, n, v);
+      else if (p.out_type == SGEMM_TYPE_BF16)
+        put(static_cast<__nv_bfloat16*>(p.out), o, n, v);
+      else
+        put(static_cast<__half*>(p.out), o, n, v);
+    }
+    ptx::cluster_sync();      // the others have read this CTA's part
+  }
 }
 
 // ---- host ---------------------------------------------------------------------------
+// The built kernels, with what they take on GB300, in ns: a slice, and a tile
+// beside its slices (8192 x 8192 x 4096 and x 8192; narrow ones 4864 x 16 .. 64).
 struct Form {
   int bq, cl;
+  bool split;
+  int slice, tile;
   const void* kernel;
 };
-#define SGEMM_GB300_MX4(BQ, CL) {BQ, CL, reinterpret_cast<const void*>(&mx4_kernel<BQ, CL>)}
-const Form kForms[] = {SGEMM_GB300_MX4(16, 1),  SGEMM_GB300_MX4(32, 1),  SGEMM_GB300_MX4(64, 1),
-                       SGEMM_GB300_MX4(128, 1), SGEMM_GB300_MX4(256, 1), SGEMM_GB300_MX4(256, 2)};
+#define SGEMM_GB300_MX4(BQ, CL, SPLIT, SLICE, TILE) \
+  {BQ, CL, SPLIT, SLICE, TILE, reinterpret_cast<const void*>(&mx4_kernel<BQ, CL, SPLIT>)}
+const Form kForms[] = {
+    SGEMM_GB300_MX4(16, 1, false, 170, 700),    SGEMM_GB300_MX4(16, 1, true, 170, 700),
+    SGEMM_GB300_MX4(32, 1, false, 190, 800),    SGEMM_GB300_MX4(32, 1, true, 190, 800),
+    SGEMM_GB300_MX4(64, 1, false, 220, 900),    SGEMM_GB300_MX4(64, 1, true, 220, 900),
+    SGEMM_GB300_MX4(128, 1, false, 283, 1000),  SGEMM_GB300_MX4(128, 1, true, 283, 1000),
+    SGEMM_GB300_MX4(256, 1, false, 383, 1900),  SGEMM_GB300_MX4(256, 2, false, 300, 2300)};
 constexpr int kNumForms = sizeof(kForms) / sizeof(kForms[0]), kMaxDevices = 64;
-struct Built {
-  bool ready;
-  int workers;
-};
+constexpr int kSplitCost = 1500;           // what cutting a tile costs, ns
 std::mutex g_mutex;
-Built g_built[kMaxDevices][kNumForms];
+bool g_ready[kMaxDevices][kNumForms];
+int g_resident[kMaxDevices][9];            // clusters of 2, 4, 8 CTAs resident at once
 
-cudaLaunchConfig_t config(const Form& f, int workers, cudaLaunchAttribute (&la)[2], cudaStream_t stream) {
+cudaLaunchConfig_t config(int ctas, int cluster, cudaLaunchAttribute (&la)[2], cudaStream_t stream) {
   la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   la[0].val.programmaticStreamSerializationAllowed = 1;
   la[1].id = cudaLaunchAttributeClusterDimension;
-  la[1].val.clusterDim.x = f.cl;
+  la[1].val.clusterDim.x = cluster;
   la[1].val.clusterDim.y = 1;
   la[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)(workers * f.cl));
+  lc.gridDim = dim3((unsigned)ctas);
   lc.blockDim = dim3(kThreads);
   lc.dynamicSmemBytes = kSmem;
   lc.stream = stream;
   lc.attrs = la;
-  lc.numAttrs = f.cl == 2 ? 2 : 1;
+  lc.numAttrs = cluster > 1 ? 2 : 1;
   return lc;
 }
 
-// Workers of a form that are resident at once (0: it cannot run).
-int workers_of(int dev, int sms, int i) {
-  if (dev < 0 || dev >= kMaxDevices) return 0;
+// Makes the kernels ready on the device; false where that fails.
+bool prepare(int dev, int sms) {
+  if (dev < 0 || dev >= kMaxDevices) return false;
   std::lock_guard<std::mutex> lock(g_mutex);
-  Built& b = g_built[dev][i];
-  if (b.ready) return b.workers;
-  const Form& f = kForms[i];
-  if (cudaFuncSetAttribute(f.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) {
-    cudaGetLastError();
-    return 0;
-  }
-  b.workers = sms;
-  if (f.cl == 2) {
-    cudaLaunchAttribute la[2];
-    cudaLaunchConfig_t lc = config(f, sms / 2 > 0 ? sms / 2 : 1, la, nullptr);
-    lc.attrs = la + 1;
-    lc.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&b.workers, f.kernel, &lc) != cudaSuccess) {
+  for (int i = 0; i < kNumForms; ++i) {
+    if (g_ready[dev][i]) continue;
+    const Form& f = kForms[i];
+    if (cudaFuncSetAttribute(f.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) {
       cudaGetLastError();
-      b.workers = 0;
+      return false;
     }
+    // (SMs form clusters within a GPC, so there can be fewer than sms / size; the
+    // kernels' shared memory leaves one CTA an SM, so one kernel stands for all)
+    for (int size = 2; size <= 8 && f.cl == 2; size *= 2) {
+      cudaLaunchAttribute la[2];
+      cudaLaunchConfig_t lc = config(sms / size * size, size, la, nullptr);
+      lc.attrs = la + 1;
+      lc.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&g_resident[dev][size], f.kernel, &lc) != cudaSuccess) {
+        cudaGetLastError();
+        g_resident[dev][size] = 0;
+      }
+    }
+    g_ready[dev][i] = true;
   }
-  b.ready = true;
-  return b.workers;
+  return true;
 }
 
 bool encode(CUtensorMap* map, CUtensorMapDataType type, const void* ptr, long long cols,
@@ -662,13 +648,35 @@ bool encode_out(CUtensorMap* map, const void* ptr, int type, long long n, long l
                 ptr, n, m, pitch, 32, 32, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-// The tile: as wide as the tokens up to 128, else the pair's.
-int choose(int M, int N) {
-  if (M <= 16) return 0;
-  if (M <= 32) return 1;
-  if (M <= 64) return 2;
-  if (M <= 128) return 3;
-  return 5;
+// The form and the parts of a tile that take least time by the table: waves of
+// whole tiles, or one wave of tiles in parts. A tile narrower than 128 columns
+// only where it holds all tokens (the scales of its rows start a tile of 128).
+// `width`, `ctas`: a tile that is asked for (0: none).
+struct Choice {
+  const Form* form;
+  int split;
+};
+Choice choose(int M, int N, int K, int sms, const int* resident, int width, int ctas) {
+  Choice best{nullptr, 1};
+  double least = 0;
+  const int slices = cdiv(K, kSliceK);
+  for (const Form& f : kForms) {
+    if (f.bq < 128 && M > f.bq) continue;
+    if (width > 0 && (f.bq != width || f.cl != ctas)) continue;
+    const double tiles = (double)cdiv(N, BP * f.cl) * cdiv(M, f.bq);
+    for (int split = f.split ? 2 : 1; split <= (f.split ? 8 : 1); split *= 2) {
+      const int size = f.split ? split : f.cl, workers = size == 1 ? sms : resident[size];
+      if (workers == 0 || (f.split && (tiles > workers || slices < 2 * split))) continue;
+      const double waves = (double)(long long)((tiles + workers - 1) / workers);
+      const double ns = waves * (f.tile + (double)cdiv(slices, split) * f.slice) +
+                        (f.split ? kSplitCost : 0);
+      if (best.form == nullptr || ns < least) {
+        least = ns;
+        best = Choice{&f, split};
+      }
+    }
+  }
+  return best;
 }
 
 int run(int M, int N, int K, const void* A, int lda, const void* SA, const void* B, int ldb,
@@ -681,37 +689,29 @@ int run(int M, int N, int K, const void* A, int lda, const void* SA, const void*
   int st = library_device_sms(dev, &sms);
   if (st != SGEMM_OK) return st;
   if (ragged::tensor_map_encode() == nullptr) return SGEMM_ERR_LAUNCH;
-  int i = choose(M, N), workers = 0;
+  if (!prepare(dev, sms)) return SGEMM_ERR_LAUNCH;
   int width = 0, ctas = 0;
   ragged::forced_tile(&width, &ctas);
-  for (int j = 0; width > 0 && j < kNumForms; ++j)
-    // (a narrow tile has the scales of its first 128 rows only at their start)
-    if (kForms[j].bq == width && kForms[j].cl == ctas && (width >= 128 || M <= width)) i = j;
-  workers = workers_of(dev, sms, i);
-  if (workers == 0 && kForms[i].cl == 2) workers = workers_of(dev, sms, --i);
-  if (workers == 0) return SGEMM_ERR_LAUNCH;
-  const Form& f = kForms[i];
-
+  Choice c{nullptr, 1};
+  if (width > 0) c = choose(M, N, K, sms, g_resident[dev], width, ctas);
+  if (c.form == nullptr) c = choose(M, N, K, sms, g_resident[dev], 0, 0);
+  if (c.form == nullptr) return SGEMM_ERR_LAUNCH;
+  const Form& f = *c.form;
+  const int workers = f.cl == 2 ? g_resident[dev][2] : sms;
   const long long tiles = (long long)cdiv(N, BP * f.cl) * cdiv(M, f.bq);
-  if (tiles > 0x7fffffffLL / 64) return SGEMM_ERR_INVALID_DIM;
-  const int slices = cdiv(K, kSliceK);
+  if (tiles > 0x7fffffffLL / 16) return SGEMM_ERR_INVALID_DIM;
   Params p = {};
   p.P = N;
   p.Q = M;
   p.K = K;
-  p.split = 1;
-  if (tiles < workers) p.split = (int)std::min<long long>(workers / tiles, std::max(1, slices / 2));
   p.chunk = out_type == SGEMM_TYPE_F32 ? 8 : 32;
   p.out = C;
   p.ldo = ldc;
   p.out_type = out_type;
-  const size_t partial = p.split > 1 ? (size_t)tiles * p.split * f.cl * BP * f.bq : 1;
   float* ws = nullptr;
   const std::unique_lock<std::mutex> lock = library_lock();   // to the launch
-  st = library_workspace(dev, stream, partial, (size_t)workers * f.cl, &ws, &p.status, nullptr,
-                         nullptr, &p.counters);
+  st = library_workspace(dev, stream, 0, 0, &ws, &p.status, nullptr, nullptr, nullptr);
   if (st != SGEMM_OK) return st;
-  p.partials = ws;
   p.timeout_ns = library_wait_timeout_ns();
 
   const long long blocks = (K + 31ll) / 32, tiles_k = (blocks + 3) / 4;
@@ -723,9 +723,9 @@ int run(int M, int N, int K, const void* A, int lda, const void* SA, const void*
   const int elem = out_type == SGEMM_TYPE_F32 ? 4 : 2;
   p.tma_out = (reinterpret_cast<uintptr_t>(C) & 15u) == 0 && (long long)ldc * elem % 16 == 0;
   if (p.tma_out && !encode_out(&mo, C, out_type, N, M, (long long)ldc * elem)) return SGEMM_ERR_LAUNCH;
-  const int used = (int)std::min<long long>(workers, tiles * p.split);
+  const int grid = c.split > 1 ? (int)tiles * c.split : (int)std::min<long long>(workers, tiles) * f.cl;
   cudaLaunchAttribute la[2];
-  const cudaLaunchConfig_t lc = config(f, used, la, stream);
+  const cudaLaunchConfig_t lc = config(grid, c.split > 1 ? c.split : f.cl, la, stream);
   void* args[] = {&p, &mp, &mq, &msp, &msq, &mo};
   if (cudaLaunchKernelExC(&lc, f.kernel, args) != cudaSuccess) {
     cudaGetLastError();
@@ -733,7 +733,7 @@ int run(int M, int N, int K, const void* A, int lda, const void* SA, const void*
   }
   char text[160];
   snprintf(text, sizeof(text), "mx4_%dx%dx%d cluster=%d grid=%d split=%d", BP * f.cl, f.bq, kSliceK,
-           f.cl, used * f.cl, p.split);
+           f.cl, grid, c.split);
   note_last_config(text);
   return SGEMM_OK;
 }

@@ -70,18 +70,78 @@ __device__ __forceinline__ float units_of(uint32_t s) {
   return __uint_as_float((254u - min(s, 252u)) << 23);   // 1 / 2^(s - 127)
 }
 
-// VW neighbours a thread (16 bytes of X, or one element), so a block of 32 is 32
-// / VW lanes, and a warp takes VW blocks at a time. All of the scales' tiles are
-// written: zeros where they belong to no block.
+// Eight neighbours of a row, as they are stored: what the kernel needs of them.
+// The largest magnitude as the bits of an FP32 value, a NaN above all numbers.
+template <typename E>
+struct Eight {
+  uint4 w;
+  __device__ __forceinline__ void load(const E* p) { w = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void clear() { w = make_uint4(0u, 0u, 0u, 0u); }
+  // (the bits of 16-bit magnitudes are in the order of the magnitudes)
+  __device__ __forceinline__ uint32_t most() const {
+    const uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
+                                __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+    const uint16_t h = (uint16_t)max(m & 0xffffu, m >> 16);
+    return __float_as_uint(to_f32(*reinterpret_cast<const E*>(&h)));
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = rows::unpack2(in[i], E{});
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+};
+template <>
+struct Eight<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldcs(reinterpret_cast<const float4*>(p));
+    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ uint32_t most() const {
+    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    return m;
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+
+// The codes of eight values, the first in the lowest bits.
+__device__ __forceinline__ uint32_t codes_of(const float (&v)[8]) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(w)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return w;
+}
+
+// Eight neighbours a thread (VEC: 16-byte aligned), so a block of 32 is 4 lanes,
+// and a warp takes 8 blocks at a time; or one element a lane. All of the scales'
+// tiles are written: zeros where they belong to no block.
 constexpr int kAhead = 4;                              // pieces of a thread
-constexpr int values_of(int vw) { return vw > 1 ? 32 * vw * kAhead : 128; }   // of a warp's share
-template <typename E, int VW>
+constexpr int values_of(bool vec) { return vec ? 256 * kAhead : 128; }   // of a warp's share
+template <typename E, bool VEC>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(const Args a) {
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  constexpr int kValues = values_of(VW);
-  const int pieces = (int)((a.block_tiles * 128ll + kValues - 1) / kValues);
+  const unsigned lane = threadIdx.x & 31, K = (unsigned)a.K;
+  const unsigned row_end = (unsigned)a.blocks * 32u, tile_end = (unsigned)a.block_tiles * 128u;
+  constexpr unsigned kValues = values_of(VEC);
+  const int pieces = (int)((tile_end + kValues - 1) / kValues);
   // (the rows that fill up the scales' tiles have zeros, too)
   const long long all = (a.M + 127ll) / 128 * 128 * pieces;
   const long long warps = (long long)gridDim.x * (kThreads / 32);
@@ -90,130 +150,117 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const Args a) {
     const bool row = sh.m < a.M;
     const E* x = static_cast<const E*>(a.x) + sh.m * a.ldx;
     unsigned char* q = a.q + sh.m * a.ldq;
-    const long long k0 = (long long)sh.piece * kValues;
-    if constexpr (VW > 1) {
-      constexpr int kLanes = 32 / VW;                  // of a block
-      rows::Piece<E, VW> in[kAhead];
+    unsigned char* scale = a.scale + scale_place(sh.m, 0, a.block_tiles);   // the row's: 512 bytes a tile
+    const unsigned k0 = (unsigned)sh.piece * kValues;
+    if constexpr (VEC) {
+      Eight<E> in[kAhead];
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
-        const long long k = k0 + j * (32 * VW) + lane * VW;
-        if (row && k < a.K) in[j] = rows::load<E, VW>(x + k);   // (K is a multiple of VW here)
+        const unsigned k = k0 + j * 256u + lane * 8u;
+        in[j].clear();
+        if (row && k < K) in[j].load(x + k);           // (K is a multiple of 8 here)
       }
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
-        const long long k = k0 + j * (32 * VW) + lane * VW;
-        if (k - lane * VW >= a.block_tiles * 128ll) break;      // (the whole warp)
-        float v[VW];
-#pragma unroll
-        for (int c = 0; c < VW; ++c) v[c] = 0.f;
-        if (row && k < a.K) rows::unpack(in[j], v);
-        uint32_t most = 0;
-#pragma unroll
-        for (int c = 0; c < VW; ++c) most = max(most, __float_as_uint(v[c]) & 0x7fffffffu);
-#pragma unroll
-        for (int d = 1; d < kLanes; d <<= 1) most = max(most, __shfl_xor_sync(kAll, most, d));
+        const unsigned k = k0 + j * 256u + lane * 8u;
+        if (k0 + j * 256u >= tile_end) break;          // (the whole warp)
+        uint32_t most = in[j].most();
+        most = max(most, __shfl_xor_sync(kAll, most, 1));
+        most = max(most, __shfl_xor_sync(kAll, most, 2));
         const uint32_t s = power_of(most);
         const float unit = units_of(s);
-        uint32_t w = 0;
+        float v[8];
+        in[j].values(v);
 #pragma unroll
-        for (int c = 0; c < VW; c += 2)
-          w |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(v[c] * unit, v[c + 1] * unit),
-                                                  __NV_E2M1, cudaRoundNearest) << (4 * c);
+        for (int c = 0; c < 8; ++c) v[c] *= unit;
         // the row's blocks are whole: past its end there are zeros
-        const bool block = row && k < a.blocks * 32ll;
-        if (block) {
-          if constexpr (VW == 8)
-            *reinterpret_cast<uint32_t*>(q + k / 2) = w;
-          else
-            *reinterpret_cast<uint16_t*>(q + k / 2) = (uint16_t)w;
-        }
-        // a group's four bytes, by its first lane
-        const uint32_t byte = block ? s : 0u;
-        const int first = lane & ~(4 * kLanes - 1);
-        const uint32_t word = byte | __shfl_sync(kAll, byte, first + kLanes) << 8 |
-                              __shfl_sync(kAll, byte, first + 2 * kLanes) << 16 |
-                              __shfl_sync(kAll, byte, first + 3 * kLanes) << 24;
-        if (lane == first && k < a.block_tiles * 128ll)
-          *reinterpret_cast<uint32_t*>(a.scale + scale_place(sh.m, (int)(k / 32), a.block_tiles)) = word;
+        const bool block = row && k < row_end;
+        if (block) *reinterpret_cast<uint32_t*>(q + k / 2) = codes_of(v);
+        // four blocks' bytes, by the first of their 16 lanes
+        uint32_t word = block ? s << (lane * 2 & 24u) : 0u;
+        word |= __shfl_xor_sync(kAll, word, 4);
+        word |= __shfl_xor_sync(kAll, word, 8);
+        if ((lane & 15u) == 0 && k < tile_end)
+          *reinterpret_cast<uint32_t*>(scale + (size_t)(k / 128) * 512) = word;
       }
     } else {
       uint32_t word = 0;
       float v[4];
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const long long k = k0 + b * 32 + lane;
-        v[b] = row && k < a.K ? to_f32(x[k]) : 0.f;
+        const unsigned k = k0 + b * 32u + lane;
+        v[b] = row && k < K ? to_f32(x[k]) : 0.f;
       }
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const long long k = k0 + b * 32 + lane;
+        const unsigned k = k0 + b * 32u + lane;
         const uint32_t s = power_of(__reduce_max_sync(kAll, __float_as_uint(v[b]) & 0x7fffffffu));
         const float unit = units_of(s);
         const float next = __shfl_down_sync(kAll, v[b], 1);
-        if (row && k - lane < a.blocks * 32ll) {
+        if (row && k0 + b * 32u < row_end) {
           word |= s << (8 * b);
-          if (!(lane & 1))
+          if (!(lane & 1u))
             q[k / 2] = (unsigned char)__nv_cvt_float2_to_fp4x2(make_float2(v[b] * unit, next * unit),
                                                                __NV_E2M1, cudaRoundNearest);
         }
       }
-      if (lane == 0)
-        *reinterpret_cast<uint32_t*>(a.scale + scale_place(sh.m, sh.piece * 4, a.block_tiles)) = word;
+      if (lane == 0) *reinterpret_cast<uint32_t*>(scale + (size_t)sh.piece * 512) = word;
     }
   }
 }
 
 // Values of a block: the code's value times the block's power, rounded to E. A
-// scale of 255 makes them NaN. Eight codes (4 bytes) a thread at a time.
+// scale of 255 makes them NaN. A thread writes 16 bytes at a time (4 or 8 values).
 template <typename E>
 __global__ void __launch_bounds__(kThreads)
     dequantize_kernel(const Args a, E* x, long long ldx, int wide) {
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  constexpr int kValues = 32 * 8 * kAhead;
-  const int lane = threadIdx.x & 31, pieces = (int)((a.K + (long long)kValues - 1) / kValues);
+  constexpr int VW = 16 / (int)sizeof(E), kPieces = 8 * kAhead / VW;
+  constexpr unsigned kValues = values_of(true);
+  const unsigned lane = threadIdx.x & 31, K = (unsigned)a.K;
+  const int pieces = (int)((K + kValues - 1) / kValues);
   const long long all = (long long)a.M * pieces, warps = (long long)gridDim.x * (kThreads / 32);
   for (long long i = blockIdx.x * (long long)(kThreads / 32) + (threadIdx.x >> 5); i < all; i += warps) {
     const Share sh = share_of(i, pieces);
-    const long long k0 = (long long)sh.piece * kValues + lane * 8;
+    const unsigned k0 = (unsigned)sh.piece * kValues + lane * VW;
     const unsigned char* q = a.q + sh.m * a.ldq;
-    uint32_t w[kAhead], s[kAhead];
+    const unsigned char* scale = a.scale + scale_place(sh.m, 0, a.block_tiles);
+    E* o = x + sh.m * ldx;
+    uint32_t w[kPieces], s[kPieces];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const long long k = k0 + j * 256;
-      if (k >= a.K) continue;
-      w[j] = __ldcs(reinterpret_cast<const uint32_t*>(q + k / 2));   // (rows are whole blocks)
-      s[j] = a.scale[scale_place(sh.m, (int)(k / 32), a.block_tiles)];
+    for (int j = 0; j < kPieces; ++j) {
+      const unsigned k = k0 + j * (32u * VW);
+      if (k >= K) continue;
+      // (rows are whole blocks)
+      if constexpr (VW == 8)
+        w[j] = __ldcs(reinterpret_cast<const uint32_t*>(q + k / 2));
+      else
+        w[j] = __ldcs(reinterpret_cast<const uint16_t*>(q + k / 2));
+      s[j] = __ldg(scale + (size_t)(k / 128) * 512 + (k / 32) % 4);
     }
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const long long k = k0 + j * 256;
-      if (k >= a.K) continue;
+    for (int j = 0; j < kPieces; ++j) {
+      const unsigned k = k0 + j * (32u * VW);
+      if (k >= K) continue;
       // 2^(s - 127): below the normal numbers for s = 0, NaN for 255
       const float unit =
           s[j] == 0 ? 0x1p-127f : __uint_as_float(s[j] == 255 ? 0x7fc00000u : s[j] << 23);
-      float v[8];
+      float v[VW];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const uint32_t code = w[j] >> (4 * c) & 15u, e = code >> 1 & 3u, f = code & 1u;
-        // E2M1: 0 and 0.5, then (1 + f / 2) 2^(e - 1)
-        const float mag = e == 0 ? 0.5f * (float)f : __uint_as_float((126u + e) << 23 | f << 22);
-        v[c] = (code & 8u ? -mag : mag) * unit;
+      for (int c = 0; c < VW; c += 2) {
+        const __half2_raw h =
+            __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(w[j] >> (4 * c) & 0xffu), __NV_E2M1);
+        const float2 f = __half22float2(__half2(h));
+        v[c] = f.x * unit;
+        v[c + 1] = f.y * unit;
       }
-      E* o = x + sh.m * ldx + k;
-      if (wide && k + 8 <= a.K) {
-        constexpr int VW = 16 / (int)sizeof(E);
-#pragma unroll
-        for (int c = 0; c < 8; c += VW) {
-          float part[VW];
-#pragma unroll
-          for (int d = 0; d < VW; ++d) part[d] = v[c + d];
-          rows::store<E, VW>(o + c, rows::pack<E, VW>(part));
-        }
+      if (wide && k + VW <= K) {
+        rows::store<E, VW>(o + k, rows::pack<E, VW>(v));
       } else {
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          if (k + c < a.K) o[c] = from_f32<E>(v[c]);
+        for (int c = 0; c < VW; ++c)
+          if (k + c < K) o[k + c] = from_f32<E>(v[c]);
       }
     }
   }
@@ -226,7 +273,7 @@ cudaError_t start(void (*kernel)(A...), long long blocks, int sms, cudaStream_t 
   cudaLaunchAttribute la[1];
   la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   la[0].val.programmaticStreamSerializationAllowed = 1;
-  lc.gridDim = dim3((unsigned)(blocks < sms * 8ll ? blocks : sms * 8ll));
+  lc.gridDim = dim3((unsigned)(blocks < sms * 64ll ? blocks : sms * 64ll));
   lc.blockDim = dim3(kThreads);
   lc.stream = stream;
   lc.attrs = la;
@@ -236,20 +283,18 @@ cudaError_t start(void (*kernel)(A...), long long blocks, int sms, cudaStream_t 
 
 template <typename E>
 cudaError_t quantize(const Args& a, int sms, cudaStream_t stream) {
-  constexpr int VW = 16 / (int)sizeof(E);
   const bool vec = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && a.ldx * sizeof(E) % 16 == 0 &&
-                   a.K % VW == 0;
-  const int values = values_of(vec ? VW : 1);
+                   a.K % 8 == 0;
+  const int values = values_of(vec);
   const long long shares = (a.M + 127ll) / 128 * 128 * ((a.block_tiles * 128ll + values - 1) / values);
-  return start(vec ? quantize_kernel<E, VW> : quantize_kernel<E, 1>,
+  return start(vec ? quantize_kernel<E, true> : quantize_kernel<E, false>,
                (shares + kThreads / 32 - 1) / (kThreads / 32), sms, stream, a);
 }
 
 template <typename E>
 cudaError_t dequantize(const Args& a, void* x, long long ldx, int sms, cudaStream_t stream) {
   const bool wide = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && ldx * sizeof(E) % 16 == 0;
-  constexpr int kValues = 32 * 8 * kAhead;
-  const long long shares = (a.K + (long long)kValues - 1) / kValues * a.M;
+  const long long shares = (a.K + (long long)values_of(true) - 1) / values_of(true) * a.M;
   return start(dequantize_kernel<E>, (shares + kThreads / 32 - 1) / (kThreads / 32), sms, stream, a,
                static_cast<E*>(x), ldx, (int)wide);
 }

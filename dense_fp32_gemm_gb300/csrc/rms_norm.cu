@@ -264,9 +264,12 @@ struct GradArgs {
 // A row per block at a time, every thread at the same places in each, so that
 // its part of dw stays in registers over all rows of the block. DW: the row
 // fits into HELD pieces a thread and dw's parts are formed.
-template <typename E, typename W, int VW, bool DW>
-__global__ void __launch_bounds__(kMaxThreads) norm_grad_kernel(const GradArgs a) {
-  constexpr int HELD = held_of(VW);
+// HELD 2 (rows of at most 512 pieces): the next row's loads are ahead, on 256
+// threads; more pieces, and their sums, leave no registers for that.
+template <typename E, typename W, int VW, int HELD, bool DW>
+__global__ void __launch_bounds__(HELD == 2 ? 256 : kMaxThreads, HELD == 2 ? 2 : 1)
+    norm_grad_kernel(const GradArgs a) {
+  constexpr bool kAhead = HELD == 2;
   __shared__ float2 part[2][kMaxThreads / 32];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
@@ -283,17 +286,31 @@ __global__ void __launch_bounds__(kMaxThreads) norm_grad_kernel(const GradArgs a
   for (int i = 0; i < (DW ? HELD : 1); ++i)
 #pragma unroll
     for (int j = 0; j < VW; ++j) dw[i][j] = 0.f;
-  for (long long m = blockIdx.x; m < a.M; m += gridDim.x) {
-    const float rstd = a.rstd[m];
-    Piece<E, VW> g[HELD], v[HELD], d[HELD];
+  Piece<E, VW> g1[HELD], v1[HELD], d1[HELD];
+  float rstd1 = 0.f;
+  auto fetch = [&](long long m) {
+    rstd1 = a.rstd[m];
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
       const unsigned c = c0 + i * step_c;
       if (c >= N) continue;
-      g[i] = load<E, VW>(dy + m * a.lddy + c);
-      v[i] = load<E, VW>(h + m * a.ldh + c);
-      if (dh != nullptr) d[i] = load<E, VW>(dh + m * a.lddh + c);
+      g1[i] = load<E, VW>(dy + m * a.lddy + c);
+      v1[i] = load<E, VW>(h + m * a.ldh + c);
+      if (dh != nullptr) d1[i] = load<E, VW>(dh + m * a.lddh + c);
     }
+  };
+  if (kAhead) fetch(blockIdx.x);
+  for (long long m = blockIdx.x; m < a.M; m += gridDim.x) {
+    if (!kAhead) fetch(m);
+    const float rstd = rstd1;
+    Piece<E, VW> g[HELD], v[HELD], d[HELD];
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+      g[i] = g1[i];
+      v[i] = v1[i];
+      d[i] = d1[i];
+    }
+    if (kAhead && m + gridDim.x < a.M) fetch(m + gridDim.x);
     float sum = 0.f;
     auto add = [&](const Piece<E, VW>& g, const Piece<E, VW>& v, unsigned c) {
       float wv[VW], gf[VW], vf[VW], s = 0.f;
@@ -382,9 +399,9 @@ __global__ void __launch_bounds__(kColumnThreads) column_kernel(const GradArgs a
   }
 }
 
-// dw[c] = sum of the parts in their order: 32 columns a block, 8 threads a
-// column, each the parts of its own residue.
-constexpr int kSumLanes = 8;
+// dw[c] = sum of the parts in an order of their own: 32 columns a block, 32
+// threads a column, each the parts of its residue.
+constexpr int kSumLanes = 32;
 template <typename W>
 __global__ void __launch_bounds__(32 * kSumLanes)
     sum_kernel(const float* partial, int parts, int N, W* dw) {
@@ -402,7 +419,7 @@ __global__ void __launch_bounds__(32 * kSumLanes)
     s[group][lane] = sum;
     __syncthreads();
     if (group == 0 && c < N) {
-#pragma unroll
+#pragma unroll 8
       for (int g = 1; g < kSumLanes; ++g) sum += s[g][lane];
       dw[c] = from_f32<W>(sum);
     }
@@ -457,20 +474,22 @@ cudaError_t forward(NormArgs a, int sms, cudaStream_t stream) {
                 blocks_of(a.M, t, sms, 512), t, stream, a);
 }
 
-// `blocks` make a part of dw each: of norm_grad_kernel where a row is `held`, else
-// slabs of column_kernel.
+// `blocks` make a part of dw each: of norm_grad_kernel where a row is `held` (in so
+// many pieces a thread), else (0) slabs of column_kernel.
 template <typename E, typename W>
 cudaError_t backward(GradArgs a, W* dw, float* partial, int blocks, int sms, cudaStream_t stream,
-                     int threads, bool vec, bool held) {
+                     int threads, bool vec, int held) {
   constexpr int VW = 16 / (int)sizeof(E);
   a.partial = partial;
   cudaError_t e = cudaSuccess;
-  if (held) {
-    e = launch(vec ? norm_grad_kernel<E, W, VW, true> : norm_grad_kernel<E, W, 1, true>, blocks,
-               threads, stream, a);
+  if (held != 0) {
+    e = launch(!vec         ? norm_grad_kernel<E, W, 1, 8, true>
+               : held == 2 ? norm_grad_kernel<E, W, VW, 2, true>
+                           : norm_grad_kernel<E, W, VW, 4, true>,
+               blocks, threads, stream, a);
   } else {
     if (a.dx != nullptr)
-      e = launch(vec ? norm_grad_kernel<E, W, VW, false> : norm_grad_kernel<E, W, 1, false>,
+      e = launch(vec ? norm_grad_kernel<E, W, VW, 4, false> : norm_grad_kernel<E, W, 1, 8, false>,
                  blocks_of(a.M, threads, sms, 512), threads, stream, a);
     if (e == cudaSuccess && dw != nullptr) {
       const long long all = (a.N + kColumnThreads - 1ll) / kColumnThreads * blocks;
@@ -648,11 +667,12 @@ SGEMM_API int sgemm_rms_norm_grad(int M, int N, int type, const void* dY, int ld
                    rows::aligned(dH, lddh, eb, 16) && rows::aligned(dX, lddx, eb, 16) &&
                    rows::aligned(weight, 0, wb, 16) && N % vw == 0;
   const long long pieces = vec ? N / vw : N;
-  const int most = rows::held_of(vec ? vw : 1);
-  const bool held = pieces <= most * rows::kMaxThreads;
-  const int threads = rows::threads_of(pieces, most, M < 2 * sms);
+  const int held = pieces > rows::held_of(vec ? vw : 1) * rows::kMaxThreads ? 0
+                   : vec ? (pieces <= 512 ? 2 : 4) : 8;
+  const int threads = held == 2 ? rows::threads_of(pieces, 2, false)
+                                : rows::threads_of(pieces, rows::held_of(vec ? vw : 1), M < 2 * sms);
   int blocks = 0;
-  if (held) {
+  if (held != 0) {
     blocks = rows::blocks_of(M, threads, sms, 512);
   } else {
     const int fill = sms * 8 / (int)((N + rows::kColumnThreads - 1ll) / rows::kColumnThreads) + 1;
