@@ -181,25 +181,38 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
-// FP32: a piece of logits into G, in place.
+// FP32: a piece of logits into G, in place. Rows start on 16 bytes; what is
+// between a row's end and the next multiple of 4 is not used.
+constexpr int kAhead = 2;                  // pieces of 16 bytes a thread
 __global__ void __launch_bounds__(kRowThreads)
     gradient_kernel(int T, int n, float* z, long long ldz, const long long* target, int col0,
                     const float* lse, const float* row_scale) {
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  const long long blocks = (n + 4ll * kRowThreads - 1) / (4 * kRowThreads);   // of a row
+  constexpr int kBlock = 4 * kAhead * kRowThreads;
+  const long long blocks = (n + (long long)kBlock - 1) / kBlock;   // of a row
   for (long long b = blockIdx.x; b < blocks * T; b += gridDim.x) {
     const long long t = b / blocks;
-    const long long c0 = (b - t * blocks) * (4 * kRowThreads) + threadIdx.x;
+    const long long c0 = (b - t * blocks) * kBlock + threadIdx.x * 4;
     float* row = z + t * ldz;
+    float4 v[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (c0 + i * (4 * kRowThreads) < n)
+        v[i] = __ldcg(reinterpret_cast<const float4*>(row + c0 + i * (4 * kRowThreads)));
     const float l = lse[t], s = row_scale[t];
     const long long a = target[t] - col0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const long long c = c0 + i * kRowThreads;
+    for (int i = 0; i < kAhead; ++i) {
+      const long long c = c0 + i * (4 * kRowThreads);
       if (c >= n) break;
-      const float e = expf(row[c] - l);
-      row[c] = s == 0.f ? 0.f : (c == a ? e - 1.f : e) * s;
+      float g[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float e = expf(g[j] - l);
+        g[j] = s == 0.f ? 0.f : (c + j == a ? e - 1.f : e) * s;
+      }
+      *reinterpret_cast<float4*>(row + c) = make_float4(g[0], g[1], g[2], g[3]);
     }
   }
 }
@@ -420,8 +433,21 @@ int backward(const Problem& q, const float* lse, const float* dloss, void* dX, i
   const size_t at_g = ws.take((size_t)T * ldg * elem);
   const size_t at_sums = ws.take(sums ? (size_t)T * H * 4 : 0);
 
+  // X, and each piece of W, serve two products: where TMA cannot read them in
+  // place they are copied once
+  Operand x = q.x();
+  Operand w0 = q.words(0, n0);
+  const bool copy_x = !x.direct(), copy_w = !w0.direct();
+  const size_t at_x = ws.take(copy_x ? x.packed_bytes(false) : 0);
+  const size_t at_w = ws.take(copy_w ? w0.packed_bytes(false) : 0);
+
   const int src = q.f32() ? ragged::kF32 : ragged::k16;
-  const Operand x = q.x();
+  auto copied = [&](Operand* a) {          // as pack_operands() will describe it
+    a->ptr = reinterpret_cast<void*>(256);
+    a->ld = a->packed_pitch(false) / a->elem;
+  };
+  if (copy_x) copied(&x);
+  if (copy_w) copied(&w0);
   auto gradient = [&](int m, int v0, void* g) {
     Params p = q.f32() ? q.plain(m, static_cast<float*>(g), ldg) : q.per_token(m, v0);
     p.out = g;
@@ -473,10 +499,10 @@ int backward(const Problem& q, const float* lse, const float* dloss, void* dX, i
   for (int i = 0; V > 0 && i < 3; ++i) {
     if ((i == 1 && dX == nullptr) || (i == 2 && dW == nullptr)) continue;
     if (i == 0)
-      st = q.f32() ? ragged::plan(src, q.type, gradient(n0, 0, somewhere), q.words(0, n0), x, &plans[i])
-                   : ragged::plan(ragged::kGrad, q.type, gradient(n0, 0, somewhere), x, q.words(0, n0), &plans[i]);
+      st = q.f32() ? ragged::plan(src, q.type, gradient(n0, 0, somewhere), w0, x, &plans[i])
+                   : ragged::plan(ragged::kGrad, q.type, gradient(n0, 0, somewhere), x, w0, &plans[i]);
     else if (i == 1)
-      st = ragged::plan(src, q.type, input(n0, 0, nullptr), q.words(0, n0), g_of(somewhere, n0), &plans[i]);
+      st = ragged::plan(src, q.type, input(n0, 0, nullptr), w0, g_of(somewhere, n0), &plans[i]);
     else
       st = ragged::plan(src, q.type, weight(n0, 0), x, g_of(somewhere, n0), &plans[i]);
     if (st != SGEMM_OK) return st;
@@ -508,11 +534,19 @@ int backward(const Problem& q, const float* lse, const float* dloss, void* dX, i
       return p;
     };
     Params p = with(gradient(m, v0, g));
-    const Operand w = q.words(v0, m);
+    Operand w = q.words(v0, m);
+    if (copy_w || (copy_x && v0 == 0)) {
+      Operand first = q.x();
+      const bool of_x = copy_x && v0 == 0;
+      st = done(ragged::pack_operands(&first, of_x ? at + at_x : nullptr, &w,
+                                      copy_w ? at + at_w : nullptr, false, sms, stream));
+      if (st != SGEMM_OK) return st;
+      if (of_x) x = first;
+    }
     if (q.f32()) {
       st = ragged::launch(plans[0], p, w, x, rest, stream, "linear_ce_grad");
       if (st != SGEMM_OK) return st;
-      const long long blocks = (m + 4ll * kRowThreads - 1) / (4 * kRowThreads) * T;
+      const long long block = 4 * kAhead * kRowThreads, blocks = (m + block - 1) / block * T;
       st = done(start(gradient_kernel, at_most(blocks, sms * 8ll), kRowThreads, stream, T, m,
                       static_cast<float*>(g), ldg, q.target, v0, lse,
                       static_cast<const float*>(row_scale)));
