@@ -232,7 +232,7 @@ bool misaligned(const void* p, int bytes) {
 }
 
 // The built kernels, and per device what prepare() said of each.
-constexpr int kMaxDevices = 64, kMaxForms = 32;
+constexpr int kMaxDevices = 64, kMaxForms = 40;
 struct Built {
   bool ready;
   int workers;
@@ -289,8 +289,12 @@ constexpr TileCost kTileCosts[] = {
     {kI8Wide, 256, 2, 364, 2500},
 };
 // Integers that have been widened cost what F16 operands do, and so do the
-// products of a loss (built from 64 columns on).
-bool loss(int src) { return src == kLse || src == kGrad; }
+// products of a loss (with tokens on the lanes built from 64 columns on, else up
+// to 64).
+bool loss(int src) { return src >= kLse; }
+bool built(int src, int bq) {
+  return src == kLse || src == kGrad ? bq >= 64 : !loss(src) || bq <= 64;
+}
 int cost_source(int src) { return src == kI8Wide || loss(src) ? k16 : src; }
 // The costs of a form: those of its own number of CTAs.
 TileCost tile_cost(int src, int bq, int cl) {
@@ -319,7 +323,7 @@ Form choose_tile(int src, const Params& p, int sms, double* ns) {
   Form best{src, 0, 1};
   double least = 0;
   for (const TileCost& c : kTileCosts) {
-    if (c.src != (loss(src) ? k16 : src) || ((p.wgrad || loss(src)) && c.bq < 64)) continue;
+    if (c.src != (loss(src) ? k16 : src) || (p.wgrad && c.bq < 64) || !built(src, c.bq)) continue;
     const int workers = sms / c.cl;
     const double groups = p.E < p.T ? p.E : (p.T > 0 ? p.T : 1);
     const double q = p.wgrad ? (double)p.E * cdiv(p.Q, c.bq)

@@ -26,7 +26,10 @@
 //   kI8Wide  the same integers, already as F16 in the workspace;
 //   kLse, kGrad  as k16, p = token and q = word of a vocabulary (X is the P side):
 //         a thread has a token's logits, of which kLse keeps the largest and
-//         the sum of exponentials, and kGrad writes the loss's gradient.
+//         the sum of exponentials, and kGrad writes the loss's gradient;
+//   kLseFew, kGradFew  the same for few tokens, p = word and q = token as in a
+//         plain product, so that the vocabulary streams through full tiles; the
+//         sums of a token go over the lanes of a warp.
 //
 // Accumulation. The tensor core adds into FP32 with truncation, an error that
 // grows with the number of instructions. A tile's sum is therefore cut into
@@ -93,7 +96,7 @@
 namespace sgemm_gb300 {
 namespace ragged {
 
-enum Src : int { k16 = 0, kF32 = 1, kI8 = 2, kI8Wide = 3, kLse = 4, kGrad = 5 };
+enum Src : int { k16 = 0, kF32 = 1, kI8 = 2, kI8Wide = 3, kLse = 4, kGrad = 5, kLseFew = 6, kGradFew = 7 };
 enum OutType : int { kOutF32 = 0, kOutBf16 = 1, kOutF16 = 2 };
 
 constexpr int BP = 128;            // tile height in p (MMA M)
@@ -123,13 +126,15 @@ struct Params {
   const float* alpha_dev; // rows, wgrad: a factor of alpha on the device; may be null
   const float* scale_p;   // kI8: scales of p and q
   const float* scale_q;
-  // kLse, kGrad: the words are col0 .. col0 + T - 1 of the vocabulary
+  // loss: the first of the product's words is number col0 of the vocabulary
   const long long* target;  // a word for each token
   int col0;
-  float2* stats;          // kLse: (largest logit, sum of exp(logit - it)), [tile of q][half][token]
-  float* at_target;       // kLse: the target's logit
-  const float* lse;       // kGrad: log of the sum of exponentials over the vocabulary
-  const float* row_scale; // kGrad: factor of a token's gradient (0: all of it is 0)
+  // kLse: (largest logit, sum of exp(logit - it)), [tile of words][half][token];
+  // kLseFew: [tile of words][quarter][token]
+  float2* stats;
+  float* at_target;       // kLse, kLseFew: the target's logit
+  const float* lse;       // kGrad, kGradFew: log of the sum of exponentials over the vocabulary
+  const float* row_scale; // the same: factor of a token's gradient (0: all of it is 0)
   int chunk;              // values of k per tensor-memory accumulation (a multiple of the slice)
   // when tiles are cut along k: the slices a part has at least, and what a cut
   // costs, in 1/16 slices: once, and for each part of the tile
@@ -517,8 +522,9 @@ __device__ __forceinline__ float exp2_fast(float v) {
 // kLse: a token's logits, some columns at a time. The sum is of exp(logit -
 // most); most is a number whatever the logits are, so columns of -infinity add
 // nothing and a NaN or +infinity among them makes the sum NaN or infinite.
+constexpr float kLeast = -3.402823466e38f;
 struct Softmax {
-  float most = -3.402823466e38f, sum = 0.f, at_target = 0.f;
+  float most = kLeast, sum = 0.f, at_target = 0.f;
   template <int N>
   __device__ __forceinline__ void add(const float (&z)[N], int n, int target) {
     float m = most;
@@ -574,6 +580,18 @@ __device__ __forceinline__ void write_gradient(T* out, const float (&z)[N], floa
         if (c0 + i < n) from_f32(out + c0 + i, g[i]);
     }
   }
+}
+
+// Largest value and sum over a warp, in every lane.
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
 }
 
 // Part of a thread's column of the tile: `n` valid values (of HC) at pitch ld,
@@ -1146,6 +1164,39 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
           softmax.add(sums, nq - c0, target < 0 ? -1 : target - c0);
           return;
         }
+        if constexpr (SRC == kLseFew) {
+          // (every lane of the warp is here) lane c keeps what column c gives
+#pragma unroll
+          for (int c = 0; c < N; ++c) {
+            if (c >= nq - c0) continue;
+            const float most = warp_max(live ? fmaxf(sums[c], kLeast) : kLeast);
+            const float sum = warp_sum(live ? exp2_fast((sums[c] - most) * kLog2e) : 0.f);
+            if (lane == c0 + c) {
+              softmax.most = most;
+              softmax.sum = sum;
+            }
+            const long long q = w.q0 + half * HC + c0 + c;
+            if (live && __ldg(p.target + q) - p.col0 == pp) p.at_target[q] = sums[c];
+          }
+          return;
+        }
+        if constexpr (SRC == kGradFew) {
+          if (!live) return;
+#pragma unroll
+          for (int c = 0; c < N; ++c) {
+            if (c >= nq - c0) continue;
+            const long long q = w.q0 + half * HC + c0 + c;
+            const float s = __ldg(p.row_scale + q);
+            float g = exp2_fast((sums[c] - __ldg(p.lse + q)) * kLog2e);
+            if (__ldg(p.target + q) - p.col0 == pp) g -= 1.f;
+            g = s == 0.f ? 0.f : g * s;
+            if (p.bf16)
+              from_f32(static_cast<__nv_bfloat16*>(p.out) + q * p.ldo + pp, g);
+            else
+              from_f32(static_cast<__half*>(p.out) + q * p.ldo + pp, g);
+          }
+          return;
+        }
         if constexpr (SRC == kGrad) {
           const long long a = (long long)pp * p.ldo + w.q0 + half * HC + c0;
           const int t = target < 0 ? -1 : target - c0;
@@ -1170,6 +1221,9 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
       };
       // once all of this warp's columns are written
       auto finish = [&] {
+        if (SRC == kLseFew && lane < min(nq, HC))
+          p.stats[(4ll * (w.p0 / BP) + quarter) * p.T + w.q0 + half * HC + lane] =
+              make_float2(softmax.most, softmax.sum);
         if (SRC != kLse || !live) return;
         p.stats[(2ll * (w.q0 / BQ) + half) * p.P + pp] = make_float2(softmax.most, softmax.sum);
         if (target >= 0) p.at_target[pp] = softmax.at_target;

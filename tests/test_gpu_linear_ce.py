@@ -131,6 +131,24 @@ def test_every_tile(tile):
         check(x, w, target, d, loss, lse, dx, dw)
 
 
+@pytest.mark.parametrize("tile", [(16, 1), (32, 1), (64, 1)])
+def test_few_tokens(tile):
+    """Words on the lanes: every built form, words and tokens that end inside a tile, tiles cut along h."""
+    for t, v, h, dtype in ((1, 70, 3000, torch.bfloat16), (40, 1000, 4000, torch.float16), (64, 20001, 72, torch.bfloat16),
+                           (17, 129, 8, torch.float16)):
+        x, w, target = inputs(t, v, h, dtype)
+        target[0], target[-1] = v - 1, 0
+        d = rand(t, seed=9)
+        try:
+            assert B.sgemm_grouped_set_tile(*tile) == 0
+            loss, lse = B.linear_cross_entropy(x, w, target)
+            assert f"128x{tile[0]}x" in B.sgemm_last_config()
+            dx, dw = B.linear_cross_entropy_grad(x, w, target, lse, d)
+        finally:
+            B.sgemm_grouped_set_tile(0)
+        check(x, w, target, d, loss, lse, dx, dw)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_several_pieces(dtype):
     """G (or FP32 logits) of more than the workspace's share."""
