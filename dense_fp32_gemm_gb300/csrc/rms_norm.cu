@@ -488,13 +488,14 @@ cudaError_t backward(GradArgs a, W* dw, float* partial, int blocks, int sms, cud
                            : norm_grad_kernel<E, W, VW, 4, true>,
                blocks, threads, stream, a);
   } else {
-    if (a.dx != nullptr)
-      e = launch(vec ? norm_grad_kernel<E, W, VW, 4, false> : norm_grad_kernel<E, W, 1, 8, false>,
-                 blocks_of(a.M, threads, sms, 512), threads, stream, a);
-    if (e == cudaSuccess && dw != nullptr) {
+    // (dw's parts first: dx may take the place of what they are made of)
+    if (dw != nullptr) {
       const long long all = (a.N + kColumnThreads - 1ll) / kColumnThreads * blocks;
       e = launch(column_kernel<E>, all < sms * 8ll ? all : sms * 8ll, kColumnThreads, stream, a, blocks);
     }
+    if (e == cudaSuccess && a.dx != nullptr)
+      e = launch(vec ? norm_grad_kernel<E, W, VW, 4, false> : norm_grad_kernel<E, W, 1, 8, false>,
+                 blocks_of(a.M, threads, sms, 512), threads, stream, a);
   }
   if (e == cudaSuccess && dw != nullptr) {
     const long long all = (a.N + 31ll) / 32;
