@@ -279,6 +279,11 @@ struct Problem {
     const long long pieces = (V + (long long)n - 1) / (long long)n;
     return (int)at_most(V, ((V + pieces - 1) / pieces + 255) / 256 * 256);
   }
+  // Tiles of P that are taken side by side: P's rows of them stay in L2 while the
+  // other operand, which may be larger, is read once. (`bytes`: of 256 rows.) With
+  // the words' tiles fastest W was read for each 256 tokens: 2048 tokens x 65536
+  // words x 2048 BF16, loss 395 us, so @@.
+  static int block(size_t bytes) { return std::max(1, (int)((32u << 20) / (bytes + 1))); }
   // Few tokens: words on the lanes, so that W streams through full tiles (10
   // tokens x 8344 words x 2912 F16: the loss in 18 us, with tokens on the lanes 37).
   bool few() const { return !f32() && T <= 64; }
@@ -301,6 +306,7 @@ struct Problem {
     p.chunk = ragged::accumulation_chunk(ragged::k16, SGEMM_TYPE_BF16);
     p.target = target;
     p.col0 = v0;
+    if (!few()) p.p_block = block(512ull * H);
     return p;
   }
   // ... FP32, written as they are
@@ -494,6 +500,7 @@ int backward(const Problem& q, const float* lse, const float* dloss, void* dX, i
     p.K = T;
     p.p_mn = p.q_mn = 1;
     p.bf16 = q.type == SGEMM_TYPE_BF16;
+    p.p_block = Problem::block(256ull * elem * T);
     p.out = static_cast<char*>(dW) + (size_t)v0 * lddw * elem;
     p.ldo = lddw;
     p.out_type = q.type;

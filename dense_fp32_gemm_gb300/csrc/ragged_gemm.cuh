@@ -117,6 +117,9 @@ struct Params {
   int K;                  // contraction length (rows); 0 skips the products
   int p_mn, q_mn;         // operand stored with k as its slow dimension
   int p_shared;           // rows: one P matrix for all groups
+  // one group: tiles of this many rows of tiles in p, side by side, before the next
+  // in q; 0: q fastest
+  int p_block;
   int bf16;               // k16: operand type (else F16; kI8Wide is F16)
   const int* offsets;     // E + 1 row bounds on the device; null: one group of T rows
   void* out;
@@ -308,9 +311,17 @@ struct Walk {
     const int n = sh->rows[u.e];
     const int qdim = p.wgrad ? p.Q : n;
     const int qt = cdiv(qdim, BQ);
-    const int tp = j / qt;     // q fastest: workers running together share weight tiles
+    int tp = j / qt;           // q fastest: workers running together share weight tiles
+    int tq = j - tp * qt;
+    if (p.p_block > 0) {
+      // where Q is larger than L2 it is read once for a block of P, not for each of its tiles
+      const int pt = cdiv(p.P, BP * CL), first = j / (p.p_block * qt) * p.p_block;
+      const int wide = min(p.p_block, pt - first), in = j - first * qt;
+      tq = in / wide;
+      tp = first + in - tq * wide;
+    }
     u.p0 = tp * (BP * CL);
-    u.q0 = (j - tp * qt) * BQ;
+    u.q0 = tq * BQ;
     u.nq = min(BQ, qdim - u.q0);
     u.nn = min(BQ, cdiv(u.nq, 16 * CL) * (16 * CL));
     u.klen = p.K == 0 ? 0 : (p.wgrad ? n : p.K);
