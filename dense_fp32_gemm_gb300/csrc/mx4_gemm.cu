@@ -189,12 +189,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();  // every role sees the abort word
   }
   const int slices = cdiv(p.K, kSliceK), tiles_q = cdiv(p.Q, BQ);
-  const int tiles = cdiv(p.P, BP * CL) * tiles_q;
-  auto unit = [&](int i) {
+  const int tiles_p = cdiv(p.P, BP * CL);
+  // A worker's tiles, q fastest (workers running together share weight tiles), every
+  // `workers`-th: a step is so many tiles of q, and of p, on (divisions between
+  // two tiles of the load loop cost what a slice costs).
+  const int step_p = workers / tiles_q, step_q = workers - step_p * tiles_q;
+  struct At {
+    int p, q;
+  };
+  auto start = [&] {
+    At t;
+    t.p = worker / tiles_q;
+    t.q = worker - t.p * tiles_q;
+    return t;
+  };
+  auto advance = [&](At& t) {
+    t.p += step_p;
+    t.q += step_q;
+    if (t.q >= tiles_q) {
+      t.q -= tiles_q;
+      ++t.p;
+    }
+  };
+  auto unit = [&](const At& t) {
     Unit u;
-    const int tp = i / tiles_q;           // q fastest: workers running together share weight tiles
-    u.p0 = tp * (BP * CL);
-    u.q0 = (i - tp * tiles_q) * BQ;
+    u.p0 = t.p * (BP * CL);
+    u.q0 = t.q * BQ;
     u.nq = min(BQ, p.Q - u.q0);
     u.nn = min(BQ, cdiv(u.nq, 16 * CL) * (16 * CL));
     u.kb = SPLIT ? (int)((long long)slices * part / split) : 0;
@@ -209,8 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ptx::elect_one()) {
       int it = 0;
       bool ok = true;
-      for (int i = worker; ok && i < tiles; i += workers) {
-        const Unit u = unit(i);
+      for (At t = start(); ok && t.p < tiles_p; advance(t)) {
+        const Unit u = unit(t);
         const int p0 = u.p0 + rank * BP, q0 = u.q0 + rank * (u.nn / CL);
         for (int ks = u.kb; ks < u.ke; ++ks, ++it) {
           const int s = it % S;
@@ -270,8 +290,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t b_desc = tc::smem_desc(base_addr + G::kP, 16, 1024, true);
       int it = 0, acc = 0;
       bool ok = true;
-      for (int i = worker; ok && i < tiles; i += workers) {
-        const Unit u = unit(i);
+      for (At t = start(); ok && t.p < tiles_p; advance(t)) {
+        const Unit u = unit(t);
         const uint32_t idesc[2] = {tc::idesc_mx4(BP * CL, u.nn, 0), tc::idesc_mx4(BP * CL, u.nn, 2)};
         for (int k0 = u.kb; k0 < u.ke && ok; k0 += p.chunk, ++acc) {
           const int buf = acc & 1;
@@ -342,8 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     int acc = 0, boxes = 0;
     bool ok = true;
-    for (int i = worker; ok && i < tiles; i += workers) {
-      const Unit u = unit(i);
+    for (At t = start(); ok && t.p < tiles_p; advance(t)) {
+      const Unit u = unit(t);
       const int pp = u.p0 + rank * BP + pr;
       const bool live = pp < p.P;
       // v: this lane's feature of the tile's columns c .. c + CH - 1
@@ -514,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (SPLIT) {
     // every thread of every CTA of the cluster comes here, whoever gave up
     ptx::cluster_sync();
-    const Unit u = unit(worker);
+    const Unit u = unit(start());
     // a warp a column, four features a lane
     for (int c = part + split * warp; c < u.nq; c += split * (kThreads / 32)) {
       const uint32_t at = base_addr + (uint32_t)(c * BP + lane * 4) * 4u;
