@@ -120,6 +120,9 @@ struct Params {
   // one group: tiles of this many rows of tiles in p, side by side, before the next
   // in q; 0: q fastest
   int p_block;
+  // few tiles are cut: those that are left after whole waves, less than a wave (else
+  // one to two waves of them)
+  int cut_rest;
   int bf16;               // k16: operand type (else F16; kI8Wide is F16)
   const int* offsets;     // E + 1 row bounds on the device; null: one group of T rows
   void* out;
@@ -773,7 +776,8 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
           parts = cutters / tiles + 1;
           saved = 16 * (mean - total / cutters);
         }
-        if (saved >= p.cut_once + parts * p.cut_part) dp = max(0, tiles / workers - 1) * workers;
+        if (saved >= p.cut_once + parts * p.cut_part)
+          dp = max(0, tiles / workers - (p.cut_rest ? 0 : 1)) * workers;
       }
       sh->dp = dp;
       int base_pos = total;
