@@ -6,6 +6,12 @@
 // 4 .. 8 units; values are rounded to the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6
 // units (ties to the even code), beyond 6 to 6. Multiplying by a power of two is
 // exact, so the codes are defined bit by bit.
+//
+// Bound by DRAM, the 16-bit form by its instructions (13 a value, 75 % of the issue
+// slots). Measured on GB300: 8192 x 4096 FP32 21.4 us, 7.1 TB/s with a part of it
+// still in L2; BF16 16.2 us, 5.2 TB/s; back to FP32 25.5 us, 6.0 TB/s. (Numbers of
+// the rows by 64-bit divisions, one load at a time: 36, 31 and 31 us.) One row of
+// 4096: 2 us.
 #include <cuda_fp4.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
