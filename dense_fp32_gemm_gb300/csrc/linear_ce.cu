@@ -22,8 +22,8 @@
 // Operations: 2 T V H forward; 6 T V H for the gradients, 2 of which form the
 // logits again (in exchange a piece of G is all that is ever stored). Bound by the
 // tensor cores under the power limit: 4096 tokens x 100003 words x 4096 BF16, loss
-// and gradients in 8.41 ms, 1596 TFLOP/s of all 8 T V H (94 % of a library
-// product's sustained 1706); 2048 x 65536 x 2048, the loss in 349 us, 1580. Small
+// and gradients in 8.5 ms, 1580 TFLOP/s of all 8 T V H (93 % of a library
+// product's sustained 1706); 2048 x 65536 x 2048, the loss in 361 us, 1523. Small
 // ones by latency: 65 x 1000 x 256 F16 in 31 us, six launches of 3 to 7 us. FP32 by
 // the conversions of its products (1000 x 8191 x 777 in 353 us, 317 in products).
 #include <cuda_runtime.h>
@@ -53,6 +53,12 @@ constexpr size_t kPieceBytes = 512u << 20;
 constexpr int kLeastWords = 2048;
 // Statistics of a piece (16 bits): 8 bytes for each token and half tile.
 constexpr size_t kStatsBytes = 256u << 20;
+
+// Values of h per tensor-core accumulation (which truncates) of the logits that the
+// loss, a 32-bit result, is made of: off by 2.7e-7 of itself at 2048 values, 1024
+// at a time 5.6e-7, 256 at a time 1.3e-7 (2048 x 65536 x 2048 361, 348 and 412 us). Those
+// of G, which is rounded to 16 bits, take what 16-bit results take.
+constexpr int kLossChunk = 512;
 
 constexpr float kLeast = -3.402823466e38f;
 constexpr uint32_t kAll = 0xffffffffu;
@@ -302,7 +308,7 @@ struct Problem {
     return few() ? 4 * ragged::cdiv(n, 128) : 2 * ragged::cdiv(n, plan.form->form.bq);
   }
   // logits of n words: 16 bits, reduced or transformed in the epilogue ...
-  Params per_token(int n, int v0) const {
+  Params per_token(int n, int v0, int chunk) const {
     Params p = {};
     p.E = 1;
     p.T = few() ? T : n;
@@ -310,7 +316,7 @@ struct Problem {
     p.K = H;
     p.bf16 = type == SGEMM_TYPE_BF16;
     p.alpha = 1.f;
-    p.chunk = ragged::accumulation_chunk(ragged::k16, SGEMM_TYPE_BF16);
+    p.chunk = chunk;
     p.target = target;
     p.col0 = v0;
     if (!few()) p.p_block = block(512ull * H);
@@ -382,8 +388,8 @@ int forward(const Problem& q, float* loss, float* lse, cudaStream_t stream) {
   if (V > 0) {
     const Operand w = q.words(0, n0);
     st = q.f32()   ? ragged::plan(ragged::kF32, q.type, q.plain(n0, nullptr, ldz), w, x, &first)
-         : q.few() ? ragged::plan(q.lse_source(), q.type, q.per_token(n0, 0), w, x, &first)
-                   : ragged::plan(q.lse_source(), q.type, q.per_token(n0, 0), x, w, &first);
+         : q.few() ? ragged::plan(q.lse_source(), q.type, q.per_token(n0, 0, kLossChunk), w, x, &first)
+                   : ragged::plan(q.lse_source(), q.type, q.per_token(n0, 0, kLossChunk), x, w, &first);
     if (st != SGEMM_OK) return st;
   }
   float* base = nullptr;
@@ -413,7 +419,7 @@ int forward(const Problem& q, float* loss, float* lse, cudaStream_t stream) {
   do {
     const int m = (int)at_most(n, V - v0);
     if (m > 0) {
-      Params p = q.f32() ? q.plain(m, z, ldz) : q.per_token(m, v0);
+      Params p = q.f32() ? q.plain(m, z, ldz) : q.per_token(m, v0, kLossChunk);
       p.status = status;
       p.counters = counters;
       p.stats = stats;
@@ -474,7 +480,7 @@ int backward(const Problem& q, const float* lse, const float* dloss, void* dX, i
   if (copy_x) copied(&x);
   if (copy_w) copied(&w0);
   auto gradient = [&](int m, int v0, void* g) {
-    Params p = q.f32() ? q.plain(m, static_cast<float*>(g), ldg) : q.per_token(m, v0);
+    Params p = q.f32() ? q.plain(m, static_cast<float*>(g), ldg) : q.per_token(m, v0, ragged::accumulation_chunk(ragged::k16, q.type));
     p.out = g;
     p.ldo = ldg;
     return p;

@@ -318,8 +318,8 @@ struct Walk {
     int tq = j - tp * qt;
     if (p.p_block > 0) {
       // where Q is larger than L2 it is read once for a block of P, not for each of its tiles
-      const int pt = cdiv(p.P, BP * CL), first = j / (p.p_block * qt) * p.p_block;
-      const int wide = min(p.p_block, pt - first), in = j - first * qt;
+      const int pt = cdiv(p.P, BP * CL), block = min(p.p_block, pt);
+      const int first = j / (block * qt) * block, wide = min(block, pt - first), in = j - first * qt;
       tq = in / wide;
       tp = first + in - tq * wide;
     }

@@ -6,6 +6,8 @@ derivatives of any order come out. The norm and the loss of the output end have
 first derivatives; asking for a second raises."""
 from __future__ import annotations
 
+import math
+
 import torch
 from torch.autograd.function import once_differentiable
 
@@ -62,6 +64,11 @@ def expert_linear(x, weight, offsets):
     return _Rows.apply(x, weight, offsets, "T")
 
 
+def _rows(x):
+    """x as a matrix of its last dimension's rows (none of them may be there)."""
+    return x.reshape(math.prod(x.shape[:-1]), x.shape[-1])
+
+
 class _Norm(torch.autograd.Function):
     """(y, h) of binding.rms_norm on rows."""
 
@@ -92,7 +99,7 @@ def rms_norm(x, weight, residual=None, eps=1e-6):
     """h / sqrt(mean(h^2) + eps) * weight over the last dimension, h = x +
     residual; with a residual (y, h) is returned. Differentiable once in x,
     weight and residual."""
-    rows = x.reshape(-1, x.shape[-1])
+    rows = _rows(x)
     if residual is None:
         return _Norm.apply(rows, weight, None, eps).view(x.shape)
     if residual.shape != x.shape:
@@ -131,7 +138,7 @@ def linear_cross_entropy(x, weight, target, ignore_index=-100, reduction="mean")
         raise ValueError('reduction must be "mean", "sum" or "none"')
     if target.shape != x.shape[:-1]:
         raise ValueError("target must have the leading dimensions of x")
-    loss = _CrossEntropy.apply(x.reshape(-1, x.shape[-1]), weight, target.reshape(-1).contiguous(), ignore_index)
+    loss = _CrossEntropy.apply(_rows(x), weight, target.reshape(-1).contiguous(), ignore_index)
     if reduction == "none":
         return loss.view(target.shape)
     if reduction == "sum":

@@ -673,7 +673,7 @@ int sgemm_rms_norm_grad(int M, int N, int type, const void* dY, int lddy, const 
  * ignore_index, and NaN where it is neither that nor in 0 .. V - 1. lse (may be
  * NULL) is written for every row. Both are FP32, and so are the logits and the
  * sums: 16-bit operands are multiplied exactly and leave the tensor cores every
- * 1024 products, FP32 ones as in sgemm_grouped(). Logits of -infinity have no
+ * 512 products, FP32 ones as in sgemm_grouped(). Logits of -infinity have no
  * share; a NaN or +infinity among a row's makes its loss NaN.
  * The vocabulary is taken in pieces, so that the workspace stays below 256 MB
  * beside the products' own (FP32: 512 MB), or the statistics (logits) of 2048

@@ -267,6 +267,19 @@ def test_captured():
         assert all(torch.equal(c, want) for _, c in graphs)
 
 
+def test_capture_needs_the_workspace():
+    ops, x = product(8, 100, 64, torch.bfloat16), rand(8, 64)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(B.SgemmError) as e:
+        with torch.cuda.graph(graph, stream=side):
+            B.mx4_quantize(x)                             # (has no need of one)
+            B.mx4_gemm(*ops)
+    assert e.value.status == B.SGEMM_ERR_CAPTURE
+    torch.cuda.synchronize()
+
+
 def test_norm_into_the_4_bit_product():
     """A layer as it is served: norm, 4 bits, product."""
     x, r = rand(50, 640).bfloat16(), rand(50, 640, seed=1).bfloat16()

@@ -87,6 +87,21 @@ def test_captured_training_step():
         assert all(torch.equal(a, b) for a, b in zip(out[2], want[2]))
 
 
+def test_layers_without_rows_or_columns():
+    w = torch.ones(0, device="cuda", requires_grad=True)
+    assert layers.rms_norm(torch.zeros(2, 3, 0, device="cuda"), w).shape == (2, 3, 0)
+    x = torch.zeros(0, 4, 8, device="cuda", requires_grad=True)
+    w = torch.ones(8, device="cuda", requires_grad=True)
+    y, h = layers.rms_norm(x, w, residual=torch.zeros(0, 4, 8, device="cuda"))
+    words = rand(5, 8).requires_grad_()
+    loss = layers.linear_cross_entropy(y, words, torch.zeros(0, 4, dtype=torch.int64, device="cuda"))
+    assert float(loss.detach()) == 0.0
+    for g in torch.autograd.grad(loss, [x, w, words]):
+        assert not bool(g.any())
+    one = layers.rms_norm(rand(8), w)                      # a single row, without leading dimensions
+    assert one.shape == (8,)
+
+
 ROUNDS = 60
 
 
