@@ -232,7 +232,7 @@ bool misaligned(const void* p, int bytes) {
 }
 
 // The built kernels, and per device what prepare() said of each.
-constexpr int kMaxDevices = 64, kMaxForms = 40;
+constexpr int kMaxDevices = 64, kMaxForms = 48;
 struct Built {
   bool ready;
   int workers;
@@ -249,7 +249,9 @@ const FormEntry* form_entry(int i) {
   i -= kNumFormsF32;
   if (i < kNumFormsI8) return &kFormsI8[i];
   i -= kNumFormsI8;
-  return i < kNumFormsLoss ? &kFormsLoss[i] : nullptr;
+  if (i < kNumFormsLoss) return &kFormsLoss[i];
+  i -= kNumFormsLoss;
+  return i < kNumFormsDense ? &kFormsDense[i] : nullptr;
 }
 
 // The entry of a form and its resident workers on `dev` (null: not built or,
@@ -289,11 +291,12 @@ constexpr TileCost kTileCosts[] = {
     {kI8Wide, 256, 2, 364, 2500},
 };
 // Integers that have been widened cost what F16 operands do, and so do the
-// products of a loss (with tokens on the lanes built from 64 columns on, else up
-// to 64).
+// products of a loss (its logits with tokens on the lanes are built from 64 columns
+// on, else up to 64).
 bool loss(int src) { return src >= kLse; }
 bool built(int src, int bq) {
-  return src == kLse || src == kGrad ? bq >= 64 : !loss(src) || bq <= 64;
+  if (src == kLse || src == kGrad) return bq >= 64;
+  return (src != kLseFew && src != kGradFew) || bq <= 64;
 }
 int cost_source(int src) { return src == kI8Wide || loss(src) ? k16 : src; }
 // The costs of a form: those of its own number of CTAs.

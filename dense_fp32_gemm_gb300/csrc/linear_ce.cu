@@ -15,9 +15,9 @@
 // G in 16 bits: each of its values is off by half a unit, some 2^-9 (BF16) or
 // 2^-12 of it, as if the operands of the two products had been rounded, which
 // they are; in dX and dW these errors add up as random ones do. So that small
-// gradients keep their bits in F16, rows are scaled by d / max|d|, times 2^14 in
-// F16 (values up to 2^14; a probability of 10^-5 is a normal number), and the
-// products by the inverse.
+// gradients keep their bits, rows are scaled by d / max|d|, times 2^14 in F16 (values
+// up to 2^14; a probability of 10^-5 is a normal number), and the products by the
+// inverse.
 //
 // Operations: 2 T V H forward; 6 T V H for the gradients, 2 of which form the
 // logits again (in exchange a piece of G is all that is ever stored). Bound by the
@@ -126,12 +126,12 @@ __global__ void __launch_bounds__(32 * kGroups) join_kernel(const Join a) {
 }
 
 // Factors of the tokens' gradients: d / c * unit, c the largest |d| (1 where
-// that is 0 or no number), and c / unit, the factor of the products. 0 for a
-// token that is not counted, NaN for one whose target is no word. One block.
+// that is 0 or no number, and in FP32), and c / unit, the factor of the products. 0
+// for a token that is not counted, NaN for one whose target is no word. One block.
 constexpr int kScaleThreads = 1024;
 __global__ void __launch_bounds__(kScaleThreads)
     scale_kernel(int T, int V, const long long* target, long long ignore, const float* d,
-                 float unit, float* row_scale, float* alpha) {
+                 int scaled, float unit, float* row_scale, float* alpha) {
   __shared__ float part[kScaleThreads / 32];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kScaleThreads)
   __syncthreads();
   most = 0.f;
   for (int i = 0; i < kScaleThreads / 32; ++i) most = fmaxf(most, part[i]);
-  const float c = most > 0.f && most <= 3e38f ? most : 1.f;
+  const float c = scaled && most > 0.f && most <= 3e38f ? most : 1.f;
   for (long long t = threadIdx.x; t < T; t += kScaleThreads) {
     const long long word = target[t];
     row_scale[t] = word == ignore              ? 0.f
@@ -472,7 +472,7 @@ int backward(const Problem& q, const float* lse, const float* dloss, void* dX, i
   const size_t at_x = ws.take(copy_x ? x.packed_bytes(false) : 0);
   const size_t at_w = ws.take(copy_w ? w0.packed_bytes(false) : 0);
 
-  const int src = q.f32() ? ragged::kF32 : ragged::k16;
+  const int src = q.f32() ? ragged::kF32 : ragged::kDense;
   auto copied = [&](Operand* a) {          // as pack_operands() will describe it
     a->ptr = reinterpret_cast<void*>(256);
     a->ld = a->packed_pitch(false) / a->elem;
@@ -562,7 +562,7 @@ int backward(const Problem& q, const float* lse, const float* dloss, void* dX, i
   char* rest = at + ws.used;
 
   st = done(start(scale_kernel, 1, kScaleThreads, stream, T, V, q.target, q.ignore, dloss,
-                  q.type == SGEMM_TYPE_F16 ? 16384.f : 1.f, row_scale, alpha));
+                  (int)!q.f32(), q.type == SGEMM_TYPE_F16 ? 16384.f : 1.f, row_scale, alpha));
   if (st != SGEMM_OK) return st;
   for (int v0 = 0; v0 < V; v0 += n) {
     const int m = (int)at_most(n, V - v0);
@@ -597,13 +597,13 @@ int backward(const Problem& q, const float* lse, const float* dloss, void* dX, i
     if (st != SGEMM_OK) return st;
     if (dX != nullptr) {
       p = with(input(m, v0, acc));
-      p.alpha_dev = alpha;
+      p.alpha_dev = q.f32() ? nullptr : alpha;
       st = ragged::launch(plans[1], p, w, g_of(g, m), rest, stream, "linear_ce_dx");
       if (st != SGEMM_OK) return st;
     }
     if (dW != nullptr) {
       p = with(weight(m, v0));
-      p.alpha_dev = alpha;
+      p.alpha_dev = q.f32() ? nullptr : alpha;
       st = ragged::launch(plans[2], p, x, g_of(g, m), rest, stream, "linear_ce_dw");
       if (st != SGEMM_OK) return st;
     }

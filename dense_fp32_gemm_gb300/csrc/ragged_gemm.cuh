@@ -29,7 +29,10 @@
 //         the sum of exponentials, and kGrad writes the loss's gradient;
 //   kLseFew, kGradFew  the same for few tokens, p = word and q = token as in a
 //         plain product, so that the vocabulary streams through full tiles; the
-//         sums of a token go over the lanes of a warp.
+//         sums of a token go over the lanes of a warp;
+//   kDense  as k16 of one group, for the products with that gradient: an order of
+//         tiles and a factor on the device that the others do without (in the
+//         kernels of grouped products the branches cost 0.2 us a launch).
 //
 // Accumulation. The tensor core adds into FP32 with truncation, an error that
 // grows with the number of instructions. A tile's sum is therefore cut into
@@ -96,7 +99,8 @@
 namespace sgemm_gb300 {
 namespace ragged {
 
-enum Src : int { k16 = 0, kF32 = 1, kI8 = 2, kI8Wide = 3, kLse = 4, kGrad = 5, kLseFew = 6, kGradFew = 7 };
+enum Src : int { k16 = 0, kF32 = 1, kI8 = 2, kI8Wide = 3, kLse = 4, kGrad = 5, kLseFew = 6, kGradFew = 7,
+                 kDense = 8 };
 enum OutType : int { kOutF32 = 0, kOutBf16 = 1, kOutF16 = 2 };
 
 constexpr int BP = 128;            // tile height in p (MMA M)
@@ -117,11 +121,11 @@ struct Params {
   int K;                  // contraction length (rows); 0 skips the products
   int p_mn, q_mn;         // operand stored with k as its slow dimension
   int p_shared;           // rows: one P matrix for all groups
-  // one group: tiles of this many rows of tiles in p, side by side, before the next
-  // in q; 0: q fastest
+  // loss, kDense: tiles of this many rows of tiles in p, side by side, before the
+  // next in q; 0: q fastest
   int p_block;
-  // few tiles are cut: those that are left after whole waves, less than a wave (else
-  // one to two waves of them)
+  // kDense: few tiles are cut, those that are left after whole waves, less than a
+  // wave (else one to two waves of them)
   int cut_rest;
   int bf16;               // k16: operand type (else F16; kI8Wide is F16)
   const int* offsets;     // E + 1 row bounds on the device; null: one group of T rows
@@ -129,7 +133,7 @@ struct Params {
   long long ldo, stride_o;  // row pitch; pitch between the groups' outputs (wgrad)
   int out_type;
   float alpha, beta;
-  const float* alpha_dev; // rows, wgrad: a factor of alpha on the device; may be null
+  const float* alpha_dev; // kDense: a factor of alpha on the device; may be null
   const float* scale_p;   // kI8: scales of p and q
   const float* scale_q;
   // loss: the first of the product's words is number col0 of the vocabulary
@@ -259,7 +263,7 @@ struct Unit {
 };
 
 // Walks the list of worker w of `workers`; every role walks its own copy.
-template <int SLICE, int BQ, int CL>
+template <int SLICE, int BQ, int CL, bool ONE>
 struct Walk {
   const Params& p;
   const Shared* sh;
@@ -316,7 +320,7 @@ struct Walk {
     const int qt = cdiv(qdim, BQ);
     int tp = j / qt;           // q fastest: workers running together share weight tiles
     int tq = j - tp * qt;
-    if (p.p_block > 0) {
+    if (ONE && p.p_block > 0) {
       // where Q is larger than L2 it is read once for a block of P, not for each of its tiles
       const int pt = cdiv(p.P, BP * CL), block = min(p.p_block, pt);
       const int first = j / (block * qt) * block, wide = min(block, pt - first), in = j - first * qt;
@@ -535,7 +539,7 @@ __device__ __forceinline__ float exp2_fast(float v) {
 
 // kLse: a token's logits, some columns at a time. The sum is of exp(logit -
 // most); most is a number whatever the logits are, so columns of -infinity add
-// nothing and a NaN or +infinity among them makes the sum NaN or infinite.
+// nothing; a NaN or +infinity among them makes the sum NaN.
 constexpr float kLeast = -3.402823466e38f;
 struct Softmax {
   float most = kLeast, sum = 0.f, at_target = 0.f;
@@ -647,7 +651,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
     ragged_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap mapP,
                   const __grid_constant__ CUtensorMap mapQ) {
   using G = Geo<SRC, BQ, CL>;
-  using List = Walk<G::kSlice, BQ, CL>;
+  using List = Walk<G::kSlice, BQ, CL, (SRC >= kLse)>;
   constexpr int SL = G::kSlice;
   constexpr int RS = G::kRawStages, RB = G::kRawBars, OS = G::kConv ? G::kOpStages : RS;
   constexpr bool kPair = CL == 2, kLoss = SRC == kLse || SRC == kGrad;
@@ -777,7 +781,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
           saved = 16 * (mean - total / cutters);
         }
         if (saved >= p.cut_once + parts * p.cut_part)
-          dp = max(0, tiles / workers - (p.cut_rest ? 0 : 1)) * workers;
+          dp = max(0, tiles / workers - (SRC == kDense && p.cut_rest ? 0 : 1)) * workers;
       }
       sh->dp = dp;
       int base_pos = total;
@@ -1157,7 +1161,7 @@ __global__ void __launch_bounds__(Geo<SRC, BQ, CL>::kThreads, 1)
       const int pp = w.p0 + rank * BP + pr;
       const bool live = pp < p.P;
       const float sp = G::kInt ? (live ? p.scale_p[pp] : 0.f)
-                               : (p.alpha_dev == nullptr ? p.alpha : p.alpha * __ldg(p.alpha_dev));
+                               : (SRC == kDense && p.alpha_dev != nullptr ? p.alpha * __ldg(p.alpha_dev) : p.alpha);
       const long long row = (long long)(p.wgrad ? 0 : w.row0) + w.q0 + half * HC;
       const long long at = (p.wgrad ? (long long)w.e * p.stride_o : 0ll) + row * p.ldo + pp;
       // kLse, kGrad: the target's column among this warp's (any other value: not there)

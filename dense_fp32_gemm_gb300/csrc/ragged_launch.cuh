@@ -67,8 +67,8 @@ struct FormEntry {
   cudaError_t (*launch)(int workers, const Params& p, const CUtensorMap& mp, const CUtensorMap& mq,
                         cudaStream_t stream);
 };
-extern const FormEntry kForms16[], kFormsF32[], kFormsI8[], kFormsLoss[];
-extern const int kNumForms16, kNumFormsF32, kNumFormsI8, kNumFormsLoss;
+extern const FormEntry kForms16[], kFormsF32[], kFormsI8[], kFormsLoss[], kFormsDense[];
+extern const int kNumForms16, kNumFormsF32, kNumFormsI8, kNumFormsLoss, kNumFormsDense;
 
 // A call of the kernel, decided but not launched (grouped.cu): its form, and
 // what it takes of the workspace, in bytes.
