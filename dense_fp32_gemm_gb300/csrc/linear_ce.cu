@@ -295,7 +295,7 @@ struct Problem {
   // Tiles of P that are taken side by side: P's rows of them stay in L2 while the
   // other operand, which may be larger, is read once. (`bytes`: of 256 rows.) With
   // the words' tiles fastest W was read for each 256 tokens: 2048 tokens x 65536
-  // words x 2048 BF16, loss 417 us, so 349.
+  // words x 2048 BF16, loss 417 us, so 349 (both in sums of 1024).
   static int block(size_t bytes) { return std::max(1, (int)((32u << 20) / (bytes + 1))); }
   // Few tokens: words on the lanes, so that W streams through full tiles (10
   // tokens x 8344 words x 2912 F16: the loss in 18 us, with tokens on the lanes 37).
@@ -564,8 +564,8 @@ int backward(const Problem& q, const float* lse, const float* dloss, void* dX, i
   st = done(start(scale_kernel, 1, kScaleThreads, stream, T, V, q.target, q.ignore, dloss,
                   (int)!q.f32(), q.type == SGEMM_TYPE_F16 ? 16384.f : 1.f, row_scale, alpha));
   if (st != SGEMM_OK) return st;
-  for (int v0 = 0; v0 < V; v0 += n) {
-    const int m = (int)at_most(n, V - v0);
+  for (long long at_word = 0; at_word < V; at_word += n) {   // (steps past 2^31 at the end)
+    const int v0 = (int)at_word, m = (int)at_most(n, V - at_word);
     auto with = [&](Params p) {
       p.status = status;
       p.counters = counters;

@@ -751,7 +751,9 @@ int run(int M, int N, int K, const void* A, int lda, const void* SA, const void*
       !encode_scales(&msp, SB, N, tiles_k, 1) || !encode_scales(&msq, SA, M, tiles_k, (f.bq + 127) / 128))
     return SGEMM_ERR_LAUNCH;
   const int elem = out_type == SGEMM_TYPE_F32 ? 4 : 2;
-  p.tma_out = (reinterpret_cast<uintptr_t>(C) & 15u) == 0 && (long long)ldc * elem % 16 == 0;
+  // (narrow tiles and cut ones are written by their threads)
+  p.tma_out = f.bq >= 128 && c.split == 1 && (reinterpret_cast<uintptr_t>(C) & 15u) == 0 &&
+              (long long)ldc * elem % 16 == 0;
   if (p.tma_out && !encode_out(&mo, C, out_type, N, M, (long long)ldc * elem)) return SGEMM_ERR_LAUNCH;
   const int grid = c.split > 1 ? (int)tiles * c.split : (int)std::min<long long>(workers, tiles) * f.cl;
   cudaLaunchAttribute la[2];

@@ -117,6 +117,43 @@ __device__ __forceinline__ void quotients(const float (&u)[VW], float step, floa
   }
 }
 
+// What a row's integers are divided by.
+struct Step {
+  float step, inv;     // 1 / step, where that is a number to multiply by (else no number)
+  bool none;           // a row of zeros, or with no numbers: its integers are 0
+};
+__device__ __forceinline__ Step step_of(uint32_t most) {
+  Step s;
+  s.step = __fdiv_rn(__uint_as_float(most), 127.f);
+  s.inv = s.step > 1e-37f ? __frcp_rn(s.step) : __uint_as_float(0x7fc00000u);
+  s.none = !(s.step > 0.f && s.step <= 3e38f);
+  return s;
+}
+
+// The integers of a piece; `wide`: q is aligned to as many bytes.
+template <int VW>
+__device__ __forceinline__ void put_quotients(const float (&u)[VW], const Step& s, signed char* q,
+                                              int wide) {
+  uint32_t b[VW];
+#pragma unroll
+  for (int j = 0; j < VW; ++j) b[j] = 0u;
+  if (!s.none) quotients<VW>(u, s.step, s.inv, b);
+  if (VW > 1 && wide) {
+    uint32_t o[VW / 4 > 0 ? VW / 4 : 1];
+#pragma unroll
+    for (int j = 0; j < VW / 4; ++j)
+      o[j] = __byte_perm(__byte_perm(b[4 * j], b[4 * j + 1], 0x0040),
+                         __byte_perm(b[4 * j + 2], b[4 * j + 3], 0x0040), 0x5410);
+    if constexpr (VW == 8)
+      *reinterpret_cast<uint2*>(q) = make_uint2(o[0], o[1]);
+    else
+      *reinterpret_cast<uint32_t*>(q) = o[0];
+  } else {
+#pragma unroll
+    for (int j = 0; j < VW; ++j) q[j] = (signed char)(b[j] & 0xffu);
+  }
+}
+
 // A row per block, in pieces of VW elements (16 bytes, or one element where
 // something is not aligned). Up to HELD pieces a thread stay in registers between
 // the pass that sums and the pass that writes, and those of the block's next row
@@ -223,37 +260,16 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a) {
         store<E, VW>(y + c, pack<E, VW>(f));
       });
     } else {
-      const float step = __fdiv_rn(__uint_as_float(t.most), 127.f);
-      // (1 / step has to be a number: else every value is divided)
-      const float inv = step > 1e-37f ? __frcp_rn(step) : __uint_as_float(0x7fc00000u);
-      const bool none = !(step > 0.f && step <= 3e38f);   // zeros, or no numbers
-      if (threadIdx.x == 0) a.scale[m] = step * rstd;
+      const Step step = step_of(t.most);
+      if (threadIdx.x == 0) a.scale[m] = step.step * rstd;
       signed char* q = static_cast<signed char*>(a.y) + m * a.ldy;
       each([&](const Piece<E, VW>& p, unsigned c) {
         float u[VW], f[VW];
         load_vector<W, VW>(w + c, u);
         unpack(p, f);
-        uint32_t b[VW];
 #pragma unroll
-        for (int j = 0; j < VW; ++j) {
-          u[j] *= f[j];
-          b[j] = 0u;
-        }
-        if (!none) quotients<VW>(u, step, inv, b);
-        if (VW > 1 && a.wide_q) {
-          uint32_t o[VW / 4 > 0 ? VW / 4 : 1];
-#pragma unroll
-          for (int j = 0; j < VW / 4; ++j)
-            o[j] = __byte_perm(__byte_perm(b[4 * j], b[4 * j + 1], 0x0040),
-                               __byte_perm(b[4 * j + 2], b[4 * j + 3], 0x0040), 0x5410);
-          if constexpr (VW == 8)
-            *reinterpret_cast<uint2*>(q + c) = make_uint2(o[0], o[1]);
-          else
-            *reinterpret_cast<uint32_t*>(q + c) = o[0];
-        } else {
-#pragma unroll
-          for (int j = 0; j < VW; ++j) q[c + j] = (signed char)(b[j] & 0xffu);
-        }
+        for (int j = 0; j < VW; ++j) u[j] *= f[j];
+        put_quotients<VW>(u, step, q + c, a.wide_q);
       });
     }
   }
@@ -386,6 +402,133 @@ __global__ void __launch_bounds__(HELD == 2 ? 256 : kMaxThreads, HELD == 2 ? 2 :
   }
 }
 
+// Short rows, of at most 32 pieces of 16 bytes: a row is one piece each of `lanes`
+// (8, 16 or 32) neighbouring threads, and its sums go over them alone. (1048576
+// rows of 128 BF16: 104 us, back 160, of 79 and 118 that the bytes take; by a block
+// a row 326 and 336. 8192 rows of 64: 1.9 and 4.0 us instead of 4.4 and 11.5.)
+constexpr int kSmallThreads = 256;
+__device__ __forceinline__ float sum_over(float v, int lanes) {
+  for (int d = lanes >> 1; d > 0; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+  return v;
+}
+template <typename E, typename W, int VW, bool I8>
+__global__ void __launch_bounds__(kSmallThreads) small_norm_kernel(const NormArgs a, int lanes) {
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const int rows = kSmallThreads / lanes, l = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes;
+  const int c = l * VW;
+  const float inv_n = 1.f / (float)a.N;
+  float w[VW];
+#pragma unroll
+  for (int j = 0; j < VW; ++j) w[j] = 0.f;
+  if (c < a.N) load_vector<W, VW>(static_cast<const W*>(a.w) + c, w);
+  // (the same number of steps for every thread: they exchange sums)
+  for (long long m0 = (long long)blockIdx.x * rows; m0 < a.M; m0 += (long long)gridDim.x * rows) {
+    const long long m = m0 + group;
+    const bool live = m < a.M && c < a.N;
+    float f[VW], u[VW];
+#pragma unroll
+    for (int j = 0; j < VW; ++j) f[j] = 0.f;
+    if (live) {
+      Piece<E, VW> p = load<E, VW>(static_cast<const E*>(a.x) + m * a.ldx + c);
+      unpack(p, f);
+      if (a.r != nullptr) {
+        unpack(load<E, VW>(static_cast<const E*>(a.r) + m * a.ldr + c), u);
+#pragma unroll
+        for (int j = 0; j < VW; ++j) f[j] += u[j];
+        p = pack<E, VW>(f);
+        unpack(p, f);
+        store<E, VW>(static_cast<E*>(a.h) + m * a.ldh + c, p);
+      }
+    }
+    float sum = 0.f;
+    uint32_t most = 0;
+#pragma unroll
+    for (int j = 0; j < VW; ++j) {
+      sum = fmaf(f[j], f[j], sum);
+      u[j] = f[j] * w[j];
+      if (I8 && live) most = max(most, __float_as_uint(u[j]) & 0x7fffffffu);
+    }
+    sum = sum_over(sum, lanes);
+    if (I8)
+      for (int d = lanes >> 1; d > 0; d >>= 1) most = max(most, __shfl_xor_sync(kAll, most, d));
+    // (squares beyond FP32's range: as in norm_kernel)
+    float down = 1.f;
+    if (__any_sync(kAll, !(sum <= 3e38f))) {
+      float scaled = 0.f;
+#pragma unroll
+      for (int j = 0; j < VW; ++j) scaled = fmaf(f[j] * 0x1p-70f, f[j] * 0x1p-70f, scaled);
+      scaled = sum_over(scaled, lanes);
+      if (!(sum <= 3e38f)) {
+        sum = scaled;
+        down = 0x1p-70f;
+      }
+    }
+    const float rstd = rsqrtf(sum * inv_n + a.eps * down * down) * down;
+    if (m < a.M && l == 0 && a.rstd != nullptr) a.rstd[m] = rstd;
+    if (!I8) {
+      if (!live) continue;
+#pragma unroll
+      for (int j = 0; j < VW; ++j) f[j] = f[j] * rstd * w[j];
+      store<E, VW>(static_cast<E*>(a.y) + m * a.ldy + c, pack<E, VW>(f));
+    } else {
+      const Step step = step_of(most);
+      if (m < a.M && l == 0) a.scale[m] = step.step * rstd;
+      if (!live) continue;
+      put_quotients<VW>(u, step, static_cast<signed char*>(a.y) + m * a.ldy + c, a.wide_q);
+    }
+  }
+}
+
+template <typename E, typename W, int VW>
+__global__ void __launch_bounds__(kSmallThreads) small_grad_kernel(const GradArgs a, int lanes) {
+  __shared__ float part[kSmallThreads][VW + 1];
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const int rows = kSmallThreads / lanes, l = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes;
+  const int c = l * VW;
+  const float inv_n = 1.f / (float)a.N;
+  float w[VW], dw[VW];
+#pragma unroll
+  for (int j = 0; j < VW; ++j) w[j] = dw[j] = 0.f;
+  if (c < a.N) load_vector<W, VW>(static_cast<const W*>(a.w) + c, w);
+  for (long long m0 = (long long)blockIdx.x * rows; m0 < a.M; m0 += (long long)gridDim.x * rows) {
+    const long long m = m0 + group;
+    const bool live = m < a.M && c < a.N;
+    float g[VW], n[VW], d[VW], sum = 0.f, rstd = 0.f;
+#pragma unroll
+    for (int j = 0; j < VW; ++j) g[j] = n[j] = d[j] = 0.f;
+    if (live) {
+      rstd = a.rstd[m];
+      unpack(load<E, VW>(static_cast<const E*>(a.dy) + m * a.lddy + c), g);
+      unpack(load<E, VW>(static_cast<const E*>(a.h) + m * a.ldh + c), n);
+      if (a.dh != nullptr) unpack(load<E, VW>(static_cast<const E*>(a.dh) + m * a.lddh + c), d);
+#pragma unroll
+      for (int j = 0; j < VW; ++j) {
+        n[j] *= rstd;
+        dw[j] = fmaf(g[j], n[j], dw[j]);
+        g[j] *= w[j];
+        sum = fmaf(g[j], n[j], sum);
+      }
+    }
+    if (a.dx == nullptr) continue;
+    const float mean = sum_over(sum, lanes) * inv_n;
+    if (!live) continue;
+#pragma unroll
+    for (int j = 0; j < VW; ++j) g[j] = rstd * fmaf(-mean, n[j], g[j]) + d[j];
+    store<E, VW>(static_cast<E*>(a.dx) + m * a.lddx + c, pack<E, VW>(g));
+  }
+  if (a.partial == nullptr) return;
+#pragma unroll
+  for (int j = 0; j < VW; ++j) part[threadIdx.x][j] = dw[j];
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.N; i += kSmallThreads) {
+    float sum = 0.f;
+    for (int r = 0; r < rows; ++r) sum += part[r * lanes + i / VW][i % VW];
+    a.partial[(long long)blockIdx.x * a.N + i] = sum;
+  }
+}
+
 // Rows too long for registers: dw's parts a column a thread, over the rows of a
 // slab (slab s has the rows s, s + slabs, ...).
 constexpr int kColumnThreads = 256;
@@ -463,6 +606,14 @@ int blocks_of(int M, int threads, int sms, int threads_per_sm) {
   return M < fit ? M : fit;
 }
 
+// Threads of a short row, and blocks of such rows.
+int small_lanes(long long pieces) { return pieces <= 8 ? 8 : (pieces <= 16 ? 16 : 32); }
+int small_blocks(int M, int lanes, int sms) {
+  const int rows = kSmallThreads / lanes;
+  const long long blocks = (M + rows - 1ll) / rows;
+  return (int)(blocks < sms * 6ll ? blocks : sms * 6ll);
+}
+
 bool aligned(const void* p, long long ld, int elem, int bytes) {
   return p == nullptr ||
          ((reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0 && ld * elem % bytes == 0);
@@ -477,20 +628,28 @@ cudaError_t forward(NormArgs a, int sms, cudaStream_t stream) {
   a.wide_q = I8 && aligned(a.y, a.ldy, 1, VW);
   const bool few = a.M < 2 * sms;
   const long long pieces = vec ? a.N / VW : a.N;
+  if (vec && pieces <= 32) {
+    const int lanes = small_lanes(pieces);
+    return launch(small_norm_kernel<E, W, VW, I8>, small_blocks(a.M, lanes, sms), kSmallThreads,
+                  stream, a, lanes);
+  }
   const int t = threads_of(pieces, held_of(vec ? VW : 1), few);
   return launch(vec ? norm_kernel<E, W, VW, I8> : norm_kernel<E, W, 1, I8>,
                 blocks_of(a.M, t, sms, 512), t, stream, a);
 }
 
 // `blocks` make a part of dw each: of norm_grad_kernel where a row is `held` (in so
-// many pieces a thread), else (0) slabs of column_kernel.
+// many pieces a thread; 1: short rows of `threads` lanes), else (0) slabs of
+// column_kernel.
 template <typename E, typename W>
 cudaError_t backward(GradArgs a, W* dw, float* partial, int blocks, int sms, cudaStream_t stream,
                      int threads, bool vec, int held) {
   constexpr int VW = 16 / (int)sizeof(E);
   a.partial = partial;
   cudaError_t e = cudaSuccess;
-  if (held != 0) {
+  if (held == 1) {
+    e = launch(small_grad_kernel<E, W, VW>, blocks, kSmallThreads, stream, a, threads);
+  } else if (held != 0) {
     e = launch(!vec         ? norm_grad_kernel<E, W, 1, 8, true>
                : held == 2 ? norm_grad_kernel<E, W, VW, 2, true>
                            : norm_grad_kernel<E, W, VW, 4, true>,
@@ -677,11 +836,14 @@ SGEMM_API int sgemm_rms_norm_grad(int M, int N, int type, const void* dY, int ld
                    rows::aligned(weight, 0, wb, 16) && N % vw == 0;
   const long long pieces = vec ? N / vw : N;
   const int held = pieces > rows::held_of(vec ? vw : 1) * rows::kMaxThreads ? 0
-                   : vec ? (pieces <= 512 ? 2 : 4) : 8;
-  const int threads = held == 2 ? rows::threads_of(pieces, 2, false)
-                                : rows::threads_of(pieces, rows::held_of(vec ? vw : 1), M < 2 * sms);
+                   : vec ? (pieces <= 32 ? 1 : (pieces <= 512 ? 2 : 4)) : 8;
+  const int threads = held == 1   ? rows::small_lanes(pieces)
+                      : held == 2 ? rows::threads_of(pieces, 2, false)
+                                  : rows::threads_of(pieces, rows::held_of(vec ? vw : 1), M < 2 * sms);
   int blocks = 0;
-  if (held != 0) {
+  if (held == 1) {
+    blocks = rows::small_blocks(M, threads, sms);
+  } else if (held != 0) {
     blocks = rows::blocks_of(M, threads, sms, 512);
   } else {
     const int fill = sms * 8 / (int)((N + rows::kColumnThreads - 1ll) / rows::kColumnThreads) + 1;

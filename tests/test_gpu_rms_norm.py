@@ -52,7 +52,7 @@ def close(got, want, slack):
 
 
 SIZES = [(1, 1), (1, 4096), (3, 7), (5, 64), (133, 1001), (300, 4096), (700, 520), (40, 16384), (6, 20000),
-         (5, 5001), (2000, 136)]
+         (5, 5001), (2000, 136), (1, 8), (30001, 64), (9001, 128), (77, 248), (5000, 256)]
 
 
 @pytest.mark.parametrize("residual", [True, False])
@@ -110,6 +110,7 @@ def test_gradients(t, m, n, with_dh):
         want = (dy.double() * nrm).sum(dim=0)
         # a block's rows (at least 152 blocks, or a row each), 608 / 8 parts and 8 groups one after another;
         # for the longest rows the rows of a slab
+        # short rows: at most 32 of them in a block add their sums to one another's
         chain = (m / (152 if n < 20000 else 1) + 1) + 76 + 8 + 40
         loose = (dy.double() * nrm).abs().sum(dim=0) * chain * U
         close(dw, want, rounding(want, wt) + loose)
@@ -204,7 +205,7 @@ def test_strides_and_guards(t, offset, pad):
 
 
 def test_in_place():
-    for n in (520, 20000, 5001):
+    for n in (64, 520, 20000, 5001):
         x, r, w = inputs(9, n, torch.bfloat16, torch.bfloat16)
         y0, h0, rstd0 = B.rms_norm(x, w, residual=r)
         x1, r1 = x.clone(), r.clone()
@@ -220,8 +221,8 @@ def test_in_place():
             assert dx is given[place] and torch.equal(dx, dx0) and torch.equal(dw, dw0)
 
 
-def test_no_numbers_and_extremes():
-    n = 96
+@pytest.mark.parametrize("n", [96, 600])
+def test_no_numbers_and_extremes(n):
     for t in TYPES:
         big = torch.finfo(t).max
         x = rand(8, n).to(t)
