@@ -393,6 +393,9 @@ def test_captured(dtype):
 
 def test_capture_needs_the_workspace():
     x, w, target = inputs(64, 500, 64, torch.bfloat16)
+    torch.cuda.synchronize()
+    B.sgemm_shutdown()                                   # no stream has one (torch hands out streams again)
+    want = B.linear_cross_entropy(x, w, target)[0]
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
@@ -401,6 +404,7 @@ def test_capture_needs_the_workspace():
             B.linear_cross_entropy(x, w, target)
     assert e.value.status == B.SGEMM_ERR_CAPTURE
     torch.cuda.synchronize()
+    assert torch.equal(B.linear_cross_entropy(x, w, target, stream=side)[0], want)
 
 
 def test_norm_loss_and_clipping():

@@ -269,6 +269,9 @@ def test_captured():
 
 def test_capture_needs_the_workspace():
     ops, x = product(8, 100, 64, torch.bfloat16), rand(8, 64)
+    torch.cuda.synchronize()
+    B.sgemm_shutdown()                                   # no stream has one (torch hands out streams again)
+    want = B.mx4_gemm(*ops)
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
@@ -278,6 +281,7 @@ def test_capture_needs_the_workspace():
             B.mx4_gemm(*ops)
     assert e.value.status == B.SGEMM_ERR_CAPTURE
     torch.cuda.synchronize()
+    assert torch.equal(B.mx4_gemm(*ops, stream=side), want)
 
 
 def test_norm_into_the_4_bit_product():
