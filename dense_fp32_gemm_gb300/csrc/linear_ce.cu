@@ -125,9 +125,10 @@ __global__ void __launch_bounds__(32 * kGroups) join_kernel(const Join a) {
   }
 }
 
-// Factors of the tokens' gradients: d / c * unit, c the largest |d| (1 where
-// that is 0 or no number, and in FP32), and c / unit, the factor of the products. 0
-// for a token that is not counted, NaN for one whose target is no word. One block.
+// Factors of the tokens' gradients: d / c * unit, c the largest |d| among the
+// numbers (an infinity leaves the other rows their range; 1 where there is none
+// above 0, and in FP32), and c / unit, the factor of the products. 0 for a token
+// that is not counted, NaN for one whose target is no word. One block.
 constexpr int kScaleThreads = 1024;
 __global__ void __launch_bounds__(kScaleThreads)
     scale_kernel(int T, int V, const long long* target, long long ignore, const float* d,
@@ -137,14 +138,14 @@ __global__ void __launch_bounds__(kScaleThreads)
   ptx::griddep_launch_dependents();
   float most = 0.f;
   for (long long t = threadIdx.x; t < T; t += kScaleThreads)
-    if (target[t] != ignore) most = fmaxf(most, fabsf(d[t]));
+    if (target[t] != ignore && fabsf(d[t]) <= -kLeast) most = fmaxf(most, fabsf(d[t]));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, o));
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = most;
   __syncthreads();
   most = 0.f;
   for (int i = 0; i < kScaleThreads / 32; ++i) most = fmaxf(most, part[i]);
-  const float c = scaled && most > 0.f && most <= 3e38f ? most : 1.f;
+  const float c = scaled && most > 0.f ? most : 1.f;
   for (long long t = threadIdx.x; t < T; t += kScaleThreads) {
     const long long word = target[t];
     row_scale[t] = word == ignore              ? 0.f

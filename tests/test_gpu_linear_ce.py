@@ -258,6 +258,26 @@ def test_upstream_gradients(dtype):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("size", [1e3, 1e-9])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_an_infinite_upstream_gradient_leaves_the_other_rows(dtype, size):
+    """Rows of dX do not depend on another row's dloss, but for the largest number
+    among them, which G is scaled by."""
+    x, w, target = inputs(90, 400, 64, dtype, ignored=0.1)
+    _, lse = B.linear_cross_entropy(x, w, target)
+    counted = (target != IGNORE).nonzero()
+    row = int(counted[0])
+    d = rand(90, seed=4, scale=size)
+    d[int(counted[1])] = 8 * size                        # the largest, without `row` and with it
+    d[row] = 0
+    want = B.linear_cross_entropy_grad(x, w, target, lse, d)[0]
+    assert bool(want.isfinite().all())
+    d[row] = float("inf")
+    got = B.linear_cross_entropy_grad(x, w, target, lse, d)[0]
+    others = torch.arange(90, device="cuda") != row
+    assert torch.equal(got[others], want[others]) and not bool(got[row].isfinite().all())
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("offset,pad", [(0, 8), (1, 3)])
 def test_strides_and_guards(dtype, offset, pad):
