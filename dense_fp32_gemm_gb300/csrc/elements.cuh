@@ -104,23 +104,78 @@ __device__ __forceinline__ Piece<E, VW> pack(const float (&v)[VW]) {
   return p;
 }
 
+// The piece at place c of a row whose elements are at first .. end - 1 (SHIFT: places
+// count from the 16-byte boundary before the row, else first is 0 and pieces are
+// whole). Beside the row it holds whatever is there, until clean() has made that
+// zeros: a load that nothing waits for. `inner`: the matrix has rows before and after
+// this one, so that what is beside it is the matrix's (else it is not read).
+template <typename E, int VW, bool SHIFT>
+__device__ __forceinline__ Piece<E, VW> load_at(const E* row, unsigned c, unsigned first, unsigned end,
+                                                bool inner) {
+  if constexpr (SHIFT) {
+    if (!inner && (c < first || c + VW > end)) {
+      Piece<E, VW> p;
+      p.w = make_uint4(0u, 0u, 0u, 0u);
+      E* e = reinterpret_cast<E*>(&p.w);
+#pragma unroll
+      for (int j = 0; j < VW; ++j)
+        if (c + j >= first && c + j < end) e[j] = row[c + j];
+      return p;
+    }
+  }
+  return load<E, VW>(row + c);
+}
+template <typename E, int VW, bool SHIFT>
+__device__ __forceinline__ Piece<E, VW> clean(Piece<E, VW> p, unsigned c, unsigned first, unsigned end) {
+  if constexpr (SHIFT) {
+    if (c < first || c + VW > end) {
+      E* e = reinterpret_cast<E*>(&p.w);
+#pragma unroll
+      for (int j = 0; j < VW; ++j)
+        if (c + j < first || c + j >= end) e[j] = from_f32<E>(0.f);
+    }
+  }
+  return p;
+}
+// (what is outside the row is not written)
+template <typename E, int VW, bool SHIFT>
+__device__ __forceinline__ void store_at(E* row, unsigned c, unsigned first, unsigned end,
+                                         const Piece<E, VW>& p) {
+  if constexpr (SHIFT) {
+    if (c < first || c + VW > end) {
+      const E* e = reinterpret_cast<const E*>(&p.w);
+#pragma unroll
+      for (int j = 0; j < VW; ++j)
+        if (c + j >= first && c + j < end) row[c + j] = e[j];
+      return;
+    }
+  }
+  store<E, VW>(row + c, p);
+}
+
 // VW values of a vector that no kernel of the call writes, as FP32; 16-byte
-// aligned where VW > 1.
-template <typename W, int VW>
+// aligned where VW > 1. SHARED: in shared memory.
+template <typename W, int VW, bool SHARED = false>
 __device__ __forceinline__ void load_vector(const W* p, float (&v)[VW]) {
+  auto get = [](auto* q) {
+    if constexpr (SHARED)
+      return *q;
+    else
+      return __ldg(q);
+  };
   if constexpr (VW == 1) {
-    v[0] = to_f32(__ldg(p));
+    v[0] = to_f32(get(p));
   } else {
     constexpr int kWords = VW * (int)sizeof(W) / 4;
     uint32_t w[kWords];
     if constexpr (kWords == 2) {
-      const uint2 a = __ldg(reinterpret_cast<const uint2*>(p));
+      const uint2 a = get(reinterpret_cast<const uint2*>(p));
       w[0] = a.x;
       w[1] = a.y;
     } else {
 #pragma unroll
       for (int i = 0; i < kWords; i += 4) {
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(p) + i / 4);
+        const uint4 a = get(reinterpret_cast<const uint4*>(p) + i / 4);
         w[i] = a.x;
         w[i + 1] = a.y;
         w[i + 2] = a.z;

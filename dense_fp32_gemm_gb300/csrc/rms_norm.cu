@@ -130,10 +130,11 @@ __device__ __forceinline__ Step step_of(uint32_t most) {
   return s;
 }
 
-// The integers of a piece; `wide`: q is aligned to as many bytes.
+// The integers of a piece; `wide`: q is aligned to as many bytes. Of the VW those
+// from `first` on and before `end` are the row's.
 template <int VW>
 __device__ __forceinline__ void put_quotients(const float (&u)[VW], const Step& s, signed char* q,
-                                              int wide) {
+                                              int wide, int first = 0, int end = VW) {
   uint32_t b[VW];
 #pragma unroll
   for (int j = 0; j < VW; ++j) b[j] = 0u;
@@ -150,8 +151,34 @@ __device__ __forceinline__ void put_quotients(const float (&u)[VW], const Step& 
       *reinterpret_cast<uint32_t*>(q) = o[0];
   } else {
 #pragma unroll
-    for (int j = 0; j < VW; ++j) q[j] = (signed char)(b[j] & 0xffu);
+    for (int j = 0; j < VW; ++j)
+      if (j >= first && j < end) q[j] = (signed char)(b[j] & 0xffu);
   }
+}
+
+// Rows that do not start on 16 bytes (SHIFT), all of the call's matrices alike: the
+// places of a row count from the boundary before it, so that all of its pieces but
+// the first and the last are whole. The rows of a block (of a group of lanes, in the
+// kernels for short rows) start at the same place after a boundary, as the
+// host takes rows that are a multiple of 16 bytes apart; so a block's weights are
+// laid out once, in shared memory, the way its pieces lie. 8192 x 4097 BF16: y 55 us,
+// 8 bits 69, gradients 95; by single elements 124, 161 and 200.
+template <typename E>
+__device__ __forceinline__ unsigned start_of(const void* p, long long m, long long ld) {
+  return (unsigned)((reinterpret_cast<uintptr_t>(p) + m * ld * sizeof(E)) & 15u) / (unsigned)sizeof(E);
+}
+// Whether the whole pieces of row m are within the matrix, whose pitch is N at least.
+__device__ __forceinline__ bool inner_row(long long m, int M, int N, int vw) {
+  return m * N >= vw && (M - 1 - m) * N >= vw;
+}
+template <typename W>
+__device__ __forceinline__ const W* lay_out(const W* w, unsigned first, unsigned end, unsigned places) {
+  extern __shared__ uint4 weights[];
+  W* out = reinterpret_cast<W*>(weights);
+  for (unsigned c = threadIdx.x; c < places; c += blockDim.x)
+    out[c] = c >= first && c < end ? w[c - first] : from_f32<W>(0.f);
+  __syncthreads();
+  return out;
 }
 
 // A row per block, in pieces of VW elements (16 bytes, or one element where
@@ -159,7 +186,7 @@ __device__ __forceinline__ void put_quotients(const float (&u)[VW], const Step& 
 // the pass that sums and the pass that writes, and those of the block's next row
 // are loaded ahead; what is left of a longer row is read again (the thread's own
 // h, or x).
-template <typename E, typename W, int VW, bool I8>
+template <typename E, typename W, int VW, bool I8, bool SHIFT>
 __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a) {
   constexpr int HELD = held_of(VW);
   __shared__ float2 part[2][kMaxThreads / 32];
@@ -169,42 +196,48 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a) {
   const E* r = static_cast<const E*>(a.r);
   const W* w = static_cast<const W*>(a.w);
   E* h = static_cast<E*>(a.h);
+  // the row's elements are at places s .. N - 1
   // (places in a row pass 2^31 before they end their loops, not 2^32)
-  const unsigned step_c = blockDim.x * VW, c0 = threadIdx.x * VW, N = (unsigned)a.N;
+  const unsigned s = SHIFT ? start_of<E>(a.x, blockIdx.x, a.ldx) : 0u;
+  const unsigned step_c = blockDim.x * VW, c0 = threadIdx.x * VW, N = (unsigned)a.N + s;
+  if (SHIFT) w = lay_out(w, s, N, (N + VW - 1) / VW * VW);
   const float inv_n = 1.f / (float)a.N;
   int buf = 0;
   Piece<E, VW> held[HELD], ahead[HELD];      // x, then h; the residual
+  auto inner = [&](long long m) { return inner_row(m, a.M, a.N, VW); };
+  auto cleaned = [&](const Piece<E, VW>& p, unsigned c) { return clean<E, VW, SHIFT>(p, c, s, N); };
   auto fetch = [&](long long m) {
+    const bool in = inner(m);
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
       const unsigned c = c0 + i * step_c;
       if (c >= N) continue;
-      held[i] = load<E, VW>(x + m * a.ldx + c);
-      if (r != nullptr) ahead[i] = load<E, VW>(r + m * a.ldr + c);
+      held[i] = load_at<E, VW, SHIFT>(x + m * a.ldx - s, c, s, N, in);
+      if (r != nullptr) ahead[i] = load_at<E, VW, SHIFT>(r + m * a.ldr - s, c, s, N, in);
     }
   };
   auto sum_of = [&](const Piece<E, VW>& p, const Piece<E, VW>& q) {
-    float s[VW], t[VW];
-    unpack(p, s);
-    unpack(q, t);
+    float f[VW], g[VW];
+    unpack(p, f);
+    unpack(q, g);
 #pragma unroll
-    for (int j = 0; j < VW; ++j) s[j] += t[j];
-    return pack<E, VW>(s);
+    for (int j = 0; j < VW; ++j) f[j] += g[j];
+    return pack<E, VW>(f);
   };
   fetch(blockIdx.x);
   for (long long m = blockIdx.x; m < a.M; m += gridDim.x) {
     float sum = 0.f;
     uint32_t most = 0;
     auto add = [&](const Piece<E, VW>& p, unsigned c) {
-      if (h != nullptr) store<E, VW>(h + m * a.ldh + c, p);
-      float f[VW], s = 0.f;
+      if (h != nullptr) store_at<E, VW, SHIFT>(h + m * a.ldh - s, c, s, N, p);
+      float f[VW], t = 0.f;
       unpack(p, f);
 #pragma unroll
-      for (int j = 0; j < VW; ++j) s = fmaf(f[j], f[j], s);
-      sum += s;
+      for (int j = 0; j < VW; ++j) t = fmaf(f[j], f[j], t);
+      sum += t;
       if (I8) {
         float v[VW];
-        load_vector<W, VW>(w + c, v);
+        load_vector<W, VW, SHIFT>(w + c, v);
         // as bits: a NaN is above infinity, so either survives
 #pragma unroll
         for (int j = 0; j < VW; ++j)
@@ -213,15 +246,16 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a) {
     };
     Piece<E, VW> row[HELD];
 #pragma unroll
-    for (int i = 0; i < HELD; ++i) row[i] = r != nullptr ? sum_of(held[i], ahead[i]) : held[i];
+    for (int i = 0; i < HELD; ++i)
+      row[i] = cleaned(r != nullptr ? sum_of(held[i], ahead[i]) : held[i], c0 + i * step_c);
     if (m + gridDim.x < a.M) fetch(m + gridDim.x);
 #pragma unroll
     for (int i = 0; i < HELD; ++i)
       if (c0 + i * step_c < N) add(row[i], c0 + i * step_c);
     for (unsigned c = c0 + HELD * step_c; c < N; c += step_c) {
-      Piece<E, VW> p = load<E, VW>(x + m * a.ldx + c);
-      if (r != nullptr) p = sum_of(p, load<E, VW>(r + m * a.ldr + c));
-      add(p, c);
+      Piece<E, VW> p = load_at<E, VW, SHIFT>(x + m * a.ldx - s, c, s, N, inner(m));
+      if (r != nullptr) p = sum_of(p, load_at<E, VW, SHIFT>(r + m * a.ldr - s, c, s, N, inner(m)));
+      add(cleaned(p, c), c);
     }
     // the row's values once more: those that were not held from h, or x
     auto each = [&](auto&& f) {
@@ -229,7 +263,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a) {
       for (int i = 0; i < HELD; ++i)
         if (c0 + i * step_c < N) f(row[i], c0 + i * step_c);
       for (unsigned c = c0 + HELD * step_c; c < N; c += step_c)
-        f(load<E, VW>(h != nullptr ? h + m * a.ldh + c : x + m * a.ldx + c), c);
+        f(cleaned(load_at<E, VW, SHIFT>((h != nullptr ? h + m * a.ldh : x + m * a.ldx) - s, c, s, N,
+                                        inner(m)), c), c);
     };
     Reduced t = reduce<I8>(sum, most, part, buf);
     // Squares beyond FP32's range (values above 1e19): once more on values that
@@ -250,26 +285,26 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a) {
     const float rstd = rsqrtf(t.sum * inv_n + a.eps * down * down) * down;
     if (threadIdx.x == 0 && a.rstd != nullptr) a.rstd[m] = rstd;
     if (!I8) {
-      E* y = static_cast<E*>(a.y) + m * a.ldy;
+      E* y = static_cast<E*>(a.y) + m * a.ldy - s;
       each([&](const Piece<E, VW>& p, unsigned c) {
         float v[VW], f[VW];
-        load_vector<W, VW>(w + c, v);
+        load_vector<W, VW, SHIFT>(w + c, v);
         unpack(p, f);
 #pragma unroll
         for (int j = 0; j < VW; ++j) f[j] = f[j] * rstd * v[j];
-        store<E, VW>(y + c, pack<E, VW>(f));
+        store_at<E, VW, SHIFT>(y, c, s, N, pack<E, VW>(f));
       });
     } else {
       const Step step = step_of(t.most);
       if (threadIdx.x == 0) a.scale[m] = step.step * rstd;
-      signed char* q = static_cast<signed char*>(a.y) + m * a.ldy;
+      signed char* q = static_cast<signed char*>(a.y) + m * a.ldy - s;
       each([&](const Piece<E, VW>& p, unsigned c) {
         float u[VW], f[VW];
-        load_vector<W, VW>(w + c, u);
+        load_vector<W, VW, SHIFT>(w + c, u);
         unpack(p, f);
 #pragma unroll
         for (int j = 0; j < VW; ++j) u[j] *= f[j];
-        put_quotients<VW>(u, step, q + c, a.wide_q);
+        put_quotients<VW>(u, step, q + c, a.wide_q, SHIFT ? (int)(s - c) : 0, SHIFT ? (int)(N - c) : VW);
       });
     }
   }
@@ -290,7 +325,7 @@ struct GradArgs {
 // fits into HELD pieces a thread and dw's parts are formed.
 // HELD 2 (rows of at most 512 pieces): the next row's loads are ahead, on 256
 // threads; more pieces, and their sums, leave no registers for that.
-template <typename E, typename W, int VW, int HELD, bool DW>
+template <typename E, typename W, int VW, int HELD, bool DW, bool SHIFT>
 __global__ void __launch_bounds__(HELD == 2 ? 256 : kMaxThreads, HELD == 2 ? 2 : 1)
     norm_grad_kernel(const GradArgs a) {
   constexpr bool kAhead = HELD == 2;
@@ -302,7 +337,9 @@ __global__ void __launch_bounds__(HELD == 2 ? 256 : kMaxThreads, HELD == 2 ? 2 :
   const E* dh = static_cast<const E*>(a.dh);
   const W* w = static_cast<const W*>(a.w);
   E* dx = static_cast<E*>(a.dx);
-  const unsigned step_c = blockDim.x * VW, c0 = threadIdx.x * VW, N = (unsigned)a.N;
+  const unsigned s = SHIFT ? start_of<E>(a.dy, blockIdx.x, a.lddy) : 0u;   // as in norm_kernel
+  const unsigned step_c = blockDim.x * VW, c0 = threadIdx.x * VW, N = (unsigned)a.N + s;
+  if (SHIFT) w = lay_out(w, s, N, (N + VW - 1) / VW * VW);
   const float inv_n = 1.f / (float)a.N;
   int buf = 0;
   float dw[DW ? HELD : 1][VW];
@@ -312,15 +349,19 @@ __global__ void __launch_bounds__(HELD == 2 ? 256 : kMaxThreads, HELD == 2 ? 2 :
     for (int j = 0; j < VW; ++j) dw[i][j] = 0.f;
   Piece<E, VW> g1[HELD], v1[HELD], d1[HELD];
   float rstd1 = 0.f;
+  auto get = [&](const E* p, long long ld, long long m, unsigned c) {
+    return load_at<E, VW, SHIFT>(p + m * ld - s, c, s, N, inner_row(m, a.M, a.N, VW));
+  };
+  auto cleaned = [&](const Piece<E, VW>& p, unsigned c) { return clean<E, VW, SHIFT>(p, c, s, N); };
   auto fetch = [&](long long m) {
     rstd1 = a.rstd[m];
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
       const unsigned c = c0 + i * step_c;
       if (c >= N) continue;
-      g1[i] = load<E, VW>(dy + m * a.lddy + c);
-      v1[i] = load<E, VW>(h + m * a.ldh + c);
-      if (dh != nullptr) d1[i] = load<E, VW>(dh + m * a.lddh + c);
+      g1[i] = get(dy, a.lddy, m, c);
+      v1[i] = get(h, a.ldh, m, c);
+      if (dh != nullptr) d1[i] = get(dh, a.lddh, m, c);
     }
   };
   if (kAhead) fetch(blockIdx.x);
@@ -330,20 +371,20 @@ __global__ void __launch_bounds__(HELD == 2 ? 256 : kMaxThreads, HELD == 2 ? 2 :
     Piece<E, VW> g[HELD], v[HELD], d[HELD];
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
-      g[i] = g1[i];
-      v[i] = v1[i];
+      g[i] = cleaned(g1[i], c0 + i * step_c);
+      v[i] = cleaned(v1[i], c0 + i * step_c);
       d[i] = d1[i];
     }
     if (kAhead && m + gridDim.x < a.M) fetch(m + gridDim.x);
     float sum = 0.f;
     auto add = [&](const Piece<E, VW>& g, const Piece<E, VW>& v, unsigned c) {
-      float wv[VW], gf[VW], vf[VW], s = 0.f;
-      load_vector<W, VW>(w + c, wv);
+      float wv[VW], gf[VW], vf[VW], t = 0.f;
+      load_vector<W, VW, SHIFT>(w + c, wv);
       unpack(g, gf);
       unpack(v, vf);
 #pragma unroll
-      for (int j = 0; j < VW; ++j) s = fmaf(gf[j] * wv[j], vf[j] * rstd, s);
-      sum += s;
+      for (int j = 0; j < VW; ++j) t = fmaf(gf[j] * wv[j], vf[j] * rstd, t);
+      sum += t;
     };
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
@@ -360,12 +401,12 @@ __global__ void __launch_bounds__(HELD == 2 ? 256 : kMaxThreads, HELD == 2 ? 2 :
     }
     if (!DW)
       for (unsigned c = c0 + HELD * step_c; c < N; c += step_c)
-        add(load<E, VW>(dy + m * a.lddy + c), load<E, VW>(h + m * a.ldh + c), c);
+        add(cleaned(get(dy, a.lddy, m, c), c), cleaned(get(h, a.ldh, m, c), c), c);
     if (dx == nullptr) continue;
     const float mean = reduce<false>(sum, 0, part, buf).sum * inv_n;
     auto put = [&](const Piece<E, VW>& g, const Piece<E, VW>& v, const Piece<E, VW>& d, unsigned c) {
       float wv[VW], gf[VW], vf[VW], df[VW];
-      load_vector<W, VW>(w + c, wv);
+      load_vector<W, VW, SHIFT>(w + c, wv);
       unpack(g, gf);
       unpack(v, vf);
       unpack(d, df);
@@ -374,15 +415,15 @@ __global__ void __launch_bounds__(HELD == 2 ? 256 : kMaxThreads, HELD == 2 ? 2 :
         const float t = rstd * fmaf(-mean, vf[j] * rstd, gf[j] * wv[j]);
         gf[j] = dh != nullptr ? t + df[j] : t;
       }
-      store<E, VW>(dx + m * a.lddx + c, pack<E, VW>(gf));
+      store_at<E, VW, SHIFT>(dx + m * a.lddx - s, c, s, N, pack<E, VW>(gf));
     };
 #pragma unroll
     for (int i = 0; i < HELD; ++i)
       if (c0 + i * step_c < N) put(g[i], v[i], d[i], c0 + i * step_c);
     if (!DW)
       for (unsigned c = c0 + HELD * step_c; c < N; c += step_c)
-        put(load<E, VW>(dy + m * a.lddy + c), load<E, VW>(h + m * a.ldh + c),
-            dh != nullptr ? load<E, VW>(dh + m * a.lddh + c) : Piece<E, VW>{}, c);
+        put(get(dy, a.lddy, m, c), get(h, a.ldh, m, c),
+            dh != nullptr ? get(dh, a.lddh, m, c) : Piece<E, VW>{}, c);
   }
   if (DW && a.partial != nullptr) {
     float* p = a.partial + (long long)blockIdx.x * a.N;
@@ -392,6 +433,10 @@ __global__ void __launch_bounds__(HELD == 2 ? 256 : kMaxThreads, HELD == 2 ? 2 :
       if (c >= N) continue;
       if constexpr (VW == 1) {
         p[c] = dw[i][0];
+      } else if constexpr (SHIFT) {
+#pragma unroll
+        for (int j = 0; j < VW; ++j)
+          if (c + j >= s && c + j < N) p[c + j - s] = dw[i][j];
       } else {
 #pragma unroll
         for (int j = 0; j < VW; j += 4)
@@ -411,34 +456,44 @@ __device__ __forceinline__ float sum_over(float v, int lanes) {
   for (int d = lanes >> 1; d > 0; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
   return v;
 }
-template <typename E, typename W, int VW, bool I8>
+template <typename E, typename W, int VW, bool I8, bool SHIFT>
 __global__ void __launch_bounds__(kSmallThreads) small_norm_kernel(const NormArgs a, int lanes) {
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const int rows = kSmallThreads / lanes, l = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes;
-  const int c = l * VW;
+  // (a group's rows are a multiple of 8 apart: all start at the same place)
+  const unsigned s = SHIFT ? start_of<E>(a.x, (long long)blockIdx.x * rows + group, a.ldx) : 0u;
+  const unsigned c = l * VW, N = (unsigned)a.N + s;
   const float inv_n = 1.f / (float)a.N;
   float w[VW];
 #pragma unroll
   for (int j = 0; j < VW; ++j) w[j] = 0.f;
-  if (c < a.N) load_vector<W, VW>(static_cast<const W*>(a.w) + c, w);
+  if constexpr (SHIFT) {
+#pragma unroll
+    for (int j = 0; j < VW; ++j)
+      if (c + j >= s && c + j < N) w[j] = to_f32(__ldg(static_cast<const W*>(a.w) + (c + j - s)));
+  } else if (c < N) {
+    load_vector<W, VW>(static_cast<const W*>(a.w) + c, w);
+  }
   // (the same number of steps for every thread: they exchange sums)
   for (long long m0 = (long long)blockIdx.x * rows; m0 < a.M; m0 += (long long)gridDim.x * rows) {
     const long long m = m0 + group;
-    const bool live = m < a.M && c < a.N;
+    const bool live = m < a.M && c < N, inner = inner_row(m, a.M, a.N, VW);
     float f[VW], u[VW];
 #pragma unroll
     for (int j = 0; j < VW; ++j) f[j] = 0.f;
     if (live) {
-      Piece<E, VW> p = load<E, VW>(static_cast<const E*>(a.x) + m * a.ldx + c);
+      Piece<E, VW> p = load_at<E, VW, SHIFT>(static_cast<const E*>(a.x) + m * a.ldx - s, c, s, N, inner);
+      p = clean<E, VW, SHIFT>(p, c, s, N);
       unpack(p, f);
       if (a.r != nullptr) {
-        unpack(load<E, VW>(static_cast<const E*>(a.r) + m * a.ldr + c), u);
+        unpack(clean<E, VW, SHIFT>(
+            load_at<E, VW, SHIFT>(static_cast<const E*>(a.r) + m * a.ldr - s, c, s, N, inner), c, s, N), u);
 #pragma unroll
         for (int j = 0; j < VW; ++j) f[j] += u[j];
         p = pack<E, VW>(f);
         unpack(p, f);
-        store<E, VW>(static_cast<E*>(a.h) + m * a.ldh + c, p);
+        store_at<E, VW, SHIFT>(static_cast<E*>(a.h) + m * a.ldh - s, c, s, N, p);
       }
     }
     float sum = 0.f;
@@ -470,39 +525,50 @@ __global__ void __launch_bounds__(kSmallThreads) small_norm_kernel(const NormArg
       if (!live) continue;
 #pragma unroll
       for (int j = 0; j < VW; ++j) f[j] = f[j] * rstd * w[j];
-      store<E, VW>(static_cast<E*>(a.y) + m * a.ldy + c, pack<E, VW>(f));
+      store_at<E, VW, SHIFT>(static_cast<E*>(a.y) + m * a.ldy - s, c, s, N, pack<E, VW>(f));
     } else {
       const Step step = step_of(most);
       if (m < a.M && l == 0) a.scale[m] = step.step * rstd;
       if (!live) continue;
-      put_quotients<VW>(u, step, static_cast<signed char*>(a.y) + m * a.ldy + c, a.wide_q);
+      put_quotients<VW>(u, step, static_cast<signed char*>(a.y) + m * a.ldy - s + c, a.wide_q,
+                        SHIFT ? (int)(s - c) : 0, SHIFT ? (int)(N - c) : VW);
     }
   }
 }
 
-template <typename E, typename W, int VW>
+template <typename E, typename W, int VW, bool SHIFT>
 __global__ void __launch_bounds__(kSmallThreads) small_grad_kernel(const GradArgs a, int lanes) {
   __shared__ float part[kSmallThreads][VW + 1];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const int rows = kSmallThreads / lanes, l = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes;
-  const int c = l * VW;
+  // (a group's rows are a multiple of 8 apart: all start at the same place)
+  const unsigned s = SHIFT ? start_of<E>(a.dy, (long long)blockIdx.x * rows + group, a.lddy) : 0u;
+  const unsigned c = l * VW, N = (unsigned)a.N + s;
   const float inv_n = 1.f / (float)a.N;
   float w[VW], dw[VW];
 #pragma unroll
   for (int j = 0; j < VW; ++j) w[j] = dw[j] = 0.f;
-  if (c < a.N) load_vector<W, VW>(static_cast<const W*>(a.w) + c, w);
+  if constexpr (SHIFT) {
+#pragma unroll
+    for (int j = 0; j < VW; ++j)
+      if (c + j >= s && c + j < N) w[j] = to_f32(__ldg(static_cast<const W*>(a.w) + (c + j - s)));
+  } else if (c < N) {
+    load_vector<W, VW>(static_cast<const W*>(a.w) + c, w);
+  }
   for (long long m0 = (long long)blockIdx.x * rows; m0 < a.M; m0 += (long long)gridDim.x * rows) {
     const long long m = m0 + group;
-    const bool live = m < a.M && c < a.N;
+    const bool live = m < a.M && c < N, inner = inner_row(m, a.M, a.N, VW);
     float g[VW], n[VW], d[VW], sum = 0.f, rstd = 0.f;
 #pragma unroll
     for (int j = 0; j < VW; ++j) g[j] = n[j] = d[j] = 0.f;
     if (live) {
       rstd = a.rstd[m];
-      unpack(load<E, VW>(static_cast<const E*>(a.dy) + m * a.lddy + c), g);
-      unpack(load<E, VW>(static_cast<const E*>(a.h) + m * a.ldh + c), n);
-      if (a.dh != nullptr) unpack(load<E, VW>(static_cast<const E*>(a.dh) + m * a.lddh + c), d);
+      unpack(clean<E, VW, SHIFT>(
+          load_at<E, VW, SHIFT>(static_cast<const E*>(a.dy) + m * a.lddy - s, c, s, N, inner), c, s, N), g);
+      unpack(clean<E, VW, SHIFT>(
+          load_at<E, VW, SHIFT>(static_cast<const E*>(a.h) + m * a.ldh - s, c, s, N, inner), c, s, N), n);
+      if (a.dh != nullptr) unpack(load_at<E, VW, SHIFT>(static_cast<const E*>(a.dh) + m * a.lddh - s, c, s, N, inner), d);
 #pragma unroll
       for (int j = 0; j < VW; ++j) {
         n[j] *= rstd;
@@ -516,7 +582,7 @@ __global__ void __launch_bounds__(kSmallThreads) small_grad_kernel(const GradArg
     if (!live) continue;
 #pragma unroll
     for (int j = 0; j < VW; ++j) g[j] = rstd * fmaf(-mean, n[j], g[j]) + d[j];
-    store<E, VW>(static_cast<E*>(a.dx) + m * a.lddx + c, pack<E, VW>(g));
+    store_at<E, VW, SHIFT>(static_cast<E*>(a.dx) + m * a.lddx - s, c, s, N, pack<E, VW>(g));
   }
   if (a.partial == nullptr) return;
 #pragma unroll
@@ -524,7 +590,10 @@ __global__ void __launch_bounds__(kSmallThreads) small_grad_kernel(const GradArg
   __syncthreads();
   for (int i = threadIdx.x; i < a.N; i += kSmallThreads) {
     float sum = 0.f;
-    for (int r = 0; r < rows; ++r) sum += part[r * lanes + i / VW][i % VW];
+    for (int r = 0; r < rows; ++r) {
+      const unsigned at = i + (SHIFT ? start_of<E>(a.dy, (long long)blockIdx.x * rows + r, a.lddy) : 0u);
+      sum += part[r * lanes + at / VW][at % VW];
+    }
     a.partial[(long long)blockIdx.x * a.N + i] = sum;
   }
 }
@@ -579,9 +648,14 @@ __global__ void __launch_bounds__(32 * kSumLanes)
 }
 
 template <typename... A>
-cudaError_t launch(void (*kernel)(A...), long long blocks, int threads, cudaStream_t stream,
-                   std::common_type_t<A>... args) {
+cudaError_t launch(void (*kernel)(A...), long long blocks, int threads, int shared_bytes,
+                   cudaStream_t stream, std::common_type_t<A>... args) {
+  if (shared_bytes > (32 << 10)) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared_bytes);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t lc = {};
+  lc.dynamicSmemBytes = (size_t)shared_bytes;
   cudaLaunchAttribute la[1];
   la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   la[0].val.programmaticStreamSerializationAllowed = 1;
@@ -594,11 +668,13 @@ cudaError_t launch(void (*kernel)(A...), long long blocks, int threads, cudaStre
 }
 
 // Threads of a row: a piece each while that leaves SMs idle otherwise (few
-// rows: latency), else as many pieces as are held.
+// rows: latency), else as many pieces as are held, and what the blocks that fit
+// leave (8192 x 4097 FP32 gradients on 288 threads, one block an SM, 173 us; on 512, 151).
 int threads_of(long long pieces, int held, bool few) {
   const long long want = few ? pieces : (pieces + held - 1) / held;
   const long long t = (want + 31) / 32 * 32;
-  return (int)(t < 32 ? 32 : (t > kMaxThreads ? kMaxThreads : t));
+  const int n = (int)(t < 32 ? 32 : (t > kMaxThreads ? kMaxThreads : t));
+  return few ? n : kMaxThreads / (kMaxThreads / n) / 32 * 32;
 }
 // Blocks: a row each, or as many as fill the SMs (`threads_per_sm` resident).
 int blocks_of(int M, int threads, int sms, int threads_per_sm) {
@@ -618,24 +694,65 @@ bool aligned(const void* p, long long ld, int elem, int bytes) {
   return p == nullptr ||
          ((reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0 && ld * elem % bytes == 0);
 }
+// Every row of p starts at the same place after a 16-byte boundary as that of x.
+bool alike(const void* p, long long ld, const void* x, long long ldx, int elem) {
+  return p == nullptr || (((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(x)) & 15u) == 0 &&
+                          (ld - ldx) * elem % 16 == 0);
+}
+
+// How a call's rows are taken: in 16-byte pieces that start with the row, in
+// pieces that start at a boundary before it, or by single elements.
+enum Access { kPieces, kShifted, kSingle };
+// Bytes of shared memory for the weights of shifted rows; longer ones are taken by
+// single elements.
+constexpr long long kMostShared = 96 << 10;
+// Shifted, unless the weights take too much, or the call is a few rows that threads
+// hold by single elements: laying out the weights, and the first and the last row,
+// whose ends are read by themselves, take 1 to 2 us (16 x 1001 BF16: 4.0 us, single 2.4;
+// 16 x 16383: 10.3 and 15.1).
+bool shift(int M, int N, int vw, int weight_bytes, int sms) {
+  return (N + 2ll * vw) * weight_bytes <= kMostShared &&
+         (M >= 2 * sms || N > held_of(1) * kMaxThreads);
+}
+// Places of a row in the worst case, in pieces of vw.
+long long pieces_of(Access access, int N, int vw) {
+  return access == kSingle ? N : (N + (access == kShifted ? vw - 1ll : 0ll) + vw - 1) / vw;
+}
+int shared_of(Access access, int N, int vw, int weight_bytes) {
+  return access == kShifted ? (int)(pieces_of(access, N, vw) * vw * weight_bytes) : 0;
+}
+// Blocks so that the rows of one, where there are several, are a multiple of 16
+// bytes apart.
+int spaced(Access access, int M, long long row_bytes, int blocks) {
+  int rows = 1;
+  while (row_bytes * rows % 16 != 0) rows *= 2;
+  return access == kShifted && blocks < M && blocks > rows ? blocks / rows * rows : blocks;
+}
 
 template <typename E, typename W, bool I8>
 cudaError_t forward(NormArgs a, int sms, cudaStream_t stream) {
   constexpr int VW = 16 / (int)sizeof(E);
-  const bool vec = aligned(a.x, a.ldx, sizeof(E), 16) && aligned(a.r, a.ldr, sizeof(E), 16) &&
-                   aligned(a.h, a.ldh, sizeof(E), 16) && aligned(a.w, 0, sizeof(W), 16) &&
-                   a.N % VW == 0 && (I8 || aligned(a.y, a.ldy, sizeof(E), 16));
-  a.wide_q = I8 && aligned(a.y, a.ldy, 1, VW);
+  const bool whole = aligned(a.x, a.ldx, sizeof(E), 16) && aligned(a.r, a.ldr, sizeof(E), 16) &&
+                     aligned(a.h, a.ldh, sizeof(E), 16) && aligned(a.w, 0, sizeof(W), 16) &&
+                     a.N % VW == 0 && (I8 || aligned(a.y, a.ldy, sizeof(E), 16));
+  const bool shifted = alike(a.r, a.ldr, a.x, a.ldx, sizeof(E)) && alike(a.h, a.ldh, a.x, a.ldx, sizeof(E)) &&
+                       (I8 || alike(a.y, a.ldy, a.x, a.ldx, sizeof(E))) &&
+                       shift(a.M, a.N, VW, sizeof(W), sms);
+  const Access access = whole ? kPieces : shifted ? kShifted : kSingle;
+  a.wide_q = I8 && access != kShifted && aligned(a.y, a.ldy, 1, VW);
   const bool few = a.M < 2 * sms;
-  const long long pieces = vec ? a.N / VW : a.N;
-  if (vec && pieces <= 32) {
+  const long long pieces = pieces_of(access, a.N, VW);
+  if (access != kSingle && pieces <= 32) {
     const int lanes = small_lanes(pieces);
-    return launch(small_norm_kernel<E, W, VW, I8>, small_blocks(a.M, lanes, sms), kSmallThreads,
-                  stream, a, lanes);
+    return launch(whole ? small_norm_kernel<E, W, VW, I8, false> : small_norm_kernel<E, W, VW, I8, true>,
+                  small_blocks(a.M, lanes, sms), kSmallThreads, 0, stream, a, lanes);
   }
-  const int t = threads_of(pieces, held_of(vec ? VW : 1), few);
-  return launch(vec ? norm_kernel<E, W, VW, I8> : norm_kernel<E, W, 1, I8>,
-                blocks_of(a.M, t, sms, 512), t, stream, a);
+  const int t = threads_of(pieces, held_of(access != kSingle ? VW : 1), few);
+  return launch(access == kPieces    ? norm_kernel<E, W, VW, I8, false>
+                : access == kShifted ? norm_kernel<E, W, VW, I8, true>
+                                     : norm_kernel<E, W, 1, I8, false>,
+                spaced(access, a.M, a.ldx * (int)sizeof(E), blocks_of(a.M, t, sms, 512)), t,
+                shared_of(access, a.N, VW, sizeof(W)), stream, a);
 }
 
 // `blocks` make a part of dw each: of norm_grad_kernel where a row is `held` (in so
@@ -643,30 +760,36 @@ cudaError_t forward(NormArgs a, int sms, cudaStream_t stream) {
 // column_kernel.
 template <typename E, typename W>
 cudaError_t backward(GradArgs a, W* dw, float* partial, int blocks, int sms, cudaStream_t stream,
-                     int threads, bool vec, int held) {
+                     int threads, Access access, int held) {
   constexpr int VW = 16 / (int)sizeof(E);
   a.partial = partial;
   cudaError_t e = cudaSuccess;
   if (held == 1) {
-    e = launch(small_grad_kernel<E, W, VW>, blocks, kSmallThreads, stream, a, threads);
+    e = launch(access == kShifted ? small_grad_kernel<E, W, VW, true> : small_grad_kernel<E, W, VW, false>,
+               blocks, kSmallThreads, 0, stream, a, threads);
   } else if (held != 0) {
-    e = launch(!vec         ? norm_grad_kernel<E, W, 1, 8, true>
-               : held == 2 ? norm_grad_kernel<E, W, VW, 2, true>
-                           : norm_grad_kernel<E, W, VW, 4, true>,
-               blocks, threads, stream, a);
+    e = launch(access == kSingle    ? norm_grad_kernel<E, W, 1, 8, true, false>
+               : access == kPieces ? (held == 2 ? norm_grad_kernel<E, W, VW, 2, true, false>
+                                                : norm_grad_kernel<E, W, VW, 4, true, false>)
+                                   : (held == 2 ? norm_grad_kernel<E, W, VW, 2, true, true>
+                                                : norm_grad_kernel<E, W, VW, 4, true, true>),
+               blocks, threads, shared_of(access, a.N, VW, sizeof(W)), stream, a);
   } else {
     // (dw's parts first: dx may take the place of what they are made of)
     if (dw != nullptr) {
       const long long all = (a.N + kColumnThreads - 1ll) / kColumnThreads * blocks;
-      e = launch(column_kernel<E>, all < sms * 8ll ? all : sms * 8ll, kColumnThreads, stream, a, blocks);
+      e = launch(column_kernel<E>, all < sms * 8ll ? all : sms * 8ll, kColumnThreads, 0, stream, a, blocks);
     }
     if (e == cudaSuccess && a.dx != nullptr)
-      e = launch(vec ? norm_grad_kernel<E, W, VW, 4, false> : norm_grad_kernel<E, W, 1, 8, false>,
-                 blocks_of(a.M, threads, sms, 512), threads, stream, a);
+      e = launch(access == kPieces    ? norm_grad_kernel<E, W, VW, 4, false, false>
+                 : access == kShifted ? norm_grad_kernel<E, W, VW, 4, false, true>
+                                      : norm_grad_kernel<E, W, 1, 8, false, false>,
+                 spaced(access, a.M, a.lddy * (int)sizeof(E), blocks_of(a.M, threads, sms, 512)), threads,
+                 shared_of(access, a.N, VW, sizeof(W)), stream, a);
   }
   if (e == cudaSuccess && dw != nullptr) {
     const long long all = (a.N + 31ll) / 32;
-    e = launch(sum_kernel<W>, all < sms * 8ll ? all : sms * 8ll, 32 * kSumLanes, stream,
+    e = launch(sum_kernel<W>, all < sms * 8ll ? all : sms * 8ll, 32 * kSumLanes, 0, stream,
                static_cast<const float*>(partial), blocks, a.N, dw);
   }
   return e;
@@ -831,10 +954,14 @@ SGEMM_API int sgemm_rms_norm_grad(int M, int N, int type, const void* dY, int ld
   a.dx = dX;
   a.lddx = lddx;
   const int vw = 16 / eb;
-  const bool vec = rows::aligned(dY, lddy, eb, 16) && rows::aligned(H, ldh, eb, 16) &&
-                   rows::aligned(dH, lddh, eb, 16) && rows::aligned(dX, lddx, eb, 16) &&
-                   rows::aligned(weight, 0, wb, 16) && N % vw == 0;
-  const long long pieces = vec ? N / vw : N;
+  const bool whole = rows::aligned(dY, lddy, eb, 16) && rows::aligned(H, ldh, eb, 16) &&
+                     rows::aligned(a.dh, lddh, eb, 16) && rows::aligned(dX, lddx, eb, 16) &&
+                     rows::aligned(weight, 0, wb, 16) && N % vw == 0;
+  const bool shifted = rows::alike(H, ldh, dY, lddy, eb) && rows::alike(a.dh, lddh, dY, lddy, eb) &&
+                       rows::alike(dX, lddx, dY, lddy, eb) && rows::shift(M, N, vw, wb, sms);
+  const rows::Access access = whole ? rows::kPieces : shifted ? rows::kShifted : rows::kSingle;
+  const bool vec = access != rows::kSingle;
+  const long long pieces = rows::pieces_of(access, N, vw);
   const int held = pieces > rows::held_of(vec ? vw : 1) * rows::kMaxThreads ? 0
                    : vec ? (pieces <= 32 ? 1 : (pieces <= 512 ? 2 : 4)) : 8;
   const int threads = held == 1   ? rows::small_lanes(pieces)
@@ -844,7 +971,7 @@ SGEMM_API int sgemm_rms_norm_grad(int M, int N, int type, const void* dY, int ld
   if (held == 1) {
     blocks = rows::small_blocks(M, threads, sms);
   } else if (held != 0) {
-    blocks = rows::blocks_of(M, threads, sms, 512);
+    blocks = rows::spaced(access, M, (long long)lddy * eb, rows::blocks_of(M, threads, sms, 512));
   } else {
     const int fill = sms * 8 / (int)((N + rows::kColumnThreads - 1ll) / rows::kColumnThreads) + 1;
     blocks = M < fill ? M : fill;
@@ -864,7 +991,7 @@ SGEMM_API int sgemm_rms_norm_grad(int M, int N, int type, const void* dY, int ld
     using E = decltype(e);
     using W = decltype(w);
     return rows::done(rows::backward<E, W>(a, static_cast<W*>(dweight), partial, blocks, sms, stream,
-                                           threads, vec, held));
+                                           threads, access, held));
   };
   if (type == SGEMM_TYPE_F32) return go(0.f, 0.f);
   if (type == SGEMM_TYPE_BF16) return weight_type == SGEMM_TYPE_F32 ? go(B{}, 0.f) : go(B{}, B{});

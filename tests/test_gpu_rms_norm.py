@@ -204,6 +204,60 @@ def test_strides_and_guards(t, offset, pad):
         assert bool((s[mask] == 77).all())
 
 
+# odd rows, many of them to a block; the longest that registers hold, and longer
+ODD = [(2000, 1001), (3000, 333), (700, 4097), (3000, 255), (30001, 65), (5000, 3), (170, 8191), (200, 8185), (9, 16377),
+       (165, 16383), (6, 20001)]
+
+
+@pytest.mark.parametrize("m,n", ODD)
+@pytest.mark.parametrize("t", TYPES)
+def test_rows_that_start_anywhere(t, m, n):
+    test_forward(t, m, n, True)
+    test_8_bits(t, m, n)
+    test_gradients(t, m, n, True)
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("n,offset,pads", [(333, 5, (2, 2, 2, 2)), (333, 5, (2, 10, 18, 2)), (333, 2, (2, 3, 2, 2)),
+                                           (40, 1, (1, 1, 1, 1)), (40, 1, (0, 0, 0, 8)), (2048, 4, (8, 8, 8, 16))])
+def test_many_rows_at_any_pitch(t, n, offset, pads):
+    """Matrices that start alike after a 16-byte boundary, and not."""
+    m = 1500
+
+    def at(values, pad):
+        store = torch.full((offset + m * (n + pad),), 77, dtype=values.dtype, device="cuda")
+        view = store[offset:].view(m, n + pad)[:, :n]
+        view.copy_(values)
+        return store, view
+
+    x, r, w = inputs(m, n, t, t)
+    ref_h, ref_rstd, ref_y = reference(x, r, w)
+    empty = torch.zeros_like(x)
+    stores, views = zip(*(at(v, p) for v, p in zip((x, r, empty, empty), pads)))
+    y, h, rstd = B.rms_norm(views[0], w, residual=views[1], Y=views[2], H=views[3])
+    assert torch.equal(h, ref_h)
+    close(rstd, ref_rstd, ref_rstd * 36 * U)
+    close(y, ref_y, rounding(ref_y, t) + ref_y.abs() * 40 * U)
+    q, scale, _ = B.rms_norm_i8(views[0], w, residual=views[1], H=views[3])
+    q0, scale0, _ = B.rms_norm_i8(x, w, residual=r)
+    assert torch.equal(q, q0)
+    close(scale, scale0.double(), scale0.double() * 76 * U)          # two of 38 U
+    dy, dh = rand(m, n, seed=7).to(t), rand(m, n, seed=8).to(t)
+    views[0].copy_(dy), views[1].copy_(dh)
+    dx, dw = B.rms_norm_grad(views[0], h, w, rstd, dH=views[1], dX=views[2])
+    _, s, _ = reference(h, None, w)
+    nrm, d = h.double() * s[:, None], dy.double() * w.double()
+    mean = (d * nrm).mean(dim=1, keepdim=True)
+    want = s[:, None] * (d - nrm * mean) + dh.double()
+    loose = s[:, None] * (d.abs() + nrm.abs() * (d * nrm).abs().mean(dim=1, keepdim=True)) * 150 * U + want.abs() * U
+    close(dx, want, rounding(want, t) + loose)                       # as in test_gradients
+    want = (dy.double() * nrm).sum(dim=0)
+    chain = (m / 152 + 1) + 76 + 8 + 40
+    close(dw, want, rounding(want, t) + (dy.double() * nrm).abs().sum(dim=0) * chain * U)
+    for store, pad in zip(stores, pads):
+        assert bool((store[:offset] == 77).all()) and bool((store[offset:].view(m, n + pad)[:, n:] == 77).all())
+
+
 def test_in_place():
     for n in (64, 520, 20000, 5001):
         x, r, w = inputs(9, n, torch.bfloat16, torch.bfloat16)
