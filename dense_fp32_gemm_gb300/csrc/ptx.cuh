@@ -159,6 +159,12 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
   return ok != 0;
 }
 
+// Brings `bytes` (a multiple of 16) from a 16-byte boundary of global memory into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(__cvta_generic_to_global(p)), "r"(bytes)
+               : "memory");
+}
+
 // A 32-bit load from the shared memory of another CTA of the cluster.
 __device__ __forceinline__ uint32_t ld_shared_cluster(uint32_t cluster_addr) {
   uint32_t v;

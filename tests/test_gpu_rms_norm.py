@@ -217,9 +217,20 @@ def test_rows_that_start_anywhere(t, m, n):
     test_gradients(t, m, n, True)
 
 
+# rows of one block, of clusters of 2, 4 and 8, and those that registers do not hold (at
+# most 35 pieces of 4 values a thread: 35 + 4 + 21 additions one after another)
+@pytest.mark.parametrize("m,n", [(1000, 8192), (333, 5120), (400, 12288), (90, 16384), (50, 20000), (30, 32768), (5, 70000)])
+@pytest.mark.parametrize("t", TYPES)
+def test_long_rows(t, m, n):
+    test_forward(t, m, n, True)
+    test_gradients(t, m, n, True)
+    test_gradients(t, m, n, False)
+
+
 @pytest.mark.parametrize("t", TYPES)
 @pytest.mark.parametrize("n,offset,pads", [(333, 5, (2, 2, 2, 2)), (333, 5, (2, 10, 18, 2)), (333, 2, (2, 3, 2, 2)),
-                                           (40, 1, (1, 1, 1, 1)), (40, 1, (0, 0, 0, 8)), (2048, 4, (8, 8, 8, 16))])
+                                           (40, 1, (1, 1, 1, 1)), (40, 1, (0, 0, 0, 8)), (2048, 4, (8, 8, 8, 16)),
+                                           (5001, 1, (0, 1, 0, 0))])
 def test_many_rows_at_any_pitch(t, n, offset, pads):
     """Matrices that start alike after a 16-byte boundary, and not."""
     m = 1500
