@@ -104,6 +104,15 @@ __device__ __forceinline__ Piece<E, VW> pack(const float (&v)[VW]) {
   return p;
 }
 
+// Elements between the 16-byte boundary before row m and its start.
+template <typename E>
+__device__ __forceinline__ unsigned start_of(const void* p, long long m, long long ld) {
+  return (unsigned)((reinterpret_cast<uintptr_t>(p) + m * ld * sizeof(E)) & 15u) / (unsigned)sizeof(E);
+}
+// Whether the whole pieces of row m are within the matrix, whose pitch is N at least.
+__device__ __forceinline__ bool inner_row(long long m, int M, int N, int vw) {
+  return m * N >= vw && (M - 1 - m) * N >= vw;
+}
 // The piece at place c of a row whose elements are at first .. end - 1 (SHIFT: places
 // count from the 16-byte boundary before the row, else first is 0 and pieces are
 // whole). Beside the row it holds whatever is there, until clean() has made that

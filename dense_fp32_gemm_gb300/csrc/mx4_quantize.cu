@@ -82,6 +82,21 @@ template <typename E>
 struct Eight {
   uint4 w;
   __device__ __forceinline__ void load(const E* p) { w = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  // from the 32 bytes around them, `skip` bytes on; the first n of them (the rest: zeros)
+  static constexpr int kChunks = 2;
+  __device__ __forceinline__ void extract(const uint4 (&from)[kChunks], unsigned skip, unsigned n) {
+    uint32_t c[8] = {from[0].x, from[0].y, from[0].z, from[0].w, from[1].x, from[1].y, from[1].z, from[1].w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) c[i] = skip & 8u ? c[i + 2] : c[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) c[i] = skip & 4u ? c[i + 1] : c[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = __funnelshift_r(c[i], c[i + 1], (skip & 2u) * 8u);
+      if (2 * i + 1 >= n) c[i] = 2 * i >= n ? 0u : c[i] & 0xffffu;
+    }
+    w = make_uint4(c[0], c[1], c[2], c[3]);
+  }
   __device__ __forceinline__ void clear() { w = make_uint4(0u, 0u, 0u, 0u); }
   // (the bits of 16-bit magnitudes are in the order of the magnitudes)
   __device__ __forceinline__ uint32_t most() const {
@@ -103,6 +118,20 @@ struct Eight {
 template <>
 struct Eight<float> {
   float4 a, b;
+  static constexpr int kChunks = 3;
+  __device__ __forceinline__ void extract(const uint4 (&from)[kChunks], unsigned skip, unsigned n) {
+    uint32_t c[12] = {from[0].x, from[0].y, from[0].z, from[0].w, from[1].x, from[1].y,
+                      from[1].z, from[1].w, from[2].x, from[2].y, from[2].z, from[2].w};
+#pragma unroll
+    for (int i = 0; i < 9; ++i) c[i] = skip & 8u ? c[i + 2] : c[i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      c[i] = skip & 4u ? c[i + 1] : c[i];
+      if (i >= n) c[i] = 0u;
+    }
+    a = make_float4(__uint_as_float(c[0]), __uint_as_float(c[1]), __uint_as_float(c[2]), __uint_as_float(c[3]));
+    b = make_float4(__uint_as_float(c[4]), __uint_as_float(c[5]), __uint_as_float(c[6]), __uint_as_float(c[7]));
+  }
   __device__ __forceinline__ void load(const float* p) {
     a = __ldcs(reinterpret_cast<const float4*>(p));
     b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
@@ -135,18 +164,43 @@ __device__ __forceinline__ uint32_t codes_of(const float (&v)[8]) {
   return w;
 }
 
-// Eight neighbours a thread (VEC: 16-byte aligned), so a block of 32 is 4 lanes,
-// and a warp takes 8 blocks at a time; or one element a lane. All of the scales'
-// tiles are written: zeros where they belong to no block.
+// The 16-byte chunks around the values k .. k + 7 of a row (of K) that may start
+// anywhere: those that hold one of the row's. What is beside the row is read with them
+// where that is the matrix's (`inner`).
+template <typename E>
+__device__ __forceinline__ void load_around(const E* row, unsigned k, unsigned K, unsigned skip, bool inner,
+                                            uint4 (&c)[Eight<E>::kChunks]) {
+  constexpr unsigned VW = 16 / sizeof(E);
+  const unsigned first = k - skip / (unsigned)sizeof(E);       // (below 0 in front of the row)
+  const E* p = row + k - skip / sizeof(E);
+#pragma unroll
+  for (unsigned i = 0; i < Eight<E>::kChunks; ++i) {
+    c[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (i > 0 && first + i * VW >= K) continue;
+    if (inner) {
+      c[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+    } else {
+      E* e = reinterpret_cast<E*>(&c[i]);
+#pragma unroll
+      for (unsigned j = 0; j < VW; ++j)
+        if (first + i * VW + j < K) e[j] = p[i * VW + j];
+    }
+  }
+}
+
+// Eight neighbours a thread, so a block of 32 is 4 lanes, and a warp takes 8 blocks
+// at a time. SHIFT: rows that do not start on 16 bytes, or do not end after a multiple
+// of 8 values; the values are taken out of the chunks around them (8192 x 4097: BF16
+// 31 us, FP32 47, by single elements 59 each). All of the scales' tiles are
+// written: zeros where they belong to no block.
 constexpr int kAhead = 4;                              // pieces of a thread
-constexpr int values_of(bool vec) { return vec ? 256 * kAhead : 128; }   // of a warp's share
-template <typename E, bool VEC>
+constexpr int kValues = 256 * kAhead;                  // of a warp's share
+template <typename E, bool SHIFT>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(const Args a) {
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const unsigned lane = threadIdx.x & 31, K = (unsigned)a.K;
   const unsigned row_end = (unsigned)a.blocks * 32u, tile_end = (unsigned)a.block_tiles * 128u;
-  constexpr unsigned kValues = values_of(VEC);
   const int pieces = (int)((tile_end + kValues - 1) / kValues);
   // (the rows that fill up the scales' tiles have zeros, too)
   const long long all = (a.M + 127ll) / 128 * 128 * pieces;
@@ -158,115 +212,121 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const Args a) {
     unsigned char* q = a.q + sh.m * a.ldq;
     unsigned char* scale = a.scale + scale_place(sh.m, 0, a.block_tiles);   // the row's: 512 bytes a tile
     const unsigned k0 = (unsigned)sh.piece * kValues;
-    if constexpr (VEC) {
-      Eight<E> in[kAhead];
+    const unsigned skip = SHIFT ? (unsigned)(reinterpret_cast<uintptr_t>(x) & 15u) : 0u;
+    const bool inner = SHIFT && rows::inner_row(sh.m, a.M, a.K, 16 / (int)sizeof(E));
+    Eight<E> in[kAhead];
+    uint4 around[SHIFT ? kAhead : 1][Eight<E>::kChunks];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const unsigned k = k0 + j * 256u + lane * 8u;
-        in[j].clear();
-        if (row && k < K) in[j].load(x + k);           // (K is a multiple of 8 here)
-      }
+    for (int j = 0; j < kAhead; ++j) {
+      const unsigned k = k0 + j * 256u + lane * 8u;
+      in[j].clear();
+      if (!row || k >= K) continue;
+      if constexpr (SHIFT)
+        load_around<E>(x, k, K, skip, inner, around[j]);
+      else
+        in[j].load(x + k);                             // (K is a multiple of 8 here)
+    }
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const unsigned k = k0 + j * 256u + lane * 8u;
-        if (k0 + j * 256u >= tile_end) break;          // (the whole warp)
-        uint32_t most = in[j].most();
-        most = max(most, __shfl_xor_sync(kAll, most, 1));
-        most = max(most, __shfl_xor_sync(kAll, most, 2));
-        const uint32_t s = power_of(most);
-        const float unit = units_of(s);
-        float v[8];
-        in[j].values(v);
+    for (int j = 0; j < kAhead; ++j) {
+      const unsigned k = k0 + j * 256u + lane * 8u;
+      if (k0 + j * 256u >= tile_end) break;            // (the whole warp)
+      if constexpr (SHIFT)
+        if (row && k < K) in[j].extract(around[j], skip, K - k);
+      uint32_t most = in[j].most();
+      most = max(most, __shfl_xor_sync(kAll, most, 1));
+      most = max(most, __shfl_xor_sync(kAll, most, 2));
+      const uint32_t s = power_of(most);
+      const float unit = units_of(s);
+      float v[8];
+      in[j].values(v);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] *= unit;
-        // the row's blocks are whole: past its end there are zeros
-        const bool block = row && k < row_end;
-        if (block) *reinterpret_cast<uint32_t*>(q + k / 2) = codes_of(v);
-        // four blocks' bytes, by the first of their 16 lanes
-        uint32_t word = block ? s << (lane * 2 & 24u) : 0u;
-        word |= __shfl_xor_sync(kAll, word, 4);
-        word |= __shfl_xor_sync(kAll, word, 8);
-        if ((lane & 15u) == 0 && k < tile_end)
-          *reinterpret_cast<uint32_t*>(scale + (size_t)(k / 128) * 512) = word;
-      }
-    } else {
-      uint32_t word = 0;
-      float v[4];
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const unsigned k = k0 + b * 32u + lane;
-        v[b] = row && k < K ? to_f32(x[k]) : 0.f;
-      }
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const unsigned k = k0 + b * 32u + lane;
-        const uint32_t s = power_of(__reduce_max_sync(kAll, __float_as_uint(v[b]) & 0x7fffffffu));
-        const float unit = units_of(s);
-        const float next = __shfl_down_sync(kAll, v[b], 1);
-        if (row && k0 + b * 32u < row_end) {
-          word |= s << (8 * b);
-          if (!(lane & 1u))
-            q[k / 2] = (unsigned char)__nv_cvt_float2_to_fp4x2(make_float2(v[b] * unit, next * unit),
-                                                               __NV_E2M1, cudaRoundNearest);
-        }
-      }
-      if (lane == 0) *reinterpret_cast<uint32_t*>(scale + (size_t)sh.piece * 512) = word;
+      for (int c = 0; c < 8; ++c) v[c] *= unit;
+      // the row's blocks are whole: past its end there are zeros
+      const bool block = row && k < row_end;
+      if (block) *reinterpret_cast<uint32_t*>(q + k / 2) = codes_of(v);
+      // four blocks' bytes, by the first of their 16 lanes
+      uint32_t word = block ? s << (lane * 2 & 24u) : 0u;
+      word |= __shfl_xor_sync(kAll, word, 4);
+      word |= __shfl_xor_sync(kAll, word, 8);
+      if ((lane & 15u) == 0 && k < tile_end)
+        *reinterpret_cast<uint32_t*>(scale + (size_t)(k / 128) * 512) = word;
     }
   }
 }
 
+// 2^(s - 127): below the normal numbers for s = 0, NaN for 255.
+__device__ __forceinline__ float power(uint32_t s) {
+  return s == 0 ? 0x1p-127f : __uint_as_float(s == 255 ? 0x7fc00000u : s << 23);
+}
+__device__ __forceinline__ uint32_t codes_at(const unsigned char* q, int word, unsigned K) {
+  return word >= 0 && (unsigned)word * 8u < K ? __ldcs(reinterpret_cast<const uint32_t*>(q) + word) : 0u;
+}
+
 // Values of a block: the code's value times the block's power, rounded to E. A
 // scale of 255 makes them NaN. A thread writes 16 bytes at a time (4 or 8 values).
-template <typename E>
-__global__ void __launch_bounds__(kThreads)
-    dequantize_kernel(const Args a, E* x, long long ldx, int wide) {
+// SHIFT: rows of X that do not start on 16 bytes; places count from the boundary
+// before the row, and a thread's codes lie in two words and up to two blocks (8192 x
+// 4097: BF16 23 us, FP32 33; by single elements 90 and 44).
+template <typename E, bool SHIFT>
+__global__ void __launch_bounds__(kThreads) dequantize_kernel(const Args a, E* x, long long ldx) {
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   constexpr int VW = 16 / (int)sizeof(E), kPieces = 8 * kAhead / VW;
-  constexpr unsigned kValues = values_of(true);
   const unsigned lane = threadIdx.x & 31, K = (unsigned)a.K;
-  const int pieces = (int)((K + kValues - 1) / kValues);
+  const int pieces = (int)((K + (SHIFT ? VW - 1u : 0u) + kValues - 1) / kValues);
   const long long all = (long long)a.M * pieces, warps = (long long)gridDim.x * (kThreads / 32);
   for (long long i = blockIdx.x * (long long)(kThreads / 32) + (threadIdx.x >> 5); i < all; i += warps) {
     const Share sh = share_of(i, pieces);
-    const unsigned k0 = (unsigned)sh.piece * kValues + lane * VW;
+    const unsigned first = SHIFT ? rows::start_of<E>(x, sh.m, ldx) : 0u, end = K + first;
+    const unsigned c0 = (unsigned)sh.piece * kValues + lane * VW;
     const unsigned char* q = a.q + sh.m * a.ldq;
     const unsigned char* scale = a.scale + scale_place(sh.m, 0, a.block_tiles);
     E* o = x + sh.m * ldx;
-    uint32_t w[kPieces], s[kPieces];
+    auto scale_of = [&](unsigned block) { return (uint32_t)__ldg(scale + (size_t)(block / 4) * 512 + block % 4); };
+    uint32_t w[kPieces], more[kPieces], s[kPieces], t[kPieces];
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) {
-      const unsigned k = k0 + j * (32u * VW);
-      if (k >= K) continue;
+      const unsigned c = c0 + j * (32u * VW);
+      if (c >= end) continue;
+      const int k = (int)(c - first);                  // (below 0 in front of the row)
       // (rows are whole blocks)
-      if constexpr (VW == 8)
-        w[j] = __ldcs(reinterpret_cast<const uint32_t*>(q + k / 2));
-      else
-        w[j] = __ldcs(reinterpret_cast<const uint16_t*>(q + k / 2));
-      s[j] = __ldg(scale + (size_t)(k / 128) * 512 + (k / 32) % 4);
+      if constexpr (SHIFT) {
+        w[j] = codes_at(q, k >> 3, K);
+        more[j] = codes_at(q, (k >> 3) + 1, K);
+        const unsigned k1 = (unsigned)max(k, 0);
+        s[j] = scale_of(k1 / 32);
+        t[j] = scale_of(min((k1 + VW - 1) / 32, (unsigned)a.blocks - 1u));
+      } else {
+        if constexpr (VW == 8)
+          w[j] = __ldcs(reinterpret_cast<const uint32_t*>(q + k / 2));
+        else
+          w[j] = __ldcs(reinterpret_cast<const uint16_t*>(q + k / 2));
+        s[j] = scale_of((unsigned)k / 32);
+      }
     }
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) {
-      const unsigned k = k0 + j * (32u * VW);
-      if (k >= K) continue;
-      // 2^(s - 127): below the normal numbers for s = 0, NaN for 255
-      const float unit =
-          s[j] == 0 ? 0x1p-127f : __uint_as_float(s[j] == 255 ? 0x7fc00000u : s[j] << 23);
+      const unsigned c = c0 + j * (32u * VW);
+      if (c >= end) continue;
+      const int k = (int)(c - first);
+      if (SHIFT) w[j] = __funnelshift_r(w[j], more[j], 4u * (k & 7));
+      const float unit = power(s[j]), unit1 = SHIFT ? power(t[j]) : unit;
+      const int in_first = SHIFT ? 32 - (k & 31) : VW;   // values of the first block
       float v[VW];
 #pragma unroll
-      for (int c = 0; c < VW; c += 2) {
+      for (int i = 0; i < VW; i += 2) {
         const __half2_raw h =
-            __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(w[j] >> (4 * c) & 0xffu), __NV_E2M1);
+            __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(w[j] >> (4 * i) & 0xffu), __NV_E2M1);
         const float2 f = __half22float2(__half2(h));
-        v[c] = f.x * unit;
-        v[c + 1] = f.y * unit;
+        v[i] = f.x * (i < in_first ? unit : unit1);
+        v[i + 1] = f.y * (i + 1 < in_first ? unit : unit1);
       }
-      if (wide && k + VW <= K) {
+      if (k >= 0 && c + VW <= end) {
         rows::store<E, VW>(o + k, rows::pack<E, VW>(v));
       } else {
 #pragma unroll
-        for (int c = 0; c < VW; ++c)
-          if (k + c < K) o[k + c] = from_f32<E>(v[c]);
+        for (int i = 0; i < VW; ++i)
+          if (k + i >= 0 && c + i < end) o[k + i] = from_f32<E>(v[i]);
       }
     }
   }
@@ -289,20 +349,20 @@ cudaError_t start(void (*kernel)(A...), long long blocks, int sms, cudaStream_t 
 
 template <typename E>
 cudaError_t quantize(const Args& a, int sms, cudaStream_t stream) {
-  const bool vec = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && a.ldx * sizeof(E) % 16 == 0 &&
-                   a.K % 8 == 0;
-  const int values = values_of(vec);
-  const long long shares = (a.M + 127ll) / 128 * 128 * ((a.block_tiles * 128ll + values - 1) / values);
-  return start(vec ? quantize_kernel<E, true> : quantize_kernel<E, false>,
+  const bool whole = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && a.ldx * sizeof(E) % 16 == 0 &&
+                     a.K % 8 == 0;
+  const long long shares = (a.M + 127ll) / 128 * 128 * ((a.block_tiles * 128ll + kValues - 1) / kValues);
+  return start(whole ? quantize_kernel<E, false> : quantize_kernel<E, true>,
                (shares + kThreads / 32 - 1) / (kThreads / 32), sms, stream, a);
 }
 
 template <typename E>
 cudaError_t dequantize(const Args& a, void* x, long long ldx, int sms, cudaStream_t stream) {
-  const bool wide = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && ldx * sizeof(E) % 16 == 0;
-  const long long shares = (a.K + (long long)values_of(true) - 1) / values_of(true) * a.M;
-  return start(dequantize_kernel<E>, (shares + kThreads / 32 - 1) / (kThreads / 32), sms, stream, a,
-               static_cast<E*>(x), ldx, (int)wide);
+  const bool whole = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && ldx * sizeof(E) % 16 == 0;
+  const long long places = a.K + (whole ? 0ll : 16 / (int)sizeof(E) - 1ll);
+  const long long shares = (places + kValues - 1) / kValues * a.M;
+  return start(whole ? dequantize_kernel<E, false> : dequantize_kernel<E, true>,
+               (shares + kThreads / 32 - 1) / (kThreads / 32), sms, stream, a, static_cast<E*>(x), ldx);
 }
 
 bool type_ok(int type) {

@@ -163,14 +163,6 @@ __device__ __forceinline__ void put_quotients(const float (&u)[VW], const Step& 
 // host takes rows that are a multiple of 16 bytes apart; so a block's weights are
 // laid out once, in shared memory, the way its pieces lie. 8192 x 4097 BF16: y 55 us,
 // 8 bits 72, gradients 93; by single elements 124, 161 and 200.
-template <typename E>
-__device__ __forceinline__ unsigned start_of(const void* p, long long m, long long ld) {
-  return (unsigned)((reinterpret_cast<uintptr_t>(p) + m * ld * sizeof(E)) & 15u) / (unsigned)sizeof(E);
-}
-// Whether the whole pieces of row m are within the matrix, whose pitch is N at least.
-__device__ __forceinline__ bool inner_row(long long m, int M, int N, int vw) {
-  return m * N >= vw && (M - 1 - m) * N >= vw;
-}
 template <typename W>
 __device__ __forceinline__ const W* lay_out(const W* w, unsigned first, unsigned end, unsigned places) {
   extern __shared__ uint4 weights[];

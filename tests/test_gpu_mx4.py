@@ -85,6 +85,32 @@ def test_rounding(t, m, k):
         assert back.dtype == out and torch.equal(back, values(q, s, m)[:, :k].to(out))
 
 
+@pytest.mark.parametrize("m,k,offset,pad", [(300, 1001, 0, 0), (1000, 33, 1, 0), (257, 4097, 3, 2), (64, 2045, 2, 3),
+                                            (50, 8191, 5, 8), (2000, 3, 0, 0), (1, 1027, 7, 0), (130, 1024, 4, 1), (9, 96, 6, 0)])
+@pytest.mark.parametrize("t", TYPES)
+def test_rows_that_start_anywhere(t, m, k, offset, pad):
+    """The codes of the same rows, aligned; back into rows that start anywhere, and nothing beside them."""
+    x = rand(m, k, seed=m + k)
+    x *= torch.pow(2.0, rand(m, k, seed=3, scale=2.0).round())
+    x = x.to(t)
+    x[m // 2, k // 2] = float("inf")
+    whole = torch.zeros(m, (k + 7) // 8 * 8, dtype=t, device="cuda")
+    whole[:, :k] = x
+    want, want_scale = B.mx4_quantize(whole)                     # (zeros behind the row: the same blocks)
+    nan = float("nan")
+    store = torch.full((offset + m * (k + pad) + 8,), nan, dtype=t, device="cuda")
+    view = store[offset:offset + m * (k + pad)].view(m, k + pad)[:, :k]
+    view.copy_(x)
+    q, scale = B.mx4_quantize(view)
+    assert torch.equal(q, want) and torch.equal(scale, want_scale)
+    view.fill_(7)
+    back = B.mx4_dequantize(q, scale, k, X=view)
+    assert back is view
+    assert torch.equal(view.nan_to_num(nan=1e4), values(q, scale, m)[:, :k].to(t).nan_to_num(nan=1e4))
+    beside = store[offset:offset + m * (k + pad)].view(m, k + pad)[:, k:]
+    assert bool(store[:offset].isnan().all()) and bool(beside.isnan().all()) and bool(store[offset + m * (k + pad):].isnan().all())
+
+
 def test_borders():
     """Every border between two values, and its neighbours, in blocks of several powers."""
     borders = [0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 7.0, 7.99]
