@@ -299,7 +299,7 @@ struct Problem {
   // words x 2048 BF16, loss 417 us, so 349 (both in sums of 1024).
   static int block(size_t bytes) { return std::max(1, (int)((32u << 20) / (bytes + 1))); }
   // Few tokens: words on the lanes, so that W streams through full tiles (10
-  // tokens x 8344 words x 2912 F16: the loss in 18 us, with tokens on the lanes 37).
+  // tokens x 8344 words x 2912 F16: the loss in 16 us, with tokens on the lanes 37).
   bool few() const { return !f32() && T <= 64; }
   int lse_source() const { return few() ? ragged::kLseFew : ragged::kLse; }
   int grad_source() const { return few() ? ragged::kGradFew : ragged::kGrad; }
