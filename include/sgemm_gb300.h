@@ -34,17 +34,19 @@
  * one stream.
  *
  * CUDA graphs: sgemm, sgemm_ex, sgemm_strided_batched, sgemm_3xtf32,
- * sgemm_grouped, sgemm_grouped_wgrad, sgemm_i8 and sgemm_grad_clip can be
+ * sgemm_grouped, sgemm_grouped_wgrad, sgemm_i8, sgemm_grad_clip,
+ * sgemm_rms_norm_grad, sgemm_linear_ce, sgemm_linear_ce_grad and sgemm_mx4 can be
  * captured into a graph and replayed, once a call of at least the same size
- * (for the grouped and 8-bit calls, whose workspace goes by the tile that
- * their sizes choose: of the same sizes) has run on the capturing stream
+ * (for all but the first four and sgemm_grad_clip, whose workspace goes by the
+ * form that their sizes choose: of the same sizes) has run on the capturing stream
  * outside the capture (it sets the device up and sizes the stream's workspace;
  * a call that would have to grow it during capture returns SGEMM_ERR_CAPTURE
  * and launches nothing). The graph keeps the stream's workspace: do not replay
  * it concurrently with other work on that stream's workspace. A later call
  * that needs a larger one gets a new block; the one that graphs hold stays
  * allocated until sgemm_shutdown(), after which they must not be replayed.
- * sgemm_noalloc needs no workspace at all.
+ * sgemm_noalloc, sgemm_rms_norm, sgemm_rms_norm_i8, sgemm_mx4_quantize and
+ * sgemm_mx4_dequantize need no workspace at all.
  */
 #ifndef SGEMM_GB300_H
 #define SGEMM_GB300_H
