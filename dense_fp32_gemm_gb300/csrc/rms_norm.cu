@@ -748,7 +748,8 @@ int shared_of(Access access, int N, int vw, int weight_bytes) {
 int spaced(Access access, int M, long long row_bytes, int blocks) {
   int rows = 1;
   while (row_bytes * rows % 16 != 0) rows *= 2;
-  return access == kShifted && blocks < M && blocks > rows ? blocks / rows * rows : blocks;
+  if (access != kShifted || blocks >= M) return blocks;
+  return blocks >= rows ? blocks / rows * rows : (M < rows ? M : rows);
 }
 
 template <typename E, typename W, bool I8>
