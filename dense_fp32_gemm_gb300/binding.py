@@ -604,7 +604,8 @@ def linear_cross_entropy(X, W, target, ignore_index=-100, loss=None, lse=None, s
 def linear_cross_entropy_grad(X, W, target, lse, dloss, ignore_index=-100, dX=None, dW=None,
                               want=(True, True), stream=None):
     """(dX, dW): gradients of linear_cross_entropy for dloss, the gradient of each
-    row's loss (float32). What is not wanted is None."""
+    row's loss (float32). What is not wanted is None. X must hold numbers in rows
+    that are not counted, too: dW adds 0 times them."""
     return _native().linear_cross_entropy_grad(X, W, target, lse, dloss, ignore_index, dX, dW,
                                                bool(want[0]), bool(want[1]), stream)
 
