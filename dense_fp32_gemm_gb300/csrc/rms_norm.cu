@@ -669,11 +669,17 @@ __global__ void __launch_bounds__(32 * kSumLanes)
   }
 }
 
+// Bytes of shared memory for the weights of shifted rows; longer ones are taken by
+// single elements.
+constexpr int kMostShared = 96 << 10;
+
+// (the limit that is set belongs to the kernel, whoever calls: always the most that any
+// call takes, so that no call lowers it between another's setting and its launch)
 template <typename... A>
 cudaError_t launch(void (*kernel)(A...), long long blocks, int threads, int shared_bytes,
                    cudaStream_t stream, std::common_type_t<A>... args) {
   if (shared_bytes > (32 << 10)) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared_bytes);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t lc = {};
@@ -725,9 +731,6 @@ bool alike(const void* p, long long ld, const void* x, long long ldx, int elem) 
 // How a call's rows are taken: in 16-byte pieces that start with the row, in
 // pieces that start at a boundary before it, or by single elements.
 enum Access { kPieces, kShifted, kSingle };
-// Bytes of shared memory for the weights of shifted rows; longer ones are taken by
-// single elements.
-constexpr long long kMostShared = 96 << 10;
 // Shifted, unless the weights take too much, or the call is a few rows that threads
 // hold by single elements: laying out the weights, and the first and the last row,
 // whose ends are read by themselves, take 1 to 2 us (16 x 1001 BF16: 4.0 us, single 2.4;
