@@ -117,6 +117,12 @@ __device__ __forceinline__ void quotients(const float (&u)[VW], float step, floa
   }
 }
 
+// Factor of the values of rows whose squares FP32 does not hold (a sum above 3e38). The
+// largest, below 2^128, have squares below 2^76 with it, 2^31 of which still add up; the
+// smallest such row, 2^31 values of 4e14, has squares of 1e-25. (With 2^-70 rows of 4096
+// values of 3e38 were beyond FP32 once more.)
+constexpr float kDown = 0x1p-90f;
+
 // What a row's integers are divided by.
 struct Step {
   float step, inv;     // 1 / step, where that is a number to multiply by (else no number)
@@ -281,7 +287,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a) {
     // are scaled down. eps is at least 1e-30, so squares below the range do not count.
     float down = 1.f;
     if (!(t.sum <= 3e38f)) {
-      down = 0x1p-70f;
+      down = kDown;
       sum = 0.f;
       each([&](const Piece<E, VW>& p, unsigned) {
         float f[VW];
@@ -534,11 +540,11 @@ __global__ void __launch_bounds__(kSmallThreads) small_norm_kernel(const NormArg
     if (__any_sync(kAll, !(sum <= 3e38f))) {
       float scaled = 0.f;
 #pragma unroll
-      for (int j = 0; j < VW; ++j) scaled = fmaf(f[j] * 0x1p-70f, f[j] * 0x1p-70f, scaled);
+      for (int j = 0; j < VW; ++j) scaled = fmaf(f[j] * kDown, f[j] * kDown, scaled);
       scaled = sum_over(scaled, lanes);
       if (!(sum <= 3e38f)) {
         sum = scaled;
-        down = 0x1p-70f;
+        down = kDown;
       }
     }
     const float rstd = rsqrtf(sum * inv_n + a.eps * down * down) * down;
