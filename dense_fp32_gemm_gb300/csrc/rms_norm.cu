@@ -752,6 +752,16 @@ long long pieces_of(Access access, int N, int vw) {
 int shared_of(Access access, int N, int vw, int weight_bytes) {
   return access == kShifted ? (int)(pieces_of(access, N, vw) * vw * weight_bytes) : 0;
 }
+// Rows that the 32 threads of a block hold by single elements (up to 256 values) and
+// shifted in one more piece than the threads have turns for, most of which are then
+// idle: from `from` pieces on, to `to`. y from 33 pieces on: 255 values, 72 MB each of x,
+// r, h and y, BF16 shifted 125 us, single 90 (257 values 124 and 166); FP32 129 78 and 62,
+// 255 58 and 49. 8 bits to 48: BF16 255 150 and 120, FP32 129 99 and 93, 189 71 and 70,
+// 197 68 and 71. Gradients from 65 on: FP32 255 79 and 62 (245 61 and 63, BF16 255 115 and 123).
+bool one_warp(int N, int vw, long long from, long long to) {
+  const long long pieces = pieces_of(kShifted, N, vw);
+  return N <= 32 * held_of(1) && pieces >= from && pieces <= to;
+}
 // Blocks so that the rows of one, where there are several, are a multiple of 16
 // bytes apart.
 int spaced(Access access, int M, long long row_bytes, int blocks) {
@@ -769,7 +779,7 @@ cudaError_t forward(NormArgs a, int sms, cudaStream_t stream) {
                      a.N % VW == 0 && (I8 || aligned(a.y, a.ldy, sizeof(E), 16));
   const bool shifted = alike(a.r, a.ldr, a.x, a.ldx, sizeof(E)) && alike(a.h, a.ldh, a.x, a.ldx, sizeof(E)) &&
                        (I8 || alike(a.y, a.ldy, a.x, a.ldx, sizeof(E))) &&
-                       shift(a.M, a.N, VW, sizeof(W), sms);
+                       shift(a.M, a.N, VW, sizeof(W), sms) && !one_warp(a.N, VW, 33, I8 ? 48 : 256);
   const Access access = whole ? kPieces : shifted ? kShifted : kSingle;
   a.wide_q = I8 && access != kShifted && aligned(a.y, a.ldy, 1, VW);
   const bool few = a.M < 2 * sms;
@@ -990,7 +1000,8 @@ SGEMM_API int sgemm_rms_norm_grad(int M, int N, int type, const void* dY, int ld
                      rows::aligned(a.dh, lddh, eb, 16) && rows::aligned(dX, lddx, eb, 16) &&
                      rows::aligned(weight, 0, wb, 16) && N % vw == 0;
   const bool shifted = rows::alike(H, ldh, dY, lddy, eb) && rows::alike(a.dh, lddh, dY, lddy, eb) &&
-                       rows::alike(dX, lddx, dY, lddy, eb) && rows::shift(M, N, vw, wb, sms);
+                       rows::alike(dX, lddx, dY, lddy, eb) && rows::shift(M, N, vw, wb, sms) &&
+                       !rows::one_warp(N, vw, 65, 256);
   const rows::Access access = whole ? rows::kPieces : shifted ? rows::kShifted : rows::kSingle;
   const bool vec = access != rows::kSingle;
   const long long pieces = rows::pieces_of(access, N, vw);
