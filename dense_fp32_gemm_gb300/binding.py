@@ -597,15 +597,17 @@ def linear_cross_entropy(X, W, target, ignore_index=-100, loss=None, lse=None, s
     """(loss, lse), float32 with a value for each row of X: the softmax cross
     entropy of the logits X @ W.T with the words target (int64), 0 where target
     is ignore_index, and the logarithm of the sum of the logits' exponentials.
-    The logits are not kept. A target that is no word gives NaN."""
+    The logits are not kept. A target that is no word gives NaN. Logits of
+    -infinity have no share; an infinite float32 operand gives NaN."""
     return _native().linear_cross_entropy(X, W, target, ignore_index, loss, lse, stream)
 
 
 def linear_cross_entropy_grad(X, W, target, lse, dloss, ignore_index=-100, dX=None, dW=None,
                               want=(True, True), stream=None):
     """(dX, dW): gradients of linear_cross_entropy for dloss, the gradient of each
-    row's loss (float32). What is not wanted is None. X must hold numbers in rows
-    that are not counted, too: dW adds 0 times them."""
+    row's loss (float32). What is not wanted is None. X must hold finite numbers in
+    rows that are not counted, too, and W in words that have no share: the products
+    add 0 times them."""
     return _native().linear_cross_entropy_grad(X, W, target, lse, dloss, ignore_index, dX, dW,
                                                bool(want[0]), bool(want[1]), stream)
 

@@ -131,7 +131,7 @@ class _CrossEntropy(torch.autograd.Function):
 def linear_cross_entropy(x, weight, target, ignore_index=-100, reduction="mean"):
     """Softmax cross entropy of x @ weight.T with the words `target` (int64, the
     leading dimensions of x), without keeping the logits. Rows whose target is
-    ignore_index are not counted (but must hold numbers). reduction: "mean" over the counted rows (0 if
+    ignore_index are not counted (but must hold finite numbers). reduction: "mean" over the counted rows (0 if
     there are none), "sum", or "none" (a value a row). Differentiable once in x
     and weight."""
     if reduction not in ("mean", "sum", "none"):

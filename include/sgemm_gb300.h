@@ -676,7 +676,9 @@ int sgemm_rms_norm_grad(int M, int N, int type, const void* dY, int lddy, const 
  * NULL) is written for every row. Both are FP32, and so are the logits and the
  * sums: 16-bit operands are multiplied exactly and leave the tensor cores every
  * 512 products, FP32 ones as in sgemm_grouped(). Logits of -infinity have no
- * share; a NaN or +infinity among a row's makes its loss NaN.
+ * share; a NaN or +infinity among a row's makes its loss NaN. (FP32 operands
+ * have no infinite logits: an infinity among them makes every logit that it takes
+ * part in NaN, as in sgemm_grouped(), and with it the row's loss.)
  * The vocabulary is taken in pieces, so that the workspace stays below 256 MB
  * beside the products' own (FP32: 512 MB), or the statistics (logits) of 2048
  * words at a time. Any leading dimensions (>= max(1, H)) and element
@@ -694,8 +696,8 @@ int sgemm_linear_ce(int type, int T, int V, int H, const void* X, int ldx, const
  *   dX = G W (T x H),   dW = G^T X (V x H), of `type`; either may be NULL.
  * The logits are formed once more; a piece of G at a time is held in `type`,
  * scaled by a power of two and max|dloss| so that F16 keeps small ones. Sums are
- * FP32, rounded once. X must hold numbers in rows that are not counted, too (0
- * times none is none). dX and dW must not overlap X, W or each other. Workspace:
+ * FP32, rounded once. X must hold finite numbers in rows that are not counted,
+ * too, and W in words that have no share (0 times an infinity or a NaN is NaN). dX and dW must not overlap X, W or each other. Workspace:
  * 512 MB (or 2048 words of G) beside the products' own, and T x H FP32 sums
  * where G takes several pieces. Errors as sgemm_linear_ce().
  */
