@@ -94,9 +94,9 @@ struct Geo {
   static constexpr bool kShare = BQ == 256;                    // accumulators share a half
   static constexpr int kSecond = kShare ? BQ / 2 : BQ;         // the second accumulator
   static constexpr int kScales = kSecond + BQ;
-  static constexpr int kSlotFit = (512 - kScales) / kCols;
-  static constexpr int kSlots = kSlotFit < kStages ? kSlotFit : kStages;   // slices' scales
-  static constexpr int kUsed = kScales + kSlots * kCols;
+  // each stage's scales have columns of their own: the MMAs that read them last are done
+  // once the stage has been loaded again
+  static constexpr int kUsed = kScales + kStages * kCols;
   // A thread of a wide tile's epilogue holds 128 sums: it needs more registers
   // than the launch gives every thread, so the other warps give some up.
   static constexpr bool kMoveRegs = BQ == 256;
@@ -316,18 +316,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int s = it % S;
             ok = wait_for(ptx::smem_addr(&sh->full[s]), (uint32_t)((it / S) & 1), abort_w, p.status,
                           kDevTimeoutFull, p.timeout_ns);
-            // the MMAs that read this slot of scales have completed (with a slot
-            // for every stage they have: the stage has been loaded again)
-            constexpr int kSlots = G::kSlots;
-            if (kSlots < S && ok && it >= kSlots)
-              ok = wait_for(ptx::smem_addr(&sh->empty[(it - kSlots) % S]),
-                            (uint32_t)(((it - kSlots) / S) & 1), abort_w, p.status,
-                            kDevTimeoutEmpty, p.timeout_ns);
             if (!ok) break;
             tc::fence_after_sync();
             const uint32_t st = (uint32_t)(s * G::kStage);
             const uint32_t scales = base_addr + st + G::kP + G::kQ;
-            const uint32_t sp = tmem + (uint32_t)(G::kScales + it % G::kSlots * G::kCols), sq = sp + 8;
+            const uint32_t sp = tmem + (uint32_t)(G::kScales + s * G::kCols), sq = sp + 8;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               tc::copy_scales<CL>(sp + h * 4, scales + h * 512);
@@ -734,6 +727,11 @@ int run(int M, int N, int K, const void* A, int lda, const void* SA, const void*
   p.P = N;
   p.Q = M;
   p.K = K;
+  // Slices of an accumulation, which truncates: 8, of 2048 values, are as exact as sums in
+  // FP32 (blocks whose powers differ by up to 2^16, 512 x 2048 x 4096: 5.5e-7, a product
+  // in FP32 5.1e-7; 4 slices 2.9e-7; without such differences the sums are exact). For 16
+  // bits 32, 1.1e-6 at 8192 values. 8192 x 8192 x 8192, FP32 out: 4 slices 300 us, 8 226,
+  // 32 173.
   p.chunk = out_type == SGEMM_TYPE_F32 ? 8 : 32;
   p.out = C;
   p.ldo = ldc;
