@@ -14,7 +14,9 @@
  *                     B(k,j) = B[k*ldb + j] for k < K, j < N;
  *                     C(i,j) = C[i*ldc + j] for i < M, j < N.
  * Elements outside those ranges (padding between rows) are never read or
- * written.
+ * written. (The norms and sgemm_mx4_quantize() at the end of this file may read
+ * what lies between two rows of a matrix, 16 bytes at a time, and make no use of
+ * it; it is never written.)
  *
  * Ownership: all matrix pointers are DEVICE pointers owned by the caller. The
  * library owns only a small per-(device, stream) workspace (split-K partial
@@ -38,7 +40,8 @@
  * sgemm_rms_norm_grad, sgemm_linear_ce, sgemm_linear_ce_grad and sgemm_mx4 can be
  * captured into a graph and replayed, once a call of at least the same size
  * (for all but the first four and sgemm_grad_clip, whose workspace goes by the
- * form that their sizes choose: of the same sizes) has run on the capturing stream
+ * form that their sizes choose: of the same sizes, leading dimensions and 16-byte
+ * alignment of the matrices) has run on the capturing stream
  * outside the capture (it sets the device up and sizes the stream's workspace;
  * a call that would have to grow it during capture returns SGEMM_ERR_CAPTURE
  * and launches nothing). The graph keeps the stream's workspace: do not replay
@@ -660,8 +663,9 @@ int sgemm_rms_norm_i8(int M, int N, int type, const void* X, int ldx, const void
  * dX is the gradient of X and of R alike. dH (may be NULL) is the gradient that
  * reaches H itself. dX or dweight (of weight_type) may be NULL: not formed. dX
  * may be dY, H or dH itself. dweight is summed in FP32 in an order that depends
- * on the sizes only, and rounded once; M == 0 sets it to zeros. Workspace and
- * capture as for sgemm(); errors as sgemm_rms_norm().
+ * on the sizes, the leading dimensions, where the matrices start within 16 bytes
+ * and the GPU's number of SMs, not on timing, and rounded once; M == 0 sets it to
+ * zeros. Workspace and capture as said above; errors as sgemm_rms_norm().
  */
 int sgemm_rms_norm_grad(int M, int N, int type, const void* dY, int lddy, const void* H, int ldh,
                         const void* weight, int weight_type, const float* rstd, const void* dH,
