@@ -71,7 +71,9 @@ struct Params {
   void* out;
   long long ldo;
   int out_type;
-  int tma_out;              // C's rows are at multiples of 16 bytes: written by TMA
+  // C's rows are at multiples of 16 bytes: 32 features at a time are written by TMA, the
+  // last ones too (1), or by their threads (2)
+  int tma_out;
   int* status;
   long long timeout_ns;
 };
@@ -374,7 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = u.nq - c;                        // valid columns from the tile's c-th on
         if constexpr (G::kStaged) {
           // token by token into the warp's buffer (16 bits: one of two, in turn),
-          // then out as one box; lane by lane where C's rows do not allow that
+          // then out as one box; lane by lane where C's rows do not allow that (every
+          // box commits a group, an empty one then, as the waits count them)
           const bool f32 = p.out_type == SGEMM_TYPE_F32;
           unsigned char* buf = base + G::kRegion + (warp - kEpiWarp0) * kOut;
           if (f32) {
@@ -397,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < CH; ++j) o[j * 32] = __float2half_rn(v[j]);
           }
-          if (p.tma_out) {
+          if (p.tma_out == 1 || (p.tma_out == 2 && pp - lane + 32 <= p.P)) {
             ptx::fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) {
@@ -406,6 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               ptx::bulk_commit();
             }
           } else {
+            if (lane == 0) ptx::bulk_commit();
             __syncwarp();
             const long long at = (long long)(u.q0 + c) * p.ldo + pp;
 #pragma unroll 4
@@ -749,9 +753,12 @@ int run(int M, int N, int K, const void* A, int lda, const void* SA, const void*
       !encode_scales(&msp, SB, N, tiles_k, 1) || !encode_scales(&msq, SA, M, tiles_k, (f.bq + 127) / 128))
     return SGEMM_ERR_LAUNCH;
   const int elem = out_type == SGEMM_TYPE_F32 ? 4 : 2;
-  // (narrow tiles and cut ones are written by their threads)
-  p.tma_out = f.bq >= 128 && c.split == 1 && (reinterpret_cast<uintptr_t>(C) & 15u) == 0 &&
-              (long long)ldc * elem % 16 == 0;
+  // (Narrow tiles and cut ones are written by their threads. A TMA store ends with the
+  // 16 bytes that the row's last value is in: in rows that end inside those it would
+  // write zeros behind them.)
+  const bool tma_out = f.bq >= 128 && c.split == 1 && (reinterpret_cast<uintptr_t>(C) & 15u) == 0 &&
+                       (long long)ldc * elem % 16 == 0;
+  p.tma_out = !tma_out ? 0 : (long long)N * elem % 16 == 0 ? 1 : 2;
   if (p.tma_out && !encode_out(&mo, C, out_type, N, M, (long long)ldc * elem)) return SGEMM_ERR_LAUNCH;
   const int grid = c.split > 1 ? (int)tiles * c.split : (int)std::min<long long>(workers, tiles) * f.cl;
   cudaLaunchAttribute la[2];
