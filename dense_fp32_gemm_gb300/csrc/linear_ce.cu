@@ -24,10 +24,10 @@
 // Operations: 2 T V H forward; 6 T V H for the gradients, 2 of which form the
 // logits again (in exchange a piece of G is all that is ever stored). Bound by the
 // tensor cores under the power limit: 4096 tokens x 100003 words x 4096 BF16, loss
-// and gradients in 8.5 ms, 1580 TFLOP/s of all 8 T V H (93 % of a library
+// and gradients in 8.5 to 8.7 ms, 1580 TFLOP/s of all 8 T V H (93 % of a library
 // product's sustained 1706); 2048 x 65536 x 2048, the loss in 361 us, 1523. Small
-// ones by latency: 65 x 1000 x 256 F16 in 31 us, six launches of 3 to 7 us. FP32 by
-// the conversions of its products (1000 x 8191 x 777 in 353 us, 317 in products).
+// ones by latency: 65 x 1000 x 256 F16 in 32 us, six launches of 3 to 7 us. FP32 by
+// the conversions of its products (1000 x 8191 x 777 in 355 us, 317 in products).
 #include <cuda_runtime.h>
 #include <algorithm>
 #include <cmath>

@@ -16,8 +16,8 @@
 //
 // Bound by DRAM, less what a row's chain of loads, block-wide sum and stores leaves
 // idle. Measured on GB300, 8192 x 4096 BF16 with a residual (a copy runs at 6.8
-// TB/s): y 43.7 us, 6.1 TB/s; 8 bits 44.3 us, 5.3 TB/s (a value takes 29
-// instructions, 61 % of the issue slots); gradients 49.6 us, 5.4 TB/s, the sum of
+// TB/s): y 43.7 us, 6.1 TB/s; 8 bits 43.3 us, 5.4 TB/s (a value takes 29
+// instructions, 61 % of the issue slots); gradients 48.4 us, 5.5 TB/s, the sum of
 // dw's parts 5 of them. One row of 4096: 4.2 us. Of the forms tried: element by
 // element instead of words 70 us (8 bits); no row ahead 118; rows of 16-byte copies
 // three deep in shared memory 57 (8 bits), 46 (y), 70 (gradients, whose weight then
@@ -477,8 +477,8 @@ __global__ void __launch_bounds__(HELD == 2 ? 256 : kMaxThreads, HELD == 2 ? 2 :
 
 // Short rows, of at most 32 pieces of 16 bytes: a row is one piece each of `lanes`
 // (8, 16 or 32) neighbouring threads, and its sums go over them alone. (1048576
-// rows of 128 BF16: 104 us, back 160, of 79 and 118 that the bytes take; by a block
-// a row 326 and 336. 8192 rows of 64: 1.9 and 4.0 us instead of 4.4 and 11.5.)
+// rows of 128 BF16: 104 us, back 178, of 79 and 118 that the bytes take; by a block
+// a row 324 and 330. 8192 rows of 64: 1.9 and 4.0 us instead of 4.4 and 11.5.)
 constexpr int kSmallThreads = 256;
 __device__ __forceinline__ float sum_over(float v, int lanes) {
   for (int d = lanes >> 1; d > 0; d >>= 1) v += __shfl_xor_sync(kAll, v, d);

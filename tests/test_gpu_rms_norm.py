@@ -217,7 +217,7 @@ def test_rows_that_start_anywhere(t, m, n):
     test_gradients(t, m, n, True)
 
 
-# rows of one block, of clusters of 2, 4 and 8, and those that registers do not hold (at
+# rows that the registers of a block hold, and those that they do not (at
 # most 35 pieces of 4 values a thread: 35 + 4 + 21 additions one after another)
 @pytest.mark.parametrize("m,n", [(1000, 8192), (333, 5120), (400, 12288), (90, 16384), (50, 20000), (30, 32768), (5, 70000)])
 @pytest.mark.parametrize("t", TYPES)
